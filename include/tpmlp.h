@@ -67,7 +67,9 @@ typedef enum {
     TPMLP_ERR_OOM = -5,               /* device allocation failed */
     TPMLP_ERR_DEVICE_TIMEOUT = -6,    /* a kernel gave up waiting on a pipeline barrier */
     TPMLP_ERR_ARCH = -7,              /* the current device is not sm_103 */
-    TPMLP_ERR_MISALIGNED = -8         /* a device pointer is not 16-byte aligned */
+    TPMLP_ERR_MISALIGNED = -8,        /* a device pointer is not 16-byte aligned */
+    TPMLP_ERR_BAD_PAGE = -9           /* a page table named a page outside its pool, or a
+                                         position lay outside the table (from tpmlp_get_status) */
 } tpmlp_status;
 
 /* Flags for tpmlp_create. */
@@ -467,6 +469,125 @@ TPMLP_API int tpmlp_linear_pack(tpmlp_ctx *ctx, const void *W, const void *b, vo
  */
 TPMLP_API int tpmlp_linear_forward(tpmlp_ctx *ctx, const void *X, int64_t M, void *out,
                                    void *stream);
+
+/*
+ * Attention over a paged key-value cache: what lies between the column-parallel Q/K/V projection
+ * and the row-parallel output projection of a layer (AI大模型分布式训练 §2.3 splits the heads into
+ * k groups; here all heads are on this GPU). Three operators share one cache: append writes the
+ * new tokens' keys and values, decode attends from one new token of each sequence, prompt from
+ * a chunk of new tokens of each.
+ *
+ * tpmlp_attn_create: a context for one head layout.
+ *   Hq, Hkv    query heads and key-value heads; Hq = G Hkv, query heads h G .. h G + G - 1 share
+ *              kv head h (G = 1: one kv head per query head); G <= 128
+ *   D          head size: 64 or 128
+ *   page_size  keys per page: 16, 32, 64, 128 or 256
+ *   flags      0 or TPMLP_FLAG_KV_E4M3
+ * Allocates the scales, the workspace of split key ranges (about 13 MB) and the status word. The
+ * context is used with the tpmlp_attn_* calls, tpmlp_destroy and the diagnostic calls; the other
+ * entry points reject it with TPMLP_ERR_INVALID_ARG. Like the GEMM calls, its calls on different
+ * streams must not overlap on the GPU (they share the workspace). All of its calls can be
+ * captured into a CUDA graph; a replay reads lengths, positions, page table and cu_q anew.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, ARCH, OOM, CUDA.
+ */
+#define TPMLP_FLAG_KV_E4M3 0x10u /* the pools hold e4m3; the value is the stored number times a
+                                    scale per kv head (tpmlp_attn_set_scales; 1 at first) */
+TPMLP_API int tpmlp_attn_create(tpmlp_ctx **out, int32_t Hq, int32_t Hkv, int32_t D,
+                                int32_t page_size, uint32_t flags);
+
+/*
+ * The rotation that tpmlp_attn_append applies to queries and keys (none at first): the first
+ * rot_dim dimensions of every head are rotated in pairs, pair i at position p by the angle
+ * p * freq[i], and the rest are left as they are.
+ *   rot_dim      0 (no rotation) or a multiple of 16 up to D
+ *   interleaved  0: pair i is dimensions i and i + rot_dim / 2; 1: 2 i and 2 i + 1
+ *   freq         host, rot_dim / 2 finite angular frequencies in radians per position (NULL with
+ *            rot_dim 0); copied. Angles are reduced in fp64, so far positions lose nothing.
+ * Host state only; it applies to calls made afterwards. Errors: INVALID_ARG, UNSUPPORTED_SHAPE.
+ */
+TPMLP_API int tpmlp_attn_set_rope(tpmlp_ctx *ctx, int32_t rot_dim, int32_t interleaved,
+                                  const double *freq);
+
+/*
+ * Scales of an e4m3 cache (TPMLP_FLAG_KV_E4M3): k_scale, v_scale device fp32 [Hkv], positive
+ * (copied; may be freed once the stream has passed this call). Errors: INVALID_ARG, CUDA.
+ */
+TPMLP_API int tpmlp_attn_set_scales(tpmlp_ctx *ctx, const void *k_scale, const void *v_scale,
+                                    void *stream);
+
+/*
+ * The caller's cache, as the calls below read it. Key j of sequence b is row j % page_size of
+ * page page_table[b][j / page_size]; a page of a pool is [Hkv][page_size][D]. Pages may be
+ * shared between sequences that only read them. Rows at or past a sequence's length are never
+ * used, whatever they hold (NaN included).
+ */
+typedef struct tpmlp_kv {
+    void *K, *V;               /* device pools, bf16 or e4m3 */
+    int64_t num_pages;         /* pages of each pool */
+    int64_t page_stride;       /* elements from page to page; 0: Hkv * page_size * D. The stride
+                                  in bytes is a multiple of 16 */
+    const int32_t *page_table; /* device int32 [B][table_pages] */
+    int64_t table_stride;      /* elements from row to row of the table; 0: table_pages */
+    int32_t table_pages;       /* columns; table_pages * page_size < 2^31 */
+    int32_t B;                 /* sequences */
+    const int32_t *lens;       /* device int32 [B]: keys of each sequence (decode and prompt:
+                                  with the new tokens'); above table_pages * page_size it counts
+                                  as that and is reported, below 0 as 0 */
+} tpmlp_kv;
+
+/*
+ * Append T new tokens: rotate q and k by the token's position, write k and v into the cache and
+ * the rotated q to Qout.
+ *   Q    device bf16, row t at Q + t ldq, Hq * D elements (NULL: only k and v)
+ *   K, V device bf16, rows of Hkv * D elements at pitch ldk, ldv (elements, multiples of 8: the
+ *        three may be column ranges of one projection's output)
+ *   pos  device int32 [T]: position of each token in its sequence; < 0: the token is skipped
+ *        (nothing of it is written, Qout's row included)
+ *   seq  device int32 [T]: its sequence (NULL: token t belongs to sequence t)
+ *   Qout device bf16, pitch ldqo; may be Q itself (with the same pitch)
+ * kv->lens is not read. Two tokens of one call must not share a position of a sequence. An
+ * e4m3 cache stores x / scale, rounded to nearest and held to +-448. One launch; T == 0 is a
+ * no-op. A position outside the table, a sequence outside [0, B) or a page outside the pool:
+ * the token's k and v are dropped and tpmlp_get_status returns TPMLP_ERR_BAD_PAGE.
+ * Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED_SHAPE, CUDA.
+ */
+TPMLP_API int tpmlp_attn_append(tpmlp_ctx *ctx, const void *Q, int64_t ldq, const void *K,
+                                int64_t ldk, const void *V, int64_t ldv, int64_t T,
+                                const int32_t *pos, const int32_t *seq, const tpmlp_kv *kv,
+                                void *Qout, int64_t ldqo, void *stream);
+
+/*
+ * Attention of one new token of each sequence over its cache:
+ *   Out[b, h] = sum_j p_j V_j,  p = softmax over j of scale * <Q[b, h], K_j>,
+ *   max(0, lens[b] - window) <= j < lens[b]   (window <= 0: all keys)
+ *   Q    device bf16, row b at Q + b ldq, Hq * D elements    Out  alike, pitch ldo
+ *   Lse  device fp32 [B][Hq] or NULL: log of the sum over j of exp(scale * <Q, K_j>), for joining
+ *        with attention over other keys
+ * A sequence without keys gets zeros and an Lse of -infinity. Sums and softmax statistics are
+ * fp32; the work is split evenly over the GPU whatever the lengths, and split sequences are
+ * joined in a fixed order (deterministic). Keys in pages outside the pool are left out and
+ * reported (TPMLP_ERR_BAD_PAGE from tpmlp_get_status). One launch; B == 0 is a no-op.
+ * Errors: INVALID_ARG (also scale not positive and finite), MISALIGNED, UNSUPPORTED_SHAPE, CUDA.
+ */
+TPMLP_API int tpmlp_attn_decode(tpmlp_ctx *ctx, const void *Q, int64_t ldq, const tpmlp_kv *kv,
+                                float scale, int32_t window, void *Out, int64_t ldo, float *Lse,
+                                void *stream);
+
+/*
+ * Causal attention of a chunk of new tokens of each sequence over its cache, which already holds
+ * their keys and values (append first). Query i of the n new tokens of sequence b (rows
+ * cu_q[b] .. cu_q[b + 1] - 1 of Q) is at position lens[b] - n + i and attends to the keys at
+ * its own and earlier positions (with window > 0: the last `window` of them). Rows as in
+ * tpmlp_attn_decode; a query at a negative position gets zeros and -infinity.
+ *   T    rows of Q and Out    cu_q  device int32 [B + 1], from 0, not decreasing, at most T; rows
+ *        outside every sequence are not written. Lse device fp32 [T][Hq] or NULL.
+ * Two launches at most; T == 0 or B == 0 is a no-op.
+ * Errors: as tpmlp_attn_decode.
+ */
+TPMLP_API int tpmlp_attn_prompt(tpmlp_ctx *ctx, const void *Q, int64_t ldq, int64_t T,
+                                const int32_t *cu_q, const tpmlp_kv *kv, float scale,
+                                int32_t window, void *Out, int64_t ldo, float *Lse,
+                                void *stream);
 
 /* Release everything the context owns (synchronises its device first). NULL is a no-op. */
 TPMLP_API void tpmlp_destroy(tpmlp_ctx *ctx);

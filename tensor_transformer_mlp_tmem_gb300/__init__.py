@@ -30,6 +30,9 @@ __all__ = [
     "tpmlp_backward_swiglu", "tpmlp_set_device_rates", "tpmlp_get_device_rates", "tpmlp_build_id",
     "tpmlp_forward_marked", "tpmlp_block_forward_marked", "tpmlp_forward_host_async",
     "tpmlp_block_forward_host_async", "tpmlp_host_wait",
+    "Attention", "PagedCache", "KvCache", "TPMLP_FLAG_KV_E4M3", "TPMLP_ERR_BAD_PAGE",
+    "tpmlp_attn_create", "tpmlp_attn_set_rope", "tpmlp_attn_set_scales", "tpmlp_attn_append",
+    "tpmlp_attn_decode", "tpmlp_attn_prompt",
 ]
 
 TPMLP_OK = 0
@@ -41,10 +44,12 @@ TPMLP_ERR_OOM = -5
 TPMLP_ERR_DEVICE_TIMEOUT = -6
 TPMLP_ERR_ARCH = -7
 TPMLP_ERR_MISALIGNED = -8
+TPMLP_ERR_BAD_PAGE = -9
 TPMLP_FLAG_Z_FP32 = 0x1
 TPMLP_FLAG_SINGLE_SM = 0x2
 TPMLP_FLAG_SWIGLU = 0x4
 TPMLP_FLAG_FIXED_ORDER = 0x8
+TPMLP_FLAG_KV_E4M3 = 0x10
 TPMLP_LINEAR_COLUMN = 0
 TPMLP_LINEAR_ROW = 1
 TPMLP_NOALLOC_SCRATCH_BYTES = 32 << 20  # the library's fixed scratch for tpmlp_forward_noalloc
@@ -54,6 +59,14 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 
 def library_path() -> str:
     return os.path.join(_PKG, "libtpmlp.so")
+
+
+class KvCache(ctypes.Structure):
+    """tpmlp_kv: a caller's paged key-value cache (pools, page table, lengths)."""
+    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("page_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("table_pages", ctypes.c_int32),
+                ("B", ctypes.c_int32), ("lens", ctypes.c_void_p)]
 
 
 class TpmlpError(RuntimeError):
@@ -109,6 +122,15 @@ def load_library() -> ctypes.CDLL:
                                    vp, vp, vp, vp], ctypes.c_int),
         "tpmlp_backward": ([vp, vp, vp, vp, vp, vp, vp, i64, i64, vp, vp, vp, vp, vp, vp],
                            ctypes.c_int),
+        "tpmlp_attn_create": ([ctypes.POINTER(vp), i32, i32, i32, i32, u32], ctypes.c_int),
+        "tpmlp_attn_set_rope": ([vp, i32, i32, ctypes.POINTER(ctypes.c_double)], ctypes.c_int),
+        "tpmlp_attn_set_scales": ([vp, vp, vp, vp], ctypes.c_int),
+        "tpmlp_attn_append": ([vp, vp, i64, vp, i64, vp, i64, i64, vp, vp, vp, vp, i64, vp],
+                              ctypes.c_int),
+        "tpmlp_attn_decode": ([vp, vp, i64, vp, ctypes.c_float, i32, vp, i64, vp, vp],
+                              ctypes.c_int),
+        "tpmlp_attn_prompt": ([vp, vp, i64, i64, vp, vp, ctypes.c_float, i32, vp, i64, vp, vp],
+                              ctypes.c_int),
         "tpmlp_destroy": ([vp], None),
         "tpmlp_strerror": ([ctypes.c_int], ctypes.c_char_p),
         "tpmlp_last_error": ([vp], ctypes.c_char_p),
@@ -288,7 +310,7 @@ def tpmlp_get_status(ctx: int, stream=None):
     """Returns (status, raw detail word); clears the device status word."""
     detail = ctypes.c_int32(0)
     rc = load_library().tpmlp_get_status(ctx, _stream(stream), ctypes.byref(detail))
-    if rc not in (TPMLP_OK, TPMLP_ERR_DEVICE_TIMEOUT):
+    if rc not in (TPMLP_OK, TPMLP_ERR_DEVICE_TIMEOUT, TPMLP_ERR_BAD_PAGE):
         _check(rc, "tpmlp_get_status", ctx)
     return rc, int(detail.value)
 
@@ -338,6 +360,46 @@ def tpmlp_backward_swiglu(ctx: int, dZ, X, Ysave, Asave, Wg, Wu, W2, B: int, S: 
         ctx, _ptr(dZ), _ptr(X), _ptr(Ysave), _ptr(Asave), _ptr(Wg), _ptr(Wu), _ptr(W2), B, S,
         _ptr(dX), _ptr(dWg), _ptr(dbg), _ptr(dWu), _ptr(dbu), _ptr(dW2), _ptr(db2),
         _stream(stream)), "tpmlp_backward_swiglu", ctx)
+
+
+def tpmlp_attn_create(Hq: int, Hkv: int, D: int, page_size: int, flags: int = 0) -> int:
+    out = ctypes.c_void_p()
+    _check(load_library().tpmlp_attn_create(ctypes.byref(out), Hq, Hkv, D, page_size, flags),
+           "tpmlp_attn_create")
+    return out.value
+
+
+def tpmlp_attn_set_rope(ctx: int, rot_dim: int, interleaved: bool, freq) -> None:
+    """freq: rot_dim / 2 angular frequencies (radians per position), any sequence of floats."""
+    values = (ctypes.c_double * max(1, rot_dim // 2))(*[float(f) for f in freq])
+    _check(load_library().tpmlp_attn_set_rope(ctx, rot_dim, int(interleaved), values),
+           "tpmlp_attn_set_rope", ctx)
+
+
+def tpmlp_attn_set_scales(ctx: int, k_scale, v_scale, stream=None) -> None:
+    _check(load_library().tpmlp_attn_set_scales(ctx, _ptr(k_scale), _ptr(v_scale),
+                                                _stream(stream)), "tpmlp_attn_set_scales", ctx)
+
+
+def tpmlp_attn_append(ctx: int, Q, ldq: int, K, ldk: int, V, ldv: int, T: int, pos, seq,
+                      kv: KvCache, Qout, ldqo: int, stream=None) -> None:
+    _check(load_library().tpmlp_attn_append(
+        ctx, _ptr(Q), ldq, _ptr(K), ldk, _ptr(V), ldv, T, _ptr(pos), _ptr(seq), ctypes.byref(kv),
+        _ptr(Qout), ldqo, _stream(stream)), "tpmlp_attn_append", ctx)
+
+
+def tpmlp_attn_decode(ctx: int, Q, ldq: int, kv: KvCache, scale: float, window: int, Out,
+                      ldo: int, Lse=None, stream=None) -> None:
+    _check(load_library().tpmlp_attn_decode(ctx, _ptr(Q), ldq, ctypes.byref(kv), scale, window,
+                                            _ptr(Out), ldo, _ptr(Lse), _stream(stream)),
+           "tpmlp_attn_decode", ctx)
+
+
+def tpmlp_attn_prompt(ctx: int, Q, ldq: int, T: int, cu_q, kv: KvCache, scale: float,
+                      window: int, Out, ldo: int, Lse=None, stream=None) -> None:
+    _check(load_library().tpmlp_attn_prompt(ctx, _ptr(Q), ldq, T, _ptr(cu_q), ctypes.byref(kv),
+                                            scale, window, _ptr(Out), ldo, _ptr(Lse),
+                                            _stream(stream)), "tpmlp_attn_prompt", ctx)
 
 
 def tpmlp_destroy(ctx) -> None:
@@ -612,3 +674,199 @@ class Linear:
 
     def status(self, stream=None):
         return tpmlp_get_status(self.ctx, stream)
+
+
+class Attention:
+    """Attention over a paged key-value cache for one head layout (tpmlp_attn_*): Hq query heads
+    of size D (64 or 128), Hkv key-value heads, page_size keys per page, a cache in "bf16" or
+    "e4m3".
+
+        attn = Attention(Hq=32, Hkv=8, D=128, page_size=64)
+        attn.set_rope(128)
+        cache = attn.new_cache(num_pages, page_table, lens)      # or PagedCache(attn, K, V, ...)
+        q = attn.append(q, k, v, cache, pos, seq)                # rotate, write k and v
+        out = attn.prompt(q, cu_q, cache)                        # a chunk of each sequence
+        out = attn.decode(q, cache)                              # one token of each sequence
+    """
+
+    def __init__(self, Hq: int, Hkv: int, D: int, page_size: int = 64, kv_dtype: str = "bf16"):
+        if kv_dtype not in ("bf16", "e4m3"):
+            raise ValueError(f"kv_dtype: expected 'bf16' or 'e4m3', got {kv_dtype!r}")
+        self.Hq, self.Hkv, self.D, self.page_size = Hq, Hkv, D, page_size
+        self.kv_dtype = kv_dtype
+        self.ctx = tpmlp_attn_create(Hq, Hkv, D, page_size,
+                                     TPMLP_FLAG_KV_E4M3 if kv_dtype == "e4m3" else 0)
+
+    def close(self):
+        if getattr(self, "ctx", None):
+            tpmlp_destroy(self.ctx)
+            self.ctx = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def set_rope(self, rot_dim: int, theta: float = 10000.0, interleaved: bool = False,
+                 freq=None):
+        """Rotate the first rot_dim dimensions of every query and key head: pair i by
+        position * theta^(-2i / rot_dim), or by position * freq[i]."""
+        if freq is None:
+            freq = [theta ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)]
+        elif len(freq) != rot_dim // 2:
+            raise ValueError(f"freq: expected {rot_dim // 2} values, got {len(freq)}")
+        tpmlp_attn_set_rope(self.ctx, rot_dim, interleaved, freq)
+
+    def set_scales(self, k_scale, v_scale, stream=None):
+        """fp32 CUDA [Hkv] scales of an e4m3 cache (a value is the stored number times them)."""
+        import torch
+        TPMLP._require(k_scale, torch.float32, (self.Hkv,), "k_scale")
+        TPMLP._require(v_scale, torch.float32, (self.Hkv,), "v_scale")
+        tpmlp_attn_set_scales(self.ctx, k_scale, v_scale, stream)
+
+    def pool_dtype(self):
+        import torch
+        return torch.bfloat16 if self.kv_dtype == "bf16" else torch.float8_e4m3fn
+
+    def new_cache(self, num_pages: int, page_table, lens):
+        """A PagedCache with its own (uninitialised) pools on page_table's device."""
+        import torch
+        shape = (num_pages, self.Hkv, self.page_size, self.D)
+        K = torch.empty(shape, dtype=self.pool_dtype(), device=page_table.device)
+        return PagedCache(self, K, torch.empty_like(K), page_table, lens)
+
+    @staticmethod
+    def _rows(t, width, what):
+        """Row pitch of a bf16 CUDA [rows, width] tensor whose rows are contiguous."""
+        import torch
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{what} must be a CUDA tensor")
+        if t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[1] != width or t.stride(1) != 1:
+            raise ValueError(f"{what}: expected bf16 [rows, {width}] with contiguous rows, got "
+                             f"{t.dtype} {tuple(t.shape)} strides {t.stride()}")
+        # the stride of a single row says nothing
+        return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), width)
+
+    @staticmethod
+    def _ints(t, n, what):
+        import torch
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{what} must be a CUDA tensor")
+        if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+            raise ValueError(f"{what}: expected contiguous int32 ({n},), got {t.dtype} "
+                             f"{tuple(t.shape)}")
+
+    def append(self, q, k, v, cache, pos, seq=None, q_out=None, stream=None):
+        """Writes k and v [T, Hkv * D] (k rotated) at positions pos [T] of sequences seq [T]
+        (None: token t is sequence t's) and returns the rotated q [T, Hq * D] (in q_out; q_out=q
+        rotates in place; q None: only k and v). Rows may be column ranges of a wider tensor."""
+        import torch
+        T, wk = k.shape[0], self.Hkv * self.D
+        ldk, ldv = self._rows(k, wk, "k"), self._rows(v, wk, "v")
+        if v.shape[0] != T:
+            raise ValueError("k and v: different numbers of tokens")
+        self._ints(pos, T, "pos")
+        if seq is not None:
+            self._ints(seq, T, "seq")
+        ldq = ldqo = 0
+        if q is not None:
+            ldq = self._rows(q, self.Hq * self.D, "q")
+            if q_out is None:
+                q_out = torch.empty((T, self.Hq * self.D), dtype=torch.bfloat16, device=q.device)
+            ldqo = self._rows(q_out, self.Hq * self.D, "q_out")
+            if q.shape[0] != T or q_out.shape[0] != T:
+                raise ValueError("q and q_out: different numbers of tokens than k")
+        tpmlp_attn_append(self.ctx, q, ldq, k, ldk, v, ldv, T, pos, seq, cache._of(self),
+                          q_out if q is not None else None, ldqo, stream)
+        return q_out if q is not None else None
+
+    def _attend(self, q, rows, out, return_lse):
+        import torch
+        width = self.Hq * self.D
+        ldq = self._rows(q, width, "q")
+        if out is None:
+            out = torch.empty((rows, width), dtype=torch.bfloat16, device=q.device)
+        ldo = self._rows(out, width, "out")
+        if q.shape[0] != rows or out.shape[0] != rows:
+            raise ValueError(f"q and out: expected {rows} rows")
+        lse = (torch.empty((rows, self.Hq), dtype=torch.float32, device=q.device)
+               if return_lse else None)
+        return ldq, out, ldo, lse
+
+    def decode(self, q, cache, scale=None, window: int = 0, out=None, return_lse: bool = False,
+               stream=None):
+        """Attention of one token of each sequence, q [B, Hq * D], over its cache (its own key
+        included: append first). scale: D ** -0.5 by default. Returns out [B, Hq * D], or (out,
+        lse [B, Hq] fp32)."""
+        kv = cache._of(self)
+        ldq, out, ldo, lse = self._attend(q, kv.B, out, return_lse)
+        tpmlp_attn_decode(self.ctx, q, ldq, kv, self.D ** -0.5 if scale is None else scale,
+                          window, out, ldo, lse, stream)
+        return (out, lse) if return_lse else out
+
+    def prompt(self, q, cu_q, cache, scale=None, window: int = 0, out=None,
+               return_lse: bool = False, stream=None):
+        """Causal attention of the new tokens q [T, Hq * D], sequence b's in rows cu_q[b] ..
+        cu_q[b + 1] - 1 (cu_q int32 [B + 1]), over the caches that already hold their keys."""
+        kv = cache._of(self)
+        self._ints(cu_q, kv.B + 1, "cu_q")
+        T = q.shape[0]
+        ldq, out, ldo, lse = self._attend(q, T, out, return_lse)
+        tpmlp_attn_prompt(self.ctx, q, ldq, T, cu_q, kv, self.D ** -0.5 if scale is None else scale,
+                          window, out, ldo, lse, stream)
+        return (out, lse) if return_lse else out
+
+    def status(self, stream=None):
+        return tpmlp_get_status(self.ctx, stream)
+
+    @property
+    def launches(self) -> int:
+        return tpmlp_launch_count(self.ctx)
+
+
+class PagedCache:
+    """The cache an Attention's calls read and write: pools K, V [num_pages, Hkv, page_size, D]
+    (bf16 or float8_e4m3fn; both with the same page stride, each page contiguous), page_table
+    int32 [B, pages] and lens int32 [B]. It holds references to the tensors; their contents may
+    change between calls (a table or lengths updated in place)."""
+
+    def __init__(self, attn: Attention, K, V, page_table, lens):
+        import torch
+        for t, what in ((K, "K"), (V, "V")):
+            if not isinstance(t, torch.Tensor) or not t.is_cuda:
+                raise TypeError(f"{what} must be a CUDA tensor")
+            shape = (attn.Hkv, attn.page_size, attn.D)
+            if t.dtype != attn.pool_dtype() or t.dim() != 4 or tuple(t.shape[1:]) != shape:
+                raise ValueError(f"{what}: expected {attn.pool_dtype()} [pages, {attn.Hkv}, "
+                                 f"{attn.page_size}, {attn.D}], got {t.dtype} {tuple(t.shape)}")
+            if t.stride()[1:] != (attn.page_size * attn.D, attn.D, 1):
+                raise ValueError(f"{what}: the pages must be contiguous")
+        if K.shape != V.shape or (K.shape[0] > 1 and K.stride(0) != V.stride(0)):
+            raise ValueError("K and V: expected the same number of pages and page stride")
+        if not isinstance(page_table, torch.Tensor) or not page_table.is_cuda:
+            raise TypeError("page_table must be a CUDA tensor")
+        if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.stride(1) != 1:
+            raise ValueError("page_table: expected int32 [B, pages] with contiguous rows")
+        B, pages = page_table.shape
+        page = attn.Hkv * attn.page_size * attn.D
+        if (K.shape[0] > 1 and K.stride(0) < page) or (B > 1 and page_table.stride(0) < pages):
+            raise ValueError("K, V, page_table: pages or rows that overlap in memory")
+        Attention._ints(lens, B, "lens")
+        self.K, self.V, self.page_table, self.lens = K, V, page_table, lens
+        self._layout = (attn.Hkv, attn.D, attn.page_size, attn.kv_dtype)
+        # the stride of a single page or row says nothing (0: dense)
+        self._kv = KvCache(K.data_ptr(), V.data_ptr(), K.shape[0],
+                           K.stride(0) if K.shape[0] > 1 else 0, page_table.data_ptr(),
+                           page_table.stride(0) if B > 1 else 0, pages, B, lens.data_ptr())
+
+    def _of(self, attn: Attention) -> KvCache:
+        if self._layout != (attn.Hkv, attn.D, attn.page_size, attn.kv_dtype):
+            raise ValueError("the cache was laid out for another head layout, page size or type")
+        return self._kv

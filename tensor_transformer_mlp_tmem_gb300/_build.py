@@ -67,7 +67,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), out: str =
     tmp = lib + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
            "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr", "-I", INCLUDE,
-           "-I", CSRC, "-DTPMLP_BUILD", f'-DTPMLP_SOURCE_HASH="{source_hash(extra_flags)}"',
+           "-I", CSRC, "--threads", "0", "-DTPMLP_BUILD", f'-DTPMLP_SOURCE_HASH="{source_hash(extra_flags)}"',
            *extra_flags, *sources(), "-o", tmp]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")

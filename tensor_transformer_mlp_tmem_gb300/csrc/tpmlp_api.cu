@@ -14,96 +14,13 @@
 #include <string>
 
 #include "tpmlp.h"
+#include "tpmlp_context.h"
 #include "tpmlp_gemm.cuh"
 #include "tpmlp_gemm_2sm.cuh"
 #include "tpmlp_norm.cuh"
 #include "tpmlp_reduce.cuh"
 #include "tpmlp_pack.cuh"
 #include "tpmlp_plan.h"
-
-// Row chunks of tpmlp_forward_host's pipeline at most (sizes the context's event arrays).
-#ifndef TPMLP_HOST_CHUNKS_MAX
-#define TPMLP_HOST_CHUNKS_MAX 4
-#endif
-static_assert(TPMLP_HOST_CHUNKS_MAX >= 1 && TPMLP_HOST_CHUNKS_MAX <= 16, "host chunk limit");
-
-struct tpmlp_ctx {
-    int device = -1;
-    int num_sms = 0;
-    int64_t H = 0, F = 0, f = 0;
-    int32_t k = 0;
-    uint32_t flags = 0;
-    int bn1 = 0, bn2 = 0;  // output tile widths of GEMM1 / GEMM2
-
-    uint16_t* W1p = nullptr;  // [k][f][H]  (gated: [k][2f][H])
-    uint16_t* W2p = nullptr;  // [k][H][f]
-    float* b1 = nullptr;      // [F]        (gated: [2F])
-    float* b2 = nullptr;      // [H]
-    bool packed = false;
-    CUtensorMap tmW1{}, tmW2{};            // B boxes for the single-SM kernel (BN rows)
-    CUtensorMap tmW1_pair{}, tmW2_pair{};  // B boxes for the CTA-pair kernel (128 rows)
-    bool pair1 = false, pair2 = false;     // GEMM1 / GEMM2 run on CTA pairs
-    int kind = 0;        // 0: MLP block; 1: column-parallel linear; 2: row-parallel linear
-    bool gated = false;  // SwiGLU block: W1p holds gate and up rows interleaved
-    int gate_block = 0;  // G: gate/up interleave block (output columns per half-tile)
-
-    uint16_t* Y = nullptr;  // [y_rows][F] intermediate activations
-    int64_t y_rows = 0;
-    void* Xs = nullptr;  // staging for tpmlp_forward_host
-    void* Zs = nullptr;
-    int64_t stage_rows = 0;
-    cudaStream_t s_in = nullptr, s_out = nullptr;  // its copy streams (created on first use)
-    cudaEvent_t host_ev[TPMLP_HOST_CHUNKS_MAX + 1] = {}, in_ev[TPMLP_HOST_CHUNKS_MAX] = {},
-                out_ev[TPMLP_HOST_CHUNKS_MAX] = {};
-    // row chunks of the last tpmlp_forward_host call (re-planned when M changes)
-    int64_t plan_M = -1;
-    int plan_n = 0;
-    int64_t plan_rows[TPMLP_HOST_CHUNKS_MAX] = {};
-    // tpmlp_forward_host_async: two staging slots used in turn, so that a call's copies in and
-    // out overlap the kernels of the calls before and after it
-    void* Xa[2] = {};
-    void* Za[2] = {};
-    int64_t async_rows = 0;
-    cudaEvent_t a_in[2] = {}, a_xfree[2] = {}, a_zready[2] = {}, a_zfree[2] = {};
-    bool a_used[2] = {};
-    uint32_t a_calls = 0;
-
-    // activation tensor maps of the last call (re-encoded only when pointer or rows change)
-    const void* x_map_ptr = nullptr;
-    int64_t x_map_rows = -1;
-    CUtensorMap tmX{};
-    const void* y_map_ptr = nullptr;
-    int64_t y_map_rows = -1;
-    CUtensorMap tmY{};
-
-    // LayerNorm in front of the block (tpmlp_set_layernorm / tpmlp_block_forward)
-    float* ln_gamma = nullptr;  // [H] fp32
-    float* ln_beta = nullptr;   // [H] fp32
-    float ln_eps = 0.0f;
-    bool ln_set = false;
-    uint16_t* Xn = nullptr;  // [xn_rows][H] normalised block input
-    int64_t xn_rows = 0;
-
-    // backward pass
-    float* zeros = nullptr;        // [max(H, F)] fp32 zeros: the "no bias" of dX
-    float* colsum = nullptr;       // partial column sums for the bias gradients
-    int64_t colsum_floats = 0;
-    uint16_t* dgu = nullptr;       // gated backward: dG and dU, [rows][2F] bf16
-    int64_t dgu_elems = 0;
-
-    // split reduction of the last tiles on CTA pairs (absent with TPMLP_FLAG_FIXED_ORDER)
-    float* sk_partial = nullptr;  // [num_sms / 2 pairs][2 units][2 CTAs][128 x 256] fp32 partials
-    uint32_t* sk_count = nullptr; // [num_sms split tiles][2 CTAs][epilogue warps] arrivals
-    uint32_t sk_epoch = 0;
-
-    tpmlp::DeviceRates rates{};  // the planners' rates (device_rates, or tpmlp_set_device_rates)
-    // row group of the tall units' sweep, for the last (512-row blocks, column blocks, pairs)
-    int tall_group = 8, tall_group_m = -1, tall_group_n = -1, tall_group_pairs = -1;
-
-    int* status = nullptr;  // device status word
-    int64_t launches = 0;
-    std::string last_error;
-};
 
 // Tile rasterisation: consecutive tiles walk down this many row blocks before moving to the
 // next column block, so the CTAs that run at the same time share operand tiles in L2.
@@ -137,22 +54,23 @@ constexpr int kHostChunksMax = TPMLP_HOST_CHUNKS_MAX;  // row chunks of tpmlp_fo
 using tpmlp::GemmArgs;
 using tpmlp::Mode;
 
+using tpmlp::aligned16;
+using tpmlp::check_device;
+using tpmlp::fail_cuda;
+using tpmlp::get_encoder;
+
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 cudaError_t g_encode_err = cudaSuccess;
+
+}  // namespace
+
+namespace tpmlp {
 
 int fail_cuda(tpmlp_ctx* c, cudaError_t e, const char* what) {
     if (c) c->last_error = std::string(what) + ": " + cudaGetErrorString(e);
     return e == cudaErrorMemoryAllocation ? TPMLP_ERR_OOM : TPMLP_ERR_CUDA;
 }
-
-#define TPMLP_CUDA(ctx, call)                                   \
-    do {                                                        \
-        cudaError_t e_ = (call);                                \
-        if (e_ != cudaSuccess) return fail_cuda(ctx, e_, #call); \
-    } while (0)
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int get_encoder(tpmlp_ctx* c) {
     std::call_once(g_encode_once, [] {
@@ -169,10 +87,11 @@ int get_encoder(tpmlp_ctx* c) {
     return TPMLP_OK;
 }
 
-// bf16 tensor map with the 128-byte swizzle; dims/strides innermost first, strides in bytes
-// for dims 1..rank-1. Out-of-range boxes are zero filled.
-int encode_map(tpmlp_ctx* c, CUtensorMap* map, const void* ptr, int rank, const uint64_t* dims,
-               const uint64_t* strides, const uint32_t* box) {
+// Tensor map with the 128-byte swizzle; dims/strides innermost first, strides in bytes for
+// dims 1..rank-1. Out-of-range boxes are zero filled.
+int encode_map_typed(tpmlp_ctx* c, CUtensorMap* map, CUtensorMapDataType type, const void* ptr,
+                     int rank, const uint64_t* dims, const uint64_t* strides,
+                     const uint32_t* box) {
     int rc = get_encoder(c);
     if (rc) return rc;
     cuuint64_t d[3], s[2];
@@ -182,14 +101,25 @@ int encode_map(tpmlp_ctx* c, CUtensorMap* map, const void* ptr, int rank, const 
         b[i] = box[i];
     }
     for (int i = 0; i + 1 < rank; ++i) s[i] = strides[i];
-    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(ptr), d, s,
-                          b, e, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    CUresult r = g_encode(map, type, rank, const_cast<void*>(ptr), d, s, b, e,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         c->last_error = "cuTensorMapEncodeTiled failed with CUresult " + std::to_string(int(r));
         return TPMLP_ERR_CUDA;
     }
     return TPMLP_OK;
+}
+
+}  // namespace tpmlp
+
+namespace {
+
+// A bf16 map.
+int encode_map(tpmlp_ctx* c, CUtensorMap* map, const void* ptr, int rank, const uint64_t* dims,
+               const uint64_t* strides, const uint32_t* box) {
+    return tpmlp::encode_map_typed(c, map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ptr, rank, dims,
+                                   strides, box);
 }
 
 int pick_bn(int64_t width) {
@@ -443,7 +373,6 @@ GemmArgs base_args(const tpmlp_ctx* c, int64_t M, int ldo, int bm, int bn, int g
     return a;
 }
 
-constexpr int kKindBlock = 0, kKindColumn = 1, kKindRow = 2;
 
 #ifdef TPMLP_TEST_HOOKS
 // Test builds only: a device index that the current-device query reports instead of the real
@@ -462,6 +391,10 @@ cudaError_t current_device(int* dev) {
     return cudaGetDevice(dev);
 }
 
+}  // namespace
+
+namespace tpmlp {
+
 // The context's device must be current on the calling thread: the context's buffers, tensor
 // maps and kernel attributes belong to that device, and a launch would otherwise run on
 // another GPU with them. Every entry point that enqueues work or touches the context's device
@@ -477,6 +410,12 @@ int check_device(tpmlp_ctx* c) {
     }
     return TPMLP_OK;
 }
+
+}  // namespace tpmlp
+
+namespace {
+
+bool is_linear(const tpmlp_ctx* c) { return c->kind == kKindColumn || c->kind == kKindRow; }
 
 // An MLP-block context on the current device whose weights are packed.
 int check_ctx(tpmlp_ctx* c) {
@@ -1252,7 +1191,8 @@ int tpmlp_host_wait(tpmlp_ctx* c) {
 int tpmlp_set_layernorm(tpmlp_ctx* c, const void* gamma, const void* beta, float eps,
                         void* stream) {
     // the block's input, or a column-parallel layer's input (LayerNorm before Q/K/V)
-    if (!c || !gamma || !beta || c->kind == kKindRow) return TPMLP_ERR_INVALID_ARG;
+    if (!c || !gamma || !beta || c->kind == kKindRow || c->kind == kKindAttention)
+        return TPMLP_ERR_INVALID_ARG;
     if (int rc = check_device(c)) return rc;
     if (!(eps >= 0.0f) || eps > 1.0f) return TPMLP_ERR_INVALID_ARG;  // also rejects NaN
     if (c->H > tpmlp::kNormMaxH) return TPMLP_ERR_UNSUPPORTED_SHAPE;
@@ -1357,7 +1297,7 @@ int tpmlp_gemm2_residual(tpmlp_ctx* c, const void* Y, int64_t M, void* Z, const 
 }
 
 int tpmlp_linear_pack(tpmlp_ctx* c, const void* W, const void* b, void* stream) {
-    if (!c || !W || !b || c->kind == kKindBlock) return TPMLP_ERR_INVALID_ARG;
+    if (!c || !W || !b || !is_linear(c)) return TPMLP_ERR_INVALID_ARG;
     if (int rc = check_device(c)) return rc;
     if (!aligned16(W) || (reinterpret_cast<uintptr_t>(b) & 1)) return TPMLP_ERR_MISALIGNED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1385,7 +1325,7 @@ int tpmlp_linear_pack(tpmlp_ctx* c, const void* W, const void* b, void* stream) 
 }
 
 int tpmlp_linear_forward(tpmlp_ctx* c, const void* X, int64_t M, void* out, void* stream) {
-    if (!c || c->kind == kKindBlock || M < 0) return TPMLP_ERR_INVALID_ARG;
+    if (!c || !is_linear(c) || M < 0) return TPMLP_ERR_INVALID_ARG;
     if (int rc = check_device(c)) return rc;
     if (!c->packed) return TPMLP_ERR_NOT_PACKED;
     if (M == 0) return TPMLP_OK;
@@ -1617,6 +1557,7 @@ int tpmlp_get_status(tpmlp_ctx* c, void* stream, int32_t* detail) {
     TPMLP_CUDA(c, cudaMemcpy(&v, c->status, sizeof(int), cudaMemcpyDeviceToHost));
     TPMLP_CUDA(c, cudaMemset(c->status, 0, sizeof(int)));
     if (detail) *detail = v;
+    if (v & kStatusBadPage) return TPMLP_ERR_BAD_PAGE;
     return v ? TPMLP_ERR_DEVICE_TIMEOUT : TPMLP_OK;
 }
 
@@ -1672,6 +1613,9 @@ void tpmlp_destroy(tpmlp_ctx* c) {
     cudaFree(c->ln_beta);
     cudaFree(c->sk_partial);
     cudaFree(c->sk_count);
+    cudaFree(c->kv_scale);
+    cudaFree(c->attn_partial);
+    cudaFree(c->attn_count);
     cudaFree(c->status);
     if (cur >= 0 && cur != c->device) cudaSetDevice(cur);
     delete c;
@@ -1688,6 +1632,7 @@ const char* tpmlp_strerror(int status) {
         case TPMLP_ERR_DEVICE_TIMEOUT: return "a kernel gave up waiting on a pipeline barrier";
         case TPMLP_ERR_ARCH: return "device is not sm_103 (GB300)";
         case TPMLP_ERR_MISALIGNED: return "device pointer not 16-byte aligned";
+        case TPMLP_ERR_BAD_PAGE: return "a page table named a page outside the pool, or a position lay outside the table";
         default: return "unknown status";
     }
 }

@@ -1,0 +1,762 @@
+// Attention over a paged key-value cache: the append kernel (rotation, page writes) and the
+// row kernel (attention of one token's query heads over a range of keys), which serves decode.
+//
+// A pool is [num_pages][Hkv][page][D]: the keys of one head in one page are contiguous, so a
+// warp that walks a head's keys reads whole 16-byte pieces of whole rows, whatever the page size.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <math_constants.h>
+
+#include "sm103_ptx.cuh"
+#include "tpmlp_context.h"
+
+namespace tpmlp {
+
+// The caller's cache and the context's head layout, as the kernels read them.
+struct KvView {
+    uint8_t* K;
+    uint8_t* V;
+    int64_t page_bytes;   // from page to page of a pool
+    int64_t head_bytes;   // from head to head of a page
+    const int32_t* table;
+    int64_t table_stride;
+    int32_t table_pages;
+    int32_t page_shift;   // log2 of the keys per page
+    int64_t num_pages;
+    const int32_t* lens;
+    int32_t B;
+    int32_t Hkv;
+    const float* scales;  // e4m3: [2][Hkv] k and v scales
+    int* status;
+};
+
+__device__ __forceinline__ void report_bad_page(int* status) {
+    atomicCAS(status, 0, kStatusBadPage);
+}
+
+// Keys of sequence b: its length held to [0, the table's capacity].
+__device__ __forceinline__ int kv_length(const KvView& kv, int b) {
+    int len = kv.lens[b];
+    const int64_t most = static_cast<int64_t>(kv.table_pages) << kv.page_shift;
+    if (len > most) {
+        report_bad_page(kv.status);
+        len = static_cast<int>(most);
+    }
+    return max(len, 0);
+}
+
+// The page that holds key `key` (inside the table) of sequence b; -1, reported, if the table
+// names none of the pool's.
+__device__ __forceinline__ int64_t kv_page(const KvView& kv, int b, int key) {
+    const int64_t p = kv.table[b * kv.table_stride + (key >> kv.page_shift)];
+    if (p >= 0 && p < kv.num_pages) return p;
+    report_bad_page(kv.status);
+    return -1;
+}
+
+// ------------------------------------------------------------------ append
+struct AppendArgs {
+    KvView kv;
+    const __nv_bfloat16 *q, *k, *v;
+    int64_t ldq, ldk, ldv;
+    __nv_bfloat16* q_out;
+    int64_t ldqo;
+    const int32_t *pos, *seq;
+    int32_t Hq;         // 0: no queries
+    int32_t rot;        // rotated dimensions, a multiple of 16
+    int32_t interleaved;
+    double turns[64];   // whole turns per position of each pair
+};
+
+constexpr int kAppendThreads = 256;
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+
+__device__ __forceinline__ uint4 pack8_bf16(const float (&f)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// x / scale to e4m3, to nearest even, held to +-448 (NaN stays NaN).
+__device__ __forceinline__ uint2 pack8_e4m3(const float (&f)[8], float scale) {
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(
+            make_float2(f[2 * i] / scale, f[2 * i + 1] / scale), __NV_SATFINITE, __NV_E4M3);
+        w[i >> 1] |= static_cast<uint32_t>(h) << (16 * (i & 1));
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+// One block per token. The rotation's sines and cosines are the same for all heads: the block
+// computes the token's rot / 2 of them once, in shared memory. The angle is taken in whole turns
+// in fp64 and reduced to [-1/2, 1/2] there, so its error is that of the fp32 result however far
+// the position (an fp32 product would be off by whole radians at position 10^7). Then each thread
+// rotates units of 16 elements: the 8 dimensions from 8u and their partners, which are the 8 from
+// rot/2 + 8u (halves) or the same 16 (neighbours).
+template <int D, bool FP8>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendArgs a) {
+    __shared__ float2 trig[D / 2];
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    const int64_t t = blockIdx.x;
+    const int pos = a.pos[t];
+    if (pos < 0) return;
+    const int half = a.rot >> 1;
+    for (int i = threadIdx.x; i < half; i += kAppendThreads) {
+        const double turn = pos * a.turns[i];
+        float s, c;
+        sincospif(2.0f * static_cast<float>(turn - rint(turn)), &s, &c);
+        trig[i] = make_float2(c, s);
+    }
+    const int b = a.seq ? a.seq[t] : static_cast<int>(t);
+    int64_t page = -1;
+    if (b >= 0 && b < a.kv.B && t <= 0x7FFFFFFF && (pos >> a.kv.page_shift) < a.kv.table_pages)
+        page = kv_page(a.kv, b, pos);
+    else if (threadIdx.x == 0)
+        report_bad_page(a.kv.status);
+    __syncthreads();
+    const int slot = pos & ((1 << a.kv.page_shift) - 1);
+    constexpr int kUnits = D / 16;  // units per head
+    const int heads = a.Hq + 2 * a.kv.Hkv;
+    for (int i = threadIdx.x; i < heads * kUnits; i += kAppendThreads) {
+        const int head = i / kUnits, u = i % kUnits;
+        const bool is_q = head < a.Hq, is_v = head >= a.Hq + a.kv.Hkv;
+        if (!is_q && page < 0) continue;
+        const int h = is_q ? head : is_v ? head - a.Hq - a.kv.Hkv : head - a.Hq;
+        const __nv_bfloat16* src = (is_q ? a.q + t * a.ldq : is_v ? a.v + t * a.ldv : a.k + t * a.ldk) +
+                                   static_cast<int64_t>(h) * D;
+        const bool rotate = !is_v && 16 * u < a.rot;
+        // the unit's two pieces of 8 dimensions
+        int d0 = 16 * u, d1 = d0 + 8;
+        if (rotate && !a.interleaved) {
+            d0 = 8 * u;
+            d1 = half + d0;
+        }
+        float x[8], y[8];
+        unpack8(*reinterpret_cast<const uint4*>(src + d0), x);
+        unpack8(*reinterpret_cast<const uint4*>(src + d1), y);
+        if (rotate) {
+            if (a.interleaved) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 r0 = trig[8 * u + j], r1 = trig[8 * u + 4 + j];
+                    const float x0 = x[2 * j], y0 = y[2 * j];
+                    x[2 * j] = x0 * r0.x - x[2 * j + 1] * r0.y;
+                    x[2 * j + 1] = x[2 * j + 1] * r0.x + x0 * r0.y;
+                    y[2 * j] = y0 * r1.x - y[2 * j + 1] * r1.y;
+                    y[2 * j + 1] = y[2 * j + 1] * r1.x + y0 * r1.y;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float2 r = trig[8 * u + j];
+                    const float x0 = x[j];
+                    x[j] = x0 * r.x - y[j] * r.y;
+                    y[j] = y[j] * r.x + x0 * r.y;
+                }
+            }
+        }
+        if (is_q || !FP8) {
+            __nv_bfloat16* dst =
+                is_q ? a.q_out + t * a.ldqo + static_cast<int64_t>(h) * D
+                     : reinterpret_cast<__nv_bfloat16*>((is_v ? a.kv.V : a.kv.K) + page * a.kv.page_bytes +
+                                                        h * a.kv.head_bytes) +
+                           static_cast<int64_t>(slot) * D;
+            *reinterpret_cast<uint4*>(dst + d0) = pack8_bf16(x);
+            *reinterpret_cast<uint4*>(dst + d1) = pack8_bf16(y);
+        } else {
+            uint8_t* dst = (is_v ? a.kv.V : a.kv.K) + page * a.kv.page_bytes + h * a.kv.head_bytes +
+                           static_cast<int64_t>(slot) * D;
+            const float scale = a.kv.scales[(is_v ? a.kv.Hkv : 0) + h];
+            *reinterpret_cast<uint2*>(dst + d0) = pack8_e4m3(x, scale);
+            *reinterpret_cast<uint2*>(dst + d1) = pack8_e4m3(y, scale);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ rows
+// Attention of single tokens: row r (a decode sequence, or one token of a prompt) has G query
+// heads to each kv head, and attends to keys [lo, hi) of its sequence.
+struct RowArgs {
+    KvView kv;
+    const __nv_bfloat16* q;
+    int64_t ldq;
+    __nv_bfloat16* out;
+    int64_t ldo;
+    float* lse;             // [rows][Hq] or null
+    const int32_t* cu_q;    // prompt: [B + 1]
+    int32_t rows;
+    int32_t Hq, G;
+    int32_t blocks_per_head;  // blocks of 8 * NT query heads that share a kv head
+    float scale_log2;         // softmax scale * log2(e)
+    int32_t window;
+    float* partial;         // [CTAs][2] slots of RowSlot floats
+    uint32_t* count;        // [CTAs] arrivals, 0 between launches
+};
+
+constexpr int kRowWarps = 8;
+constexpr int kRowThreads = 32 * kRowWarps;
+// fp32 values of a partial sum: O [16][128], m [16], l [16].
+constexpr int kRowSlotFloats = 16 * 128 + 32;
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1, bool half) {
+    if (half)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transpose of an 8 x 8 matrix of 16-bit values spread over the warp (lane 4 r + c holds row r,
+// columns 2 c and 2 c + 1).
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t v) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v), __NV_E4M3);
+    return static_cast<uint32_t>(h.x) | static_cast<uint32_t>(h.y) << 16;
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_bf162(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Loads of what another kernel of the stream may have just written: through L2 (the read-only
+// path must not be used while this kernel may overlap the writer's end).
+__device__ __forceinline__ uint4 load16(const uint8_t* p) {
+    return __ldcg(reinterpret_cast<const uint4*>(p));
+}
+
+// Keys of row r: sequence b, [lo, hi).
+struct RowRange {
+    int b, lo, hi;
+    bool write;
+};
+
+template <bool PROMPT>
+__device__ __forceinline__ RowRange row_range(const RowArgs& a, int r) {
+    RowRange x{r, 0, 0, true};
+    if constexpr (PROMPT) {
+        // the last sequence that starts at or before r
+        int lo = 0, hi = a.kv.B;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (a.cu_q[mid] <= r) lo = mid;
+            else hi = mid;
+        }
+        x.b = lo;
+        const int first = a.cu_q[lo], next = a.cu_q[lo + 1];
+        x.write = r >= first && r < next;
+        if (!x.write) return x;
+        const int len = kv_length(a.kv, lo);
+        x.hi = min(max(len - next + r + 1, 0), len);
+    } else {
+        x.hi = kv_length(a.kv, r);
+    }
+    if (a.window > 0) x.lo = max(0, x.hi - a.window);
+    return x;
+}
+
+// The kernel's shape. A warp takes KT keys at a time and holds all their K and V in registers
+// (8 KB of cache per warp and iteration): K rows are the A operand of S^T = K Q^T (16 keys x 8
+// query heads a matrix instruction), so the loads are whole 16-byte pieces of the rows as they
+// lie in memory, in an order of the reduction index that Q's registers share; V is the A operand
+// of O^T = V^T P^T, its pairs of keys put together with byte permutes. No shared memory, no
+// barriers and no copies are needed on the way: the bound is DRAM.
+template <int D, bool FP8, int NT>
+struct RowShape {
+    static constexpr int kElem = FP8 ? 1 : 2;
+    static constexpr int kSub = 256 / (D * kElem);   // subtiles of 16 keys
+    static constexpr int KT = 16 * kSub;
+    static constexpr int kStep = KT * kRowWarps;     // keys of a CTA's step
+    static constexpr int kRows = 8 * NT;             // query heads of a block
+    static constexpr int NK = D * kElem / 64;        // 16-byte pieces of a K row per thread
+    static constexpr int NV = D / 8;                 // V dimensions per thread
+    static constexpr int kQRegs = D / 8;             // Q registers per 8 query heads
+    static constexpr int kPitch = D + 4;             // fp32 row of the merge buffer
+    static constexpr int kSmem = kRowWarps * kRows * (kPitch + 2) * 4;
+};
+
+// The dimension that element e of lane group g's V registers stands for.
+template <int D, bool FP8>
+__device__ __forceinline__ int v_dim(int g, int e) {
+    if constexpr (D == 128 && !FP8) return e < 8 ? 8 * g + e : 64 + 8 * g + (e - 8);
+    else return (D / 8) * g + e;
+}
+
+template <int D, bool FP8, int NT, bool PROMPT>
+__global__ void __launch_bounds__(kRowThreads, NT == 1 ? 2 : 1)
+attn_row_kernel(const __grid_constant__ RowArgs a) {
+    using S = RowShape<D, FP8, NT>;
+    extern __shared__ float smem[];
+    float* const sO = smem;                                       // [warps][rows][pitch]
+    float* const sM = sO + kRowWarps * S::kRows * S::kPitch;      // [warps][rows]
+    float* const sL = sM + kRowWarps * S::kRows;                  // [warps][rows]
+    __shared__ int64_t s_scan[kRowWarps + 1];
+    __shared__ int64_t s_found[2];
+    __shared__ uint32_t s_last;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, t = lane & 3;
+
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+
+    auto steps_of = [&](const RowRange& x) {
+        return max(1, (x.hi - (x.lo & ~15) + S::kStep - 1) / S::kStep);
+    };
+    // Sum of the rows' steps: the work of every (row, kv head, block of query heads) segment is
+    // its row's steps, and each CTA takes an equal run of all segments' steps.
+    const int64_t per_row = static_cast<int64_t>(a.kv.Hkv) * a.blocks_per_head;
+    int64_t mine = 0;
+    for (int r = tid; r < a.rows; r += kRowThreads) mine += steps_of(row_range<PROMPT>(a, r));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(~0u, mine, o);
+    if (lane == 0) s_scan[warp] = mine;
+    __syncthreads();
+    int64_t total = 0;
+#pragma unroll
+    for (int w = 0; w < kRowWarps; ++w) total += s_scan[w];
+    total *= per_row;
+    const int64_t per_cta = (total + gridDim.x - 1) / gridDim.x;
+    int64_t at = per_cta * blockIdx.x;
+    const int64_t end = min(at + per_cta, total);
+    if (at >= end) return;
+
+    // The row that holds this CTA's first step.
+    {
+        int64_t before = 0;
+        for (int r0 = 0; r0 < a.rows; r0 += kRowThreads) {
+            const int r = r0 + tid;
+            const int64_t c = r < a.rows ? steps_of(row_range<PROMPT>(a, r)) : 0;
+            int64_t sum = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t v = __shfl_up_sync(~0u, sum, o);
+                if (lane >= o) sum += v;
+            }
+            __syncthreads();
+            if (lane == 31) s_scan[warp] = sum;
+            if (tid == 0) s_found[0] = -1;
+            __syncthreads();
+            int64_t base = before;
+            for (int w = 0; w < warp; ++w) base += s_scan[w];
+            const int64_t first = (base + sum - c) * per_row;
+            if (r < a.rows && at >= first && at < first + c * per_row) {
+                s_found[0] = r;
+                s_found[1] = first;
+            }
+            for (int w = 0; w < kRowWarps; ++w) before += s_scan[w];
+            __syncthreads();
+            if (s_found[0] >= 0) break;
+        }
+    }
+    if (s_found[0] < 0) return;  // only if the lengths changed during the launch
+    int row = static_cast<int>(s_found[0]);
+    RowRange range = row_range<PROMPT>(a, row);
+    int steps = steps_of(range);
+    int64_t segment_start;  // first step of the current segment
+    int part;               // kv head * blocks_per_head + block
+    {
+        const int64_t into = at - s_found[1];
+        part = static_cast<int>(into / steps);
+        segment_start = s_found[1] + static_cast<int64_t>(part) * steps;
+    }
+
+    while (at < end) {
+        const int step0 = static_cast<int>(at - segment_start);
+        const int n = static_cast<int>(min(static_cast<int64_t>(steps - step0), end - at));
+        const int h = part / a.blocks_per_head;
+        const int q0 = (part % a.blocks_per_head) * S::kRows;  // first query head of the block
+        const int valid = min(a.G - q0, S::kRows);
+
+        // Q: the reduction order of the K pieces. In the 8-bit cache's fp16 products each row is
+        // scaled by a power of two to a largest magnitude in [1, 2), so that no bf16 value
+        // overflows; the scores are scaled back.
+        uint32_t qr[NT][S::kQRegs];
+        float c_log2[NT][2];  // score -> log2 units, for the lane's query columns 2 t, 2 t + 1
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int qi = nt * 8 + g;
+            const __nv_bfloat16* src =
+                a.q + row * a.ldq + (static_cast<int64_t>(h) * a.G + q0 + qi) * D;
+            const bool on = qi < valid;
+            if constexpr (!FP8) {
+#pragma unroll
+                for (int j = 0; j < S::NK; ++j) {
+                    const uint4 v = on ? load16(reinterpret_cast<const uint8_t*>(src + 8 * (t + 4 * j)))
+                                       : make_uint4(0, 0, 0, 0);
+                    qr[nt][4 * j] = v.x;
+                    qr[nt][4 * j + 1] = v.y;
+                    qr[nt][4 * j + 2] = v.z;
+                    qr[nt][4 * j + 3] = v.w;
+                }
+                c_log2[nt][0] = c_log2[nt][1] = a.scale_log2;
+            } else {
+                float x[S::NK][2][8];
+                float big = 0.0f;
+#pragma unroll
+                for (int j = 0; j < S::NK; ++j)
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        const uint4 v =
+                            on ? load16(reinterpret_cast<const uint8_t*>(src + 16 * (t + 4 * j) + 8 * p))
+                               : make_uint4(0, 0, 0, 0);
+                        unpack8(v, x[j][p]);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(x[j][p][i]));
+                    }
+                big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
+                big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
+                // exponent of the row's largest magnitude (rows of zeros, infinities and the
+                // ends of the exponent range stay as they are)
+                int e = static_cast<int>(__float_as_uint(big) >> 23) - 127;
+                if (e < -100 || e > 100) e = 0;
+                const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+                for (int j = 0; j < S::NK; ++j)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        qr[nt][8 * j + i] = pack_half2(x[j][i >> 2][2 * (i & 3)] * down,
+                                                       x[j][i >> 2][2 * (i & 3) + 1] * down);
+                const float ks = a.scale_log2 * a.kv.scales[h];
+                c_log2[nt][0] = ks * __shfl_sync(~0u, up, 8 * t);
+                c_log2[nt][1] = ks * __shfl_sync(~0u, up, 8 * t + 4);
+            }
+        }
+
+        float o[NT][S::NV / 2][4];  // O^T: (dim e, q 2t), (dim e, q 2t+1), (dim e + NV/2, ...)
+        float m[NT][2], l[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            m[nt][0] = m[nt][1] = -CUDART_INF_F;
+            l[nt][0] = l[nt][1] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < S::NV / 2; ++i)
+                o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.0f;
+        }
+
+        const int64_t head_off = h * a.kv.head_bytes;
+        const int lo16 = range.lo & ~15;
+        for (int it = 0; it < n; ++it) {
+            const int key0 = lo16 + ((step0 + it) * kRowWarps + warp) * S::KT;
+            if (key0 >= range.hi) break;  // the warp's keys only grow
+            uint4 kr[S::kSub][2][S::NK];
+            uint4 vr[S::kSub][4][S::NV * S::kElem >= 16 ? S::NV * S::kElem / 16 : 1];
+            bool ok[S::kSub];
+#pragma unroll
+            for (int u = 0; u < S::kSub; ++u) {
+                const int kb = key0 + 16 * u;
+                int64_t page = -1;
+                if (kb < range.hi) page = kv_page(a.kv, range.b, kb);
+                ok[u] = page >= 0;
+                const int64_t off = page * a.kv.page_bytes + head_off +
+                                    static_cast<int64_t>(kb & ((1 << a.kv.page_shift) - 1)) * (D * S::kElem);
+                const uint8_t* kp = a.kv.K + off;
+                const uint8_t* vp = a.kv.V + off;
+#pragma unroll
+                for (int rr = 0; rr < 2; ++rr) {
+                    const int key = kb + g + 8 * rr;
+                    const bool on = ok[u] && key >= range.lo && key < range.hi;
+#pragma unroll
+                    for (int j = 0; j < S::NK; ++j)
+                        kr[u][rr][j] = on ? load16(kp + (g + 8 * rr) * (D * S::kElem) + 16 * (t + 4 * j))
+                                          : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int kk = 2 * t + (x & 1) + 8 * (x >> 1);
+                    const int key = kb + kk;
+                    const bool on = ok[u] && key >= range.lo && key < range.hi;
+                    const uint8_t* src = vp + kk * (D * S::kElem);
+                    if constexpr (S::NV * S::kElem == 32) {
+                        vr[u][x][0] = on ? load16(src + 16 * g) : make_uint4(0, 0, 0, 0);
+                        vr[u][x][1] = on ? load16(src + 128 + 16 * g) : make_uint4(0, 0, 0, 0);
+                    } else if constexpr (S::NV * S::kElem == 16) {
+                        vr[u][x][0] = on ? load16(src + 16 * g) : make_uint4(0, 0, 0, 0);
+                    } else {
+                        const uint2 v = on ? __ldcg(reinterpret_cast<const uint2*>(src + 8 * g))
+                                           : make_uint2(0, 0);
+                        vr[u][x][0] = make_uint4(v.x, v.y, 0, 0);
+                    }
+                }
+            }
+            // S^T = K Q^T, in log2 units
+            float s[S::kSub][NT][4];
+            float top[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = -CUDART_INF_F;
+#pragma unroll
+            for (int u = 0; u < S::kSub; ++u) {
+                const int kb = key0 + 16 * u;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float(&acc)[4] = s[u][nt];
+                    acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < S::NK; ++j) {
+                        const uint4 x = kr[u][0][j], y = kr[u][1][j];
+                        if constexpr (!FP8) {
+                            mma_16816(acc, x.x, y.x, x.y, y.y, qr[nt][4 * j], qr[nt][4 * j + 1], false);
+                            mma_16816(acc, x.z, y.z, x.w, y.w, qr[nt][4 * j + 2], qr[nt][4 * j + 3], false);
+                        } else {
+                            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                            for (int w = 0; w < 4; ++w)
+                                mma_16816(acc, e4m3x2_to_half2(xs[w] & 0xFFFF), e4m3x2_to_half2(ys[w] & 0xFFFF),
+                                          e4m3x2_to_half2(xs[w] >> 16), e4m3x2_to_half2(ys[w] >> 16),
+                                          qr[nt][8 * j + 2 * w], qr[nt][8 * j + 2 * w + 1], true);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int key = kb + g + 8 * (i >> 1);
+                        const bool on = ok[u] && key >= range.lo && key < range.hi;
+                        acc[i] = on ? acc[i] * c_log2[nt][i & 1] : -CUDART_INF_F;
+                        top[nt][i & 1] = fmaxf(top[nt][i & 1], acc[i]);
+                    }
+                }
+            }
+            // running maximum and sum
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float f[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float v = top[nt][i];
+                    v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
+                    v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
+                    v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
+                    const float now = fmaxf(m[nt][i], v);
+                    f[i] = now == m[nt][i] ? 1.0f : exp2_approx(m[nt][i] - now);
+                    m[nt][i] = now;
+                    l[nt][i] *= f[i];
+                }
+                if (__any_sync(~0u, f[0] != 1.0f || f[1] != 1.0f)) {
+#pragma unroll
+                    for (int i = 0; i < S::NV / 2; ++i) {
+                        o[nt][i][0] *= f[0];
+                        o[nt][i][1] *= f[1];
+                        o[nt][i][2] *= f[0];
+                        o[nt][i][3] *= f[1];
+                    }
+                }
+            }
+            // P^T and O^T += V^T P^T. P is rounded to the operands' 16 bits (half a step of a
+            // weight that is at most 1); its sum is taken before the rounding, in fp32. In fp16
+            // the weights are raised by 2^10 first, so that small ones of a long
+            // cache stay clear of fp16's smallest steps; it cancels against the sum.
+#pragma unroll
+            for (int u = 0; u < S::kSub; ++u) {
+                uint32_t pb[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float p[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float mm = m[nt][i & 1] == -CUDART_INF_F ? 0.0f : m[nt][i & 1];
+                        p[i] = exp2_approx(s[u][nt][i] - mm + (FP8 ? 10.0f : 0.0f));
+                        l[nt][i & 1] += p[i];
+                    }
+                    pb[nt][0] = transpose_8x8(FP8 ? pack_half2(p[0], p[1]) : pack_bf162(p[0], p[1]));
+                    pb[nt][1] = transpose_8x8(FP8 ? pack_half2(p[2], p[3]) : pack_bf162(p[2], p[3]));
+                }
+#pragma unroll
+                for (int i = 0; i < S::NV / 2; ++i) {
+                    uint32_t av[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        // rows e = i, i + NV/2 (x & 1); keys 2t, 2t+1 or 2t+8, 2t+9 (x >> 1)
+                        const int e = i + (x & 1) * (S::NV / 2), ka = 2 * (x >> 1);
+                        auto word = [&](int key, int w) {
+                            const uint4& v = vr[u][key][w >> 2];
+                            return (w & 3) == 0 ? v.x : (w & 3) == 1 ? v.y : (w & 3) == 2 ? v.z : v.w;
+                        };
+                        if constexpr (!FP8) {
+                            const int w = e >> 1;
+                            av[x] = __byte_perm(word(ka, w), word(ka + 1, w), (e & 1) ? 0x7632 : 0x5410);
+                        } else {
+                            const int w = e >> 2, k = e & 3;
+                            av[x] = e4m3x2_to_half2(
+                                __byte_perm(word(ka, w), word(ka + 1, w), (k + 4) * 16 + k) & 0xFFFF);
+                        }
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_16816(o[nt][i], av[0], av[1], av[2], av[3], pb[nt][0], pb[nt][1], FP8);
+                }
+            }
+        }
+
+        // The warps' sums of this segment, joined in shared memory.
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float v = l[nt][i];
+                v += __shfl_xor_sync(~0u, v, 4);
+                v += __shfl_xor_sync(~0u, v, 8);
+                v += __shfl_xor_sync(~0u, v, 16);
+                l[nt][i] = v;
+            }
+        __syncthreads();  // the segment before has been read
+        if (g == 0)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = nt * 8 + 2 * t + i;
+                    sM[warp * S::kRows + r] = m[nt][i];
+                    sL[warp * S::kRows + r] = l[nt][i];
+                }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float* dst = sO + (warp * S::kRows + nt * 8 + 2 * t + i) * S::kPitch;
+#pragma unroll
+                for (int e = 0; e < S::NV; e += 4) {
+                    const int k = e % (S::NV / 2), hi = e >= S::NV / 2 ? 2 : 0;
+                    *reinterpret_cast<float4*>(dst + v_dim<D, FP8>(g, e)) =
+                        make_float4(o[nt][k][hi + i], o[nt][k + 1][hi + i], o[nt][k + 2][hi + i],
+                                    o[nt][k + 3][hi + i]);
+                }
+            }
+        __syncthreads();
+
+        // Contributors of the segment: the CTAs whose runs meet its steps.
+        const int first = static_cast<int>(segment_start / per_cta);
+        const int last = static_cast<int>((segment_start + steps - 1) / per_cta);
+        const bool whole = first == last;
+        float* const slot = a.partial + (static_cast<int64_t>(blockIdx.x) * 2 + (step0 == 0)) * kRowSlotFloats;
+        const float v_scale = FP8 ? a.kv.scales[a.kv.Hkv + h] : 1.0f;
+
+        auto finish = [&](int r, int d, float4 v, float mm, float ll) {
+            if (!range.write) return;
+            const int64_t head = static_cast<int64_t>(h) * a.G + q0 + r;
+            const float inv = ll == 0.0f ? 0.0f : v_scale / ll;  // no keys: zeros
+            uint2 w;
+            w.x = pack_bf162(v.x * inv, v.y * inv);
+            w.y = pack_bf162(v.z * inv, v.w * inv);
+            *reinterpret_cast<uint2*>(a.out + row * a.ldo + head * D + d) = w;
+            if (a.lse && d == 0)
+                a.lse[static_cast<int64_t>(row) * a.Hq + head] =
+                    ll == 0.0f ? -CUDART_INF_F
+                               : (mm + log2f(ll) - (FP8 ? 10.0f : 0.0f)) * 0.69314718055994531f;
+        };
+        for (int i = tid; i < valid * (D / 4); i += kRowThreads) {
+            const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+            float mm = -CUDART_INF_F;
+#pragma unroll
+            for (int w = 0; w < kRowWarps; ++w) mm = fmaxf(mm, sM[w * S::kRows + r]);
+            const float safe = mm == -CUDART_INF_F ? 0.0f : mm;
+            float ll = 0.0f;
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int w = 0; w < kRowWarps; ++w) {
+                const float f = exp2_approx(sM[w * S::kRows + r] - safe);
+                const float4 x = *reinterpret_cast<const float4*>(sO + (w * S::kRows + r) * S::kPitch + d);
+                ll += f * sL[w * S::kRows + r];
+                v.x += f * x.x;
+                v.y += f * x.y;
+                v.z += f * x.z;
+                v.w += f * x.w;
+            }
+            if (whole) {
+                finish(r, d, v, mm, ll);
+            } else {
+                __stcg(reinterpret_cast<float4*>(slot + r * D + d), v);
+                if (d == 0) {
+                    __stcg(slot + 16 * 128 + r, mm);
+                    __stcg(slot + 16 * 128 + 16 + r, ll);
+                }
+            }
+        }
+        if (!whole) {
+            // The last contributor to arrive sums all of them, first to last. The counter
+            // belongs to the first contributor, which starts one split segment at most.
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) s_last = atomicAdd(a.count + first, 1u) == static_cast<uint32_t>(last - first);
+            __syncthreads();
+            if (s_last) {
+                __threadfence();
+                if (tid == 0) a.count[first] = 0;
+                for (int i = tid; i < valid * (D / 4); i += kRowThreads) {
+                    const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+                    float mm = -CUDART_INF_F;
+                    for (int c = first; c <= last; ++c)
+                        mm = fmaxf(mm, __ldcg(a.partial + (static_cast<int64_t>(c) * 2 + (c == first)) * kRowSlotFloats +
+                                              16 * 128 + r));
+                    const float safe = mm == -CUDART_INF_F ? 0.0f : mm;
+                    float ll = 0.0f;
+                    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+                    for (int c = first; c <= last; ++c) {
+                        const float* p = a.partial + (static_cast<int64_t>(c) * 2 + (c == first)) * kRowSlotFloats;
+                        const float f = exp2_approx(__ldcg(p + 16 * 128 + r) - safe);
+                        const float4 x = __ldcg(reinterpret_cast<const float4*>(p + r * D + d));
+                        ll += f * __ldcg(p + 16 * 128 + 16 + r);
+                        v.x += f * x.x;
+                        v.y += f * x.y;
+                        v.z += f * x.z;
+                        v.w += f * x.w;
+                    }
+                    finish(r, d, v, mm, ll);
+                }
+            }
+        }
+
+        // the next segment
+        at += n;
+        segment_start += steps;
+        if (++part == static_cast<int>(per_row)) {
+            part = 0;
+            if (++row < a.rows) {
+                range = row_range<PROMPT>(a, row);
+                steps = steps_of(range);
+            }
+        }
+    }
+}
+
+}  // namespace tpmlp

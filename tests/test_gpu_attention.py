@@ -1,0 +1,318 @@
+"""The paged-cache attention operators on the GPU against plain fp64 references."""
+import math
+
+import pytest
+import torch
+
+import attention_ref as ref
+import tensor_transformer_mlp_tmem_gb300 as tp
+
+pytestmark = pytest.mark.gpu
+
+
+def on_device(c, attn):
+    if c["kv"] != "bf16":
+        attn.set_scales(c["ks"].cuda(), c["vs"].cuda())
+    return tp.PagedCache(attn, c["K"].cuda(), c["V"].cuda(), c["table"].cuda(), c["lens"].cuda())
+
+
+def ok(attn):
+    torch.cuda.synchronize()
+    rc, detail = attn.status()
+    assert rc == tp.TPMLP_OK, f"device status {rc} ({detail:#x})"
+
+
+def queries(rows, Hq, D, seed):
+    g = torch.Generator().manual_seed(1000 + seed)
+    return torch.randn((rows, Hq * D), generator=g).bfloat16()
+
+
+def check_rows(c, q, got, lse, spans, Hq, D, scale):
+    """spans: (row, sequence, lo, hi) of every row that must have been written."""
+    out, lse = got.cpu().double().view(-1, Hq, D), lse.cpu().double()
+    for r, b, lo, hi in spans:
+        o, l, spread, big = ref.attend(c, b, q[r].double().view(Hq, D), hi, lo, scale)
+        tol = ref.out_tolerance(o, spread, c["kv"])
+        err = (out[r] - o).abs()
+        assert bool((err <= tol).all()), (r, b, lo, hi, float((err / tol).max()))
+        if hi <= lo:
+            assert bool((lse[r] == -math.inf).all())
+        else:
+            assert bool(((lse[r] - l).abs() <= ref.lse_tolerance(l, big, D)).all()), (r, b, lo, hi)
+
+
+# ------------------------------------------------------------------ append
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Hq,Hkv,D,page,rot,interleaved,T", [
+    (4, 4, 128, 16, 128, False, 1),
+    (12, 2, 64, 32, 64, True, 37),
+    (5, 5, 64, 16, 32, False, 130),
+    (24, 3, 128, 64, 48, True, 65),
+    (16, 1, 128, 256, 96, False, 9),
+    (3, 1, 64, 128, 0, False, 7),
+])
+def test_append_matches_definition(lib, kv, Hq, Hkv, D, page, rot, interleaved, T):
+    lens = [200, 1, 77]
+    c = ref.make(Hkv, D, page, kv, lens, seed=T)
+    g = torch.Generator().manual_seed(T)
+    width = (Hq + 2 * Hkv) * D
+    qkv = torch.randn((T, width + 8), generator=g).bfloat16()  # rows wider than the three parts
+    # distinct (sequence, position) places, some tokens skipped
+    places = [(b, p) for b, n in enumerate(lens) for p in range(n)]
+    pick = torch.randperm(len(places), generator=g)[:T].tolist()
+    seq = torch.tensor([places[i][0] for i in pick], dtype=torch.int32)
+    pos = torch.tensor([places[i][1] for i in pick], dtype=torch.int32)
+    pos[::5] = -1 if T > 5 else pos[::5]
+    freq = [1e4 ** (-2 * i / rot) for i in range(rot // 2)] if rot else []
+    with tp.Attention(Hq, Hkv, D, page, kv_dtype=kv) as attn:
+        if rot:
+            attn.set_rope(rot, interleaved=interleaved)
+        cache = on_device(c, attn)
+        d = qkv.cuda()
+        q, k, v = d[:, :Hq * D], d[:, Hq * D:(Hq + Hkv) * D], d[:, (Hq + Hkv) * D:width]
+        q_out = torch.full((T, Hq * D), 7.0, dtype=torch.bfloat16, device="cuda")
+        attn.append(q, k, v, cache, pos.cuda(), seq.cuda(), q_out=q_out)
+        ok(attn)
+        inplace = attn.append(q, k, v, cache, pos.cuda(), seq.cuda(), q_out=q)
+        ok(attn)
+        kept = pos >= 0
+        assert torch.equal(inplace[kept], q_out[kept])
+        assert bool((q_out[~kept] == 7.0).all())  # skipped tokens are not written
+        K, V = cache.K.cpu().float().double(), cache.V.cpu().float().double()
+    x = qkv.double()
+    wantq = x[:, :Hq * D].view(T, Hq, D)
+    wantk = x[:, Hq * D:(Hq + Hkv) * D].reshape(T, Hkv, D)
+    wantv = x[:, (Hq + Hkv) * D:width].reshape(T, Hkv, D)
+    if rot:
+        wantq = ref.rotate(wantq, pos, rot, interleaved, freq)
+        wantk = ref.rotate(wantk, pos, rot, interleaved, freq)
+    # fp32 rotation of two operands up to 2^3, sines to 2^-22
+    slack = 2.0 ** -18
+    err = (q_out.cpu().double().view(T, Hq, D) - wantq).abs()[kept]
+    assert bool((err <= wantq.abs()[kept] * ref.HALF_STEP["bf16"] + slack).all())
+    old = {"K": c["K"].float().double(), "V": c["V"].float().double()}
+    for name, got, want, scale in (("K", K, wantk, c["ks"]), ("V", V, wantv, c["vs"])):
+        scale = scale.double()[:, None]
+        touched = torch.zeros(got.shape[0], page, dtype=torch.bool)
+        for t in range(T):
+            if pos[t] < 0:
+                continue
+            pg, sl = int(c["table"][seq[t], pos[t] // page]), int(pos[t]) % page
+            touched[pg, sl] = True
+            w = want[t] / scale
+            if kv == "e4m3":
+                w = w.clamp(-448, 448)
+                tol = w.abs() * ref.HALF_STEP["e4m3"] + 2.0 ** -10 + slack / scale
+            else:
+                tol = w.abs() * ref.HALF_STEP["bf16"] + slack
+            assert bool(((got[pg, :, sl] - w).abs() <= tol).all()), (name, t)
+        # every other row keeps what it held (NaN where nothing is stored)
+        a, b = got.transpose(1, 2)[~touched], old[name].transpose(1, 2)[~touched]
+        assert bool(((a == b) | (a.isnan() & b.isnan())).all())
+
+
+def test_append_far_positions(lib):
+    """Angles of far positions: 2^-18 of the exact rotation at position 2^22 + 5."""
+    D, page = 64, 16
+    far = (1 << 22) + 5
+    with tp.Attention(1, 1, D, page) as attn:
+        attn.set_rope(D, theta=1e6)
+        table = torch.zeros((1, far // page + 1), dtype=torch.int32, device="cuda")
+        K = torch.zeros((1, 1, page, D), dtype=torch.bfloat16, device="cuda")
+        cache = tp.PagedCache(attn, K, K.clone(), table, torch.tensor([far + 1], dtype=torch.int32, device="cuda"))
+        q = queries(1, 1, D, 3)
+        got = attn.append(q.cuda(), q.cuda(), q.cuda(), cache, torch.tensor([far], dtype=torch.int32, device="cuda"))
+        ok(attn)
+    freq = [1e6 ** (-2 * i / D) for i in range(D // 2)]
+    want = ref.rotate(q.double().view(1, 1, D), torch.tensor([far]), D, False, freq).view(1, D)
+    assert bool(((got.cpu().double() - want).abs() <= want.abs() * 2.0 ** -8 + 2.0 ** -18).all())
+
+
+def test_append_saturates_and_keeps_nan(lib):
+    with tp.Attention(1, 1, 64, 16, kv_dtype="e4m3") as attn:
+        K = torch.zeros((1, 1, 16, 64), device="cuda").to(torch.float8_e4m3fn)
+        table = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+        cache = tp.PagedCache(attn, K, K.clone(), table, torch.ones(1, dtype=torch.int32, device="cuda"))
+        x = torch.zeros((1, 64), dtype=torch.bfloat16, device="cuda")
+        x[0, 0], x[0, 1], x[0, 2], x[0, 3] = 1e6, -1e6, math.nan, math.inf
+        assert attn.append(None, x, x, cache, torch.zeros(1, dtype=torch.int32, device="cuda")) is None
+        ok(attn)
+        got = cache.V[0, 0, 0, :5].float().cpu()
+    assert got[0] == 448 and got[1] == -448 and got[2].isnan() and got[3] == 448 and got[4] == 0
+
+
+# ------------------------------------------------------------------ decode
+SHAPES = [  # Hq, Hkv, D, page, lens, window
+    (4, 4, 128, 16, [1, 0, 17, 300, 16], 0),
+    (12, 12, 64, 16, [777], 0),
+    (32, 8, 128, 64, [1, 129, 128, 127, 2, 0, 515], 0),
+    (8, 1, 64, 32, [1000, 31, 33], 0),
+    (24, 2, 128, 32, [5, 64, 1023], 0),      # 12 query heads to a kv head
+    (40, 1, 128, 128, [260, 1], 0),          # 40: three blocks of query heads
+    (18, 2, 64, 256, [511, 3], 0),           # 9
+    (6, 2, 128, 16, [1, 40, 333, 0], 33),    # windows
+    (16, 4, 64, 64, [200, 64, 65], 64),
+    (4, 2, 128, 32, [100, 7], 1),
+]
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Hq,Hkv,D,page,lens,window", SHAPES)
+def test_decode_matches_definition(lib, kv, Hq, Hkv, D, page, lens, window):
+    c = ref.make(Hkv, D, page, kv, lens, seed=Hq + D)
+    B = len(lens)
+    q = queries(B, Hq, D, page)
+    scale = 1.0 / math.sqrt(D)
+    with tp.Attention(Hq, Hkv, D, page, kv_dtype=kv) as attn:
+        cache = on_device(c, attn)
+        wide = torch.zeros((B, Hq * D + 16), dtype=torch.bfloat16, device="cuda")
+        wide[:, :Hq * D] = q.cuda()
+        out = torch.full((B, Hq * D + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+        got, lse = attn.decode(wide[:, :Hq * D], cache, window=window, out=out[:, :Hq * D], return_lse=True)
+        ok(attn)
+        assert bool((out[:, Hq * D:] == 7.0).all())
+        again, lse2 = attn.decode(q.cuda(), cache, window=window, return_lse=True)
+        ok(attn)
+        assert torch.equal(again, got) and torch.equal(lse, lse2)  # deterministic
+    spans = [(b, b, max(0, n - window) if window else 0, n) for b, n in enumerate(lens)]
+    check_rows(c, q, got, lse, spans, Hq, D, scale)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_decode_long_sequence_is_split_and_joined(lib, kv):
+    c = ref.make(2, 128, 64, kv, [20001, 3], seed=9)
+    q = queries(2, 8, 128, 9) * 3  # peaked weights
+    with tp.Attention(8, 2, 128, 64, kv_dtype=kv) as attn:
+        cache = on_device(c, attn)
+        got, lse = attn.decode(q.cuda(), cache, return_lse=True)
+        ok(attn)
+    check_rows(c, q, got, lse, [(0, 0, 0, 20001), (1, 1, 0, 3)], 8, 128, 128 ** -0.5)
+
+
+def test_decode_many_sequences(lib):
+    """More sequences than a block has threads, lengths 0 to 40."""
+    lens = [(7 * b) % 41 for b in range(700)]
+    c = ref.make(1, 64, 16, "bf16", lens, seed=4)
+    q = queries(700, 3, 64, 4)
+    with tp.Attention(3, 1, 64, 16) as attn:
+        got, lse = attn.decode(q.cuda(), on_device(c, attn), return_lse=True)
+        ok(attn)
+    check_rows(c, q, got, lse, [(b, b, 0, n) for b, n in enumerate(lens)], 3, 64, 0.125)
+
+
+def test_decode_reads_lengths_on_replay_and_other_streams(lib):
+    """A captured call replays with new lengths and queries; a side stream gives the same."""
+    lens = [400, 90, 1]
+    c = ref.make(2, 128, 32, "bf16", lens, seed=5)
+    q = queries(3, 4, 128, 5)
+    with tp.Attention(4, 2, 128, 32) as attn:
+        cache = on_device(c, attn)
+        qd, out = q.cuda(), torch.empty((3, 512), dtype=torch.bfloat16, device="cuda")
+        lse = None
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            attn.decode(qd, cache, out=out)
+        for now in (lens, [33, 0, 1], [256, 90, 0]):
+            cache.lens.copy_(torch.tensor(now, dtype=torch.int32))
+            graph.replay()
+            ok(attn)
+            want, lse = attn.decode(qd, cache, return_lse=True)
+            ok(attn)
+            assert torch.equal(out, want)
+            check_rows(c, q, out, lse, [(b, b, 0, n) for b, n in enumerate(now)], 4, 128, 128 ** -0.5)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        got = attn.decode(qd, cache, stream=side)
+        side.synchronize()
+        assert torch.equal(got, out)
+
+
+# ------------------------------------------------------------------ prompt
+def prompt_spans(lens, new, window):
+    spans, r = [], 0
+    for b, (m, n) in enumerate(zip(lens, new)):
+        for i in range(n):
+            hi = max(0, m - n + i + 1)
+            spans.append((r, b, max(0, hi - window) if window else 0, hi))
+            r += 1
+    return spans
+
+
+PROMPTS = [  # Hq, Hkv, D, page, lens, new, window
+    (4, 4, 128, 16, [61], [61], 0),
+    (12, 12, 64, 16, [1, 130, 0, 300], [1, 130, 0, 17], 0),
+    (8, 2, 128, 64, [257, 64, 5], [129, 64, 2], 0),
+    (24, 2, 128, 32, [200, 33], [90, 33], 0),      # 12 query heads to a kv head
+    (40, 1, 64, 128, [150], [70], 0),
+    (6, 2, 64, 16, [3, 50], [5, 50], 0),           # two queries before the first key
+    (4, 1, 128, 32, [300, 100], [200, 100], 50),
+    (2, 2, 64, 256, [600], [600], 129),
+    (3, 1, 128, 64, [515, 1], [515, 1], 0),
+]
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Hq,Hkv,D,page,lens,new,window", PROMPTS)
+def test_prompt_matches_definition(lib, kv, Hq, Hkv, D, page, lens, new, window):
+    c = ref.make(Hkv, D, page, kv, lens, seed=Hq + D + 1)
+    T = sum(new) + 3  # three rows that belong to no sequence
+    q = queries(T, Hq, D, page)
+    cu = torch.tensor([sum(new[:b]) for b in range(len(new) + 1)], dtype=torch.int32).cuda()
+    with tp.Attention(Hq, Hkv, D, page, kv_dtype=kv) as attn:
+        cache = on_device(c, attn)
+        wide = torch.zeros((T, Hq * D + 24), dtype=torch.bfloat16, device="cuda")
+        wide[:, :Hq * D] = q.cuda()
+        out = torch.full((T, Hq * D + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+        got, lse = attn.prompt(wide[:, :Hq * D], cu, cache, window=window, out=out[:, :Hq * D], return_lse=True)
+        ok(attn)
+        assert bool((out[:, Hq * D:] == 7.0).all()) and bool((out[-3:] == 7.0).all())
+        again = attn.prompt(q.cuda(), cu, cache, window=window)
+        ok(attn)
+        assert torch.equal(again[:-3], got[:-3])
+    check_rows(c, q, got, lse, prompt_spans(lens, new, window), Hq, D, 1.0 / math.sqrt(D))
+
+
+# ------------------------------------------------------------------ bad tables
+def test_bad_pages_are_left_out_and_reported(lib):
+    """A page outside the pool: its keys are left out of decode and prompt, append drops the
+    token; every call says so in the status and the context stays usable. The page numbers are
+    checked against the pool before any address is made from them."""
+    lens = [70, 40]
+    c = ref.make(2, 64, 16, "bf16", lens, seed=6)
+    q = queries(2, 4, 64, 6)
+    with tp.Attention(4, 2, 64, 16) as attn:
+        cache = on_device(c, attn)
+        good = attn.decode(q.cuda(), cache)
+        ok(attn)
+        for bad in (-5, c["K"].shape[0], 1 << 30):
+            cache.page_table[0, 4] = bad  # keys 64..69
+            got, lse = attn.decode(q.cuda(), cache, return_lse=True)
+            torch.cuda.synchronize()
+            assert attn.status()[0] == tp.TPMLP_ERR_BAD_PAGE
+            check_rows(c, q, got, lse, [(0, 0, 0, 64), (1, 1, 0, 40)], 4, 64, 0.125)
+            cu = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+            got, lse = attn.prompt(q.cuda(), cu, cache, return_lse=True)
+            torch.cuda.synchronize()
+            assert attn.status()[0] == tp.TPMLP_ERR_BAD_PAGE
+            check_rows(c, q, got, lse, [(0, 0, 0, 64), (1, 1, 0, 40)], 4, 64, 0.125)
+            k = q[:, :128].cuda()
+            before = cache.K.clone()
+            attn.append(None, k, k, cache, torch.tensor([66, -1], dtype=torch.int32, device="cuda"))
+            torch.cuda.synchronize()
+            assert attn.status()[0] == tp.TPMLP_ERR_BAD_PAGE
+            assert torch.equal(before.view(torch.int16), cache.K.view(torch.int16))
+        cache.page_table[0, 4] = int(c["table"][0, 4])
+        # positions and sequences outside the table
+        for pos, seq in (([80, -1], [0, 0]), ([0, -1], [2, 0]), ([0, -1], [-1, 0])):
+            attn.append(None, k, k, cache, torch.tensor(pos, dtype=torch.int32, device="cuda"),
+                        torch.tensor(seq, dtype=torch.int32, device="cuda"))
+            torch.cuda.synchronize()
+            assert attn.status()[0] == tp.TPMLP_ERR_BAD_PAGE
+        # a length above the table's capacity counts as the capacity (80 keys)
+        cache.lens[0] = 81
+        attn.decode(q.cuda(), cache)
+        torch.cuda.synchronize()
+        assert attn.status()[0] == tp.TPMLP_ERR_BAD_PAGE
+        cache.lens[0] = 70
+        assert torch.equal(attn.decode(q.cuda(), cache), good)
+        ok(attn)
