@@ -483,7 +483,7 @@ TPMLP_API int tpmlp_linear_forward(tpmlp_ctx *ctx, const void *X, int64_t M, voi
  *   D          head size: 64 or 128
  *   page_size  keys per page: 16, 32, 64, 128 or 256
  *   flags      0 or TPMLP_FLAG_KV_E4M3
- * Allocates the scales, the workspace of split key ranges (about 13 MB) and the status word. The
+ * Allocates the scales, the workspace of split key ranges (about 40 MB) and the status word. The
  * context is used with the tpmlp_attn_* calls, tpmlp_destroy and the diagnostic calls; the other
  * entry points reject it with TPMLP_ERR_INVALID_ARG. Like the GEMM calls, its calls on different
  * streams must not overlap on the GPU (they share the workspace). All of its calls can be
@@ -581,7 +581,9 @@ TPMLP_API int tpmlp_attn_decode(tpmlp_ctx *ctx, const void *Q, int64_t ldq, cons
  * tpmlp_attn_decode; a query at a negative position gets zeros and -infinity.
  *   T    rows of Q and Out    cu_q  device int32 [B + 1], from 0, not decreasing, at most T; rows
  *        outside every sequence are not written. Lse device fp32 [T][Hq] or NULL.
- * Two launches at most; T == 0 or B == 0 is a no-op.
+ * A value (V) that is not finite also reaches earlier queries of its own chunk, up to 2 * 128 / G
+ * tokens back (its weight there is 0, and 0 times it is NaN); a key (K) does not.
+ * One launch; T == 0 or B == 0 is a no-op.
  * Errors: as tpmlp_attn_decode.
  */
 TPMLP_API int tpmlp_attn_prompt(tpmlp_ctx *ctx, const void *Q, int64_t ldq, int64_t T,

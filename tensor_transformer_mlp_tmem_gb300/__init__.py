@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 
 __all__ = [
     "TPMLP", "TpmlpError", "load_library", "library_path",
@@ -168,13 +169,12 @@ def _ptr(x) -> int | None:
 
 def _stream(s) -> int | None:
     if s is None:
-        try:
-            import torch
-            if torch.cuda.is_available() and torch.cuda.is_initialized():
-                return int(torch.cuda.current_stream().cuda_stream) or None
-        except Exception:  # torch absent: the legacy default stream
-            pass
-        return None
+        # torch's current stream, if the program uses torch and it has started CUDA (else the
+        # legacy default stream)
+        torch = sys.modules.get("torch")
+        if torch is None or not torch.cuda.is_initialized():
+            return None
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) or None
     if isinstance(s, int):
         return s or None
     if hasattr(s, "cuda_stream"):
@@ -692,8 +692,14 @@ class Attention:
     def __init__(self, Hq: int, Hkv: int, D: int, page_size: int = 64, kv_dtype: str = "bf16"):
         if kv_dtype not in ("bf16", "e4m3"):
             raise ValueError(f"kv_dtype: expected 'bf16' or 'e4m3', got {kv_dtype!r}")
+        import torch
         self.Hq, self.Hkv, self.D, self.page_size = Hq, Hkv, D, page_size
         self.kv_dtype = kv_dtype
+        self._lib = load_library()
+        self._wq, self._wk, self._scale = Hq * D, Hkv * D, D ** -0.5
+        self._layout = (Hkv, D, page_size, kv_dtype)
+        self._Tensor, self._bf16 = torch.Tensor, torch.bfloat16
+        self._int32, self._float32 = torch.int32, torch.float32
         self.ctx = tpmlp_attn_create(Hq, Hkv, D, page_size,
                                      TPMLP_FLAG_KV_E4M3 if kv_dtype == "e4m3" else 0)
 
@@ -742,85 +748,85 @@ class Attention:
         K = torch.empty(shape, dtype=self.pool_dtype(), device=page_table.device)
         return PagedCache(self, K, torch.empty_like(K), page_table, lens)
 
-    @staticmethod
-    def _rows(t, width, what):
+    # The checks below run on every call of a decode step, whose kernels take a few microseconds:
+    # each tensor's properties are read once, and the messages are made only on failure.
+    def _rows(self, t, rows, width, what):
         """Row pitch of a bf16 CUDA [rows, width] tensor whose rows are contiguous."""
-        import torch
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        if not isinstance(t, self._Tensor) or not t.is_cuda:
             raise TypeError(f"{what} must be a CUDA tensor")
-        if t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[1] != width or t.stride(1) != 1:
-            raise ValueError(f"{what}: expected bf16 [rows, {width}] with contiguous rows, got "
+        if t.dtype is not self._bf16 or t.shape != (rows, width) or t.stride(1) != 1:
+            raise ValueError(f"{what}: expected bf16 [{rows}, {width}] with contiguous rows, got "
                              f"{t.dtype} {tuple(t.shape)} strides {t.stride()}")
-        # the stride of a single row says nothing
-        return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), width)
+        return t.stride(0) if rows > 1 else width  # the stride of a single row says nothing
 
-    @staticmethod
-    def _ints(t, n, what):
-        import torch
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    def _ints(self, t, n, what):
+        """Address of a contiguous int32 CUDA [n] tensor."""
+        if not isinstance(t, self._Tensor) or not t.is_cuda:
             raise TypeError(f"{what} must be a CUDA tensor")
-        if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        if t.dtype is not self._int32 or t.shape != (n,) or not t.is_contiguous():
             raise ValueError(f"{what}: expected contiguous int32 ({n},), got {t.dtype} "
                              f"{tuple(t.shape)}")
+        return t.data_ptr()
 
     def append(self, q, k, v, cache, pos, seq=None, q_out=None, stream=None):
         """Writes k and v [T, Hkv * D] (k rotated) at positions pos [T] of sequences seq [T]
         (None: token t is sequence t's) and returns the rotated q [T, Hq * D] (in q_out; q_out=q
         rotates in place; q None: only k and v). Rows may be column ranges of a wider tensor."""
-        import torch
-        T, wk = k.shape[0], self.Hkv * self.D
-        ldk, ldv = self._rows(k, wk, "k"), self._rows(v, wk, "v")
-        if v.shape[0] != T:
-            raise ValueError("k and v: different numbers of tokens")
-        self._ints(pos, T, "pos")
+        T = k.shape[0]
+        ldk, ldv = self._rows(k, T, self._wk, "k"), self._rows(v, T, self._wk, "v")
+        pos = self._ints(pos, T, "pos")
         if seq is not None:
-            self._ints(seq, T, "seq")
+            seq = self._ints(seq, T, "seq")
+        qp = op = None
         ldq = ldqo = 0
         if q is not None:
-            ldq = self._rows(q, self.Hq * self.D, "q")
+            ldq = self._rows(q, T, self._wq, "q")
             if q_out is None:
-                q_out = torch.empty((T, self.Hq * self.D), dtype=torch.bfloat16, device=q.device)
-            ldqo = self._rows(q_out, self.Hq * self.D, "q_out")
-            if q.shape[0] != T or q_out.shape[0] != T:
-                raise ValueError("q and q_out: different numbers of tokens than k")
-        tpmlp_attn_append(self.ctx, q, ldq, k, ldk, v, ldv, T, pos, seq, cache._of(self),
-                          q_out if q is not None else None, ldqo, stream)
-        return q_out if q is not None else None
-
-    def _attend(self, q, rows, out, return_lse):
-        import torch
-        width = self.Hq * self.D
-        ldq = self._rows(q, width, "q")
-        if out is None:
-            out = torch.empty((rows, width), dtype=torch.bfloat16, device=q.device)
-        ldo = self._rows(out, width, "out")
-        if q.shape[0] != rows or out.shape[0] != rows:
-            raise ValueError(f"q and out: expected {rows} rows")
-        lse = (torch.empty((rows, self.Hq), dtype=torch.float32, device=q.device)
-               if return_lse else None)
-        return ldq, out, ldo, lse
+                q_out = q.new_empty((T, self._wq))
+            ldqo = self._rows(q_out, T, self._wq, "q_out")
+            qp, op = q.data_ptr(), q_out.data_ptr()
+        else:
+            q_out = None
+        rc = self._lib.tpmlp_attn_append(self.ctx, qp, ldq, k.data_ptr(), ldk, v.data_ptr(), ldv,
+                                         T, pos, seq, cache._of(self), op, ldqo, _stream(stream))
+        if rc:
+            _check(rc, "tpmlp_attn_append", self.ctx)
+        return q_out
 
     def decode(self, q, cache, scale=None, window: int = 0, out=None, return_lse: bool = False,
                stream=None):
         """Attention of one token of each sequence, q [B, Hq * D], over its cache (its own key
         included: append first). scale: D ** -0.5 by default. Returns out [B, Hq * D], or (out,
         lse [B, Hq] fp32)."""
-        kv = cache._of(self)
-        ldq, out, ldo, lse = self._attend(q, kv.B, out, return_lse)
-        tpmlp_attn_decode(self.ctx, q, ldq, kv, self.D ** -0.5 if scale is None else scale,
-                          window, out, ldo, lse, stream)
+        kv, B = cache._of(self), cache.B
+        ldq = self._rows(q, B, self._wq, "q")
+        if out is None:
+            out = q.new_empty((B, self._wq))
+        ldo = self._rows(out, B, self._wq, "out")
+        lse = q.new_empty((B, self.Hq), dtype=self._float32) if return_lse else None
+        rc = self._lib.tpmlp_attn_decode(
+            self.ctx, q.data_ptr(), ldq, kv, self._scale if scale is None else scale, window,
+            out.data_ptr(), ldo, lse.data_ptr() if return_lse else None, _stream(stream))
+        if rc:
+            _check(rc, "tpmlp_attn_decode", self.ctx)
         return (out, lse) if return_lse else out
 
     def prompt(self, q, cu_q, cache, scale=None, window: int = 0, out=None,
                return_lse: bool = False, stream=None):
         """Causal attention of the new tokens q [T, Hq * D], sequence b's in rows cu_q[b] ..
         cu_q[b + 1] - 1 (cu_q int32 [B + 1]), over the caches that already hold their keys."""
-        kv = cache._of(self)
-        self._ints(cu_q, kv.B + 1, "cu_q")
-        T = q.shape[0]
-        ldq, out, ldo, lse = self._attend(q, T, out, return_lse)
-        tpmlp_attn_prompt(self.ctx, q, ldq, T, cu_q, kv, self.D ** -0.5 if scale is None else scale,
-                          window, out, ldo, lse, stream)
+        kv, T = cache._of(self), q.shape[0]
+        cu = self._ints(cu_q, cache.B + 1, "cu_q")
+        ldq = self._rows(q, T, self._wq, "q")
+        if out is None:
+            out = q.new_empty((T, self._wq))
+        ldo = self._rows(out, T, self._wq, "out")
+        lse = q.new_empty((T, self.Hq), dtype=self._float32) if return_lse else None
+        rc = self._lib.tpmlp_attn_prompt(
+            self.ctx, q.data_ptr(), ldq, T, cu, kv, self._scale if scale is None else scale,
+            window, out.data_ptr(), ldo, lse.data_ptr() if return_lse else None, _stream(stream))
+        if rc:
+            _check(rc, "tpmlp_attn_prompt", self.ctx)
         return (out, lse) if return_lse else out
 
     def status(self, stream=None):
@@ -858,15 +864,16 @@ class PagedCache:
         page = attn.Hkv * attn.page_size * attn.D
         if (K.shape[0] > 1 and K.stride(0) < page) or (B > 1 and page_table.stride(0) < pages):
             raise ValueError("K, V, page_table: pages or rows that overlap in memory")
-        Attention._ints(lens, B, "lens")
-        self.K, self.V, self.page_table, self.lens = K, V, page_table, lens
-        self._layout = (attn.Hkv, attn.D, attn.page_size, attn.kv_dtype)
+        attn._ints(lens, B, "lens")
+        self.K, self.V, self.page_table, self.lens, self.B = K, V, page_table, lens, B
+        self._layout = attn._layout
         # the stride of a single page or row says nothing (0: dense)
         self._kv = KvCache(K.data_ptr(), V.data_ptr(), K.shape[0],
                            K.stride(0) if K.shape[0] > 1 else 0, page_table.data_ptr(),
                            page_table.stride(0) if B > 1 else 0, pages, B, lens.data_ptr())
+        self._ref = ctypes.byref(self._kv)
 
-    def _of(self, attn: Attention) -> KvCache:
-        if self._layout != (attn.Hkv, attn.D, attn.page_size, attn.kv_dtype):
+    def _of(self, attn: Attention):
+        if self._layout != attn._layout:
             raise ValueError("the cache was laid out for another head layout, page size or type")
-        return self._kv
+        return self._ref

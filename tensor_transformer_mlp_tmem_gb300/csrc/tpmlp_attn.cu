@@ -9,6 +9,7 @@
 #include <new>
 
 #include "tpmlp_attn.cuh"
+#include "tpmlp_attn_prompt.cuh"
 #include "tpmlp_context.h"
 
 using tpmlp::aligned16;
@@ -34,6 +35,7 @@ int check_rows(tpmlp_ctx* c, const void* p, int64_t ld, int64_t width) {
 int check_kv(tpmlp_ctx* c, const tpmlp_kv* kv, bool lens) {
     if (!kv || !kv->K || !kv->V || !kv->page_table || (lens && !kv->lens)) return TPMLP_ERR_INVALID_ARG;
     if (kv->num_pages <= 0 || kv->table_pages <= 0 || kv->B < 0) return TPMLP_ERR_INVALID_ARG;
+    if (kv->num_pages > INT_MAX) return TPMLP_ERR_UNSUPPORTED_SHAPE;
     if (kv->table_stride != 0 && kv->table_stride < kv->table_pages) return TPMLP_ERR_INVALID_ARG;
     const int64_t page = static_cast<int64_t>(c->heads_kv) * c->page_size * c->head_dim;
     if (kv->page_stride != 0 && kv->page_stride < page) return TPMLP_ERR_INVALID_ARG;
@@ -98,28 +100,91 @@ int allow_smem(tpmlp_ctx* c, Kernel kern, uint32_t smem, std::atomic<uint64_t>& 
     return TPMLP_OK;
 }
 
-template <int D, bool FP8, int NT, bool PROMPT>
+template <int D, bool FP8, int NT>
 int launch_rows(tpmlp_ctx* c, const tpmlp::RowArgs& a, cudaStream_t s) {
     using S = tpmlp::RowShape<D, FP8, NT>;
-    auto kern = tpmlp::attn_row_kernel<D, FP8, NT, PROMPT>;
+    auto kern = tpmlp::attn_row_kernel<D, FP8, NT>;
     static std::atomic<uint64_t> done{0};
     if (int rc = allow_smem(c, kern, S::kSmem, done)) return rc;
     const int grid = c->num_sms * (NT == 1 ? kRowCtasPerSm : 1);
     return launch(c, kern, grid, tpmlp::kRowThreads, S::kSmem, s, a);
 }
 
-template <bool PROMPT>
 int run_rows(tpmlp_ctx* c, tpmlp::RowArgs& a, cudaStream_t s) {
     const bool wide = a.G > 8;
     a.blocks_per_head = (a.G + 15) / 16;
     if (c->head_dim == 128) {
         if (is_e4m3(c))
-            return wide ? launch_rows<128, true, 2, PROMPT>(c, a, s) : launch_rows<128, true, 1, PROMPT>(c, a, s);
-        return wide ? launch_rows<128, false, 2, PROMPT>(c, a, s) : launch_rows<128, false, 1, PROMPT>(c, a, s);
+            return wide ? launch_rows<128, true, 2>(c, a, s) : launch_rows<128, true, 1>(c, a, s);
+        return wide ? launch_rows<128, false, 2>(c, a, s) : launch_rows<128, false, 1>(c, a, s);
     }
     if (is_e4m3(c))
-        return wide ? launch_rows<64, true, 2, PROMPT>(c, a, s) : launch_rows<64, true, 1, PROMPT>(c, a, s);
-    return wide ? launch_rows<64, false, 2, PROMPT>(c, a, s) : launch_rows<64, false, 1, PROMPT>(c, a, s);
+        return wide ? launch_rows<64, true, 2>(c, a, s) : launch_rows<64, true, 1>(c, a, s);
+    return wide ? launch_rows<64, false, 2>(c, a, s) : launch_rows<64, false, 1>(c, a, s);
+}
+
+template <int D, bool FP8>
+int launch_prompt(tpmlp_ctx* c, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                  const tpmlp::PromptArgs& a, cudaStream_t s) {
+    using S = tpmlp::PromptSmem<D, FP8>;
+    auto kern = tpmlp::attn_prompt_kernel<D, FP8>;
+    static std::atomic<uint64_t> done{0};
+    if (int rc = allow_smem(c, kern, S::kTotal, done)) return rc;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(c->num_sms), 1, 1);
+    cfg.blockDim = dim3(S::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = S::kTotal;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    TPMLP_CUDA(c, cudaLaunchKernelEx(&cfg, kern, q, k, v, a));
+    ++c->launches;
+    return TPMLP_OK;
+}
+
+// The pool as [page][Hkv * page size][D], in boxes of 64 columns and one page's (at most a
+// block's) rows.
+int pool_map(tpmlp_ctx* c, CUtensorMap* map, const void* pool, const tpmlp::KvView& kv) {
+    const uint64_t dims[3] = {static_cast<uint64_t>(c->head_dim),
+                              static_cast<uint64_t>(c->heads_kv) * c->page_size,
+                              static_cast<uint64_t>(kv.num_pages)};
+    const uint64_t strides[2] = {static_cast<uint64_t>(c->head_dim) * 2, static_cast<uint64_t>(kv.page_bytes)};
+    const uint32_t box[3] = {64, static_cast<uint32_t>(std::min(c->page_size, tpmlp::kPB)), 1};
+    return tpmlp::encode_map_typed(c, map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, pool, 3, dims, strides, box);
+}
+
+int run_prompt(tpmlp_ctx* c, const tpmlp::RowArgs& r, const int32_t* cu_q, int64_t T, cudaStream_t s) {
+    tpmlp::PromptArgs a{};
+    a.kv = r.kv;
+    a.q = r.q;
+    a.ldq = r.ldq;
+    a.out = r.out;
+    a.ldo = r.ldo;
+    a.lse = r.lse;
+    a.cu_q = cu_q;
+    a.T = static_cast<int32_t>(T);
+    a.Hq = r.Hq;
+    a.G = r.G;
+    a.tpt = tpmlp::kPB / r.G;
+    a.scale_log2 = r.scale_log2;
+    a.window = r.window;
+    a.partial = c->attn_partial;
+    a.count = c->attn_count;
+    CUtensorMap q{}, k{}, v{};
+    if (!is_e4m3(c)) {
+        const uint64_t dims[3] = {static_cast<uint64_t>(c->head_dim), static_cast<uint64_t>(c->heads_q),
+                                  static_cast<uint64_t>(T)};
+        const uint64_t strides[2] = {static_cast<uint64_t>(c->head_dim) * 2, static_cast<uint64_t>(a.ldq) * 2};
+        const uint32_t box[3] = {64, static_cast<uint32_t>(a.G), static_cast<uint32_t>(a.tpt)};
+        int rc = tpmlp::encode_map_typed(c, &q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, 3, dims, strides, box);
+        if (rc || (rc = pool_map(c, &k, a.kv.K, a.kv)) || (rc = pool_map(c, &v, a.kv.V, a.kv))) return rc;
+    }
+    if (c->head_dim == 128)
+        return is_e4m3(c) ? launch_prompt<128, true>(c, q, k, v, a, s) : launch_prompt<128, false>(c, q, k, v, a, s);
+    return is_e4m3(c) ? launch_prompt<64, true>(c, q, k, v, a, s) : launch_prompt<64, false>(c, q, k, v, a, s);
 }
 
 // What decode and prompt check alike; rows: rows of Q and Out.
@@ -187,6 +252,9 @@ int tpmlp_attn_create(tpmlp_ctx** out, int32_t Hq, int32_t Hkv, int32_t D, int32
     c->head_dim = D;
     c->page_size = page_size;
     const size_t ctas = static_cast<size_t>(c->num_sms) * kRowCtasPerSm;
+    // two slots per CTA of either kernel (the prompt kernel's hold two tiles each)
+    const size_t partial = std::max(ctas * 2 * tpmlp::kRowSlotFloats,
+                                    static_cast<size_t>(c->num_sms) * 4 * tpmlp::kPromptSlotFloats);
     const size_t scales = static_cast<size_t>(Hkv) * 2;
     cudaError_t e;
     float* ones = new (std::nothrow) float[scales];
@@ -196,7 +264,7 @@ int tpmlp_attn_create(tpmlp_ctx** out, int32_t Hq, int32_t Hkv, int32_t D, int32
     }
     std::fill(ones, ones + scales, 1.0f);
     if ((e = cudaMalloc(&c->kv_scale, scales * sizeof(float))) != cudaSuccess ||
-        (e = cudaMalloc(&c->attn_partial, ctas * 2 * tpmlp::kRowSlotFloats * sizeof(float))) != cudaSuccess ||
+        (e = cudaMalloc(&c->attn_partial, partial * sizeof(float))) != cudaSuccess ||
         (e = cudaMalloc(&c->attn_count, ctas * sizeof(uint32_t))) != cudaSuccess ||
         (e = cudaMalloc(&c->status, sizeof(int))) != cudaSuccess ||
         (e = cudaMemset(c->attn_count, 0, ctas * sizeof(uint32_t))) != cudaSuccess ||
@@ -282,7 +350,7 @@ int tpmlp_attn_decode(tpmlp_ctx* c, const void* Q, int64_t ldq, const tpmlp_kv* 
     if (int rc = check_attend(c, Q, ldq, kv, scale, Out, ldo, Lse)) return rc;
     tpmlp::RowArgs a = row_args(c, Q, ldq, kv, scale, window, Out, ldo, Lse);
     a.rows = kv->B;
-    return run_rows<false>(c, a, static_cast<cudaStream_t>(stream));
+    return run_rows(c, a, static_cast<cudaStream_t>(stream));
 }
 
 int tpmlp_attn_prompt(tpmlp_ctx* c, const void* Q, int64_t ldq, int64_t T, const int32_t* cu_q,
@@ -295,10 +363,8 @@ int tpmlp_attn_prompt(tpmlp_ctx* c, const void* Q, int64_t ldq, int64_t T, const
     if (int rc = check_attend(c, Q, ldq, kv, scale, Out, ldo, Lse)) return rc;
     if (!cu_q) return TPMLP_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(cu_q) & 3) return TPMLP_ERR_MISALIGNED;
-    tpmlp::RowArgs a = row_args(c, Q, ldq, kv, scale, window, Out, ldo, Lse);
-    a.rows = static_cast<int32_t>(T);
-    a.cu_q = cu_q;
-    return run_rows<true>(c, a, static_cast<cudaStream_t>(stream));
+    const tpmlp::RowArgs a = row_args(c, Q, ldq, kv, scale, window, Out, ldo, Lse);
+    return run_prompt(c, a, cu_q, T, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

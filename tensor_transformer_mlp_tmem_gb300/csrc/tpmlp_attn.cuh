@@ -1,5 +1,5 @@
 // Attention over a paged key-value cache: the append kernel (rotation, page writes) and the
-// row kernel (attention of one token's query heads over a range of keys), which serves decode.
+// row kernel (decode: attention of one token's query heads over its sequence's keys).
 //
 // A pool is [num_pages][Hkv][page][D]: the keys of one head in one page are contiguous, so a
 // warp that walks a head's keys reads whole 16-byte pieces of whole rows, whatever the page size.
@@ -192,8 +192,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 }
 
 // ------------------------------------------------------------------ rows
-// Attention of single tokens: row r (a decode sequence, or one token of a prompt) has G query
-// heads to each kv head, and attends to keys [lo, hi) of its sequence.
+// Attention of one token of each sequence: row b has G query heads to each kv head, and attends to
+// keys [lo, hi) of sequence b.
 struct RowArgs {
     KvView kv;
     const __nv_bfloat16* q;
@@ -201,8 +201,7 @@ struct RowArgs {
     __nv_bfloat16* out;
     int64_t ldo;
     float* lse;             // [rows][Hq] or null
-    const int32_t* cu_q;    // prompt: [B + 1]
-    int32_t rows;
+    int32_t rows;           // sequences
     int32_t Hq, G;
     int32_t blocks_per_head;  // blocks of 8 * NT query heads that share a kv head
     float scale_log2;         // softmax scale * log2(e)
@@ -266,32 +265,13 @@ __device__ __forceinline__ uint4 load16(const uint8_t* p) {
     return __ldcg(reinterpret_cast<const uint4*>(p));
 }
 
-// Keys of row r: sequence b, [lo, hi).
+// Keys of a row: [lo, hi) of its sequence.
 struct RowRange {
-    int b, lo, hi;
-    bool write;
+    int lo, hi;
 };
 
-template <bool PROMPT>
-__device__ __forceinline__ RowRange row_range(const RowArgs& a, int r) {
-    RowRange x{r, 0, 0, true};
-    if constexpr (PROMPT) {
-        // the last sequence that starts at or before r
-        int lo = 0, hi = a.kv.B;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (a.cu_q[mid] <= r) lo = mid;
-            else hi = mid;
-        }
-        x.b = lo;
-        const int first = a.cu_q[lo], next = a.cu_q[lo + 1];
-        x.write = r >= first && r < next;
-        if (!x.write) return x;
-        const int len = kv_length(a.kv, lo);
-        x.hi = min(max(len - next + r + 1, 0), len);
-    } else {
-        x.hi = kv_length(a.kv, r);
-    }
+__device__ __forceinline__ RowRange row_range(const RowArgs& a, int b) {
+    RowRange x{0, kv_length(a.kv, b)};
     if (a.window > 0) x.lo = max(0, x.hi - a.window);
     return x;
 }
@@ -323,7 +303,7 @@ __device__ __forceinline__ int v_dim(int g, int e) {
     else return (D / 8) * g + e;
 }
 
-template <int D, bool FP8, int NT, bool PROMPT>
+template <int D, bool FP8, int NT>
 __global__ void __launch_bounds__(kRowThreads, NT == 1 ? 2 : 1)
 attn_row_kernel(const __grid_constant__ RowArgs a) {
     using S = RowShape<D, FP8, NT>;
@@ -347,7 +327,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
     // its row's steps, and each CTA takes an equal run of all segments' steps.
     const int64_t per_row = static_cast<int64_t>(a.kv.Hkv) * a.blocks_per_head;
     int64_t mine = 0;
-    for (int r = tid; r < a.rows; r += kRowThreads) mine += steps_of(row_range<PROMPT>(a, r));
+    for (int r = tid; r < a.rows; r += kRowThreads) mine += steps_of(row_range(a, r));
 #pragma unroll
     for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(~0u, mine, o);
     if (lane == 0) s_scan[warp] = mine;
@@ -366,7 +346,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         int64_t before = 0;
         for (int r0 = 0; r0 < a.rows; r0 += kRowThreads) {
             const int r = r0 + tid;
-            const int64_t c = r < a.rows ? steps_of(row_range<PROMPT>(a, r)) : 0;
+            const int64_t c = r < a.rows ? steps_of(row_range(a, r)) : 0;
             int64_t sum = c;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -391,7 +371,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
     }
     if (s_found[0] < 0) return;  // only if the lengths changed during the launch
     int row = static_cast<int>(s_found[0]);
-    RowRange range = row_range<PROMPT>(a, row);
+    RowRange range = row_range(a, row);
     int steps = steps_of(range);
     int64_t segment_start;  // first step of the current segment
     int part;               // kv head * blocks_per_head + block
@@ -487,7 +467,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
             for (int u = 0; u < S::kSub; ++u) {
                 const int kb = key0 + 16 * u;
                 int64_t page = -1;
-                if (kb < range.hi) page = kv_page(a.kv, range.b, kb);
+                if (kb < range.hi) page = kv_page(a.kv, row, kb);
                 ok[u] = page >= 0;
                 const int64_t off = page * a.kv.page_bytes + head_off +
                                     static_cast<int64_t>(kb & ((1 << a.kv.page_shift) - 1)) * (D * S::kElem);
@@ -671,7 +651,6 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         const float v_scale = FP8 ? a.kv.scales[a.kv.Hkv + h] : 1.0f;
 
         auto finish = [&](int r, int d, float4 v, float mm, float ll) {
-            if (!range.write) return;
             const int64_t head = static_cast<int64_t>(h) * a.G + q0 + r;
             const float inv = ll == 0.0f ? 0.0f : v_scale / ll;  // no keys: zeros
             uint2 w;
@@ -752,7 +731,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         if (++part == static_cast<int>(per_row)) {
             part = 0;
             if (++row < a.rows) {
-                range = row_range<PROMPT>(a, row);
+                range = row_range(a, row);
                 steps = steps_of(range);
             }
         }

@@ -1,0 +1,948 @@
+// Causal attention of chunks of new tokens over a paged cache, on the tensor cores.
+//
+// For one kv head, G query heads and TPT = floor(128 / G) consecutive tokens make a tile of up to
+// 128 rows (row = token * G + head of the group), so that grouped heads share each K and V tile.
+// A CTA works on an item of two tiles (2 TPT tokens of one kv head) and walks the item's keys in
+// blocks of 128:
+//   S_t = Q_t K^T      tcgen05.mma, both operands in shared memory, S fp32 in tensor memory
+//   P_t = 2^(S c - m)  one thread per row, written back over S in 16 bits
+//   O_t += P_t V       tcgen05.mma, P from tensor memory, V from shared memory (keys are the
+//                      reduction, so V is read as it lies, D contiguous)
+// While the softmax warps of one tile work, the tensor core runs the other tile's two products.
+//
+// Warps: 0-3 softmax of tile 0, 4-7 of tile 1 (a warp may read the 32 tensor-memory lanes of its
+// rank mod 4), 8 issues the MMAs, 9 loads K and V (and Q) by TMA, page by page, 10-11 idle;
+// e4m3 caches: 12-15 convert the loaded bytes to fp16.
+#pragma once
+
+#include "tpmlp_attn.cuh"
+#include "tpmlp_gemm.cuh"
+
+namespace tpmlp {
+
+constexpr int kPB = 128;          // keys per block = rows per tile
+constexpr int kPromptItems = 1024;  // items whose sizes a CTA tabulates
+constexpr int kCoarse = 512;        // entries of the table of sequences
+constexpr int kPromptCode = 0x2000;  // wait sites: kPromptCode | role
+// fp32 values of a tile's partial sums: O in groups of 4 columns [D/4][128][4], m [128], l [128].
+constexpr int kPromptSlotFloats = 128 * 128 + 256;
+// A row's reference maximum follows its running maximum only when that has grown by more than
+// 2^8: weights then stay below 2^8 (no loss in fp32, bf16 or fp16) and O is rarely rescaled.
+constexpr float kLazyLog2 = 8.0f;
+constexpr float kRaiseLog2 = 6.0f;  // e4m3 caches: fp16 weights are raised by 2^6 (see the rows)
+
+struct PromptArgs {
+    KvView kv;
+    const __nv_bfloat16* q;
+    int64_t ldq;
+    __nv_bfloat16* out;
+    int64_t ldo;
+    float* lse;
+    const int32_t* cu_q;
+    int32_t T, Hq, G, tpt;  // tpt: tokens per tile
+    float scale_log2;
+    int32_t window;
+    float* partial;   // [CTAs][2 pieces][2 tiles] slots
+    uint32_t* count;  // [CTAs][2 tiles], 0 between launches
+};
+
+template <int D, bool FP8>
+struct PromptSmem {
+    static constexpr uint32_t kTile = kPB * D * 2;   // a Q, K or V tile of 16-bit values
+    static constexpr uint32_t kRaw = FP8 ? kPB * D : 0;
+    static constexpr int kStages = D == 128 ? (FP8 ? 3 : 4) : 6;
+    static constexpr int kRaws = FP8 ? 3 : 0;
+    static constexpr uint32_t kStage0 = 2 * kTile;
+    static constexpr uint32_t kRaw0 = kStage0 + kStages * kTile;
+    static constexpr uint32_t kBars = kRaw0 + kRaws * kRaw;
+    static constexpr int kNumBars = 2 * kStages + 2 * kRaws + 16;
+    static constexpr uint32_t kTables = kBars + (8 * kNumBars + 64 + 127) / 128 * 128;
+    static constexpr uint32_t kTotal = 1024 + kTables + (kCoarse + 1) * 8 + (kPromptItems + 1) * 4 + 256;
+    static_assert(kTotal <= 232448, "dynamic shared memory per CTA");
+    static constexpr int kThreads = FP8 ? 512 : 384;
+};
+
+// D[tmem] (+)= A[tmem] * B[smem]: the 16-bit A operand lies in tensor memory, two values to a
+// column.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                       uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+          "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+          "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+          "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
+          "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void fence_async_shared() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+        : "memory");
+}
+template <int R>
+__device__ __forceinline__ void regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+// B operand with the reduction (keys) along rows: blocks of 64 columns of D, each 128 keys x 128
+// bytes with the 128-byte swizzle; 16 KB from block to block, 1 KB from 8 keys to 8 keys.
+__device__ __forceinline__ uint64_t sdesc_v(uint32_t saddr) {
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(16384 >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+           (static_cast<uint64_t>(2) << 61);
+}
+
+// Instruction descriptor: fp32 accumulators, bf16 or fp16 operands, A K-major, B K- or N-major.
+__host__ __device__ constexpr uint32_t prompt_idesc(int N, bool half, bool b_mn) {
+    return (1u << 4) | (half ? 0u : (1u << 7) | (1u << 10)) | (b_mn ? 1u << 16 : 0u) |
+           (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+}
+
+// A sequence's new tokens: rows [first, first + n) of Q, at positions len - n ...
+struct PromptSeq {
+    int first, n, len;
+    __device__ __forceinline__ int hi(int token) const {  // keys that the token may see end here
+        return max(0, min(len, len - n + token + 1));
+    }
+};
+__device__ __forceinline__ PromptSeq prompt_seq(const PromptArgs& a, int b) {
+    PromptSeq s;
+    s.first = max(0, min(a.cu_q[b], a.T));
+    s.n = max(0, min(a.cu_q[b + 1], a.T) - s.first);
+    s.len = kv_length(a.kv, b);
+    return s;
+}
+
+// An item, or the part of its key blocks [b0, b1) that one CTA computes.
+struct Piece {
+    bool valid;
+    int b, h, tok0;        // sequence, kv head, first token of tile 0
+    PromptSeq seq;
+    int tokens[2];         // of each tile
+    int lo[2], hi[2];      // each tile's blocks
+    int last_hi[2];        // end of the keys of each tile's last token
+    int b0, b1;
+    int first, last;       // contributing CTAs
+    int starts;            // 1: the item's first blocks are in this piece
+    __device__ __forceinline__ int begin(int t) const { return max(lo[t], b0); }
+    __device__ __forceinline__ int end(int t) const { return min(hi[t], b1); }
+};
+
+__device__ __forceinline__ int prompt_lo_key(const PromptArgs& a, int hi) {
+    return a.window > 0 ? max(0, hi - a.window) : 0;
+}
+
+// The blocks of tokens [tok0, tok0 + 2 tpt) of a sequence.
+__device__ __forceinline__ void item_blocks(const PromptArgs& a, Piece& p) {
+    p.b0 = 0x7FFFFFFF;
+    p.b1 = 0;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int k0 = p.tok0 + t * a.tpt;
+        p.tokens[t] = max(0, min(p.seq.n - k0, a.tpt));
+        p.lo[t] = p.hi[t] = p.last_hi[t] = 0;
+        if (p.tokens[t] > 0) {
+            p.last_hi[t] = p.seq.hi(k0 + p.tokens[t] - 1);
+            p.hi[t] = (p.last_hi[t] + kPB - 1) / kPB;
+            p.lo[t] = min(p.hi[t], prompt_lo_key(a, p.seq.hi(k0)) / kPB);
+        }
+        if (p.hi[t] > p.lo[t]) {
+            p.b0 = min(p.b0, p.lo[t]);
+            p.b1 = max(p.b1, p.hi[t]);
+        }
+    }
+    if (p.b1 == 0) p.b0 = 0;
+}
+
+// The CTA's work list. Items are numbered sequence by sequence; within a sequence in groups of
+// kv heads that together fill the GPU, so that the heads in flight keep their K and V in L2, and
+// within a group from the last tokens (most keys) to the first.
+struct PromptWork {
+    const int64_t* coarse;  // items before each run of `run` sequences
+    const int* units;       // blocks before each item (split lists)
+    int runs, run;          // entries of coarse, sequences per entry
+    int64_t items;
+    bool split;             // equal runs of blocks instead of whole items
+    int64_t at, end;        // whole: round, -; split: blocks
+    int64_t per;
+
+    __device__ __forceinline__ static int tiles(const PromptArgs& a, const PromptSeq& s) {
+        return (s.n + 2 * a.tpt - 1) / (2 * a.tpt);
+    }
+    __device__ __forceinline__ void item(const PromptArgs& a, int64_t k, Piece& p) const {
+        int lo = 0, hi = runs;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (coarse[mid] <= k) lo = mid;
+            else hi = mid;
+        }
+        int64_t r = k - coarse[lo];
+        int b = lo * run;
+        PromptSeq s = prompt_seq(a, b);
+        int nt = tiles(a, s);
+        while (r >= static_cast<int64_t>(nt) * a.kv.Hkv && b + 1 < a.kv.B) {
+            r -= static_cast<int64_t>(nt) * a.kv.Hkv;
+            s = prompt_seq(a, ++b);
+            nt = tiles(a, s);
+        }
+        nt = max(nt, 1);
+        const int group = max(1, (static_cast<int>(gridDim.x) + nt - 1) / nt);
+        const int64_t per_group = static_cast<int64_t>(nt) * group;
+        const int h0 = static_cast<int>(r / per_group) * group;
+        const int j = static_cast<int>(r % per_group);
+        const int heads = max(1, min(group, a.kv.Hkv - h0));
+        p.b = b;
+        p.seq = s;
+        p.h = min(h0 + j % heads, a.kv.Hkv - 1);
+        p.tok0 = (nt - 1 - j / heads) * 2 * a.tpt;
+        item_blocks(a, p);
+    }
+    __device__ __forceinline__ Piece next(const PromptArgs& a) {
+        Piece p;
+        p.valid = false;
+        if (!split) {
+            // rounds of items dealt in alternating direction
+            const int64_t g = gridDim.x, c = blockIdx.x;
+            const int64_t k = at * g + ((at & 1) ? g - 1 - c : c);
+            ++at;
+            if (at * g - g >= items || k >= items) return p;
+            item(a, k, p);
+            p.valid = true;
+            p.first = p.last = 0;
+            p.starts = 1;
+            return p;
+        }
+        if (at >= end) return p;
+        int lo = 0, hi = static_cast<int>(items);
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (units[mid] <= at) lo = mid;
+            else hi = mid;
+        }
+        item(a, lo, p);
+        p.valid = true;
+        const int u0 = units[lo], u1 = units[lo + 1];
+        p.first = u0 / static_cast<int>(per);
+        p.last = (u1 - 1) / static_cast<int>(per);
+        p.starts = at == u0;
+        const int64_t stop = min(end, static_cast<int64_t>(u1));
+        const int base = p.b0;
+        if (p.b1 > p.b0) {
+            p.b0 = base + static_cast<int>(at - u0);
+            p.b1 = base + static_cast<int>(stop - u0);
+        }
+        at = stop;
+        return p;
+    }
+};
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__(PromptSmem<D, FP8>::kThreads, 1)
+attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PromptArgs a) {
+    using L = PromptSmem<D, FP8>;
+    constexpr int NST = L::kStages, NRAW = L::kRaws;
+    constexpr uint32_t kIdescS = prompt_idesc(kPB, FP8, false);
+    constexpr uint32_t kIdescO = prompt_idesc(D, FP8, true);
+    constexpr uint32_t kHalf = 16384;  // bytes of 64 columns x 128 rows
+
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* const base_ptr = smem_raw + (base - raw);
+    const uint32_t bars = base + L::kBars;
+    auto full = [&](int s) { return bars + 8u * s; };
+    auto empty = [&](int s) { return bars + 8u * (NST + s); };
+    auto raw_full = [&](int s) { return bars + 8u * (2 * NST + s); };
+    auto raw_empty = [&](int s) { return bars + 8u * (2 * NST + NRAW + s); };
+    const uint32_t more = bars + 8u * (2 * NST + 2 * NRAW);
+    auto q_full = [&](int t) { return more + 8u * t; };
+    const uint32_t q_empty = more + 16u;
+    auto s_full = [&](int t) { return more + 24u + 8u * t; };
+    auto p_full = [&](int t) { return more + 40u + 8u * t; };
+    auto o_full = [&](int t) { return more + 56u + 8u * t; };
+    auto o_empty = [&](int t) { return more + 72u + 8u * t; };
+    const uint32_t drain = more + 88u;
+    auto join_in = [&](int t) { return more + 96u + 8u * t; };
+    auto join_out = [&](int t) { return more + 112u + 8u * t; };
+    uint32_t* const ctl = reinterpret_cast<uint32_t*>(base_ptr + L::kBars + 8 * L::kNumBars);
+    volatile uint32_t* const abort_flag = ctl + 1;
+    uint32_t* const s_last = ctl + 2;      // [2]
+    volatile uint32_t* const groups = ctl + 4;  // [8] loaded groups of 16 keys of the last 8 blocks
+    int64_t* const coarse = reinterpret_cast<int64_t*>(base_ptr + L::kTables);
+    int* const units = reinterpret_cast<int*>(coarse + kCoarse + 1);
+    int64_t* const found = reinterpret_cast<int64_t*>(base_ptr + L::kTables + (kCoarse + 1) * 8 +
+                                                      ((kPromptItems + 2) * 4 + 7) / 8 * 8);
+
+    const int warp = __shfl_sync(~0u, static_cast<int>(threadIdx.x) >> 5, 0);
+    const int lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NST; ++s) {
+            ptx::mbar_init(full(s), FP8 ? 4 : 1);
+            ptx::mbar_init(empty(s), 1);
+        }
+        for (int s = 0; s < NRAW; ++s) {
+            ptx::mbar_init(raw_full(s), 1);
+            ptx::mbar_init(raw_empty(s), 4);
+        }
+        for (int t = 0; t < 2; ++t) {
+            ptx::mbar_init(q_full(t), FP8 ? 4 : 1);
+            ptx::mbar_init(s_full(t), 1);
+            ptx::mbar_init(p_full(t), 4);
+            ptx::mbar_init(o_full(t), 1);
+            ptx::mbar_init(o_empty(t), 4);
+            ptx::mbar_init(join_in(t), 4);
+            ptx::mbar_init(join_out(t), 1);
+        }
+        ptx::mbar_init(q_empty, 1);
+        ptx::mbar_init(drain, 1);
+        *abort_flag = 0u;
+        ptx::fence_barrier_init();
+    }
+    if (!FP8 && warp == 9 && lane == 0) {
+        ptx::prefetch_tensormap(&tmQ);
+        ptx::prefetch_tensormap(&tmK);
+        ptx::prefetch_tensormap(&tmV);
+    }
+    if (warp == 8) {
+        ptx::tmem_alloc(ptx::smem_addr(ctl), 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+
+    // ---------------------------------------------------------------- the work list
+    PromptWork work;
+    work.coarse = coarse;
+    work.units = units;
+    work.run = (a.kv.B + kCoarse - 1) / kCoarse;
+    work.runs = (a.kv.B + work.run - 1) / work.run;
+    for (int e = threadIdx.x; e < work.runs; e += L::kThreads) {
+        int64_t n = 0;
+        for (int b = e * work.run; b < min(a.kv.B, (e + 1) * work.run); ++b)
+            n += static_cast<int64_t>(PromptWork::tiles(a, prompt_seq(a, b))) * a.kv.Hkv;
+        coarse[e] = n;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        const int each = (work.runs + 31) / 32;
+        int64_t sum = 0;
+        for (int i = 0; i < each; ++i)
+            if (lane * each + i < work.runs) sum += coarse[lane * each + i];
+        int64_t before = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(~0u, before, o);
+            if (lane >= o) before += v;
+        }
+        if (lane == 31) found[0] = before;
+        before -= sum;
+        for (int i = 0; i < each; ++i)
+            if (lane * each + i < work.runs) {
+                const int64_t n = coarse[lane * each + i];
+                coarse[lane * each + i] = before;
+                before += n;
+            }
+    }
+    __syncthreads();
+    work.items = found[0];
+    work.split = false;
+    work.at = 0;
+    work.end = 0;
+    work.per = 1;
+    if (work.items <= kPromptItems) {
+        // Few items: tabulate their blocks, and split the blocks evenly where the longest item,
+        // or the last round's, would keep the GPU waiting for more than a join costs (about
+        // kJoinBlocks blocks of time).
+        constexpr int kJoinBlocks = 8;
+        const int n = static_cast<int>(work.items);
+        for (int i = threadIdx.x; i < n; i += L::kThreads) {
+            Piece p;
+            work.item(a, i, p);
+            units[i] = max(1, p.b1 - p.b0);
+        }
+        __syncthreads();
+        if (warp == 0) {
+            const int each = (n + 31) / 32;
+            int sum = 0, most = 0;
+            for (int i = 0; i < each; ++i)
+                if (lane * each + i < n) {
+                    sum += units[lane * each + i];
+                    most = max(most, units[lane * each + i]);
+                }
+            int before = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(~0u, before, o);
+                if (lane >= o) before += v;
+                most = max(most, __shfl_xor_sync(~0u, most, o));
+            }
+            if (lane == 31) found[0] = before;
+            if (lane == 0) found[1] = most;
+            before -= sum;
+            for (int i = 0; i < each; ++i)
+                if (lane * each + i < n) {
+                    const int u = units[lane * each + i];
+                    units[lane * each + i] = before;
+                    before += u;
+                }
+        }
+        __syncthreads();
+        const int total = static_cast<int>(found[0]), most = static_cast<int>(found[1]);
+        if (threadIdx.x == 0) units[n] = total;
+        const int g = static_cast<int>(gridDim.x);
+        const int share = max((total + g - 1) / g, 1);
+        const int whole = n <= g ? most : share + most / 2;
+        if (whole > share + kJoinBlocks) {
+            work.split = true;
+            work.per = share;
+            work.at = static_cast<int64_t>(share) * blockIdx.x;
+            work.end = min(work.at + share, static_cast<int64_t>(total));
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(ctl);
+    auto tmem_s = [&](int t) { return tmem + 256u + 128u * t; };
+    auto tmem_o = [&](int t) { return tmem + 128u * t; };
+    auto wait = [&](uint32_t bar, uint32_t parity, int role) {
+        return __all_sync(~0u, ptx::mbar_wait(bar, parity, abort_flag, a.kv.status, kPromptCode | role));
+    };
+
+    // The register split sums to what the block was launched with (384 x 168, 512 x 128).
+    if (warp < 8) regs_up<FP8 ? 192 : 216>();
+    else regs_down<FP8 ? 64 : 72>();
+
+    if (warp < 8) {
+        // ------------------------------------------------------------ softmax of one tile
+        const int t = warp >> 2;
+        const int row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        uint32_t s_phase = 0, o_phase = 0, q_phase = 0, j_phase = 0, blocks = 0;
+        const int token = row / a.G, head = row - token * a.G;
+        for (Piece p = work.next(a); p.valid;) {
+            const bool mine = token < p.tokens[t] && token < a.tpt;
+            const int tok = p.tok0 + t * a.tpt + token;
+            const int hi = p.seq.hi(mine ? tok : p.seq.n - 1);
+            const int lo = prompt_lo_key(a, hi);
+            const int64_t qrow = p.seq.first + tok;
+            const int64_t qhead = static_cast<int64_t>(p.h) * a.G + head;
+            float c = a.scale_log2;
+            if constexpr (FP8) {
+                // Q in fp16: the row scaled by a power of two to a largest magnitude in [1, 2)
+                // (see the row kernel); one thread converts its own row
+                if (!wait(q_empty, q_phase ^ 1u, 1)) break;
+                q_phase ^= 1u;
+                const __nv_bfloat16* src = a.q + qrow * a.ldq + qhead * D;
+                uint4 v[D / 8];
+                float big = 0.0f;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    v[i] = mine ? load16(reinterpret_cast<const uint8_t*>(src + 8 * i)) : make_uint4(0, 0, 0, 0);
+                    float f[8];
+                    unpack8(v[i], f);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) big = fmaxf(big, fabsf(f[j]));
+                }
+                int e = static_cast<int>(__float_as_uint(big) >> 23) - 127;
+                if (e < -100 || e > 100) e = 0;
+                const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                c *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * a.kv.scales[p.h];
+                uint8_t* const dst = base_ptr + t * L::kTile + row * 128;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    float f[8];
+                    unpack8(v[i], f);
+                    *reinterpret_cast<uint4*>(dst + (i >> 3) * kHalf + (((i & 7) ^ (row & 7)) << 4)) =
+                        make_uint4(pack_half2(f[0] * down, f[1] * down), pack_half2(f[2] * down, f[3] * down),
+                                   pack_half2(f[4] * down, f[5] * down), pack_half2(f[6] * down, f[7] * down));
+                }
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full(t));
+            }
+            const int first_hi = p.seq.hi(p.tok0 + t * a.tpt);  // of the tile's first token
+            const int last_lo = prompt_lo_key(a, p.last_hi[t]);
+            float m = -CUDART_INF_F, l = 0.0f;  // reference maximum (log2 units), sum
+            const int begin = p.begin(t), end = p.end(t);
+            bool ok = true;
+            for (int i = begin; i < end; ++i) {
+                if (!(ok = wait(s_full(t), s_phase, 2))) break;
+                s_phase ^= 1u;
+                ptx::tc_fence_after();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) ptx::tmem_ld_32x32b_x32(tmem_s(t) + lanes + 32 * j, s[j]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) ptx::tmem_wait_ld(s[j]);
+                const int key0 = i * kPB;
+                const uint32_t have = groups[(blocks + i - p.b0) & 7];
+                if (first_hi < key0 + kPB || last_lo > key0 || have != 0xFFu) {
+                    const int below = hi - key0, from = lo - key0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            const int col = 32 * j + k;
+                            const bool on = col < below && col >= from && ((have >> (col >> 4)) & 1u);
+                            s[j][k] = on ? s[j][k] : 0xFF800000u;
+                        }
+                }
+                float top[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) top[j] = fmaxf(top[j], __uint_as_float(s[j][k]));
+                const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
+                float f = 1.0f;
+                if (now > m + kLazyLog2 || (m == -CUDART_INF_F && now != m)) {
+                    f = exp2_approx(m - now);
+                    m = now;
+                    l *= f;
+                }
+                // the reference moved: O of the blocks before is scaled. Its products are done:
+                // they were issued before this block's S, whose commit has arrived.
+                if (i > begin && __any_sync(~0u, f != 1.0f)) {
+#pragma unroll 1
+                    for (int j = 0; j < D; j += 32) {
+                        uint32_t o[32];
+                        ptx::tmem_ld_32x32b_x32(tmem_o(t) + lanes + j, o);
+                        ptx::tmem_wait_ld(o);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                        tmem_st_x32(tmem_o(t) + lanes + j, o);
+                    }
+                }
+                const float shift = (m == -CUDART_INF_F ? 0.0f : m) - (FP8 ? kRaiseLog2 : 0.0f);
+                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const int j = 2 * half + (k >> 4), x = 2 * (k & 15);
+                        const float p0 = exp2_approx(fmaf(__uint_as_float(s[j][x]), c, -shift));
+                        const float p1 = exp2_approx(fmaf(__uint_as_float(s[j][x + 1]), c, -shift));
+                        sum[2 * (k & 1)] += p0;
+                        sum[2 * (k & 1) + 1] += p1;
+                        w[k] = FP8 ? pack_half2(p0, p1) : pack_bf162(p0, p1);
+                    }
+                    tmem_st_x32(tmem_s(t) + lanes + 32 * half, w);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_wait_st();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full(t));
+            }
+            if (!ok) break;
+            // -------------------------------------------------------- the tile's result
+            const bool any = end > begin;
+            if (any) {
+                if (!wait(o_full(t), o_phase, 3)) break;
+                o_phase ^= 1u;
+                ptx::tc_fence_after();
+            }
+            blocks += p.b1 - p.b0;
+            const Piece nxt = work.next(a);
+            const bool whole = p.first == p.last;
+            float* const slots = a.partial + static_cast<int64_t>(t) * kPromptSlotFloats;
+            float* const slot = slots + (static_cast<int64_t>(blockIdx.x) * 2 + p.starts) * 2 * kPromptSlotFloats;
+            const float v_scale = FP8 ? a.kv.scales[a.kv.Hkv + p.h] : 1.0f;
+            __nv_bfloat16* const dst = a.out + qrow * a.ldo + qhead * D;
+            auto put = [&](int col, const float* v, float inv) {  // 32 columns of the row
+#pragma unroll
+                for (int k = 0; k < 32; k += 8) {
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = v[k + e] * inv;
+                    *reinterpret_cast<uint4*>(dst + col + k) = pack8_bf16(x);
+                }
+            };
+            auto put_lse = [&](float mm, float ll) {
+                if (a.lse)
+                    a.lse[qrow * a.Hq + qhead] =
+                        ll == 0.0f ? -CUDART_INF_F
+                                   : (mm + log2f(ll) - (FP8 ? kRaiseLog2 : 0.0f)) * 0.69314718055994531f;
+            };
+            const float inv = l == 0.0f ? 0.0f : v_scale / l;  // no keys: zeros
+#pragma unroll 1
+            for (int col = 0; col < D; col += 32) {
+                uint32_t o[32];
+                if (any) {
+                    ptx::tmem_ld_32x32b_x32(tmem_o(t) + lanes + col, o);
+                    ptx::tmem_wait_ld(o);
+                    if (col + 32 == D) {
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(o_empty(t));
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = 0u;
+                }
+                if (!mine) continue;
+                if (whole) {
+                    float v[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) v[k] = l == 0.0f ? 0.0f : __uint_as_float(o[k]);
+                    put(col, v, inv);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4)
+                        __stcg(reinterpret_cast<float4*>(slot + (col + k) * 128 + row * 4),
+                               make_float4(__uint_as_float(o[k]), __uint_as_float(o[k + 1]),
+                                           __uint_as_float(o[k + 2]), __uint_as_float(o[k + 3])));
+                }
+            }
+            if (whole) {
+                if (mine) put_lse(m, l);
+            } else if (p.tokens[t] > 0) {
+                // The last contributor to arrive sums all of them, first to last (see the row
+                // kernel); each tile's 128 threads count and join on their own.
+                if (mine) {
+                    __stcg(slot + 128 * 128 + row, m);
+                    __stcg(slot + 128 * 128 + 128 + row, l);
+                }
+                __threadfence();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(join_in(t));
+                if (warp == 4 * t) {
+                    if (!wait(join_in(t), j_phase, 13)) break;
+                    if (lane == 0) {
+                        __threadfence();
+                        const uint32_t n = atomicAdd(a.count + 2 * p.first + t, 1u);
+                        s_last[t] = n == static_cast<uint32_t>(p.last - p.first);
+                        if (s_last[t]) a.count[2 * p.first + t] = 0;
+                        __threadfence();
+                        mbar_arrive(join_out(t));
+                    }
+                    __syncwarp();
+                }
+                if (!wait(join_out(t), j_phase, 14)) break;
+                j_phase ^= 1u;
+                if (*reinterpret_cast<volatile uint32_t*>(s_last + t) && mine) {
+                    __threadfence();
+                    auto slot_of = [&](int cta) {
+                        return slots + (static_cast<int64_t>(cta) * 2 + (cta == p.first)) * 2 * kPromptSlotFloats;
+                    };
+                    float mm = -CUDART_INF_F;
+                    for (int x = p.first; x <= p.last; ++x)
+                        mm = fmaxf(mm, __ldcg(slot_of(x) + 128 * 128 + row));
+                    const float safe = mm == -CUDART_INF_F ? 0.0f : mm;
+                    float ll = 0.0f;
+                    for (int x = p.first; x <= p.last; ++x)
+                        ll += exp2_approx(__ldcg(slot_of(x) + 128 * 128 + row) - safe) *
+                              __ldcg(slot_of(x) + 128 * 128 + 128 + row);
+                    const float scale = ll == 0.0f ? 0.0f : v_scale / ll;
+#pragma unroll 1
+                    for (int col = 0; col < D; col += 32) {
+                        float v[32];
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) v[k] = 0.0f;
+#pragma unroll 1
+                        for (int x = p.first; x <= p.last; ++x) {
+                            const float* src = slot_of(x);
+                            const float w = exp2_approx(__ldcg(src + 128 * 128 + row) - safe);
+#pragma unroll
+                            for (int k = 0; k < 32; k += 4) {
+                                const float4 y = __ldcg(reinterpret_cast<const float4*>(src + (col + k) * 128 + row * 4));
+                                v[k] += w * y.x;
+                                v[k + 1] += w * y.y;
+                                v[k + 2] += w * y.z;
+                                v[k + 3] += w * y.w;
+                            }
+                        }
+                        put(col, v, scale);
+                    }
+                    put_lse(mm, ll);
+                }
+            }
+            p = nxt;
+        }
+    } else if (warp == 8) {
+        // ------------------------------------------------------------ MMA issuer
+        uint32_t stage = 0, phase = 0;
+        uint32_t q_phase = 0, p_phase[2] = {0, 0}, oe_phase[2] = {0, 0}, blocks = 0;
+        bool ok = true;
+        for (Piece p = work.next(a); ok && p.valid;) {
+            const Piece nxt = work.next(a);
+            if (p.b1 > p.b0 || FP8) {
+                if (!(ok = wait(q_full(0), q_phase, 4) && wait(q_full(1), q_phase, 4))) break;
+                q_phase ^= 1u;
+                ptx::tc_fence_after();
+            }
+            // K of block i and V of block i - 1 meet in step i: while one tile's softmax of
+            // block i - 1 runs, the other tile's two products of step i do.
+            for (int i = p.b0; ok && i <= p.b1; ++i) {
+                const bool has_k = i < p.b1, has_v = i > p.b0;
+                const uint32_t vs = stage, vph = phase;
+                uint32_t ks = stage, kph = phase;
+                if (has_v) {
+                    if (++ks == NST) {
+                        ks = 0;
+                        kph ^= 1u;
+                    }
+                }
+                const uint32_t sv = base + L::kStage0 + vs * L::kTile, sk = base + L::kStage0 + ks * L::kTile;
+                bool v_ready = false, k_ready = false;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const bool pv = has_v && i - 1 >= p.lo[t] && i - 1 < p.hi[t];
+                    const bool qk = has_k && i >= p.lo[t] && i < p.hi[t];
+                    if (pv) {
+                        if (!v_ready) {
+                            if (!(ok = wait(full(vs), vph, 5))) break;
+                            v_ready = true;
+                            // Rows of V that no query of the item may see, in a group of 16 that
+                            // the product reads: past the item's last key or in a page that is
+                            // not there. Their weights are 0, but 0 times what they hold may be
+                            // NaN; they are cleared first.
+                            const int in = max(p.last_hi[0], p.last_hi[1]) - (i - 1) * kPB;
+                            const uint32_t have = groups[(blocks + i - 1 - p.b0) & 7];
+                            if (in < kPB || have != 0xFFu) {
+                                const int upto = min(kPB, (in + 15) & ~15);
+                                for (int r = have == 0xFFu ? in : 0; r < upto; ++r)
+                                    if (r >= in || !((have >> (r >> 4)) & 1u))
+                                        if (lane < D / 8)
+                                            *reinterpret_cast<uint4*>(base_ptr + (sv - base) + (lane >> 3) * kHalf +
+                                                                      r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                                fence_async_shared();
+                                __syncwarp();
+                            }
+                            ptx::tc_fence_after();
+                        }
+                        const bool fresh = i - 1 == p.begin(t);
+                        if (fresh) {  // the tile's result before this one has been read
+                            if (!(ok = wait(o_empty(t), oe_phase[t] ^ 1u, 6))) break;
+                            oe_phase[t] ^= 1u;
+                        }
+                        if (!(ok = wait(p_full(t), p_phase[t], 7))) break;
+                        p_phase[t] ^= 1u;
+                        ptx::tc_fence_after();
+                        if (lane == 0) {
+                            const int steps = min(kPB, p.last_hi[t] - (i - 1) * kPB + 15) / 16;
+                            for (int k = 0; k < steps; ++k)
+                                mma_ts(tmem_o(t), tmem_s(t) + 8 * k, sdesc_v(sv) + 128 * k, kIdescO,
+                                       fresh && k == 0 ? 0u : 1u);
+                            if (i == p.end(t)) ptx::mma_commit(o_full(t));
+                        }
+                    }
+                    if (qk) {
+                        if (!k_ready) {
+                            if (!(ok = wait(full(ks), kph, 8))) break;
+                            k_ready = true;
+                            ptx::tc_fence_after();
+                        }
+                        if (lane == 0) {
+#pragma unroll
+                            for (int k = 0; k < D / 16; ++k) {
+                                const uint32_t off = (k >> 2) * (kHalf >> 4) + 2 * (k & 3);
+                                ptx::mma_bf16_ss(tmem_s(t), sdesc_k128(base + t * L::kTile) + off,
+                                                 sdesc_k128(sk) + off, kIdescS, k ? 1u : 0u);
+                            }
+                            ptx::mma_commit(s_full(t));
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                // stages whose block neither tile uses are passed over in the same order
+                if (has_v) {
+                    if (!v_ready && !(ok = wait(full(vs), vph, 5))) break;
+                    if (lane == 0) ptx::mma_commit(empty(vs));
+                    stage = ks;
+                    phase = kph;
+                }
+                if (has_k) {
+                    if (!k_ready && !(ok = wait(full(ks), kph, 8))) break;
+                    if (lane == 0) {
+                        ptx::mma_commit(empty(ks));
+                        if (i + 1 == p.b1) ptx::mma_commit(q_empty);  // the last use of Q
+                    }
+                    if (++stage == NST) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                __syncwarp();
+            }
+            if (FP8 && p.b1 == p.b0 && lane == 0) ptx::mma_commit(q_empty);
+            __syncwarp();
+            blocks += p.b1 - p.b0;
+            p = nxt;
+        }
+        if (lane == 0) {
+            // every product has completed before tensor memory is released
+            ptx::mma_commit(drain);
+            ptx::mbar_wait_drain(drain, 0);
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        // ------------------------------------------------------------ TMA producer
+        const int rows = min(1 << a.kv.page_shift, kPB);  // of a copy
+        const int copies = kPB / rows;
+        uint32_t stage = 0, phase = 0, issued = 0, q_phase = 0, q_loads = 0, blocks = 0;
+        constexpr int NR = FP8 ? NRAW : NST;
+        bool ok = true;
+        for (Piece p = work.next(a); ok && p.valid;) {
+            if (!FP8 && p.b1 > p.b0) {
+                if (!(ok = wait(q_empty, q_phase ^ 1u, 9))) break;
+                q_phase ^= 1u;
+                if (lane == 0) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        ptx::mbar_arrive_expect_tx(q_full(t), static_cast<uint32_t>(a.tpt * a.G) * D * 2);
+                        for (int x = 0; x < D / 64; ++x)
+                            ptx::tma_load_3d(base + t * L::kTile + x * kHalf, &tmQ, q_full(t), 64 * x, p.h * a.G,
+                                             p.seq.first + p.tok0 + t * a.tpt);
+                    }
+                }
+                ++q_loads;
+            }
+            const int top = max(p.last_hi[0], p.last_hi[1]);
+            for (int i = p.b0; ok && i < p.b1; ++i) {
+                const int key = i * kPB + lane * rows;
+                const bool in = lane < copies && key < top;
+                const int64_t page = in ? kv_page(a.kv, p.b, key) : -1;
+                const uint32_t there = __ballot_sync(~0u, page >= 0);
+                // groups of 16 keys that are there; those past the item's keys count as such
+                uint32_t have = 0;
+                for (int x = 0; x < copies; ++x)
+                    if (((there >> x) & 1u) || i * kPB + x * rows >= top)
+                        have |= ((1u << (rows / 16)) - 1u) << (x * (rows / 16));
+                if (lane == 0) groups[(blocks + i - p.b0) & 7] = have;
+                const int slot = key & ((1 << a.kv.page_shift) - 1);
+                for (int kv = 0; kv < 2; ++kv) {
+                    const uint32_t bar_full = FP8 ? raw_full(stage) : full(stage);
+                    if (!(ok = wait(FP8 ? raw_empty(stage) : empty(stage), phase ^ 1u, 10))) break;
+                    if (lane == 0)
+                        ptx::mbar_arrive_expect_tx(bar_full, static_cast<uint32_t>(__popc(there) * rows) * D * (FP8 ? 1 : 2));
+                    __syncwarp();
+                    if (page >= 0) {
+                        if constexpr (FP8) {
+                            bulk_load(base + L::kRaw0 + stage * L::kRaw + lane * rows * D,
+                                      (kv ? a.kv.V : a.kv.K) + page * a.kv.page_bytes + p.h * a.kv.head_bytes +
+                                          static_cast<int64_t>(slot) * D,
+                                      static_cast<uint32_t>(rows) * D, bar_full);
+                        } else {
+                            const uint32_t dst = base + L::kStage0 + stage * L::kTile + lane * rows * 128;
+#pragma unroll
+                            for (int x = 0; x < D / 64; ++x)
+                                ptx::tma_load_3d(dst + x * kHalf, kv ? &tmV : &tmK, bar_full, 64 * x,
+                                                 (p.h << a.kv.page_shift) + slot, static_cast<int>(page));
+                        }
+                    }
+                    __syncwarp();
+                    ++issued;
+                    if (++stage == NR) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            blocks += p.b1 - p.b0;
+            p = work.next(a);
+        }
+        if (!ok && lane == 0) {
+            // wait for the copies still in flight before the CTA may exit
+            for (uint32_t s = 0; s < NR && s < issued; ++s) {
+                const uint32_t last = s + ((issued - 1 - s) / NR) * NR;
+                ptx::mbar_wait_drain(FP8 ? raw_full(s) : full(s), (last / NR) & 1u);
+            }
+            if (q_loads)
+                for (int t = 0; t < 2; ++t) ptx::mbar_wait_drain(q_full(t), (q_loads - 1) & 1u);
+        }
+        __syncwarp();
+    } else {
+        if constexpr (FP8) {
+            if (warp >= 12) {
+                // -------------------------------------------------------- e4m3 -> fp16
+                uint32_t rs = 0, rph = 0, stage = 0, phase = 0;
+                bool ok = true;
+                const int tid = (warp - 12) * 32 + lane;
+                for (Piece p = work.next(a); ok && p.valid; p = work.next(a)) {
+                    for (int n = 2 * (p.b1 - p.b0); ok && n > 0; --n) {
+                        if (!(ok = wait(raw_full(rs), rph, 11))) break;
+                        if (!(ok = wait(empty(stage), phase ^ 1u, 12))) break;
+                        const uint8_t* src = base_ptr + L::kRaw0 + rs * L::kRaw;
+                        uint8_t* dst = base_ptr + L::kStage0 + stage * L::kTile;
+                        constexpr int kPieces = kPB * D / 16 / 128;  // 16-byte pieces per thread
+#pragma unroll 4
+                        for (int x = 0; x < kPieces; ++x) {
+                            const int piece = x * 128 + tid;
+                            const int r = piece / (D / 16), j = piece % (D / 16);
+                            const uint4 v = *reinterpret_cast<const uint4*>(src + piece * 16);
+                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                            uint32_t h[8];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                h[2 * k] = e4m3x2_to_half2(w[k] & 0xFFFF);
+                                h[2 * k + 1] = e4m3x2_to_half2(w[k] >> 16);
+                            }
+                            // the two 16-byte chunks in an order that spreads a row's writes over
+                            // all banks
+                            uint8_t* const d = dst + (j >> 2) * kHalf + r * 128;
+                            const int c0 = 2 * (j & 3), swap = (j >> 2) & 1;
+                            const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+                            *reinterpret_cast<uint4*>(d + (((c0 + swap) ^ (r & 7)) << 4)) = swap ? hi : lo;
+                            *reinterpret_cast<uint4*>(d + (((c0 + 1 - swap) ^ (r & 7)) << 4)) = swap ? lo : hi;
+                        }
+                        fence_async_shared();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(full(stage));
+                            mbar_arrive(raw_empty(rs));
+                        }
+                        if (++rs == NRAW) {
+                            rs = 0;
+                            rph ^= 1u;
+                        }
+                        if (++stage == NST) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                }
+            }
+        }
+    }
+
+    __syncwarp();
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace tpmlp

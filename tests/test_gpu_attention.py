@@ -272,6 +272,77 @@ def test_prompt_matches_definition(lib, kv, Hq, Hkv, D, page, lens, new, window)
     check_rows(c, q, got, lse, prompt_spans(lens, new, window), Hq, D, 1.0 / math.sqrt(D))
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Hq,Hkv,D,page,lens,new,window", [
+    (8, 2, 128, 64, [9001], [3], 0),               # few queries, many keys: split and joined
+    (4, 1, 64, 16, [20011, 5, 0, 129], [40, 2, 0, 129], 0),
+    (4, 4, 128, 128, [7000, 7000], [300, 17], 3000),
+])
+def test_prompt_splits_long_sequences(lib, kv, Hq, Hkv, D, page, lens, new, window):
+    c = ref.make(Hkv, D, page, kv, lens, seed=17)
+    q = queries(sum(new), Hq, D, 17) * 2
+    cu = torch.tensor([sum(new[:b]) for b in range(len(new) + 1)], dtype=torch.int32).cuda()
+    with tp.Attention(Hq, Hkv, D, page, kv_dtype=kv) as attn:
+        cache = on_device(c, attn)
+        got, lse = attn.prompt(q.cuda(), cu, cache, window=window, return_lse=True)
+        ok(attn)
+        for _ in range(3):  # deterministic, and the counters are back at 0
+            assert torch.equal(attn.prompt(q.cuda(), cu, cache, window=window), got)
+        ok(attn)
+    spans = prompt_spans(lens, new, window)
+    check_rows(c, q, got, lse, spans[:6] + spans[6::23] + spans[-3:], Hq, D, 1.0 / math.sqrt(D))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_prompt_many_items(lib, kv):
+    """More items than a block tabulates (whole items, dealt in rounds): rows checked in part."""
+    lens, new = [3300, 50, 700], [3000, 50, 699]
+    Hq, Hkv, D = 96, 12, 64
+    c = ref.make(Hkv, D, 32, kv, lens, seed=18)
+    q = queries(sum(new), Hq, D, 18)
+    cu = torch.tensor([0, 3000, 3050, 3749], dtype=torch.int32).cuda()
+    with tp.Attention(Hq, Hkv, D, 32, kv_dtype=kv) as attn:
+        got, lse = attn.prompt(q.cuda(), cu, on_device(c, attn), return_lse=True)
+        ok(attn)
+    check_rows(c, q, got, lse, prompt_spans(lens, new, 0)[::97], Hq, D, 0.125)
+
+
+def test_prompt_many_sequences(lib):
+    """More sequences than the table of sequences has entries."""
+    lens = [(5 * b) % 23 for b in range(1500)]
+    new = [min(n, (3 * b) % 7) for b, n in enumerate(lens)]
+    c = ref.make(1, 64, 16, "bf16", lens, seed=19)
+    q = queries(sum(new), 2, 64, 19)
+    cu = torch.tensor([sum(new[:b]) for b in range(1501)], dtype=torch.int32).cuda()
+    with tp.Attention(2, 1, 64, 16) as attn:
+        got, lse = attn.prompt(q.cuda(), cu, on_device(c, attn), return_lse=True)
+        ok(attn)
+    check_rows(c, q, got, lse, prompt_spans(lens, new, 0), 2, 64, 0.125)
+
+
+def test_prompt_replays_with_other_lengths(lib):
+    lens, new = [300, 90], [100, 90]
+    c = ref.make(2, 128, 32, "bf16", lens, seed=20)
+    q = queries(190, 4, 128, 20)
+    with tp.Attention(4, 2, 128, 32) as attn:
+        cache = on_device(c, attn)
+        qd, out = q.cuda(), torch.empty((190, 512), dtype=torch.bfloat16, device="cuda")
+        cu = torch.tensor([0, 100, 190], dtype=torch.int32, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            attn.prompt(qd, cu, cache, out=out)
+        for now, n in ((lens, new), ([200, 20], [170, 20]), ([0, 90], [0, 1])):
+            cache.lens.copy_(torch.tensor(now, dtype=torch.int32))
+            cu.copy_(torch.tensor([0, n[0], n[0] + n[1]], dtype=torch.int32))
+            out.fill_(7.0)
+            graph.replay()
+            ok(attn)
+            want, lse = attn.prompt(qd, cu, cache, return_lse=True)
+            ok(attn)
+            assert torch.equal(out[:sum(n)], want[:sum(n)]) and bool((out[sum(n):] == 7.0).all())
+            check_rows(c, q, out, lse, prompt_spans(now, n, 0)[::7], 4, 128, 128 ** -0.5)
+
+
 # ------------------------------------------------------------------ bad tables
 def test_bad_pages_are_left_out_and_reported(lib):
     """A page outside the pool: its keys are left out of decode and prompt, append drops the
