@@ -11,8 +11,10 @@
 // While the softmax warps of one tile work, the tensor core runs the other tile's two products.
 //
 // Warps: 0-3 softmax of tile 0, 4-7 of tile 1 (a warp may read the 32 tensor-memory lanes of its
-// rank mod 4), 8 issues the MMAs, 9 loads K and V (and Q) by TMA, page by page, 10-11 idle;
-// e4m3 caches: 12-15 convert the loaded bytes to fp16.
+// rank mod 4), 8 and 10 issue the MMAs of tile 0 and 1, 9 loads K and V (and Q) by TMA, page by
+// page, 11 makes the work list; e4m3 caches: 12-15 convert the loaded bytes to fp16. One warp
+// per tile issues MMAs because each waits for four barriers a block: with one warp for both
+// tiles the tensor core idled during those waits (GPT-3-shaped prompt: 516 us against MEASURE2).
 #pragma once
 
 #include "tpmlp_attn.cuh"
@@ -51,12 +53,13 @@ struct PromptSmem {
     static constexpr uint32_t kTile = kPB * D * 2;   // a Q, K or V tile of 16-bit values
     static constexpr uint32_t kRaw = FP8 ? kPB * D : 0;
     static constexpr int kStages = D == 128 ? (FP8 ? 3 : 4) : 6;
-    static constexpr int kRaws = FP8 ? 3 : 0;
+    static constexpr int kRaws = FP8 ? (D == 128 ? 2 : 3) : 0;
     static constexpr uint32_t kStage0 = 2 * kTile;
     static constexpr uint32_t kRaw0 = kStage0 + kStages * kTile;
     static constexpr uint32_t kBars = kRaw0 + kRaws * kRaw;
-    static constexpr int kNumBars = 2 * kStages + 2 * kRaws + 16;
-    static constexpr uint32_t kTables = kBars + (8 * kNumBars + 64 + 127) / 128 * 128;
+    static constexpr int kNumBars = 2 * kStages + 2 * kRaws + 24;
+    static constexpr uint32_t kStore0 = kBars + (8 * kNumBars + 64 + 4 * 96 + 127) / 128 * 128;
+    static constexpr uint32_t kTables = kStore0 + 8 * 2048;  // 2 KB of output staging per softmax warp
     static constexpr uint32_t kTotal = 1024 + kTables + (kCoarse + 1) * 8 + (kPromptItems + 1) * 4 + 256;
     static_assert(kTotal <= 232448, "dynamic shared memory per CTA");
     static constexpr int kThreads = FP8 ? 512 : 384;
@@ -101,6 +104,17 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
         "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
         : "memory");
 }
+// One lane of the (converged) warp, the same one every time: the MMAs of a warp are issued and
+// committed by one thread.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
 template <int R>
 __device__ __forceinline__ void regs_up() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
@@ -108,6 +122,31 @@ __device__ __forceinline__ void regs_up() {
 template <int R>
 __device__ __forceinline__ void regs_down() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+// Packed fp32 pairs and the three-operand maximum.
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+    return d;
+}
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(x), "f"(y), "f"(z));
+    return d;
 }
 
 // B operand with the reduction (keys) along rows: blocks of 64 columns of D, each 128 keys x 128
@@ -141,8 +180,9 @@ __device__ __forceinline__ PromptSeq prompt_seq(const PromptArgs& a, int b) {
 
 // An item, or the part of its key blocks [b0, b1) that one CTA computes.
 struct Piece {
-    bool valid;
-    int b, h, tok0;        // sequence, kv head, first token of tile 0
+    int valid;
+    int h, tok0;           // kv head, first token of tile 0
+    int b;                 // sequence
     PromptSeq seq;
     int tokens[2];         // of each tile
     int lo[2], hi[2];      // each tile's blocks
@@ -153,6 +193,8 @@ struct Piece {
     __device__ __forceinline__ int begin(int t) const { return max(lo[t], b0); }
     __device__ __forceinline__ int end(int t) const { return min(hi[t], b1); }
 };
+static_assert(sizeof(Piece) <= 96, "piece slots");
+constexpr int kPieces = 4;  // pieces between the work list's warp and the others
 
 __device__ __forceinline__ int prompt_lo_key(const PromptArgs& a, int hi) {
     return a.window > 0 ? max(0, hi - a.window) : 0;
@@ -225,7 +267,7 @@ struct PromptWork {
     }
     __device__ __forceinline__ Piece next(const PromptArgs& a) {
         Piece p;
-        p.valid = false;
+        p.valid = 0;
         if (!split) {
             // rounds of items dealt in alternating direction
             const int64_t g = gridDim.x, c = blockIdx.x;
@@ -233,7 +275,7 @@ struct PromptWork {
             ++at;
             if (at * g - g >= items || k >= items) return p;
             item(a, k, p);
-            p.valid = true;
+            p.valid = 1;
             p.first = p.last = 0;
             p.starts = 1;
             return p;
@@ -246,7 +288,7 @@ struct PromptWork {
             else hi = mid;
         }
         item(a, lo, p);
-        p.valid = true;
+        p.valid = 1;
         const int u0 = units[lo], u1 = units[lo + 1];
         p.first = u0 / static_cast<int>(per);
         p.last = (u1 - 1) / static_cast<int>(per);
@@ -291,10 +333,13 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     const uint32_t drain = more + 88u;
     auto join_in = [&](int t) { return more + 96u + 8u * t; };
     auto join_out = [&](int t) { return more + 112u + 8u * t; };
+    auto piece_full = [&](int s) { return more + 128u + 8u * s; };
+    auto piece_empty = [&](int s) { return more + 160u + 8u * s; };
     uint32_t* const ctl = reinterpret_cast<uint32_t*>(base_ptr + L::kBars + 8 * L::kNumBars);
     volatile uint32_t* const abort_flag = ctl + 1;
     uint32_t* const s_last = ctl + 2;      // [2]
     volatile uint32_t* const groups = ctl + 4;  // [8] loaded groups of 16 keys of the last 8 blocks
+    const Piece* const pieces = reinterpret_cast<const Piece*>(base_ptr + L::kBars + 8 * L::kNumBars + 64);
     int64_t* const coarse = reinterpret_cast<int64_t*>(base_ptr + L::kTables);
     int* const units = reinterpret_cast<int*>(coarse + kCoarse + 1);
     int64_t* const found = reinterpret_cast<int64_t*>(base_ptr + L::kTables + (kCoarse + 1) * 8 +
@@ -306,7 +351,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     if (threadIdx.x == 0) {
         for (int s = 0; s < NST; ++s) {
             ptx::mbar_init(full(s), FP8 ? 4 : 1);
-            ptx::mbar_init(empty(s), 1);
+            ptx::mbar_init(empty(s), 2);
         }
         for (int s = 0; s < NRAW; ++s) {
             ptx::mbar_init(raw_full(s), 1);
@@ -321,8 +366,12 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             ptx::mbar_init(join_in(t), 4);
             ptx::mbar_init(join_out(t), 1);
         }
-        ptx::mbar_init(q_empty, 1);
-        ptx::mbar_init(drain, 1);
+        for (int s = 0; s < kPieces; ++s) {
+            ptx::mbar_init(piece_full(s), 1);
+            ptx::mbar_init(piece_empty(s), FP8 ? 15 : 11);
+        }
+        ptx::mbar_init(q_empty, 2);
+        ptx::mbar_init(drain, 2);
         *abort_flag = 0u;
         ptx::fence_barrier_init();
     }
@@ -433,13 +482,34 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(ctl);
     auto tmem_s = [&](int t) { return tmem + 256u + 128u * t; };
     auto tmem_o = [&](int t) { return tmem + 128u * t; };
+    // The bounded wait reads the global timer, which takes longer than most waits here last: poll
+    // for a while first.
     auto wait = [&](uint32_t bar, uint32_t parity, int role) {
-        return __all_sync(~0u, ptx::mbar_wait(bar, parity, abort_flag, a.kv.status, kPromptCode | role));
+        bool done = false;
+        for (int n = 0; n < 64 && !done; ++n) done = ptx::mbar_try_wait(bar, parity);
+        return __all_sync(~0u, done || ptx::mbar_wait(bar, parity, abort_flag, a.kv.status, kPromptCode | role));
     };
 
     // The register split sums to what the block was launched with (384 x 168, 512 x 128).
     if (warp < 8) regs_up<FP8 ? 192 : 216>();
     else regs_down<FP8 ? 64 : 72>();
+
+    // The pieces, in the order that every role goes through them. next_piece() waits for one (null:
+    // no more, or a wait gave up); release_piece() hands its slot back.
+    uint32_t piece_at = 0;
+    auto piece_of = [&](uint32_t k) {
+        return reinterpret_cast<const Piece*>(reinterpret_cast<const uint8_t*>(pieces) + (k % kPieces) * 96);
+    };
+    auto next_piece = [&]() -> const Piece* {
+        if (!wait(piece_full(piece_at % kPieces), (piece_at / kPieces) & 1u, 15)) return nullptr;
+        const Piece* p = piece_of(piece_at);
+        return p->valid ? p : nullptr;
+    };
+    auto release_piece = [&] {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(piece_empty(piece_at % kPieces));
+        ++piece_at;
+    };
 
     if (warp < 8) {
         // ------------------------------------------------------------ softmax of one tile
@@ -448,20 +518,17 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         uint32_t s_phase = 0, o_phase = 0, q_phase = 0, j_phase = 0, blocks = 0;
         const int token = row / a.G, head = row - token * a.G;
-        for (Piece p = work.next(a); p.valid;) {
-            const bool mine = token < p.tokens[t] && token < a.tpt;
-            const int tok = p.tok0 + t * a.tpt + token;
-            const int hi = p.seq.hi(mine ? tok : p.seq.n - 1);
-            const int lo = prompt_lo_key(a, hi);
-            const int64_t qrow = p.seq.first + tok;
-            const int64_t qhead = static_cast<int64_t>(p.h) * a.G + head;
+        while (const Piece* p = next_piece()) {
+            const bool mine = token < p->tokens[t];
+            const int tok = p->tok0 + t * a.tpt + token;
             float c = a.scale_log2;
             if constexpr (FP8) {
                 // Q in fp16: the row scaled by a power of two to a largest magnitude in [1, 2)
                 // (see the row kernel); one thread converts its own row
                 if (!wait(q_empty, q_phase ^ 1u, 1)) break;
                 q_phase ^= 1u;
-                const __nv_bfloat16* src = a.q + qrow * a.ldq + qhead * D;
+                const __nv_bfloat16* src = a.q + static_cast<int64_t>(p->seq.first + tok) * a.ldq +
+                                           (static_cast<int64_t>(p->h) * a.G + head) * D;
                 uint4 v[D / 8];
                 float big = 0.0f;
 #pragma unroll
@@ -475,7 +542,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 int e = static_cast<int>(__float_as_uint(big) >> 23) - 127;
                 if (e < -100 || e > 100) e = 0;
                 const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                c *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * a.kv.scales[p.h];
+                c *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * a.kv.scales[p->h];
                 uint8_t* const dst = base_ptr + t * L::kTile + row * 128;
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i) {
@@ -489,39 +556,50 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 __syncwarp();
                 if (lane == 0) mbar_arrive(q_full(t));
             }
-            const int first_hi = p.seq.hi(p.tok0 + t * a.tpt);  // of the tile's first token
-            const int last_lo = prompt_lo_key(a, p.last_hi[t]);
             float m = -CUDART_INF_F, l = 0.0f;  // reference maximum (log2 units), sum
-            const int begin = p.begin(t), end = p.end(t);
+            const int begin = p->begin(t), end = p->end(t);
+            // keys that this row sees: [lo, hi); that every row of the tile sees: [last_lo, first_hi)
+            const int hi = p->seq.hi(mine ? tok : p->seq.n - 1);
+            const int lo = prompt_lo_key(a, hi);
+            const int first_hi = p->seq.hi(p->tok0 + t * a.tpt);
+            const int last_lo = prompt_lo_key(a, p->last_hi[t]);
+            const uint32_t block0 = blocks - p->b0;
+            blocks += p->b1 - p->b0;
             bool ok = true;
             for (int i = begin; i < end; ++i) {
                 if (!(ok = wait(s_full(t), s_phase, 2))) break;
                 s_phase ^= 1u;
                 ptx::tc_fence_after();
-                uint32_t s[4][32];
+                uint32_t s[128];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) ptx::tmem_ld_32x32b_x32(tmem_s(t) + lanes + 32 * j, s[j]);
+                for (int j = 0; j < 4; ++j)
+                    ptx::tmem_ld_32x32b_x32(tmem_s(t) + lanes + 32 * j, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * j));
 #pragma unroll
-                for (int j = 0; j < 4; ++j) ptx::tmem_wait_ld(s[j]);
+                for (int j = 0; j < 4; ++j) ptx::tmem_wait_ld(*reinterpret_cast<uint32_t(*)[32]>(s + 32 * j));
                 const int key0 = i * kPB;
-                const uint32_t have = groups[(blocks + i - p.b0) & 7];
-                if (first_hi < key0 + kPB || last_lo > key0 || have != 0xFFu) {
+                const uint32_t have = groups[(block0 + i) & 7];
+                if (last_lo > key0 || have != 0xFFu) {
                     const int below = hi - key0, from = lo - key0;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                    for (int k = 0; k < 128; ++k) {
+                        const bool on = k < below && k >= from && ((have >> (k >> 4)) & 1u);
+                        s[k] = on ? s[k] : 0xFF800000u;
+                    }
+                } else if (first_hi < key0 + kPB) {
+                    const int below = hi - key0;
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            const int col = 32 * j + k;
-                            const bool on = col < below && col >= from && ((have >> (col >> 4)) & 1u);
-                            s[j][k] = on ? s[j][k] : 0xFF800000u;
-                        }
+                    for (int k = 0; k < 128; ++k) s[k] = k < below ? s[k] : 0xFF800000u;
                 }
-                float top[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+                float top[4];
 #pragma unroll
-                for (int k = 0; k < 32; ++k)
+                for (int j = 0; j < 4; ++j) {
+                    top[j] = __uint_as_float(s[j]);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) top[j] = fmaxf(top[j], __uint_as_float(s[j][k]));
-                const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
+                    for (int k = 4; k < 124; k += 8)
+                        top[j] = max3(top[j], __uint_as_float(s[k + j]), __uint_as_float(s[k + 4 + j]));
+                    top[j] = fmaxf(top[j], __uint_as_float(s[124 + j]));
+                }
+                const float now = fmaxf(max3(top[0], top[1], top[2]), top[3]) * c;
                 float f = 1.0f;
                 if (now > m + kLazyLog2 || (m == -CUDART_INF_F && now != m)) {
                     f = exp2_approx(m - now);
@@ -541,23 +619,25 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                         tmem_st_x32(tmem_o(t) + lanes + j, o);
                     }
                 }
-                const float shift = (m == -CUDART_INF_F ? 0.0f : m) - (FP8 ? kRaiseLog2 : 0.0f);
-                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                // P = 2^(S c - m), two values to an instruction where there is one
+                const float shift = (FP8 ? kRaiseLog2 : 0.0f) - (m == -CUDART_INF_F ? 0.0f : m);
+                const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
+                float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     uint32_t w[32];
 #pragma unroll
                     for (int k = 0; k < 32; ++k) {
-                        const int j = 2 * half + (k >> 4), x = 2 * (k & 15);
-                        const float p0 = exp2_approx(fmaf(__uint_as_float(s[j][x]), c, -shift));
-                        const float p1 = exp2_approx(fmaf(__uint_as_float(s[j][x + 1]), c, -shift));
-                        sum[2 * (k & 1)] += p0;
-                        sum[2 * (k & 1) + 1] += p1;
-                        w[k] = FP8 ? pack_half2(p0, p1) : pack_bf162(p0, p1);
+                        const int x = 64 * half + 2 * k;
+                        float2 e = fma2(make_float2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), c2, shift2);
+                        e.x = exp2_approx(e.x);
+                        e.y = exp2_approx(e.y);
+                        sum[k & 1] = add2(sum[k & 1], e);
+                        w[k] = FP8 ? pack_half2(e.x, e.y) : pack_bf162(e.x, e.y);
                     }
                     tmem_st_x32(tmem_s(t) + lanes + 32 * half, w);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 tmem_wait_st();
                 ptx::tc_fence_before();
                 __syncwarp();
@@ -571,61 +651,76 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 o_phase ^= 1u;
                 ptx::tc_fence_after();
             }
-            blocks += p.b1 - p.b0;
-            const Piece nxt = work.next(a);
-            const bool whole = p.first == p.last;
+            const int64_t qrow = p->seq.first + tok;
+            const int64_t qhead = static_cast<int64_t>(p->h) * a.G + head;
+            const int from = p->first, upto = p->last;
+            const bool whole = from == upto;
             float* const slots = a.partial + static_cast<int64_t>(t) * kPromptSlotFloats;
-            float* const slot = slots + (static_cast<int64_t>(blockIdx.x) * 2 + p.starts) * 2 * kPromptSlotFloats;
-            const float v_scale = FP8 ? a.kv.scales[a.kv.Hkv + p.h] : 1.0f;
-            __nv_bfloat16* const dst = a.out + qrow * a.ldo + qhead * D;
-            auto put = [&](int col, const float* v, float inv) {  // 32 columns of the row
+            float* const slot = slots + (static_cast<int64_t>(blockIdx.x) * 2 + p->starts) * 2 * kPromptSlotFloats;
+            const float v_scale = FP8 ? a.kv.scales[a.kv.Hkv + p->h] : 1.0f;
+            __nv_bfloat16* const dst = mine ? a.out + qrow * a.ldo + qhead * D : nullptr;
+            uint8_t* const stage = base_ptr + L::kStore0 + warp * 2048;
+            // 32 columns of the warp's 32 rows: through shared memory, so that four lanes write 64
+            // contiguous bytes of a row
+            auto put = [&](int col, const float* v, float inv) {
+                __syncwarp();
 #pragma unroll
-                for (int k = 0; k < 32; k += 8) {
+                for (int k = 0; k < 4; ++k) {
                     float x[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = v[k + e] * inv;
-                    *reinterpret_cast<uint4*>(dst + col + k) = pack8_bf16(x);
+                    for (int e = 0; e < 8; ++e) x[e] = v[8 * k + e] * inv;
+                    *reinterpret_cast<uint4*>(stage + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) = pack8_bf16(x);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int r = 8 * k + (lane >> 2), x = lane & 3;
+                    __nv_bfloat16* const to = reinterpret_cast<__nv_bfloat16*>(
+                        __shfl_sync(~0u, reinterpret_cast<unsigned long long>(dst), r));
+                    const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 64 + ((x ^ ((r >> 1) & 3)) << 4));
+                    if (to) *reinterpret_cast<uint4*>(to + col + 8 * x) = w;
                 }
             };
             auto put_lse = [&](float mm, float ll) {
-                if (a.lse)
+                if (a.lse && mine)
                     a.lse[qrow * a.Hq + qhead] =
                         ll == 0.0f ? -CUDART_INF_F
                                    : (mm + log2f(ll) - (FP8 ? kRaiseLog2 : 0.0f)) * 0.69314718055994531f;
             };
             const float inv = l == 0.0f ? 0.0f : v_scale / l;  // no keys: zeros
+            if (p->tokens[t] > 0) {
 #pragma unroll 1
-            for (int col = 0; col < D; col += 32) {
-                uint32_t o[32];
-                if (any) {
-                    ptx::tmem_ld_32x32b_x32(tmem_o(t) + lanes + col, o);
-                    ptx::tmem_wait_ld(o);
-                    if (col + 32 == D) {
-                        ptx::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(o_empty(t));
+                for (int col = 0; col < D; col += 32) {
+                    uint32_t o[32];
+                    if (any) {
+                        ptx::tmem_ld_32x32b_x32(tmem_o(t) + lanes + col, o);
+                        ptx::tmem_wait_ld(o);
+                        if (col + 32 == D) {
+                            ptx::tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(o_empty(t));
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = 0u;
                     }
-                } else {
+                    if (whole) {
+                        float v[32];
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] = 0u;
-                }
-                if (!mine) continue;
-                if (whole) {
-                    float v[32];
+                        for (int k = 0; k < 32; ++k) v[k] = l == 0.0f ? 0.0f : __uint_as_float(o[k]);
+                        put(col, v, inv);
+                    } else if (mine) {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) v[k] = l == 0.0f ? 0.0f : __uint_as_float(o[k]);
-                    put(col, v, inv);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 32; k += 4)
-                        __stcg(reinterpret_cast<float4*>(slot + (col + k) * 128 + row * 4),
-                               make_float4(__uint_as_float(o[k]), __uint_as_float(o[k + 1]),
-                                           __uint_as_float(o[k + 2]), __uint_as_float(o[k + 3])));
+                        for (int k = 0; k < 32; k += 4)
+                            __stcg(reinterpret_cast<float4*>(slot + (col + k) * 128 + row * 4),
+                                   make_float4(__uint_as_float(o[k]), __uint_as_float(o[k + 1]),
+                                               __uint_as_float(o[k + 2]), __uint_as_float(o[k + 3])));
+                    }
                 }
             }
             if (whole) {
-                if (mine) put_lse(m, l);
-            } else if (p.tokens[t] > 0) {
+                put_lse(m, l);
+            } else if (p->tokens[t] > 0) {
                 // The last contributor to arrive sums all of them, first to last (see the row
                 // kernel); each tile's 128 threads count and join on their own.
                 if (mine) {
@@ -639,9 +734,9 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     if (!wait(join_in(t), j_phase, 13)) break;
                     if (lane == 0) {
                         __threadfence();
-                        const uint32_t n = atomicAdd(a.count + 2 * p.first + t, 1u);
-                        s_last[t] = n == static_cast<uint32_t>(p.last - p.first);
-                        if (s_last[t]) a.count[2 * p.first + t] = 0;
+                        const uint32_t n = atomicAdd(a.count + 2 * from + t, 1u);
+                        s_last[t] = n == static_cast<uint32_t>(upto - from);
+                        if (s_last[t]) a.count[2 * from + t] = 0;
                         __threadfence();
                         mbar_arrive(join_out(t));
                     }
@@ -649,36 +744,38 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 }
                 if (!wait(join_out(t), j_phase, 14)) break;
                 j_phase ^= 1u;
-                if (*reinterpret_cast<volatile uint32_t*>(s_last + t) && mine) {
+                if (*reinterpret_cast<volatile uint32_t*>(s_last + t)) {
                     __threadfence();
                     auto slot_of = [&](int cta) {
-                        return slots + (static_cast<int64_t>(cta) * 2 + (cta == p.first)) * 2 * kPromptSlotFloats;
+                        return slots + (static_cast<int64_t>(cta) * 2 + (cta == from)) * 2 * kPromptSlotFloats;
                     };
-                    float mm = -CUDART_INF_F;
-                    for (int x = p.first; x <= p.last; ++x)
-                        mm = fmaxf(mm, __ldcg(slot_of(x) + 128 * 128 + row));
+                    float mm = -CUDART_INF_F, ll = 0.0f;
+                    if (mine)
+                        for (int x = from; x <= upto; ++x) mm = fmaxf(mm, __ldcg(slot_of(x) + 128 * 128 + row));
                     const float safe = mm == -CUDART_INF_F ? 0.0f : mm;
-                    float ll = 0.0f;
-                    for (int x = p.first; x <= p.last; ++x)
-                        ll += exp2_approx(__ldcg(slot_of(x) + 128 * 128 + row) - safe) *
-                              __ldcg(slot_of(x) + 128 * 128 + 128 + row);
+                    if (mine)
+                        for (int x = from; x <= upto; ++x)
+                            ll += exp2_approx(__ldcg(slot_of(x) + 128 * 128 + row) - safe) *
+                                  __ldcg(slot_of(x) + 128 * 128 + 128 + row);
                     const float scale = ll == 0.0f ? 0.0f : v_scale / ll;
 #pragma unroll 1
                     for (int col = 0; col < D; col += 32) {
                         float v[32];
 #pragma unroll
                         for (int k = 0; k < 32; ++k) v[k] = 0.0f;
+                        if (mine) {
 #pragma unroll 1
-                        for (int x = p.first; x <= p.last; ++x) {
-                            const float* src = slot_of(x);
-                            const float w = exp2_approx(__ldcg(src + 128 * 128 + row) - safe);
+                            for (int x = from; x <= upto; ++x) {
+                                const float* src = slot_of(x);
+                                const float w = exp2_approx(__ldcg(src + 128 * 128 + row) - safe);
 #pragma unroll
-                            for (int k = 0; k < 32; k += 4) {
-                                const float4 y = __ldcg(reinterpret_cast<const float4*>(src + (col + k) * 128 + row * 4));
-                                v[k] += w * y.x;
-                                v[k + 1] += w * y.y;
-                                v[k + 2] += w * y.z;
-                                v[k + 3] += w * y.w;
+                                for (int k = 0; k < 32; k += 4) {
+                                    const float4 y = __ldcg(reinterpret_cast<const float4*>(src + (col + k) * 128 + row * 4));
+                                    v[k] += w * y.x;
+                                    v[k + 1] += w * y.y;
+                                    v[k + 2] += w * y.z;
+                                    v[k + 3] += w * y.w;
+                                }
                             }
                         }
                         put(col, v, scale);
@@ -686,121 +783,106 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     put_lse(mm, ll);
                 }
             }
-            p = nxt;
+            release_piece();
         }
-    } else if (warp == 8) {
-        // ------------------------------------------------------------ MMA issuer
-        uint32_t stage = 0, phase = 0;
-        uint32_t q_phase = 0, p_phase[2] = {0, 0}, oe_phase[2] = {0, 0}, blocks = 0;
+    } else if (warp == 8 || warp == 10) {
+        // ------------------------------------------------------------ MMAs of one tile
+        const int t = (warp - 8) >> 1;
+        const uint32_t ts = tmem_s(t), to = tmem_o(t);
+        const uint64_t dq = sdesc_k128(base + t * L::kTile);
+        uint32_t stage = 0, phase = 0, q_phase = 0, p_phase = 0, o_phase = 0, blocks = 0;
         bool ok = true;
-        for (Piece p = work.next(a); ok && p.valid;) {
-            const Piece nxt = work.next(a);
-            if (p.b1 > p.b0 || FP8) {
-                if (!(ok = wait(q_full(0), q_phase, 4) && wait(q_full(1), q_phase, 4))) break;
+        while (ok) {
+            const Piece* p = next_piece();
+            if (!p) break;
+            const int b0 = p->b0, b1 = p->b1, begin = p->begin(t), end = p->end(t), last_hi = p->last_hi[t];
+            const int item_hi = max(p->last_hi[0], p->last_hi[1]);
+            if (b1 > b0 || FP8) {
+                if (!(ok = wait(q_full(t), q_phase, 4))) break;
                 q_phase ^= 1u;
                 ptx::tc_fence_after();
             }
-            // K of block i and V of block i - 1 meet in step i: while one tile's softmax of
-            // block i - 1 runs, the other tile's two products of step i do.
-            for (int i = p.b0; ok && i <= p.b1; ++i) {
-                const bool has_k = i < p.b1, has_v = i > p.b0;
-                const uint32_t vs = stage, vph = phase;
-                uint32_t ks = stage, kph = phase;
-                if (has_v) {
-                    if (++ks == NST) {
-                        ks = 0;
-                        kph ^= 1u;
-                    }
-                }
-                const uint32_t sv = base + L::kStage0 + vs * L::kTile, sk = base + L::kStage0 + ks * L::kTile;
-                bool v_ready = false, k_ready = false;
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const bool pv = has_v && i - 1 >= p.lo[t] && i - 1 < p.hi[t];
-                    const bool qk = has_k && i >= p.lo[t] && i < p.hi[t];
-                    if (pv) {
-                        if (!v_ready) {
-                            if (!(ok = wait(full(vs), vph, 5))) break;
-                            v_ready = true;
-                            // Rows of V that no query of the item may see, in a group of 16 that
-                            // the product reads: past the item's last key or in a page that is
-                            // not there. Their weights are 0, but 0 times what they hold may be
-                            // NaN; they are cleared first.
-                            const int in = max(p.last_hi[0], p.last_hi[1]) - (i - 1) * kPB;
-                            const uint32_t have = groups[(blocks + i - 1 - p.b0) & 7];
-                            if (in < kPB || have != 0xFFu) {
-                                const int upto = min(kPB, (in + 15) & ~15);
-                                for (int r = have == 0xFFu ? in : 0; r < upto; ++r)
-                                    if (r >= in || !((have >> (r >> 4)) & 1u))
-                                        if (lane < D / 8)
-                                            *reinterpret_cast<uint4*>(base_ptr + (sv - base) + (lane >> 3) * kHalf +
-                                                                      r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
-                                fence_async_shared();
-                                __syncwarp();
-                            }
-                            ptx::tc_fence_after();
+            // K of block i and V of block i - 1 meet in step i: S of block i may overwrite P of
+            // block i - 1 once the product with it has been issued.
+            for (int i = b0; i <= b1; ++i) {
+                if (i > b0) {
+                    if (!(ok = wait(full(stage), phase, 5))) break;
+                    if (i > begin && i <= end) {
+                        // Rows of V that no query of the item may see, in a group of 16 that the
+                        // product reads: past the item's last key or in a page that is not
+                        // there. Their weights are 0, but 0 times what they hold may be NaN;
+                        // they are cleared first (by both tiles' warps alike).
+                        const uint32_t sv = L::kStage0 + stage * L::kTile;
+                        const int in = item_hi - (i - 1) * kPB;
+                        const uint32_t have = groups[(blocks + i - 1 - b0) & 7];
+                        if (in < kPB || have != 0xFFu) {
+                            const int upto = min(kPB, (in + 15) & ~15);
+                            for (int r = have == 0xFFu ? in : 0; r < upto; ++r)
+                                if ((r >= in || !((have >> (r >> 4)) & 1u)) && lane < D / 8)
+                                    *reinterpret_cast<uint4*>(base_ptr + sv + (lane >> 3) * kHalf + r * 128 +
+                                                              (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                            fence_async_shared();
+                            __syncwarp();
                         }
-                        const bool fresh = i - 1 == p.begin(t);
+                        const bool fresh = i - 1 == begin;
                         if (fresh) {  // the tile's result before this one has been read
-                            if (!(ok = wait(o_empty(t), oe_phase[t] ^ 1u, 6))) break;
-                            oe_phase[t] ^= 1u;
+                            if (!(ok = wait(o_empty(t), o_phase ^ 1u, 6))) break;
+                            o_phase ^= 1u;
                         }
-                        if (!(ok = wait(p_full(t), p_phase[t], 7))) break;
-                        p_phase[t] ^= 1u;
+                        if (!(ok = wait(p_full(t), p_phase, 7))) break;
+                        p_phase ^= 1u;
                         ptx::tc_fence_after();
-                        if (lane == 0) {
-                            const int steps = min(kPB, p.last_hi[t] - (i - 1) * kPB + 15) / 16;
-                            for (int k = 0; k < steps; ++k)
-                                mma_ts(tmem_o(t), tmem_s(t) + 8 * k, sdesc_v(sv) + 128 * k, kIdescO,
-                                       fresh && k == 0 ? 0u : 1u);
-                            if (i == p.end(t)) ptx::mma_commit(o_full(t));
-                        }
-                    }
-                    if (qk) {
-                        if (!k_ready) {
-                            if (!(ok = wait(full(ks), kph, 8))) break;
-                            k_ready = true;
-                            ptx::tc_fence_after();
-                        }
-                        if (lane == 0) {
+                        const int steps = min(kPB, last_hi - (i - 1) * kPB + 15) / 16;
+                        const uint64_t dv = sdesc_v(base + sv);
+                        if (elect_one()) {
+                            if (steps == kPB / 16) {
 #pragma unroll
-                            for (int k = 0; k < D / 16; ++k) {
-                                const uint32_t off = (k >> 2) * (kHalf >> 4) + 2 * (k & 3);
-                                ptx::mma_bf16_ss(tmem_s(t), sdesc_k128(base + t * L::kTile) + off,
-                                                 sdesc_k128(sk) + off, kIdescS, k ? 1u : 0u);
+                                for (int k = 0; k < kPB / 16; ++k)
+                                    mma_ts(to, ts + 8 * k, dv + 128 * k, kIdescO, k == 0 ? !fresh : 1u);
+                            } else {
+                                for (int k = 0; k < steps; ++k)
+                                    mma_ts(to, ts + 8 * k, dv + 128 * k, kIdescO, k == 0 ? !fresh : 1u);
                             }
-                            ptx::mma_commit(s_full(t));
+                            if (i == end) ptx::mma_commit(o_full(t));
                         }
+                        __syncwarp();
                     }
-                    __syncwarp();
-                }
-                if (!ok) break;
-                // stages whose block neither tile uses are passed over in the same order
-                if (has_v) {
-                    if (!v_ready && !(ok = wait(full(vs), vph, 5))) break;
-                    if (lane == 0) ptx::mma_commit(empty(vs));
-                    stage = ks;
-                    phase = kph;
-                }
-                if (has_k) {
-                    if (!k_ready && !(ok = wait(full(ks), kph, 8))) break;
-                    if (lane == 0) {
-                        ptx::mma_commit(empty(ks));
-                        if (i + 1 == p.b1) ptx::mma_commit(q_empty);  // the last use of Q
-                    }
+                    if (elect_one()) ptx::mma_commit(empty(stage));
                     if (++stage == NST) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
-                __syncwarp();
+                if (i < b1) {
+                    if (!(ok = wait(full(stage), phase, 8))) break;
+                    ptx::tc_fence_after();
+                    const uint64_t dk = sdesc_k128(base + L::kStage0 + stage * L::kTile);
+                    if (elect_one()) {
+                        if (i >= begin && i < end) {
+#pragma unroll
+                            for (int k = 0; k < D / 16; ++k) {
+                                const uint32_t off = (k >> 2) * (kHalf >> 4) + 2 * (k & 3);
+                                ptx::mma_bf16_ss(ts, dq + off, dk + off, kIdescS, k ? 1u : 0u);
+                            }
+                            ptx::mma_commit(s_full(t));
+                        }
+                        ptx::mma_commit(empty(stage));
+                        if (i + 1 == b1) ptx::mma_commit(q_empty);  // the last use of Q
+                    }
+                    __syncwarp();
+                    if (++stage == NST) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
             }
-            if (FP8 && p.b1 == p.b0 && lane == 0) ptx::mma_commit(q_empty);
-            __syncwarp();
-            blocks += p.b1 - p.b0;
-            p = nxt;
+            if (!ok) break;
+            if (FP8 && b1 == b0 && elect_one()) ptx::mma_commit(q_empty);
+            blocks += b1 - b0;
+            release_piece();
         }
-        if (lane == 0) {
+        __syncwarp();
+        if (elect_one()) {
             // every product has completed before tensor memory is released
             ptx::mma_commit(drain);
             ptx::mbar_wait_drain(drain, 0);
@@ -813,8 +895,12 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         uint32_t stage = 0, phase = 0, issued = 0, q_phase = 0, q_loads = 0, blocks = 0;
         constexpr int NR = FP8 ? NRAW : NST;
         bool ok = true;
-        for (Piece p = work.next(a); ok && p.valid;) {
-            if (!FP8 && p.b1 > p.b0) {
+        while (ok) {
+            const Piece* p = next_piece();
+            if (!p) break;
+            const int b0 = p->b0, b1 = p->b1, h = p->h, b = p->b;
+            const int top = max(p->last_hi[0], p->last_hi[1]);
+            if (!FP8 && b1 > b0) {
                 if (!(ok = wait(q_empty, q_phase ^ 1u, 9))) break;
                 q_phase ^= 1u;
                 if (lane == 0) {
@@ -822,35 +908,37 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     for (int t = 0; t < 2; ++t) {
                         ptx::mbar_arrive_expect_tx(q_full(t), static_cast<uint32_t>(a.tpt * a.G) * D * 2);
                         for (int x = 0; x < D / 64; ++x)
-                            ptx::tma_load_3d(base + t * L::kTile + x * kHalf, &tmQ, q_full(t), 64 * x, p.h * a.G,
-                                             p.seq.first + p.tok0 + t * a.tpt);
+                            ptx::tma_load_3d(base + t * L::kTile + x * kHalf, &tmQ, q_full(t), 64 * x, h * a.G,
+                                             p->seq.first + p->tok0 + t * a.tpt);
                     }
                 }
                 ++q_loads;
             }
-            const int top = max(p.last_hi[0], p.last_hi[1]);
-            for (int i = p.b0; ok && i < p.b1; ++i) {
+            for (int i = b0; ok && i < b1; ++i) {
                 const int key = i * kPB + lane * rows;
                 const bool in = lane < copies && key < top;
-                const int64_t page = in ? kv_page(a.kv, p.b, key) : -1;
+                const int64_t page = in ? kv_page(a.kv, b, key) : -1;
                 const uint32_t there = __ballot_sync(~0u, page >= 0);
                 // groups of 16 keys that are there; those past the item's keys count as such
-                uint32_t have = 0;
-                for (int x = 0; x < copies; ++x)
-                    if (((there >> x) & 1u) || i * kPB + x * rows >= top)
-                        have |= ((1u << (rows / 16)) - 1u) << (x * (rows / 16));
-                if (lane == 0) groups[(blocks + i - p.b0) & 7] = have;
+                uint32_t have = 0xFFu;
+                const uint32_t missing = __ballot_sync(~0u, in && page < 0);
+                if (missing) {
+                    for (int x = 0; x < copies; ++x)
+                        if ((missing >> x) & 1u) have &= ~(((1u << (rows / 16)) - 1u) << (x * (rows / 16)));
+                }
                 const int slot = key & ((1 << a.kv.page_shift) - 1);
                 for (int kv = 0; kv < 2; ++kv) {
                     const uint32_t bar_full = FP8 ? raw_full(stage) : full(stage);
                     if (!(ok = wait(FP8 ? raw_empty(stage) : empty(stage), phase ^ 1u, 10))) break;
-                    if (lane == 0)
+                    if (lane == 0) {
+                        if (kv == 0) groups[(blocks + i - b0) & 7] = have;
                         ptx::mbar_arrive_expect_tx(bar_full, static_cast<uint32_t>(__popc(there) * rows) * D * (FP8 ? 1 : 2));
+                    }
                     __syncwarp();
                     if (page >= 0) {
                         if constexpr (FP8) {
                             bulk_load(base + L::kRaw0 + stage * L::kRaw + lane * rows * D,
-                                      (kv ? a.kv.V : a.kv.K) + page * a.kv.page_bytes + p.h * a.kv.head_bytes +
+                                      (kv ? a.kv.V : a.kv.K) + page * a.kv.page_bytes + h * a.kv.head_bytes +
                                           static_cast<int64_t>(slot) * D,
                                       static_cast<uint32_t>(rows) * D, bar_full);
                         } else {
@@ -858,7 +946,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 #pragma unroll
                             for (int x = 0; x < D / 64; ++x)
                                 ptx::tma_load_3d(dst + x * kHalf, kv ? &tmV : &tmK, bar_full, 64 * x,
-                                                 (p.h << a.kv.page_shift) + slot, static_cast<int>(page));
+                                                 (h << a.kv.page_shift) + slot, static_cast<int>(page));
                         }
                     }
                     __syncwarp();
@@ -869,8 +957,9 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     }
                 }
             }
-            blocks += p.b1 - p.b0;
-            p = work.next(a);
+            if (!ok) break;
+            blocks += b1 - b0;
+            release_piece();
         }
         if (!ok && lane == 0) {
             // wait for the copies still in flight before the CTA may exit
@@ -882,55 +971,66 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 for (int t = 0; t < 2; ++t) ptx::mbar_wait_drain(q_full(t), (q_loads - 1) & 1u);
         }
         __syncwarp();
-    } else {
-        if constexpr (FP8) {
-            if (warp >= 12) {
-                // -------------------------------------------------------- e4m3 -> fp16
-                uint32_t rs = 0, rph = 0, stage = 0, phase = 0;
-                bool ok = true;
-                const int tid = (warp - 12) * 32 + lane;
-                for (Piece p = work.next(a); ok && p.valid; p = work.next(a)) {
-                    for (int n = 2 * (p.b1 - p.b0); ok && n > 0; --n) {
-                        if (!(ok = wait(raw_full(rs), rph, 11))) break;
-                        if (!(ok = wait(empty(stage), phase ^ 1u, 12))) break;
-                        const uint8_t* src = base_ptr + L::kRaw0 + rs * L::kRaw;
-                        uint8_t* dst = base_ptr + L::kStage0 + stage * L::kTile;
-                        constexpr int kPieces = kPB * D / 16 / 128;  // 16-byte pieces per thread
+    } else if (warp == 11) {
+        // ------------------------------------------------------------ work list
+        for (;; ++piece_at) {
+            const Piece p = work.next(a);
+            if (!wait(piece_empty(piece_at % kPieces), ((piece_at / kPieces) & 1u) ^ 1u, 16)) break;
+            if (lane == 0) {
+                *const_cast<Piece*>(piece_of(piece_at)) = p;
+                mbar_arrive(piece_full(piece_at % kPieces));
+            }
+            __syncwarp();
+            if (!p.valid) break;
+        }
+    } else if (FP8) {
+        // ------------------------------------------------------------ e4m3 -> fp16
+        uint32_t rs = 0, rph = 0, stage = 0, phase = 0;
+        bool ok = true;
+        const int tid = (warp - 12) * 32 + lane;
+        while (ok) {
+            const Piece* p = next_piece();
+            if (!p) break;
+            const int n = 2 * (p->b1 - p->b0);
+            release_piece();
+            for (int x0 = 0; x0 < n; ++x0) {
+                if (!(ok = wait(raw_full(rs), rph, 11))) break;
+                if (!(ok = wait(empty(stage), phase ^ 1u, 12))) break;
+                const uint8_t* src = base_ptr + L::kRaw0 + rs * L::kRaw;
+                uint8_t* dst = base_ptr + L::kStage0 + stage * L::kTile;
+                constexpr int kParts = kPB * D / 16 / 128;  // 16-byte parts per thread
 #pragma unroll 4
-                        for (int x = 0; x < kPieces; ++x) {
-                            const int piece = x * 128 + tid;
-                            const int r = piece / (D / 16), j = piece % (D / 16);
-                            const uint4 v = *reinterpret_cast<const uint4*>(src + piece * 16);
-                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                            uint32_t h[8];
+                for (int x = 0; x < kParts; ++x) {
+                    const int part = x * 128 + tid;
+                    const int r = part / (D / 16), j = part % (D / 16);
+                    const uint4 v = *reinterpret_cast<const uint4*>(src + part * 16);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t h[8];
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                h[2 * k] = e4m3x2_to_half2(w[k] & 0xFFFF);
-                                h[2 * k + 1] = e4m3x2_to_half2(w[k] >> 16);
-                            }
-                            // the two 16-byte chunks in an order that spreads a row's writes over
-                            // all banks
-                            uint8_t* const d = dst + (j >> 2) * kHalf + r * 128;
-                            const int c0 = 2 * (j & 3), swap = (j >> 2) & 1;
-                            const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-                            *reinterpret_cast<uint4*>(d + (((c0 + swap) ^ (r & 7)) << 4)) = swap ? hi : lo;
-                            *reinterpret_cast<uint4*>(d + (((c0 + 1 - swap) ^ (r & 7)) << 4)) = swap ? lo : hi;
-                        }
-                        fence_async_shared();
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(full(stage));
-                            mbar_arrive(raw_empty(rs));
-                        }
-                        if (++rs == NRAW) {
-                            rs = 0;
-                            rph ^= 1u;
-                        }
-                        if (++stage == NST) {
-                            stage = 0;
-                            phase ^= 1u;
-                        }
+                    for (int k = 0; k < 4; ++k) {
+                        h[2 * k] = e4m3x2_to_half2(w[k] & 0xFFFF);
+                        h[2 * k + 1] = e4m3x2_to_half2(w[k] >> 16);
                     }
+                    // the two 16-byte chunks in an order that spreads a row's writes over all banks
+                    uint8_t* const d = dst + (j >> 2) * kHalf + r * 128;
+                    const int c0 = 2 * (j & 3), swap = (j >> 2) & 1;
+                    const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+                    *reinterpret_cast<uint4*>(d + (((c0 + swap) ^ (r & 7)) << 4)) = swap ? hi : lo;
+                    *reinterpret_cast<uint4*>(d + (((c0 + 1 - swap) ^ (r & 7)) << 4)) = swap ? lo : hi;
+                }
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(full(stage));
+                    mbar_arrive(raw_empty(rs));
+                }
+                if (++rs == NRAW) {
+                    rs = 0;
+                    rph ^= 1u;
+                }
+                if (++stage == NST) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
         }
