@@ -255,6 +255,7 @@ int tpmlp_attn_create(tpmlp_ctx** out, int32_t Hq, int32_t Hkv, int32_t D, int32
     // two slots per CTA of either kernel (the prompt kernel's hold two tiles each)
     const size_t partial = std::max(ctas * 2 * tpmlp::kRowSlotFloats,
                                     static_cast<size_t>(c->num_sms) * 4 * tpmlp::kPromptSlotFloats);
+    const size_t counters = ctas + 2;  // a counter per CTA (prompt: per tile), the deal's two
     const size_t scales = static_cast<size_t>(Hkv) * 2;
     cudaError_t e;
     float* ones = new (std::nothrow) float[scales];
@@ -265,9 +266,9 @@ int tpmlp_attn_create(tpmlp_ctx** out, int32_t Hq, int32_t Hkv, int32_t D, int32
     std::fill(ones, ones + scales, 1.0f);
     if ((e = cudaMalloc(&c->kv_scale, scales * sizeof(float))) != cudaSuccess ||
         (e = cudaMalloc(&c->attn_partial, partial * sizeof(float))) != cudaSuccess ||
-        (e = cudaMalloc(&c->attn_count, ctas * sizeof(uint32_t))) != cudaSuccess ||
+        (e = cudaMalloc(&c->attn_count, counters * sizeof(uint32_t))) != cudaSuccess ||
         (e = cudaMalloc(&c->status, sizeof(int))) != cudaSuccess ||
-        (e = cudaMemset(c->attn_count, 0, ctas * sizeof(uint32_t))) != cudaSuccess ||
+        (e = cudaMemset(c->attn_count, 0, counters * sizeof(uint32_t))) != cudaSuccess ||
         (e = cudaMemset(c->status, 0, sizeof(int))) != cudaSuccess ||
         (e = cudaMemcpy(c->kv_scale, ones, scales * sizeof(float), cudaMemcpyHostToDevice)) != cudaSuccess) {
         delete[] ones;

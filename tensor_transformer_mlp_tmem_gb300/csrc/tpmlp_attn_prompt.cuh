@@ -2,8 +2,8 @@
 //
 // For one kv head, G query heads and TPT = floor(128 / G) consecutive tokens make a tile of up to
 // 128 rows (row = token * G + head of the group), so that grouped heads share each K and V tile.
-// A CTA works on an item of two tiles (2 TPT tokens of one kv head) and walks the item's keys in
-// blocks of 128:
+// A CTA works on an item of two tiles (2 TPT tokens of one kv head). K and V come in blocks of
+// 128 keys; the tiles step through them 64 keys at a time:
 //   S_t = Q_t K^T      tcgen05.mma, both operands in shared memory, S fp32 in tensor memory
 //   P_t = 2^(S c - m)  one thread per row, written back over S in 16 bits
 //   O_t += P_t V       tcgen05.mma, P from tensor memory, V from shared memory (keys are the
@@ -22,7 +22,8 @@
 
 namespace tpmlp {
 
-constexpr int kPB = 128;          // keys per block = rows per tile
+constexpr int kPB = 128;          // keys per block (a stage) = rows per tile
+constexpr int kSB = 64;           // keys per step: S has two buffers of 64 columns per tile
 constexpr int kPromptItems = 1024;  // items whose sizes a CTA tabulates
 constexpr int kCoarse = 512;        // entries of the table of sequences
 constexpr int kPromptCode = 0x2000;  // wait sites: kPromptCode | role
@@ -45,7 +46,7 @@ struct PromptArgs {
     float scale_log2;
     int32_t window;
     float* partial;   // [CTAs][2 pieces][2 tiles] slots
-    uint32_t* count;  // [CTAs][2 tiles], 0 between launches
+    uint32_t* count;  // [CTAs][2 tiles] arrivals, then items dealt and CTAs done; 0 between launches
 };
 
 template <int D, bool FP8>
@@ -57,7 +58,7 @@ struct PromptSmem {
     static constexpr uint32_t kStage0 = 2 * kTile;
     static constexpr uint32_t kRaw0 = kStage0 + kStages * kTile;
     static constexpr uint32_t kBars = kRaw0 + kRaws * kRaw;
-    static constexpr int kNumBars = 2 * kStages + 2 * kRaws + 24;
+    static constexpr int kNumBars = 2 * kStages + 2 * kRaws + 30;
     static constexpr uint32_t kStore0 = kBars + (8 * kNumBars + 64 + 4 * 96 + 127) / 128 * 128;
     static constexpr uint32_t kTables = kStore0 + 8 * 2048;  // 2 KB of output staging per softmax warp
     static constexpr uint32_t kTotal = 1024 + kTables + (kCoarse + 1) * 8 + (kPromptItems + 1) * 4 + 256;
@@ -185,22 +186,22 @@ struct Piece {
     int b;                 // sequence
     PromptSeq seq;
     int tokens[2];         // of each tile
-    int lo[2], hi[2];      // each tile's blocks
+    int lo[2], hi[2];      // each tile's steps
     int last_hi[2];        // end of the keys of each tile's last token
-    int b0, b1;
+    int b0, b1;            // blocks
     int first, last;       // contributing CTAs
     int starts;            // 1: the item's first blocks are in this piece
-    __device__ __forceinline__ int begin(int t) const { return max(lo[t], b0); }
-    __device__ __forceinline__ int end(int t) const { return min(hi[t], b1); }
+    __device__ __forceinline__ int begin(int t) const { return max(lo[t], 2 * b0); }
+    __device__ __forceinline__ int end(int t) const { return min(hi[t], 2 * b1); }
 };
 static_assert(sizeof(Piece) <= 96, "piece slots");
-constexpr int kPieces = 4;  // pieces between the work list's warp and the others
+constexpr int kPieces = 2;  // pieces between the work list's warp and the others: one ahead
 
 __device__ __forceinline__ int prompt_lo_key(const PromptArgs& a, int hi) {
     return a.window > 0 ? max(0, hi - a.window) : 0;
 }
 
-// The blocks of tokens [tok0, tok0 + 2 tpt) of a sequence.
+// The steps and blocks of tokens [tok0, tok0 + 2 tpt) of a sequence.
 __device__ __forceinline__ void item_blocks(const PromptArgs& a, Piece& p) {
     p.b0 = 0x7FFFFFFF;
     p.b1 = 0;
@@ -211,12 +212,12 @@ __device__ __forceinline__ void item_blocks(const PromptArgs& a, Piece& p) {
         p.lo[t] = p.hi[t] = p.last_hi[t] = 0;
         if (p.tokens[t] > 0) {
             p.last_hi[t] = p.seq.hi(k0 + p.tokens[t] - 1);
-            p.hi[t] = (p.last_hi[t] + kPB - 1) / kPB;
-            p.lo[t] = min(p.hi[t], prompt_lo_key(a, p.seq.hi(k0)) / kPB);
+            p.hi[t] = (p.last_hi[t] + kSB - 1) / kSB;
+            p.lo[t] = min(p.hi[t], prompt_lo_key(a, p.seq.hi(k0)) / kSB);
         }
         if (p.hi[t] > p.lo[t]) {
-            p.b0 = min(p.b0, p.lo[t]);
-            p.b1 = max(p.b1, p.hi[t]);
+            p.b0 = min(p.b0, p.lo[t] / 2);
+            p.b1 = max(p.b1, (p.hi[t] + 1) / 2);
         }
     }
     if (p.b1 == 0) p.b0 = 0;
@@ -231,8 +232,7 @@ struct PromptWork {
     int runs, run;          // entries of coarse, sequences per entry
     int64_t items;
     bool split;             // equal runs of blocks instead of whole items
-    int64_t at, end;        // whole: round, -; split: blocks
-    int64_t per;
+    int64_t at, end, per;   // split: this CTA's run of blocks, the length of every run
 
     __device__ __forceinline__ static int tiles(const PromptArgs& a, const PromptSeq& s) {
         return (s.n + 2 * a.tpt - 1) / (2 * a.tpt);
@@ -269,11 +269,12 @@ struct PromptWork {
         Piece p;
         p.valid = 0;
         if (!split) {
-            // rounds of items dealt in alternating direction
-            const int64_t g = gridDim.x, c = blockIdx.x;
-            const int64_t k = at * g + ((at & 1) ? g - 1 - c : c);
-            ++at;
-            if (at * g - g >= items || k >= items) return p;
+            // items are dealt to whichever CTA asks next (who computes an item does not change
+            // its result); one lane asks
+            uint32_t k = 0;
+            if ((threadIdx.x & 31) == 0) k = atomicAdd(a.count + 2 * gridDim.x, 1u);
+            k = __shfl_sync(~0u, k, 0);
+            if (k >= items) return p;
             item(a, k, p);
             p.valid = 1;
             p.first = p.last = 0;
@@ -310,7 +311,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PromptArgs a) {
     using L = PromptSmem<D, FP8>;
     constexpr int NST = L::kStages, NRAW = L::kRaws;
-    constexpr uint32_t kIdescS = prompt_idesc(kPB, FP8, false);
+    constexpr uint32_t kIdescS = prompt_idesc(kSB, FP8, false);
     constexpr uint32_t kIdescO = prompt_idesc(D, FP8, true);
     constexpr uint32_t kHalf = 16384;  // bytes of 64 columns x 128 rows
 
@@ -326,15 +327,16 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     const uint32_t more = bars + 8u * (2 * NST + 2 * NRAW);
     auto q_full = [&](int t) { return more + 8u * t; };
     const uint32_t q_empty = more + 16u;
-    auto s_full = [&](int t) { return more + 24u + 8u * t; };
-    auto p_full = [&](int t) { return more + 40u + 8u * t; };
-    auto o_full = [&](int t) { return more + 56u + 8u * t; };
-    auto o_empty = [&](int t) { return more + 72u + 8u * t; };
-    const uint32_t drain = more + 88u;
-    auto join_in = [&](int t) { return more + 96u + 8u * t; };
-    auto join_out = [&](int t) { return more + 112u + 8u * t; };
-    auto piece_full = [&](int s) { return more + 128u + 8u * s; };
-    auto piece_empty = [&](int s) { return more + 160u + 8u * s; };
+    const uint32_t drain = more + 24u;
+    auto o_full = [&](int t) { return more + 32u + 8u * t; };
+    auto o_empty = [&](int t) { return more + 48u + 8u * t; };
+    auto join_in = [&](int t) { return more + 64u + 8u * t; };
+    auto join_out = [&](int t) { return more + 80u + 8u * t; };
+    auto s_full = [&](int t, int buf) { return more + 96u + 16u * t + 8u * buf; };
+    auto p_full = [&](int t, int buf) { return more + 128u + 16u * t + 8u * buf; };
+    auto piece_full = [&](int s) { return more + 160u + 8u * s; };
+    auto piece_empty = [&](int s) { return more + 192u + 8u * s; };
+    auto pv_done = [&](int t) { return more + 224u + 8u * t; };
     uint32_t* const ctl = reinterpret_cast<uint32_t*>(base_ptr + L::kBars + 8 * L::kNumBars);
     volatile uint32_t* const abort_flag = ctl + 1;
     uint32_t* const s_last = ctl + 2;      // [2]
@@ -359,9 +361,12 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         }
         for (int t = 0; t < 2; ++t) {
             ptx::mbar_init(q_full(t), FP8 ? 4 : 1);
-            ptx::mbar_init(s_full(t), 1);
-            ptx::mbar_init(p_full(t), 4);
+            for (int buf = 0; buf < 2; ++buf) {
+                ptx::mbar_init(s_full(t, buf), 1);
+                ptx::mbar_init(p_full(t, buf), 4);
+            }
             ptx::mbar_init(o_full(t), 1);
+            ptx::mbar_init(pv_done(t), 1);
             ptx::mbar_init(o_empty(t), 4);
             ptx::mbar_init(join_in(t), 4);
             ptx::mbar_init(join_out(t), 1);
@@ -423,8 +428,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     __syncthreads();
     work.items = found[0];
     work.split = false;
-    work.at = 0;
-    work.end = 0;
+    work.at = work.end = 0;
     work.per = 1;
     if (work.items <= kPromptItems) {
         // Few items: tabulate their blocks, and split the blocks evenly where the longest item,
@@ -491,8 +495,8 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     };
 
     // The register split sums to what the block was launched with (384 x 168, 512 x 128).
-    if (warp < 8) regs_up<FP8 ? 192 : 216>();
-    else regs_down<FP8 ? 64 : 72>();
+    if (warp < 8) regs_up<FP8 ? 160 : 184>();
+    else regs_down<FP8 ? 96 : 136>();
 
     // The pieces, in the order that every role goes through them. next_piece() waits for one (null:
     // no more, or a wait gave up); release_piece() hands its slot back.
@@ -516,7 +520,8 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         const int t = warp >> 2;
         const int row = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        uint32_t s_phase = 0, o_phase = 0, q_phase = 0, j_phase = 0, blocks = 0;
+        uint32_t s_phase[2] = {0, 0}, o_phase = 0, q_phase = 0, j_phase = 0, blocks = 0;
+        uint32_t pv_count = 0;  // products P V of this tile so far
         const int token = row / a.G, head = row - token * a.G;
         while (const Piece* p = next_piece()) {
             const bool mine = token < p->tokens[t];
@@ -566,38 +571,40 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             const uint32_t block0 = blocks - p->b0;
             blocks += p->b1 - p->b0;
             bool ok = true;
-            for (int i = begin; i < end; ++i) {
-                if (!(ok = wait(s_full(t), s_phase, 2))) break;
-                s_phase ^= 1u;
+            for (int j = begin; j < end; ++j) {
+                const int buf = j & 1;
+                if (!(ok = wait(s_full(t, buf), buf ? s_phase[1] : s_phase[0], 2))) break;
+                if (buf) s_phase[1] ^= 1u;
+                else s_phase[0] ^= 1u;
                 ptx::tc_fence_after();
-                uint32_t s[128];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    ptx::tmem_ld_32x32b_x32(tmem_s(t) + lanes + 32 * j, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * j));
-#pragma unroll
-                for (int j = 0; j < 4; ++j) ptx::tmem_wait_ld(*reinterpret_cast<uint32_t(*)[32]>(s + 32 * j));
-                const int key0 = i * kPB;
-                const uint32_t have = groups[(block0 + i) & 7];
-                if (last_lo > key0 || have != 0xFFu) {
+                const uint32_t ts = tmem_s(t) + lanes + kSB * buf;
+                uint32_t s[kSB];
+                ptx::tmem_ld_32x32b_x32(ts, *reinterpret_cast<uint32_t(*)[32]>(s));
+                ptx::tmem_ld_32x32b_x32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+                ptx::tmem_wait_ld(*reinterpret_cast<uint32_t(*)[32]>(s));
+                ptx::tmem_wait_ld(*reinterpret_cast<uint32_t(*)[32]>(s + 32));
+                const int key0 = j * kSB;
+                const uint32_t have = (groups[(block0 + (j >> 1)) & 7] >> (4 * buf)) & 0xFu;
+                if (last_lo > key0 || have != 0xFu) {
                     const int below = hi - key0, from = lo - key0;
 #pragma unroll
-                    for (int k = 0; k < 128; ++k) {
+                    for (int k = 0; k < kSB; ++k) {
                         const bool on = k < below && k >= from && ((have >> (k >> 4)) & 1u);
                         s[k] = on ? s[k] : 0xFF800000u;
                     }
-                } else if (first_hi < key0 + kPB) {
+                } else if (first_hi < key0 + kSB) {
                     const int below = hi - key0;
 #pragma unroll
-                    for (int k = 0; k < 128; ++k) s[k] = k < below ? s[k] : 0xFF800000u;
+                    for (int k = 0; k < kSB; ++k) s[k] = k < below ? s[k] : 0xFF800000u;
                 }
                 float top[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    top[j] = __uint_as_float(s[j]);
+                for (int x = 0; x < 4; ++x) {
+                    top[x] = __uint_as_float(s[x]);
 #pragma unroll
-                    for (int k = 4; k < 124; k += 8)
-                        top[j] = max3(top[j], __uint_as_float(s[k + j]), __uint_as_float(s[k + 4 + j]));
-                    top[j] = fmaxf(top[j], __uint_as_float(s[124 + j]));
+                    for (int k = 4; k < kSB - 4; k += 8)
+                        top[x] = max3(top[x], __uint_as_float(s[k + x]), __uint_as_float(s[k + 4 + x]));
+                    top[x] = fmaxf(top[x], __uint_as_float(s[kSB - 4 + x]));
                 }
                 const float now = fmaxf(max3(top[0], top[1], top[2]), top[3]) * c;
                 float f = 1.0f;
@@ -606,42 +613,41 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     m = now;
                     l *= f;
                 }
-                // the reference moved: O of the blocks before is scaled. Its products are done:
-                // they were issued before this block's S, whose commit has arrived.
-                if (i > begin && __any_sync(~0u, f != 1.0f)) {
+                // the reference moved: O of the steps before is scaled, once the last of their
+                // products (of the other buffer) is done
+                if (j > begin && __any_sync(~0u, f != 1.0f)) {
+                    if (!(ok = wait(pv_done(t), (pv_count - 1) & 1u, 17))) break;
+                    ptx::tc_fence_after();
 #pragma unroll 1
-                    for (int j = 0; j < D; j += 32) {
+                    for (int x = 0; x < D; x += 32) {
                         uint32_t o[32];
-                        ptx::tmem_ld_32x32b_x32(tmem_o(t) + lanes + j, o);
+                        ptx::tmem_ld_32x32b_x32(tmem_o(t) + lanes + x, o);
                         ptx::tmem_wait_ld(o);
 #pragma unroll
                         for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                        tmem_st_x32(tmem_o(t) + lanes + j, o);
+                        tmem_st_x32(tmem_o(t) + lanes + x, o);
                     }
                 }
+                ++pv_count;
                 // P = 2^(S c - m), two values to an instruction where there is one
                 const float shift = (FP8 ? kRaiseLog2 : 0.0f) - (m == -CUDART_INF_F ? 0.0f : m);
                 const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
                 float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                uint32_t w[32];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t w[32];
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const int x = 64 * half + 2 * k;
-                        float2 e = fma2(make_float2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), c2, shift2);
-                        e.x = exp2_approx(e.x);
-                        e.y = exp2_approx(e.y);
-                        sum[k & 1] = add2(sum[k & 1], e);
-                        w[k] = FP8 ? pack_half2(e.x, e.y) : pack_bf162(e.x, e.y);
-                    }
-                    tmem_st_x32(tmem_s(t) + lanes + 32 * half, w);
+                for (int k = 0; k < 32; ++k) {
+                    float2 e = fma2(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), c2, shift2);
+                    e.x = exp2_approx(e.x);
+                    e.y = exp2_approx(e.y);
+                    sum[k & 1] = add2(sum[k & 1], e);
+                    w[k] = FP8 ? pack_half2(e.x, e.y) : pack_bf162(e.x, e.y);
                 }
+                tmem_st_x32(ts, w);
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 tmem_wait_st();
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full(t));
+                if (lane == 0) mbar_arrive(p_full(t, buf));
             }
             if (!ok) break;
             // -------------------------------------------------------- the tile's result
@@ -790,7 +796,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         const int t = (warp - 8) >> 1;
         const uint32_t ts = tmem_s(t), to = tmem_o(t);
         const uint64_t dq = sdesc_k128(base + t * L::kTile);
-        uint32_t stage = 0, phase = 0, q_phase = 0, p_phase = 0, o_phase = 0, blocks = 0;
+        uint32_t stage = 0, phase = 0, q_phase = 0, p_phase[2] = {0, 0}, o_phase = 0, blocks = 0;
         bool ok = true;
         while (ok) {
             const Piece* p = next_piece();
@@ -802,78 +808,91 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 q_phase ^= 1u;
                 ptx::tc_fence_after();
             }
-            // K of block i and V of block i - 1 meet in step i: S of block i may overwrite P of
-            // block i - 1 once the product with it has been issued.
+            // Round i: O += P V for the two steps of block i - 1, each followed by S of the step
+            // two later (block i), which may overwrite that P once its product has been issued.
+            // So a step's S is ready before the softmax of the step before it has ended.
             for (int i = b0; i <= b1; ++i) {
+                const uint32_t vs = stage, vph = phase;
+                uint32_t ks = vs, kph = vph;
+                if (i > b0 && ++ks == NST) {
+                    ks = 0;
+                    kph ^= 1u;
+                }
+                const uint32_t sv = L::kStage0 + vs * L::kTile;
+                const uint64_t dv = sdesc_v(base + sv), dk = sdesc_k128(base + L::kStage0 + ks * L::kTile);
                 if (i > b0) {
-                    if (!(ok = wait(full(stage), phase, 5))) break;
-                    if (i > begin && i <= end) {
-                        // Rows of V that no query of the item may see, in a group of 16 that the
-                        // product reads: past the item's last key or in a page that is not
-                        // there. Their weights are 0, but 0 times what they hold may be NaN;
-                        // they are cleared first (by both tiles' warps alike).
-                        const uint32_t sv = L::kStage0 + stage * L::kTile;
-                        const int in = item_hi - (i - 1) * kPB;
-                        const uint32_t have = groups[(blocks + i - 1 - b0) & 7];
-                        if (in < kPB || have != 0xFFu) {
-                            const int upto = min(kPB, (in + 15) & ~15);
-                            for (int r = have == 0xFFu ? in : 0; r < upto; ++r)
-                                if ((r >= in || !((have >> (r >> 4)) & 1u)) && lane < D / 8)
-                                    *reinterpret_cast<uint4*>(base_ptr + sv + (lane >> 3) * kHalf + r * 128 +
-                                                              (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
-                            fence_async_shared();
-                            __syncwarp();
-                        }
-                        const bool fresh = i - 1 == begin;
+                    if (!(ok = wait(full(vs), vph, 5))) break;
+                    // Rows of V that no query of the item may see, in a group of 16 that the
+                    // product reads: past the item's last key or in a page that is not there.
+                    // Their weights are 0, but 0 times what they hold may be NaN; they are
+                    // cleared first (by both tiles' warps alike).
+                    const int in = item_hi - (i - 1) * kPB;
+                    const uint32_t have = groups[(blocks + i - 1 - b0) & 7];
+                    if (in < kPB || have != 0xFFu) {
+                        const int upto = min(kPB, (in + 15) & ~15);
+                        for (int r = have == 0xFFu ? in : 0; r < upto; ++r)
+                            if ((r >= in || !((have >> (r >> 4)) & 1u)) && lane < D / 8)
+                                *reinterpret_cast<uint4*>(base_ptr + sv + (lane >> 3) * kHalf + r * 128 +
+                                                          (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        fence_async_shared();
+                        __syncwarp();
+                    }
+                }
+                if (i < b1) {
+                    if (!(ok = wait(full(ks), kph, 8))) break;
+                    ptx::tc_fence_after();
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int jv = 2 * (i - 1) + u, jk = 2 * i + u;
+                    if (jv >= begin && jv < end) {
+                        const bool fresh = jv == begin;
                         if (fresh) {  // the tile's result before this one has been read
                             if (!(ok = wait(o_empty(t), o_phase ^ 1u, 6))) break;
                             o_phase ^= 1u;
                         }
-                        if (!(ok = wait(p_full(t), p_phase, 7))) break;
-                        p_phase ^= 1u;
+                        if (!(ok = wait(p_full(t, u), p_phase[u], 7))) break;
+                        p_phase[u] ^= 1u;
                         ptx::tc_fence_after();
-                        const int steps = min(kPB, last_hi - (i - 1) * kPB + 15) / 16;
-                        const uint64_t dv = sdesc_v(base + sv);
+                        const int groups16 = min(kSB, last_hi - jv * kSB + 15) / 16;
                         if (elect_one()) {
-                            if (steps == kPB / 16) {
+                            if (groups16 == kSB / 16) {
 #pragma unroll
-                                for (int k = 0; k < kPB / 16; ++k)
-                                    mma_ts(to, ts + 8 * k, dv + 128 * k, kIdescO, k == 0 ? !fresh : 1u);
+                                for (int k = 0; k < kSB / 16; ++k)
+                                    mma_ts(to, ts + kSB * u + 8 * k, dv + 512 * u + 128 * k, kIdescO, k == 0 ? !fresh : 1u);
                             } else {
-                                for (int k = 0; k < steps; ++k)
-                                    mma_ts(to, ts + 8 * k, dv + 128 * k, kIdescO, k == 0 ? !fresh : 1u);
+                                for (int k = 0; k < groups16; ++k)
+                                    mma_ts(to, ts + kSB * u + 8 * k, dv + 512 * u + 128 * k, kIdescO, k == 0 ? !fresh : 1u);
                             }
-                            if (i == end) ptx::mma_commit(o_full(t));
+                            ptx::mma_commit(pv_done(t));
+                            if (jv + 1 == end) ptx::mma_commit(o_full(t));
                         }
                         __syncwarp();
                     }
-                    if (elect_one()) ptx::mma_commit(empty(stage));
-                    if (++stage == NST) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                }
-                if (i < b1) {
-                    if (!(ok = wait(full(stage), phase, 8))) break;
-                    ptx::tc_fence_after();
-                    const uint64_t dk = sdesc_k128(base + L::kStage0 + stage * L::kTile);
-                    if (elect_one()) {
-                        if (i >= begin && i < end) {
+                    if (jk >= begin && jk < end && i < b1) {
+                        if (elect_one()) {
 #pragma unroll
                             for (int k = 0; k < D / 16; ++k) {
                                 const uint32_t off = (k >> 2) * (kHalf >> 4) + 2 * (k & 3);
-                                ptx::mma_bf16_ss(ts, dq + off, dk + off, kIdescS, k ? 1u : 0u);
+                                ptx::mma_bf16_ss(ts + kSB * u, dq + off, dk + 512 * u + off, kIdescS, k ? 1u : 0u);
                             }
-                            ptx::mma_commit(s_full(t));
+                            ptx::mma_commit(s_full(t, u));
                         }
-                        ptx::mma_commit(empty(stage));
-                        if (i + 1 == b1) ptx::mma_commit(q_empty);  // the last use of Q
+                        __syncwarp();
                     }
-                    __syncwarp();
-                    if (++stage == NST) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                }
+                if (!ok) break;
+                if (elect_one()) {
+                    if (i > b0) ptx::mma_commit(empty(vs));
+                    if (i < b1) ptx::mma_commit(empty(ks));
+                    if (i + 1 == b1) ptx::mma_commit(q_empty);  // the last use of Q
+                }
+                __syncwarp();
+                stage = ks;
+                phase = kph;
+                if (i < b1 && ++stage == NST) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
             if (!ok) break;
@@ -982,6 +1001,14 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             }
             __syncwarp();
             if (!p.valid) break;
+        }
+        if (!work.split && lane == 0) {
+            // the last CTA to have asked in vain leaves the counters at 0 for the next launch
+            uint32_t* const done = a.count + 2 * gridDim.x + 1;
+            if (atomicAdd(done, 1u) == gridDim.x - 1) {
+                done[-1] = 0;
+                done[0] = 0;
+            }
         }
     } else if (FP8) {
         // ------------------------------------------------------------ e4m3 -> fp16
