@@ -523,12 +523,12 @@ TPMLP_API int tpmlp_attn_set_scales(tpmlp_ctx *ctx, const void *k_scale, const v
  */
 typedef struct tpmlp_kv {
     void *K, *V;               /* device pools, bf16 or e4m3 */
-    int64_t num_pages;         /* pages of each pool */
+    int64_t num_pages;         /* pages of each pool (below 2^31) */
     int64_t page_stride;       /* elements from page to page; 0: Hkv * page_size * D. The stride
                                   in bytes is a multiple of 16 */
     const int32_t *page_table; /* device int32 [B][table_pages] */
     int64_t table_stride;      /* elements from row to row of the table; 0: table_pages */
-    int32_t table_pages;       /* columns; table_pages * page_size < 2^31 */
+    int32_t table_pages;       /* columns; table_pages * page_size <= 2^31 - 2^16 */
     int32_t B;                 /* sequences */
     const int32_t *lens;       /* device int32 [B]: keys of each sequence (decode and prompt:
                                   with the new tokens'); above table_pages * page_size it counts

@@ -39,8 +39,9 @@ int check_kv(tpmlp_ctx* c, const tpmlp_kv* kv, bool lens) {
     if (kv->table_stride != 0 && kv->table_stride < kv->table_pages) return TPMLP_ERR_INVALID_ARG;
     const int64_t page = static_cast<int64_t>(c->heads_kv) * c->page_size * c->head_dim;
     if (kv->page_stride != 0 && kv->page_stride < page) return TPMLP_ERR_INVALID_ARG;
-    if (static_cast<int64_t>(kv->table_pages) * c->page_size > INT_MAX) {
-        c->last_error = "a sequence's table holds 2^31 keys or more";
+    // key numbers stay below 2^31 with a step of every kernel past the end
+    if (static_cast<int64_t>(kv->table_pages) * c->page_size > (int64_t(1) << 31) - (1 << 16)) {
+        c->last_error = "a sequence's table holds more than 2^31 - 2^16 keys";
         return TPMLP_ERR_UNSUPPORTED_SHAPE;
     }
     const int elem = is_e4m3(c) ? 1 : 2;
@@ -62,7 +63,7 @@ tpmlp::KvView view_of(const tpmlp_ctx* c, const tpmlp_kv* kv) {
     v.table_stride = kv->table_stride ? kv->table_stride : kv->table_pages;
     v.table_pages = kv->table_pages;
     while ((1 << v.page_shift) < c->page_size) ++v.page_shift;
-    v.num_pages = kv->num_pages;
+    v.num_pages = static_cast<int32_t>(kv->num_pages);
     v.lens = kv->lens;
     v.B = kv->B;
     v.Hkv = c->heads_kv;
@@ -100,27 +101,29 @@ int allow_smem(tpmlp_ctx* c, Kernel kern, uint32_t smem, std::atomic<uint64_t>& 
     return TPMLP_OK;
 }
 
-template <int D, bool FP8, int NT>
+template <int D, bool FP8, int NB>
 int launch_rows(tpmlp_ctx* c, const tpmlp::RowArgs& a, cudaStream_t s) {
-    using S = tpmlp::RowShape<D, FP8, NT>;
-    auto kern = tpmlp::attn_row_kernel<D, FP8, NT>;
+    using S = tpmlp::RowShape<D, FP8, NB>;
+    auto kern = tpmlp::attn_row_kernel<D, FP8, NB>;
     static std::atomic<uint64_t> done{0};
     if (int rc = allow_smem(c, kern, S::kSmem, done)) return rc;
-    const int grid = c->num_sms * (NT == 1 ? kRowCtasPerSm : 1);
+    const int grid = c->num_sms * kRowCtasPerSm;
     return launch(c, kern, grid, tpmlp::kRowThreads, S::kSmem, s, a);
 }
 
+template <int D, bool FP8>
+int run_rows_of(tpmlp_ctx* c, tpmlp::RowArgs& a, cudaStream_t s) {
+    // blocks of 8 query heads of a kv head that a CTA's warps share out; more than four in turns
+    const int blocks = (a.G + 7) / 8;
+    a.blocks_per_head = (blocks + 3) / 4;
+    if (blocks == 1) return launch_rows<D, FP8, 1>(c, a, s);
+    if (blocks == 2) return launch_rows<D, FP8, 2>(c, a, s);
+    return launch_rows<D, FP8, 4>(c, a, s);
+}
+
 int run_rows(tpmlp_ctx* c, tpmlp::RowArgs& a, cudaStream_t s) {
-    const bool wide = a.G > 8;
-    a.blocks_per_head = (a.G + 15) / 16;
-    if (c->head_dim == 128) {
-        if (is_e4m3(c))
-            return wide ? launch_rows<128, true, 2>(c, a, s) : launch_rows<128, true, 1>(c, a, s);
-        return wide ? launch_rows<128, false, 2>(c, a, s) : launch_rows<128, false, 1>(c, a, s);
-    }
-    if (is_e4m3(c))
-        return wide ? launch_rows<64, true, 2>(c, a, s) : launch_rows<64, true, 1>(c, a, s);
-    return wide ? launch_rows<64, false, 2>(c, a, s) : launch_rows<64, false, 1>(c, a, s);
+    if (c->head_dim == 128) return is_e4m3(c) ? run_rows_of<128, true>(c, a, s) : run_rows_of<128, false>(c, a, s);
+    return is_e4m3(c) ? run_rows_of<64, true>(c, a, s) : run_rows_of<64, false>(c, a, s);
 }
 
 template <int D, bool FP8>

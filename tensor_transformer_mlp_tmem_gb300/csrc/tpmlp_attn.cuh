@@ -25,7 +25,7 @@ struct KvView {
     int64_t table_stride;
     int32_t table_pages;
     int32_t page_shift;   // log2 of the keys per page
-    int64_t num_pages;
+    int32_t num_pages;
     const int32_t* lens;
     int32_t B;
     int32_t Hkv;
@@ -50,8 +50,8 @@ __device__ __forceinline__ int kv_length(const KvView& kv, int b) {
 
 // The page that holds key `key` (inside the table) of sequence b; -1, reported, if the table
 // names none of the pool's.
-__device__ __forceinline__ int64_t kv_page(const KvView& kv, int b, int key) {
-    const int64_t p = kv.table[b * kv.table_stride + (key >> kv.page_shift)];
+__device__ __forceinline__ int kv_page(const KvView& kv, int b, int key) {
+    const int p = kv.table[b * kv.table_stride + (key >> kv.page_shift)];
     if (p >= 0 && p < kv.num_pages) return p;
     report_bad_page(kv.status);
     return -1;
@@ -113,8 +113,8 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float (&f)[8], float scale) {
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendArgs a) {
     __shared__ float2 trig[D / 2];
-    ptx::griddep_launch_dependents();
     ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
     const int64_t t = blockIdx.x;
     const int pos = a.pos[t];
     if (pos < 0) return;
@@ -212,8 +212,8 @@ struct RowArgs {
 
 constexpr int kRowWarps = 8;
 constexpr int kRowThreads = 32 * kRowWarps;
-// fp32 values of a partial sum: O [16][128], m [16], l [16].
-constexpr int kRowSlotFloats = 16 * 128 + 32;
+// fp32 values of a partial sum: O [32][128], m [32], l [32].
+constexpr int kRowSlotFloats = 32 * 128 + 64;
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1, bool half) {
@@ -264,6 +264,10 @@ __device__ __forceinline__ float exp2_approx(float x) {
 __device__ __forceinline__ uint4 load16(const uint8_t* p) {
     return __ldcg(reinterpret_cast<const uint4*>(p));
 }
+template <bool L1>
+__device__ __forceinline__ uint4 load_kv16(const uint8_t* p) {
+    return L1 ? __ldca(reinterpret_cast<const uint4*>(p)) : __ldcg(reinterpret_cast<const uint4*>(p));
+}
 
 // Keys of a row: [lo, hi) of its sequence.
 struct RowRange {
@@ -276,24 +280,28 @@ __device__ __forceinline__ RowRange row_range(const RowArgs& a, int b) {
     return x;
 }
 
-// The kernel's shape. A warp takes KT keys at a time and holds all their K and V in registers
-// (8 KB of cache per warp and iteration): K rows are the A operand of S^T = K Q^T (16 keys x 8
-// query heads a matrix instruction), so the loads are whole 16-byte pieces of the rows as they
-// lie in memory, in an order of the reduction index that Q's registers share; V is the A operand
-// of O^T = V^T P^T, its pairs of keys put together with byte permutes. No shared memory, no
-// barriers and no copies are needed on the way: the bound is DRAM.
-template <int D, bool FP8, int NT>
+// The kernel's shape. A warp takes KT keys at a time and holds all their K and V in registers (8 KB
+// of cache per warp and iteration): K rows are the A operand of S^T = K Q^T (16 keys x 8 query
+// heads a matrix instruction), so the loads are whole 16-byte pieces of the rows as they lie in
+// memory, in an order of the reduction index that Q's registers share; V is the A operand of
+// O^T = V^T P^T, its pairs of keys put together with byte permutes. No shared memory, no barriers
+// and no copies are needed on the way: 16 warps an SM keep 128 KB of loads in flight, and the
+// bound is DRAM. NB warps take the same keys for NB blocks of 8 query heads; all but the first
+// find them in L1.
+template <int D, bool FP8, int NB>
 struct RowShape {
     static constexpr int kElem = FP8 ? 1 : 2;
     static constexpr int kSub = 256 / (D * kElem);   // subtiles of 16 keys
     static constexpr int KT = 16 * kSub;
-    static constexpr int kStep = KT * kRowWarps;     // keys of a CTA's step
-    static constexpr int kRows = 8 * NT;             // query heads of a block
+    static constexpr int kParts = kRowWarps / NB;    // warps that share out the keys
+    static constexpr int kStep = KT * kParts;        // keys of a CTA's step
+    static constexpr int kRows = 8 * NB;             // query heads of a CTA
     static constexpr int NK = D * kElem / 64;        // 16-byte pieces of a K row per thread
     static constexpr int NV = D / 8;                 // V dimensions per thread
+    static constexpr int kVPieces = NV * kElem >= 16 ? NV * kElem / 16 : 1;  // 16-byte pieces of a V row
     static constexpr int kQRegs = D / 8;             // Q registers per 8 query heads
     static constexpr int kPitch = D + 4;             // fp32 row of the merge buffer
-    static constexpr int kSmem = kRowWarps * kRows * (kPitch + 2) * 4;
+    static constexpr int kSmem = kRowWarps * 8 * (kPitch + 2) * 4;
 };
 
 // The dimension that element e of lane group g's V registers stands for.
@@ -303,22 +311,24 @@ __device__ __forceinline__ int v_dim(int g, int e) {
     else return (D / 8) * g + e;
 }
 
-template <int D, bool FP8, int NT>
-__global__ void __launch_bounds__(kRowThreads, NT == 1 ? 2 : 1)
+template <int D, bool FP8, int NB>
+__global__ void __launch_bounds__(kRowThreads, 2)
 attn_row_kernel(const __grid_constant__ RowArgs a) {
-    using S = RowShape<D, FP8, NT>;
+    using S = RowShape<D, FP8, NB>;
+    constexpr int NT = 1;
     extern __shared__ float smem[];
-    float* const sO = smem;                                       // [warps][rows][pitch]
-    float* const sM = sO + kRowWarps * S::kRows * S::kPitch;      // [warps][rows]
-    float* const sL = sM + kRowWarps * S::kRows;                  // [warps][rows]
+    float* const sO = smem;                                       // [parts][rows][pitch]
+    float* const sM = sO + S::kParts * S::kRows * S::kPitch;      // [parts][rows]
+    float* const sL = sM + S::kParts * S::kRows;                  // [parts][rows]
     __shared__ int64_t s_scan[kRowWarps + 1];
     __shared__ int64_t s_found[2];
     __shared__ uint32_t s_last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
+    const int part_of = warp / NB, block = warp % NB;  // the warp's share of the keys, its 8 query heads
 
-    ptx::griddep_launch_dependents();
     ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
 
     auto steps_of = [&](const RowRange& x) {
         return max(1, (x.hi - (x.lo & ~15) + S::kStep - 1) / S::kStep);
@@ -395,7 +405,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         float c_log2[NT][2];  // score -> log2 units, for the lane's query columns 2 t, 2 t + 1
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int qi = nt * 8 + g;
+            const int qi = block * 8 + g;
             const __nv_bfloat16* src =
                 a.q + row * a.ldq + (static_cast<int64_t>(h) * a.G + q0 + qi) * D;
             const bool on = qi < valid;
@@ -458,7 +468,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         const int64_t head_off = h * a.kv.head_bytes;
         const int lo16 = range.lo & ~15;
         for (int it = 0; it < n; ++it) {
-            const int key0 = lo16 + ((step0 + it) * kRowWarps + warp) * S::KT;
+            const int key0 = lo16 + ((step0 + it) * S::kParts + part_of) * S::KT;
             if (key0 >= range.hi) break;  // the warp's keys only grow
             uint4 kr[S::kSub][2][S::NK];
             uint4 vr[S::kSub][4][S::NV * S::kElem >= 16 ? S::NV * S::kElem / 16 : 1];
@@ -479,7 +489,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
                     const bool on = ok[u] && key >= range.lo && key < range.hi;
 #pragma unroll
                     for (int j = 0; j < S::NK; ++j)
-                        kr[u][rr][j] = on ? load16(kp + (g + 8 * rr) * (D * S::kElem) + 16 * (t + 4 * j))
+                        kr[u][rr][j] = on ? load_kv16<(NB > 1)>(kp + (g + 8 * rr) * (D * S::kElem) + 16 * (t + 4 * j))
                                           : make_uint4(0, 0, 0, 0);
                 }
 #pragma unroll
@@ -489,10 +499,10 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
                     const bool on = ok[u] && key >= range.lo && key < range.hi;
                     const uint8_t* src = vp + kk * (D * S::kElem);
                     if constexpr (S::NV * S::kElem == 32) {
-                        vr[u][x][0] = on ? load16(src + 16 * g) : make_uint4(0, 0, 0, 0);
-                        vr[u][x][1] = on ? load16(src + 128 + 16 * g) : make_uint4(0, 0, 0, 0);
+                        vr[u][x][0] = on ? load_kv16<(NB > 1)>(src + 16 * g) : make_uint4(0, 0, 0, 0);
+                        vr[u][x][1] = on ? load_kv16<(NB > 1)>(src + 128 + 16 * g) : make_uint4(0, 0, 0, 0);
                     } else if constexpr (S::NV * S::kElem == 16) {
-                        vr[u][x][0] = on ? load16(src + 16 * g) : make_uint4(0, 0, 0, 0);
+                        vr[u][x][0] = on ? load_kv16<(NB > 1)>(src + 16 * g) : make_uint4(0, 0, 0, 0);
                     } else {
                         const uint2 v = on ? __ldcg(reinterpret_cast<const uint2*>(src + 8 * g))
                                            : make_uint2(0, 0);
@@ -580,29 +590,32 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
                     pb[nt][0] = transpose_8x8(FP8 ? pack_half2(p[0], p[1]) : pack_bf162(p[0], p[1]));
                     pb[nt][1] = transpose_8x8(FP8 ? pack_half2(p[2], p[3]) : pack_bf162(p[2], p[3]));
                 }
+                // word w of key x's dimensions
+                auto word = [&](int x, int w) {
+                    const uint4& y = vr[u][x][w >> 2];
+                    return (w & 3) == 0 ? y.x : (w & 3) == 1 ? y.y : (w & 3) == 2 ? y.z : y.w;
+                };
 #pragma unroll
-                for (int i = 0; i < S::NV / 2; ++i) {
-                    uint32_t av[4];
+                for (int i = 0; i < S::NV / 2; i += 2) {
+                    // fragments of two instructions: dimensions i, i + 1 and those NV/2 further on
+                    uint32_t av[2][4];
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        // rows e = i, i + NV/2 (x & 1); keys 2t, 2t+1 or 2t+8, 2t+9 (x >> 1)
+                        // rows e, keys 2t, 2t+1 or 2t+8, 2t+9 (x >> 1)
                         const int e = i + (x & 1) * (S::NV / 2), ka = 2 * (x >> 1);
-                        auto word = [&](int key, int w) {
-                            const uint4& v = vr[u][key][w >> 2];
-                            return (w & 3) == 0 ? v.x : (w & 3) == 1 ? v.y : (w & 3) == 2 ? v.z : v.w;
-                        };
                         if constexpr (!FP8) {
-                            const int w = e >> 1;
-                            av[x] = __byte_perm(word(ka, w), word(ka + 1, w), (e & 1) ? 0x7632 : 0x5410);
+                            av[0][x] = __byte_perm(word(ka, e >> 1), word(ka + 1, e >> 1), 0x5410);
+                            av[1][x] = __byte_perm(word(ka, e >> 1), word(ka + 1, e >> 1), 0x7632);
                         } else {
-                            const int w = e >> 2, k = e & 3;
-                            av[x] = e4m3x2_to_half2(
-                                __byte_perm(word(ka, w), word(ka + 1, w), (k + 4) * 16 + k) & 0xFFFF);
+                            const uint32_t both =
+                                __byte_perm(word(ka, e >> 2), word(ka + 1, e >> 2), (e & 2) ? 0x7362 : 0x5140);
+                            av[0][x] = e4m3x2_to_half2(both & 0xFFFF);
+                            av[1][x] = e4m3x2_to_half2(both >> 16);
                         }
                     }
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma_16816(o[nt][i], av[0], av[1], av[2], av[3], pb[nt][0], pb[nt][1], FP8);
+                    for (int y = 0; y < 2; ++y)
+                        mma_16816(o[0][i + y], av[y][0], av[y][1], av[y][2], av[y][3], pb[0][0], pb[0][1], FP8);
                 }
             }
         }
@@ -624,15 +637,15 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int r = nt * 8 + 2 * t + i;
-                    sM[warp * S::kRows + r] = m[nt][i];
-                    sL[warp * S::kRows + r] = l[nt][i];
+                    const int r = block * 8 + 2 * t + i;
+                    sM[part_of * S::kRows + r] = m[nt][i];
+                    sL[part_of * S::kRows + r] = l[nt][i];
                 }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                float* dst = sO + (warp * S::kRows + nt * 8 + 2 * t + i) * S::kPitch;
+                float* dst = sO + (part_of * S::kRows + block * 8 + 2 * t + i) * S::kPitch;
 #pragma unroll
                 for (int e = 0; e < S::NV; e += 4) {
                     const int k = e % (S::NV / 2), hi = e >= S::NV / 2 ? 2 : 0;
@@ -666,12 +679,12 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
             const int r = i / (D / 4), d = (i % (D / 4)) * 4;
             float mm = -CUDART_INF_F;
 #pragma unroll
-            for (int w = 0; w < kRowWarps; ++w) mm = fmaxf(mm, sM[w * S::kRows + r]);
+            for (int w = 0; w < S::kParts; ++w) mm = fmaxf(mm, sM[w * S::kRows + r]);
             const float safe = mm == -CUDART_INF_F ? 0.0f : mm;
             float ll = 0.0f;
             float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-            for (int w = 0; w < kRowWarps; ++w) {
+            for (int w = 0; w < S::kParts; ++w) {
                 const float f = exp2_approx(sM[w * S::kRows + r] - safe);
                 const float4 x = *reinterpret_cast<const float4*>(sO + (w * S::kRows + r) * S::kPitch + d);
                 ll += f * sL[w * S::kRows + r];
@@ -685,8 +698,8 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
             } else {
                 __stcg(reinterpret_cast<float4*>(slot + r * D + d), v);
                 if (d == 0) {
-                    __stcg(slot + 16 * 128 + r, mm);
-                    __stcg(slot + 16 * 128 + 16 + r, ll);
+                    __stcg(slot + 32 * 128 + r, mm);
+                    __stcg(slot + 32 * 128 + 32 + r, ll);
                 }
             }
         }
@@ -705,16 +718,16 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
                     float mm = -CUDART_INF_F;
                     for (int c = first; c <= last; ++c)
                         mm = fmaxf(mm, __ldcg(a.partial + (static_cast<int64_t>(c) * 2 + (c == first)) * kRowSlotFloats +
-                                              16 * 128 + r));
+                                              32 * 128 + r));
                     const float safe = mm == -CUDART_INF_F ? 0.0f : mm;
                     float ll = 0.0f;
                     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
                     for (int c = first; c <= last; ++c) {
                         const float* p = a.partial + (static_cast<int64_t>(c) * 2 + (c == first)) * kRowSlotFloats;
-                        const float f = exp2_approx(__ldcg(p + 16 * 128 + r) - safe);
+                        const float f = exp2_approx(__ldcg(p + 32 * 128 + r) - safe);
                         const float4 x = __ldcg(reinterpret_cast<const float4*>(p + r * D + d));
-                        ll += f * __ldcg(p + 16 * 128 + 16 + r);
+                        ll += f * __ldcg(p + 32 * 128 + 32 + r);
                         v.x += f * x.x;
                         v.y += f * x.y;
                         v.z += f * x.z;

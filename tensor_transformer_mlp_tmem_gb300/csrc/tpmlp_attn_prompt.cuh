@@ -389,8 +389,8 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         ptx::tmem_alloc(ptx::smem_addr(ctl), 512);
         ptx::tmem_relinquish();
     }
-    ptx::griddep_launch_dependents();
     ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
 
     // ---------------------------------------------------------------- the work list
     PromptWork work;
