@@ -212,23 +212,25 @@ struct RowArgs {
 
 constexpr int kRowWarps = 8;
 constexpr int kRowThreads = 32 * kRowWarps;
+// e4m3 caches: fp16 weights are raised by 2^10, so that the small ones of a long cache stay clear of
+// fp16's smallest steps; it cancels against the sum.
+constexpr float kRowRaise = 10.0f;
 // fp32 values of a partial sum: O [32][128], m [32], l [32].
 constexpr int kRowSlotFloats = 32 * 128 + 64;
 
-__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                          uint32_t a3, uint32_t b0, uint32_t b1, bool half) {
-    if (half)
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-            "{%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    else
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-            "{%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+__device__ __forceinline__ void mma_16816_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                               uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_16816_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // Transpose of an 8 x 8 matrix of 16-bit values spread over the warp (lane 4 r + c holds row r,
@@ -239,9 +241,15 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
     return r;
 }
 
-__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t v) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v), __NV_E4M3);
-    return static_cast<uint32_t>(h.x) | static_cast<uint32_t>(h.y) << 16;
+// Four e4m3 values as two pairs of fp16 (exact). The halves of the register are named, not
+// masked and shifted out: that would cost as much again as the conversions.
+__device__ __forceinline__ void e4m3x4_to_half2(uint32_t v, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(v));
 }
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
@@ -287,7 +295,8 @@ __device__ __forceinline__ RowRange row_range(const RowArgs& a, int b) {
 // O^T = V^T P^T, its pairs of keys put together with byte permutes. No shared memory, no barriers
 // and no copies are needed on the way: 16 warps an SM keep 128 KB of loads in flight, and the
 // bound is DRAM. NB warps take the same keys for NB blocks of 8 query heads; all but the first
-// find them in L1.
+// find them in L1. e4m3 values are converted to fp16 in registers (the 8-bit forms of these matrix
+// instructions take three times as long as the fp16 ones on this GPU).
 template <int D, bool FP8, int NB>
 struct RowShape {
     static constexpr int kElem = FP8 ? 1 : 2;
@@ -299,7 +308,7 @@ struct RowShape {
     static constexpr int NK = D * kElem / 64;        // 16-byte pieces of a K row per thread
     static constexpr int NV = D / 8;                 // V dimensions per thread
     static constexpr int kVPieces = NV * kElem >= 16 ? NV * kElem / 16 : 1;  // 16-byte pieces of a V row
-    static constexpr int kQRegs = D / 8;             // Q registers per 8 query heads
+    static constexpr int kQRegs = D / 8;             // Q registers of 8 query heads
     static constexpr int kPitch = D + 4;             // fp32 row of the merge buffer
     static constexpr int kSmem = kRowWarps * 8 * (kPitch + 2) * 4;
 };
@@ -315,7 +324,6 @@ template <int D, bool FP8, int NB>
 __global__ void __launch_bounds__(kRowThreads, 2)
 attn_row_kernel(const __grid_constant__ RowArgs a) {
     using S = RowShape<D, FP8, NB>;
-    constexpr int NT = 1;
     extern __shared__ float smem[];
     float* const sO = smem;                                       // [parts][rows][pitch]
     float* const sM = sO + S::kParts * S::kRows * S::kPitch;      // [parts][rows]
@@ -398,28 +406,26 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         const int q0 = (part % a.blocks_per_head) * S::kRows;  // first query head of the block
         const int valid = min(a.G - q0, S::kRows);
 
-        // Q: the reduction order of the K pieces. In the 8-bit cache's fp16 products each row is
+        // Q in the reduction order of the K pieces. In the 8-bit cache's fp16 products each row is
         // scaled by a power of two to a largest magnitude in [1, 2), so that no bf16 value
         // overflows; the scores are scaled back.
-        uint32_t qr[NT][S::kQRegs];
-        float c_log2[NT][2];  // score -> log2 units, for the lane's query columns 2 t, 2 t + 1
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        uint32_t qr[S::kQRegs];
+        float c_log2[2];  // score -> log2 units, for the lane's query columns 2 t, 2 t + 1
+        {
             const int qi = block * 8 + g;
-            const __nv_bfloat16* src =
-                a.q + row * a.ldq + (static_cast<int64_t>(h) * a.G + q0 + qi) * D;
+            const __nv_bfloat16* src = a.q + row * a.ldq + (static_cast<int64_t>(h) * a.G + q0 + qi) * D;
             const bool on = qi < valid;
             if constexpr (!FP8) {
 #pragma unroll
                 for (int j = 0; j < S::NK; ++j) {
                     const uint4 v = on ? load16(reinterpret_cast<const uint8_t*>(src + 8 * (t + 4 * j)))
                                        : make_uint4(0, 0, 0, 0);
-                    qr[nt][4 * j] = v.x;
-                    qr[nt][4 * j + 1] = v.y;
-                    qr[nt][4 * j + 2] = v.z;
-                    qr[nt][4 * j + 3] = v.w;
+                    qr[4 * j] = v.x;
+                    qr[4 * j + 1] = v.y;
+                    qr[4 * j + 2] = v.z;
+                    qr[4 * j + 3] = v.w;
                 }
-                c_log2[nt][0] = c_log2[nt][1] = a.scale_log2;
+                c_log2[0] = c_log2[1] = a.scale_log2;
             } else {
                 float x[S::NK][2][8];
                 float big = 0.0f;
@@ -427,17 +433,16 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
                 for (int j = 0; j < S::NK; ++j)
 #pragma unroll
                     for (int p = 0; p < 2; ++p) {
-                        const uint4 v =
-                            on ? load16(reinterpret_cast<const uint8_t*>(src + 16 * (t + 4 * j) + 8 * p))
-                               : make_uint4(0, 0, 0, 0);
+                        const uint4 v = on ? load16(reinterpret_cast<const uint8_t*>(src + 16 * (t + 4 * j) + 8 * p))
+                                           : make_uint4(0, 0, 0, 0);
                         unpack8(v, x[j][p]);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(x[j][p][i]));
                     }
                 big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
                 big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
-                // exponent of the row's largest magnitude (rows of zeros, infinities and the
-                // ends of the exponent range stay as they are)
+                // exponent of the row's largest magnitude (rows of zeros, infinities and the ends of
+                // the exponent range stay as they are)
                 int e = static_cast<int>(__float_as_uint(big) >> 23) - 127;
                 if (e < -100 || e > 100) e = 0;
                 const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
@@ -446,24 +451,19 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
                 for (int j = 0; j < S::NK; ++j)
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        qr[nt][8 * j + i] = pack_half2(x[j][i >> 2][2 * (i & 3)] * down,
-                                                       x[j][i >> 2][2 * (i & 3) + 1] * down);
+                        qr[8 * j + i] = pack_half2(x[j][i >> 2][2 * (i & 3)] * down, x[j][i >> 2][2 * (i & 3) + 1] * down);
                 const float ks = a.scale_log2 * a.kv.scales[h];
-                c_log2[nt][0] = ks * __shfl_sync(~0u, up, 8 * t);
-                c_log2[nt][1] = ks * __shfl_sync(~0u, up, 8 * t + 4);
+                c_log2[0] = ks * __shfl_sync(~0u, up, 8 * t);
+                c_log2[1] = ks * __shfl_sync(~0u, up, 8 * t + 4);
             }
         }
 
-        float o[NT][S::NV / 2][4];  // O^T: (dim e, q 2t), (dim e, q 2t+1), (dim e + NV/2, ...)
-        float m[NT][2], l[NT][2];
+        float o[S::NV / 2][4];  // O^T: (dim e, q 2t), (dim e, q 2t+1), (dim e + NV/2, ...)
+        float m[2], l[2];
+        m[0] = m[1] = -CUDART_INF_F;
+        l[0] = l[1] = 0.0f;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            m[nt][0] = m[nt][1] = -CUDART_INF_F;
-            l[nt][0] = l[nt][1] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < S::NV / 2; ++i)
-                o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.0f;
-        }
+        for (int i = 0; i < S::NV / 2; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
 
         const int64_t head_off = h * a.kv.head_bytes;
         const int lo16 = range.lo & ~15;
@@ -471,7 +471,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
             const int key0 = lo16 + ((step0 + it) * S::kParts + part_of) * S::KT;
             if (key0 >= range.hi) break;  // the warp's keys only grow
             uint4 kr[S::kSub][2][S::NK];
-            uint4 vr[S::kSub][4][S::NV * S::kElem >= 16 ? S::NV * S::kElem / 16 : 1];
+            uint4 vr[S::kSub][4][S::kVPieces];
             bool ok[S::kSub];
 #pragma unroll
             for (int u = 0; u < S::kSub; ++u) {
@@ -498,162 +498,150 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
                     const int key = kb + kk;
                     const bool on = ok[u] && key >= range.lo && key < range.hi;
                     const uint8_t* src = vp + kk * (D * S::kElem);
-                    if constexpr (S::NV * S::kElem == 32) {
-                        vr[u][x][0] = on ? load_kv16<(NB > 1)>(src + 16 * g) : make_uint4(0, 0, 0, 0);
-                        vr[u][x][1] = on ? load_kv16<(NB > 1)>(src + 128 + 16 * g) : make_uint4(0, 0, 0, 0);
-                    } else if constexpr (S::NV * S::kElem == 16) {
-                        vr[u][x][0] = on ? load_kv16<(NB > 1)>(src + 16 * g) : make_uint4(0, 0, 0, 0);
-                    } else {
-                        const uint2 v = on ? __ldcg(reinterpret_cast<const uint2*>(src + 8 * g))
-                                           : make_uint2(0, 0);
+                    if constexpr (S::NV * S::kElem == 8) {
+                        const uint2 v = on ? __ldcg(reinterpret_cast<const uint2*>(src + 8 * g)) : make_uint2(0, 0);
                         vr[u][x][0] = make_uint4(v.x, v.y, 0, 0);
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < S::kVPieces; ++y)
+                            vr[u][x][y] = on ? load_kv16<(NB > 1)>(src + 128 * y + 16 * g) : make_uint4(0, 0, 0, 0);
                     }
                 }
             }
             // S^T = K Q^T, in log2 units
-            float s[S::kSub][NT][4];
-            float top[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = -CUDART_INF_F;
+            float s[S::kSub][4];
+            float top[2] = {-CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
             for (int u = 0; u < S::kSub; ++u) {
                 const int kb = key0 + 16 * u;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float(&acc)[4] = s[u][nt];
-                    acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
+                float(&acc)[4] = s[u];
+                acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
+                if constexpr (!FP8) {
 #pragma unroll
                     for (int j = 0; j < S::NK; ++j) {
                         const uint4 x = kr[u][0][j], y = kr[u][1][j];
-                        if constexpr (!FP8) {
-                            mma_16816(acc, x.x, y.x, x.y, y.y, qr[nt][4 * j], qr[nt][4 * j + 1], false);
-                            mma_16816(acc, x.z, y.z, x.w, y.w, qr[nt][4 * j + 2], qr[nt][4 * j + 3], false);
-                        } else {
-                            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+                        mma_16816_bf16(acc, x.x, y.x, x.y, y.y, qr[4 * j], qr[4 * j + 1]);
+                        mma_16816_bf16(acc, x.z, y.z, x.w, y.w, qr[4 * j + 2], qr[4 * j + 3]);
+                    }
+                } else {
 #pragma unroll
-                            for (int w = 0; w < 4; ++w)
-                                mma_16816(acc, e4m3x2_to_half2(xs[w] & 0xFFFF), e4m3x2_to_half2(ys[w] & 0xFFFF),
-                                          e4m3x2_to_half2(xs[w] >> 16), e4m3x2_to_half2(ys[w] >> 16),
-                                          qr[nt][8 * j + 2 * w], qr[nt][8 * j + 2 * w + 1], true);
+                    for (int j = 0; j < S::NK; ++j) {
+                        const uint4 x = kr[u][0][j], y = kr[u][1][j];
+                        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            uint32_t f[4];
+                            e4m3x4_to_half2(xs[w], f[0], f[2]);
+                            e4m3x4_to_half2(ys[w], f[1], f[3]);
+                            mma_16816_f16(acc, f[0], f[1], f[2], f[3], qr[8 * j + 2 * w], qr[8 * j + 2 * w + 1]);
                         }
                     }
+                }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int key = kb + g + 8 * (i >> 1);
-                        const bool on = ok[u] && key >= range.lo && key < range.hi;
-                        acc[i] = on ? acc[i] * c_log2[nt][i & 1] : -CUDART_INF_F;
-                        top[nt][i & 1] = fmaxf(top[nt][i & 1], acc[i]);
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    const int key = kb + g + 8 * (i >> 1);
+                    const bool on = ok[u] && key >= range.lo && key < range.hi;
+                    acc[i] = on ? acc[i] * c_log2[i & 1] : -CUDART_INF_F;
+                    top[i & 1] = fmaxf(top[i & 1], acc[i]);
                 }
             }
             // running maximum and sum
+            float f[2], base[2];  // base: what a score's exponent is taken from
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float f[2];
+            for (int i = 0; i < 2; ++i) {
+                float v = top[i];
+                v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
+                v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
+                v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
+                const float now = fmaxf(m[i], v);
+                f[i] = now == m[i] ? 1.0f : exp2_approx(m[i] - now);
+                m[i] = now;
+                l[i] *= f[i];
+                base[i] = (now == -CUDART_INF_F ? 0.0f : now) - (FP8 ? kRowRaise : 0.0f);
+            }
+            if (__any_sync(~0u, f[0] != 1.0f || f[1] != 1.0f)) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float v = top[nt][i];
-                    v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
-                    v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
-                    v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
-                    const float now = fmaxf(m[nt][i], v);
-                    f[i] = now == m[nt][i] ? 1.0f : exp2_approx(m[nt][i] - now);
-                    m[nt][i] = now;
-                    l[nt][i] *= f[i];
-                }
-                if (__any_sync(~0u, f[0] != 1.0f || f[1] != 1.0f)) {
-#pragma unroll
-                    for (int i = 0; i < S::NV / 2; ++i) {
-                        o[nt][i][0] *= f[0];
-                        o[nt][i][1] *= f[1];
-                        o[nt][i][2] *= f[0];
-                        o[nt][i][3] *= f[1];
-                    }
+                for (int i = 0; i < S::NV / 2; ++i) {
+                    o[i][0] *= f[0];
+                    o[i][1] *= f[1];
+                    o[i][2] *= f[0];
+                    o[i][3] *= f[1];
                 }
             }
-            // P^T and O^T += V^T P^T. P is rounded to the operands' 16 bits (half a step of a
-            // weight that is at most 1); its sum is taken before the rounding, in fp32. In fp16
-            // the weights are raised by 2^10 first, so that small ones of a long
-            // cache stay clear of fp16's smallest steps; it cancels against the sum.
+            // P^T, rounded to 16 bits (half a step of a weight); its sum is taken before the
+            // rounding, in fp32
+            uint32_t pb[S::kSub][2];
 #pragma unroll
             for (int u = 0; u < S::kSub; ++u) {
-                uint32_t pb[NT][2];
+                float p[4];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float p[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float mm = m[nt][i & 1] == -CUDART_INF_F ? 0.0f : m[nt][i & 1];
-                        p[i] = exp2_approx(s[u][nt][i] - mm + (FP8 ? 10.0f : 0.0f));
-                        l[nt][i & 1] += p[i];
-                    }
-                    pb[nt][0] = transpose_8x8(FP8 ? pack_half2(p[0], p[1]) : pack_bf162(p[0], p[1]));
-                    pb[nt][1] = transpose_8x8(FP8 ? pack_half2(p[2], p[3]) : pack_bf162(p[2], p[3]));
+                for (int i = 0; i < 4; ++i) {
+                    p[i] = exp2_approx(s[u][i] - base[i & 1]);
+                    l[i & 1] += p[i];
                 }
-                // word w of key x's dimensions
-                auto word = [&](int x, int w) {
-                    const uint4& y = vr[u][x][w >> 2];
-                    return (w & 3) == 0 ? y.x : (w & 3) == 1 ? y.y : (w & 3) == 2 ? y.z : y.w;
-                };
+                pb[u][0] = transpose_8x8(FP8 ? pack_half2(p[0], p[1]) : pack_bf162(p[0], p[1]));
+                pb[u][1] = transpose_8x8(FP8 ? pack_half2(p[2], p[3]) : pack_bf162(p[2], p[3]));
+            }
+            // O^T += V^T P^T
+            // word w of the dimensions of the lane's key x
+            auto word = [&](int u, int x, int w) {
+                const uint4& y = vr[u][x][w >> 2];
+                return (w & 3) == 0 ? y.x : (w & 3) == 1 ? y.y : (w & 3) == 2 ? y.z : y.w;
+            };
+#pragma unroll
+            for (int u = 0; u < S::kSub; ++u)
 #pragma unroll
                 for (int i = 0; i < S::NV / 2; i += 2) {
                     // fragments of two instructions: dimensions i, i + 1 and those NV/2 further on
+                    // (x & 1); keys 2t, 2t+1 and 2t+8, 2t+9 (x >> 1)
                     uint32_t av[2][4];
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        // rows e, keys 2t, 2t+1 or 2t+8, 2t+9 (x >> 1)
                         const int e = i + (x & 1) * (S::NV / 2), ka = 2 * (x >> 1);
                         if constexpr (!FP8) {
-                            av[0][x] = __byte_perm(word(ka, e >> 1), word(ka + 1, e >> 1), 0x5410);
-                            av[1][x] = __byte_perm(word(ka, e >> 1), word(ka + 1, e >> 1), 0x7632);
+                            av[0][x] = __byte_perm(word(u, ka, e >> 1), word(u, ka + 1, e >> 1), 0x5410);
+                            av[1][x] = __byte_perm(word(u, ka, e >> 1), word(u, ka + 1, e >> 1), 0x7632);
                         } else {
                             const uint32_t both =
-                                __byte_perm(word(ka, e >> 2), word(ka + 1, e >> 2), (e & 2) ? 0x7362 : 0x5140);
-                            av[0][x] = e4m3x2_to_half2(both & 0xFFFF);
-                            av[1][x] = e4m3x2_to_half2(both >> 16);
+                                __byte_perm(word(u, ka, e >> 2), word(u, ka + 1, e >> 2), (e & 2) ? 0x7362 : 0x5140);
+                            e4m3x4_to_half2(both, av[0][x], av[1][x]);
                         }
                     }
 #pragma unroll
-                    for (int y = 0; y < 2; ++y)
-                        mma_16816(o[0][i + y], av[y][0], av[y][1], av[y][2], av[y][3], pb[0][0], pb[0][1], FP8);
+                    for (int y = 0; y < 2; ++y) {
+                        if constexpr (FP8)
+                            mma_16816_f16(o[i + y], av[y][0], av[y][1], av[y][2], av[y][3], pb[u][0], pb[u][1]);
+                        else
+                            mma_16816_bf16(o[i + y], av[y][0], av[y][1], av[y][2], av[y][3], pb[u][0], pb[u][1]);
+                    }
                 }
-            }
         }
 
         // The warps' sums of this segment, joined in shared memory.
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float v = l[nt][i];
-                v += __shfl_xor_sync(~0u, v, 4);
-                v += __shfl_xor_sync(~0u, v, 8);
-                v += __shfl_xor_sync(~0u, v, 16);
-                l[nt][i] = v;
-            }
+        for (int i = 0; i < 2; ++i) {
+            float v = l[i];
+            v += __shfl_xor_sync(~0u, v, 4);
+            v += __shfl_xor_sync(~0u, v, 8);
+            v += __shfl_xor_sync(~0u, v, 16);
+            l[i] = v;
+        }
         __syncthreads();  // the segment before has been read
-        if (g == 0)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int r = block * 8 + 2 * t + i;
-                    sM[part_of * S::kRows + r] = m[nt][i];
-                    sL[part_of * S::kRows + r] = l[nt][i];
-                }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float* dst = sO + (part_of * S::kRows + block * 8 + 2 * t + i) * S::kPitch;
-#pragma unroll
-                for (int e = 0; e < S::NV; e += 4) {
-                    const int k = e % (S::NV / 2), hi = e >= S::NV / 2 ? 2 : 0;
-                    *reinterpret_cast<float4*>(dst + v_dim<D, FP8>(g, e)) =
-                        make_float4(o[nt][k][hi + i], o[nt][k + 1][hi + i], o[nt][k + 2][hi + i],
-                                    o[nt][k + 3][hi + i]);
-                }
+        for (int i = 0; i < 2; ++i) {
+            const int r = part_of * S::kRows + block * 8 + 2 * t + i;
+            if (g == 0) {
+                sM[r] = m[i];
+                sL[r] = l[i];
             }
+            float* dst = sO + r * S::kPitch;
+#pragma unroll
+            for (int e = 0; e < S::NV; e += 4) {
+                const int k = e % (S::NV / 2), hi = e >= S::NV / 2 ? 2 : 0;
+                *reinterpret_cast<float4*>(dst + v_dim<D, FP8>(g, e)) =
+                    make_float4(o[k][hi + i], o[k + 1][hi + i], o[k + 2][hi + i], o[k + 3][hi + i]);
+            }
+        }
         __syncthreads();
 
         // Contributors of the segment: the CTAs whose runs meet its steps.
@@ -673,7 +661,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
             if (a.lse && d == 0)
                 a.lse[static_cast<int64_t>(row) * a.Hq + head] =
                     ll == 0.0f ? -CUDART_INF_F
-                               : (mm + log2f(ll) - (FP8 ? 10.0f : 0.0f)) * 0.69314718055994531f;
+                               : (mm + log2f(ll) - (FP8 ? kRowRaise : 0.0f)) * 0.69314718055994531f;
         };
         for (int i = tid; i < valid * (D / 4); i += kRowThreads) {
             const int r = i / (D / 4), d = (i % (D / 4)) * 4;

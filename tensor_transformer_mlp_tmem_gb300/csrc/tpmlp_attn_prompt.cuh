@@ -1035,8 +1035,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     uint32_t h[8];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        h[2 * k] = e4m3x2_to_half2(w[k] & 0xFFFF);
-                        h[2 * k + 1] = e4m3x2_to_half2(w[k] >> 16);
+                        e4m3x4_to_half2(w[k], h[2 * k], h[2 * k + 1]);
                     }
                     // the two 16-byte chunks in an order that spreads a row's writes over all banks
                     uint8_t* const d = dst + (j >> 2) * kHalf + r * 128;
