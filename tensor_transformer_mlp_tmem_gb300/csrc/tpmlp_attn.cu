@@ -101,24 +101,27 @@ int allow_smem(tpmlp_ctx* c, Kernel kern, uint32_t smem, std::atomic<uint64_t>& 
     return TPMLP_OK;
 }
 
-template <int D, bool FP8, int NB>
+template <int D, bool FP8, int NB, int NT>
 int launch_rows(tpmlp_ctx* c, const tpmlp::RowArgs& a, cudaStream_t s) {
-    using S = tpmlp::RowShape<D, FP8, NB>;
-    auto kern = tpmlp::attn_row_kernel<D, FP8, NB>;
+    using S = tpmlp::RowShape<D, FP8, NB, NT>;
+    auto kern = tpmlp::attn_row_kernel<D, FP8, NB, NT>;
     static std::atomic<uint64_t> done{0};
     if (int rc = allow_smem(c, kern, S::kSmem, done)) return rc;
-    const int grid = c->num_sms * kRowCtasPerSm;
+    const int grid = c->num_sms * S::kCtasPerSm;
     return launch(c, kern, grid, tpmlp::kRowThreads, S::kSmem, s, a);
 }
 
 template <int D, bool FP8>
 int run_rows_of(tpmlp_ctx* c, tpmlp::RowArgs& a, cudaStream_t s) {
-    // blocks of 8 query heads of a kv head that a CTA's warps share out; more than four in turns
+    // A warp takes 8 or 16 query heads of a kv head, or two warps take 32 between them; more in
+    // turns. 16 to a warp (8 warps an SM with twice the registers) was 5 to 25 % faster than 8 to
+    // each of two warps over the same keys: 4096 keys x 64 sequences x 8 kv heads of 128, 12 query
+    // heads each, 220 against 232 us in bf16, 135 against 174 us in e4m3.
     const int blocks = (a.G + 7) / 8;
     a.blocks_per_head = (blocks + 3) / 4;
-    if (blocks == 1) return launch_rows<D, FP8, 1>(c, a, s);
-    if (blocks == 2) return launch_rows<D, FP8, 2>(c, a, s);
-    return launch_rows<D, FP8, 4>(c, a, s);
+    if (blocks == 1) return launch_rows<D, FP8, 1, 1>(c, a, s);
+    if (blocks == 2) return launch_rows<D, FP8, 1, 2>(c, a, s);
+    return launch_rows<D, FP8, 2, 2>(c, a, s);
 }
 
 int run_rows(tpmlp_ctx* c, tpmlp::RowArgs& a, cudaStream_t s) {
@@ -338,12 +341,19 @@ int tpmlp_attn_append(tpmlp_ctx* c, const void* Q, int64_t ldq, const void* K, i
     a.rot = c->rot_dim;
     a.interleaved = c->rope_interleaved;
     std::memcpy(a.turns, c->rope_turns, sizeof(a.turns));
+    // Parts of a token: two blocks an SM where there are few tokens, each thread with a unit at
+    // least. One token of 96 heads of 128: MEASURE5.
+    const int64_t units = static_cast<int64_t>(a.Hq + 2 * c->heads_kv) * (c->head_dim / 16);
+    const int64_t most = (units + tpmlp::kAppendThreads - 1) / tpmlp::kAppendThreads;
+    a.parts = static_cast<int32_t>(std::min(most, std::max<int64_t>(1, 2 * c->num_sms / T)));
+    a.part_units = static_cast<int32_t>((units + a.parts - 1) / a.parts);
+    const int64_t grid = T * a.parts;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (c->head_dim == 128)
-        return is_e4m3(c) ? launch(c, tpmlp::append_kernel<128, true>, T, tpmlp::kAppendThreads, 0, s, a)
-                          : launch(c, tpmlp::append_kernel<128, false>, T, tpmlp::kAppendThreads, 0, s, a);
-    return is_e4m3(c) ? launch(c, tpmlp::append_kernel<64, true>, T, tpmlp::kAppendThreads, 0, s, a)
-                      : launch(c, tpmlp::append_kernel<64, false>, T, tpmlp::kAppendThreads, 0, s, a);
+        return is_e4m3(c) ? launch(c, tpmlp::append_kernel<128, true>, grid, tpmlp::kAppendThreads, 0, s, a)
+                          : launch(c, tpmlp::append_kernel<128, false>, grid, tpmlp::kAppendThreads, 0, s, a);
+    return is_e4m3(c) ? launch(c, tpmlp::append_kernel<64, true>, grid, tpmlp::kAppendThreads, 0, s, a)
+                      : launch(c, tpmlp::append_kernel<64, false>, grid, tpmlp::kAppendThreads, 0, s, a);
 }
 
 int tpmlp_attn_decode(tpmlp_ctx* c, const void* Q, int64_t ldq, const tpmlp_kv* kv, float scale,

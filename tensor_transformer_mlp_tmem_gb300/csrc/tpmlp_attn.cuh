@@ -68,10 +68,18 @@ struct AppendArgs {
     int32_t Hq;         // 0: no queries
     int32_t rot;        // rotated dimensions, a multiple of 16
     int32_t interleaved;
+    int32_t parts;      // blocks per token
+    int32_t part_units; // units of each
     double turns[64];   // whole turns per position of each pair
 };
 
-constexpr int kAppendThreads = 256;
+// Loads of what another kernel of the stream may have just written: through L2 (the read-only
+// path must not be used while this kernel may overlap the writer's end).
+__device__ __forceinline__ uint4 load16(const uint8_t* p) {
+    return __ldcg(reinterpret_cast<const uint4*>(p));
+}
+constexpr int kAppendThreads = 128;
+constexpr int kAppendUnits = 4;  // units of 16 elements that a thread has in flight
 
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -104,89 +112,118 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float (&f)[8], float scale) {
     return make_uint2(w[0], w[1]);
 }
 
-// One block per token. The rotation's sines and cosines are the same for all heads: the block
-// computes the token's rot / 2 of them once, in shared memory. The angle is taken in whole turns
-// in fp64 and reduced to [-1/2, 1/2] there, so its error is that of the fp32 result however far
-// the position (an fp32 product would be off by whole radians at position 10^7). Then each thread
+// A block takes a token, or one of `parts` equal parts of it where there are few tokens. The
+// rotation's sines and cosines are the same for all heads: the block computes the token's rot / 2
+// of them once, in shared memory, while its first loads are under way. The angle is taken in whole
+// turns in fp64 and reduced to [-1/2, 1/2] there, so its error is that of the fp32 result however
+// far the position (an fp32 product would be off by whole radians at position 10^7). A thread
 // rotates units of 16 elements: the 8 dimensions from 8u and their partners, which are the 8 from
-// rot/2 + 8u (halves) or the same 16 (neighbours).
+// rot/2 + 8u (halves) or the same 16 (neighbours). Bound by DRAM; MEASURE4.
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendArgs a) {
     __shared__ float2 trig[D / 2];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    const int64_t t = blockIdx.x;
-    const int pos = a.pos[t];
-    if (pos < 0) return;
-    const int half = a.rot >> 1;
-    for (int i = threadIdx.x; i < half; i += kAppendThreads) {
-        const double turn = pos * a.turns[i];
-        float s, c;
-        sincospif(2.0f * static_cast<float>(turn - rint(turn)), &s, &c);
-        trig[i] = make_float2(c, s);
-    }
-    const int b = a.seq ? a.seq[t] : static_cast<int>(t);
-    int64_t page = -1;
-    if (b >= 0 && b < a.kv.B && t <= 0x7FFFFFFF && (pos >> a.kv.page_shift) < a.kv.table_pages)
-        page = kv_page(a.kv, b, pos);
-    else if (threadIdx.x == 0)
-        report_bad_page(a.kv.status);
-    __syncthreads();
-    const int slot = pos & ((1 << a.kv.page_shift) - 1);
     constexpr int kUnits = D / 16;  // units per head
-    const int heads = a.Hq + 2 * a.kv.Hkv;
-    for (int i = threadIdx.x; i < heads * kUnits; i += kAppendThreads) {
-        const int head = i / kUnits, u = i % kUnits;
-        const bool is_q = head < a.Hq, is_v = head >= a.Hq + a.kv.Hkv;
-        if (!is_q && page < 0) continue;
-        const int h = is_q ? head : is_v ? head - a.Hq - a.kv.Hkv : head - a.Hq;
-        const __nv_bfloat16* src = (is_q ? a.q + t * a.ldq : is_v ? a.v + t * a.ldv : a.k + t * a.ldk) +
-                                   static_cast<int64_t>(h) * D;
-        const bool rotate = !is_v && 16 * u < a.rot;
-        // the unit's two pieces of 8 dimensions
-        int d0 = 16 * u, d1 = d0 + 8;
-        if (rotate && !a.interleaved) {
-            d0 = 8 * u;
-            d1 = half + d0;
+    const int64_t t = blockIdx.x / a.parts;
+    const int units = (a.Hq + 2 * a.kv.Hkv) * kUnits;
+    const int begin = static_cast<int>(blockIdx.x % a.parts) * a.part_units;
+    const int end = min(begin + a.part_units, units);
+    const int half = a.rot >> 1;
+    const int pos = a.pos[t];
+    const int b = a.seq ? a.seq[t] : static_cast<int>(t);
+    int page = -1;
+    for (int first = begin; first < end; first += kAppendThreads * kAppendUnits) {
+        uint4 raw[kAppendUnits][2];
+        // unit i: its part of the token, head, whether it is rotated, its two pieces of 8 dimensions
+        struct Unit {
+            int kind, h, d0, d1;  // kind: 0 q, 1 k, 2 v
+            bool rotate;
+        };
+        auto unit = [&](int i) {
+            Unit x;
+            const int head = i / kUnits, u = i % kUnits;
+            x.kind = head < a.Hq ? 0 : head < a.Hq + a.kv.Hkv ? 1 : 2;
+            x.h = x.kind == 0 ? head : x.kind == 1 ? head - a.Hq : head - a.Hq - a.kv.Hkv;
+            x.rotate = x.kind != 2 && 16 * u < a.rot;
+            x.d0 = 16 * u;
+            x.d1 = x.d0 + 8;
+            if (x.rotate && !a.interleaved) {
+                x.d0 = 8 * u;
+                x.d1 = half + x.d0;
+            }
+            return x;
+        };
+#pragma unroll
+        for (int y = 0; y < kAppendUnits; ++y) {
+            const int i = first + y * kAppendThreads + static_cast<int>(threadIdx.x);
+            if (i >= end) break;
+            const Unit x = unit(i);
+            const __nv_bfloat16* src = (x.kind == 0 ? a.q + t * a.ldq : x.kind == 1 ? a.k + t * a.ldk : a.v + t * a.ldv) +
+                                       static_cast<int64_t>(x.h) * D;
+            raw[y][0] = load16(reinterpret_cast<const uint8_t*>(src + x.d0));
+            raw[y][1] = load16(reinterpret_cast<const uint8_t*>(src + x.d1));
         }
-        float x[8], y[8];
-        unpack8(*reinterpret_cast<const uint4*>(src + d0), x);
-        unpack8(*reinterpret_cast<const uint4*>(src + d1), y);
-        if (rotate) {
-            if (a.interleaved) {
+        if (first == begin) {
+            if (pos < 0) return;
+            for (int i = threadIdx.x; i < half; i += kAppendThreads) {
+                const double turn = pos * a.turns[i];
+                float s, c;
+                sincospif(2.0f * static_cast<float>(turn - rint(turn)), &s, &c);
+                trig[i] = make_float2(c, s);
+            }
+            if (b >= 0 && b < a.kv.B && (pos >> a.kv.page_shift) < a.kv.table_pages) page = kv_page(a.kv, b, pos);
+            else if (threadIdx.x == 0) report_bad_page(a.kv.status);
+            __syncthreads();
+        }
+        const int slot = pos & ((1 << a.kv.page_shift) - 1);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 r0 = trig[8 * u + j], r1 = trig[8 * u + 4 + j];
-                    const float x0 = x[2 * j], y0 = y[2 * j];
-                    x[2 * j] = x0 * r0.x - x[2 * j + 1] * r0.y;
-                    x[2 * j + 1] = x[2 * j + 1] * r0.x + x0 * r0.y;
-                    y[2 * j] = y0 * r1.x - y[2 * j + 1] * r1.y;
-                    y[2 * j + 1] = y[2 * j + 1] * r1.x + y0 * r1.y;
-                }
-            } else {
+        for (int y = 0; y < kAppendUnits; ++y) {
+            const int i = first + y * kAppendThreads + static_cast<int>(threadIdx.x);
+            if (i >= end) break;
+            const Unit w = unit(i);
+            float x0[8], x1[8];
+            unpack8(raw[y][0], x0);
+            unpack8(raw[y][1], x1);
+            if (w.rotate) {
+                const float2* const r = trig + 8 * (i % kUnits);
+                if (a.interleaved) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float2 r = trig[8 * u + j];
-                    const float x0 = x[j];
-                    x[j] = x0 * r.x - y[j] * r.y;
-                    y[j] = y[j] * r.x + x0 * r.y;
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 r0 = r[j], r1 = r[4 + j];
+                        const float p0 = x0[2 * j], p1 = x1[2 * j];
+                        x0[2 * j] = p0 * r0.x - x0[2 * j + 1] * r0.y;
+                        x0[2 * j + 1] = x0[2 * j + 1] * r0.x + p0 * r0.y;
+                        x1[2 * j] = p1 * r1.x - x1[2 * j + 1] * r1.y;
+                        x1[2 * j + 1] = x1[2 * j + 1] * r1.x + p1 * r1.y;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 r0 = r[j];
+                        const float p0 = x0[j];
+                        x0[j] = p0 * r0.x - x1[j] * r0.y;
+                        x1[j] = x1[j] * r0.x + p0 * r0.y;
+                    }
                 }
             }
-        }
-        if (is_q || !FP8) {
-            __nv_bfloat16* dst =
-                is_q ? a.q_out + t * a.ldqo + static_cast<int64_t>(h) * D
-                     : reinterpret_cast<__nv_bfloat16*>((is_v ? a.kv.V : a.kv.K) + page * a.kv.page_bytes +
-                                                        h * a.kv.head_bytes) +
-                           static_cast<int64_t>(slot) * D;
-            *reinterpret_cast<uint4*>(dst + d0) = pack8_bf16(x);
-            *reinterpret_cast<uint4*>(dst + d1) = pack8_bf16(y);
-        } else {
-            uint8_t* dst = (is_v ? a.kv.V : a.kv.K) + page * a.kv.page_bytes + h * a.kv.head_bytes +
-                           static_cast<int64_t>(slot) * D;
-            const float scale = a.kv.scales[(is_v ? a.kv.Hkv : 0) + h];
-            *reinterpret_cast<uint2*>(dst + d0) = pack8_e4m3(x, scale);
-            *reinterpret_cast<uint2*>(dst + d1) = pack8_e4m3(y, scale);
+            if (w.kind == 0) {
+                __nv_bfloat16* const dst = a.q_out + t * a.ldqo + static_cast<int64_t>(w.h) * D;
+                *reinterpret_cast<uint4*>(dst + w.d0) = pack8_bf16(x0);
+                *reinterpret_cast<uint4*>(dst + w.d1) = pack8_bf16(x1);
+                continue;
+            }
+            if (page < 0) continue;
+            uint8_t* const at = (w.kind == 2 ? a.kv.V : a.kv.K) + page * a.kv.page_bytes + w.h * a.kv.head_bytes +
+                                static_cast<int64_t>(slot) * (D * (FP8 ? 1 : 2));
+            if constexpr (FP8) {
+                const float scale = a.kv.scales[(w.kind == 2 ? a.kv.Hkv : 0) + w.h];
+                *reinterpret_cast<uint2*>(at + w.d0) = pack8_e4m3(x0, scale);
+                *reinterpret_cast<uint2*>(at + w.d1) = pack8_e4m3(x1, scale);
+            } else {
+                *reinterpret_cast<uint4*>(at + 2 * w.d0) = pack8_bf16(x0);
+                *reinterpret_cast<uint4*>(at + 2 * w.d1) = pack8_bf16(x1);
+            }
         }
     }
 }
@@ -203,7 +240,7 @@ struct RowArgs {
     float* lse;             // [rows][Hq] or null
     int32_t rows;           // sequences
     int32_t Hq, G;
-    int32_t blocks_per_head;  // blocks of 8 * NT query heads that share a kv head
+    int32_t blocks_per_head;  // a CTA's blocks of query heads (RowShape::kRows) that share a kv head
     float scale_log2;         // softmax scale * log2(e)
     int32_t window;
     float* partial;         // [CTAs][2] slots of RowSlot floats
@@ -267,11 +304,6 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
-// Loads of what another kernel of the stream may have just written: through L2 (the read-only
-// path must not be used while this kernel may overlap the writer's end).
-__device__ __forceinline__ uint4 load16(const uint8_t* p) {
-    return __ldcg(reinterpret_cast<const uint4*>(p));
-}
 template <bool L1>
 __device__ __forceinline__ uint4 load_kv16(const uint8_t* p) {
     return L1 ? __ldca(reinterpret_cast<const uint4*>(p)) : __ldcg(reinterpret_cast<const uint4*>(p));
@@ -294,23 +326,27 @@ __device__ __forceinline__ RowRange row_range(const RowArgs& a, int b) {
 // memory, in an order of the reduction index that Q's registers share; V is the A operand of
 // O^T = V^T P^T, its pairs of keys put together with byte permutes. No shared memory, no barriers
 // and no copies are needed on the way: 16 warps an SM keep 128 KB of loads in flight, and the
-// bound is DRAM. NB warps take the same keys for NB blocks of 8 query heads; all but the first
-// find them in L1. e4m3 values are converted to fp16 in registers (the 8-bit forms of these matrix
+// bound is DRAM (64 sequences of 4096 keys x 32 heads in bf16: 6.6 TB/s, 97 % of a copy's rate).
+// Tried and slower by a fifth to a third: the same tiles copied to shared memory ahead of use
+// (cp.async; their reads then lie in every product's way), and loading the next tile's K and V
+// in registers while this one is in use (spills). A warp holds NT blocks of 8 query heads; NB
+// warps take the same keys for more of them, and all but the first find the keys in L1. e4m3 values are converted to fp16 in registers (the 8-bit forms of these matrix
 // instructions take three times as long as the fp16 ones on this GPU).
-template <int D, bool FP8, int NB>
+template <int D, bool FP8, int NB, int NT>
 struct RowShape {
     static constexpr int kElem = FP8 ? 1 : 2;
     static constexpr int kSub = 256 / (D * kElem);   // subtiles of 16 keys
     static constexpr int KT = 16 * kSub;
     static constexpr int kParts = kRowWarps / NB;    // warps that share out the keys
     static constexpr int kStep = KT * kParts;        // keys of a CTA's step
-    static constexpr int kRows = 8 * NB;             // query heads of a CTA
+    static constexpr int kRows = 8 * NB * NT;        // query heads of a CTA
+    static constexpr int kCtasPerSm = NT == 1 ? 2 : 1;
     static constexpr int NK = D * kElem / 64;        // 16-byte pieces of a K row per thread
     static constexpr int NV = D / 8;                 // V dimensions per thread
     static constexpr int kVPieces = NV * kElem >= 16 ? NV * kElem / 16 : 1;  // 16-byte pieces of a V row
     static constexpr int kQRegs = D / 8;             // Q registers of 8 query heads
     static constexpr int kPitch = D + 4;             // fp32 row of the merge buffer
-    static constexpr int kSmem = kRowWarps * 8 * (kPitch + 2) * 4;
+    static constexpr int kSmem = kRowWarps * 8 * NT * (kPitch + 2) * 4;
 };
 
 // The dimension that element e of lane group g's V registers stands for.
@@ -320,10 +356,10 @@ __device__ __forceinline__ int v_dim(int g, int e) {
     else return (D / 8) * g + e;
 }
 
-template <int D, bool FP8, int NB>
-__global__ void __launch_bounds__(kRowThreads, 2)
+template <int D, bool FP8, int NB, int NT>
+__global__ void __launch_bounds__(kRowThreads, RowShape<D, FP8, NB, NT>::kCtasPerSm)
 attn_row_kernel(const __grid_constant__ RowArgs a) {
-    using S = RowShape<D, FP8, NB>;
+    using S = RowShape<D, FP8, NB, NT>;
     extern __shared__ float smem[];
     float* const sO = smem;                                       // [parts][rows][pitch]
     float* const sM = sO + S::kParts * S::kRows * S::kPitch;      // [parts][rows]
@@ -342,25 +378,42 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         return max(1, (x.hi - (x.lo & ~15) + S::kStep - 1) / S::kStep);
     };
     // Sum of the rows' steps: the work of every (row, kv head, block of query heads) segment is
-    // its row's steps, and each CTA takes an equal run of all segments' steps.
+    // its row's steps, and each CTA takes an equal run of all segments' steps. Then the row that
+    // holds this CTA's first step.
     const int64_t per_row = static_cast<int64_t>(a.kv.Hkv) * a.blocks_per_head;
-    int64_t mine = 0;
-    for (int r = tid; r < a.rows; r += kRowThreads) mine += steps_of(row_range(a, r));
+    int64_t per_cta, at, end;
+    int row = -1;
+    int64_t row_start = 0;  // first step of that row
+    auto share = [&](int64_t total) {
+        per_cta = (total + gridDim.x - 1) / gridDim.x;
+        at = per_cta * blockIdx.x;
+        end = min(at + per_cta, total);
+    };
+    if (a.rows <= 32) {
+        // every warp for itself, a row to a lane: no barrier in a small call's way
+        const uint32_t c = lane < a.rows ? steps_of(row_range(a, lane)) : 0;
+        uint32_t sum = c;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(~0u, mine, o);
-    if (lane == 0) s_scan[warp] = mine;
-    __syncthreads();
-    int64_t total = 0;
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(~0u, sum, o);
+            if (lane >= o) sum += v;
+        }
+        share(__shfl_sync(~0u, sum, 31) * per_row);
+        if (at >= end) return;
+        row = __ffs(__ballot_sync(~0u, at < sum * per_row)) - 1;
+        row_start = __shfl_sync(~0u, sum - c, row) * per_row;
+    } else {
+        int64_t mine = 0;
+        for (int r = tid; r < a.rows; r += kRowThreads) mine += steps_of(row_range(a, r));
 #pragma unroll
-    for (int w = 0; w < kRowWarps; ++w) total += s_scan[w];
-    total *= per_row;
-    const int64_t per_cta = (total + gridDim.x - 1) / gridDim.x;
-    int64_t at = per_cta * blockIdx.x;
-    const int64_t end = min(at + per_cta, total);
-    if (at >= end) return;
-
-    // The row that holds this CTA's first step.
-    {
+        for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(~0u, mine, o);
+        if (lane == 0) s_scan[warp] = mine;
+        __syncthreads();
+        int64_t total = 0;
+#pragma unroll
+        for (int w = 0; w < kRowWarps; ++w) total += s_scan[w];
+        share(total * per_row);
+        if (at >= end) return;
         int64_t before = 0;
         for (int r0 = 0; r0 < a.rows; r0 += kRowThreads) {
             const int r = r0 + tid;
@@ -386,17 +439,18 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
             __syncthreads();
             if (s_found[0] >= 0) break;
         }
+        row = static_cast<int>(s_found[0]);
+        row_start = s_found[1];
+        if (row < 0) return;  // only if the lengths changed during the launch
     }
-    if (s_found[0] < 0) return;  // only if the lengths changed during the launch
-    int row = static_cast<int>(s_found[0]);
     RowRange range = row_range(a, row);
     int steps = steps_of(range);
     int64_t segment_start;  // first step of the current segment
     int part;               // kv head * blocks_per_head + block
     {
-        const int64_t into = at - s_found[1];
+        const int64_t into = at - row_start;
         part = static_cast<int>(into / steps);
-        segment_start = s_found[1] + static_cast<int64_t>(part) * steps;
+        segment_start = row_start + static_cast<int64_t>(part) * steps;
     }
 
     while (at < end) {
@@ -409,10 +463,11 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         // Q in the reduction order of the K pieces. In the 8-bit cache's fp16 products each row is
         // scaled by a power of two to a largest magnitude in [1, 2), so that no bf16 value
         // overflows; the scores are scaled back.
-        uint32_t qr[S::kQRegs];
-        float c_log2[2];  // score -> log2 units, for the lane's query columns 2 t, 2 t + 1
-        {
-            const int qi = block * 8 + g;
+        uint32_t qr[NT][S::kQRegs];
+        float c_log2[NT][2];  // score -> log2 units, for the lane's query columns 2 t, 2 t + 1
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int qi = (block * NT + nt) * 8 + g;
             const __nv_bfloat16* src = a.q + row * a.ldq + (static_cast<int64_t>(h) * a.G + q0 + qi) * D;
             const bool on = qi < valid;
             if constexpr (!FP8) {
@@ -420,12 +475,12 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
                 for (int j = 0; j < S::NK; ++j) {
                     const uint4 v = on ? load16(reinterpret_cast<const uint8_t*>(src + 8 * (t + 4 * j)))
                                        : make_uint4(0, 0, 0, 0);
-                    qr[4 * j] = v.x;
-                    qr[4 * j + 1] = v.y;
-                    qr[4 * j + 2] = v.z;
-                    qr[4 * j + 3] = v.w;
+                    qr[nt][4 * j] = v.x;
+                    qr[nt][4 * j + 1] = v.y;
+                    qr[nt][4 * j + 2] = v.z;
+                    qr[nt][4 * j + 3] = v.w;
                 }
-                c_log2[0] = c_log2[1] = a.scale_log2;
+                c_log2[nt][0] = c_log2[nt][1] = a.scale_log2;
             } else {
                 float x[S::NK][2][8];
                 float big = 0.0f;
@@ -451,19 +506,22 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
                 for (int j = 0; j < S::NK; ++j)
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        qr[8 * j + i] = pack_half2(x[j][i >> 2][2 * (i & 3)] * down, x[j][i >> 2][2 * (i & 3) + 1] * down);
+                        qr[nt][8 * j + i] = pack_half2(x[j][i >> 2][2 * (i & 3)] * down, x[j][i >> 2][2 * (i & 3) + 1] * down);
                 const float ks = a.scale_log2 * a.kv.scales[h];
-                c_log2[0] = ks * __shfl_sync(~0u, up, 8 * t);
-                c_log2[1] = ks * __shfl_sync(~0u, up, 8 * t + 4);
+                c_log2[nt][0] = ks * __shfl_sync(~0u, up, 8 * t);
+                c_log2[nt][1] = ks * __shfl_sync(~0u, up, 8 * t + 4);
             }
         }
 
-        float o[S::NV / 2][4];  // O^T: (dim e, q 2t), (dim e, q 2t+1), (dim e + NV/2, ...)
-        float m[2], l[2];
-        m[0] = m[1] = -CUDART_INF_F;
-        l[0] = l[1] = 0.0f;
+        float o[NT][S::NV / 2][4];  // O^T: (dim e, q 2t), (dim e, q 2t+1), (dim e + NV/2, ...)
+        float m[NT][2], l[NT][2];
 #pragma unroll
-        for (int i = 0; i < S::NV / 2; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+        for (int nt = 0; nt < NT; ++nt) {
+            m[nt][0] = m[nt][1] = -CUDART_INF_F;
+            l[nt][0] = l[nt][1] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < S::NV / 2; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.0f;
+        }
 
         const int64_t head_off = h * a.kv.head_bytes;
         const int lo16 = range.lo & ~15;
@@ -509,31 +567,34 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
                 }
             }
             // S^T = K Q^T, in log2 units
-            float s[S::kSub][4];
-            float top[2] = {-CUDART_INF_F, -CUDART_INF_F};
+            float s[S::kSub][NT][4];
+            float top[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = -CUDART_INF_F;
 #pragma unroll
             for (int u = 0; u < S::kSub; ++u) {
                 const int kb = key0 + 16 * u;
-                float(&acc)[4] = s[u];
-                acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
-                if constexpr (!FP8) {
 #pragma unroll
-                    for (int j = 0; j < S::NK; ++j) {
-                        const uint4 x = kr[u][0][j], y = kr[u][1][j];
-                        mma_16816_bf16(acc, x.x, y.x, x.y, y.y, qr[4 * j], qr[4 * j + 1]);
-                        mma_16816_bf16(acc, x.z, y.z, x.w, y.w, qr[4 * j + 2], qr[4 * j + 3]);
-                    }
-                } else {
+                for (int nt = 0; nt < NT; ++nt) s[u][nt][0] = s[u][nt][1] = s[u][nt][2] = s[u][nt][3] = 0.0f;
 #pragma unroll
-                    for (int j = 0; j < S::NK; ++j) {
-                        const uint4 x = kr[u][0][j], y = kr[u][1][j];
+                for (int j = 0; j < S::NK; ++j) {
+                    const uint4 x = kr[u][0][j], y = kr[u][1][j];
+                    if constexpr (!FP8) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma_16816_bf16(s[u][nt], x.x, y.x, x.y, y.y, qr[nt][4 * j], qr[nt][4 * j + 1]);
+                            mma_16816_bf16(s[u][nt], x.z, y.z, x.w, y.w, qr[nt][4 * j + 2], qr[nt][4 * j + 3]);
+                        }
+                    } else {
                         const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
                         for (int w = 0; w < 4; ++w) {
                             uint32_t f[4];
                             e4m3x4_to_half2(xs[w], f[0], f[2]);
                             e4m3x4_to_half2(ys[w], f[1], f[3]);
-                            mma_16816_f16(acc, f[0], f[1], f[2], f[3], qr[8 * j + 2 * w], qr[8 * j + 2 * w + 1]);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma_16816_f16(s[u][nt], f[0], f[1], f[2], f[3], qr[nt][8 * j + 2 * w], qr[nt][8 * j + 2 * w + 1]);
                         }
                     }
                 }
@@ -541,47 +602,56 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
                 for (int i = 0; i < 4; ++i) {
                     const int key = kb + g + 8 * (i >> 1);
                     const bool on = ok[u] && key >= range.lo && key < range.hi;
-                    acc[i] = on ? acc[i] * c_log2[i & 1] : -CUDART_INF_F;
-                    top[i & 1] = fmaxf(top[i & 1], acc[i]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        s[u][nt][i] = on ? s[u][nt][i] * c_log2[nt][i & 1] : -CUDART_INF_F;
+                        top[nt][i & 1] = fmaxf(top[nt][i & 1], s[u][nt][i]);
+                    }
                 }
             }
             // running maximum and sum
-            float f[2], base[2];  // base: what a score's exponent is taken from
+            float base[NT][2];  // what a score's exponent is taken from
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float v = top[i];
-                v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
-                v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
-                v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
-                const float now = fmaxf(m[i], v);
-                f[i] = now == m[i] ? 1.0f : exp2_approx(m[i] - now);
-                m[i] = now;
-                l[i] *= f[i];
-                base[i] = (now == -CUDART_INF_F ? 0.0f : now) - (FP8 ? kRowRaise : 0.0f);
-            }
-            if (__any_sync(~0u, f[0] != 1.0f || f[1] != 1.0f)) {
+            for (int nt = 0; nt < NT; ++nt) {
+                float f[2];
 #pragma unroll
-                for (int i = 0; i < S::NV / 2; ++i) {
-                    o[i][0] *= f[0];
-                    o[i][1] *= f[1];
-                    o[i][2] *= f[0];
-                    o[i][3] *= f[1];
+                for (int i = 0; i < 2; ++i) {
+                    float v = top[nt][i];
+                    v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
+                    v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
+                    v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
+                    const float now = fmaxf(m[nt][i], v);
+                    f[i] = now == m[nt][i] ? 1.0f : exp2_approx(m[nt][i] - now);
+                    m[nt][i] = now;
+                    l[nt][i] *= f[i];
+                    base[nt][i] = (now == -CUDART_INF_F ? 0.0f : now) - (FP8 ? kRowRaise : 0.0f);
+                }
+                if (__any_sync(~0u, f[0] != 1.0f || f[1] != 1.0f)) {
+#pragma unroll
+                    for (int i = 0; i < S::NV / 2; ++i) {
+                        o[nt][i][0] *= f[0];
+                        o[nt][i][1] *= f[1];
+                        o[nt][i][2] *= f[0];
+                        o[nt][i][3] *= f[1];
+                    }
                 }
             }
             // P^T, rounded to 16 bits (half a step of a weight); its sum is taken before the
             // rounding, in fp32
-            uint32_t pb[S::kSub][2];
+            uint32_t pb[S::kSub][NT][2];
 #pragma unroll
-            for (int u = 0; u < S::kSub; ++u) {
-                float p[4];
+            for (int u = 0; u < S::kSub; ++u)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    p[i] = exp2_approx(s[u][i] - base[i & 1]);
-                    l[i & 1] += p[i];
+                for (int nt = 0; nt < NT; ++nt) {
+                    float p[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        p[i] = exp2_approx(s[u][nt][i] - base[nt][i & 1]);
+                        l[nt][i & 1] += p[i];
+                    }
+                    pb[u][nt][0] = transpose_8x8(FP8 ? pack_half2(p[0], p[1]) : pack_bf162(p[0], p[1]));
+                    pb[u][nt][1] = transpose_8x8(FP8 ? pack_half2(p[2], p[3]) : pack_bf162(p[2], p[3]));
                 }
-                pb[u][0] = transpose_8x8(FP8 ? pack_half2(p[0], p[1]) : pack_bf162(p[0], p[1]));
-                pb[u][1] = transpose_8x8(FP8 ? pack_half2(p[2], p[3]) : pack_bf162(p[2], p[3]));
-            }
             // O^T += V^T P^T
             // word w of the dimensions of the lane's key x
             auto word = [&](int u, int x, int w) {
@@ -608,40 +678,46 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
                         }
                     }
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        if constexpr (FP8)
-                            mma_16816_f16(o[i + y], av[y][0], av[y][1], av[y][2], av[y][3], pb[u][0], pb[u][1]);
-                        else
-                            mma_16816_bf16(o[i + y], av[y][0], av[y][1], av[y][2], av[y][3], pb[u][0], pb[u][1]);
-                    }
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if constexpr (FP8)
+                                mma_16816_f16(o[nt][i + y], av[y][0], av[y][1], av[y][2], av[y][3], pb[u][nt][0], pb[u][nt][1]);
+                            else
+                                mma_16816_bf16(o[nt][i + y], av[y][0], av[y][1], av[y][2], av[y][3], pb[u][nt][0], pb[u][nt][1]);
+                        }
                 }
         }
 
         // The warps' sums of this segment, joined in shared memory.
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float v = l[i];
-            v += __shfl_xor_sync(~0u, v, 4);
-            v += __shfl_xor_sync(~0u, v, 8);
-            v += __shfl_xor_sync(~0u, v, 16);
-            l[i] = v;
-        }
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float v = l[nt][i];
+                v += __shfl_xor_sync(~0u, v, 4);
+                v += __shfl_xor_sync(~0u, v, 8);
+                v += __shfl_xor_sync(~0u, v, 16);
+                l[nt][i] = v;
+            }
         __syncthreads();  // the segment before has been read
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = part_of * S::kRows + block * 8 + 2 * t + i;
-            if (g == 0) {
-                sM[r] = m[i];
-                sL[r] = l[i];
-            }
-            float* dst = sO + r * S::kPitch;
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < S::NV; e += 4) {
-                const int k = e % (S::NV / 2), hi = e >= S::NV / 2 ? 2 : 0;
-                *reinterpret_cast<float4*>(dst + v_dim<D, FP8>(g, e)) =
-                    make_float4(o[k][hi + i], o[k + 1][hi + i], o[k + 2][hi + i], o[k + 3][hi + i]);
+            for (int i = 0; i < 2; ++i) {
+                const int r = part_of * S::kRows + (block * NT + nt) * 8 + 2 * t + i;
+                if (g == 0) {
+                    sM[r] = m[nt][i];
+                    sL[r] = l[nt][i];
+                }
+                float* dst = sO + r * S::kPitch;
+#pragma unroll
+                for (int e = 0; e < S::NV; e += 4) {
+                    const int k = e % (S::NV / 2), hi = e >= S::NV / 2 ? 2 : 0;
+                    *reinterpret_cast<float4*>(dst + v_dim<D, FP8>(g, e)) =
+                        make_float4(o[nt][k][hi + i], o[nt][k + 1][hi + i], o[nt][k + 2][hi + i], o[nt][k + 3][hi + i]);
+                }
             }
-        }
         __syncthreads();
 
         // Contributors of the segment: the CTAs whose runs meet its steps.
