@@ -591,6 +591,44 @@ TPMLP_API int tpmlp_attn_prompt(tpmlp_ctx *ctx, const void *Q, int64_t ldq, int6
                                 int32_t window, void *Out, int64_t ldo, float *Lse,
                                 void *stream);
 
+/*
+ * The three calls above with their arguments in one structure, for bindings that pay per argument
+ * (a decode step's calls take a few microseconds): the same checks, kernels and errors. `scale` is
+ * rounded to fp32. NULL: INVALID_ARG.
+ */
+typedef struct tpmlp_append_args {
+    tpmlp_ctx *ctx;
+    const void *Q;
+    int64_t ldq;
+    const void *K;
+    int64_t ldk;
+    const void *V;
+    int64_t ldv;
+    int64_t T;
+    const int32_t *pos, *seq;
+    const tpmlp_kv *kv;
+    void *Qout;
+    int64_t ldqo;
+    void *stream;
+} tpmlp_append_args;
+typedef struct tpmlp_attend_args {
+    tpmlp_ctx *ctx;
+    const void *Q;
+    int64_t ldq;
+    int64_t T;             /* prompt only */
+    const int32_t *cu_q;   /* prompt only */
+    const tpmlp_kv *kv;
+    double scale;
+    int64_t window;        /* within int32_t */
+    void *Out;
+    int64_t ldo;
+    float *Lse;
+    void *stream;
+} tpmlp_attend_args;
+TPMLP_API int tpmlp_attn_append_packed(const tpmlp_append_args *args);
+TPMLP_API int tpmlp_attn_decode_packed(const tpmlp_attend_args *args);
+TPMLP_API int tpmlp_attn_prompt_packed(const tpmlp_attend_args *args);
+
 /* Release everything the context owns (synchronises its device first). NULL is a no-op. */
 TPMLP_API void tpmlp_destroy(tpmlp_ctx *ctx);
 

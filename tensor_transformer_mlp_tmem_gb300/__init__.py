@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import sys
 
 __all__ = [
@@ -33,7 +34,8 @@ __all__ = [
     "tpmlp_block_forward_host_async", "tpmlp_host_wait",
     "Attention", "PagedCache", "KvCache", "TPMLP_FLAG_KV_E4M3", "TPMLP_ERR_BAD_PAGE",
     "tpmlp_attn_create", "tpmlp_attn_set_rope", "tpmlp_attn_set_scales", "tpmlp_attn_append",
-    "tpmlp_attn_decode", "tpmlp_attn_prompt",
+    "tpmlp_attn_decode", "tpmlp_attn_prompt", "tpmlp_attn_append_packed",
+    "tpmlp_attn_decode_packed", "tpmlp_attn_prompt_packed",
 ]
 
 TPMLP_OK = 0
@@ -132,6 +134,9 @@ def load_library() -> ctypes.CDLL:
                               ctypes.c_int),
         "tpmlp_attn_prompt": ([vp, vp, i64, i64, vp, vp, ctypes.c_float, i32, vp, i64, vp, vp],
                               ctypes.c_int),
+        "tpmlp_attn_append_packed": ([vp], ctypes.c_int),
+        "tpmlp_attn_decode_packed": ([vp], ctypes.c_int),
+        "tpmlp_attn_prompt_packed": ([vp], ctypes.c_int),
         "tpmlp_destroy": ([vp], None),
         "tpmlp_strerror": ([ctypes.c_int], ctypes.c_char_p),
         "tpmlp_last_error": ([vp], ctypes.c_char_p),
@@ -400,6 +405,21 @@ def tpmlp_attn_prompt(ctx: int, Q, ldq: int, T: int, cu_q, kv: KvCache, scale: f
     _check(load_library().tpmlp_attn_prompt(ctx, _ptr(Q), ldq, T, _ptr(cu_q), ctypes.byref(kv),
                                             scale, window, _ptr(Out), ldo, _ptr(Lse),
                                             _stream(stream)), "tpmlp_attn_prompt", ctx)
+
+
+def tpmlp_attn_append_packed(args: int) -> None:
+    """args: address of a tpmlp_append_args."""
+    _check(load_library().tpmlp_attn_append_packed(args), "tpmlp_attn_append_packed")
+
+
+def tpmlp_attn_decode_packed(args: int) -> None:
+    """args: address of a tpmlp_attend_args."""
+    _check(load_library().tpmlp_attn_decode_packed(args), "tpmlp_attn_decode_packed")
+
+
+def tpmlp_attn_prompt_packed(args: int) -> None:
+    """args: address of a tpmlp_attend_args."""
+    _check(load_library().tpmlp_attn_prompt_packed(args), "tpmlp_attn_prompt_packed")
 
 
 def tpmlp_destroy(ctx) -> None:
@@ -676,6 +696,11 @@ class Linear:
         return tpmlp_get_status(self.ctx, stream)
 
 
+# tpmlp_append_args and tpmlp_attend_args
+_APPEND = struct.Struct("@PPqPqPqqPPPPqP")
+_ATTEND = struct.Struct("@PPqqPPdqPqPP")
+
+
 class Attention:
     """Attention over a paged key-value cache for one head layout (tpmlp_attn_*): Hq query heads
     of size D (64 or 128), Hkv key-value heads, page_size keys per page, a cache in "bf16" or
@@ -698,6 +723,8 @@ class Attention:
         self._lib = load_library()
         self._wq, self._wk, self._scale = Hq * D, Hkv * D, D ** -0.5
         self._layout = (Hkv, D, page_size, kv_dtype)
+        self._args = ctypes.create_string_buffer(max(_APPEND.size, _ATTEND.size))
+        self._args_at = ctypes.addressof(self._args)
         self._Tensor, self._bf16 = torch.Tensor, torch.bfloat16
         self._int32, self._float32 = torch.int32, torch.float32
         self.ctx = tpmlp_attn_create(Hq, Hkv, D, page_size,
@@ -749,15 +776,19 @@ class Attention:
         return PagedCache(self, K, torch.empty_like(K), page_table, lens)
 
     # The checks below run on every call of a decode step, whose kernels take a few microseconds:
-    # each tensor's properties are read once, and the messages are made only on failure.
+    # each of a tensor's properties is read once, the messages are made only on failure, and the
+    # arguments go to the library in one structure (ctypes takes 0.2 us for each of its own).
     def _rows(self, t, rows, width, what):
         """Row pitch of a bf16 CUDA [rows, width] tensor whose rows are contiguous."""
         if not isinstance(t, self._Tensor) or not t.is_cuda:
             raise TypeError(f"{what} must be a CUDA tensor")
-        if t.dtype is not self._bf16 or t.shape != (rows, width) or t.stride(1) != 1:
-            raise ValueError(f"{what}: expected bf16 [{rows}, {width}] with contiguous rows, got "
-                             f"{t.dtype} {tuple(t.shape)} strides {t.stride()}")
-        return t.stride(0) if rows > 1 else width  # the stride of a single row says nothing
+        if t.dtype is not self._bf16 or t.shape != (rows, width):
+            raise ValueError(f"{what}: expected bf16 [{rows}, {width}], got {t.dtype} "
+                             f"{tuple(t.shape)}")
+        pitch, step = t.stride()
+        if step != 1:
+            raise ValueError(f"{what}: expected contiguous rows, got strides {t.stride()}")
+        return pitch if rows > 1 else width  # the stride of a single row says nothing
 
     def _ints(self, t, n, what):
         """Address of a contiguous int32 CUDA [n] tensor."""
@@ -774,11 +805,7 @@ class Attention:
         rotates in place; q None: only k and v). Rows may be column ranges of a wider tensor."""
         T = k.shape[0]
         ldk, ldv = self._rows(k, T, self._wk, "k"), self._rows(v, T, self._wk, "v")
-        pos = self._ints(pos, T, "pos")
-        if seq is not None:
-            seq = self._ints(seq, T, "seq")
-        qp = op = None
-        ldq = ldqo = 0
+        qp = op = ldq = ldqo = 0
         if q is not None:
             ldq = self._rows(q, T, self._wq, "q")
             if q_out is None:
@@ -787,8 +814,11 @@ class Attention:
             qp, op = q.data_ptr(), q_out.data_ptr()
         else:
             q_out = None
-        rc = self._lib.tpmlp_attn_append(self.ctx, qp, ldq, k.data_ptr(), ldk, v.data_ptr(), ldv,
-                                         T, pos, seq, cache._of(self), op, ldqo, _stream(stream))
+        _APPEND.pack_into(self._args, 0, self.ctx or 0, qp, ldq, k.data_ptr(), ldk, v.data_ptr(), ldv,
+                          T, self._ints(pos, T, "pos"),
+                          0 if seq is None else self._ints(seq, T, "seq"), cache._of(self), op,
+                          ldqo, _stream(stream) or 0)
+        rc = self._lib.tpmlp_attn_append_packed(self._args_at)
         if rc:
             _check(rc, "tpmlp_attn_append", self.ctx)
         return q_out
@@ -804,9 +834,10 @@ class Attention:
             out = q.new_empty((B, self._wq))
         ldo = self._rows(out, B, self._wq, "out")
         lse = q.new_empty((B, self.Hq), dtype=self._float32) if return_lse else None
-        rc = self._lib.tpmlp_attn_decode(
-            self.ctx, q.data_ptr(), ldq, kv, self._scale if scale is None else scale, window,
-            out.data_ptr(), ldo, lse.data_ptr() if return_lse else None, _stream(stream))
+        _ATTEND.pack_into(self._args, 0, self.ctx or 0, q.data_ptr(), ldq, 0, 0, kv,
+                          self._scale if scale is None else scale, window, out.data_ptr(), ldo,
+                          lse.data_ptr() if return_lse else 0, _stream(stream) or 0)
+        rc = self._lib.tpmlp_attn_decode_packed(self._args_at)
         if rc:
             _check(rc, "tpmlp_attn_decode", self.ctx)
         return (out, lse) if return_lse else out
@@ -822,9 +853,10 @@ class Attention:
             out = q.new_empty((T, self._wq))
         ldo = self._rows(out, T, self._wq, "out")
         lse = q.new_empty((T, self.Hq), dtype=self._float32) if return_lse else None
-        rc = self._lib.tpmlp_attn_prompt(
-            self.ctx, q.data_ptr(), ldq, T, cu, kv, self._scale if scale is None else scale,
-            window, out.data_ptr(), ldo, lse.data_ptr() if return_lse else None, _stream(stream))
+        _ATTEND.pack_into(self._args, 0, self.ctx or 0, q.data_ptr(), ldq, T, cu, kv,
+                          self._scale if scale is None else scale, window, out.data_ptr(), ldo,
+                          lse.data_ptr() if return_lse else 0, _stream(stream) or 0)
+        rc = self._lib.tpmlp_attn_prompt_packed(self._args_at)
         if rc:
             _check(rc, "tpmlp_attn_prompt", self.ctx)
         return (out, lse) if return_lse else out
@@ -871,9 +903,10 @@ class PagedCache:
         self._kv = KvCache(K.data_ptr(), V.data_ptr(), K.shape[0],
                            K.stride(0) if K.shape[0] > 1 else 0, page_table.data_ptr(),
                            page_table.stride(0) if B > 1 else 0, pages, B, lens.data_ptr())
-        self._ref = ctypes.byref(self._kv)
+        self._at = ctypes.addressof(self._kv)
 
-    def _of(self, attn: Attention):
+    def _of(self, attn: Attention) -> int:
+        """Address of the cache's tpmlp_kv."""
         if self._layout != attn._layout:
             raise ValueError("the cache was laid out for another head layout, page size or type")
-        return self._ref
+        return self._at

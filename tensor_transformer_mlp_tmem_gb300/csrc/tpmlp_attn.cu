@@ -381,6 +381,24 @@ int tpmlp_attn_prompt(tpmlp_ctx* c, const void* Q, int64_t ldq, int64_t T, const
     return run_prompt(c, a, cu_q, T, static_cast<cudaStream_t>(stream));
 }
 
+int tpmlp_attn_append_packed(const tpmlp_append_args* a) {
+    if (!a) return TPMLP_ERR_INVALID_ARG;
+    return tpmlp_attn_append(a->ctx, a->Q, a->ldq, a->K, a->ldk, a->V, a->ldv, a->T, a->pos, a->seq, a->kv, a->Qout,
+                             a->ldqo, a->stream);
+}
+
+int tpmlp_attn_decode_packed(const tpmlp_attend_args* a) {
+    if (!a || a->window > INT_MAX || a->window < INT_MIN) return TPMLP_ERR_INVALID_ARG;
+    return tpmlp_attn_decode(a->ctx, a->Q, a->ldq, a->kv, static_cast<float>(a->scale),
+                             static_cast<int32_t>(a->window), a->Out, a->ldo, a->Lse, a->stream);
+}
+
+int tpmlp_attn_prompt_packed(const tpmlp_attend_args* a) {
+    if (!a || a->window > INT_MAX || a->window < INT_MIN) return TPMLP_ERR_INVALID_ARG;
+    return tpmlp_attn_prompt(a->ctx, a->Q, a->ldq, a->T, a->cu_q, a->kv, static_cast<float>(a->scale),
+                             static_cast<int32_t>(a->window), a->Out, a->ldo, a->Lse, a->stream);
+}
+
 }  // extern "C"
 
 #ifdef TPMLP_TEST_HOOKS

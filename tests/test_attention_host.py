@@ -188,3 +188,39 @@ def test_rope_and_scales_arguments(hooks, ctx):
         assert hooks.tpmlp_attn_set_scales(e4m3, 16, None, None) == INV
     finally:
         hooks.tpmlp_destroy(e4m3)
+
+
+def test_packed_calls_check_alike(hooks, ctx):
+    """The one-structure forms take the fields in the header's order and give the same answers."""
+    import struct
+    append_args, attend_args = struct.Struct("@PPqPqPqqPPPPqP"), struct.Struct("@PPqqPPdqPqPP")
+    cache = kv()
+    at = ctypes.addressof(cache)
+
+    def packed(name, layout, *fields):
+        buf = ctypes.create_string_buffer(layout.pack(*fields))
+        fn = getattr(hooks, name)
+        fn.argtypes = [ctypes.c_void_p]
+        return fn(ctypes.addressof(buf))
+
+    for name in ("append", "decode", "prompt"):
+        fn = getattr(hooks, f"tpmlp_attn_{name}_packed")
+        fn.argtypes = [ctypes.c_void_p]
+        assert fn(None) == INV
+
+    def app(T=0, ldq=1536, pos=256, c=ctx, q=64):
+        return packed("tpmlp_attn_append_packed", append_args, c, q, ldq, 64, 1536, 64, 1536, T,
+                      pos, 0, at, 128, 1024, 0)
+
+    assert app() == OK and app(T=-1) == INV and app(T=1, pos=257) == MIS and app(c=0) == INV
+    assert app(T=3, ldq=1016) == INV and app(T=3, q=72) == MIS
+
+    def dec(window=0, scale=0.1, ldo=1024, kv_at=at, name="decode", T=5, cu=256):
+        return packed(f"tpmlp_attn_{name}_packed", attend_args, ctx, 64, 1024, T, cu, kv_at, scale,
+                      window, 128, ldo, 18, 0)  # the Lse address is misaligned: the last check
+
+    for name in ("decode", "prompt"):
+        assert dec(name=name) == MIS
+        assert dec(name=name, scale=0.0) == INV and dec(name=name, ldo=1016) == INV
+        assert dec(name=name, kv_at=0) == INV and dec(name=name, window=1 << 40) == INV
+    assert dec(name="prompt", T=0) == OK and dec(name="prompt", T=-1) == INV
