@@ -328,8 +328,8 @@ __device__ __forceinline__ RowRange row_range(const RowArgs& a, int b) {
 // and no copies are needed on the way: 16 warps an SM keep 128 KB of loads in flight, and the
 // bound is DRAM (64 sequences of 4096 keys x 32 heads in bf16: 6.6 TB/s, 97 % of a copy's rate).
 // Tried and slower by a fifth to a third: the same tiles copied to shared memory ahead of use
-// (cp.async; their reads then lie in every product's way), and loading the next tile's K and V
-// in registers while this one is in use (spills). A warp holds NT blocks of 8 query heads; NB
+// (cp.async), also for the wide head groups alone, and loading the next tile's K and V in
+// registers while this one is in use (spills). A warp holds NT blocks of 8 query heads; NB
 // warps take the same keys for more of them, and all but the first find the keys in L1. e4m3 values are converted to fp16 in registers (the 8-bit forms of these matrix
 // instructions take three times as long as the fp16 ones on this GPU).
 template <int D, bool FP8, int NB, int NT>
@@ -528,27 +528,32 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         for (int it = 0; it < n; ++it) {
             const int key0 = lo16 + ((step0 + it) * S::kParts + part_of) * S::KT;
             if (key0 >= range.hi) break;  // the warp's keys only grow
-            uint4 kr[S::kSub][2][S::NK];
-            uint4 vr[S::kSub][4][S::kVPieces];
+            int page[S::kSub];
             bool ok[S::kSub];
 #pragma unroll
             for (int u = 0; u < S::kSub; ++u) {
                 const int kb = key0 + 16 * u;
-                int64_t page = -1;
-                if (kb < range.hi) page = kv_page(a.kv, row, kb);
-                ok[u] = page >= 0;
-                const int64_t off = page * a.kv.page_bytes + head_off +
+                page[u] = -1;
+                if (kb < range.hi) page[u] = kv_page(a.kv, row, kb);
+                ok[u] = page[u] >= 0;
+            }
+            uint4 kr[S::kSub][2][S::NK];
+            uint4 vr[S::kSub][4][S::kVPieces];
+#pragma unroll
+            for (int u = 0; u < S::kSub; ++u) {
+                const int kb = key0 + 16 * u;
+                const int64_t off = page[u] * a.kv.page_bytes + head_off +
                                     static_cast<int64_t>(kb & ((1 << a.kv.page_shift) - 1)) * (D * S::kElem);
                 const uint8_t* kp = a.kv.K + off;
                 const uint8_t* vp = a.kv.V + off;
 #pragma unroll
-                for (int rr = 0; rr < 2; ++rr) {
-                    const int key = kb + g + 8 * rr;
+                for (int r = 0; r < 2; ++r) {
+                    const int key = kb + g + 8 * r;
                     const bool on = ok[u] && key >= range.lo && key < range.hi;
 #pragma unroll
                     for (int j = 0; j < S::NK; ++j)
-                        kr[u][rr][j] = on ? load_kv16<(NB > 1)>(kp + (g + 8 * rr) * (D * S::kElem) + 16 * (t + 4 * j))
-                                          : make_uint4(0, 0, 0, 0);
+                        kr[u][r][j] = on ? load_kv16<(NB > 1)>(kp + (g + 8 * r) * (D * S::kElem) + 16 * (t + 4 * j))
+                                         : make_uint4(0, 0, 0, 0);
                 }
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
@@ -557,8 +562,8 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
                     const bool on = ok[u] && key >= range.lo && key < range.hi;
                     const uint8_t* src = vp + kk * (D * S::kElem);
                     if constexpr (S::NV * S::kElem == 8) {
-                        const uint2 v = on ? __ldcg(reinterpret_cast<const uint2*>(src + 8 * g)) : make_uint2(0, 0);
-                        vr[u][x][0] = make_uint4(v.x, v.y, 0, 0);
+                        const uint2 w = on ? __ldcg(reinterpret_cast<const uint2*>(src + 8 * g)) : make_uint2(0, 0);
+                        vr[u][x][0] = make_uint4(w.x, w.y, 0, 0);
                     } else {
 #pragma unroll
                         for (int y = 0; y < S::kVPieces; ++y)
