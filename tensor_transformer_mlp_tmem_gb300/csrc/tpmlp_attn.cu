@@ -101,10 +101,10 @@ int allow_smem(tpmlp_ctx* c, Kernel kern, uint32_t smem, std::atomic<uint64_t>& 
     return TPMLP_OK;
 }
 
-template <int D, bool FP8, int NB, int NT>
+template <int D, bool FP8, int NT>
 int launch_rows(tpmlp_ctx* c, const tpmlp::RowArgs& a, cudaStream_t s) {
-    using S = tpmlp::RowShape<D, FP8, NB, NT>;
-    auto kern = tpmlp::attn_row_kernel<D, FP8, NB, NT>;
+    using S = tpmlp::RowShape<D, FP8, NT>;
+    auto kern = tpmlp::attn_row_kernel<D, FP8, NT>;
     static std::atomic<uint64_t> done{0};
     if (int rc = allow_smem(c, kern, S::kSmem, done)) return rc;
     const int grid = c->num_sms * S::kCtasPerSm;
@@ -112,19 +112,11 @@ int launch_rows(tpmlp_ctx* c, const tpmlp::RowArgs& a, cudaStream_t s) {
 }
 
 template <int D, bool FP8>
-int run_rows_of(tpmlp_ctx* c, tpmlp::RowArgs& a, cudaStream_t s) {
-    // A warp takes 8 or 16 query heads of a kv head, or two warps take 32 between them; more in
-    // turns. 16 to a warp (8 warps an SM with twice the registers) was 5 to 25 % faster than 8 to
-    // each of two warps over the same keys: 4096 keys x 64 sequences x 8 kv heads of 128, 12 query
-    // heads each, 220 against 232 us in bf16, 135 against 174 us in e4m3.
-    const int blocks = (a.G + 7) / 8;
-    a.blocks_per_head = (blocks + 3) / 4;
-    if (blocks == 1) return launch_rows<D, FP8, 1, 1>(c, a, s);
-    if (blocks == 2) return launch_rows<D, FP8, 1, 2>(c, a, s);
-    return launch_rows<D, FP8, 2, 2>(c, a, s);
+int run_rows_of(tpmlp_ctx* c, const tpmlp::RowArgs& a, cudaStream_t s) {
+    return a.G > 8 ? launch_rows<D, FP8, 2>(c, a, s) : launch_rows<D, FP8, 1>(c, a, s);
 }
 
-int run_rows(tpmlp_ctx* c, tpmlp::RowArgs& a, cudaStream_t s) {
+int run_rows(tpmlp_ctx* c, const tpmlp::RowArgs& a, cudaStream_t s) {
     if (c->head_dim == 128) return is_e4m3(c) ? run_rows_of<128, true>(c, a, s) : run_rows_of<128, false>(c, a, s);
     return is_e4m3(c) ? run_rows_of<64, true>(c, a, s) : run_rows_of<64, false>(c, a, s);
 }
@@ -364,6 +356,14 @@ int tpmlp_attn_decode(tpmlp_ctx* c, const void* Q, int64_t ldq, const tpmlp_kv* 
     if (int rc = check_attend(c, Q, ldq, kv, scale, Out, ldo, Lse)) return rc;
     tpmlp::RowArgs a = row_args(c, Q, ldq, kv, scale, window, Out, ldo, Lse);
     a.rows = kv->B;
+    // Wide head groups fill the tiles of the prompt kernel's products, which take the same time for
+    // any G; the row kernel's grows with every 8 heads. 64 sequences of 4096 keys, 8 kv heads, row
+    // kernel against prompt kernel, us: D = 128 in bf16, G = 8: 167, 188; 12: 220, 194; 16: 223, 189.
+    // In e4m3, G = 16: 139, 219. D = 64, G = 16: in bf16 114, 147; in e4m3 80, 173. With G = 24 the row
+    // kernel would take its keys twice: 388, 197 (D = 128) and 198, 161 (D = 64) in bf16, 238, 223
+    // and 153, 176 in e4m3; from G = 33 on three times and more.
+    if (a.G > 16 || (a.G > 8 && c->head_dim == 128 && !is_e4m3(c)))
+        return run_prompt(c, a, nullptr, kv->B, static_cast<cudaStream_t>(stream));
     return run_rows(c, a, static_cast<cudaStream_t>(stream));
 }
 

@@ -240,7 +240,6 @@ struct RowArgs {
     float* lse;             // [rows][Hq] or null
     int32_t rows;           // sequences
     int32_t Hq, G;
-    int32_t blocks_per_head;  // a CTA's blocks of query heads (RowShape::kRows) that share a kv head
     float scale_log2;         // softmax scale * log2(e)
     int32_t window;
     float* partial;         // [CTAs][2] slots of RowSlot floats
@@ -252,8 +251,8 @@ constexpr int kRowThreads = 32 * kRowWarps;
 // e4m3 caches: fp16 weights are raised by 2^10, so that the small ones of a long cache stay clear of
 // fp16's smallest steps; it cancels against the sum.
 constexpr float kRowRaise = 10.0f;
-// fp32 values of a partial sum: O [32][128], m [32], l [32].
-constexpr int kRowSlotFloats = 32 * 128 + 64;
+// fp32 values of a partial sum: O [16][128], m [16], l [16].
+constexpr int kRowSlotFloats = 16 * 128 + 32;
 
 __device__ __forceinline__ void mma_16816_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                                uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -304,11 +303,6 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
-template <bool L1>
-__device__ __forceinline__ uint4 load_kv16(const uint8_t* p) {
-    return L1 ? __ldca(reinterpret_cast<const uint4*>(p)) : __ldcg(reinterpret_cast<const uint4*>(p));
-}
-
 // Keys of a row: [lo, hi) of its sequence.
 struct RowRange {
     int lo, hi;
@@ -329,17 +323,16 @@ __device__ __forceinline__ RowRange row_range(const RowArgs& a, int b) {
 // bound is DRAM (64 sequences of 4096 keys x 32 heads in bf16: 6.6 TB/s, 97 % of a copy's rate).
 // Tried and slower by a fifth to a third: the same tiles copied to shared memory ahead of use
 // (cp.async), also for the wide head groups alone, and loading the next tile's K and V in
-// registers while this one is in use (spills). A warp holds NT blocks of 8 query heads; NB
-// warps take the same keys for more of them, and all but the first find the keys in L1. e4m3 values are converted to fp16 in registers (the 8-bit forms of these matrix
-// instructions take three times as long as the fp16 ones on this GPU).
-template <int D, bool FP8, int NB, int NT>
+// registers while this one is in use (spills). A warp holds NT = 1 or 2 blocks of
+// 8 query heads (2: one CTA an SM). e4m3 values are converted to fp16 in registers (the 8-bit forms
+// of these matrix instructions take three times as long as the fp16 ones on this GPU).
+template <int D, bool FP8, int NT>
 struct RowShape {
     static constexpr int kElem = FP8 ? 1 : 2;
     static constexpr int kSub = 256 / (D * kElem);   // subtiles of 16 keys
     static constexpr int KT = 16 * kSub;
-    static constexpr int kParts = kRowWarps / NB;    // warps that share out the keys
-    static constexpr int kStep = KT * kParts;        // keys of a CTA's step
-    static constexpr int kRows = 8 * NB * NT;        // query heads of a CTA
+    static constexpr int kStep = KT * kRowWarps;     // keys of a CTA's step
+    static constexpr int kRows = 8 * NT;             // query heads
     static constexpr int kCtasPerSm = NT == 1 ? 2 : 1;
     static constexpr int NK = D * kElem / 64;        // 16-byte pieces of a K row per thread
     static constexpr int NV = D / 8;                 // V dimensions per thread
@@ -356,20 +349,19 @@ __device__ __forceinline__ int v_dim(int g, int e) {
     else return (D / 8) * g + e;
 }
 
-template <int D, bool FP8, int NB, int NT>
-__global__ void __launch_bounds__(kRowThreads, RowShape<D, FP8, NB, NT>::kCtasPerSm)
+template <int D, bool FP8, int NT>
+__global__ void __launch_bounds__(kRowThreads, RowShape<D, FP8, NT>::kCtasPerSm)
 attn_row_kernel(const __grid_constant__ RowArgs a) {
-    using S = RowShape<D, FP8, NB, NT>;
+    using S = RowShape<D, FP8, NT>;
     extern __shared__ float smem[];
     float* const sO = smem;                                       // [parts][rows][pitch]
-    float* const sM = sO + S::kParts * S::kRows * S::kPitch;      // [parts][rows]
-    float* const sL = sM + S::kParts * S::kRows;                  // [parts][rows]
+    float* const sM = sO + kRowWarps * S::kRows * S::kPitch;      // [parts][rows]
+    float* const sL = sM + kRowWarps * S::kRows;                  // [parts][rows]
     __shared__ int64_t s_scan[kRowWarps + 1];
     __shared__ int64_t s_found[2];
     __shared__ uint32_t s_last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
-    const int part_of = warp / NB, block = warp % NB;  // the warp's share of the keys, its 8 query heads
 
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
@@ -377,10 +369,9 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
     auto steps_of = [&](const RowRange& x) {
         return max(1, (x.hi - (x.lo & ~15) + S::kStep - 1) / S::kStep);
     };
-    // Sum of the rows' steps: the work of every (row, kv head, block of query heads) segment is
-    // its row's steps, and each CTA takes an equal run of all segments' steps. Then the row that
+    // Sum of the rows' steps: the work of every (row, kv head) segment is its row's steps, and each CTA takes an equal run of all segments' steps. Then the row that
     // holds this CTA's first step.
-    const int64_t per_row = static_cast<int64_t>(a.kv.Hkv) * a.blocks_per_head;
+    const int64_t per_row = a.kv.Hkv;
     int64_t per_cta, at, end;
     int row = -1;
     int64_t row_start = 0;  // first step of that row
@@ -446,19 +437,16 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
     RowRange range = row_range(a, row);
     int steps = steps_of(range);
     int64_t segment_start;  // first step of the current segment
-    int part;               // kv head * blocks_per_head + block
+    int h;                  // kv head
     {
         const int64_t into = at - row_start;
-        part = static_cast<int>(into / steps);
-        segment_start = row_start + static_cast<int64_t>(part) * steps;
+        h = static_cast<int>(into / steps);
+        segment_start = row_start + static_cast<int64_t>(h) * steps;
     }
 
     while (at < end) {
         const int step0 = static_cast<int>(at - segment_start);
         const int n = static_cast<int>(min(static_cast<int64_t>(steps - step0), end - at));
-        const int h = part / a.blocks_per_head;
-        const int q0 = (part % a.blocks_per_head) * S::kRows;  // first query head of the block
-        const int valid = min(a.G - q0, S::kRows);
 
         // Q in the reduction order of the K pieces. In the 8-bit cache's fp16 products each row is
         // scaled by a power of two to a largest magnitude in [1, 2), so that no bf16 value
@@ -467,9 +455,9 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         float c_log2[NT][2];  // score -> log2 units, for the lane's query columns 2 t, 2 t + 1
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int qi = (block * NT + nt) * 8 + g;
-            const __nv_bfloat16* src = a.q + row * a.ldq + (static_cast<int64_t>(h) * a.G + q0 + qi) * D;
-            const bool on = qi < valid;
+            const int qi = nt * 8 + g;
+            const __nv_bfloat16* src = a.q + row * a.ldq + (static_cast<int64_t>(h) * a.G + qi) * D;
+            const bool on = qi < a.G;
             if constexpr (!FP8) {
 #pragma unroll
                 for (int j = 0; j < S::NK; ++j) {
@@ -526,7 +514,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         const int64_t head_off = h * a.kv.head_bytes;
         const int lo16 = range.lo & ~15;
         for (int it = 0; it < n; ++it) {
-            const int key0 = lo16 + ((step0 + it) * S::kParts + part_of) * S::KT;
+            const int key0 = lo16 + ((step0 + it) * kRowWarps + warp) * S::KT;
             if (key0 >= range.hi) break;  // the warp's keys only grow
             int page[S::kSub];
             bool ok[S::kSub];
@@ -552,7 +540,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
                     const bool on = ok[u] && key >= range.lo && key < range.hi;
 #pragma unroll
                     for (int j = 0; j < S::NK; ++j)
-                        kr[u][r][j] = on ? load_kv16<(NB > 1)>(kp + (g + 8 * r) * (D * S::kElem) + 16 * (t + 4 * j))
+                        kr[u][r][j] = on ? load16(kp + (g + 8 * r) * (D * S::kElem) + 16 * (t + 4 * j))
                                          : make_uint4(0, 0, 0, 0);
                 }
 #pragma unroll
@@ -567,7 +555,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
                     } else {
 #pragma unroll
                         for (int y = 0; y < S::kVPieces; ++y)
-                            vr[u][x][y] = on ? load_kv16<(NB > 1)>(src + 128 * y + 16 * g) : make_uint4(0, 0, 0, 0);
+                            vr[u][x][y] = on ? load16(src + 128 * y + 16 * g) : make_uint4(0, 0, 0, 0);
                     }
                 }
             }
@@ -710,7 +698,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int r = part_of * S::kRows + (block * NT + nt) * 8 + 2 * t + i;
+                const int r = warp * S::kRows + nt * 8 + 2 * t + i;
                 if (g == 0) {
                     sM[r] = m[nt][i];
                     sL[r] = l[nt][i];
@@ -733,7 +721,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         const float v_scale = FP8 ? a.kv.scales[a.kv.Hkv + h] : 1.0f;
 
         auto finish = [&](int r, int d, float4 v, float mm, float ll) {
-            const int64_t head = static_cast<int64_t>(h) * a.G + q0 + r;
+            const int64_t head = static_cast<int64_t>(h) * a.G + r;
             const float inv = ll == 0.0f ? 0.0f : v_scale / ll;  // no keys: zeros
             uint2 w;
             w.x = pack_bf162(v.x * inv, v.y * inv);
@@ -744,16 +732,16 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
                     ll == 0.0f ? -CUDART_INF_F
                                : (mm + log2f(ll) - (FP8 ? kRowRaise : 0.0f)) * 0.69314718055994531f;
         };
-        for (int i = tid; i < valid * (D / 4); i += kRowThreads) {
+        for (int i = tid; i < a.G * (D / 4); i += kRowThreads) {
             const int r = i / (D / 4), d = (i % (D / 4)) * 4;
             float mm = -CUDART_INF_F;
 #pragma unroll
-            for (int w = 0; w < S::kParts; ++w) mm = fmaxf(mm, sM[w * S::kRows + r]);
+            for (int w = 0; w < kRowWarps; ++w) mm = fmaxf(mm, sM[w * S::kRows + r]);
             const float safe = mm == -CUDART_INF_F ? 0.0f : mm;
             float ll = 0.0f;
             float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-            for (int w = 0; w < S::kParts; ++w) {
+            for (int w = 0; w < kRowWarps; ++w) {
                 const float f = exp2_approx(sM[w * S::kRows + r] - safe);
                 const float4 x = *reinterpret_cast<const float4*>(sO + (w * S::kRows + r) * S::kPitch + d);
                 ll += f * sL[w * S::kRows + r];
@@ -767,8 +755,8 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
             } else {
                 __stcg(reinterpret_cast<float4*>(slot + r * D + d), v);
                 if (d == 0) {
-                    __stcg(slot + 32 * 128 + r, mm);
-                    __stcg(slot + 32 * 128 + 32 + r, ll);
+                    __stcg(slot + 16 * 128 + r, mm);
+                    __stcg(slot + 16 * 128 + 16 + r, ll);
                 }
             }
         }
@@ -782,21 +770,21 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
             if (s_last) {
                 __threadfence();
                 if (tid == 0) a.count[first] = 0;
-                for (int i = tid; i < valid * (D / 4); i += kRowThreads) {
+                for (int i = tid; i < a.G * (D / 4); i += kRowThreads) {
                     const int r = i / (D / 4), d = (i % (D / 4)) * 4;
                     float mm = -CUDART_INF_F;
                     for (int c = first; c <= last; ++c)
                         mm = fmaxf(mm, __ldcg(a.partial + (static_cast<int64_t>(c) * 2 + (c == first)) * kRowSlotFloats +
-                                              32 * 128 + r));
+                                              16 * 128 + r));
                     const float safe = mm == -CUDART_INF_F ? 0.0f : mm;
                     float ll = 0.0f;
                     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
                     for (int c = first; c <= last; ++c) {
                         const float* p = a.partial + (static_cast<int64_t>(c) * 2 + (c == first)) * kRowSlotFloats;
-                        const float f = exp2_approx(__ldcg(p + 32 * 128 + r) - safe);
+                        const float f = exp2_approx(__ldcg(p + 16 * 128 + r) - safe);
                         const float4 x = __ldcg(reinterpret_cast<const float4*>(p + r * D + d));
-                        ll += f * __ldcg(p + 32 * 128 + 32 + r);
+                        ll += f * __ldcg(p + 16 * 128 + 16 + r);
                         v.x += f * x.x;
                         v.y += f * x.y;
                         v.z += f * x.z;
@@ -810,8 +798,8 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         // the next segment
         at += n;
         segment_start += steps;
-        if (++part == static_cast<int>(per_row)) {
-            part = 0;
+        if (++h == a.kv.Hkv) {
+            h = 0;
             if (++row < a.rows) {
                 range = row_range(a, row);
                 steps = steps_of(range);

@@ -41,7 +41,7 @@ struct PromptArgs {
     __nv_bfloat16* out;
     int64_t ldo;
     float* lse;
-    const int32_t* cu_q;
+    const int32_t* cu_q;  // null: one token of each sequence (T = B)
     int32_t T, Hq, G, tpt;  // tpt: tokens per tile
     float scale_log2;
     int32_t window;
@@ -173,8 +173,8 @@ struct PromptSeq {
 };
 __device__ __forceinline__ PromptSeq prompt_seq(const PromptArgs& a, int b) {
     PromptSeq s;
-    s.first = max(0, min(a.cu_q[b], a.T));
-    s.n = max(0, min(a.cu_q[b + 1], a.T) - s.first);
+    s.first = a.cu_q ? max(0, min(a.cu_q[b], a.T)) : b;
+    s.n = a.cu_q ? max(0, min(a.cu_q[b + 1], a.T) - s.first) : 1;
     s.len = kv_length(a.kv, b);
     return s;
 }

@@ -227,6 +227,33 @@ def test_decode_reads_lengths_on_replay_and_other_streams(lib):
         assert torch.equal(got, out)
 
 
+WIDE = [  # more than 8 query heads to a kv head
+    (24, 2, 128, 16, [1, 40, 333, 0], 33),
+    (40, 2, 64, 64, [129, 0, 1, 700, 65], 0),
+    (17, 1, 128, 32, [20, 2000], 129),
+    (128, 1, 64, 128, [300, 5], 0),          # the widest group
+    (10, 1, 64, 16, [100, 17], 16),
+]
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Hq,Hkv,D,page,lens,window", WIDE)
+def test_decode_wide_groups(lib, kv, Hq, Hkv, D, page, lens, window):
+    test_decode_matches_definition(lib, kv, Hq, Hkv, D, page, lens, window)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_decode_wide_groups_many_and_long(lib, kv):
+    lens = [(7 * b) % 41 for b in range(600)]
+    lens[77] = 9000
+    c = ref.make(1, 64, 16, kv, lens, seed=14)
+    q = queries(600, 20, 64, 14)
+    with tp.Attention(20, 1, 64, 16, kv_dtype=kv) as attn:
+        got, lse = attn.decode(q.cuda(), on_device(c, attn), return_lse=True)
+        ok(attn)
+    check_rows(c, q, got, lse, [(b, b, 0, n) for b, n in enumerate(lens)], 20, 64, 0.125)
+
+
 # ------------------------------------------------------------------ prompt
 def prompt_spans(lens, new, window):
     spans, r = [], 0
