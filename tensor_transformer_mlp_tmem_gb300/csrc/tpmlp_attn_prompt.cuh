@@ -12,7 +12,7 @@
 //
 // Warps: 0-3 softmax of tile 0, 4-7 of tile 1 (a warp may read the 32 tensor-memory lanes of its
 // rank mod 4), 8 and 10 issue the MMAs of tile 0 and 1, 9 loads K and V (and Q) by TMA, page by
-// page, 11 makes the work list; e4m3 caches: 12-15 convert the loaded bytes to fp16. One warp
+// page, 11 makes the work list; e4m3 caches: 12-19 convert the loaded bytes to fp16. One warp
 // per tile issues MMAs because each waits for four barriers a block: with one warp for both
 // tiles the tensor core idled during those waits (GPT-3-shaped prompt: 516 us against MEASURE2).
 #pragma once
@@ -63,7 +63,7 @@ struct PromptSmem {
     static constexpr uint32_t kTables = kStore0 + 8 * 2048;  // 2 KB of output staging per softmax warp
     static constexpr uint32_t kTotal = 1024 + kTables + (kCoarse + 1) * 8 + (kPromptItems + 1) * 4 + 256;
     static_assert(kTotal <= 232448, "dynamic shared memory per CTA");
-    static constexpr int kThreads = FP8 ? 512 : 384;
+    static constexpr int kThreads = FP8 ? 640 : 384;
 };
 
 // D[tmem] (+)= A[tmem] * B[smem]: the 16-bit A operand lies in tensor memory, two values to a
@@ -352,12 +352,12 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NST; ++s) {
-            ptx::mbar_init(full(s), FP8 ? 4 : 1);
+            ptx::mbar_init(full(s), FP8 ? 8 : 1);
             ptx::mbar_init(empty(s), 2);
         }
         for (int s = 0; s < NRAW; ++s) {
             ptx::mbar_init(raw_full(s), 1);
-            ptx::mbar_init(raw_empty(s), 4);
+            ptx::mbar_init(raw_empty(s), 8);
         }
         for (int t = 0; t < 2; ++t) {
             ptx::mbar_init(q_full(t), FP8 ? 4 : 1);
@@ -373,7 +373,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         }
         for (int s = 0; s < kPieces; ++s) {
             ptx::mbar_init(piece_full(s), 1);
-            ptx::mbar_init(piece_empty(s), FP8 ? 15 : 11);
+            ptx::mbar_init(piece_empty(s), FP8 ? 19 : 11);
         }
         ptx::mbar_init(q_empty, 2);
         ptx::mbar_init(drain, 2);
@@ -494,9 +494,9 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         return __all_sync(~0u, done || ptx::mbar_wait(bar, parity, abort_flag, a.kv.status, kPromptCode | role));
     };
 
-    // The register split sums to what the block was launched with (384 x 168, 512 x 128).
-    if (warp < 8) regs_up<FP8 ? 160 : 184>();
-    else regs_down<FP8 ? 96 : 136>();
+    // The register split sums to what the block was launched with (384 x 168, 640 x 96).
+    if (warp < 8) regs_up<FP8 ? 144 : 184>();
+    else regs_down<FP8 ? 64 : 136>();
 
     // The pieces, in the order that every role goes through them. next_piece() waits for one (null:
     // no more, or a wait gave up); release_piece() hands its slot back.
@@ -1025,22 +1025,22 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 if (!(ok = wait(empty(stage), phase ^ 1u, 12))) break;
                 const uint8_t* src = base_ptr + L::kRaw0 + rs * L::kRaw;
                 uint8_t* dst = base_ptr + L::kStage0 + stage * L::kTile;
-                constexpr int kParts = kPB * D / 16 / 128;  // 16-byte parts per thread
-#pragma unroll 4
-                for (int x = 0; x < kParts; ++x) {
-                    const int part = x * 128 + tid;
-                    const int r = part / (D / 16), j = part % (D / 16);
-                    const uint4 v = *reinterpret_cast<const uint4*>(src + part * 16);
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t h[8];
+                constexpr int kParts = kPB * D / 16 / 256;  // 16-byte parts per thread
+                uint4 v[kParts];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        e4m3x4_to_half2(w[k], h[2 * k], h[2 * k + 1]);
-                    }
+                for (int x = 0; x < kParts; ++x) v[x] = *reinterpret_cast<const uint4*>(src + (x * 256 + tid) * 16);
+#pragma unroll
+                for (int x = 0; x < kParts; ++x) {
+                    const int part = x * 256 + tid;
+                    const int r = part / (D / 16), j = part % (D / 16);
+                    uint4 lo, hi;
+                    e4m3x4_to_half2(v[x].x, lo.x, lo.y);
+                    e4m3x4_to_half2(v[x].y, lo.z, lo.w);
+                    e4m3x4_to_half2(v[x].z, hi.x, hi.y);
+                    e4m3x4_to_half2(v[x].w, hi.z, hi.w);
                     // the two 16-byte chunks in an order that spreads a row's writes over all banks
                     uint8_t* const d = dst + (j >> 2) * kHalf + r * 128;
                     const int c0 = 2 * (j & 3), swap = (j >> 2) & 1;
-                    const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
                     *reinterpret_cast<uint4*>(d + (((c0 + swap) ^ (r & 7)) << 4)) = swap ? hi : lo;
                     *reinterpret_cast<uint4*>(d + (((c0 + 1 - swap) ^ (r & 7)) << 4)) = swap ? lo : hi;
                 }
