@@ -520,7 +520,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         const int t = warp >> 2;
         const int row = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        uint32_t s_phase[2] = {0, 0}, o_phase = 0, q_phase = 0, j_phase = 0, blocks = 0;
+        uint32_t s_phase = 0, o_phase = 0, q_phase = 0, j_phase = 0, blocks = 0;
         uint32_t pv_count = 0;  // products P V of this tile so far
         const int token = row / a.G, head = row - token * a.G;
         while (const Piece* p = next_piece()) {
@@ -573,9 +573,9 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             bool ok = true;
             for (int j = begin; j < end; ++j) {
                 const int buf = j & 1;
-                if (!(ok = wait(s_full(t, buf), buf ? s_phase[1] : s_phase[0], 2))) break;
-                if (buf) s_phase[1] ^= 1u;
-                else s_phase[0] ^= 1u;
+                if (!(ok = wait(s_full(t, buf), (s_phase >> buf) & 1u, 2))) break;
+                s_phase ^= 1u << buf;
+                const uint32_t have = (groups[(block0 + (j >> 1)) & 7] >> (4 * buf)) & 0xFu;
                 ptx::tc_fence_after();
                 const uint32_t ts = tmem_s(t) + lanes + kSB * buf;
                 uint32_t s[kSB];
@@ -584,7 +584,6 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 ptx::tmem_wait_ld(*reinterpret_cast<uint32_t(*)[32]>(s));
                 ptx::tmem_wait_ld(*reinterpret_cast<uint32_t(*)[32]>(s + 32));
                 const int key0 = j * kSB;
-                const uint32_t have = (groups[(block0 + (j >> 1)) & 7] >> (4 * buf)) & 0xFu;
                 if (last_lo > key0 || have != 0xFu) {
                     const int below = hi - key0, from = lo - key0;
 #pragma unroll
@@ -608,7 +607,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 }
                 const float now = fmaxf(max3(top[0], top[1], top[2]), top[3]) * c;
                 float f = 1.0f;
-                if (now > m + kLazyLog2 || (m == -CUDART_INF_F && now != m)) {
+                if (now > m + kLazyLog2) {
                     f = exp2_approx(m - now);
                     m = now;
                     l *= f;
