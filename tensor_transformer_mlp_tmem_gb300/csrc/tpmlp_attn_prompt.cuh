@@ -606,25 +606,25 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     top[x] = fmaxf(top[x], __uint_as_float(s[kSB - 4 + x]));
                 }
                 const float now = fmaxf(max3(top[0], top[1], top[2]), top[3]) * c;
-                float f = 1.0f;
-                if (now > m + kLazyLog2) {
-                    f = exp2_approx(m - now);
-                    m = now;
+                const bool move = now > m + kLazyLog2;
+                if (__any_sync(~0u, move)) {
+                    const float f = move ? exp2_approx(m - now) : 1.0f;
+                    if (move) m = now;
                     l *= f;
-                }
-                // the reference moved: O of the steps before is scaled, once the last of their
-                // products (of the other buffer) is done
-                if (j > begin && __any_sync(~0u, f != 1.0f)) {
-                    if (!(ok = wait(pv_done(t), (pv_count - 1) & 1u, 17))) break;
-                    ptx::tc_fence_after();
+                    // O of the steps before is scaled, once the last of their products (of the
+                    // other buffer) is done
+                    if (j > begin) {
+                        if (!(ok = wait(pv_done(t), (pv_count - 1) & 1u, 17))) break;
+                        ptx::tc_fence_after();
 #pragma unroll 1
-                    for (int x = 0; x < D; x += 32) {
-                        uint32_t o[32];
-                        ptx::tmem_ld_32x32b_x32(tmem_o(t) + lanes + x, o);
-                        ptx::tmem_wait_ld(o);
+                        for (int x = 0; x < D; x += 32) {
+                            uint32_t o[32];
+                            ptx::tmem_ld_32x32b_x32(tmem_o(t) + lanes + x, o);
+                            ptx::tmem_wait_ld(o);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                        tmem_st_x32(tmem_o(t) + lanes + x, o);
+                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                            tmem_st_x32(tmem_o(t) + lanes + x, o);
+                        }
                     }
                 }
                 ++pv_count;
@@ -650,12 +650,6 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             }
             if (!ok) break;
             // -------------------------------------------------------- the tile's result
-            const bool any = end > begin;
-            if (any) {
-                if (!wait(o_full(t), o_phase, 3)) break;
-                o_phase ^= 1u;
-                ptx::tc_fence_after();
-            }
             const int64_t qrow = p->seq.first + tok;
             const int64_t qhead = static_cast<int64_t>(p->h) * a.G + head;
             const int from = p->first, upto = p->last;
@@ -665,6 +659,11 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             const float v_scale = FP8 ? a.kv.scales[a.kv.Hkv + p->h] : 1.0f;
             __nv_bfloat16* const dst = mine ? a.out + qrow * a.ldo + qhead * D : nullptr;
             uint8_t* const stage = base_ptr + L::kStore0 + warp * 2048;
+            __nv_bfloat16* rows_to[4];  // rows 8k + lane / 4, from their lanes
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                rows_to[k] = reinterpret_cast<__nv_bfloat16*>(
+                    __shfl_sync(~0u, reinterpret_cast<unsigned long long>(dst), 8 * k + (lane >> 2)));
             // 32 columns of the warp's 32 rows: through shared memory, so that four lanes write 64
             // contiguous bytes of a row
             auto put = [&](int col, const float* v, float inv) {
@@ -680,10 +679,8 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int r = 8 * k + (lane >> 2), x = lane & 3;
-                    __nv_bfloat16* const to = reinterpret_cast<__nv_bfloat16*>(
-                        __shfl_sync(~0u, reinterpret_cast<unsigned long long>(dst), r));
                     const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 64 + ((x ^ ((r >> 1) & 3)) << 4));
-                    if (to) *reinterpret_cast<uint4*>(to + col + 8 * x) = w;
+                    if (rows_to[k]) *reinterpret_cast<uint4*>(rows_to[k] + col + 8 * x) = w;
                 }
             };
             auto put_lse = [&](float mm, float ll) {
@@ -693,33 +690,44 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                                    : (mm + log2f(ll) - (FP8 ? kRaiseLog2 : 0.0f)) * 0.69314718055994531f;
             };
             const float inv = l == 0.0f ? 0.0f : v_scale / l;  // no keys: zeros
+            const bool any = end > begin;
+            if (any) {
+                if (!wait(o_full(t), o_phase, 3)) break;
+                o_phase ^= 1u;
+                ptx::tc_fence_after();
+            }
             if (p->tokens[t] > 0) {
 #pragma unroll 1
-                for (int col = 0; col < D; col += 32) {
-                    uint32_t o[32];
+                for (int col = 0; col < D; col += 64) {
+                    uint32_t o[2][32];
                     if (any) {
-                        ptx::tmem_ld_32x32b_x32(tmem_o(t) + lanes + col, o);
-                        ptx::tmem_wait_ld(o);
-                        if (col + 32 == D) {
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) ptx::tmem_ld_32x32b_x32(tmem_o(t) + lanes + col + 32 * x, o[x]);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) ptx::tmem_wait_ld(o[x]);
+                        if (col + 64 == D) {
                             ptx::tc_fence_before();
                             __syncwarp();
                             if (lane == 0) mbar_arrive(o_empty(t));
                         }
                     } else {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = 0u;
+                        for (int k = 0; k < 32; ++k) o[0][k] = o[1][k] = 0u;
                     }
-                    if (whole) {
-                        float v[32];
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) v[k] = l == 0.0f ? 0.0f : __uint_as_float(o[k]);
-                        put(col, v, inv);
-                    } else if (mine) {
+                    for (int x = 0; x < 2; ++x) {
+                        if (whole) {
+                            float v[32];
 #pragma unroll
-                        for (int k = 0; k < 32; k += 4)
-                            __stcg(reinterpret_cast<float4*>(slot + (col + k) * 128 + row * 4),
-                                   make_float4(__uint_as_float(o[k]), __uint_as_float(o[k + 1]),
-                                               __uint_as_float(o[k + 2]), __uint_as_float(o[k + 3])));
+                            for (int k = 0; k < 32; ++k) v[k] = l == 0.0f ? 0.0f : __uint_as_float(o[x][k]);
+                            put(col + 32 * x, v, inv);
+                        } else if (mine) {
+#pragma unroll
+                            for (int k = 0; k < 32; k += 4)
+                                __stcg(reinterpret_cast<float4*>(slot + (col + 32 * x + k) * 128 + row * 4),
+                                       make_float4(__uint_as_float(o[x][k]), __uint_as_float(o[x][k + 1]),
+                                                   __uint_as_float(o[x][k + 2]), __uint_as_float(o[x][k + 3])));
+                        }
                     }
                 }
             }
