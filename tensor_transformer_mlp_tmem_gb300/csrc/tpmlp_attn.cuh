@@ -48,13 +48,20 @@ __device__ __forceinline__ int kv_length(const KvView& kv, int b) {
     return max(len, 0);
 }
 
-// The page that holds key `key` (inside the table) of sequence b; -1, reported, if the table
-// names none of the pool's.
-__device__ __forceinline__ int kv_page(const KvView& kv, int b, int key) {
-    const int p = kv.table[b * kv.table_stride + (key >> kv.page_shift)];
+// The table's entry for key `key` (inside the table) of sequence b.
+__device__ __forceinline__ int kv_entry(const KvView& kv, int b, int key) {
+    return kv.table[b * kv.table_stride + (key >> kv.page_shift)];
+}
+
+// A table entry as a page of the pool; -1, reported, if it names none.
+__device__ __forceinline__ int kv_checked(const KvView& kv, int p) {
     if (p >= 0 && p < kv.num_pages) return p;
     report_bad_page(kv.status);
     return -1;
+}
+
+__device__ __forceinline__ int kv_page(const KvView& kv, int b, int key) {
+    return kv_checked(kv, kv_entry(kv, b, key));
 }
 
 // ------------------------------------------------------------------ append

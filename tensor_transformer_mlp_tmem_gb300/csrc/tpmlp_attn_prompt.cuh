@@ -940,10 +940,18 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 }
                 ++q_loads;
             }
+            // the table's entry for this lane's copy of a block, looked up a block ahead
+            auto entry = [&](int i) {
+                const int key = i * kPB + lane * rows;
+                return lane < copies && key < top && i < b1 ? kv_entry(a.kv, b, key) : 0;
+            };
+            int next = entry(b0);
             for (int i = b0; ok && i < b1; ++i) {
                 const int key = i * kPB + lane * rows;
                 const bool in = lane < copies && key < top;
-                const int64_t page = in ? kv_page(a.kv, b, key) : -1;
+                const int found_page = next;
+                next = entry(i + 1);
+                const int64_t page = in ? kv_checked(a.kv, found_page) : -1;
                 const uint32_t there = __ballot_sync(~0u, page >= 0);
                 // groups of 16 keys that are there; those past the item's keys count as such
                 uint32_t have = 0xFFu;
