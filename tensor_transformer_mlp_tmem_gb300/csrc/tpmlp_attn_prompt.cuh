@@ -224,8 +224,9 @@ __device__ __forceinline__ void item_blocks(const PromptArgs& a, Piece& p) {
 }
 
 // The CTA's work list. Items are numbered sequence by sequence; within a sequence in groups of
-// kv heads that together fill the GPU, so that the heads in flight keep their K and V in L2, and
-// within a group from the last tokens (most keys) to the first.
+// kv heads, so that the heads in flight keep their K and V in L2, and within a group from the last
+// tokens (most keys) to the first. A group has two items or more for each CTA: with one, a last
+// group's largest items were started when little else was left (GPT-3-shaped prompt: 326 us).
 struct PromptWork {
     const int64_t* coarse;  // items before each run of `run` sequences
     const int* units;       // blocks before each item (split lists)
@@ -254,7 +255,9 @@ struct PromptWork {
             nt = tiles(a, s);
         }
         nt = max(nt, 1);
-        const int group = max(1, (static_cast<int>(gridDim.x) + nt - 1) / nt);
+        const int groups = max(1, static_cast<int>(min(static_cast<int64_t>(nt) * a.kv.Hkv / (2 * gridDim.x),
+                                                       static_cast<int64_t>(a.kv.Hkv))));
+        const int group = (a.kv.Hkv + groups - 1) / groups;
         const int64_t per_group = static_cast<int64_t>(nt) * group;
         const int h0 = static_cast<int>(r / per_group) * group;
         const int j = static_cast<int>(r % per_group);
@@ -1008,8 +1011,9 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     } else if (warp == 11) {
         // ------------------------------------------------------------ work list
         for (;; ++piece_at) {
-            const Piece p = work.next(a);
+            // (an item is asked for only when there is room for it)
             if (!wait(piece_empty(piece_at % kPieces), ((piece_at / kPieces) & 1u) ^ 1u, 16)) break;
+            const Piece p = work.next(a);
             if (lane == 0) {
                 *const_cast<Piece*>(piece_of(piece_at)) = p;
                 mbar_arrive(piece_full(piece_at % kPieces));
