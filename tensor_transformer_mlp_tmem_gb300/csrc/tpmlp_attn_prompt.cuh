@@ -229,11 +229,11 @@ __device__ __forceinline__ void item_blocks(const PromptArgs& a, Piece& p) {
 // group's largest items were started when little else was left (GPT-3-shaped prompt: 326 us).
 struct PromptWork {
     const int64_t* coarse;  // items before each run of `run` sequences
-    const int* units;       // blocks before each item (split lists)
+    const int* units;       // work before each item (split lists)
     int runs, run;          // entries of coarse, sequences per entry
     int64_t items;
-    bool split;             // equal runs of blocks instead of whole items
-    int64_t at, end, per;   // split: this CTA's run of blocks, the length of every run
+    bool split;             // equal runs of work instead of whole items
+    int64_t at, end, per;   // split: this CTA's run of work, the length of every run
 
     __device__ __forceinline__ static int tiles(const PromptArgs& a, const PromptSeq& s) {
         return (s.n + 2 * a.tpt - 1) / (2 * a.tpt);
@@ -284,26 +284,29 @@ struct PromptWork {
             p.starts = 1;
             return p;
         }
-        if (at >= end) return p;
-        int lo = 0, hi = static_cast<int>(items);
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (units[mid] <= at) lo = mid;
-            else hi = mid;
+        while (at < end) {
+            int lo = 0, hi = static_cast<int>(items);
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (units[mid] <= at) lo = mid;
+                else hi = mid;
+            }
+            // an item's units: one for its start, then its blocks
+            const int u0 = units[lo], u1 = units[lo + 1];
+            const int from = max(static_cast<int>(at) - u0 - 1, 0);
+            at = min(end, static_cast<int64_t>(u1));
+            const int upto = static_cast<int>(at) - u0 - 1;
+            if (upto == 0 && u1 > u0 + 1) continue;  // the start alone: its blocks are the next CTA's
+            item(a, lo, p);
+            p.valid = 1;
+            p.first = (u0 + (u1 > u0 + 1)) / static_cast<int>(per);
+            p.last = (u1 - 1) / static_cast<int>(per);
+            p.starts = from == 0;
+            const int base = p.b0;
+            p.b0 = base + from;
+            p.b1 = base + upto;
+            return p;
         }
-        item(a, lo, p);
-        p.valid = 1;
-        const int u0 = units[lo], u1 = units[lo + 1];
-        p.first = u0 / static_cast<int>(per);
-        p.last = (u1 - 1) / static_cast<int>(per);
-        p.starts = at == u0;
-        const int64_t stop = min(end, static_cast<int64_t>(u1));
-        const int base = p.b0;
-        if (p.b1 > p.b0) {
-            p.b0 = base + static_cast<int>(at - u0);
-            p.b1 = base + static_cast<int>(stop - u0);
-        }
-        at = stop;
         return p;
     }
 };
@@ -434,15 +437,18 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     work.at = work.end = 0;
     work.per = 1;
     if (work.items <= kPromptItems) {
-        // Few items: tabulate their blocks, and split the blocks evenly where the longest item,
-        // or the last round's, would keep the GPU waiting for more than a join costs (about
-        // kJoinBlocks blocks of time).
-        constexpr int kJoinBlocks = 8;
+        // Few items: tabulate their work (a block of time each for an item's start and its
+        // result, and its blocks), and split it evenly where the longest item, or about half of
+        // it in the last round, would keep the GPU waiting for more than a tenth over what the
+        // split's partial sums and joins cost (kJoinBlocks blocks of time, about 25 us). Whole items
+        // against a split, us: 4096 tokens of 32 heads 107, 122; 2048 of 32 heads with 8 kv heads
+        // 45, 50; 256 of them on 8192 keys 99, 50; two chunks of 1000 on 24000 e4m3 keys 786, 700.
+        constexpr int kJoinBlocks = 16;
         const int n = static_cast<int>(work.items);
         for (int i = threadIdx.x; i < n; i += L::kThreads) {
             Piece p;
             work.item(a, i, p);
-            units[i] = max(1, p.b1 - p.b0);
+            units[i] = 1 + p.b1 - p.b0;
         }
         __syncthreads();
         if (warp == 0) {
@@ -476,7 +482,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         const int g = static_cast<int>(gridDim.x);
         const int share = max((total + g - 1) / g, 1);
         const int whole = n <= g ? most : share + most / 2;
-        if (whole > share + kJoinBlocks) {
+        if (10 * whole > 11 * (share + kJoinBlocks)) {
             work.split = true;
             work.per = share;
             work.at = static_cast<int64_t>(share) * blockIdx.x;
@@ -775,26 +781,30 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                                   __ldcg(slot_of(x) + 128 * 128 + 128 + row);
                     const float scale = ll == 0.0f ? 0.0f : v_scale / ll;
 #pragma unroll 1
-                    for (int col = 0; col < D; col += 32) {
-                        float v[32];
+                    for (int col = 0; col < D; col += 64) {
+                        float v[64];
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) v[k] = 0.0f;
+                        for (int k = 0; k < 64; ++k) v[k] = 0.0f;
                         if (mine) {
 #pragma unroll 1
                             for (int x = from; x <= upto; ++x) {
                                 const float* src = slot_of(x);
+                                float4 y[16];
+#pragma unroll
+                                for (int k = 0; k < 16; ++k)
+                                    y[k] = __ldcg(reinterpret_cast<const float4*>(src + (col + 4 * k) * 128 + row * 4));
                                 const float w = exp2_approx(__ldcg(src + 128 * 128 + row) - safe);
 #pragma unroll
-                                for (int k = 0; k < 32; k += 4) {
-                                    const float4 y = __ldcg(reinterpret_cast<const float4*>(src + (col + k) * 128 + row * 4));
-                                    v[k] += w * y.x;
-                                    v[k + 1] += w * y.y;
-                                    v[k + 2] += w * y.z;
-                                    v[k + 3] += w * y.w;
+                                for (int k = 0; k < 16; ++k) {
+                                    v[4 * k] += w * y[k].x;
+                                    v[4 * k + 1] += w * y[k].y;
+                                    v[4 * k + 2] += w * y[k].z;
+                                    v[4 * k + 3] += w * y[k].w;
                                 }
                             }
                         }
                         put(col, v, scale);
+                        put(col + 32, v + 32, scale);
                     }
                     put_lse(mm, ll);
                 }
