@@ -376,12 +376,13 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
     auto steps_of = [&](const RowRange& x) {
         return max(1, (x.hi - (x.lo & ~15) + S::kStep - 1) / S::kStep);
     };
-    // Sum of the rows' steps: the work of every (row, kv head) segment is its row's steps, and each CTA takes an equal run of all segments' steps. Then the row that
-    // holds this CTA's first step.
+    // Sum of the rows' work: a (row, kv head) segment's is its row's steps and one unit more for its
+    // start, merge and result (about a step's time), and each CTA takes an equal run of all
+    // segments' work. Then the row that holds this CTA's first unit.
     const int64_t per_row = a.kv.Hkv;
     int64_t per_cta, at, end;
     int row = -1;
-    int64_t row_start = 0;  // first step of that row
+    int64_t row_start = 0;  // first unit of that row
     auto share = [&](int64_t total) {
         per_cta = (total + gridDim.x - 1) / gridDim.x;
         at = per_cta * blockIdx.x;
@@ -389,7 +390,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
     };
     if (a.rows <= 32) {
         // every warp for itself, a row to a lane: no barrier in a small call's way
-        const uint32_t c = lane < a.rows ? steps_of(row_range(a, lane)) : 0;
+        const uint32_t c = lane < a.rows ? 1 + steps_of(row_range(a, lane)) : 0;
         uint32_t sum = c;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -402,7 +403,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         row_start = __shfl_sync(~0u, sum - c, row) * per_row;
     } else {
         int64_t mine = 0;
-        for (int r = tid; r < a.rows; r += kRowThreads) mine += steps_of(row_range(a, r));
+        for (int r = tid; r < a.rows; r += kRowThreads) mine += 1 + steps_of(row_range(a, r));
 #pragma unroll
         for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(~0u, mine, o);
         if (lane == 0) s_scan[warp] = mine;
@@ -415,7 +416,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         int64_t before = 0;
         for (int r0 = 0; r0 < a.rows; r0 += kRowThreads) {
             const int r = r0 + tid;
-            const int64_t c = r < a.rows ? steps_of(row_range(a, r)) : 0;
+            const int64_t c = r < a.rows ? 1 + steps_of(row_range(a, r)) : 0;
             int64_t sum = c;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -443,17 +444,19 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
     }
     RowRange range = row_range(a, row);
     int steps = steps_of(range);
-    int64_t segment_start;  // first step of the current segment
+    int64_t segment_start;  // first unit of the current segment
     int h;                  // kv head
     {
         const int64_t into = at - row_start;
-        h = static_cast<int>(into / steps);
-        segment_start = row_start + static_cast<int64_t>(h) * steps;
+        h = static_cast<int>(into / (steps + 1));
+        segment_start = row_start + static_cast<int64_t>(h) * (steps + 1);
     }
 
     while (at < end) {
-        const int step0 = static_cast<int>(at - segment_start);
-        const int n = static_cast<int>(min(static_cast<int64_t>(steps - step0), end - at));
+        const int step0 = max(static_cast<int>(at - segment_start) - 1, 0);
+        at = min(end, segment_start + steps + 1);
+        const int n = static_cast<int>(at - segment_start) - 1 - step0;
+        if (n <= 0) return;  // the start alone: the segment's steps are the next CTA's
 
         // Q in the reduction order of the K pieces. In the 8-bit cache's fp16 products each row is
         // scaled by a power of two to a largest magnitude in [1, 2), so that no bf16 value
@@ -721,8 +724,8 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         __syncthreads();
 
         // Contributors of the segment: the CTAs whose runs meet its steps.
-        const int first = static_cast<int>(segment_start / per_cta);
-        const int last = static_cast<int>((segment_start + steps - 1) / per_cta);
+        const int first = static_cast<int>((segment_start + 1) / per_cta);
+        const int last = static_cast<int>((segment_start + steps) / per_cta);
         const bool whole = first == last;
         float* const slot = a.partial + (static_cast<int64_t>(blockIdx.x) * 2 + (step0 == 0)) * kRowSlotFloats;
         const float v_scale = FP8 ? a.kv.scales[a.kv.Hkv + h] : 1.0f;
@@ -803,8 +806,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         }
 
         // the next segment
-        at += n;
-        segment_start += steps;
+        segment_start += steps + 1;
         if (++h == a.kv.Hkv) {
             h = 0;
             if (++row < a.rows) {
