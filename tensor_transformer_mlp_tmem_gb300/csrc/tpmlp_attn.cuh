@@ -254,6 +254,10 @@ struct RowArgs {
 };
 
 constexpr int kRowWarps = 8;
+// A segment's fixed time (its start, merge and result) in steps, as it counts in the CTAs' shares. 0, 1,
+// 2, 3: 64 sequences of 8192 keys at most x 32 heads 616, 591, 593, 596 us; 48 sequences in e4m3, 12
+// heads to a kv head 115, 104, 101, 102; one sequence of 131072 keys 92, 90, 89, 91.
+constexpr int kSegmentStart = 2;
 constexpr int kRowThreads = 32 * kRowWarps;
 // e4m3 caches: fp16 weights are raised by 2^10, so that the small ones of a long cache stay clear of
 // fp16's smallest steps; it cancels against the sum.
@@ -376,9 +380,8 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
     auto steps_of = [&](const RowRange& x) {
         return max(1, (x.hi - (x.lo & ~15) + S::kStep - 1) / S::kStep);
     };
-    // Sum of the rows' work: a (row, kv head) segment's is its row's steps and one unit more for its
-    // start, merge and result (about a step's time), and each CTA takes an equal run of all
-    // segments' work. Then the row that holds this CTA's first unit.
+    // Sum of the rows' work: a (row, kv head) segment's is its row's steps and kSegmentStart, and each
+    // CTA takes an equal run of all segments' work. Then the row that holds this CTA's first unit.
     const int64_t per_row = a.kv.Hkv;
     int64_t per_cta, at, end;
     int row = -1;
@@ -390,7 +393,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
     };
     if (a.rows <= 32) {
         // every warp for itself, a row to a lane: no barrier in a small call's way
-        const uint32_t c = lane < a.rows ? 1 + steps_of(row_range(a, lane)) : 0;
+        const uint32_t c = lane < a.rows ? kSegmentStart + steps_of(row_range(a, lane)) : 0;
         uint32_t sum = c;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -403,7 +406,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         row_start = __shfl_sync(~0u, sum - c, row) * per_row;
     } else {
         int64_t mine = 0;
-        for (int r = tid; r < a.rows; r += kRowThreads) mine += 1 + steps_of(row_range(a, r));
+        for (int r = tid; r < a.rows; r += kRowThreads) mine += kSegmentStart + steps_of(row_range(a, r));
 #pragma unroll
         for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(~0u, mine, o);
         if (lane == 0) s_scan[warp] = mine;
@@ -416,7 +419,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         int64_t before = 0;
         for (int r0 = 0; r0 < a.rows; r0 += kRowThreads) {
             const int r = r0 + tid;
-            const int64_t c = r < a.rows ? 1 + steps_of(row_range(a, r)) : 0;
+            const int64_t c = r < a.rows ? kSegmentStart + steps_of(row_range(a, r)) : 0;
             int64_t sum = c;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -448,14 +451,14 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
     int h;                  // kv head
     {
         const int64_t into = at - row_start;
-        h = static_cast<int>(into / (steps + 1));
-        segment_start = row_start + static_cast<int64_t>(h) * (steps + 1);
+        h = static_cast<int>(into / (steps + kSegmentStart));
+        segment_start = row_start + static_cast<int64_t>(h) * (steps + kSegmentStart);
     }
 
     while (at < end) {
-        const int step0 = max(static_cast<int>(at - segment_start) - 1, 0);
-        at = min(end, segment_start + steps + 1);
-        const int n = static_cast<int>(at - segment_start) - 1 - step0;
+        const int step0 = max(static_cast<int>(at - segment_start) - kSegmentStart, 0);
+        at = min(end, segment_start + steps + kSegmentStart);
+        const int n = static_cast<int>(at - segment_start) - kSegmentStart - step0;
         if (n <= 0) return;  // the start alone: the segment's steps are the next CTA's
 
         // Q in the reduction order of the K pieces. In the 8-bit cache's fp16 products each row is
@@ -724,8 +727,8 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         __syncthreads();
 
         // Contributors of the segment: the CTAs whose runs meet its steps.
-        const int first = static_cast<int>((segment_start + 1) / per_cta);
-        const int last = static_cast<int>((segment_start + steps) / per_cta);
+        const int first = static_cast<int>((segment_start + kSegmentStart) / per_cta);
+        const int last = static_cast<int>((segment_start + kSegmentStart + steps - 1) / per_cta);
         const bool whole = first == last;
         float* const slot = a.partial + (static_cast<int64_t>(blockIdx.x) * 2 + (step0 == 0)) * kRowSlotFloats;
         const float v_scale = FP8 ? a.kv.scales[a.kv.Hkv + h] : 1.0f;
@@ -806,7 +809,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         }
 
         // the next segment
-        segment_start += steps + 1;
+        segment_start += steps + kSegmentStart;
         if (++h == a.kv.Hkv) {
             h = 0;
             if (++row < a.rows) {
