@@ -13,8 +13,19 @@
 // Warps: 0-3 softmax of tile 0, 4-7 of tile 1 (a warp may read the 32 tensor-memory lanes of its
 // rank mod 4), 8 and 10 issue the MMAs of tile 0 and 1, 9 loads K and V (and Q) by TMA, page by
 // page, 11 makes the work list; e4m3 caches: 12-19 convert the loaded bytes to fp16. One warp
-// per tile issues MMAs because each waits for four barriers a block: with one warp for both
-// tiles the tensor core idled during those waits (GPT-3-shaped prompt: 516 us against MEASURE2).
+// per tile issues MMAs because each waits for several barriers a step: with one warp for both
+// tiles the tensor core idled during those waits.
+//
+// What bounds it (GPT-3-shaped prompt, 4096 tokens x 96 heads of 128: 300-320 us, 1.3 PFLOP/s, about
+// 70 % of the measured bf16 rate, at the board's power limit): two bounds lie close together. A
+// softmax step takes a warp about 1300 cycles, most of them issue slots that the tiles' warps share,
+// so 128 keys of both tiles take 2600; and their products 2048 cycles of the tensor core, which
+// S's 64 columns stretch (Q is read again for every 64 keys, and shared memory feeds the tensor core
+// at 128 bytes a cycle). Leaving out all exponentials, half of Q K^T or half of P V changed the time
+// by 3 to 4 % each. Steps of 64 keys with two buffers of S per tile let a softmax follow the one
+// before it at once; with steps of 128 and one buffer (S, P and both O fill tensor memory) every
+// softmax waited for the two products before it: 416 against 486 us. Two groups of softmax warps to
+// a tile, for even and odd steps or for halves of a block, gained nothing (361 against 340; 439).
 #pragma once
 
 #include "tpmlp_attn.cuh"
