@@ -518,8 +518,9 @@ TPMLP_API int tpmlp_attn_set_scales(tpmlp_ctx *ctx, const void *k_scale, const v
 /*
  * The caller's cache, as the calls below read it. Key j of sequence b is row j % page_size of
  * page page_table[b][j / page_size]; a page of a pool is [Hkv][page_size][D]. Pages may be
- * shared between sequences that only read them. Rows at or past a sequence's length are never
- * used, whatever they hold (NaN included).
+ * shared between sequences that only read them. Rows at or past a sequence's length, and rows
+ * before every query's window, are never used, whatever they hold (NaN included); the table's
+ * entries of pages that hold nothing else are not looked at.
  */
 typedef struct tpmlp_kv {
     void *K, *V;               /* device pools, bf16 or e4m3 */

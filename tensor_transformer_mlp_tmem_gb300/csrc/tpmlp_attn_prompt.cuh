@@ -199,6 +199,7 @@ struct Piece {
     int tokens[2];         // of each tile
     int lo[2], hi[2];      // each tile's steps
     int last_hi[2];        // end of the keys of each tile's last token
+    int lo_key;            // first key that any of the item's tokens sees
     int b0, b1;            // blocks
     int first, last;       // contributing CTAs
     int starts;            // 1: the item's first blocks are in this piece
@@ -216,6 +217,7 @@ __device__ __forceinline__ int prompt_lo_key(const PromptArgs& a, int hi) {
 __device__ __forceinline__ void item_blocks(const PromptArgs& a, Piece& p) {
     p.b0 = 0x7FFFFFFF;
     p.b1 = 0;
+    p.lo_key = prompt_lo_key(a, p.seq.hi(p.tok0));
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         const int k0 = p.tok0 + t * a.tpt;
@@ -237,7 +239,7 @@ __device__ __forceinline__ void item_blocks(const PromptArgs& a, Piece& p) {
 // The CTA's work list. Items are numbered sequence by sequence; within a sequence in groups of
 // kv heads, so that the heads in flight keep their K and V in L2, and within a group from the last
 // tokens (most keys) to the first. A group has two items or more for each CTA: with one, a last
-// group's largest items were started when little else was left (GPT-3-shaped prompt: 326 us).
+// group's largest items were started when little else was left (GPT-3-shaped prompt: 326 us, so 302).
 struct PromptWork {
     const int64_t* coarse;  // items before each run of `run` sequences
     const int* units;       // work before each item (split lists)
@@ -833,7 +835,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             const Piece* p = next_piece();
             if (!p) break;
             const int b0 = p->b0, b1 = p->b1, begin = p->begin(t), end = p->end(t), last_hi = p->last_hi[t];
-            const int item_hi = max(p->last_hi[0], p->last_hi[1]);
+            const int item_hi = max(p->last_hi[0], p->last_hi[1]), item_lo = p->lo_key;
             if (b1 > b0 || FP8) {
                 if (!(ok = wait(q_full(t), q_phase, 4))) break;
                 q_phase ^= 1u;
@@ -854,17 +856,18 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 if (i > b0) {
                     if (!(ok = wait(full(vs), vph, 5))) break;
                     // Rows of V that no query of the item may see, in a group of 16 that the
-                    // product reads: past the item's last key or in a page that is not there.
-                    // Their weights are 0, but 0 times what they hold may be NaN; they are
-                    // cleared first (by both tiles' warps alike).
-                    const int in = item_hi - (i - 1) * kPB;
+                    // product reads: past the item's last key, before its first (a window's), or
+                    // in a page that is not there. Their weights are 0, but 0 times what they hold
+                    // may be NaN; they are cleared first (by both tiles' warps alike).
+                    const int in = item_hi - (i - 1) * kPB, low = item_lo - (i - 1) * kPB;
                     const uint32_t have = groups[(blocks + i - 1 - b0) & 7];
-                    if (in < kPB || have != 0xFFu) {
-                        const int upto = min(kPB, (in + 15) & ~15);
-                        for (int r = have == 0xFFu ? in : 0; r < upto; ++r)
-                            if ((r >= in || !((have >> (r >> 4)) & 1u)) && lane < D / 8)
-                                *reinterpret_cast<uint4*>(base_ptr + sv + (lane >> 3) * kHalf + r * 128 +
-                                                          (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    if (in < kPB || low > 0 || have != 0xFFu) {
+                        constexpr int kLanes = D / 8;  // to a row, 16 bytes each per 64 columns
+                        const int upto = min(kPB, (in + 15) & ~15), piece = lane % kLanes;
+                        for (int r = (have == 0xFFu && low <= 0 ? in : 0) + lane / kLanes; r < upto; r += 32 / kLanes)
+                            if (r >= in || r < low || !((have >> (r >> 4)) & 1u))
+                                *reinterpret_cast<uint4*>(base_ptr + sv + (piece >> 3) * kHalf + r * 128 +
+                                                          (piece & 7) * 16) = make_uint4(0, 0, 0, 0);
                         fence_async_shared();
                         __syncwarp();
                     }
@@ -949,7 +952,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             const Piece* p = next_piece();
             if (!p) break;
             const int b0 = p->b0, b1 = p->b1, h = p->h, b = p->b;
-            const int top = max(p->last_hi[0], p->last_hi[1]);
+            const int top = max(p->last_hi[0], p->last_hi[1]), low = p->lo_key;
             if (!FP8 && b1 > b0) {
                 if (!(ok = wait(q_empty, q_phase ^ 1u, 9))) break;
                 q_phase ^= 1u;
@@ -964,20 +967,23 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 }
                 ++q_loads;
             }
-            // the table's entry for this lane's copy of a block, looked up a block ahead
-            auto entry = [&](int i) {
+            // whether this lane copies a part of block i: not past the item's last key, and no page
+            // that lies before its first (a window's user may have given that page away)
+            auto wanted = [&](int i) {
                 const int key = i * kPB + lane * rows;
-                return lane < copies && key < top && i < b1 ? kv_entry(a.kv, b, key) : 0;
+                return lane < copies && i < b1 && key < top && key + rows > low;
             };
+            // the table's entry for this lane's copy of a block, looked up a block ahead
+            auto entry = [&](int i) { return wanted(i) ? kv_entry(a.kv, b, i * kPB + lane * rows) : 0; };
             int next = entry(b0);
             for (int i = b0; ok && i < b1; ++i) {
                 const int key = i * kPB + lane * rows;
-                const bool in = lane < copies && key < top;
+                const bool in = wanted(i);
                 const int found_page = next;
                 next = entry(i + 1);
                 const int64_t page = in ? kv_checked(a.kv, found_page) : -1;
                 const uint32_t there = __ballot_sync(~0u, page >= 0);
-                // groups of 16 keys that are there; those past the item's keys count as such
+                // groups of 16 keys that are there; those outside the item's keys count as such
                 uint32_t have = 0xFFu;
                 const uint32_t missing = __ballot_sync(~0u, in && page < 0);
                 if (missing) {

@@ -414,3 +414,43 @@ def test_bad_pages_are_left_out_and_reported(lib):
         cache.lens[0] = 70
         assert torch.equal(attn.decode(q.cuda(), cache), good)
         ok(attn)
+
+
+# ------------------------------------------------------------------ what a window leaves behind
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Hq,Hkv,D,page,lens,new,window", [
+    (4, 2, 128, 16, [900, 300], [200, 40], 100),
+    (4, 4, 64, 64, [513, 130], [1, 64], 33),
+    (2, 1, 128, 256, [700], [300], 50),
+    (12, 1, 64, 32, [400, 65, 9000], [17, 65, 3], 1),
+    (3, 3, 128, 128, [1000], [500], 131),
+])
+def test_keys_before_every_window_are_not_used(lib, kv, Hq, Hkv, D, page, lens, new, window):
+    """Keys and values that lie before every query's window are NaN, and table entries of pages that
+    hold nothing else name no page: results are as ever, and no status is raised."""
+    c = ref.make(Hkv, D, page, kv, lens, seed=31)
+    K, V, table = c["K"].float(), c["V"].float(), c["table"].clone()
+
+    def poison(firsts):
+        for b, first in enumerate(firsts):
+            for key in range(first):
+                at = int(c["table"][b, key // page])
+                K[at, :, key % page] = math.nan
+                V[at, :, key % page] = math.nan
+            table[b, :first // page] = torch.tensor([-1, 1 << 30])[torch.arange(first // page) % 2].int()
+        return dict(c, K=K.to(c["K"].dtype), V=V.to(c["V"].dtype), table=table)
+
+    T, B = sum(new), len(lens)
+    q = queries(T, Hq, D, 31)
+    cu = torch.tensor([sum(new[:b]) for b in range(B + 1)], dtype=torch.int32).cuda()
+    with tp.Attention(Hq, Hkv, D, page, kv_dtype=kv) as attn:
+        cache = on_device(poison([max(0, n - m + 1 - window) for n, m in zip(lens, new)]), attn)
+        got, lse = attn.prompt(q.cuda(), cu, cache, window=window, return_lse=True)
+        ok(attn)
+        spans = prompt_spans(lens, new, window)
+        check_rows(c, q, got, lse, spans[:40] + spans[40::7] + spans[-3:], Hq, D, 1.0 / math.sqrt(D))
+        cache = on_device(poison([max(0, n - window) for n in lens]), attn)
+        got, lse = attn.decode(q[:B].cuda(), cache, window=window, return_lse=True)
+        ok(attn)
+        check_rows(c, q, got, lse, [(b, b, max(0, n - window), n) for b, n in enumerate(lens)], Hq, D,
+                   1.0 / math.sqrt(D))
