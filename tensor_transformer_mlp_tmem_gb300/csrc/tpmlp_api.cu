@@ -1556,6 +1556,8 @@ int tpmlp_get_status(tpmlp_ctx* c, void* stream, int32_t* detail) {
     int v = 0;
     TPMLP_CUDA(c, cudaMemcpy(&v, c->status, sizeof(int), cudaMemcpyDeviceToHost));
     TPMLP_CUDA(c, cudaMemset(c->status, 0, sizeof(int)));
+    // an attention kernel that gave up may have left arrivals behind
+    if (v && c->attn_count) TPMLP_CUDA(c, cudaMemset(c->attn_count, 0, c->attn_counters * sizeof(uint32_t)));
     if (detail) *detail = v;
     if (v & kStatusBadPage) return TPMLP_ERR_BAD_PAGE;
     return v ? TPMLP_ERR_DEVICE_TIMEOUT : TPMLP_OK;

@@ -254,6 +254,7 @@ int tpmlp_attn_create(tpmlp_ctx** out, int32_t Hq, int32_t Hkv, int32_t D, int32
     const size_t partial = std::max(ctas * 2 * tpmlp::kRowSlotFloats,
                                     static_cast<size_t>(c->num_sms) * 4 * tpmlp::kPromptSlotFloats);
     const size_t counters = ctas + 2;  // a counter per CTA (prompt: per tile), the deal's two
+    c->attn_counters = counters;
     const size_t scales = static_cast<size_t>(Hkv) * 2;
     cudaError_t e;
     float* ones = new (std::nothrow) float[scales];
@@ -359,9 +360,9 @@ int tpmlp_attn_decode(tpmlp_ctx* c, const void* Q, int64_t ldq, const tpmlp_kv* 
     // Wide head groups fill the tiles of the prompt kernel's products, which take the same time for
     // any G; the row kernel's grows with every 8 heads. 64 sequences of 4096 keys, 8 kv heads, row
     // kernel against prompt kernel, us: D = 128 in bf16, G = 8: 167, 188; 12: 220, 194; 16: 223, 189.
-    // In e4m3, G = 16: 139, 219. D = 64, G = 16: in bf16 114, 147; in e4m3 80, 173. With G = 24 the row
-    // kernel would take its keys twice: 388, 197 (D = 128) and 198, 161 (D = 64) in bf16, 238, 223
-    // and 153, 176 in e4m3; from G = 33 on three times and more.
+    // In e4m3, G = 16: 135, 223. D = 64, G = 16: in bf16 114, 147; in e4m3 80, 194. With G = 24 the row
+    // kernel would take its keys twice: 388, 197 (D = 128) and 198, 161 (D = 64) in bf16, 238, 229
+    // and 153, 199 in e4m3; from G = 33 on three times and more.
     if (a.G > 16 || (a.G > 8 && c->head_dim == 128 && !is_e4m3(c)))
         return run_prompt(c, a, nullptr, kv->B, static_cast<cudaStream_t>(stream));
     return run_rows(c, a, static_cast<cudaStream_t>(stream));

@@ -472,10 +472,11 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     sum += units[lane * each + i];
                     most = max(most, units[lane * each + i]);
                 }
-            int before = sum;
+            // in 64 bits: 1024 items of 2^24 blocks (a lane's 32 items stay below 2^31)
+            int64_t before = sum;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(~0u, before, o);
+                const int64_t v = __shfl_up_sync(~0u, before, o);
                 if (lane >= o) before += v;
                 most = max(most, __shfl_xor_sync(~0u, most, o));
             }
@@ -485,17 +486,19 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             for (int i = 0; i < each; ++i)
                 if (lane * each + i < n) {
                     const int u = units[lane * each + i];
-                    units[lane * each + i] = before;
+                    units[lane * each + i] = static_cast<int>(before);
                     before += u;
                 }
         }
         __syncthreads();
-        const int total = static_cast<int>(found[0]), most = static_cast<int>(found[1]);
+        const int64_t all = found[0];
+        const int total = static_cast<int>(min(all, static_cast<int64_t>(INT_MAX)));
+        const int most = static_cast<int>(found[1]);
         if (threadIdx.x == 0) units[n] = total;
         const int g = static_cast<int>(gridDim.x);
         const int share = max((total + g - 1) / g, 1);
         const int whole = n <= g ? most : share + most / 2;
-        if (10 * whole > 11 * (share + kJoinBlocks)) {
+        if (all == total && 10 * whole > 11 * (share + kJoinBlocks)) {
             work.split = true;
             work.per = share;
             work.at = static_cast<int64_t>(share) * blockIdx.x;
@@ -994,12 +997,18 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 for (int kv = 0; kv < 2; ++kv) {
                     const uint32_t bar_full = FP8 ? raw_full(stage) : full(stage);
                     if (!(ok = wait(FP8 ? raw_empty(stage) : empty(stage), phase ^ 1u, 10))) break;
-                    if (lane == 0) {
+#ifdef TPMLP_TEST_SKIP_STAGE
+                    // a stage that is never filled: the waits for it run out
+                    const bool fill = issued != TPMLP_TEST_SKIP_STAGE;
+#else
+                    constexpr bool fill = true;
+#endif
+                    if (lane == 0 && fill) {
                         if (kv == 0) groups[(blocks + i - b0) & 7] = have;
                         ptx::mbar_arrive_expect_tx(bar_full, static_cast<uint32_t>(__popc(there) * rows) * D * (FP8 ? 1 : 2));
                     }
                     __syncwarp();
-                    if (page >= 0) {
+                    if (page >= 0 && fill) {
                         if constexpr (FP8) {
                             bulk_load(base + L::kRaw0 + stage * L::kRaw + lane * rows * D,
                                       (kv ? a.kv.V : a.kv.K) + page * a.kv.page_bytes + h * a.kv.head_bytes +

@@ -100,6 +100,7 @@ struct tpmlp_ctx {
     float* kv_scale = nullptr;       // [2][heads_kv] fp32: the k scales, then the v scales
     float* attn_partial = nullptr;   // partial sums of split key ranges (tpmlp_attn.cuh)
     uint32_t* attn_count = nullptr;  // arrivals at a split key range, one counter per CTA
+    size_t attn_counters = 0;        // entries of attn_count
 
     int* status = nullptr;  // device status word
     int64_t launches = 0;
