@@ -334,11 +334,12 @@ int tpmlp_attn_append(tpmlp_ctx* c, const void* Q, int64_t ldq, const void* K, i
     a.rot = c->rot_dim;
     a.interleaved = c->rope_interleaved;
     std::memcpy(a.turns, c->rope_turns, sizeof(a.turns));
-    // Parts of a token: two blocks an SM where there are few tokens, each thread with a unit at
-    // least. One token of 32 + 32 heads of 128: 2.3 us (one block: 3.5 us).
+    // Parts of a token: as many blocks as run at once where there are few tokens, each thread with
+    // a unit at least. One token of 32 + 32 heads of 128: 2.4 us (one block: 3.5 us); 256 tokens of 96
+    // + 8 heads into e4m3: 4.5 us (two, four blocks an SM: 5.7, 4.8).
     const int64_t units = static_cast<int64_t>(a.Hq + 2 * c->heads_kv) * (c->head_dim / 16);
     const int64_t most = (units + tpmlp::kAppendThreads - 1) / tpmlp::kAppendThreads;
-    a.parts = static_cast<int32_t>(std::min(most, std::max<int64_t>(1, 2 * c->num_sms / T)));
+    a.parts = static_cast<int32_t>(std::min(most, std::max<int64_t>(1, tpmlp::kAppendBlocks * c->num_sms / T)));
     a.part_units = static_cast<int32_t>((units + a.parts - 1) / a.parts);
     const int64_t grid = T * a.parts;
     cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -86,7 +86,10 @@ __device__ __forceinline__ uint4 load16(const uint8_t* p) {
     return __ldcg(reinterpret_cast<const uint4*>(p));
 }
 constexpr int kAppendThreads = 128;
-constexpr int kAppendUnits = 4;  // units of 16 elements that a thread has in flight
+constexpr int kAppendUnits = 3;  // units of 16 elements that a thread has in flight
+// Blocks an SM, which hold a thread to 64 registers. 16384 tokens of 32 query and 8 kv heads: 6, 7, 8, 9
+// blocks 74, 70, 66, 69 us; 8 blocks and units of 2, 4: 71, 79 us.
+constexpr int kAppendBlocks = 8;
 
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -124,12 +127,13 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float (&f)[8], float scale) {
 // of them once, in shared memory, while its first loads are under way. The angle is taken in whole
 // turns in fp64 and reduced to [-1/2, 1/2] there, so its error is that of the fp32 result however
 // far the position (an fp32 product would be off by whole radians at position 10^7). A thread
-// rotates units of 16 elements: the 8 dimensions from 8u and their partners, which are the 8 from
-// rot/2 + 8u (halves) or the same 16 (neighbours). Bound by DRAM: 16384
-// tokens of 32 query and 8 kv heads of 128 in 73 us, 5.5 TB/s (256 threads a block, each loading a
-// unit when it had the sines: 87 us).
+// takes units of 16 elements: 8 dimensions of the lower half of a head's rotated (or other)
+// dimensions and the 8 of the upper half that lie as far on, so that neighbouring threads read and
+// write neighbouring 16 bytes; where halves are rotated they are the partners. Bound by DRAM: 16384
+// tokens of 32 query and 8 kv heads of 128 in 66 us, 6.1 TB/s, 90 % of a copy's rate (256 threads a
+// block, each loading a unit when it had the sines: 87 us).
 template <int D, bool FP8>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) append_kernel(const __grid_constant__ AppendArgs a) {
     __shared__ float2 trig[D / 2];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
@@ -155,12 +159,10 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
             x.kind = head < a.Hq ? 0 : head < a.Hq + a.kv.Hkv ? 1 : 2;
             x.h = x.kind == 0 ? head : x.kind == 1 ? head - a.Hq : head - a.Hq - a.kv.Hkv;
             x.rotate = x.kind != 2 && 16 * u < a.rot;
-            x.d0 = 16 * u;
-            x.d1 = x.d0 + 8;
-            if (x.rotate && !a.interleaved) {
-                x.d0 = 8 * u;
-                x.d1 = half + x.d0;
-            }
+            const int first = x.kind == 2 || x.rotate ? 0 : a.rot;
+            const int dims = x.kind == 2 ? D : x.rotate ? a.rot : D - a.rot;
+            x.d0 = first + 8 * (u - first / 16);
+            x.d1 = x.d0 + dims / 2;
             return x;
         };
 #pragma unroll
@@ -195,11 +197,10 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
             unpack8(raw[y][0], x0);
             unpack8(raw[y][1], x1);
             if (w.rotate) {
-                const float2* const r = trig + 8 * (i % kUnits);
                 if (a.interleaved) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float2 r0 = r[j], r1 = r[4 + j];
+                        const float2 r0 = trig[w.d0 / 2 + j], r1 = trig[w.d1 / 2 + j];
                         const float p0 = x0[2 * j], p1 = x1[2 * j];
                         x0[2 * j] = p0 * r0.x - x0[2 * j + 1] * r0.y;
                         x0[2 * j + 1] = x0[2 * j + 1] * r0.x + p0 * r0.y;
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
                 } else {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const float2 r0 = r[j];
+                        const float2 r0 = trig[w.d0 + j];
                         const float p0 = x0[j];
                         x0[j] = p0 * r0.x - x1[j] * r0.y;
                         x1[j] = x1[j] * r0.x + p0 * r0.y;
