@@ -185,6 +185,23 @@ int run_prompt(tpmlp_ctx* c, const tpmlp::RowArgs& r, const int32_t* cu_q, int64
     return is_e4m3(c) ? launch_prompt<64, true>(c, q, k, v, a, s) : launch_prompt<64, false>(c, q, k, v, a, s);
 }
 
+// Tokens of an append block: as many as its threads' units hold, but no fewer blocks than run at
+// once. 16384 tokens of 12 + 12 heads of 64, 16 + 2 of 64, 8 + 1 of 128 in e4m3, 1 + 1 of 64: 30, 16, 23,
+// 9 us (a block for each token: 37, 27, 34, 25).
+int64_t append_tokens(const tpmlp_ctx* c, int64_t units, int64_t T) {
+    const int64_t hold = tpmlp::kAppendThreads * tpmlp::kAppendUnits / units;
+    const int64_t fill = T / (static_cast<int64_t>(tpmlp::kAppendBlocks) * c->num_sms);
+    return std::max<int64_t>(1, std::min({hold, fill, static_cast<int64_t>(tpmlp::kAppendTokens)}));
+}
+
+template <int D, bool FP8>
+int run_append(tpmlp_ctx* c, const tpmlp::AppendArgs& a, cudaStream_t s) {
+    if (a.tokens > 1)
+        return launch(c, tpmlp::append_kernel<D, FP8, true>, (a.T + int64_t(a.tokens) - 1) / a.tokens,
+                      tpmlp::kAppendThreads, 0, s, a);
+    return launch(c, tpmlp::append_kernel<D, FP8, false>, int64_t(a.T) * a.parts, tpmlp::kAppendThreads, 0, s, a);
+}
+
 // What decode and prompt check alike; rows: rows of Q and Out.
 int check_attend(tpmlp_ctx* c, const void* Q, int64_t ldq, const tpmlp_kv* kv, float scale,
                  const void* Out, int64_t ldo, const float* Lse) {
@@ -341,13 +358,12 @@ int tpmlp_attn_append(tpmlp_ctx* c, const void* Q, int64_t ldq, const void* K, i
     const int64_t most = (units + tpmlp::kAppendThreads - 1) / tpmlp::kAppendThreads;
     a.parts = static_cast<int32_t>(std::min(most, std::max<int64_t>(1, tpmlp::kAppendBlocks * c->num_sms / T)));
     a.part_units = static_cast<int32_t>((units + a.parts - 1) / a.parts);
-    const int64_t grid = T * a.parts;
+    a.T = static_cast<int32_t>(T);
+    a.tokens = static_cast<int32_t>(append_tokens(c, units, T));
+    a.per_unit = static_cast<uint32_t>((uint64_t(1) << 32) / units + 1);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (c->head_dim == 128)
-        return is_e4m3(c) ? launch(c, tpmlp::append_kernel<128, true>, grid, tpmlp::kAppendThreads, 0, s, a)
-                          : launch(c, tpmlp::append_kernel<128, false>, grid, tpmlp::kAppendThreads, 0, s, a);
-    return is_e4m3(c) ? launch(c, tpmlp::append_kernel<64, true>, grid, tpmlp::kAppendThreads, 0, s, a)
-                      : launch(c, tpmlp::append_kernel<64, false>, grid, tpmlp::kAppendThreads, 0, s, a);
+    if (c->head_dim == 128) return is_e4m3(c) ? run_append<128, true>(c, a, s) : run_append<128, false>(c, a, s);
+    return is_e4m3(c) ? run_append<64, true>(c, a, s) : run_append<64, false>(c, a, s);
 }
 
 int tpmlp_attn_decode(tpmlp_ctx* c, const void* Q, int64_t ldq, const tpmlp_kv* kv, float scale,

@@ -77,6 +77,9 @@ struct AppendArgs {
     int32_t interleaved;
     int32_t parts;      // blocks per token
     int32_t part_units; // units of each
+    int32_t T;
+    int32_t tokens;     // tokens per block (more than one: parts is 1)
+    uint32_t per_unit;  // 2^32 / units of a token, rounded up
     double turns[64];   // whole turns per position of each pair
 };
 
@@ -90,6 +93,7 @@ constexpr int kAppendUnits = 3;  // units of 16 elements that a thread has in fl
 // Blocks an SM, which hold a thread to 64 registers. 16384 tokens of 32 query and 8 kv heads: 6, 7, 8, 9
 // blocks 74, 70, 66, 69 us; 8 blocks and units of 2, 4: 71, 79 us.
 constexpr int kAppendBlocks = 8;
+constexpr int kAppendTokens = 8;  // tokens of a block, at most
 
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -122,7 +126,8 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float (&f)[8], float scale) {
     return make_uint2(w[0], w[1]);
 }
 
-// A block takes a token, or one of `parts` equal parts of it where there are few tokens. The
+// A block takes a token, one of `parts` equal parts of it where there are few tokens, or (MANY)
+// several tokens where a token has so few heads that its units would leave threads idle. The
 // rotation's sines and cosines are the same for all heads: the block computes the token's rot / 2
 // of them once, in shared memory, while its first loads are under way. The angle is taken in whole
 // turns in fp64 and reduced to [-1/2, 1/2] there, so its error is that of the fp32 result however
@@ -130,31 +135,39 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float (&f)[8], float scale) {
 // takes units of 16 elements: 8 dimensions of the lower half of a head's rotated (or other)
 // dimensions and the 8 of the upper half that lie as far on, so that neighbouring threads read and
 // write neighbouring 16 bytes; where halves are rotated they are the partners. Bound by DRAM: 16384
-// tokens of 32 query and 8 kv heads of 128 in 66 us, 6.1 TB/s, 90 % of a copy's rate (256 threads a
+// tokens of 32 query and 8 kv heads of 128 in 67 us, 6.0 TB/s, 89 % of a copy's rate (256 threads a
 // block, each loading a unit when it had the sines: 87 us).
-template <int D, bool FP8>
+template <int D, bool FP8, bool MANY>
 __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) append_kernel(const __grid_constant__ AppendArgs a) {
-    __shared__ float2 trig[D / 2];
+    constexpr int kTokens = MANY ? kAppendTokens : 1;
+    __shared__ float2 trig[kTokens * (D / 2)];
+    __shared__ int2 places[kTokens];  // MANY: position and page of each token
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     constexpr int kUnits = D / 16;  // units per head
-    const int64_t t = blockIdx.x / a.parts;
+    const int64_t t0 = MANY ? static_cast<int64_t>(blockIdx.x) * a.tokens : blockIdx.x / a.parts;
+    const int tokens = MANY ? static_cast<int>(min(static_cast<int64_t>(a.tokens), a.T - t0)) : 1;
     const int units = (a.Hq + 2 * a.kv.Hkv) * kUnits;
-    const int begin = static_cast<int>(blockIdx.x % a.parts) * a.part_units;
-    const int end = min(begin + a.part_units, units);
+    const int begin = MANY ? 0 : static_cast<int>(blockIdx.x % a.parts) * a.part_units;
+    const int end = MANY ? tokens * units : min(begin + a.part_units, units);
     const int half = a.rot >> 1;
-    const int pos = a.pos[t];
-    const int b = a.seq ? a.seq[t] : static_cast<int>(t);
-    int page = -1;
+    // the position and sequence of this thread's token (MANY: of the block's thread-th)
+    const bool own = !MANY || static_cast<int>(threadIdx.x) < tokens;
+    const int64_t t_own = t0 + (MANY ? threadIdx.x : 0);
+    int pos = own ? a.pos[t_own] : -1, page = -1;
+    const int b = !own ? -1 : a.seq ? a.seq[t_own] : static_cast<int>(t_own);
     for (int first = begin; first < end; first += kAppendThreads * kAppendUnits) {
         uint4 raw[kAppendUnits][2];
-        // unit i: its part of the token, head, whether it is rotated, its two pieces of 8 dimensions
+        // unit i: its token of the block, part of the token, head, whether it is rotated, its two
+        // pieces of 8 dimensions
         struct Unit {
-            int kind, h, d0, d1;  // kind: 0 q, 1 k, 2 v
+            int token, kind, h, d0, d1;  // kind: 0 q, 1 k, 2 v
             bool rotate;
         };
         auto unit = [&](int i) {
             Unit x;
+            x.token = MANY ? static_cast<int>(__umulhi(static_cast<uint32_t>(i), a.per_unit)) : 0;
+            if (MANY) i -= x.token * units;
             const int head = i / kUnits, u = i % kUnits;
             x.kind = head < a.Hq ? 0 : head < a.Hq + a.kv.Hkv ? 1 : 2;
             x.h = x.kind == 0 ? head : x.kind == 1 ? head - a.Hq : head - a.Hq - a.kv.Hkv;
@@ -170,29 +183,47 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) append_kernel(c
             const int i = first + y * kAppendThreads + static_cast<int>(threadIdx.x);
             if (i >= end) break;
             const Unit x = unit(i);
+            const int64_t t = t0 + x.token;
             const __nv_bfloat16* src = (x.kind == 0 ? a.q + t * a.ldq : x.kind == 1 ? a.k + t * a.ldk : a.v + t * a.ldv) +
                                        static_cast<int64_t>(x.h) * D;
             raw[y][0] = load16(reinterpret_cast<const uint8_t*>(src + x.d0));
             raw[y][1] = load16(reinterpret_cast<const uint8_t*>(src + x.d1));
         }
         if (first == begin) {
-            if (pos < 0) return;
-            for (int i = threadIdx.x; i < half; i += kAppendThreads) {
-                const double turn = pos * a.turns[i];
+            if (!MANY && pos < 0) return;
+            // the table's entry, asked for before the sines of many tokens and after those of one
+            // (16384 tokens of 12 + 12 heads of 64: 30 against 35 us; of 32 + 8 heads of 128: 70 against 67)
+            auto look_up = [&] {
+                const bool inside = b >= 0 && b < a.kv.B && pos >= 0 && (pos >> a.kv.page_shift) < a.kv.table_pages;
+                return inside ? kv_entry(a.kv, b, pos) : -1;
+            };
+            int entry = MANY ? look_up() : -1;
+            for (int i = threadIdx.x; i < (MANY ? tokens * (D / 2) : half); i += kAppendThreads) {
+                const int d = i % (D / 2);
+                if (MANY && d >= half) continue;
+                const double turn = (MANY ? a.pos[t0 + i / (D / 2)] : pos) * a.turns[d];
                 float s, c;
                 sincospif(2.0f * static_cast<float>(turn - rint(turn)), &s, &c);
                 trig[i] = make_float2(c, s);
             }
-            if (b >= 0 && b < a.kv.B && (pos >> a.kv.page_shift) < a.kv.table_pages) page = kv_page(a.kv, b, pos);
-            else if (threadIdx.x == 0) report_bad_page(a.kv.status);
+            if (!MANY) entry = look_up();
+            if (pos >= 0) page = kv_checked(a.kv, entry);  // -1: the token's k and v are dropped
+            if (MANY && own) places[threadIdx.x] = make_int2(pos, page);
             __syncthreads();
         }
-        const int slot = pos & ((1 << a.kv.page_shift) - 1);
 #pragma unroll
         for (int y = 0; y < kAppendUnits; ++y) {
             const int i = first + y * kAppendThreads + static_cast<int>(threadIdx.x);
             if (i >= end) break;
             const Unit w = unit(i);
+            if constexpr (MANY) {
+                pos = places[w.token].x;
+                page = places[w.token].y;
+                if (pos < 0) continue;
+            }
+            const int64_t t = t0 + w.token;
+            const int slot = pos & ((1 << a.kv.page_shift) - 1);
+            const float2* const turns = trig + w.token * (D / 2);
             float x0[8], x1[8];
             unpack8(raw[y][0], x0);
             unpack8(raw[y][1], x1);
@@ -200,7 +231,7 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) append_kernel(c
                 if (a.interleaved) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float2 r0 = trig[w.d0 / 2 + j], r1 = trig[w.d1 / 2 + j];
+                        const float2 r0 = turns[w.d0 / 2 + j], r1 = turns[w.d1 / 2 + j];
                         const float p0 = x0[2 * j], p1 = x1[2 * j];
                         x0[2 * j] = p0 * r0.x - x0[2 * j + 1] * r0.y;
                         x0[2 * j + 1] = x0[2 * j + 1] * r0.x + p0 * r0.y;
@@ -210,7 +241,7 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) append_kernel(c
                 } else {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const float2 r0 = trig[w.d0 + j];
+                        const float2 r0 = turns[w.d0 + j];
                         const float p0 = x0[j];
                         x0[j] = p0 * r0.x - x1[j] * r0.y;
                         x1[j] = x1[j] * r0.x + p0 * r0.y;

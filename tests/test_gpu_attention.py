@@ -454,3 +454,88 @@ def test_keys_before_every_window_are_not_used(lib, kv, Hq, Hkv, D, page, lens, 
         ok(attn)
         check_rows(c, q, got, lse, [(b, b, max(0, n - window), n) for b, n in enumerate(lens)], Hq, D,
                    1.0 / math.sqrt(D))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Hq,Hkv,D,page,rot,interleaved,T", [
+    (1, 1, 64, 16, 64, False, 20001),        # 8 tokens to a block, the last block holds one
+    (5, 5, 64, 32, 32, True, 9000),          # 6, dimensions that are not rotated
+    (12, 2, 64, 64, 64, False, 5003),        # 4
+    (8, 1, 128, 128, 128, False, 5001),      # 4
+    (14, 2, 128, 16, 96, True, 2500),        # 2
+    (6, 6, 128, 256, 0, False, 2433),
+])
+def test_append_many_tokens_of_few_heads(lib, kv, Hq, Hkv, D, page, rot, interleaved, T):
+    """Blocks of several tokens: as by definition, and the same bits as in small calls."""
+    lens = [T // 2 + 9, 1, T - T // 2 + 30]
+    c = ref.make(Hkv, D, page, kv, lens, seed=T)
+    g = torch.Generator().manual_seed(T)
+    q = torch.randn((T, Hq * D), generator=g).bfloat16()
+    k = torch.randn((T, Hkv * D), generator=g).bfloat16()
+    v = torch.randn((T, Hkv * D), generator=g).bfloat16()
+    places = torch.tensor([(b, p) for b, n in enumerate(lens) for p in range(n)], dtype=torch.int32)
+    places = places[torch.randperm(len(places), generator=g)[:T]]
+    seq, pos = places[:, 0].contiguous(), places[:, 1].contiguous()
+    pos[::7] = -1
+    with tp.Attention(Hq, Hkv, D, page, kv_dtype=kv) as attn:
+        if rot:
+            attn.set_rope(rot, interleaved=interleaved)
+        whole, parts = on_device(c, attn), on_device(c, attn)
+        d = [x.cuda() for x in (q, k, v, pos, seq)]
+        out = torch.full((T, Hq * D), 7.0, dtype=torch.bfloat16, device="cuda")
+        attn.append(*d[:3], whole, d[3], d[4], q_out=out)
+        ok(attn)
+        small = torch.full_like(out, 7.0)
+        for i in range(0, T, 1000):
+            x = [y[i:i + 1000] for y in d]
+            attn.append(*x[:3], parts, x[3], x[4], q_out=small[i:i + 1000])
+        ok(attn)
+        assert torch.equal(out, small)
+        assert torch.equal(whole.K.view(torch.uint8), parts.K.view(torch.uint8))
+        assert torch.equal(whole.V.view(torch.uint8), parts.V.view(torch.uint8))
+        kept = pos >= 0
+        assert bool((out.cpu()[~kept] == 7.0).all())
+        K, V = whole.K.cpu().float().double(), whole.V.cpu().float().double()
+    freq = [1e4 ** (-2 * i / rot) for i in range(rot // 2)] if rot else []
+    wantq, wantk = q.double().view(T, Hq, D), k.double().view(T, Hkv, D)
+    if rot:
+        wantq = ref.rotate(wantq, pos, rot, interleaved, freq)
+        wantk = ref.rotate(wantk, pos, rot, interleaved, freq)
+    slack = 2.0 ** -18
+    err = (out.cpu().double().view(T, Hq, D) - wantq).abs()[kept]
+    assert bool((err <= wantq.abs()[kept] * ref.HALF_STEP["bf16"] + slack).all())
+    pages = c["table"][seq[kept].long(), (pos[kept] // page).long()].long()
+    for got, want, scale in ((K, wantk, c["ks"]), (V, v.double().view(T, Hkv, D), c["vs"])):
+        scale = scale.double()[:, None]
+        w = want[kept] / scale
+        if kv == "e4m3":
+            w = w.clamp(-448, 448)
+            tol = w.abs() * ref.HALF_STEP["e4m3"] + 2.0 ** -10 + slack / scale
+        else:
+            tol = w.abs() * ref.HALF_STEP["bf16"] + slack
+        assert bool(((got[pages, :, (pos[kept] % page).long()] - w).abs() <= tol).all())
+
+
+def test_append_many_tokens_reports_bad_places(lib):
+    """Blocks of several tokens: a bad place drops its own token's k and v only."""
+    T, D, page = 4000, 64, 16
+    c = ref.make(1, D, page, "bf16", [T], seed=51)
+    x = torch.randn((T, D), generator=torch.Generator().manual_seed(51)).bfloat16()
+    pos = torch.arange(T, dtype=torch.int32)
+    with tp.Attention(1, 1, D, page) as attn:
+        cache = on_device(c, attn)
+        seq = torch.zeros(T, dtype=torch.int32)
+        bad = torch.tensor([5, 6, 1000, 3999])
+        pos[5], pos[1000] = 1 << 20, T + page
+        seq[6], seq[3999] = 1, -1
+        before = cache.V.clone()
+        got = attn.append(x.cuda(), x.cuda(), x.cuda(), cache, pos.cuda(), seq.cuda())
+        torch.cuda.synchronize()
+        assert attn.status()[0] == tp.TPMLP_ERR_BAD_PAGE
+        assert torch.equal(got.cpu(), x)  # queries are written all the same
+        good = torch.ones(T, dtype=torch.bool)
+        good[bad] = False
+        at = torch.arange(T)
+        pages = c["table"][0, at // page].long()
+        now, old = cache.V.cpu()[pages, 0, at % page], before.cpu()[pages, 0, at % page]
+        assert torch.equal(now[good], x[good]) and torch.equal(now[~good], old[~good])
