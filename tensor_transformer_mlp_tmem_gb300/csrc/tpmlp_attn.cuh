@@ -293,6 +293,7 @@ constexpr int kRowWarps = 8;
 // heads to a kv head 115, 104, 101, 102; one sequence of 131072 keys 92, 90, 89, 91.
 constexpr int kSegmentStart = 2;
 constexpr int kRowThreads = 32 * kRowWarps;
+constexpr int kJoinLoads = 8;  // contributors of a split range whose sums a thread loads at once
 // e4m3 caches: fp16 weights are raised by 2^10, so that the small ones of a long cache stay clear of
 // fp16's smallest steps; it cancels against the sum.
 constexpr float kRowRaise = 10.0f;
@@ -819,23 +820,36 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
                 if (tid == 0) a.count[first] = 0;
                 for (int i = tid; i < a.G * (D / 4); i += kRowThreads) {
                     const int r = i / (D / 4), d = (i % (D / 4)) * 4;
-                    float mm = -CUDART_INF_F;
-                    for (int c = first; c <= last; ++c)
-                        mm = fmaxf(mm, __ldcg(a.partial + (static_cast<int64_t>(c) * 2 + (c == first)) * kRowSlotFloats +
-                                              16 * 128 + r));
-                    const float safe = mm == -CUDART_INF_F ? 0.0f : mm;
-                    float ll = 0.0f;
+                    // (one pass with a running maximum, the loads of eight contributors in flight)
+                    float mm = -CUDART_INF_F, ll = 0.0f;
                     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-                    for (int c = first; c <= last; ++c) {
-                        const float* p = a.partial + (static_cast<int64_t>(c) * 2 + (c == first)) * kRowSlotFloats;
-                        const float f = exp2_approx(__ldcg(p + 16 * 128 + r) - safe);
-                        const float4 x = __ldcg(reinterpret_cast<const float4*>(p + r * D + d));
-                        ll += f * __ldcg(p + 16 * 128 + 16 + r);
-                        v.x += f * x.x;
-                        v.y += f * x.y;
-                        v.z += f * x.z;
-                        v.w += f * x.w;
+                    for (int c0 = first; c0 <= last; c0 += kJoinLoads) {
+                        float mx[kJoinLoads], lx[kJoinLoads], top = mm;
+                        float4 x[kJoinLoads];
+#pragma unroll
+                        for (int u = 0; u < kJoinLoads; ++u) {
+                            const int c = min(c0 + u, last);
+                            const float* p = a.partial + (static_cast<int64_t>(c) * 2 + (c == first)) * kRowSlotFloats;
+                            mx[u] = __ldcg(p + 16 * 128 + r);
+                            lx[u] = __ldcg(p + 16 * 128 + 16 + r);
+                            x[u] = __ldcg(reinterpret_cast<const float4*>(p + r * D + d));
+                        }
+#pragma unroll
+                        for (int u = 0; u < kJoinLoads; ++u) top = fmaxf(top, mx[u]);
+                        const float safe = top == -CUDART_INF_F ? 0.0f : top;
+                        const float f = exp2_approx(mm - safe);
+                        mm = top;
+                        ll *= f;
+                        v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+#pragma unroll
+                        for (int u = 0; u < kJoinLoads; ++u) {
+                            const float w = c0 + u <= last ? exp2_approx(mx[u] - safe) : 0.0f;
+                            ll += w * lx[u];
+                            v.x += w * x[u].x;
+                            v.y += w * x[u].y;
+                            v.z += w * x[u].z;
+                            v.w += w * x[u].w;
+                        }
                     }
                     finish(r, d, v, mm, ll);
                 }
