@@ -289,8 +289,8 @@ struct RowArgs {
 
 constexpr int kRowWarps = 8;
 // A segment's fixed time (its start, merge and result) in steps, as it counts in the CTAs' shares. 0, 1,
-// 2, 3: 64 sequences of 8192 keys at most x 32 heads 616, 591, 593, 596 us; 48 sequences in e4m3, 12
-// heads to a kv head 115, 104, 101, 102; one sequence of 131072 keys 92, 90, 89, 91.
+// 2, 3: 64 sequences of 8192 keys at most x 32 heads 617, 590, 591, 595 us; 48 sequences in e4m3, 12
+// heads to a kv head 118, 104, 100, 101; one sequence of 131072 keys 88, 87, 85, 88.
 constexpr int kSegmentStart = 2;
 constexpr int kRowThreads = 32 * kRowWarps;
 constexpr int kJoinLoads = 8;  // contributors of a split range whose sums a thread loads at once

@@ -533,10 +533,14 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         // Few items: tabulate their work (a block of time each for an item's start and its
         // result, and its blocks), and split it evenly where the longest item, or about half of
         // it in the last round, would keep the GPU waiting for more than a tenth over what the
-        // split's partial sums and joins cost (kJoinBlocks blocks of time, about 25 us). Whole items
-        // against a split, us: 4096 tokens of 32 heads 107, 122; 2048 of 32 heads with 8 kv heads
-        // 45, 50; 256 of them on 8192 keys 99, 50; two chunks of 1000 on 24000 e4m3 keys 786, 700.
-        constexpr int kJoinBlocks = 16;
+        // split's partial sums and joins cost: kJoinFew blocks of time where there is no more
+        // than an item for a CTA, kJoinMany where there are more (every CTA then has two pieces
+        // to hand over, and what was dealt would have filled the gaps). Whole items against a
+        // split, us: 4096 tokens of 32 heads 105, 123; 2048 of 32 heads with 8 kv heads 44, 50; 256
+        // of them on 8192 keys 99, 48; two chunks of 1000 on 24000 e4m3 keys 786, 655; of no more
+        // items than CTAs, 8 times 4 tokens on 4000 keys 45, 37; 2048 tokens of 12 heads of 64 30,
+        // 26; 3 times 700 on 3000 e4m3 keys 60, 67.
+        constexpr int kJoinFew = 8, kJoinMany = 16;
         const int n = static_cast<int>(work.items);
         for (int i = threadIdx.x; i < n; i += L::kThreads) {
             Piece p;
@@ -578,7 +582,8 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         const int g = static_cast<int>(gridDim.x);
         const int share = max((total + g - 1) / g, 1);
         const int whole = n <= g ? most : share + most / 2;
-        if (all == total && 10 * whole > 11 * (share + kJoinBlocks)) {
+        const int join = n <= g ? kJoinFew : kJoinMany;
+        if (all == total && 10 * whole > 11 * (share + join)) {
             work.split = true;
             work.per = share;
             work.at = static_cast<int64_t>(share) * blockIdx.x;
