@@ -387,9 +387,11 @@ TPMLP_API int tpmlp_backward_swiglu(tpmlp_ctx *ctx, const void *dZ, const void *
                                     void *dW2, void *db2, void *stream);
 
 /*
- * Read and clear the device status word that the kernels set when a bounded wait gives up
- * (synchronises `stream`). Returns TPMLP_OK, TPMLP_ERR_DEVICE_TIMEOUT or TPMLP_ERR_CUDA.
- * *detail (optional) receives the raw word: which barrier wait gave up.
+ * Read and clear the device status that the kernels set when a bounded wait gives up, or when an
+ * attention call meets a bad page (synchronises `stream`). Returns TPMLP_OK,
+ * TPMLP_ERR_DEVICE_TIMEOUT (outputs of a call since the last reading are incomplete, whatever else
+ * was reported), TPMLP_ERR_BAD_PAGE (the calls ended, without the bad pages' keys), INVALID_ARG
+ * or CUDA. *detail (optional) receives which barrier wait gave up, and 0x10000 after a bad page.
  */
 TPMLP_API int tpmlp_get_status(tpmlp_ctx *ctx, void *stream, int32_t *detail);
 

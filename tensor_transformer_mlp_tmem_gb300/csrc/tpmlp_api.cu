@@ -1019,8 +1019,8 @@ int create_context(tpmlp_ctx** out, int64_t H, int64_t F, int32_t k, uint32_t fl
         (second && (e = cudaMalloc(&c->W2p, static_cast<size_t>(H) * F * 2)) != cudaSuccess) ||
         (first && (e = cudaMalloc(&c->b1, parts1 * F * 4)) != cudaSuccess) ||
         (second && (e = cudaMalloc(&c->b2, static_cast<size_t>(H) * 4)) != cudaSuccess) ||
-        (e = cudaMalloc(&c->status, sizeof(int))) != cudaSuccess ||
-        (e = cudaMemset(c->status, 0, sizeof(int))) != cudaSuccess) {
+        (e = cudaMalloc(&c->status, kStatusWords * sizeof(int))) != cudaSuccess ||
+        (e = cudaMemset(c->status, 0, kStatusWords * sizeof(int))) != cudaSuccess) {
         rc = (e == cudaErrorMemoryAllocation) ? TPMLP_ERR_OOM : TPMLP_ERR_CUDA;
         tpmlp_destroy(c);
         return rc;
@@ -1553,14 +1553,16 @@ int tpmlp_get_status(tpmlp_ctx* c, void* stream, int32_t* detail) {
     if (int rc = check_device(c)) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     TPMLP_CUDA(c, cudaStreamSynchronize(s));
-    int v = 0;
-    TPMLP_CUDA(c, cudaMemcpy(&v, c->status, sizeof(int), cudaMemcpyDeviceToHost));
-    TPMLP_CUDA(c, cudaMemset(c->status, 0, sizeof(int)));
+    int v[kStatusWords] = {};
+    TPMLP_CUDA(c, cudaMemcpy(v, c->status, sizeof(v), cudaMemcpyDeviceToHost));
+    TPMLP_CUDA(c, cudaMemset(c->status, 0, sizeof(v)));
+    const bool any = v[0] != 0 || v[kBadPageWord] != 0;
     // an attention kernel that gave up may have left arrivals behind
-    if (v && c->attn_count) TPMLP_CUDA(c, cudaMemset(c->attn_count, 0, c->attn_counters * sizeof(uint32_t)));
-    if (detail) *detail = v;
-    if (v & kStatusBadPage) return TPMLP_ERR_BAD_PAGE;
-    return v ? TPMLP_ERR_DEVICE_TIMEOUT : TPMLP_OK;
+    if (any && c->attn_count) TPMLP_CUDA(c, cudaMemset(c->attn_count, 0, c->attn_counters * sizeof(uint32_t)));
+    if (detail) *detail = v[0] | (v[kBadPageWord] ? kStatusBadPage : 0);
+    // a wait that gave up left outputs unwritten: it is said first
+    if (v[0]) return TPMLP_ERR_DEVICE_TIMEOUT;
+    return v[kBadPageWord] ? TPMLP_ERR_BAD_PAGE : TPMLP_OK;
 }
 
 int tpmlp_packed_buffer(const tpmlp_ctx* c, int32_t which, const void** ptr, int64_t* bytes) {

@@ -283,9 +283,9 @@ int tpmlp_attn_create(tpmlp_ctx** out, int32_t Hq, int32_t Hkv, int32_t D, int32
     if ((e = cudaMalloc(&c->kv_scale, scales * sizeof(float))) != cudaSuccess ||
         (e = cudaMalloc(&c->attn_partial, partial * sizeof(float))) != cudaSuccess ||
         (e = cudaMalloc(&c->attn_count, counters * sizeof(uint32_t))) != cudaSuccess ||
-        (e = cudaMalloc(&c->status, sizeof(int))) != cudaSuccess ||
+        (e = cudaMalloc(&c->status, kStatusWords * sizeof(int))) != cudaSuccess ||
         (e = cudaMemset(c->attn_count, 0, counters * sizeof(uint32_t))) != cudaSuccess ||
-        (e = cudaMemset(c->status, 0, sizeof(int))) != cudaSuccess ||
+        (e = cudaMemset(c->status, 0, kStatusWords * sizeof(int))) != cudaSuccess ||
         (e = cudaMemcpy(c->kv_scale, ones, scales * sizeof(float), cudaMemcpyHostToDevice)) != cudaSuccess) {
         delete[] ones;
         tpmlp_destroy(c);

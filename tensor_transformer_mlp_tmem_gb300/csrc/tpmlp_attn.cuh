@@ -30,11 +30,11 @@ struct KvView {
     int32_t B;
     int32_t Hkv;
     const float* scales;  // e4m3: [2][Hkv] k and v scales
-    int* status;
+    int* status;          // kStatusWords
 };
 
 __device__ __forceinline__ void report_bad_page(int* status) {
-    atomicCAS(status, 0, kStatusBadPage);
+    *reinterpret_cast<volatile int*>(status + kBadPageWord) = 1;
 }
 
 // Keys of sequence b: its length held to [0, the table's capacity].

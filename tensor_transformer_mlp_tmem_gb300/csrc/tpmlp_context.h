@@ -102,13 +102,15 @@ struct tpmlp_ctx {
     uint32_t* attn_count = nullptr;  // arrivals at a split key range, one counter per CTA
     size_t attn_counters = 0;        // entries of attn_count
 
-    int* status = nullptr;  // device status word
+    int* status = nullptr;  // device status: kStatusWords
     int64_t launches = 0;
     std::string last_error;
 };
 
-// Bit of the device status word that marks a page table's bad entry; without it the word names
-// a wait that gave up.
+// The device status: word 0 names the first wait that gave up, word kBadPageWord is 1 after a bad
+// entry of a page table. Each is recorded whatever the other holds. tpmlp_get_status hands them out
+// as one number, word 0 with the bit kStatusBadPage.
+constexpr int kStatusWords = 2, kBadPageWord = 1;
 constexpr int kStatusBadPage = 0x10000;
 
 namespace tpmlp {

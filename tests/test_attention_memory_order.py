@@ -1,0 +1,74 @@
+"""Order of an attention context's own memory operations against the caller's streams, on a fake of
+the CUDA runtime (fake_cuda.h): what the library clears or fills on its own account is done before
+the call returns, so it can neither meet the work of a stream that does not wait for the default
+stream nor overwrite what that work has written."""
+import ctypes
+import os
+
+import pytest
+
+import tensor_transformer_mlp_tmem_gb300 as tp
+from tensor_transformer_mlp_tmem_gb300 import _build
+
+FAKE = os.path.join(os.path.dirname(os.path.abspath(__file__)), "fake_cuda.h")
+Hq, Hkv, D, PAGE = 8, 2, 128, 64
+SIDE = 4096  # a stream that does not block on the default one
+BAD_PAGE_BIT = 0x10000
+
+
+@pytest.fixture(scope="module")
+def lib(tmp_path_factory):
+    path = _build.build(out=str(tmp_path_factory.mktemp("fake") / "libtpmlp_fake.so"),
+                        extra_flags=["-include", FAKE])
+    h = ctypes.CDLL(path)
+    vp, i32 = ctypes.c_void_p, ctypes.c_int32
+    h.tpmlp_attn_create.argtypes = [ctypes.POINTER(vp), i32, i32, i32, i32, ctypes.c_uint32]
+    h.tpmlp_get_status.argtypes = [vp, vp, ctypes.POINTER(i32)]
+    h.tpmlp_destroy.argtypes = [vp]
+    h.fake_block.restype = vp
+    h.fake_block_bytes.restype = ctypes.c_int64
+    return h
+
+
+class Context:
+    """An attention context whose blocks the test reads and writes as a kernel would."""
+
+    def __init__(self, lib, flags=0):
+        first = lib.fake_blocks()
+        self.ctx = ctypes.c_void_p()
+        assert lib.tpmlp_attn_create(ctypes.byref(self.ctx), Hq, Hkv, D, PAGE, flags) == tp.TPMLP_OK
+        at = [(lib.fake_block(i), lib.fake_block_bytes(i)) for i in range(first, lib.fake_blocks())]
+        (scales, _), (_, _), (count, bytes_), (status, words) = at
+        self.scales = (ctypes.c_float * (2 * Hkv)).from_address(scales)
+        self.count = (ctypes.c_uint32 * (bytes_ // 4)).from_address(count)
+        self.word = (ctypes.c_int32 * (words // 4)).from_address(status)
+
+
+@pytest.fixture
+def context(lib):
+    c = Context(lib)
+    lib.fake_catch_up()
+    yield c
+    lib.tpmlp_destroy(c.ctx)
+
+
+def status(lib, c, stream=SIDE):
+    detail = ctypes.c_int32(-1)
+    return lib.tpmlp_get_status(c.ctx, stream, ctypes.byref(detail)), detail.value
+
+
+def test_a_bad_page_does_not_hide_a_wait_that_ran_out(lib, context):
+    """Both kinds of report stand beside each other, and the one that leaves outputs unwritten is
+    answered first."""
+    assert status(lib, context) == (tp.TPMLP_OK, 0)
+    lib.fake_catch_up()
+    context.word[1] = 1
+    assert status(lib, context) == (tp.TPMLP_ERR_BAD_PAGE, BAD_PAGE_BIT)
+    lib.fake_catch_up()
+    context.word[0], context.word[1] = 0x2005, 1
+    assert status(lib, context) == (tp.TPMLP_ERR_DEVICE_TIMEOUT, BAD_PAGE_BIT | 0x2005)
+    lib.fake_catch_up()
+    context.word[0] = 0x2005
+    assert status(lib, context) == (tp.TPMLP_ERR_DEVICE_TIMEOUT, 0x2005)
+    lib.fake_catch_up()
+    assert status(lib, context) == (tp.TPMLP_OK, 0)

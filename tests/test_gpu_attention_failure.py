@@ -81,3 +81,32 @@ def test_prompt_wait_runs_out_and_is_reported(lib, stall_lib, kv):
         assert torch.equal(out, want)
     finally:
         stall_lib.tpmlp_destroy(ctx)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_a_bad_page_does_not_hide_a_wait_that_ran_out(lib, stall_lib, kv):
+    """The call meets a page outside the pool in its first block of keys, then a wait runs out: the
+    caller is told that the call did not end, and of the page beside it."""
+    Hq, Hkv, D, page, new, longest = 4, 1, 128, 64, 3, 64000
+    c = ref.make(Hkv, D, page, kv, [longest], seed=42)
+    q = torch.zeros((new, Hq * D), dtype=torch.bfloat16, device="cuda")
+    K, V, table = c["K"].cuda(), c["V"].cuda(), c["table"].cuda()
+    table[0, 0] = -1
+    lens = torch.tensor([longest], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, new], dtype=torch.int32, device="cuda")
+    out = torch.zeros_like(q)
+    view = tp.KvCache(K=K.data_ptr(), V=V.data_ptr(), num_pages=K.shape[0], page_stride=0,
+                      page_table=table.data_ptr(), table_stride=0, table_pages=table.shape[1], B=1,
+                      lens=lens.data_ptr())
+    ctx, detail = ctypes.c_void_p(), ctypes.c_int32(0)
+    flags = tp.TPMLP_FLAG_KV_E4M3 if kv == "e4m3" else 0
+    assert stall_lib.tpmlp_attn_create(ctypes.byref(ctx), Hq, Hkv, D, page, flags) == 0
+    try:
+        torch.cuda.synchronize()
+        assert stall_lib.tpmlp_attn_prompt(ctx, q.data_ptr(), Hq * D, new, cu.data_ptr(), ctypes.byref(view),
+                                           0.1, 0, out.data_ptr(), Hq * D, None, None) == 0
+        assert stall_lib.tpmlp_get_status(ctx, None, ctypes.byref(detail)) == tp.TPMLP_ERR_DEVICE_TIMEOUT
+        assert detail.value & 0x10000 and detail.value & 0xFF00 == PROMPT_SITES, hex(detail.value)
+        assert stall_lib.tpmlp_get_status(ctx, None, ctypes.byref(detail)) == tp.TPMLP_OK
+    finally:
+        stall_lib.tpmlp_destroy(ctx)
