@@ -1552,13 +1552,18 @@ int tpmlp_get_status(tpmlp_ctx* c, void* stream, int32_t* detail) {
     if (!c) return TPMLP_ERR_INVALID_ARG;
     if (int rc = check_device(c)) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    TPMLP_CUDA(c, cudaStreamSynchronize(s));
+    // All on the caller's stream, and ended before the return: a reset on the default stream would
+    // run beside the next call's kernels on a stream that does not wait for it.
     int v[kStatusWords] = {};
-    TPMLP_CUDA(c, cudaMemcpy(v, c->status, sizeof(v), cudaMemcpyDeviceToHost));
-    TPMLP_CUDA(c, cudaMemset(c->status, 0, sizeof(v)));
+    TPMLP_CUDA(c, cudaMemcpyAsync(v, c->status, sizeof(v), cudaMemcpyDeviceToHost, s));
+    TPMLP_CUDA(c, cudaStreamSynchronize(s));
     const bool any = v[0] != 0 || v[kBadPageWord] != 0;
-    // an attention kernel that gave up may have left arrivals behind
-    if (any && c->attn_count) TPMLP_CUDA(c, cudaMemset(c->attn_count, 0, c->attn_counters * sizeof(uint32_t)));
+    if (any) TPMLP_CUDA(c, cudaMemsetAsync(c->status, 0, sizeof(v), s));
+    // An attention kernel that gave up may have left arrivals behind. (A bad page leaves none, and
+    // what is counted then may be a call's that runs on another stream.)
+    if (v[0] && c->attn_count)
+        TPMLP_CUDA(c, cudaMemsetAsync(c->attn_count, 0, c->attn_counters * sizeof(uint32_t), s));
+    if (any) TPMLP_CUDA(c, cudaStreamSynchronize(s));
     if (detail) *detail = v[0] | (v[kBadPageWord] ? kStatusBadPage : 0);
     // a wait that gave up left outputs unwritten: it is said first
     if (v[0]) return TPMLP_ERR_DEVICE_TIMEOUT;

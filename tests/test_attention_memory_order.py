@@ -72,3 +72,24 @@ def test_a_bad_page_does_not_hide_a_wait_that_ran_out(lib, context):
     assert status(lib, context) == (tp.TPMLP_ERR_DEVICE_TIMEOUT, 0x2005)
     lib.fake_catch_up()
     assert status(lib, context) == (tp.TPMLP_OK, 0)
+
+
+def test_status_is_cleared_before_the_next_call(lib, context):
+    """What a call enqueued on a side stream right after reports and counts stays; what the call that
+    gave up left at its joins is gone."""
+    context.word[0], context.count[7] = 0x2005, 3
+    assert status(lib, context) == (tp.TPMLP_ERR_DEVICE_TIMEOUT, 0x2005)
+    assert context.word[0] == 0 and context.count[7] == 0
+    context.word[0], context.count[9] = 0x2003, 2  # the next call's kernel
+    lib.fake_catch_up()
+    assert context.word[0] == 0x2003 and context.count[9] == 2
+
+
+@pytest.mark.parametrize("bad_page", [0, 1])
+def test_arrivals_of_a_call_that_runs_are_left_alone(lib, context, bad_page):
+    """Without a wait that ran out nothing is left behind, and the arrivals may be those of a call on
+    another stream."""
+    context.word[1], context.count[5] = bad_page, 2
+    assert status(lib, context)[0] == (tp.TPMLP_ERR_BAD_PAGE if bad_page else tp.TPMLP_OK)
+    lib.fake_catch_up()
+    assert context.count[5] == 2 and context.word[1] == 0
