@@ -286,7 +286,9 @@ int tpmlp_attn_create(tpmlp_ctx** out, int32_t Hq, int32_t Hkv, int32_t D, int32
         (e = cudaMalloc(&c->status, kStatusWords * sizeof(int))) != cudaSuccess ||
         (e = cudaMemset(c->attn_count, 0, counters * sizeof(uint32_t))) != cudaSuccess ||
         (e = cudaMemset(c->status, 0, kStatusWords * sizeof(int))) != cudaSuccess ||
-        (e = cudaMemcpy(c->kv_scale, ones, scales * sizeof(float), cudaMemcpyHostToDevice)) != cudaSuccess) {
+        (e = cudaMemcpy(c->kv_scale, ones, scales * sizeof(float), cudaMemcpyHostToDevice)) != cudaSuccess ||
+        // streams made without blocking do not wait for the default stream, where these run
+        (e = cudaStreamSynchronize(nullptr)) != cudaSuccess) {
         delete[] ones;
         tpmlp_destroy(c);
         cudaGetLastError();

@@ -61,8 +61,21 @@ inline cudaError_t set_async(void* p, int v, size_t n, cudaStream_t s) {
 }
 inline cudaError_t set(void* p, int v, size_t n) { return set_async(p, v, n, nullptr); }
 inline cudaError_t copy_async(void* to, const void* from, size_t n, cudaMemcpyKind kind, cudaStream_t s) {
-    queues[s].push_back([=] { std::memcpy(to, from, n); });
-    if (kind != cudaMemcpyDeviceToDevice) run(s);  // pageable host memory
+    if (kind == cudaMemcpyDeviceToDevice) {
+        queues[s].push_back([=] { std::memcpy(to, from, n); });
+        return cudaSuccess;
+    }
+    // Pageable host memory: the stream is waited for, then the copy made; one to the device may end
+    // after the call, from a buffer of the runtime's.
+    run(s);
+    if (kind == cudaMemcpyDeviceToHost) {
+        std::memcpy(to, from, n);
+    } else {
+        const auto* const bytes = static_cast<const uint8_t*>(from);
+        queues[s].push_back([to, staged = std::vector<uint8_t>(bytes, bytes + n)] {
+            std::memcpy(to, staged.data(), staged.size());
+        });
+    }
     return cudaSuccess;
 }
 inline cudaError_t copy(void* to, const void* from, size_t n, cudaMemcpyKind kind) {

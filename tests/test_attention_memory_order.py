@@ -93,3 +93,24 @@ def test_arrivals_of_a_call_that_runs_are_left_alone(lib, context, bad_page):
     assert status(lib, context)[0] == (tp.TPMLP_ERR_BAD_PAGE if bad_page else tp.TPMLP_OK)
     lib.fake_catch_up()
     assert context.count[5] == 2 and context.word[1] == 0
+
+
+@pytest.mark.parametrize("flags", [0, tp.TPMLP_FLAG_KV_E4M3])
+def test_a_new_context_is_ready_for_every_stream(lib, flags):
+    """What the first calls on a side stream set and count stays: nothing of the context's own set-up
+    is still to run."""
+    c = Context(lib, flags)
+    assert list(c.scales) == [1.0] * (2 * Hkv) and not any(c.count) and not any(c.word)
+    c.scales[1], c.count[3], c.word[0], c.word[1] = 0.5, 1, 0x2001, 1
+    lib.fake_catch_up()
+    assert (c.scales[1], c.count[3], c.word[0], c.word[1]) == (0.5, 1, 0x2001, 1)
+    lib.tpmlp_destroy(c.ctx)
+
+
+@pytest.mark.parametrize("which", range(4))
+def test_a_context_that_finds_no_memory_is_refused(lib, which):
+    lib.fake_fail_allocation(lib.fake_blocks() + which)
+    out = ctypes.c_void_p()
+    assert lib.tpmlp_attn_create(ctypes.byref(out), Hq, Hkv, D, PAGE, 0) == tp.TPMLP_ERR_OOM
+    assert out.value is None
+    lib.fake_catch_up()
