@@ -547,6 +547,22 @@ int ensure_y(tpmlp_ctx* c, int64_t rows) {
     return TPMLP_OK;
 }
 
+// The zeros that stand for "no bias" of dX; waited for, like the memsets of create_context.
+int ensure_zeros(tpmlp_ctx* c) {
+    if (c->zeros) return TPMLP_OK;
+    const size_t bytes = static_cast<size_t>(std::max(c->H, c->F)) * 4;
+    float* z = nullptr;
+    TPMLP_CUDA(c, cudaMalloc(&z, bytes));
+    cudaError_t e = cudaMemset(z, 0, bytes);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
+    if (e != cudaSuccess) {
+        cudaFree(z);
+        return fail_cuda(c, e, "zeros of the backward pass");
+    }
+    c->zeros = z;
+    return TPMLP_OK;
+}
+
 int check_tokens(int64_t B, int64_t S) {
     if (B < 0 || S < 0) return TPMLP_ERR_INVALID_ARG;
     if (S > 0 && B > (int64_t(1) << 31) / S) return TPMLP_ERR_UNSUPPORTED_SHAPE;
@@ -1036,6 +1052,11 @@ int create_context(tpmlp_ctx** out, int64_t H, int64_t F, int32_t k, uint32_t fl
         tpmlp_destroy(c);
         return rc;
     }
+    // the memsets run on the default stream, which streams made without blocking do not wait for
+    if (cudaStreamSynchronize(nullptr) != cudaSuccess) {
+        tpmlp_destroy(c);
+        return TPMLP_ERR_CUDA;
+    }
     *out = c;
     return TPMLP_OK;
 }
@@ -1370,11 +1391,7 @@ int tpmlp_backward(tpmlp_ctx* c, const void* dZ, const void* X, const void* Ysav
                           static_cast<const void*>(dW2), static_cast<const void*>(db2)})
         if (!aligned16(p)) return TPMLP_ERR_MISALIGNED;
     if ((rc = ensure_y(c, M))) return rc;  // the context's Y buffer holds dA
-    if (!c->zeros) {
-        const size_t n = static_cast<size_t>(std::max(c->H, c->F));
-        TPMLP_CUDA(c, cudaMalloc(&c->zeros, n * 4));
-        TPMLP_CUDA(c, cudaMemset(c->zeros, 0, n * 4));
-    }
+    if ((rc = ensure_zeros(c))) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
 
     // (1) dA = (dZ W2^T) * GeLU'(A): the first GEMM's tiling over the caller's W2 [F][H],
@@ -1468,11 +1485,7 @@ int tpmlp_backward_swiglu(tpmlp_ctx* c, const void* dZ, const void* X, const voi
         TPMLP_CUDA(c, cudaMalloc(&c->dgu, static_cast<size_t>(rows * 2 * F) * 2));
         c->dgu_elems = rows * 2 * F;
     }
-    if (!c->zeros) {
-        const size_t n = static_cast<size_t>(std::max(H, F));
-        TPMLP_CUDA(c, cudaMalloc(&c->zeros, n * 4));
-        TPMLP_CUDA(c, cudaMemset(c->zeros, 0, n * 4));
-    }
+    if ((rc = ensure_zeros(c))) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     // The non-gated context's tile choices: the pair kernel where the output width allows.
     const bool single = (c->flags & TPMLP_FLAG_SINGLE_SM) != 0;

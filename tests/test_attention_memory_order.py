@@ -19,7 +19,7 @@ BAD_PAGE_BIT = 0x10000
 @pytest.fixture(scope="module")
 def lib(tmp_path_factory):
     path = _build.build(out=str(tmp_path_factory.mktemp("fake") / "libtpmlp_fake.so"),
-                        extra_flags=["-include", FAKE])
+                        extra_flags=["-include", FAKE, "-DTPMLP_TEST_HOOKS"])
     h = ctypes.CDLL(path)
     vp, i32 = ctypes.c_void_p, ctypes.c_int32
     h.tpmlp_attn_create.argtypes = [ctypes.POINTER(vp), i32, i32, i32, i32, ctypes.c_uint32]
@@ -114,3 +114,37 @@ def test_a_context_that_finds_no_memory_is_refused(lib, which):
     assert lib.tpmlp_attn_create(ctypes.byref(out), Hq, Hkv, D, PAGE, 0) == tp.TPMLP_ERR_OOM
     assert out.value is None
     lib.fake_catch_up()
+
+
+def test_a_new_block_context_is_ready_for_every_stream(lib):
+    """The same of a block's context: its status and the counters of its split tiles."""
+    lib.tpmlp_create.argtypes = [ctypes.POINTER(ctypes.c_void_p), ctypes.c_int64, ctypes.c_int64, ctypes.c_int32,
+                                 ctypes.c_uint32]
+    first, ctx = lib.fake_blocks(), ctypes.c_void_p()
+    assert lib.tpmlp_create(ctypes.byref(ctx), 256, 1024, 2, 0) == tp.TPMLP_OK
+    blocks = range(first, lib.fake_blocks())
+    status_words, counters = [  # 8 bytes, and 152 tiles x 2 CTAs x a counter per epilogue warp
+        next((ctypes.c_int32 * (n // 4)).from_address(lib.fake_block(i))
+             for i in blocks for n in [lib.fake_block_bytes(i)] if wanted(n))
+        for wanted in (lambda n: n == 8, lambda n: n % (152 * 2 * 4) == 0 and 1 <= n // (152 * 2 * 4) <= 16)]
+    assert not any(status_words) and not any(counters)
+    status_words[0], counters[5] = 0x101, 7
+    lib.fake_catch_up()
+    assert status_words[0] == 0x101 and counters[5] == 7
+    lib.tpmlp_destroy(ctx)
+
+
+def test_the_backward_pass_has_its_zeros_on_every_stream(lib):
+    """The zeros that a backward pass makes on its first call hold before anything is enqueued (the
+    call itself ends at its first tensor map: there is no driver here)."""
+    lib.tpmlp_test_host_context.restype = ctypes.c_void_p
+    lib.tpmlp_test_set_current_device(0)
+    ctx = ctypes.c_void_p(lib.tpmlp_test_host_context(ctypes.c_int64(256), ctypes.c_int64(1024), 2, 0, 0, 1, 0))
+    first, at = lib.fake_blocks(), ctypes.c_void_p(1 << 20)
+    i64 = ctypes.c_int64
+    assert lib.tpmlp_backward(ctx, at, at, at, at, at, at, i64(1), i64(64), at, at, at, at, at,
+                              ctypes.c_void_p(SIDE)) != tp.TPMLP_OK
+    zeros = [i for i in range(first, lib.fake_blocks()) if lib.fake_block_bytes(i) == 4 * 1024]
+    assert len(zeros) == 1 and not any((ctypes.c_uint32 * 1024).from_address(lib.fake_block(zeros[0])))
+    lib.tpmlp_test_set_current_device(-1)
+    lib.tpmlp_destroy(ctx)
