@@ -844,7 +844,8 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
                         v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
 #pragma unroll
                         for (int u = 0; u < kJoinLoads; ++u) {
-                            const float w = c0 + u <= last ? exp2_approx(mx[u] - safe) : 0.0f;
+                            if (c0 + u > last) break;  // (not a weight of 0: an infinite sum stays infinite)
+                            const float w = exp2_approx(mx[u] - safe);
                             ll += w * lx[u];
                             v.x += w * x[u].x;
                             v.y += w * x[u].y;

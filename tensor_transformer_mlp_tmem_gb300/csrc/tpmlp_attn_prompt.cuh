@@ -381,7 +381,8 @@ __device__ __forceinline__ void join_rows(const PromptArgs& a, const Piece& p, i
             }
 #pragma unroll
             for (int u = 0; u < kAtOnce; ++u) {
-                const float f = x0 + u <= upto ? exp2_approx(w[u] - safe) : 0.0f;
+                if (x0 + u > upto) break;  // (not a weight of 0: an infinite sum stays infinite)
+                const float f = exp2_approx(w[u] - safe);
 #pragma unroll
                 for (int k = 0; k < kChunk / 4; ++k) {
                     v[4 * k] += f * y[u][k].x;
