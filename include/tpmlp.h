@@ -584,8 +584,9 @@ TPMLP_API int tpmlp_attn_decode(tpmlp_ctx *ctx, const void *Q, int64_t ldq, cons
  * tpmlp_attn_decode; a query at a negative position gets zeros and -infinity.
  *   T    rows of Q and Out    cu_q  device int32 [B + 1], from 0, not decreasing, at most T; rows
  *        outside every sequence are not written. Lse device fp32 [T][Hq] or NULL.
- * A value (V) that is not finite also reaches earlier queries of its own chunk, up to 2 * 128 / G
- * tokens back (its weight there is 0, and 0 times it is NaN); a key (K) does not.
+ * Keys and values that are not finite reach the queries that attend to them and no others (a value
+ * that reaches only some of a chunk's queries makes the kernel compute up to 2 * 128 / G of them
+ * twice).
  * One launch; T == 0 or B == 0 is a no-op.
  * Errors: as tpmlp_attn_decode.
  */

@@ -69,8 +69,8 @@ struct PromptSmem {
     static constexpr uint32_t kStage0 = 2 * kTile;
     static constexpr uint32_t kRaw0 = kStage0 + kStages * kTile;
     static constexpr uint32_t kBars = kRaw0 + kRaws * kRaw;
-    static constexpr int kNumBars = 2 * kStages + 2 * kRaws + 30;
-    static constexpr uint32_t kStore0 = kBars + (8 * kNumBars + 64 + 4 * 96 + 127) / 128 * 128;
+    static constexpr int kNumBars = 2 * kStages + 2 * kRaws + 32;
+    static constexpr uint32_t kStore0 = kBars + (8 * kNumBars + 64 + 2 * 96 + 127) / 128 * 128;
     static constexpr uint32_t kTables = kStore0 + 8 * 2048;  // 2 KB of output staging per softmax warp
     static constexpr uint32_t kTotal = 1024 + kTables + (kCoarse + 1) * 8 + (kPromptItems + 1) * 4 + 256;
     static_assert(kTotal <= 232448, "dynamic shared memory per CTA");
@@ -203,6 +203,8 @@ struct Piece {
     int b0, b1;            // blocks
     int first, last;       // contributing CTAs
     int starts;            // 1: the item's first blocks are in this piece
+    int redo;              // tiles (bits) found to need the careful way, 0 at first
+    int careful;           // 0, or the tiles whose results are made again, the careful way
     __device__ __forceinline__ int begin(int t) const { return max(lo[t], 2 * b0); }
     __device__ __forceinline__ int end(int t) const { return min(hi[t], 2 * b1); }
 };
@@ -234,6 +236,7 @@ __device__ __forceinline__ void item_blocks(const PromptArgs& a, Piece& p) {
         }
     }
     if (p.b1 == 0) p.b0 = 0;
+    p.redo = p.careful = 0;
 }
 
 // The CTA's work list. Items are numbered sequence by sequence; within a sequence in groups of
@@ -323,6 +326,105 @@ struct PromptWork {
         return p;
     }
 };
+
+// A value (V) that is not finite, at a key that some of an item's tokens see and others do not: the
+// product P V carries it to the others too (its weight is 0 there, and 0 times it is NaN). An item is
+// therefore computed as if there were none; a tile whose sums are not finite though its weights' are is
+// computed once more, the careful way: the MMA warps clear such values of such keys in the loaded
+// tile, and add_cleared adds them to the rows that see them (a weight above 0 times them is what
+// they are). The check costs 0 to 1.3 % (GPT-3-shaped prompt 321 and 321 us, the ragged batch 92.6 and
+// 93.8), and the work list's wait for it 0.4 us at the end of a call; with no values that are not
+// finite nothing else is done.
+// Keys [lo, hi) that all of the item's tokens see.
+struct SeenByAll {
+    int lo, hi;
+    __device__ __forceinline__ SeenByAll(const PromptArgs& a, const Piece& p)
+        : lo(prompt_lo_key(a, max(p.last_hi[0], p.last_hi[1]))), hi(p.seq.hi(p.tok0)) {}
+    __device__ __forceinline__ bool operator()(int key) const { return key >= lo && key < hi; }
+};
+template <bool FP8>
+__device__ __forceinline__ void clear_not_finite(uint4& v) {
+    constexpr uint32_t kExponent = FP8 ? 0x7C00u : 0x7F80u;  // fp16, bf16
+    uint32_t w[4] = {v.x, v.y, v.z, v.w}, found = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t lo = (w[e] & kExponent) == kExponent ? 0xFFFFu : 0u;
+        const uint32_t hi = ((w[e] >> 16) & kExponent) == kExponent ? 0xFFFF0000u : 0u;
+        w[e] &= ~(lo | hi);
+        found |= lo | hi;
+    }
+    if (found) v = make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Rows of V that no query of the item may see, in a group of 16 that the product reads: past the
+// item's last key, before its first (a window's), or in a page that is not there. Their weights are
+// 0, but 0 times what they hold may be NaN; they are cleared first (by both tiles' warps alike). The
+// careful way, so are values that are not finite, of keys that some tokens do not see.
+template <int D, bool FP8>
+__device__ __forceinline__ void clear_values(const PromptArgs& a, const Piece& p, uint8_t* block, int key0,
+                                             uint32_t have, int lane) {
+    constexpr int kLanes = D / 8;  // to a row, 16 bytes each per 64 columns
+    const int in = max(p.last_hi[0], p.last_hi[1]) - key0, low = p.lo_key - key0;
+    const bool careful = p.careful != 0;
+    const SeenByAll all(a, p);
+    const int upto = min(kPB, (in + 15) & ~15), piece = lane % kLanes;
+    for (int r = (have == 0xFFu && low <= 0 && !careful ? in : 0) + lane / kLanes; r < upto; r += 32 / kLanes) {
+        uint4& v = *reinterpret_cast<uint4*>(block + (piece >> 3) * 16384 + r * 128 + (piece & 7) * 16);
+        if (r >= in || r < low || !((have >> (r >> 4)) & 1u)) v = make_uint4(0, 0, 0, 0);
+        else if (careful && !all(key0 + r)) clear_not_finite<FP8>(v);
+    }
+}
+// (out of line for e4m3 caches, whose MMA warps have few registers)
+template <int D>
+__device__ __noinline__ void clear_values_e4m3(const PromptArgs& a, const Piece& p, uint8_t* block, int key0,
+                                               uint32_t have, int lane) {
+    clear_values<D, true>(a, p, block, key0, have, lane);
+}
+// The warp's 32 rows of O, at `to` in tensor memory; the lane's row sees keys [lo, hi).
+template <int D, bool FP8>
+__device__ __noinline__ void add_cleared(const PromptArgs& a, const Piece& p, int lo, int hi, uint32_t to) {
+    const int from = max(lo, p.b0 * kPB), upto = min(hi, p.b1 * kPB);
+    const SeenByAll all(a, p);
+#pragma unroll 1
+    for (int x = 0; x < D; x += 32) {
+        uint32_t o[32];
+        ptx::tmem_ld_32x32b_x32(to + x, o);
+        ptx::tmem_wait_ld(o);
+#pragma unroll 1
+        for (int key = from; key < upto; ++key) {
+            if (all(key)) key = all.hi;
+            if (key >= upto) break;
+            const int page = kv_page(a.kv, p.b, key);
+            if (page < 0) continue;
+            const int64_t slot = key & ((1 << a.kv.page_shift) - 1);
+            const uint8_t* src = a.kv.V + page * a.kv.page_bytes + p.h * a.kv.head_bytes + (slot * D + x) * (FP8 ? 1 : 2);
+#pragma unroll
+            for (int k = 0; k < (FP8 ? 2 : 4); ++k) {
+                const uint4 v = load16(src + 16 * k);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (FP8) {
+#pragma unroll
+                        for (int b = 0; b < 4; ++b)  // e4m3 has NaN and no infinity
+                            if (((w[e] >> (8 * b)) & 0x7Fu) == 0x7Fu) o[16 * k + 4 * e + b] = 0x7FFFFFFFu;
+                    } else {
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            const uint32_t f = b ? w[e] & 0xFFFF0000u : w[e] << 16;
+                            if ((f & 0x7F800000u) == 0x7F800000u) {
+                                uint32_t& y = o[8 * k + 2 * e + b];
+                                y = __float_as_uint(__uint_as_float(y) + __uint_as_float(f));
+                            }
+                        }
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        tmem_st_x32(to + x, o);
+    }
+    tmem_wait_st();
+}
 
 // The result of the first `count` rows of tile t of a split item, from its contributors' slots, first
 // to last. The tile's 128 threads call it (row: the thread's number), P to a row of the result, each
@@ -437,6 +539,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     auto piece_full = [&](int s) { return more + 160u + 8u * s; };
     auto piece_empty = [&](int s) { return more + 192u + 8u * s; };
     auto pv_done = [&](int t) { return more + 224u + 8u * t; };
+    auto checked = [&](int s) { return more + 240u + 8u * s; };  // both tiles' sums of a piece
     uint32_t* const ctl = reinterpret_cast<uint32_t*>(base_ptr + L::kBars + 8 * L::kNumBars);
     volatile uint32_t* const abort_flag = ctl + 1;
     uint32_t* const s_last = ctl + 2;      // [2]
@@ -474,6 +577,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         for (int s = 0; s < kPieces; ++s) {
             ptx::mbar_init(piece_full(s), 1);
             ptx::mbar_init(piece_empty(s), FP8 ? 19 : 11);
+            ptx::mbar_init(checked(s), 8);
         }
         ptx::mbar_init(q_empty, 2);
         ptx::mbar_init(drain, 2);
@@ -802,12 +906,28 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             };
             const float inv = l == 0.0f ? 0.0f : v_scale / l;  // no keys: zeros
             const bool any = end > begin;
+            // The tile has to be done again if a row's sums are not finite though its weights' is
+            // (one token to an item: all rows see the same keys).
+            const int careful = p->careful;
+            const bool suspect = any && mine && a.cu_q && !careful && l - l == 0.0f;
+            // (the other tile's result may stand already)
+            const bool give = p->tokens[t] > 0 && (!careful || ((careful >> t) & 1));
             if (any) {
                 if (!wait(o_full(t), o_phase, 3)) break;
                 o_phase ^= 1u;
                 ptx::tc_fence_after();
+                if (careful) add_cleared<D, FP8>(a, *p, lo, mine ? hi : 0, tmem_o(t) + lanes);
             }
-            if (p->tokens[t] > 0) {
+            float2 not_finite[4] = {};  // NaN once a sum is not finite
+            auto check = [&] {
+                const float2 x = add2(add2(not_finite[0], not_finite[1]), add2(not_finite[2], not_finite[3]));
+                if (suspect && !(x.x + x.y == 0.0f)) atomicOr(&const_cast<Piece*>(p)->redo, 1 << t);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(checked(piece_at % kPieces));
+            };
+            if (p->tokens[t] == 0) {
+                check();
+            } else {
 #pragma unroll 1
                 for (int col = 0; col < D; col += 64) {
                     uint32_t o[2][32];
@@ -821,10 +941,18 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                             __syncwarp();
                             if (lane == 0) mbar_arrive(o_empty(t));
                         }
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+#pragma unroll
+                            for (int k = 0; k < 32; k += 2)
+                                not_finite[k / 2 & 3] = fma2(make_float2(__uint_as_float(o[x][k]), __uint_as_float(o[x][k + 1])),
+                                                             make_float2(0.0f, 0.0f), not_finite[k / 2 & 3]);
                     } else {
 #pragma unroll
                         for (int k = 0; k < 32; ++k) o[0][k] = o[1][k] = 0u;
                     }
+                    if (col + 64 == D) check();
+                    if (!give) continue;
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         if (whole) {
@@ -843,8 +971,8 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 }
             }
             if (whole) {
-                put_lse(m, l);
-            } else if (p->tokens[t] > 0) {
+                if (give) put_lse(m, l);
+            } else if (give) {
                 // The last contributor to arrive sums all of them, first to last (see the row
                 // kernel); each tile's 128 threads count and join on their own.
                 if (mine) {
@@ -857,11 +985,14 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 if (warp == 4 * t) {
                     if (!wait(join_in(t), j_phase, 13)) break;
                     if (lane == 0) {
-                        __threadfence();
-                        const uint32_t n = atomicAdd(a.count + 2 * from + t, 1u);
-                        s_last[t] = n == static_cast<uint32_t>(upto - from);
-                        if (s_last[t]) a.count[2 * from + t] = 0;
-                        __threadfence();
+                        s_last[t] = 0;
+                        if (!((*const_cast<const volatile int*>(&p->redo) >> t) & 1)) {
+                            __threadfence();
+                            const uint32_t n = atomicAdd(a.count + 2 * from + t, 1u);
+                            s_last[t] = n == static_cast<uint32_t>(upto - from);
+                            if (s_last[t]) a.count[2 * from + t] = 0;
+                            __threadfence();
+                        }
                         mbar_arrive(join_out(t));
                     }
                     __syncwarp();
@@ -890,7 +1021,8 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             const Piece* p = next_piece();
             if (!p) break;
             const int b0 = p->b0, b1 = p->b1, begin = p->begin(t), end = p->end(t), last_hi = p->last_hi[t];
-            const int item_hi = max(p->last_hi[0], p->last_hi[1]), item_lo = p->lo_key;
+            const int item_hi = max(p->last_hi[0], p->last_hi[1]);
+            const int item_lo = p->careful ? INT_MAX : p->lo_key;  // (the careful way looks at every block)
             if (b1 > b0 || FP8) {
                 if (!(ok = wait(q_full(t), q_phase, 4))) break;
                 q_phase ^= 1u;
@@ -910,19 +1042,11 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 const uint64_t dv = sdesc_v(base + sv), dk = sdesc_k128(base + L::kStage0 + ks * L::kTile);
                 if (i > b0) {
                     if (!(ok = wait(full(vs), vph, 5))) break;
-                    // Rows of V that no query of the item may see, in a group of 16 that the
-                    // product reads: past the item's last key, before its first (a window's), or
-                    // in a page that is not there. Their weights are 0, but 0 times what they hold
-                    // may be NaN; they are cleared first (by both tiles' warps alike).
-                    const int in = item_hi - (i - 1) * kPB, low = item_lo - (i - 1) * kPB;
                     const uint32_t have = groups[(blocks + i - 1 - b0) & 7];
-                    if (in < kPB || low > 0 || have != 0xFFu) {
-                        constexpr int kLanes = D / 8;  // to a row, 16 bytes each per 64 columns
-                        const int upto = min(kPB, (in + 15) & ~15), piece = lane % kLanes;
-                        for (int r = (have == 0xFFu && low <= 0 ? in : 0) + lane / kLanes; r < upto; r += 32 / kLanes)
-                            if (r >= in || r < low || !((have >> (r >> 4)) & 1u))
-                                *reinterpret_cast<uint4*>(base_ptr + sv + (piece >> 3) * kHalf + r * 128 +
-                                                          (piece & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    if (item_hi < i * kPB || item_lo > (i - 1) * kPB || have != 0xFFu) {
+                        const Piece& q = *piece_of(piece_at);
+                        if constexpr (FP8) clear_values_e4m3<D>(a, q, base_ptr + sv, (i - 1) * kPB, have, lane);
+                        else clear_values<D, false>(a, q, base_ptr + sv, (i - 1) * kPB, have, lane);
                         fence_async_shared();
                         __syncwarp();
                     }
@@ -1098,12 +1222,37 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         __syncwarp();
     } else if (warp == 11) {
         // ------------------------------------------------------------ work list
+        bool ended = false;
+        uint32_t next_redo = 0;  // the piece after the last one to be done again
         for (;; ++piece_at) {
             // (an item is asked for only when there is room for it)
             if (!wait(piece_empty(piece_at % kPieces), ((piece_at / kPieces) & 1u) ^ 1u, 16)) break;
-            const Piece p = work.next(a);
+            // A piece that has to be done again, the careful way, is the next one: the one that was
+            // in this slot, or, with no more items, the one before, once its sums are known.
+            Piece p;
+            p.valid = 0;
+            auto redone = [&](uint32_t k) {
+                const Piece* const old = piece_of(k);
+                if (!old->redo || k + 1 == next_redo) return false;
+                p = *old;
+                p.careful = old->redo;
+                p.redo = 0;
+                next_redo = k + 1;
+                return true;
+            };
+            if (piece_at < kPieces || !redone(piece_at - kPieces)) {
+                if (!ended) p = work.next(a);
+                if (!p.valid) {
+                    ended = true;
+                    if (piece_at > 0) {
+                        if (!wait(checked((piece_at - 1) % kPieces), ((piece_at - 1) / kPieces) & 1u, 16)) break;
+                        redone(piece_at - 1);
+                    }
+                }
+            }
             if (lane == 0) {
-                *const_cast<Piece*>(piece_of(piece_at)) = p;
+                if (p.valid) *const_cast<Piece*>(piece_of(piece_at)) = p;
+                else const_cast<Piece*>(piece_of(piece_at))->valid = 0;
                 mbar_arrive(piece_full(piece_at % kPieces));
             }
             __syncwarp();
