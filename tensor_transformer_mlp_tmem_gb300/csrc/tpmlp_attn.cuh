@@ -349,6 +349,16 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
+// e4m3 caches: the power of two by which a query row is divided before it is rounded to fp16, from
+// the row's largest magnitude: that one comes to [2^14, 2^15), so that no bf16 value overflows and
+// only what is 2^-28 of it and less meets fp16's smallest steps. The scores are multiplied by it
+// again; it is held above 2^-100 so that it does not vanish with them. (Infinities stay infinite.)
+__device__ __forceinline__ int query_exponent(float largest) {
+    const int e = static_cast<int>(__float_as_uint(largest) >> 23) - 127 - 14;
+    return largest == 0.0f ? 0 : max(-100, min(e, 113));
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
 // Keys of a row: [lo, hi) of its sequence.
 struct RowRange {
     int lo, hi;
@@ -497,9 +507,8 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         const int n = static_cast<int>(at - segment_start) - kSegmentStart - step0;
         if (n <= 0) return;  // the start alone: the segment's steps are the next CTA's
 
-        // Q in the reduction order of the K pieces. In the 8-bit cache's fp16 products each row is
-        // scaled by a power of two to a largest magnitude in [1, 2), so that no bf16 value
-        // overflows; the scores are scaled back.
+        // Q in the reduction order of the K pieces; for an 8-bit cache's products in fp16, scaled
+        // (query_exponent), and the scores scaled back.
         uint32_t qr[NT][S::kQRegs];
         float c_log2[NT][2];  // score -> log2 units, for the lane's query columns 2 t, 2 t + 1
 #pragma unroll
@@ -533,12 +542,8 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
                     }
                 big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
                 big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
-                // exponent of the row's largest magnitude (rows of zeros, infinities and the ends of
-                // the exponent range stay as they are)
-                int e = static_cast<int>(__float_as_uint(big) >> 23) - 127;
-                if (e < -100 || e > 100) e = 0;
-                const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+                const int e = query_exponent(big);
+                const float down = power_of_two(-e), up = power_of_two(e);
 #pragma unroll
                 for (int j = 0; j < S::NK; ++j)
 #pragma unroll

@@ -743,8 +743,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             const int tok = p->tok0 + t * a.tpt + token;
             float c = a.scale_log2;
             if constexpr (FP8) {
-                // Q in fp16: the row scaled by a power of two to a largest magnitude in [1, 2)
-                // (see the row kernel); one thread converts its own row
+                // Q in fp16, scaled (query_exponent); one thread converts its own row
                 if (!wait(q_empty, q_phase ^ 1u, 1)) break;
                 q_phase ^= 1u;
                 const __nv_bfloat16* src = a.q + static_cast<int64_t>(p->seq.first + tok) * a.ldq +
@@ -759,10 +758,9 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 #pragma unroll
                     for (int j = 0; j < 8; ++j) big = fmaxf(big, fabsf(f[j]));
                 }
-                int e = static_cast<int>(__float_as_uint(big) >> 23) - 127;
-                if (e < -100 || e > 100) e = 0;
-                const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                c *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * a.kv.scales[p->h];
+                const int e = query_exponent(big);
+                const float down = power_of_two(-e);
+                c = c * a.kv.scales[p->h] * power_of_two(e);
                 uint8_t* const dst = base_ptr + t * L::kTile + row * 128;
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i) {
