@@ -849,13 +849,15 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
                         v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
 #pragma unroll
                         for (int u = 0; u < kJoinLoads; ++u) {
-                            if (c0 + u > last) break;  // (not a weight of 0: an infinite sum stays infinite)
-                            const float w = exp2_approx(mx[u] - safe);
+                            // past the last one, sums of 0 as well: a weight of 0 alone would make
+                            // NaN of an infinite sum (and a branch here would hold up the loads)
+                            const bool on = c0 + u <= last;
+                            const float w = on ? exp2_approx(mx[u] - safe) : 0.0f;
                             ll += w * lx[u];
-                            v.x += w * x[u].x;
-                            v.y += w * x[u].y;
-                            v.z += w * x[u].z;
-                            v.w += w * x[u].w;
+                            v.x += w * (on ? x[u].x : 0.0f);
+                            v.y += w * (on ? x[u].y : 0.0f);
+                            v.z += w * (on ? x[u].z : 0.0f);
+                            v.w += w * (on ? x[u].w : 0.0f);
                         }
                     }
                     finish(r, d, v, mm, ll);

@@ -332,9 +332,8 @@ struct PromptWork {
 // therefore computed as if there were none; a tile whose sums are not finite though its weights' are is
 // computed once more, the careful way: the MMA warps clear such values of such keys in the loaded
 // tile, and add_cleared adds them to the rows that see them (a weight above 0 times them is what
-// they are). The check costs 0 to 1.3 % (GPT-3-shaped prompt 321 and 321 us, the ragged batch 92.6 and
-// 93.8), and the work list's wait for it 0.4 us at the end of a call; with no values that are not
-// finite nothing else is done.
+// they are). Without such values that costs next to nothing (before and after, us: GPT-3-shaped
+// prompt 321, 321; ragged batch 94.4, 94.3; e4m3 chunks 657, 657; 61 tokens 7.75, 7.88).
 // Keys [lo, hi) that all of the item's tokens see.
 struct SeenByAll {
     int lo, hi;
@@ -483,14 +482,15 @@ __device__ __forceinline__ void join_rows(const PromptArgs& a, const Piece& p, i
             }
 #pragma unroll
             for (int u = 0; u < kAtOnce; ++u) {
-                if (x0 + u > upto) break;  // (not a weight of 0: an infinite sum stays infinite)
-                const float f = exp2_approx(w[u] - safe);
+                // past the last one, sums of 0 as well (see the row kernel)
+                const bool on = x0 + u <= upto;
+                const float f = on ? exp2_approx(w[u] - safe) : 0.0f;
 #pragma unroll
                 for (int k = 0; k < kChunk / 4; ++k) {
-                    v[4 * k] += f * y[u][k].x;
-                    v[4 * k + 1] += f * y[u][k].y;
-                    v[4 * k + 2] += f * y[u][k].z;
-                    v[4 * k + 3] += f * y[u][k].w;
+                    v[4 * k] += f * (on ? y[u][k].x : 0.0f);
+                    v[4 * k + 1] += f * (on ? y[u][k].y : 0.0f);
+                    v[4 * k + 2] += f * (on ? y[u][k].z : 0.0f);
+                    v[4 * k + 3] += f * (on ? y[u][k].w : 0.0f);
                 }
             }
         }
