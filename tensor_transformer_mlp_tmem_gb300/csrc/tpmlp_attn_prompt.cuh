@@ -28,6 +28,8 @@
 // a tile, for even and odd steps or for halves of a block, gained nothing (361 against 340; 439).
 #pragma once
 
+#include <cfloat>
+
 #include "tpmlp_attn.cuh"
 #include "tpmlp_gemm.cuh"
 
@@ -761,6 +763,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 const int e = query_exponent(big);
                 const float down = power_of_two(-e);
                 c = c * a.kv.scales[p->h] * power_of_two(e);
+                if (c == 0.0f) c = FLT_MIN;  // 0 times a masked score of -infinity would be NaN
                 uint8_t* const dst = base_ptr + t * L::kTile + row * 128;
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i) {

@@ -34,3 +34,22 @@ def test_queries_of_any_size_over_e4m3(lib, k, Hq, Hkv, D, page):
         got, lse = attn.prompt(q.cuda(), cu, cache, return_lse=True)
         ok(attn)
         check_rows(c, q, got, lse, prompt_spans(lens, new, 0)[::4] + [(1, 0, 0, 232)], Hq, D, 1.0 / math.sqrt(D))
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,page", [(4, 2, 128, 64), (40, 2, 64, 64)])
+def test_scores_too_small_for_fp32(lib, Hq, Hkv, D, page):
+    """A softmax scale and scales of the keys whose product is 0 in fp32: all weights are alike, and
+    masked keys stay masked."""
+    lens, new = [300, 17], [70, 17]
+    c = ref.make(Hkv, D, page, "e4m3", lens, seed=72)
+    c["ks"] = torch.full((Hkv,), 1e-8)
+    q = queries(87, Hq, D, 72)
+    cu = torch.tensor([0, 70, 87], dtype=torch.int32).cuda()
+    with tp.Attention(Hq, Hkv, D, page, kv_dtype="e4m3") as attn:
+        cache = on_device(c, attn)
+        got, lse = attn.decode(q[:2].cuda(), cache, scale=1e-38, return_lse=True)
+        ok(attn)
+        check_rows(c, q, got, lse, [(b, b, 0, n) for b, n in enumerate(lens)], Hq, D, 1e-38)
+        got, lse = attn.prompt(q.cuda(), cu, cache, scale=1e-38, return_lse=True)
+        ok(attn)
+        check_rows(c, q, got, lse, prompt_spans(lens, new, 0)[::4], Hq, D, 1e-38)
