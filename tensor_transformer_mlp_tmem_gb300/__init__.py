@@ -712,6 +712,9 @@ class Attention:
         q = attn.append(q, k, v, cache, pos, seq)                # rotate, write k and v
         out = attn.prompt(q, cu_q, cache)                        # a chunk of each sequence
         out = attn.decode(q, cache)                              # one token of each sequence
+
+    With stream=, a call runs there and not on the current stream: the caller orders the two (its
+    tensors have to be ready, and to live until the call has passed).
     """
 
     def __init__(self, Hq: int, Hkv: int, D: int, page_size: int = 64, kv_dtype: str = "bf16"):
@@ -799,6 +802,22 @@ class Attention:
                              f"{tuple(t.shape)}")
         return t.data_ptr()
 
+    @staticmethod
+    def _new(like, shape, stream, dtype=None):
+        """A result for a call on `stream`. Its memory is that stream's: memory that was freed on the
+        current one may have work pending there. The current stream, where the result is usually
+        read, is noted, so that the memory is not handed on before it has passed."""
+        if stream is None:
+            return like.new_empty(shape, dtype=dtype)
+        import torch
+        raw, current = _stream(stream) or 0, torch.cuda.current_stream()
+        if raw == current.cuda_stream:
+            return like.new_empty(shape, dtype=dtype)
+        with torch.cuda.stream(torch.cuda.ExternalStream(raw) if raw else torch.cuda.default_stream()):
+            t = like.new_empty(shape, dtype=dtype)
+        t.record_stream(current)
+        return t
+
     def append(self, q, k, v, cache, pos, seq=None, q_out=None, stream=None):
         """Writes k and v [T, Hkv * D] (k rotated) at positions pos [T] of sequences seq [T]
         (None: token t is sequence t's) and returns the rotated q [T, Hq * D] (in q_out; q_out=q
@@ -809,7 +828,7 @@ class Attention:
         if q is not None:
             ldq = self._rows(q, T, self._wq, "q")
             if q_out is None:
-                q_out = q.new_empty((T, self._wq))
+                q_out = self._new(q, (T, self._wq), stream)
             ldqo = self._rows(q_out, T, self._wq, "q_out")
             qp, op = q.data_ptr(), q_out.data_ptr()
         else:
@@ -831,9 +850,9 @@ class Attention:
         kv, B = cache._of(self), cache.B
         ldq = self._rows(q, B, self._wq, "q")
         if out is None:
-            out = q.new_empty((B, self._wq))
+            out = self._new(q, (B, self._wq), stream)
         ldo = self._rows(out, B, self._wq, "out")
-        lse = q.new_empty((B, self.Hq), dtype=self._float32) if return_lse else None
+        lse = self._new(q, (B, self.Hq), stream, self._float32) if return_lse else None
         _ATTEND.pack_into(self._args, 0, self.ctx or 0, q.data_ptr(), ldq, 0, 0, kv,
                           self._scale if scale is None else scale, window, out.data_ptr(), ldo,
                           lse.data_ptr() if return_lse else 0, _stream(stream) or 0)
@@ -850,9 +869,9 @@ class Attention:
         cu = self._ints(cu_q, cache.B + 1, "cu_q")
         ldq = self._rows(q, T, self._wq, "q")
         if out is None:
-            out = q.new_empty((T, self._wq))
+            out = self._new(q, (T, self._wq), stream)
         ldo = self._rows(out, T, self._wq, "out")
-        lse = q.new_empty((T, self.Hq), dtype=self._float32) if return_lse else None
+        lse = self._new(q, (T, self.Hq), stream, self._float32) if return_lse else None
         _ATTEND.pack_into(self._args, 0, self.ctx or 0, q.data_ptr(), ldq, T, cu, kv,
                           self._scale if scale is None else scale, window, out.data_ptr(), ldo,
                           lse.data_ptr() if return_lse else 0, _stream(stream) or 0)
