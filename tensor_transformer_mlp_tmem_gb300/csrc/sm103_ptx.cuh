@@ -51,22 +51,27 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
 }
 
 // Upper bound on any single pipeline wait. The longest legitimate wait is one output
-// tile's whole reduction (well under a millisecond at the largest shapes).
+// tile's whole reduction (well under a millisecond at the largest shapes). Test builds set a
+// shorter one (TPMLP_TEST_WAIT_NS).
+#ifndef TPMLP_TEST_WAIT_NS
 constexpr uint64_t kWaitLimitNs = 1000ull * 1000ull * 1000ull;  // 1 s
+#else
+constexpr uint64_t kWaitLimitNs = TPMLP_TEST_WAIT_NS;
+#endif
 
 // Wait until phase `parity` of the barrier has completed. Gives up -- returning false --
 // when another role of the CTA has already given up (*abort != 0) or when the wait has
-// lasted kWaitLimitNs; in the latter case it raises *abort and records `code` in the
+// lasted limit_ns; in the latter case it raises *abort and records `code` in the
 // device status word (first writer wins). Never traps, never spins forever.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort,
-                                          int* status, int code) {
+                                          int* status, int code, uint64_t limit_ns = kWaitLimitNs) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t spin = 1;; ++spin) {
         if (mbar_try_wait(bar, parity)) return true;
         if ((spin & 15u) == 0) {
             if (*abort) return false;
-            if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            if (globaltimer_ns() - t0 > limit_ns) {
                 *abort = 1u;
                 atomicCAS(status, 0, code);
                 return false;

@@ -40,6 +40,10 @@ constexpr int kSB = 64;           // keys per step: S has two buffers of 64 colu
 constexpr int kPromptItems = 1024;  // items whose sizes a CTA tabulates
 constexpr int kCoarse = 512;        // entries of the table of sequences
 constexpr int kPromptCode = 0x2000;  // wait sites: kPromptCode | role
+// Limit of the waits that last as long as another role's piece (2^24 blocks of keys at 2 us each, at
+// most). The roles that such a wait is for have the usual limit for every step of theirs, and end
+// this one at once when they give up.
+constexpr uint64_t kPieceWaitNs = 60ull * 1000 * 1000 * 1000;
 // fp32 values of a tile's partial sums: O in groups of 4 columns [D/4][128][4], m [128], l [128].
 constexpr int kPromptSlotFloats = 128 * 128 + 256;
 // A row's reference maximum follows its running maximum only when that has grown by more than
@@ -705,10 +709,10 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     auto tmem_o = [&](int t) { return tmem + 128u * t; };
     // The bounded wait reads the global timer, which takes longer than most waits here last: poll
     // for a while first.
-    auto wait = [&](uint32_t bar, uint32_t parity, int role) {
+    auto wait = [&](uint32_t bar, uint32_t parity, int role, uint64_t limit_ns = ptx::kWaitLimitNs) {
         bool done = false;
         for (int n = 0; n < 64 && !done; ++n) done = ptx::mbar_try_wait(bar, parity);
-        return __all_sync(~0u, done || ptx::mbar_wait(bar, parity, abort_flag, a.kv.status, kPromptCode | role));
+        return __all_sync(~0u, done || ptx::mbar_wait(bar, parity, abort_flag, a.kv.status, kPromptCode | role, limit_ns));
     };
 
     // The register split sums to what the block was launched with (384 x 168, 640 x 96).
@@ -722,7 +726,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         return reinterpret_cast<const Piece*>(reinterpret_cast<const uint8_t*>(pieces) + (k % kPieces) * 96);
     };
     auto next_piece = [&]() -> const Piece* {
-        if (!wait(piece_full(piece_at % kPieces), (piece_at / kPieces) & 1u, 15)) return nullptr;
+        if (!wait(piece_full(piece_at % kPieces), (piece_at / kPieces) & 1u, 15, kPieceWaitNs)) return nullptr;
         const Piece* p = piece_of(piece_at);
         return p->valid ? p : nullptr;
     };
@@ -746,7 +750,8 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             float c = a.scale_log2;
             if constexpr (FP8) {
                 // Q in fp16, scaled (query_exponent); one thread converts its own row
-                if (!wait(q_empty, q_phase ^ 1u, 1)) break;
+                // (a tile without rows gets here while the other one is at the piece before)
+                if (!wait(q_empty, q_phase ^ 1u, 1, kPieceWaitNs)) break;
                 q_phase ^= 1u;
                 const __nv_bfloat16* src = a.q + static_cast<int64_t>(p->seq.first + tok) * a.ldq +
                                            (static_cast<int64_t>(p->h) * a.G + head) * D;
@@ -1227,7 +1232,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         uint32_t next_redo = 0;  // the piece after the last one to be done again
         for (;; ++piece_at) {
             // (an item is asked for only when there is room for it)
-            if (!wait(piece_empty(piece_at % kPieces), ((piece_at / kPieces) & 1u) ^ 1u, 16)) break;
+            if (!wait(piece_empty(piece_at % kPieces), ((piece_at / kPieces) & 1u) ^ 1u, 16, kPieceWaitNs)) break;
             // A piece that has to be done again, the careful way, is the next one: the one that was
             // in this slot, or, with no more items, the one before, once its sums are known.
             Piece p;
@@ -1246,7 +1251,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 if (!p.valid) {
                     ended = true;
                     if (piece_at > 0) {
-                        if (!wait(checked((piece_at - 1) % kPieces), ((piece_at - 1) / kPieces) & 1u, 16)) break;
+                        if (!wait(checked((piece_at - 1) % kPieces), ((piece_at - 1) / kPieces) & 1u, 16, kPieceWaitNs)) break;
                         redone(piece_at - 1);
                     }
                 }

@@ -110,3 +110,53 @@ def test_a_bad_page_does_not_hide_a_wait_that_ran_out(lib, stall_lib, kv):
         assert stall_lib.tpmlp_get_status(ctx, None, ctypes.byref(detail)) == tp.TPMLP_OK
     finally:
         stall_lib.tpmlp_destroy(ctx)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_a_long_piece_is_not_taken_for_a_wait_that_ran_out(lib, tmp_path_factory, kv):
+    """Roles of the prompt kernel that have nothing to do wait for the others' whole piece, however
+    long its keys. Here each step's limit is 2 ms and a piece (409600 keys, all on one page) takes
+    longer, two of them to a CTA."""
+    path = _build.build(out=str(tmp_path_factory.mktemp("short") / "libtpmlp_short.so"),
+                        extra_flags=["-DTPMLP_TEST_WAIT_NS=2000000ull"])
+    dbg = ctypes.CDLL(path)
+    vp, i64, i32, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
+    dbg.tpmlp_attn_create.argtypes = [ctypes.POINTER(vp), i32, i32, i32, i32, ctypes.c_uint32]
+    dbg.tpmlp_attn_prompt.argtypes = [vp, vp, i64, i64, vp, ctypes.POINTER(tp.KvCache), f32, i32, vp, i64, vp, vp]
+    dbg.tpmlp_get_status.argtypes = [vp, vp, ctypes.POINTER(i32)]
+    dbg.tpmlp_destroy.argtypes = [vp]
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    H, D, page, B, keys = sms, 64, 256, 2, 1600 * 256
+    c = ref.make(H, D, page, kv, [page], seed=43, extra_pages=0)
+    q = torch.randn((B, H * D), generator=torch.Generator().manual_seed(43)).bfloat16()
+    K, V, qd = c["K"].cuda(), c["V"].cuda(), q.cuda()
+    table = torch.zeros((B, 1600), dtype=torch.int32, device="cuda")
+    lens = torch.full((B,), keys, dtype=torch.int32, device="cuda")
+    cu = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    out, lse = torch.zeros_like(qd), torch.zeros((B, H), device="cuda")
+    view = tp.KvCache(K=K.data_ptr(), V=V.data_ptr(), num_pages=K.shape[0], page_stride=0,
+                      page_table=table.data_ptr(), table_stride=0, table_pages=1600, B=B, lens=lens.data_ptr())
+    c["ks"] = c["vs"] = torch.ones(H)  # as a new context has them
+    scale = 0.02 / 60.0 if kv == "e4m3" else 0.02
+    ctx, detail = ctypes.c_void_p(), ctypes.c_int32(0)
+    assert dbg.tpmlp_attn_create(ctypes.byref(ctx), H, H, D, page, tp.TPMLP_FLAG_KV_E4M3 if kv == "e4m3" else 0) == 0
+    try:
+        torch.cuda.synchronize()
+        start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        start.record()
+        assert dbg.tpmlp_attn_prompt(ctx, qd.data_ptr(), H * D, B, cu.data_ptr(), ctypes.byref(view), scale, 0,
+                                     out.data_ptr(), H * D, lse.data_ptr(),
+                                     torch.cuda.current_stream().cuda_stream) == 0
+        end.record()
+        rc = dbg.tpmlp_get_status(ctx, torch.cuda.current_stream().cuda_stream, ctypes.byref(detail))
+        assert rc == tp.TPMLP_OK, f"{rc} ({detail.value:#x}) after {start.elapsed_time(end):.1f} ms"
+        assert start.elapsed_time(end) > 2 * 2.0  # the pieces outlasted the limit
+    finally:
+        dbg.tpmlp_destroy(ctx)
+    # the same weights over one page's keys. O is summed in 4 products a step, 25600 in all, each of
+    # which may drop 2^-23 of the sum, all one way at worst; the weights' sum in 6400 steps (2^-24)
+    for b in range(B):
+        o, l, spread, _ = ref.attend(c, 0, q[b].double().view(H, D), page, 0, scale)
+        tol = ref.out_tolerance(o, spread, kv) + (25600 * 2.0 ** -23 + 6400 * 2.0 ** -24) * spread
+        assert bool(((out[b].cpu().double().view(H, D) - o).abs() <= tol).all())
+        assert bool(((lse[b].cpu().double() - l - math.log(1600)).abs() <= 6400 * 2.0 ** -24 + 2.0 ** -14).all())
