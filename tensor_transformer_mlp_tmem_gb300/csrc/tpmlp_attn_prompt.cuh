@@ -1216,8 +1216,9 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             blocks += b1 - b0;
             release_piece();
         }
-        if (!ok && lane == 0) {
-            // wait for the copies still in flight before the CTA may exit
+        if ((!ok || *abort_flag) && lane == 0) {
+            // wait for the copies still in flight before the CTA may exit (also when another role
+            // gave up, and no piece came after the last one)
             for (uint32_t s = 0; s < NR && s < issued; ++s) {
                 const uint32_t last = s + ((issued - 1 - s) / NR) * NR;
                 ptx::mbar_wait_drain(FP8 ? raw_full(s) : full(s), (last / NR) & 1u);
