@@ -410,7 +410,7 @@ template <int D, bool FP8, int NT>
 __global__ void __launch_bounds__(kRowThreads, RowShape<D, FP8, NT>::kCtasPerSm)
 attn_row_kernel(const __grid_constant__ RowArgs a) {
     using S = RowShape<D, FP8, NT>;
-    extern __shared__ float smem[];
+    extern __shared__ __align__(16) float smem[];  // (read and written in float4)
     float* const sO = smem;                                       // [parts][rows][pitch]
     float* const sM = sO + kRowWarps * S::kRows * S::kPitch;      // [parts][rows]
     float* const sL = sM + kRowWarps * S::kRows;                  // [parts][rows]
