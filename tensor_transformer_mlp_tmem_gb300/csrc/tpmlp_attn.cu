@@ -113,7 +113,9 @@ int launch_rows(tpmlp_ctx* c, const tpmlp::RowArgs& a, cudaStream_t s) {
 
 template <int D, bool FP8>
 int run_rows_of(tpmlp_ctx* c, const tpmlp::RowArgs& a, cudaStream_t s) {
-    return a.G > 8 ? launch_rows<D, FP8, 2>(c, a, s) : launch_rows<D, FP8, 1>(c, a, s);
+    if constexpr (tpmlp::row_heads(D, FP8) > 8)
+        if (a.G > 8) return launch_rows<D, FP8, 2>(c, a, s);
+    return launch_rows<D, FP8, 1>(c, a, s);
 }
 
 int run_rows(tpmlp_ctx* c, const tpmlp::RowArgs& a, cudaStream_t s) {
@@ -376,13 +378,7 @@ int tpmlp_attn_decode(tpmlp_ctx* c, const void* Q, int64_t ldq, const tpmlp_kv* 
     if (int rc = check_attend(c, Q, ldq, kv, scale, Out, ldo, Lse)) return rc;
     tpmlp::RowArgs a = row_args(c, Q, ldq, kv, scale, window, Out, ldo, Lse);
     a.rows = kv->B;
-    // Wide head groups fill the tiles of the prompt kernel's products, which take the same time for
-    // any G; the row kernel's grows with every 8 heads. 64 sequences of 4096 keys, 8 kv heads, row
-    // kernel against prompt kernel, us: D = 128 in bf16, G = 8: 167, 188; 12: 220, 194; 16: 223, 189.
-    // In e4m3, G = 16: 135, 223. D = 64, G = 16: in bf16 114, 147; in e4m3 80, 194. With G = 24 the row
-    // kernel would take its keys twice: 388, 197 (D = 128) and 198, 161 (D = 64) in bf16, 238, 229
-    // and 153, 199 in e4m3; from G = 33 on three times and more.
-    if (a.G > 16 || (a.G > 8 && c->head_dim == 128 && !is_e4m3(c)))
+    if (a.G > tpmlp::row_heads(c->head_dim, is_e4m3(c)))
         return run_prompt(c, a, nullptr, kv->B, static_cast<cudaStream_t>(stream));
     return run_rows(c, a, static_cast<cudaStream_t>(stream));
 }

@@ -287,6 +287,15 @@ struct RowArgs {
     uint32_t* count;        // [CTAs] arrivals, 0 between launches
 };
 
+// Query heads to a kv head that this kernel takes, at most; decode of wider groups goes to the prompt
+// kernel, whose products' tiles they fill and which takes the same time for any G, while this
+// kernel's time grows with every 8 heads. 64 sequences of 4096 keys, 8 kv heads, this kernel against
+// the prompt kernel, us: D = 128 in bf16, G = 8: 167, 188; 12: 220, 194; 16: 223, 189. In e4m3,
+// G = 16: 135, 223. D = 64, G = 16: in bf16 114, 147; in e4m3 80, 194. With G = 24 this kernel would
+// take its keys twice: 388, 197 (D = 128) and 198, 161 (D = 64) in bf16, 238, 229 and 153, 199 in e4m3;
+// from G = 33 on three times and more.
+constexpr int row_heads(int D, bool fp8) { return D == 128 && !fp8 ? 8 : 16; }
+
 constexpr int kRowWarps = 8;
 // A segment's fixed time (its start, merge and result) in steps, as it counts in the CTAs' shares. 0, 1,
 // 2, 3: 64 sequences of 8192 keys at most x 32 heads 617, 590, 591, 595 us; 48 sequences in e4m3, 12
