@@ -101,10 +101,10 @@ int allow_smem(tpmlp_ctx* c, Kernel kern, uint32_t smem, std::atomic<uint64_t>& 
     return TPMLP_OK;
 }
 
-template <int D, bool FP8, int NT>
+template <int D, bool FP8, int NT, int PASSES>
 int launch_rows(tpmlp_ctx* c, const tpmlp::RowArgs& a, cudaStream_t s) {
     using S = tpmlp::RowShape<D, FP8, NT>;
-    auto kern = tpmlp::attn_row_kernel<D, FP8, NT>;
+    auto kern = tpmlp::attn_row_kernel<D, FP8, NT, PASSES>;
     static std::atomic<uint64_t> done{0};
     if (int rc = allow_smem(c, kern, S::kSmem, done)) return rc;
     const int grid = c->num_sms * S::kCtasPerSm;
@@ -113,9 +113,11 @@ int launch_rows(tpmlp_ctx* c, const tpmlp::RowArgs& a, cudaStream_t s) {
 
 template <int D, bool FP8>
 int run_rows_of(tpmlp_ctx* c, const tpmlp::RowArgs& a, cudaStream_t s) {
+    if constexpr (tpmlp::row_heads(D, FP8) > 16)
+        if (a.G > 16) return launch_rows<D, FP8, 2, 2>(c, a, s);
     if constexpr (tpmlp::row_heads(D, FP8) > 8)
-        if (a.G > 8) return launch_rows<D, FP8, 2>(c, a, s);
-    return launch_rows<D, FP8, 1>(c, a, s);
+        if (a.G > 8) return launch_rows<D, FP8, 2, 1>(c, a, s);
+    return launch_rows<D, FP8, 1, 1>(c, a, s);
 }
 
 int run_rows(tpmlp_ctx* c, const tpmlp::RowArgs& a, cudaStream_t s) {
@@ -433,5 +435,10 @@ extern "C" TPMLP_API tpmlp_ctx* tpmlp_test_attn_context(int32_t Hq, int32_t Hkv,
     c->head_dim = D;
     c->page_size = page_size;
     return c;
+}
+
+// Test builds only: whether decode of G heads to a kv head takes the row kernel.
+extern "C" TPMLP_API int tpmlp_test_decode_on_rows(int32_t G, int32_t D, uint32_t flags) {
+    return G <= tpmlp::row_heads(D, (flags & TPMLP_FLAG_KV_E4M3) != 0);
 }
 #endif

@@ -289,12 +289,13 @@ struct RowArgs {
 
 // Query heads to a kv head that this kernel takes, at most; decode of wider groups goes to the prompt
 // kernel, whose products' tiles they fill and which takes the same time for any G, while this
-// kernel's time grows with every 8 heads. 64 sequences of 4096 keys, 8 kv heads, this kernel against
-// the prompt kernel, us: D = 128 in bf16, G = 8: 167, 188; 12: 220, 194; 16: 223, 189. In e4m3,
-// G = 16: 135, 223. D = 64, G = 16: in bf16 114, 147; in e4m3 80, 194. With G = 24 this kernel would
-// take its keys twice: 388, 197 (D = 128) and 198, 161 (D = 64) in bf16, 238, 229 and 153, 199 in e4m3;
-// from G = 33 on three times and more.
-constexpr int row_heads(int D, bool fp8) { return D == 128 && !fp8 ? 8 : 16; }
+// kernel's time grows with every 8 heads, and from 17 on it takes its keys twice (PASSES; the second
+// time from L2). 64 sequences of 4096 keys, 8 kv heads, this kernel against the prompt kernel, us:
+//   D = 128, bf16: G = 8: 165, 188; 9: 215, 190; 16: 216, 187; 24: 417, 192
+//   D = 128, e4m3: G = 16: 130, 223; 17: 244, 212; 32: 249, 214
+//   D = 64, bf16:  G = 16: 112, 147; 17: 208, 147; 32: 210, 146
+//   D = 64, e4m3:  G = 16: 77, 194; 17: 125, 191; 32: 129, 191; from G = 33 on three times and more
+constexpr int row_heads(int D, bool fp8) { return D == 128 ? (fp8 ? 16 : 8) : (fp8 ? 32 : 16); }
 
 constexpr int kRowWarps = 8;
 // A segment's fixed time (its start, merge and result) in steps, as it counts in the CTAs' shares. 0, 1,
@@ -415,7 +416,7 @@ __device__ __forceinline__ int v_dim(int g, int e) {
     else return (D / 8) * g + e;
 }
 
-template <int D, bool FP8, int NT>
+template <int D, bool FP8, int NT, int PASSES>
 __global__ void __launch_bounds__(kRowThreads, RowShape<D, FP8, NT>::kCtasPerSm)
 attn_row_kernel(const __grid_constant__ RowArgs a) {
     using S = RowShape<D, FP8, NT>;
@@ -435,9 +436,9 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
     auto steps_of = [&](const RowRange& x) {
         return max(1, (x.hi - (x.lo & ~15) + S::kStep - 1) / S::kStep);
     };
-    // Sum of the rows' work: a (row, kv head) segment's is its row's steps and kSegmentStart, and each
-    // CTA takes an equal run of all segments' work. Then the row that holds this CTA's first unit.
-    const int64_t per_row = a.kv.Hkv;
+    // Sum of the rows' work: a (row, kv head, pass) segment's is its row's steps and kSegmentStart, and
+    // each CTA takes an equal run of all segments' work. Then the row that holds this CTA's first unit.
+    const int64_t per_row = static_cast<int64_t>(a.kv.Hkv) * PASSES;
     int64_t per_cta, at, end;
     int row = -1;
     int64_t row_start = 0;  // first unit of that row
@@ -503,11 +504,11 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
     RowRange range = row_range(a, row);
     int steps = steps_of(range);
     int64_t segment_start;  // first unit of the current segment
-    int h;                  // kv head
+    int part;               // kv head * PASSES + pass
     {
         const int64_t into = at - row_start;
-        h = static_cast<int>(into / (steps + kSegmentStart));
-        segment_start = row_start + static_cast<int64_t>(h) * (steps + kSegmentStart);
+        part = static_cast<int>(into / (steps + kSegmentStart));
+        segment_start = row_start + static_cast<int64_t>(part) * (steps + kSegmentStart);
     }
 
     while (at < end) {
@@ -515,6 +516,9 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         at = min(end, segment_start + steps + kSegmentStart);
         const int n = static_cast<int>(at - segment_start) - kSegmentStart - step0;
         if (n <= 0) return;  // the start alone: the segment's steps are the next CTA's
+        const int h = part / PASSES;
+        const int q0 = part % PASSES * S::kRows;  // the pass's query heads of the group
+        auto heads = [&] { return PASSES > 1 ? min(a.G - q0, S::kRows) : a.G; };  // of them
 
         // Q in the reduction order of the K pieces; for an 8-bit cache's products in fp16, scaled
         // (query_exponent), and the scores scaled back.
@@ -523,8 +527,8 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int qi = nt * 8 + g;
-            const __nv_bfloat16* src = a.q + row * a.ldq + (static_cast<int64_t>(h) * a.G + qi) * D;
-            const bool on = qi < a.G;
+            const __nv_bfloat16* src = a.q + row * a.ldq + (static_cast<int64_t>(h) * a.G + q0 + qi) * D;
+            const bool on = qi < heads();
             if constexpr (!FP8) {
 #pragma unroll
                 for (int j = 0; j < S::NK; ++j) {
@@ -784,7 +788,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         const float v_scale = FP8 ? a.kv.scales[a.kv.Hkv + h] : 1.0f;
 
         auto finish = [&](int r, int d, float4 v, float mm, float ll) {
-            const int64_t head = static_cast<int64_t>(h) * a.G + r;
+            const int64_t head = static_cast<int64_t>(h) * a.G + q0 + r;
             const float inv = ll == 0.0f ? 0.0f : v_scale / ll;  // no keys: zeros
             uint2 w;
             w.x = pack_bf162(v.x * inv, v.y * inv);
@@ -795,7 +799,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
                     ll == 0.0f ? -CUDART_INF_F
                                : (mm + log2f(ll) - (FP8 ? kRowRaise : 0.0f)) * 0.69314718055994531f;
         };
-        for (int i = tid; i < a.G * (D / 4); i += kRowThreads) {
+        for (int i = tid; i < heads() * (D / 4); i += kRowThreads) {
             const int r = i / (D / 4), d = (i % (D / 4)) * 4;
             float mm = -CUDART_INF_F;
 #pragma unroll
@@ -833,7 +837,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
             if (s_last) {
                 __threadfence();
                 if (tid == 0) a.count[first] = 0;
-                for (int i = tid; i < a.G * (D / 4); i += kRowThreads) {
+                for (int i = tid; i < heads() * (D / 4); i += kRowThreads) {
                     const int r = i / (D / 4), d = (i % (D / 4)) * 4;
                     // (one pass with a running maximum, the loads of eight contributors in flight)
                     float mm = -CUDART_INF_F, ll = 0.0f;
@@ -876,8 +880,8 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
 
         // the next segment
         segment_start += steps + kSegmentStart;
-        if (++h == a.kv.Hkv) {
-            h = 0;
+        if (++part == a.kv.Hkv * PASSES) {
+            part = 0;
             if (++row < a.rows) {
                 range = row_range(a, row);
                 steps = steps_of(range);

@@ -138,3 +138,18 @@ def test_prompt_of_groups_of_more_than_64(lib, kv, Hq, Hkv, D, page, lens, new, 
         got, lse = attn.prompt(q.cuda(), cu, on_device(c, attn), window=window, return_lse=True)
         ok(attn)
     check_rows(c, q, got, lse, prompt_spans(lens, new, window)[::3], Hq, D, 1.0 / math.sqrt(D))
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(17, 1), (72, 3), (64, 2)])
+def test_decode_in_two_passes_over_the_heads(lib, Hq, Hkv):
+    """Groups of 17 to 32 heads of 64 over an e4m3 cache, sequences of no, few and many keys."""
+    lens = [9000, 0, 1, 130, 4097] + [(11 * b) % 90 for b in range(40)]
+    c = ref.make(Hkv, 64, 32, "e4m3", lens, seed=94)
+    q = queries(len(lens), Hq, 64, 94)
+    with tp.Attention(Hq, Hkv, 64, 32, kv_dtype="e4m3") as attn:
+        cache = on_device(c, attn)
+        for window in (0, 77):
+            got, lse = attn.decode(q.cuda(), cache, window=window, return_lse=True)
+            ok(attn)
+            spans = [(b, b, max(0, n - window) if window else 0, n) for b, n in enumerate(lens)]
+            check_rows(c, q, got, lse, spans, Hq, 64, 0.125)
