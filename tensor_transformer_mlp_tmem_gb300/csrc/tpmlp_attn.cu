@@ -74,9 +74,9 @@ tpmlp::KvView view_of(const tpmlp_ctx* c, const tpmlp_kv* kv) {
 
 // Launch with programmatic stream serialisation (the kernels wait in griddep_wait before they
 // touch global memory).
-template <typename Kernel, typename Args>
+template <typename Kernel, typename... Args>
 int launch(tpmlp_ctx* c, Kernel kern, int64_t grid, int threads, uint32_t smem, cudaStream_t s,
-           const Args& args) {
+           const Args&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
     cfg.blockDim = dim3(threads, 1, 1);
@@ -87,7 +87,7 @@ int launch(tpmlp_ctx* c, Kernel kern, int64_t grid, int threads, uint32_t smem, 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    TPMLP_CUDA(c, cudaLaunchKernelEx(&cfg, kern, args));
+    TPMLP_CUDA(c, cudaLaunchKernelEx(&cfg, kern, args...));
     ++c->launches;
     return TPMLP_OK;
 }
@@ -132,19 +132,7 @@ int launch_prompt(tpmlp_ctx* c, const CUtensorMap& q, const CUtensorMap& k, cons
     auto kern = tpmlp::attn_prompt_kernel<D, FP8>;
     static std::atomic<uint64_t> done{0};
     if (int rc = allow_smem(c, kern, S::kTotal, done)) return rc;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(c->num_sms), 1, 1);
-    cfg.blockDim = dim3(S::kThreads, 1, 1);
-    cfg.dynamicSmemBytes = S::kTotal;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    TPMLP_CUDA(c, cudaLaunchKernelEx(&cfg, kern, q, k, v, a));
-    ++c->launches;
-    return TPMLP_OK;
+    return launch(c, kern, c->num_sms, S::kThreads, S::kTotal, s, q, k, v, a);
 }
 
 // The pool as [page][Hkv * page size][D], in boxes of 64 columns and one page's (at most a
