@@ -390,7 +390,8 @@ TPMLP_API int tpmlp_backward_swiglu(tpmlp_ctx *ctx, const void *dZ, const void *
  * Read and clear the device status that the kernels set when a bounded wait gives up, or when an
  * attention call meets a bad page (synchronises `stream`). Returns TPMLP_OK,
  * TPMLP_ERR_DEVICE_TIMEOUT (outputs of a call since the last reading are incomplete, whatever else
- * was reported), TPMLP_ERR_BAD_PAGE (the calls ended, without the bad pages' keys), INVALID_ARG
+ * was reported; reading it also clears what an attention call left at its joins, so that the next
+ * calls are right), TPMLP_ERR_BAD_PAGE (the calls ended, without the bad pages' keys), INVALID_ARG
  * or CUDA. *detail (optional) receives which barrier wait gave up, and 0x10000 after a bad page.
  */
 TPMLP_API int tpmlp_get_status(tpmlp_ctx *ctx, void *stream, int32_t *detail);
@@ -567,9 +568,12 @@ TPMLP_API int tpmlp_attn_append(tpmlp_ctx *ctx, const void *Q, int64_t ldq, cons
  *   Lse  device fp32 [B][Hq] or NULL: log of the sum over j of exp(scale * <Q, K_j>), for joining
  *        with attention over other keys
  * A sequence without keys gets zeros and an Lse of -infinity. Sums and softmax statistics are
- * fp32; the work is split evenly over the GPU whatever the lengths, and split sequences are
- * joined in a fixed order (deterministic). Keys in pages outside the pool are left out and
- * reported (TPMLP_ERR_BAD_PAGE from tpmlp_get_status). One launch; B == 0 is a no-op.
+ * fp32. The work is split evenly over the GPU whatever the lengths, and split sequences are
+ * joined in a fixed order (deterministic). The exception: wide groups (G > 8 for bf16 with D = 128,
+ * G > 32 for e4m3 with D = 64, else G > 16) with B * Hkv > 1024, where a sequence's kv head is dealt
+ * to the SMs as a whole, and one long sequence among many takes its own time. Keys in pages outside the pool are left out and
+ * reported (TPMLP_ERR_BAD_PAGE from tpmlp_get_status). With a bf16 cache the weights are rounded to
+ * bf16 for the product with V, with an e4m3 cache to fp16. One launch; B == 0 is a no-op.
  * Errors: INVALID_ARG (also scale not positive and finite), MISALIGNED, UNSUPPORTED_SHAPE, CUDA.
  */
 TPMLP_API int tpmlp_attn_decode(tpmlp_ctx *ctx, const void *Q, int64_t ldq, const tpmlp_kv *kv,

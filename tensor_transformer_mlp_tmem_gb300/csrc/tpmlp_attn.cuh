@@ -696,8 +696,8 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
                     }
                 }
             }
-            // P^T, rounded to 16 bits (half a step of a weight); its sum is taken before the
-            // rounding, in fp32
+            // P^T, rounded to 16 bits for the product with V, of V's type: half a step of a weight is
+            // 2^-8 of it in bf16, 2^-11 in fp16. Its sum is taken before the rounding, in fp32.
             uint32_t pb[S::kSub][NT][2];
 #pragma unroll
             for (int u = 0; u < S::kSub; ++u)

@@ -16,16 +16,18 @@
 // per tile issues MMAs because each waits for several barriers a step: with one warp for both
 // tiles the tensor core idled during those waits.
 //
-// What bounds it (GPT-3-shaped prompt, 4096 tokens x 96 heads of 128: 300-320 us, 1.3 PFLOP/s, about
-// 70 % of the measured bf16 rate, at the board's power limit): two bounds lie close together. A
-// softmax step takes a warp about 1300 cycles, most of them issue slots that the tiles' warps share,
-// so 128 keys of both tiles take 2600; and their products 2048 cycles of the tensor core, which
-// S's 64 columns stretch (Q is read again for every 64 keys, and shared memory feeds the tensor core
-// at 128 bytes a cycle). Leaving out all exponentials, half of Q K^T or half of P V changed the time
-// by 3 to 4 % each. Steps of 64 keys with two buffers of S per tile let a softmax follow the one
-// before it at once; with steps of 128 and one buffer (S, P and both O fill tensor memory) every
-// softmax waited for the two products before it: 416 against 486 us. Two groups of softmax warps to
-// a tile, for even and odd steps or for halves of a block, gained nothing (361 against 340; 439).
+// What bounds it (GPT-3-shaped prompt, 4096 tokens x 96 heads of 128: 305-324 us, 1.3 PFLOP/s,
+// about two thirds of the measured bf16 rate, at the board's power limit): two bounds lie close
+// together. A softmax step takes a warp about 1300 cycles, so 128 keys of both tiles take 2600.
+// That is a chain of latencies (load of S, maximum, weights, store, one after the other) more than
+// of issue slots: two such warps share a scheduler, which issues about 0.55 instructions a cycle.
+// And their products take 2048 cycles of the tensor core, which S's 64 columns stretch (Q is read
+// again for every 64 keys, and shared memory feeds the tensor core at 128 bytes a cycle). Leaving
+// out all exponentials, half of Q K^T or half of P V changed the time by 3 to 4 % each. Steps of
+// 64 keys with two buffers of S per tile let a softmax follow the one before it at once; with
+// steps of 128 and one buffer (S, P and both O fill tensor memory) every softmax waited for the
+// two products before it: 416 against 486 us. Two groups of softmax warps to a tile, for even and
+// odd steps or for halves of a block, gained nothing (361 against 340; 439).
 #pragma once
 
 #include <cfloat>
@@ -248,7 +250,8 @@ __device__ __forceinline__ void item_blocks(const PromptArgs& a, Piece& p) {
 // The CTA's work list. Items are numbered sequence by sequence; within a sequence in groups of
 // kv heads, so that the heads in flight keep their K and V in L2, and within a group from the last
 // tokens (most keys) to the first. A group has two items or more for each CTA: with one, a last
-// group's largest items were started when little else was left (GPT-3-shaped prompt: 326 us, so 302).
+// group's largest items were started when little else was left (GPT-3-shaped prompt: 326 us, so 302, on
+// the box of that day; 305-324 since).
 struct PromptWork {
     const int64_t* coarse;  // items before each run of `run` sequences
     const int* units;       // work before each item (split lists)
@@ -339,7 +342,7 @@ struct PromptWork {
 // computed once more, the careful way: the MMA warps clear such values of such keys in the loaded
 // tile, and add_cleared adds them to the rows that see them (a weight above 0 times them is what
 // they are). Without such values that costs next to nothing (before and after, us: GPT-3-shaped
-// prompt 321, 321; ragged batch 94.4, 94.3; e4m3 chunks 657, 657; 61 tokens 7.75, 7.88).
+// prompt 321, 321; ragged batch 94.4, 94.2; e4m3 chunks 657, 657; 61 tokens 7.7, 7.9-8.0).
 // Keys [lo, hi) that all of the item's tokens see.
 struct SeenByAll {
     int lo, hi;
@@ -860,6 +863,9 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     e.x = exp2_approx(e.x);
                     e.y = exp2_approx(e.y);
                     sum[k & 1] = add2(sum[k & 1], e);
+                    // rounded to 16 bits for the product with V, of V's type (both operands of these
+                    // instructions have one type): half a step of a weight is 2^-8 of it in bf16,
+                    // 2^-11 in fp16; its sum is taken before
                     w[k] = FP8 ? pack_half2(e.x, e.y) : pack_bf162(e.x, e.y);
                 }
                 tmem_st_x32(ts, w);
