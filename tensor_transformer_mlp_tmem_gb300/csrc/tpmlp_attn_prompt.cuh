@@ -250,8 +250,8 @@ __device__ __forceinline__ void item_blocks(const PromptArgs& a, Piece& p) {
 // The CTA's work list. Items are numbered sequence by sequence; within a sequence in groups of
 // kv heads, so that the heads in flight keep their K and V in L2, and within a group from the last
 // tokens (most keys) to the first. A group has two items or more for each CTA: with one, a last
-// group's largest items were started when little else was left (GPT-3-shaped prompt: 326 us, so 302, on
-// the box of that day; 305-324 since).
+// group's largest items were started when little else was left (GPT-3-shaped prompt: 326 us, so 302,
+// both in one session; 305-324 over all).
 struct PromptWork {
     const int64_t* coarse;  // items before each run of `run` sequences
     const int* units;       // work before each item (split lists)
