@@ -20,14 +20,14 @@
 // about two thirds of the measured bf16 rate, at the board's power limit): two bounds lie close
 // together. A softmax step takes a warp about 1300 cycles, so 128 keys of both tiles take 2600.
 // That is a chain of latencies (load of S, maximum, weights, store, one after the other) more than
-// of issue slots: two such warps share a scheduler, which issues about 0.55 instructions a cycle.
-// And their products take 2048 cycles of the tensor core, which S's 64 columns stretch (Q is read
-// again for every 64 keys, and shared memory feeds the tensor core at 128 bytes a cycle). Leaving
-// out all exponentials, half of Q K^T or half of P V changed the time by 3 to 4 % each. Steps of
-// 64 keys with two buffers of S per tile let a softmax follow the one before it at once; with
-// steps of 128 and one buffer (S, P and both O fill tensor memory) every softmax waited for the
-// two products before it: 416 against 486 us. Two groups of softmax warps to a tile, for even and
-// odd steps or for halves of a block, gained nothing (361 against 340; 439).
+// of issue slots: two such warps share a scheduler, which issues 0.4 instructions a cycle over a
+// launch. And their products take 2048 cycles of the tensor core, which S's 64 columns stretch (Q
+// is read again for every 64 keys, and shared memory feeds the tensor core at 128 bytes a cycle).
+// Leaving out all exponentials, half of Q K^T or half of P V changed the time by 3 to 4 % each.
+// Steps of 64 keys with two buffers of S per tile let a softmax follow the one before it at once;
+// with steps of 128 and one buffer (S, P and both O fill tensor memory) every softmax waited for
+// the two products before it: 416 against 486 us. Two groups of softmax warps to a tile, for even
+// and odd steps or for halves of a block, gained nothing (361 against 340; 439).
 #pragma once
 
 #include <cfloat>
