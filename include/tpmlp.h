@@ -519,6 +519,22 @@ TPMLP_API int tpmlp_attn_set_scales(tpmlp_ctx *ctx, const void *k_scale, const v
                                     void *stream);
 
 /*
+ * Norms of queries and keys that tpmlp_attn_append applies before the rotation (none at first): each
+ * head x of Q and K becomes
+ *   x[d] / sqrt(mean over d of x[d]^2 + eps) * w[d]
+ * in fp32, without a rounding before the rotation's result. V is left as it is.
+ *   q_weight, k_weight  device bf16 [D], shared by all heads (per_head 0), or [Hq, D] and [Hkv, D]
+ *                       (per_head 1); copied, and may be freed once the stream has passed this call.
+ *                       Both NULL: no norms
+ *   eps                 2^-40 <= eps <= 1
+ * It applies to appends made afterwards. A captured append keeps per_head and eps and reads the weights
+ * of the last call anew on replay. The first call allocates their memory (not under stream capture).
+ * Errors: INVALID_ARG, MISALIGNED, OOM, CUDA.
+ */
+TPMLP_API int tpmlp_attn_set_norms(tpmlp_ctx *ctx, const void *q_weight, const void *k_weight,
+                                   int32_t per_head, float eps, void *stream);
+
+/*
  * The caller's cache, as the calls below read it. Key j of sequence b is row j % page_size of
  * page page_table[b][j / page_size]; a page of a pool is [Hkv][page_size][D]. Pages may be
  * shared between sequences that only read them. Rows at or past a sequence's length, and rows
@@ -540,7 +556,8 @@ typedef struct tpmlp_kv {
 } tpmlp_kv;
 
 /*
- * Append T new tokens: rotate q and k by the token's position, write k and v into the cache and
+ * Append T new tokens: norm the heads of q and k (tpmlp_attn_set_norms), rotate them by the token's
+ * position (tpmlp_attn_set_rope), write k and v into the cache and
  * the rotated q to Qout.
  *   Q    device bf16, row t at Q + t ldq, Hq * D elements (NULL: only k and v)
  *   K, V device bf16, rows of Hkv * D elements at pitch ldk, ldv (elements, multiples of 8: the
@@ -600,7 +617,51 @@ TPMLP_API int tpmlp_attn_prompt(tpmlp_ctx *ctx, const void *Q, int64_t ldq, int6
                                 void *stream);
 
 /*
- * The three calls above with their arguments in one structure, for bindings that pay per argument
+ * Attention of new tokens to all keys of another sequence's cache, without a causal mask: a decoder's
+ * tokens to an encoder's states, whose keys and values tpmlp_attn_append wrote (K and V of the states;
+ * without Q), or several beams to the states they share.
+ *   Out[t, h] = sum_j p_j V_j,  p = softmax over all j < lens[b] of scale * <Q[t, h], K_j>
+ * for rows t = cu_q[b] .. cu_q[b + 1] - 1, each sequence's keys being read once for up to 256 / G of
+ * them. Rows, Lse and rows of no sequence as in tpmlp_attn_prompt; a sequence without keys gives zeros
+ * and -infinity. With one row to a sequence, tpmlp_attn_decode without a window computes the same.
+ * One launch; T == 0 or B == 0 is a no-op.
+ * Errors: as tpmlp_attn_decode.
+ */
+TPMLP_API int tpmlp_attn_cross(tpmlp_ctx *ctx, const void *Q, int64_t ldq, int64_t T,
+                               const int32_t *cu_q, const tpmlp_kv *kv, float scale, void *Out,
+                               int64_t ldo, float *Lse, void *stream);
+
+/*
+ * Decode of one token of each sequence of a batch whose sequences share prefixes: sequence b's keys
+ * are those of its prefix and then its own, one softmax over both, and a prefix's keys are read once
+ * for all of its sequences (for up to 256 / G of them at a time).
+ *   prefix  the prefixes' keys: row g of its page table, lens[g] keys (prefix->B prefixes; the pools may
+ *           be kv's)
+ *   cu      device int32 [prefix->B + 1], not decreasing, at most kv->B: sequences cu[g] .. cu[g + 1] - 1
+ *           have prefix g; those before cu[0] and from cu[prefix->B] on have none
+ *   kv      each sequence's own keys, with the new token's, as in tpmlp_attn_decode. A key's rotation is
+ *           the caller's: own keys are appended at their positions behind the prefix, so kv's page table
+ *           for tpmlp_attn_append may differ from the one here
+ * The rest as in tpmlp_attn_decode, without a window. A sequence without keys of its own attends to its
+ * prefix alone. Two launches; kv->B == 0 is a no-op. Results over prefixes pass through a workspace in
+ * fp32 that grows with kv->B: tpmlp_attn_reserve first, to keep the allocation out of a timed region;
+ * under stream capture a call that would have to grow it returns INVALID_ARG.
+ * Errors: as tpmlp_attn_decode, and OOM.
+ */
+TPMLP_API int tpmlp_attn_decode_shared(tpmlp_ctx *ctx, const void *Q, int64_t ldq,
+                                       const tpmlp_kv *prefix, const int32_t *cu,
+                                       const tpmlp_kv *kv, float scale, void *Out, int64_t ldo,
+                                       float *Lse, void *stream);
+
+/*
+ * Make the workspace of tpmlp_attn_decode_shared hold max_sequences sequences (Hq * (D + 1) fp32 each). A
+ * workspace that grows keeps its smaller forms until tpmlp_destroy, for the graphs that were captured
+ * with them. Errors: INVALID_ARG, UNSUPPORTED_SHAPE, OOM, CUDA.
+ */
+TPMLP_API int tpmlp_attn_reserve(tpmlp_ctx *ctx, int64_t max_sequences);
+
+/*
+ * The calls above with their arguments in one structure, for bindings that pay per argument
  * (a decode step's calls take a few microseconds): the same checks, kernels and errors. `scale` is
  * rounded to fp32. NULL: INVALID_ARG.
  */
@@ -623,8 +684,8 @@ typedef struct tpmlp_attend_args {
     tpmlp_ctx *ctx;
     const void *Q;
     int64_t ldq;
-    int64_t T;             /* prompt only */
-    const int32_t *cu_q;   /* prompt only */
+    int64_t T;             /* prompt and cross only */
+    const int32_t *cu_q;   /* prompt and cross only */
     const tpmlp_kv *kv;
     double scale;
     int64_t window;        /* within int32_t */
@@ -633,9 +694,24 @@ typedef struct tpmlp_attend_args {
     float *Lse;
     void *stream;
 } tpmlp_attend_args;
+typedef struct tpmlp_shared_args {
+    tpmlp_ctx *ctx;
+    const void *Q;
+    int64_t ldq;
+    const tpmlp_kv *prefix;
+    const int32_t *cu;
+    const tpmlp_kv *kv;
+    double scale;
+    void *Out;
+    int64_t ldo;
+    float *Lse;
+    void *stream;
+} tpmlp_shared_args;
 TPMLP_API int tpmlp_attn_append_packed(const tpmlp_append_args *args);
 TPMLP_API int tpmlp_attn_decode_packed(const tpmlp_attend_args *args);
 TPMLP_API int tpmlp_attn_prompt_packed(const tpmlp_attend_args *args);
+TPMLP_API int tpmlp_attn_cross_packed(const tpmlp_attend_args *args); /* window: 0 */
+TPMLP_API int tpmlp_attn_decode_shared_packed(const tpmlp_shared_args *args);
 
 /* Release everything the context owns (synchronises its device first). NULL is a no-op. */
 TPMLP_API void tpmlp_destroy(tpmlp_ctx *ctx);

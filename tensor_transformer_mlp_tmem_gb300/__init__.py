@@ -35,7 +35,9 @@ __all__ = [
     "Attention", "PagedCache", "KvCache", "TPMLP_FLAG_KV_E4M3", "TPMLP_ERR_BAD_PAGE",
     "tpmlp_attn_create", "tpmlp_attn_set_rope", "tpmlp_attn_set_scales", "tpmlp_attn_append",
     "tpmlp_attn_decode", "tpmlp_attn_prompt", "tpmlp_attn_append_packed",
-    "tpmlp_attn_decode_packed", "tpmlp_attn_prompt_packed",
+    "tpmlp_attn_decode_packed", "tpmlp_attn_prompt_packed", "tpmlp_attn_set_norms",
+    "tpmlp_attn_cross", "tpmlp_attn_decode_shared", "tpmlp_attn_reserve",
+    "tpmlp_attn_cross_packed", "tpmlp_attn_decode_shared_packed",
 ]
 
 TPMLP_OK = 0
@@ -134,6 +136,14 @@ def load_library() -> ctypes.CDLL:
                               ctypes.c_int),
         "tpmlp_attn_prompt": ([vp, vp, i64, i64, vp, vp, ctypes.c_float, i32, vp, i64, vp, vp],
                               ctypes.c_int),
+        "tpmlp_attn_set_norms": ([vp, vp, vp, i32, ctypes.c_float, vp], ctypes.c_int),
+        "tpmlp_attn_cross": ([vp, vp, i64, i64, vp, vp, ctypes.c_float, vp, i64, vp, vp],
+                             ctypes.c_int),
+        "tpmlp_attn_decode_shared": ([vp, vp, i64, vp, vp, vp, ctypes.c_float, vp, i64, vp, vp],
+                                     ctypes.c_int),
+        "tpmlp_attn_reserve": ([vp, i64], ctypes.c_int),
+        "tpmlp_attn_cross_packed": ([vp], ctypes.c_int),
+        "tpmlp_attn_decode_shared_packed": ([vp], ctypes.c_int),
         "tpmlp_attn_append_packed": ([vp], ctypes.c_int),
         "tpmlp_attn_decode_packed": ([vp], ctypes.c_int),
         "tpmlp_attn_prompt_packed": ([vp], ctypes.c_int),
@@ -386,6 +396,12 @@ def tpmlp_attn_set_scales(ctx: int, k_scale, v_scale, stream=None) -> None:
                                                 _stream(stream)), "tpmlp_attn_set_scales", ctx)
 
 
+def tpmlp_attn_set_norms(ctx: int, q_weight, k_weight, per_head: bool = False, eps: float = 1e-6,
+                         stream=None) -> None:
+    _check(load_library().tpmlp_attn_set_norms(ctx, _ptr(q_weight), _ptr(k_weight), int(per_head),
+                                               eps, _stream(stream)), "tpmlp_attn_set_norms", ctx)
+
+
 def tpmlp_attn_append(ctx: int, Q, ldq: int, K, ldk: int, V, ldv: int, T: int, pos, seq,
                       kv: KvCache, Qout, ldqo: int, stream=None) -> None:
     _check(load_library().tpmlp_attn_append(
@@ -405,6 +421,34 @@ def tpmlp_attn_prompt(ctx: int, Q, ldq: int, T: int, cu_q, kv: KvCache, scale: f
     _check(load_library().tpmlp_attn_prompt(ctx, _ptr(Q), ldq, T, _ptr(cu_q), ctypes.byref(kv),
                                             scale, window, _ptr(Out), ldo, _ptr(Lse),
                                             _stream(stream)), "tpmlp_attn_prompt", ctx)
+
+
+def tpmlp_attn_cross(ctx: int, Q, ldq: int, T: int, cu_q, kv: KvCache, scale: float, Out, ldo: int,
+                     Lse=None, stream=None) -> None:
+    _check(load_library().tpmlp_attn_cross(ctx, _ptr(Q), ldq, T, _ptr(cu_q), ctypes.byref(kv), scale,
+                                           _ptr(Out), ldo, _ptr(Lse), _stream(stream)),
+           "tpmlp_attn_cross", ctx)
+
+
+def tpmlp_attn_decode_shared(ctx: int, Q, ldq: int, prefix: KvCache, cu, kv: KvCache, scale: float,
+                             Out, ldo: int, Lse=None, stream=None) -> None:
+    _check(load_library().tpmlp_attn_decode_shared(
+        ctx, _ptr(Q), ldq, ctypes.byref(prefix), _ptr(cu), ctypes.byref(kv), scale, _ptr(Out), ldo,
+        _ptr(Lse), _stream(stream)), "tpmlp_attn_decode_shared", ctx)
+
+
+def tpmlp_attn_reserve(ctx: int, max_sequences: int) -> None:
+    _check(load_library().tpmlp_attn_reserve(ctx, max_sequences), "tpmlp_attn_reserve", ctx)
+
+
+def tpmlp_attn_cross_packed(args: int) -> None:
+    """args: address of a tpmlp_attend_args."""
+    _check(load_library().tpmlp_attn_cross_packed(args), "tpmlp_attn_cross_packed")
+
+
+def tpmlp_attn_decode_shared_packed(args: int) -> None:
+    """args: address of a tpmlp_shared_args."""
+    _check(load_library().tpmlp_attn_decode_shared_packed(args), "tpmlp_attn_decode_shared_packed")
 
 
 def tpmlp_attn_append_packed(args: int) -> None:
@@ -696,9 +740,10 @@ class Linear:
         return tpmlp_get_status(self.ctx, stream)
 
 
-# tpmlp_append_args and tpmlp_attend_args
+# tpmlp_append_args, tpmlp_attend_args and tpmlp_shared_args
 _APPEND = struct.Struct("@PPqPqPqqPPPPqP")
 _ATTEND = struct.Struct("@PPqqPPdqPqPP")
+_SHARED = struct.Struct("@PPqPPPdPqPP")
 
 
 class Attention:
@@ -712,6 +757,8 @@ class Attention:
         q = attn.append(q, k, v, cache, pos, seq)                # rotate, write k and v
         out = attn.prompt(q, cu_q, cache)                        # a chunk of each sequence
         out = attn.decode(q, cache)                              # one token of each sequence
+        out = attn.decode_shared(q, cache, prefix, cu)           # the same behind shared prefixes
+        out = attn.cross(q, cu_q, states)                        # to all keys of another sequence
 
     With stream=, a call runs there and not on the current stream: the caller orders the two (its
     tensors have to be ready, and to live until the call has passed).
@@ -726,7 +773,7 @@ class Attention:
         self._lib = load_library()
         self._wq, self._wk, self._scale = Hq * D, Hkv * D, D ** -0.5
         self._layout = (Hkv, D, page_size, kv_dtype)
-        self._args = ctypes.create_string_buffer(max(_APPEND.size, _ATTEND.size))
+        self._args = ctypes.create_string_buffer(max(_APPEND.size, _ATTEND.size, _SHARED.size))
         self._args_at = ctypes.addressof(self._args)
         self._Tensor, self._bf16 = torch.Tensor, torch.bfloat16
         self._int32, self._float32 = torch.int32, torch.float32
@@ -766,6 +813,26 @@ class Attention:
         TPMLP._require(k_scale, torch.float32, (self.Hkv,), "k_scale")
         TPMLP._require(v_scale, torch.float32, (self.Hkv,), "v_scale")
         tpmlp_attn_set_scales(self.ctx, k_scale, v_scale, stream)
+
+    def set_norms(self, q_weight, k_weight, eps: float = 1e-6, stream=None):
+        """append() norms every query and key head x before it rotates it: x over the root of the mean
+        of its squares plus eps, times a weight. bf16 CUDA weights [D], shared by the heads, or [Hq, D]
+        and [Hkv, D]; None and None: no norms."""
+        import torch
+        heads = False
+        if q_weight is not None or k_weight is not None:
+            for w, n, what in ((q_weight, self.Hq, "q_weight"), (k_weight, self.Hkv, "k_weight")):
+                if not isinstance(w, torch.Tensor) or not w.is_cuda:
+                    raise TypeError(f"{what} must be a CUDA tensor")
+                heads = w.dim() == 2
+                TPMLP._require(w, torch.bfloat16, (n, self.D) if heads else (self.D,), what)
+            if q_weight.dim() != k_weight.dim():
+                raise ValueError("q_weight and k_weight: expected a weight per head in both or in none")
+        tpmlp_attn_set_norms(self.ctx, q_weight, k_weight, heads, eps, stream)
+
+    def reserve(self, max_sequences: int):
+        """Room for decode_shared() of so many sequences (it grows on demand, but not in a graph)."""
+        tpmlp_attn_reserve(self.ctx, max_sequences)
 
     def pool_dtype(self):
         import torch
@@ -878,6 +945,46 @@ class Attention:
         rc = self._lib.tpmlp_attn_prompt_packed(self._args_at)
         if rc:
             _check(rc, "tpmlp_attn_prompt", self.ctx)
+        return (out, lse) if return_lse else out
+
+    def cross(self, q, cu_q, cache, scale=None, out=None, return_lse: bool = False, stream=None):
+        """Attention of the rows q [T, Hq * D], sequence b's in rows cu_q[b] .. cu_q[b + 1] - 1 (cu_q
+        int32 [B + 1]), to all keys of its cache: tokens or beams to an encoder's states, without a
+        causal mask. With one row to a sequence decode() computes the same."""
+        kv, T = cache._of(self), q.shape[0]
+        cu = self._ints(cu_q, cache.B + 1, "cu_q")
+        ldq = self._rows(q, T, self._wq, "q")
+        if out is None:
+            out = self._new(q, (T, self._wq), stream)
+        ldo = self._rows(out, T, self._wq, "out")
+        lse = self._new(q, (T, self.Hq), stream, self._float32) if return_lse else None
+        _ATTEND.pack_into(self._args, 0, self.ctx or 0, q.data_ptr(), ldq, T, cu, kv,
+                          self._scale if scale is None else scale, 0, out.data_ptr(), ldo,
+                          lse.data_ptr() if return_lse else 0, _stream(stream) or 0)
+        rc = self._lib.tpmlp_attn_cross_packed(self._args_at)
+        if rc:
+            _check(rc, "tpmlp_attn_cross", self.ctx)
+        return (out, lse) if return_lse else out
+
+    def decode_shared(self, q, cache, prefix, cu, scale=None, out=None, return_lse: bool = False,
+                      stream=None):
+        """decode() of sequences that share prefixes: sequences cu[g] .. cu[g + 1] - 1 (cu int32
+        [prefix.B + 1]) attend to the keys of prefix g, a sequence of the PagedCache `prefix`, and then
+        to their own in `cache` (their new token's included). A prefix's keys are read once for all of
+        its sequences; sequences before cu[0] and from cu[prefix.B] on have no prefix."""
+        kv, shared, B = cache._of(self), prefix._of(self), cache.B
+        at = self._ints(cu, prefix.B + 1, "cu")
+        ldq = self._rows(q, B, self._wq, "q")
+        if out is None:
+            out = self._new(q, (B, self._wq), stream)
+        ldo = self._rows(out, B, self._wq, "out")
+        lse = self._new(q, (B, self.Hq), stream, self._float32) if return_lse else None
+        _SHARED.pack_into(self._args, 0, self.ctx or 0, q.data_ptr(), ldq, shared, at, kv,
+                          self._scale if scale is None else scale, out.data_ptr(), ldo,
+                          lse.data_ptr() if return_lse else 0, _stream(stream) or 0)
+        rc = self._lib.tpmlp_attn_decode_shared_packed(self._args_at)
+        if rc:
+            _check(rc, "tpmlp_attn_decode_shared", self.ctx)
         return (out, lse) if return_lse else out
 
     def status(self, stream=None):

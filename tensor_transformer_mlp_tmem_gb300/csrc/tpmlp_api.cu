@@ -1638,6 +1638,8 @@ void tpmlp_destroy(tpmlp_ctx* c) {
     cudaFree(c->kv_scale);
     cudaFree(c->attn_partial);
     cudaFree(c->attn_count);
+    cudaFree(c->norm_w);
+    for (float* p : c->shared) cudaFree(p);
     cudaFree(c->status);
     if (cur >= 0 && cur != c->device) cudaSetDevice(cur);
     delete c;

@@ -2,231 +2,39 @@
 // launches. As in tpmlp_api.cu, every entry point returns a tpmlp_status and no C++ exception
 // crosses this boundary.
 #include <algorithm>
-#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstring>
 #include <new>
 
-#include "tpmlp_attn.cuh"
-#include "tpmlp_attn_prompt.cuh"
-#include "tpmlp_context.h"
+#include "tpmlp_attn_launch.h"
 
-using tpmlp::aligned16;
-using tpmlp::check_device;
+using namespace tpmlp;
 
 namespace {
 
 constexpr int kRowCtasPerSm = 2;
 
-bool is_e4m3(const tpmlp_ctx* c) { return (c->flags & TPMLP_FLAG_KV_E4M3) != 0; }
-
-// Rows of `width` bf16 elements at pitch ld that 16-byte loads may read.
-int check_rows(tpmlp_ctx* c, const void* p, int64_t ld, int64_t width) {
-    if (!p) return TPMLP_ERR_INVALID_ARG;
-    if (ld < width || ld > (int64_t(1) << 40)) {
-        c->last_error = "a row pitch is smaller than its row";
-        return TPMLP_ERR_INVALID_ARG;
-    }
-    if (!aligned16(p) || ld % 8) return TPMLP_ERR_MISALIGNED;
-    return TPMLP_OK;
-}
-
-int check_kv(tpmlp_ctx* c, const tpmlp_kv* kv, bool lens) {
-    if (!kv || !kv->K || !kv->V || !kv->page_table || (lens && !kv->lens)) return TPMLP_ERR_INVALID_ARG;
-    if (kv->num_pages <= 0 || kv->table_pages <= 0 || kv->B < 0) return TPMLP_ERR_INVALID_ARG;
-    if (kv->num_pages > INT_MAX) return TPMLP_ERR_UNSUPPORTED_SHAPE;
-    if (kv->table_stride != 0 && kv->table_stride < kv->table_pages) return TPMLP_ERR_INVALID_ARG;
-    const int64_t page = static_cast<int64_t>(c->heads_kv) * c->page_size * c->head_dim;
-    if (kv->page_stride != 0 && kv->page_stride < page) return TPMLP_ERR_INVALID_ARG;
-    // key numbers stay below 2^31 with a step of every kernel past the end
-    if (static_cast<int64_t>(kv->table_pages) * c->page_size > (int64_t(1) << 31) - (1 << 16)) {
-        c->last_error = "a sequence's table holds more than 2^31 - 2^16 keys";
-        return TPMLP_ERR_UNSUPPORTED_SHAPE;
-    }
-    const int elem = is_e4m3(c) ? 1 : 2;
-    if (!aligned16(kv->K) || !aligned16(kv->V) || kv->page_stride * elem % 16) return TPMLP_ERR_MISALIGNED;
-    if ((reinterpret_cast<uintptr_t>(kv->page_table) | reinterpret_cast<uintptr_t>(kv->lens)) & 3)
-        return TPMLP_ERR_MISALIGNED;
-    return TPMLP_OK;
-}
-
-tpmlp::KvView view_of(const tpmlp_ctx* c, const tpmlp_kv* kv) {
-    const int elem = is_e4m3(c) ? 1 : 2;
-    const int64_t head = static_cast<int64_t>(c->page_size) * c->head_dim;
-    tpmlp::KvView v{};
-    v.K = static_cast<uint8_t*>(kv->K);
-    v.V = static_cast<uint8_t*>(kv->V);
-    v.page_bytes = (kv->page_stride ? kv->page_stride : head * c->heads_kv) * elem;
-    v.head_bytes = head * elem;
-    v.table = kv->page_table;
-    v.table_stride = kv->table_stride ? kv->table_stride : kv->table_pages;
-    v.table_pages = kv->table_pages;
-    while ((1 << v.page_shift) < c->page_size) ++v.page_shift;
-    v.num_pages = static_cast<int32_t>(kv->num_pages);
-    v.lens = kv->lens;
-    v.B = kv->B;
-    v.Hkv = c->heads_kv;
-    v.scales = c->kv_scale;
-    v.status = c->status;
-    return v;
-}
-
-// Launch with programmatic stream serialisation (the kernels wait in griddep_wait before they
-// touch global memory).
-template <typename Kernel, typename... Args>
-int launch(tpmlp_ctx* c, Kernel kern, int64_t grid, int threads, uint32_t smem, cudaStream_t s,
-           const Args&... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-    cfg.blockDim = dim3(threads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    TPMLP_CUDA(c, cudaLaunchKernelEx(&cfg, kern, args...));
-    ++c->launches;
-    return TPMLP_OK;
-}
-
-template <typename Kernel>
-int allow_smem(tpmlp_ctx* c, Kernel kern, uint32_t smem, std::atomic<uint64_t>& done) {
-    const uint64_t bit = uint64_t(1) << (c->device & 63);
-    if (done.load(std::memory_order_acquire) & bit) return TPMLP_OK;
-    TPMLP_CUDA(c, cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    done.fetch_or(bit, std::memory_order_acq_rel);
-    return TPMLP_OK;
-}
-
-template <int D, bool FP8, int NT, int PASSES>
-int launch_rows(tpmlp_ctx* c, const tpmlp::RowArgs& a, cudaStream_t s) {
-    using S = tpmlp::RowShape<D, FP8, NT>;
-    auto kern = tpmlp::attn_row_kernel<D, FP8, NT, PASSES>;
-    static std::atomic<uint64_t> done{0};
-    if (int rc = allow_smem(c, kern, S::kSmem, done)) return rc;
-    const int grid = c->num_sms * S::kCtasPerSm;
-    return launch(c, kern, grid, tpmlp::kRowThreads, S::kSmem, s, a);
-}
-
-template <int D, bool FP8>
-int run_rows_of(tpmlp_ctx* c, const tpmlp::RowArgs& a, cudaStream_t s) {
-    if constexpr (tpmlp::row_heads(D, FP8) > 16)
-        if (a.G > 16) return launch_rows<D, FP8, 2, 2>(c, a, s);
-    if constexpr (tpmlp::row_heads(D, FP8) > 8)
-        if (a.G > 8) return launch_rows<D, FP8, 2, 1>(c, a, s);
-    return launch_rows<D, FP8, 1, 1>(c, a, s);
-}
-
-int run_rows(tpmlp_ctx* c, const tpmlp::RowArgs& a, cudaStream_t s) {
-    if (c->head_dim == 128) return is_e4m3(c) ? run_rows_of<128, true>(c, a, s) : run_rows_of<128, false>(c, a, s);
-    return is_e4m3(c) ? run_rows_of<64, true>(c, a, s) : run_rows_of<64, false>(c, a, s);
-}
-
-template <int D, bool FP8>
-int launch_prompt(tpmlp_ctx* c, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                  const tpmlp::PromptArgs& a, cudaStream_t s) {
-    using S = tpmlp::PromptSmem<D, FP8>;
-    auto kern = tpmlp::attn_prompt_kernel<D, FP8>;
-    static std::atomic<uint64_t> done{0};
-    if (int rc = allow_smem(c, kern, S::kTotal, done)) return rc;
-    return launch(c, kern, c->num_sms, S::kThreads, S::kTotal, s, q, k, v, a);
-}
-
-// The pool as [page][Hkv * page size][D], in boxes of 64 columns and one page's (at most a
-// block's) rows.
-int pool_map(tpmlp_ctx* c, CUtensorMap* map, const void* pool, const tpmlp::KvView& kv) {
-    const uint64_t dims[3] = {static_cast<uint64_t>(c->head_dim),
-                              static_cast<uint64_t>(c->heads_kv) * c->page_size,
-                              static_cast<uint64_t>(kv.num_pages)};
-    const uint64_t strides[2] = {static_cast<uint64_t>(c->head_dim) * 2, static_cast<uint64_t>(kv.page_bytes)};
-    const uint32_t box[3] = {64, static_cast<uint32_t>(std::min(c->page_size, tpmlp::kPB)), 1};
-    return tpmlp::encode_map_typed(c, map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, pool, 3, dims, strides, box);
-}
-
-int run_prompt(tpmlp_ctx* c, const tpmlp::RowArgs& r, const int32_t* cu_q, int64_t T, cudaStream_t s) {
-    tpmlp::PromptArgs a{};
-    a.kv = r.kv;
-    a.q = r.q;
-    a.ldq = r.ldq;
-    a.out = r.out;
-    a.ldo = r.ldo;
-    a.lse = r.lse;
-    a.cu_q = cu_q;
-    a.T = static_cast<int32_t>(T);
-    a.Hq = r.Hq;
-    a.G = r.G;
-    a.tpt = tpmlp::kPB / r.G;
-    a.scale_log2 = r.scale_log2;
-    a.window = r.window;
-    a.partial = c->attn_partial;
-    a.count = c->attn_count;
-    CUtensorMap q{}, k{}, v{};
-    if (!is_e4m3(c)) {
-        const uint64_t dims[3] = {static_cast<uint64_t>(c->head_dim), static_cast<uint64_t>(c->heads_q),
-                                  static_cast<uint64_t>(T)};
-        const uint64_t strides[2] = {static_cast<uint64_t>(c->head_dim) * 2, static_cast<uint64_t>(a.ldq) * 2};
-        const uint32_t box[3] = {64, static_cast<uint32_t>(a.G), static_cast<uint32_t>(a.tpt)};
-        int rc = tpmlp::encode_map_typed(c, &q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, 3, dims, strides, box);
-        if (rc || (rc = pool_map(c, &k, a.kv.K, a.kv)) || (rc = pool_map(c, &v, a.kv.V, a.kv))) return rc;
-    }
-    if (c->head_dim == 128)
-        return is_e4m3(c) ? launch_prompt<128, true>(c, q, k, v, a, s) : launch_prompt<128, false>(c, q, k, v, a, s);
-    return is_e4m3(c) ? launch_prompt<64, true>(c, q, k, v, a, s) : launch_prompt<64, false>(c, q, k, v, a, s);
-}
-
 // Tokens of an append block: as many as its threads' units hold, but no fewer blocks than run at
 // once. 16384 tokens of 12 + 12 heads of 64, 16 + 2 of 64, 8 + 1 of 128 in e4m3, 1 + 1 of 64: 30, 16, 23,
 // 9 us (a block for each token: 37, 27, 34, 25).
 int64_t append_tokens(const tpmlp_ctx* c, int64_t units, int64_t T) {
-    const int64_t hold = tpmlp::kAppendThreads * tpmlp::kAppendUnits / units;
-    const int64_t fill = T / (static_cast<int64_t>(tpmlp::kAppendBlocks) * c->num_sms);
-    return std::max<int64_t>(1, std::min({hold, fill, static_cast<int64_t>(tpmlp::kAppendTokens)}));
+    const int64_t hold = kAppendThreads * kAppendUnits / units;
+    const int64_t fill = T / (static_cast<int64_t>(kAppendBlocks) * c->num_sms);
+    return std::max<int64_t>(1, std::min({hold, fill, static_cast<int64_t>(kAppendTokens)}));
+}
+
+template <int D, bool FP8, bool NORM>
+int launch_append(tpmlp_ctx* c, const AppendArgs& a, cudaStream_t s) {
+    if (a.tokens > 1)
+        return launch(c, append_kernel<D, FP8, true, NORM>, (a.T + int64_t(a.tokens) - 1) / a.tokens,
+                      kAppendThreads, 0, s, a);
+    return launch(c, append_kernel<D, FP8, false, NORM>, int64_t(a.T) * a.parts, kAppendThreads, 0, s, a);
 }
 
 template <int D, bool FP8>
-int run_append(tpmlp_ctx* c, const tpmlp::AppendArgs& a, cudaStream_t s) {
-    if (a.tokens > 1)
-        return launch(c, tpmlp::append_kernel<D, FP8, true>, (a.T + int64_t(a.tokens) - 1) / a.tokens,
-                      tpmlp::kAppendThreads, 0, s, a);
-    return launch(c, tpmlp::append_kernel<D, FP8, false>, int64_t(a.T) * a.parts, tpmlp::kAppendThreads, 0, s, a);
-}
-
-// What decode and prompt check alike; rows: rows of Q and Out.
-int check_attend(tpmlp_ctx* c, const void* Q, int64_t ldq, const tpmlp_kv* kv, float scale,
-                 const void* Out, int64_t ldo, const float* Lse) {
-    if (int rc = check_kv(c, kv, true)) return rc;
-    if (!(scale > 0.0f) || !std::isfinite(scale)) return TPMLP_ERR_INVALID_ARG;
-    const int64_t width = static_cast<int64_t>(c->heads_q) * c->head_dim;
-    if (int rc = check_rows(c, Q, ldq, width)) return rc;
-    if (int rc = check_rows(c, Out, ldo, width)) return rc;
-    if (reinterpret_cast<uintptr_t>(Lse) & 3) return TPMLP_ERR_MISALIGNED;
-    return TPMLP_OK;
-}
-
-tpmlp::RowArgs row_args(const tpmlp_ctx* c, const void* Q, int64_t ldq, const tpmlp_kv* kv,
-                        float scale, int32_t window, void* Out, int64_t ldo, float* Lse) {
-    tpmlp::RowArgs a{};
-    a.kv = view_of(c, kv);
-    a.q = static_cast<const __nv_bfloat16*>(Q);
-    a.ldq = ldq;
-    a.out = static_cast<__nv_bfloat16*>(Out);
-    a.ldo = ldo;
-    a.lse = Lse;
-    a.Hq = c->heads_q;
-    a.G = c->heads_q / c->heads_kv;
-    a.scale_log2 = scale * 1.44269504088896341f;
-    a.window = window;
-    a.partial = c->attn_partial;
-    a.count = c->attn_count;
-    return a;
-}
-
-int check_attention(tpmlp_ctx* c) {
-    if (!c || c->kind != kKindAttention) return TPMLP_ERR_INVALID_ARG;
-    return check_device(c);
+int run_append(tpmlp_ctx* c, const AppendArgs& a, cudaStream_t s) {
+    return c->norm_on ? launch_append<D, FP8, true>(c, a, s) : launch_append<D, FP8, false>(c, a, s);
 }
 
 }  // namespace
@@ -260,8 +68,8 @@ int tpmlp_attn_create(tpmlp_ctx** out, int32_t Hq, int32_t Hkv, int32_t D, int32
     c->page_size = page_size;
     const size_t ctas = static_cast<size_t>(c->num_sms) * kRowCtasPerSm;
     // two slots per CTA of either kernel (the prompt kernel's hold two tiles each)
-    const size_t partial = std::max(ctas * 2 * tpmlp::kRowSlotFloats,
-                                    static_cast<size_t>(c->num_sms) * 4 * tpmlp::kPromptSlotFloats);
+    const size_t partial = std::max(ctas * 2 * kRowSlotFloats,
+                                    static_cast<size_t>(c->num_sms) * 4 * kPromptSlotFloats);
     const size_t counters = ctas + 2;  // a counter per CTA (prompt: per tile), the deal's two
     c->attn_counters = counters;
     const size_t scales = static_cast<size_t>(Hkv) * 2;
@@ -313,6 +121,34 @@ int tpmlp_attn_set_scales(tpmlp_ctx* c, const void* k_scale, const void* v_scale
     return TPMLP_OK;
 }
 
+int tpmlp_attn_set_norms(tpmlp_ctx* c, const void* q_weight, const void* k_weight, int32_t per_head,
+                         float eps, void* stream) {
+    if (!c || c->kind != kKindAttention || (q_weight != nullptr) != (k_weight != nullptr))
+        return TPMLP_ERR_INVALID_ARG;
+    if (!q_weight) {
+        c->norm_on = false;
+        return TPMLP_OK;
+    }
+    if (per_head != 0 && per_head != 1) return TPMLP_ERR_INVALID_ARG;
+    if (!(eps >= 0x1p-40f && eps <= 1.0f)) return TPMLP_ERR_INVALID_ARG;
+    if (int rc = check_device(c)) return rc;
+    if (!aligned16(q_weight) || !aligned16(k_weight)) return TPMLP_ERR_MISALIGNED;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const size_t head = static_cast<size_t>(c->head_dim) * sizeof(uint16_t);
+    if (!c->norm_w) {
+        if (int rc = refuse_allocation(c, s, "tpmlp_attn_set_norms before the capture")) return rc;
+        if (int rc = allocate(c, reinterpret_cast<void**>(&c->norm_w), (c->heads_q + c->heads_kv) * head)) return rc;
+    }
+    const size_t nq = per_head ? c->heads_q : 1, nk = per_head ? c->heads_kv : 1;
+    TPMLP_CUDA(c, cudaMemcpyAsync(c->norm_w, q_weight, nq * head, cudaMemcpyDeviceToDevice, s));
+    TPMLP_CUDA(c, cudaMemcpyAsync(c->norm_w + c->heads_q * c->head_dim, k_weight, nk * head,
+                                  cudaMemcpyDeviceToDevice, s));
+    c->norm_on = true;
+    c->norm_per_head = per_head != 0;
+    c->norm_eps = eps;
+    return TPMLP_OK;
+}
+
 int tpmlp_attn_append(tpmlp_ctx* c, const void* Q, int64_t ldq, const void* K, int64_t ldk,
                       const void* V, int64_t ldv, int64_t T, const int32_t* pos,
                       const int32_t* seq, const tpmlp_kv* kv, void* Qout, int64_t ldqo,
@@ -329,7 +165,7 @@ int tpmlp_attn_append(tpmlp_ctx* c, const void* Q, int64_t ldq, const void* K, i
     int rc;
     if (Q && ((rc = check_rows(c, Q, ldq, wq)) || (rc = check_rows(c, Qout, ldqo, wq)))) return rc;
     if ((rc = check_rows(c, K, ldk, wk)) || (rc = check_rows(c, V, ldv, wk))) return rc;
-    tpmlp::AppendArgs a{};
+    AppendArgs a{};
     a.kv = view_of(c, kv);
     a.q = static_cast<const __nv_bfloat16*>(Q);
     a.k = static_cast<const __nv_bfloat16*>(K);
@@ -349,9 +185,19 @@ int tpmlp_attn_append(tpmlp_ctx* c, const void* Q, int64_t ldq, const void* K, i
     // a unit at least. One token of 32 + 32 heads of 128: 2.4 us (one block: 3.5 us); 256 tokens of 96
     // + 8 heads into e4m3: 4.5 us (two, four blocks an SM: 5.7, 4.8).
     const int64_t units = static_cast<int64_t>(a.Hq + 2 * c->heads_kv) * (c->head_dim / 16);
-    const int64_t most = (units + tpmlp::kAppendThreads - 1) / tpmlp::kAppendThreads;
-    a.parts = static_cast<int32_t>(std::min(most, std::max<int64_t>(1, tpmlp::kAppendBlocks * c->num_sms / T)));
+    const int64_t most = (units + kAppendThreads - 1) / kAppendThreads;
+    a.parts = static_cast<int32_t>(std::min(most, std::max<int64_t>(1, kAppendBlocks * c->num_sms / T)));
     a.part_units = static_cast<int32_t>((units + a.parts - 1) / a.parts);
+    if (c->norm_on) {
+        // whole heads to a block: their units' threads add up the squares
+        const int32_t per_head = c->head_dim / 16;
+        a.part_units = (a.part_units + per_head - 1) / per_head * per_head;
+        a.parts = static_cast<int32_t>((units + a.part_units - 1) / a.part_units);
+        a.wq = reinterpret_cast<const __nv_bfloat16*>(c->norm_w);
+        a.wk = a.wq + static_cast<int64_t>(c->heads_q) * c->head_dim;
+        a.w_stride = c->norm_per_head ? c->head_dim : 0;
+        a.eps = c->norm_eps;
+    }
     a.T = static_cast<int32_t>(T);
     a.tokens = static_cast<int32_t>(append_tokens(c, units, T));
     a.per_unit = static_cast<uint32_t>((uint64_t(1) << 32) / units + 1);
@@ -366,11 +212,11 @@ int tpmlp_attn_decode(tpmlp_ctx* c, const void* Q, int64_t ldq, const tpmlp_kv* 
     if (!kv) return TPMLP_ERR_INVALID_ARG;
     if (kv->B == 0) return TPMLP_OK;
     if (int rc = check_attend(c, Q, ldq, kv, scale, Out, ldo, Lse)) return rc;
-    tpmlp::RowArgs a = row_args(c, Q, ldq, kv, scale, window, Out, ldo, Lse);
+    RowArgs a = row_args(c, Q, ldq, kv, scale, window, Out, ldo, Lse);
     a.rows = kv->B;
-    if (a.G > tpmlp::row_heads(c->head_dim, is_e4m3(c)))
-        return run_prompt(c, a, nullptr, kv->B, static_cast<cudaStream_t>(stream));
-    return run_rows(c, a, static_cast<cudaStream_t>(stream));
+    if (a.G > row_heads(c->head_dim, is_e4m3(c)))
+        return run_prompt<false>(c, a, nullptr, kv->B, static_cast<cudaStream_t>(stream));
+    return run_rows<false>(c, a, static_cast<cudaStream_t>(stream));
 }
 
 int tpmlp_attn_prompt(tpmlp_ctx* c, const void* Q, int64_t ldq, int64_t T, const int32_t* cu_q,
@@ -383,8 +229,8 @@ int tpmlp_attn_prompt(tpmlp_ctx* c, const void* Q, int64_t ldq, int64_t T, const
     if (int rc = check_attend(c, Q, ldq, kv, scale, Out, ldo, Lse)) return rc;
     if (!cu_q) return TPMLP_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(cu_q) & 3) return TPMLP_ERR_MISALIGNED;
-    const tpmlp::RowArgs a = row_args(c, Q, ldq, kv, scale, window, Out, ldo, Lse);
-    return run_prompt(c, a, cu_q, T, static_cast<cudaStream_t>(stream));
+    const RowArgs a = row_args(c, Q, ldq, kv, scale, window, Out, ldo, Lse);
+    return run_prompt<false>(c, a, cu_q, T, static_cast<cudaStream_t>(stream));
 }
 
 int tpmlp_attn_append_packed(const tpmlp_append_args* a) {
@@ -427,6 +273,6 @@ extern "C" TPMLP_API tpmlp_ctx* tpmlp_test_attn_context(int32_t Hq, int32_t Hkv,
 
 // Test builds only: whether decode of G heads to a kv head takes the row kernel.
 extern "C" TPMLP_API int tpmlp_test_decode_on_rows(int32_t G, int32_t D, uint32_t flags) {
-    return G <= tpmlp::row_heads(D, (flags & TPMLP_FLAG_KV_E4M3) != 0);
+    return G <= row_heads(D, (flags & TPMLP_FLAG_KV_E4M3) != 0);
 }
 #endif

@@ -81,6 +81,11 @@ struct AppendArgs {
     int32_t tokens;     // tokens per block (more than one: parts is 1)
     uint32_t per_unit;  // 2^32 / units of a token, rounded up
     double turns[64];   // whole turns per position of each pair
+    // norms of query and key heads (NORM): weights, elements from head to head (0: all heads share
+    // them), what is added to the mean square
+    const __nv_bfloat16 *wq, *wk;
+    int64_t w_stride;
+    float eps;
 };
 
 // Loads of what another kernel of the stream may have just written: through L2 (the read-only
@@ -126,6 +131,46 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float (&f)[8], float scale) {
     return make_uint2(w[0], w[1]);
 }
 
+// Sum over the lanes that hold a head's units: D / 16 neighbours, of which all or none are here.
+template <int D>
+__device__ __forceinline__ float head_sum(float v) {
+    constexpr int kUnits = D / 16;
+    const uint32_t lanes = ((1u << kUnits) - 1u) << (threadIdx.x & 31u & ~(kUnits - 1u));
+#pragma unroll
+    for (int o = 1; o < kUnits; o <<= 1) v += __shfl_xor_sync(lanes, v, o);
+    return v;
+}
+
+// The lane's 16 elements x0, x1 of a head over the head's root mean square, times their weights (bf16,
+// 8 to a register group): x / sqrt(mean x^2 + eps) * w, in fp32 and not rounded. Squares that leave
+// fp32 are taken once more of x 2^-80, where eps vanishes beside them.
+template <int D>
+__device__ __forceinline__ void norm_head(float (&x0)[8], float (&x1)[8], const uint4& w0, const uint4& w1, float eps) {
+    auto squares = [&](float down) {
+        float s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float u = x0[j] * down, v = x1[j] * down;
+            s = fmaf(u, u, fmaf(v, v, s));
+        }
+        return head_sum<D>(s);
+    };
+    float s = squares(1.0f), down = 1.0f;
+    if (!(s < 0x1p126f)) {
+        down = 0x1p-80f;
+        s = squares(down);
+        eps = 0.0f;
+    }
+    const float by = rsqrtf(s * (1.0f / D) + eps) * down;
+    float w[8];
+    unpack8(w0, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x0[j] *= by * w[j];
+    unpack8(w1, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x1[j] *= by * w[j];
+}
+
 // A block takes a token, one of `parts` equal parts of it where there are few tokens, or (MANY)
 // several tokens where a token has so few heads that its units would leave threads idle. The
 // rotation's sines and cosines are the same for all heads: the block computes the token's rot / 2
@@ -137,7 +182,7 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float (&f)[8], float scale) {
 // write neighbouring 16 bytes; where halves are rotated they are the partners. Bound by DRAM: 16384
 // tokens of 32 query and 8 kv heads of 128 in 67 us, 6.0 TB/s, 89 % of a copy's rate (256 threads a
 // block, each loading a unit when it had the sines: 87 us).
-template <int D, bool FP8, bool MANY>
+template <int D, bool FP8, bool MANY, bool NORM>
 __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) append_kernel(const __grid_constant__ AppendArgs a) {
     constexpr int kTokens = MANY ? kAppendTokens : 1;
     __shared__ float2 trig[kTokens * (D / 2)];
@@ -227,6 +272,13 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) append_kernel(c
             float x0[8], x1[8];
             unpack8(raw[y][0], x0);
             unpack8(raw[y][1], x1);
+            if constexpr (NORM) {
+                if (w.kind != 2) {
+                    const __nv_bfloat16* const weight = (w.kind == 0 ? a.wq : a.wk) + w.h * a.w_stride;
+                    norm_head<D>(x0, x1, *reinterpret_cast<const uint4*>(weight + w.d0),
+                                 *reinterpret_cast<const uint4*>(weight + w.d1), a.eps);
+                }
+            }
             if (w.rotate) {
                 if (a.interleaved) {
 #pragma unroll
@@ -285,7 +337,25 @@ struct RowArgs {
     int32_t window;
     float* partial;         // [CTAs][2] slots of RowSlot floats
     uint32_t* count;        // [CTAs] arrivals, 0 between launches
+    // JOIN: each row's result over keys of another cache, fp32 [rows][Hq][D], and the log2 of its sum
+    // of weights [rows][Hq] (-infinity: no keys, and the result is not looked at)
+    const float *other, *other_lse;
 };
+
+// How a row's sums over its own keys (maximum m in log2 units, sum l of weights that were raised by
+// 2^raise) and its result over other keys, whose weights sum to 2^lo, make one softmax: the factors of
+// the unscaled sum and of that result, and the log of the sum of all weights.
+struct Joined {
+    float own, other, lse;
+};
+__device__ __forceinline__ Joined join_keys(float m, float l, float raise, float lo) {
+    const float mine = l == 0.0f ? -CUDART_INF_F : m + log2f(l) - raise;
+    const float top = fmaxf(mine, lo), safe = top == -CUDART_INF_F ? 0.0f : top;
+    const float x = exp2f(mine - safe), y = exp2f(lo - safe), sum = x + y;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // no keys at all: zeros
+    return {l == 0.0f ? 0.0f : x * inv / l, y * inv,
+            sum == 0.0f ? -CUDART_INF_F : (top + log2f(sum)) * 0.69314718055994531f};
+}
 
 // Query heads to a kv head that this kernel takes, at most; decode of wider groups goes to the prompt
 // kernel, whose products' tiles they fill and which takes the same time for any G, while this
@@ -416,7 +486,10 @@ __device__ __forceinline__ int v_dim(int g, int e) {
     else return (D / 8) * g + e;
 }
 
-template <int D, bool FP8, int NT, int PASSES>
+// JOIN: the launch before is the one that writes a.other, and nothing else that this kernel reads. That
+// launch let this one start only when everything before itself was done, so only what follows the first
+// segment's keys waits for it.
+template <int D, bool FP8, int NT, int PASSES, bool JOIN>
 __global__ void __launch_bounds__(kRowThreads, RowShape<D, FP8, NT>::kCtasPerSm)
 attn_row_kernel(const __grid_constant__ RowArgs a) {
     using S = RowShape<D, FP8, NT>;
@@ -430,8 +503,13 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
 
-    ptx::griddep_wait();
+    if constexpr (!JOIN) ptx::griddep_wait();
     ptx::griddep_launch_dependents();
+    bool waited = !JOIN;
+    auto wait_for_other = [&] {
+        if (!waited) ptx::griddep_wait();
+        waited = true;
+    };
 
     auto steps_of = [&](const RowRange& x) {
         return max(1, (x.hi - (x.lo & ~15) + S::kStep - 1) / S::kStep);
@@ -457,7 +535,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
             if (lane >= o) sum += v;
         }
         share(__shfl_sync(~0u, sum, 31) * per_row);
-        if (at >= end) return;
+        if (at >= end) return wait_for_other();
         row = __ffs(__ballot_sync(~0u, at < sum * per_row)) - 1;
         row_start = __shfl_sync(~0u, sum - c, row) * per_row;
     } else {
@@ -471,7 +549,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
 #pragma unroll
         for (int w = 0; w < kRowWarps; ++w) total += s_scan[w];
         share(total * per_row);
-        if (at >= end) return;
+        if (at >= end) return wait_for_other();
         int64_t before = 0;
         for (int r0 = 0; r0 < a.rows; r0 += kRowThreads) {
             const int r = r0 + tid;
@@ -499,7 +577,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         }
         row = static_cast<int>(s_found[0]);
         row_start = s_found[1];
-        if (row < 0) return;  // only if the lengths changed during the launch
+        if (row < 0) return wait_for_other();  // only if the lengths changed during the launch
     }
     RowRange range = row_range(a, row);
     int steps = steps_of(range);
@@ -515,7 +593,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         const int step0 = max(static_cast<int>(at - segment_start) - kSegmentStart, 0);
         at = min(end, segment_start + steps + kSegmentStart);
         const int n = static_cast<int>(at - segment_start) - kSegmentStart - step0;
-        if (n <= 0) return;  // the start alone: the segment's steps are the next CTA's
+        if (n <= 0) return wait_for_other();  // the start alone: the segment's steps are the next CTA's
         const int h = part / PASSES;
         const int q0 = part % PASSES * S::kRows;  // the pass's query heads of the group
         auto heads = [&] { return PASSES > 1 ? min(a.G - q0, S::kRows) : a.G; };  // of them
@@ -749,6 +827,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
                 }
         }
 
+        wait_for_other();  // (the partial sums' memory is the launch's before, too)
         // The warps' sums of this segment, joined in shared memory.
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -789,6 +868,20 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
 
         auto finish = [&](int r, int d, float4 v, float mm, float ll) {
             const int64_t head = static_cast<int64_t>(h) * a.G + q0 + r;
+            if constexpr (JOIN) {
+                const int64_t at_row = static_cast<int64_t>(row) * a.Hq + head;
+                const float lo = __ldcg(a.other_lse + at_row);
+                const Joined j = join_keys(mm, ll, FP8 ? kRowRaise : 0.0f, lo);
+                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (lo != -CUDART_INF_F) x = __ldcg(reinterpret_cast<const float4*>(a.other + at_row * D + d));
+                const float own = j.own * v_scale;
+                uint2 w;
+                w.x = pack_bf162(v.x * own + x.x * j.other, v.y * own + x.y * j.other);
+                w.y = pack_bf162(v.z * own + x.z * j.other, v.w * own + x.w * j.other);
+                *reinterpret_cast<uint2*>(a.out + row * a.ldo + head * D + d) = w;
+                if (a.lse && d == 0) a.lse[at_row] = j.lse;
+                return;
+            }
             const float inv = ll == 0.0f ? 0.0f : v_scale / ll;  // no keys: zeros
             uint2 w;
             w.x = pack_bf162(v.x * inv, v.y * inv);

@@ -1,0 +1,237 @@
+// Argument checks and launches that the attention entry points share (tpmlp_attn.cu,
+// tpmlp_attn_open.cu).
+#pragma once
+
+#include <algorithm>
+#include <atomic>
+#include <climits>
+#include <cmath>
+#include <string>
+
+#include "tpmlp_attn.cuh"
+#include "tpmlp_attn_prompt.cuh"
+#include "tpmlp_context.h"
+
+namespace tpmlp {
+
+inline bool is_e4m3(const tpmlp_ctx* c) { return (c->flags & TPMLP_FLAG_KV_E4M3) != 0; }
+
+// Rows of `width` bf16 elements at pitch ld that 16-byte loads may read.
+inline int check_rows(tpmlp_ctx* c, const void* p, int64_t ld, int64_t width) {
+    if (!p) return TPMLP_ERR_INVALID_ARG;
+    if (ld < width || ld > (int64_t(1) << 40)) {
+        c->last_error = "a row pitch is smaller than its row";
+        return TPMLP_ERR_INVALID_ARG;
+    }
+    if (!aligned16(p) || ld % 8) return TPMLP_ERR_MISALIGNED;
+    return TPMLP_OK;
+}
+
+inline int check_kv(tpmlp_ctx* c, const tpmlp_kv* kv, bool lens) {
+    if (!kv || !kv->K || !kv->V || !kv->page_table || (lens && !kv->lens)) return TPMLP_ERR_INVALID_ARG;
+    if (kv->num_pages <= 0 || kv->table_pages <= 0 || kv->B < 0) return TPMLP_ERR_INVALID_ARG;
+    if (kv->num_pages > INT_MAX) return TPMLP_ERR_UNSUPPORTED_SHAPE;
+    if (kv->table_stride != 0 && kv->table_stride < kv->table_pages) return TPMLP_ERR_INVALID_ARG;
+    const int64_t page = static_cast<int64_t>(c->heads_kv) * c->page_size * c->head_dim;
+    if (kv->page_stride != 0 && kv->page_stride < page) return TPMLP_ERR_INVALID_ARG;
+    // key numbers stay below 2^31 with a step of every kernel past the end
+    if (static_cast<int64_t>(kv->table_pages) * c->page_size > (int64_t(1) << 31) - (1 << 16)) {
+        c->last_error = "a sequence's table holds more than 2^31 - 2^16 keys";
+        return TPMLP_ERR_UNSUPPORTED_SHAPE;
+    }
+    const int elem = is_e4m3(c) ? 1 : 2;
+    if (!aligned16(kv->K) || !aligned16(kv->V) || kv->page_stride * elem % 16) return TPMLP_ERR_MISALIGNED;
+    if ((reinterpret_cast<uintptr_t>(kv->page_table) | reinterpret_cast<uintptr_t>(kv->lens)) & 3)
+        return TPMLP_ERR_MISALIGNED;
+    return TPMLP_OK;
+}
+
+inline KvView view_of(const tpmlp_ctx* c, const tpmlp_kv* kv) {
+    const int elem = is_e4m3(c) ? 1 : 2;
+    const int64_t head = static_cast<int64_t>(c->page_size) * c->head_dim;
+    KvView v{};
+    v.K = static_cast<uint8_t*>(kv->K);
+    v.V = static_cast<uint8_t*>(kv->V);
+    v.page_bytes = (kv->page_stride ? kv->page_stride : head * c->heads_kv) * elem;
+    v.head_bytes = head * elem;
+    v.table = kv->page_table;
+    v.table_stride = kv->table_stride ? kv->table_stride : kv->table_pages;
+    v.table_pages = kv->table_pages;
+    while ((1 << v.page_shift) < c->page_size) ++v.page_shift;
+    v.num_pages = static_cast<int32_t>(kv->num_pages);
+    v.lens = kv->lens;
+    v.B = kv->B;
+    v.Hkv = c->heads_kv;
+    v.scales = c->kv_scale;
+    v.status = c->status;
+    return v;
+}
+
+// What a call that would have to allocate answers while its stream is being captured (`first`: the
+// call to be made before the capture).
+inline int refuse_allocation(tpmlp_ctx* c, cudaStream_t s, const char* first) {
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    TPMLP_CUDA(c, cudaStreamIsCapturing(s, &st));
+    if (st == cudaStreamCaptureStatusNone) return TPMLP_OK;
+    c->last_error = std::string("no allocation under stream capture: call ") + first;
+    return TPMLP_ERR_INVALID_ARG;
+}
+
+inline int allocate(tpmlp_ctx* c, void** p, size_t bytes) {
+    const cudaError_t e = cudaMalloc(p, bytes);
+    if (e == cudaSuccess) return TPMLP_OK;
+    *p = nullptr;
+    if (e != cudaErrorMemoryAllocation) return fail_cuda(c, e, "cudaMalloc");
+    cudaGetLastError();
+    return TPMLP_ERR_OOM;
+}
+
+// Launch with programmatic stream serialisation (the kernels wait in griddep_wait before they
+// touch global memory).
+template <typename Kernel, typename... Args>
+int launch(tpmlp_ctx* c, Kernel kern, int64_t grid, int threads, uint32_t smem, cudaStream_t s,
+           const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    TPMLP_CUDA(c, cudaLaunchKernelEx(&cfg, kern, args...));
+    ++c->launches;
+    return TPMLP_OK;
+}
+
+template <typename Kernel>
+int allow_smem(tpmlp_ctx* c, Kernel kern, uint32_t smem, std::atomic<uint64_t>& done) {
+    const uint64_t bit = uint64_t(1) << (c->device & 63);
+    if (done.load(std::memory_order_acquire) & bit) return TPMLP_OK;
+    TPMLP_CUDA(c, cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    done.fetch_or(bit, std::memory_order_acq_rel);
+    return TPMLP_OK;
+}
+
+template <int D, bool FP8, int NT, int PASSES, bool JOIN>
+int launch_rows(tpmlp_ctx* c, const RowArgs& a, cudaStream_t s) {
+    using S = RowShape<D, FP8, NT>;
+    auto kern = attn_row_kernel<D, FP8, NT, PASSES, JOIN>;
+    static std::atomic<uint64_t> done{0};
+    if (int rc = allow_smem(c, kern, S::kSmem, done)) return rc;
+    const int grid = c->num_sms * S::kCtasPerSm;
+    return launch(c, kern, grid, kRowThreads, S::kSmem, s, a);
+}
+
+template <int D, bool FP8, bool JOIN>
+int run_rows_of(tpmlp_ctx* c, const RowArgs& a, cudaStream_t s) {
+    if constexpr (row_heads(D, FP8) > 16)
+        if (a.G > 16) return launch_rows<D, FP8, 2, 2, JOIN>(c, a, s);
+    if constexpr (row_heads(D, FP8) > 8)
+        if (a.G > 8) return launch_rows<D, FP8, 2, 1, JOIN>(c, a, s);
+    return launch_rows<D, FP8, 1, 1, JOIN>(c, a, s);
+}
+
+template <bool JOIN>
+int run_rows(tpmlp_ctx* c, const RowArgs& a, cudaStream_t s) {
+    if (c->head_dim == 128) return is_e4m3(c) ? run_rows_of<128, true, JOIN>(c, a, s) : run_rows_of<128, false, JOIN>(c, a, s);
+    return is_e4m3(c) ? run_rows_of<64, true, JOIN>(c, a, s) : run_rows_of<64, false, JOIN>(c, a, s);
+}
+
+template <int D, bool FP8, bool OPEN>
+int launch_prompt(tpmlp_ctx* c, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                  const PromptArgs& a, cudaStream_t s) {
+    using S = PromptSmem<D, FP8>;
+    auto kern = attn_prompt_kernel<D, FP8, OPEN>;
+    static std::atomic<uint64_t> done{0};
+    if (int rc = allow_smem(c, kern, S::kTotal, done)) return rc;
+    return launch(c, kern, c->num_sms, S::kThreads, S::kTotal, s, q, k, v, a);
+}
+
+// The pool as [page][Hkv * page size][D], in boxes of 64 columns and one page's (at most a
+// block's) rows.
+inline int pool_map(tpmlp_ctx* c, CUtensorMap* map, const void* pool, const KvView& kv) {
+    const uint64_t dims[3] = {static_cast<uint64_t>(c->head_dim),
+                              static_cast<uint64_t>(c->heads_kv) * c->page_size,
+                              static_cast<uint64_t>(kv.num_pages)};
+    const uint64_t strides[2] = {static_cast<uint64_t>(c->head_dim) * 2, static_cast<uint64_t>(kv.page_bytes)};
+    const uint32_t box[3] = {64, static_cast<uint32_t>(std::min(c->page_size, kPB)), 1};
+    return encode_map_typed(c, map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, pool, 3, dims, strides, box);
+}
+
+// part, part_lse (OPEN): see PromptArgs.
+template <bool OPEN>
+int run_prompt(tpmlp_ctx* c, const RowArgs& r, const int32_t* cu_q, int64_t T, cudaStream_t s,
+               float* part = nullptr, float* part_lse = nullptr) {
+    PromptArgs a{};
+    a.kv = r.kv;
+    a.q = r.q;
+    a.ldq = r.ldq;
+    a.out = r.out;
+    a.ldo = r.ldo;
+    a.lse = r.lse;
+    a.cu_q = cu_q;
+    a.T = static_cast<int32_t>(T);
+    a.Hq = r.Hq;
+    a.G = r.G;
+    a.tpt = kPB / r.G;
+    a.scale_log2 = r.scale_log2;
+    a.window = r.window;
+    a.partial = c->attn_partial;
+    a.count = c->attn_count;
+    a.part = part;
+    a.part_lse = part_lse;
+    a.other = r.other;
+    a.other_lse = r.other_lse;
+    CUtensorMap q{}, k{}, v{};
+    if (!is_e4m3(c)) {
+        const uint64_t dims[3] = {static_cast<uint64_t>(c->head_dim), static_cast<uint64_t>(c->heads_q),
+                                  static_cast<uint64_t>(T)};
+        const uint64_t strides[2] = {static_cast<uint64_t>(c->head_dim) * 2, static_cast<uint64_t>(a.ldq) * 2};
+        const uint32_t box[3] = {64, static_cast<uint32_t>(a.G), static_cast<uint32_t>(a.tpt)};
+        int rc = encode_map_typed(c, &q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, 3, dims, strides, box);
+        if (rc || (rc = pool_map(c, &k, a.kv.K, a.kv)) || (rc = pool_map(c, &v, a.kv.V, a.kv))) return rc;
+    }
+    if (c->head_dim == 128)
+        return is_e4m3(c) ? launch_prompt<128, true, OPEN>(c, q, k, v, a, s) : launch_prompt<128, false, OPEN>(c, q, k, v, a, s);
+    return is_e4m3(c) ? launch_prompt<64, true, OPEN>(c, q, k, v, a, s) : launch_prompt<64, false, OPEN>(c, q, k, v, a, s);
+}
+
+// What decode and prompt check alike; rows: rows of Q and Out.
+inline int check_attend(tpmlp_ctx* c, const void* Q, int64_t ldq, const tpmlp_kv* kv, float scale,
+                 const void* Out, int64_t ldo, const float* Lse) {
+    if (int rc = check_kv(c, kv, true)) return rc;
+    if (!(scale > 0.0f) || !std::isfinite(scale)) return TPMLP_ERR_INVALID_ARG;
+    const int64_t width = static_cast<int64_t>(c->heads_q) * c->head_dim;
+    if (int rc = check_rows(c, Q, ldq, width)) return rc;
+    if (int rc = check_rows(c, Out, ldo, width)) return rc;
+    if (reinterpret_cast<uintptr_t>(Lse) & 3) return TPMLP_ERR_MISALIGNED;
+    return TPMLP_OK;
+}
+
+inline RowArgs row_args(const tpmlp_ctx* c, const void* Q, int64_t ldq, const tpmlp_kv* kv,
+                        float scale, int32_t window, void* Out, int64_t ldo, float* Lse) {
+    RowArgs a{};
+    a.kv = view_of(c, kv);
+    a.q = static_cast<const __nv_bfloat16*>(Q);
+    a.ldq = ldq;
+    a.out = static_cast<__nv_bfloat16*>(Out);
+    a.ldo = ldo;
+    a.lse = Lse;
+    a.Hq = c->heads_q;
+    a.G = c->heads_q / c->heads_kv;
+    a.scale_log2 = scale * 1.44269504088896341f;
+    a.window = window;
+    a.partial = c->attn_partial;
+    a.count = c->attn_count;
+    return a;
+}
+
+inline int check_attention(tpmlp_ctx* c) {
+    if (!c || c->kind != kKindAttention) return TPMLP_ERR_INVALID_ARG;
+    return check_device(c);
+}
+
+}  // namespace tpmlp

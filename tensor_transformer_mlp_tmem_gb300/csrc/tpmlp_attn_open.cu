@@ -1,0 +1,88 @@
+// Entry points of attention without a causal mask (include/tpmlp.h): to all keys of another sequence,
+// and of one token of each sequence to a prefix that several share and to its own keys. In a
+// translation unit of its own: its kernels compile beside those of tpmlp_attn.cu.
+#include <climits>
+
+#include "tpmlp_attn_launch.h"
+
+using namespace tpmlp;
+
+namespace {
+
+// The workspace of decode_shared holds `rows` sequences.
+int reserve_shared(tpmlp_ctx* c, int64_t rows, cudaStream_t s, bool own_call) {
+    if (rows <= c->shared_rows) return TPMLP_OK;
+    if (!own_call)
+        if (int rc = refuse_allocation(c, s, "tpmlp_attn_reserve before the capture")) return rc;
+    const int64_t now = std::max(rows, 2 * c->shared_rows);
+    void* p = nullptr;
+    const size_t bytes = static_cast<size_t>(now) * c->heads_q * (c->head_dim + 1) * sizeof(float);
+    if (int rc = allocate(c, &p, bytes)) return rc;
+    c->shared[c->shared_n++] = static_cast<float*>(p);
+    c->shared_rows = now;
+    return TPMLP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int tpmlp_attn_cross(tpmlp_ctx* c, const void* Q, int64_t ldq, int64_t T, const int32_t* cu_q,
+                     const tpmlp_kv* kv, float scale, void* Out, int64_t ldo, float* Lse, void* stream) {
+    if (int rc = check_attention(c)) return rc;
+    if (!kv || T < 0) return TPMLP_ERR_INVALID_ARG;
+    if (T == 0 || kv->B == 0) return TPMLP_OK;
+    if (T > INT_MAX / 2) return TPMLP_ERR_UNSUPPORTED_SHAPE;
+    if (int rc = check_attend(c, Q, ldq, kv, scale, Out, ldo, Lse)) return rc;
+    if (!cu_q) return TPMLP_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(cu_q) & 3) return TPMLP_ERR_MISALIGNED;
+    const RowArgs a = row_args(c, Q, ldq, kv, scale, 0, Out, ldo, Lse);
+    return run_prompt<true>(c, a, cu_q, T, static_cast<cudaStream_t>(stream));
+}
+
+int tpmlp_attn_reserve(tpmlp_ctx* c, int64_t max_sequences) {
+    if (int rc = check_attention(c)) return rc;
+    if (max_sequences < 0) return TPMLP_ERR_INVALID_ARG;
+    if (max_sequences > INT_MAX / 2) return TPMLP_ERR_UNSUPPORTED_SHAPE;
+    return reserve_shared(c, max_sequences, nullptr, true);
+}
+
+int tpmlp_attn_decode_shared(tpmlp_ctx* c, const void* Q, int64_t ldq, const tpmlp_kv* prefix,
+                             const int32_t* cu, const tpmlp_kv* kv, float scale, void* Out,
+                             int64_t ldo, float* Lse, void* stream) {
+    if (int rc = check_attention(c)) return rc;
+    if (!kv || !prefix) return TPMLP_ERR_INVALID_ARG;
+    if (kv->B == 0) return TPMLP_OK;
+    if (prefix->B == 0) return tpmlp_attn_decode(c, Q, ldq, kv, scale, 0, Out, ldo, Lse, stream);
+    if (kv->B > INT_MAX / 2) return TPMLP_ERR_UNSUPPORTED_SHAPE;
+    if (int rc = check_attend(c, Q, ldq, kv, scale, Out, ldo, Lse)) return rc;
+    if (int rc = check_kv(c, prefix, true)) return rc;
+    if (!cu) return TPMLP_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(cu) & 3) return TPMLP_ERR_MISALIGNED;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (int rc = reserve_shared(c, kv->B, s, false)) return rc;
+    float* const part = c->shared[c->shared_n - 1];
+    float* const part_lse = part + c->shared_rows * c->heads_q * c->head_dim;
+    const RowArgs p = row_args(c, Q, ldq, prefix, scale, 0, Out, ldo, nullptr);
+    if (int rc = run_prompt<true>(c, p, cu, kv->B, s, part, part_lse)) return rc;
+    RowArgs a = row_args(c, Q, ldq, kv, scale, 0, Out, ldo, Lse);
+    a.rows = kv->B;
+    a.other = part;
+    a.other_lse = part_lse;
+    if (a.G > row_heads(c->head_dim, is_e4m3(c))) return run_prompt<true>(c, a, nullptr, kv->B, s);
+    return run_rows<true>(c, a, s);
+}
+
+int tpmlp_attn_cross_packed(const tpmlp_attend_args* a) {
+    if (!a || a->window != 0) return TPMLP_ERR_INVALID_ARG;
+    return tpmlp_attn_cross(a->ctx, a->Q, a->ldq, a->T, a->cu_q, a->kv, static_cast<float>(a->scale), a->Out,
+                            a->ldo, a->Lse, a->stream);
+}
+
+int tpmlp_attn_decode_shared_packed(const tpmlp_shared_args* a) {
+    if (!a) return TPMLP_ERR_INVALID_ARG;
+    return tpmlp_attn_decode_shared(a->ctx, a->Q, a->ldq, a->prefix, a->cu, a->kv, static_cast<float>(a->scale),
+                                    a->Out, a->ldo, a->Lse, a->stream);
+}
+
+}  // extern "C"

@@ -101,6 +101,15 @@ struct tpmlp_ctx {
     float* attn_partial = nullptr;   // partial sums of split key ranges (tpmlp_attn.cuh)
     uint32_t* attn_count = nullptr;  // arrivals at a split key range, one counter per CTA
     size_t attn_counters = 0;        // entries of attn_count
+    uint16_t* norm_w = nullptr;      // [heads_q + heads_kv][head_dim] bf16 (tpmlp_attn_set_norms)
+    bool norm_on = false, norm_per_head = false;
+    float norm_eps = 0.0f;
+    // tpmlp_attn_decode_shared: results over prefixes, fp32 [shared_rows][heads_q][head_dim] and the
+    // logs [shared_rows][heads_q]. Captured graphs hold a buffer's address, so the smaller ones before
+    // the last stay until the context goes; each is at least twice the one before.
+    float* shared[40] = {};
+    int shared_n = 0;
+    int64_t shared_rows = 0;
 
     int* status = nullptr;  // device status: kStatusWords
     int64_t launches = 0;
