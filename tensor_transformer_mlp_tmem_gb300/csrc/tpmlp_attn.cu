@@ -15,6 +15,40 @@ namespace {
 
 constexpr int kRowCtasPerSm = 2;
 
+template <int D, bool FP8>
+int launch_prompt(tpmlp_ctx* c, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                  const PromptArgs& a, cudaStream_t s) {
+    using S = PromptSmem<D, FP8>;
+    auto kern = attn_prompt_kernel<D, FP8>;
+    static std::atomic<uint64_t> done{0};
+    if (int rc = allow_smem(c, kern, S::kTotal, done)) return rc;
+    return launch(c, kern, c->num_sms, S::kThreads, S::kTotal, s, q, k, v, a);
+}
+
+int run_prompt(tpmlp_ctx* c, const RowArgs& r, const int32_t* cu_q, int64_t T, cudaStream_t s) {
+    PromptArgs a{};
+    a.kv = r.kv;
+    a.q = r.q;
+    a.ldq = r.ldq;
+    a.out = r.out;
+    a.ldo = r.ldo;
+    a.lse = r.lse;
+    a.cu_q = cu_q;
+    a.T = static_cast<int32_t>(T);
+    a.Hq = r.Hq;
+    a.G = r.G;
+    a.tpt = kPB / r.G;
+    a.scale_log2 = r.scale_log2;
+    a.window = r.window;
+    a.partial = c->attn_partial;
+    a.count = c->attn_count;
+    CUtensorMap q{}, k{}, v{};
+    if (int rc = prompt_maps(c, r, T, a.tpt, &q, &k, &v)) return rc;
+    if (c->head_dim == 128)
+        return is_e4m3(c) ? launch_prompt<128, true>(c, q, k, v, a, s) : launch_prompt<128, false>(c, q, k, v, a, s);
+    return is_e4m3(c) ? launch_prompt<64, true>(c, q, k, v, a, s) : launch_prompt<64, false>(c, q, k, v, a, s);
+}
+
 // Tokens of an append block: as many as its threads' units hold, but no fewer blocks than run at
 // once. 16384 tokens of 12 + 12 heads of 64, 16 + 2 of 64, 8 + 1 of 128 in e4m3, 1 + 1 of 64: 30, 16, 23,
 // 9 us (a block for each token: 37, 27, 34, 25).
@@ -215,7 +249,7 @@ int tpmlp_attn_decode(tpmlp_ctx* c, const void* Q, int64_t ldq, const tpmlp_kv* 
     RowArgs a = row_args(c, Q, ldq, kv, scale, window, Out, ldo, Lse);
     a.rows = kv->B;
     if (a.G > row_heads(c->head_dim, is_e4m3(c)))
-        return run_prompt<false>(c, a, nullptr, kv->B, static_cast<cudaStream_t>(stream));
+        return run_prompt(c, a, nullptr, kv->B, static_cast<cudaStream_t>(stream));
     return run_rows<false>(c, a, static_cast<cudaStream_t>(stream));
 }
 
@@ -230,7 +264,7 @@ int tpmlp_attn_prompt(tpmlp_ctx* c, const void* Q, int64_t ldq, int64_t T, const
     if (!cu_q) return TPMLP_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(cu_q) & 3) return TPMLP_ERR_MISALIGNED;
     const RowArgs a = row_args(c, Q, ldq, kv, scale, window, Out, ldo, Lse);
-    return run_prompt<false>(c, a, cu_q, T, static_cast<cudaStream_t>(stream));
+    return run_prompt(c, a, cu_q, T, static_cast<cudaStream_t>(stream));
 }
 
 int tpmlp_attn_append_packed(const tpmlp_append_args* a) {

@@ -107,10 +107,12 @@ int launch(tpmlp_ctx* c, Kernel kern, int64_t grid, int threads, uint32_t smem, 
 }
 
 template <typename Kernel>
-int allow_smem(tpmlp_ctx* c, Kernel kern, uint32_t smem, std::atomic<uint64_t>& done) {
+int allow_smem(tpmlp_ctx* c, Kernel kern, uint32_t smem, std::atomic<uint64_t>& done, int carveout = -1) {
     const uint64_t bit = uint64_t(1) << (c->device & 63);
     if (done.load(std::memory_order_acquire) & bit) return TPMLP_OK;
     TPMLP_CUDA(c, cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    if (carveout >= 0)
+        TPMLP_CUDA(c, cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, carveout));
     done.fetch_or(bit, std::memory_order_acq_rel);
     return TPMLP_OK;
 }
@@ -120,7 +122,11 @@ int launch_rows(tpmlp_ctx* c, const RowArgs& a, cudaStream_t s) {
     using S = RowShape<D, FP8, NT>;
     auto kern = attn_row_kernel<D, FP8, NT, PASSES, JOIN>;
     static std::atomic<uint64_t> done{0};
-    if (int rc = allow_smem(c, kern, S::kSmem, done)) return rc;
+    // Loads in flight lie in what shared memory leaves of an SM's 256 KB. Without this an SM keeps the split
+    // of the launch before it while that has room enough: behind a prompt kernel 28 KB of loads, and 64
+    // sequences of at most 1024 keys x 32 heads take 150 us instead of 98.
+    constexpr int kCarveout = static_cast<int>((S::kCtasPerSm * (S::kSmem + 2048) * 100 + 233471) / 233472);
+    if (int rc = allow_smem(c, kern, S::kSmem, done, kCarveout)) return rc;
     const int grid = c->num_sms * S::kCtasPerSm;
     return launch(c, kern, grid, kRowThreads, S::kSmem, s, a);
 }
@@ -140,16 +146,6 @@ int run_rows(tpmlp_ctx* c, const RowArgs& a, cudaStream_t s) {
     return is_e4m3(c) ? run_rows_of<64, true, JOIN>(c, a, s) : run_rows_of<64, false, JOIN>(c, a, s);
 }
 
-template <int D, bool FP8, bool OPEN>
-int launch_prompt(tpmlp_ctx* c, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                  const PromptArgs& a, cudaStream_t s) {
-    using S = PromptSmem<D, FP8>;
-    auto kern = attn_prompt_kernel<D, FP8, OPEN>;
-    static std::atomic<uint64_t> done{0};
-    if (int rc = allow_smem(c, kern, S::kTotal, done)) return rc;
-    return launch(c, kern, c->num_sms, S::kThreads, S::kTotal, s, q, k, v, a);
-}
-
 // The pool as [page][Hkv * page size][D], in boxes of 64 columns and one page's (at most a
 // block's) rows.
 inline int pool_map(tpmlp_ctx* c, CUtensorMap* map, const void* pool, const KvView& kv) {
@@ -161,42 +157,17 @@ inline int pool_map(tpmlp_ctx* c, CUtensorMap* map, const void* pool, const KvVi
     return encode_map_typed(c, map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, pool, 3, dims, strides, box);
 }
 
-// part, part_lse (OPEN): see PromptArgs.
-template <bool OPEN>
-int run_prompt(tpmlp_ctx* c, const RowArgs& r, const int32_t* cu_q, int64_t T, cudaStream_t s,
-               float* part = nullptr, float* part_lse = nullptr) {
-    PromptArgs a{};
-    a.kv = r.kv;
-    a.q = r.q;
-    a.ldq = r.ldq;
-    a.out = r.out;
-    a.ldo = r.ldo;
-    a.lse = r.lse;
-    a.cu_q = cu_q;
-    a.T = static_cast<int32_t>(T);
-    a.Hq = r.Hq;
-    a.G = r.G;
-    a.tpt = kPB / r.G;
-    a.scale_log2 = r.scale_log2;
-    a.window = r.window;
-    a.partial = c->attn_partial;
-    a.count = c->attn_count;
-    a.part = part;
-    a.part_lse = part_lse;
-    a.other = r.other;
-    a.other_lse = r.other_lse;
-    CUtensorMap q{}, k{}, v{};
-    if (!is_e4m3(c)) {
-        const uint64_t dims[3] = {static_cast<uint64_t>(c->head_dim), static_cast<uint64_t>(c->heads_q),
-                                  static_cast<uint64_t>(T)};
-        const uint64_t strides[2] = {static_cast<uint64_t>(c->head_dim) * 2, static_cast<uint64_t>(a.ldq) * 2};
-        const uint32_t box[3] = {64, static_cast<uint32_t>(a.G), static_cast<uint32_t>(a.tpt)};
-        int rc = encode_map_typed(c, &q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, 3, dims, strides, box);
-        if (rc || (rc = pool_map(c, &k, a.kv.K, a.kv)) || (rc = pool_map(c, &v, a.kv.V, a.kv))) return rc;
-    }
-    if (c->head_dim == 128)
-        return is_e4m3(c) ? launch_prompt<128, true, OPEN>(c, q, k, v, a, s) : launch_prompt<128, false, OPEN>(c, q, k, v, a, s);
-    return is_e4m3(c) ? launch_prompt<64, true, OPEN>(c, q, k, v, a, s) : launch_prompt<64, false, OPEN>(c, q, k, v, a, s);
+// The tensor maps of a bf16 cache's pools and of T rows of queries in boxes of G heads x `tokens`.
+inline int prompt_maps(tpmlp_ctx* c, const RowArgs& r, int64_t T, int tokens, CUtensorMap* q, CUtensorMap* k,
+                       CUtensorMap* v) {
+    if (is_e4m3(c)) return TPMLP_OK;
+    const uint64_t dims[3] = {static_cast<uint64_t>(c->head_dim), static_cast<uint64_t>(c->heads_q),
+                              static_cast<uint64_t>(T)};
+    const uint64_t strides[2] = {static_cast<uint64_t>(c->head_dim) * 2, static_cast<uint64_t>(r.ldq) * 2};
+    const uint32_t box[3] = {64, static_cast<uint32_t>(r.G), static_cast<uint32_t>(tokens)};
+    if (int rc = encode_map_typed(c, q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, r.q, 3, dims, strides, box)) return rc;
+    if (int rc = pool_map(c, k, r.kv.K, r.kv)) return rc;
+    return pool_map(c, v, r.kv.V, r.kv);
 }
 
 // What decode and prompt check alike; rows: rows of Q and Out.

@@ -4,10 +4,50 @@
 #include <climits>
 
 #include "tpmlp_attn_launch.h"
+#include "tpmlp_attn_open.cuh"
 
 using namespace tpmlp;
 
 namespace {
+
+template <int D, bool FP8>
+int launch_open(tpmlp_ctx* c, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                const OpenArgs& a, cudaStream_t s) {
+    using S = OpenShape<D, FP8>;
+    auto kern = attn_open_kernel<D, FP8>;
+    static std::atomic<uint64_t> done{0};
+    if (int rc = allow_smem(c, kern, S::kTotal, done)) return rc;
+    return launch(c, kern, c->num_sms, S::kThreads, S::kTotal, s, q, k, v, a);
+}
+
+// part, part_lse: see OpenArgs.
+int run_open(tpmlp_ctx* c, const RowArgs& r, const int32_t* cu_q, int64_t T, cudaStream_t s,
+                    float* part = nullptr, float* part_lse = nullptr) {
+    OpenArgs a{};
+    a.kv = r.kv;
+    a.q = r.q;
+    a.ldq = r.ldq;
+    a.out = r.out;
+    a.ldo = r.ldo;
+    a.lse = r.lse;
+    a.cu_q = cu_q;
+    a.T = static_cast<int32_t>(T);
+    a.Hq = r.Hq;
+    a.G = r.G;
+    a.tpt = kPB / r.G;
+    a.scale_log2 = r.scale_log2;
+    a.partial = c->attn_partial;
+    a.count = c->attn_count;
+    a.part = part;
+    a.part_lse = part_lse;
+    a.other = r.other;
+    a.other_lse = r.other_lse;
+    CUtensorMap q{}, k{}, v{};
+    if (int rc = prompt_maps(c, r, T, a.tpt, &q, &k, &v)) return rc;
+    if (c->head_dim == 128)
+        return is_e4m3(c) ? launch_open<128, true>(c, q, k, v, a, s) : launch_open<128, false>(c, q, k, v, a, s);
+    return is_e4m3(c) ? launch_open<64, true>(c, q, k, v, a, s) : launch_open<64, false>(c, q, k, v, a, s);
+}
 
 // The workspace of decode_shared holds `rows` sequences.
 int reserve_shared(tpmlp_ctx* c, int64_t rows, cudaStream_t s, bool own_call) {
@@ -37,7 +77,7 @@ int tpmlp_attn_cross(tpmlp_ctx* c, const void* Q, int64_t ldq, int64_t T, const 
     if (!cu_q) return TPMLP_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(cu_q) & 3) return TPMLP_ERR_MISALIGNED;
     const RowArgs a = row_args(c, Q, ldq, kv, scale, 0, Out, ldo, Lse);
-    return run_prompt<true>(c, a, cu_q, T, static_cast<cudaStream_t>(stream));
+    return run_open(c, a, cu_q, T, static_cast<cudaStream_t>(stream));
 }
 
 int tpmlp_attn_reserve(tpmlp_ctx* c, int64_t max_sequences) {
@@ -64,12 +104,12 @@ int tpmlp_attn_decode_shared(tpmlp_ctx* c, const void* Q, int64_t ldq, const tpm
     float* const part = c->shared[c->shared_n - 1];
     float* const part_lse = part + c->shared_rows * c->heads_q * c->head_dim;
     const RowArgs p = row_args(c, Q, ldq, prefix, scale, 0, Out, ldo, nullptr);
-    if (int rc = run_prompt<true>(c, p, cu, kv->B, s, part, part_lse)) return rc;
+    if (int rc = run_open(c, p, cu, kv->B, s, part, part_lse)) return rc;
     RowArgs a = row_args(c, Q, ldq, kv, scale, 0, Out, ldo, Lse);
     a.rows = kv->B;
     a.other = part;
     a.other_lse = part_lse;
-    if (a.G > row_heads(c->head_dim, is_e4m3(c))) return run_prompt<true>(c, a, nullptr, kv->B, s);
+    if (a.G > row_heads(c->head_dim, is_e4m3(c))) return run_open(c, a, nullptr, kv->B, s);
     return run_rows<true>(c, a, s);
 }
 

@@ -1,0 +1,1137 @@
+// Attention of rows to all keys of their sequence (no causal mask) over a paged cache, on the tensor
+// cores: tokens or beams to an encoder's states, and a batch's single tokens to a prefix they share.
+//
+// Tiles, items, key blocks and the two products are those of the causal kernel
+// (tpmlp_attn_prompt.cuh): a tile is up to 128 rows (row = token * G + head of the group), an item two
+// tiles of one kv head, K and V come in blocks of 128 keys, and the tiles step through them 64 keys
+// at a time: S = Q K^T in tensor memory, P = 2^(S c - m) over S in 16 bits, O += P V. Without a mask all
+// rows of an item see the same keys, which is what this kernel is made of:
+//  - every item of a sequence has the same number of blocks, so that a CTA finds its share of the work
+//    by arithmetic, for any number of items;
+//  - values that are not finite need no second way (no row has a weight of 0 for a key it should not
+//    see, but for the last block's, whose rows are cleared);
+//  - heads of 64 leave tensor memory for an accumulator O for even and one for odd steps. Each has its
+//    own four softmax warps (a stream), whose maxima and sums meet at the end of the item.
+//
+// Warps: 4 per stream do softmax (D = 64: streams (tile, parity) 00, 01, 10, 11; D = 128: one to a
+// tile), then one warp each for the MMAs of tile 0, the loads, the MMAs of tile 1 and the work list;
+// e4m3 caches: further ones convert the loaded bytes to fp16.
+//
+// What bounds it: a softmax step is a chain of latencies of one warp (load of S 110 cycles, maximum 270,
+// weights 355, store 50, hand-over 200, alone on its scheduler), so the streams on a scheduler share it
+// well: MEASURED
+#pragma once
+
+#include "tpmlp_attn_prompt.cuh"
+
+namespace tpmlp {
+
+constexpr int kOpenCode = 0x4000;  // wait sites: kOpenCode | role
+constexpr int kOpenRuns = 512;     // entries of the table of sequences
+
+struct OpenArgs {
+    KvView kv;
+    const __nv_bfloat16* q;
+    int64_t ldq;
+    __nv_bfloat16* out;
+    int64_t ldo;
+    float* lse;
+    const int32_t* cu_q;  // null: one row of each sequence (T = B)
+    int32_t T, Hq, G, tpt;  // tpt: tokens per tile
+    float scale_log2;
+    float* partial;   // [CTAs][2 pieces][2 tiles] slots of kPromptSlotFloats
+    uint32_t* count;  // [CTAs][2 tiles] arrivals, then items dealt and CTAs done; 0 between launches
+    // where results go instead of out, in fp32 (null: they go to out), or what they are joined with on
+    // the way to out (null: nothing); both as RowArgs' other and other_lse
+    float *part, *part_lse;
+    const float *other, *other_lse;
+};
+
+template <int D, bool FP8>
+struct OpenShape {
+    static constexpr int U = D == 64 ? 2 : 1;  // streams to a tile
+    static constexpr int kGroups = 2 * U;      // of four softmax warps
+    static constexpr int kConvert = FP8 ? (D == 64 ? 4 : 8) : 0;  // warps that convert
+    static constexpr int kWarp0 = 4 * kGroups;                    // first of the other roles
+    static constexpr int kThreads = 32 * (kWarp0 + 4 + kConvert);
+    // Registers of a softmax thread and of the others: together at most what the block is launched with
+    // (65536 over its threads, a multiple of 8 each: 168, 96, 96, 80).
+    static constexpr int kLaunch = 65536 / kThreads / 8 * 8;
+    static constexpr int kSoftmaxRegs = D == 128 ? (FP8 ? 144 : 184) : (FP8 ? 88 : 104);
+    static constexpr int kOtherRegs = D == 128 ? (FP8 ? 64 : 136) : 64;
+    static_assert(32 * kWarp0 * kSoftmaxRegs + (kThreads - 32 * kWarp0) * kOtherRegs <= kThreads * kLaunch,
+                  "the register split draws on what the block was launched with");
+
+    static constexpr bool kReload = U == 2 && FP8;  // scores are loaded twice instead of being held
+
+    static constexpr uint32_t kTile = kPB * D * 2;  // a Q, K or V tile of 16-bit values
+    static constexpr uint32_t kRaw = FP8 ? kPB * D : 0;
+    static constexpr int kStages = D == 128 ? (FP8 ? 3 : 4) : 8;
+    static constexpr int kRaws = FP8 ? (D == 128 ? 2 : 4) : 0;
+    static constexpr uint32_t kStage0 = 2 * kTile;
+    static constexpr uint32_t kRaw0 = kStage0 + kStages * kTile;
+    static constexpr uint32_t kBars = kRaw0 + kRaws * kRaw;
+    static constexpr int kNumBars = 2 * kStages + 2 * kRaws + 48;
+    static constexpr uint32_t kCtl = kBars + 8 * kNumBars;  // TMEM address, abort, s_last [2], groups [8]
+    static constexpr uint32_t kPieces0 = kCtl + 64;
+    static constexpr uint32_t kMeet = kPieces0 + 4 * 64;    // [2][2 tiles][U][128] (m, l), U = 2
+    static constexpr uint32_t kUp = kMeet + (U == 2 ? 2 * 2 * U * 128 * 8 : 0);  // [2 tiles][128] fp32, e4m3
+    static constexpr uint32_t kTables = kUp + (FP8 ? 2 * 128 * 4 : 0);
+    static constexpr uint32_t kTotal = 1024 + kTables + 2 * (kOpenRuns + 1) * 8 + 64;
+    static_assert(kTotal <= 232448, "dynamic shared memory per CTA");
+    static_assert(kStages / 2 + 1 < 8, "blocks in flight, against the ring of loaded groups");
+};
+
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// A sequence's rows: [first, first + n) of Q, all of which see its first `len` keys.
+struct OpenSeq {
+    int first, n, len;
+};
+__device__ __forceinline__ OpenSeq open_seq(const OpenArgs& a, int b) {
+    OpenSeq s;
+    s.first = a.cu_q ? max(0, min(a.cu_q[b], a.T)) : b;
+    s.n = a.cu_q ? max(0, min(a.cu_q[b + 1], a.T) - s.first) : 1;
+    s.len = kv_length(a.kv, b);
+    return s;
+}
+
+// An item, or the part of its key blocks [b0, b1) that one CTA computes.
+struct OpenPiece {
+    int valid;
+    int h, b;            // kv head, sequence
+    int len;             // its keys
+    int row0;            // row of Q of tile 0's first token
+    int tokens[2];       // of each tile
+    int b0, b1;          // blocks
+    int first, last;     // contributing CTAs
+    int starts;          // 1: the item's first blocks are in this piece
+    __device__ __forceinline__ int begin() const { return 2 * b0; }
+    __device__ __forceinline__ int end(int t) const {
+        return tokens[t] > 0 ? min((len + kSB - 1) / kSB, 2 * b1) : 2 * b0;
+    }
+};
+static_assert(sizeof(OpenPiece) <= 64, "piece slots");
+constexpr int kOpenPieces = 4;  // between the work list's warp and the others
+
+// The CTA's work list. A sequence's items are numbered by kv head and then by tile, so that those that
+// share keys are at work together. An item's work is a unit for its start and its blocks.
+struct OpenWork {
+    const int64_t *items_at, *units_at;  // items and work before each run of `run` sequences
+    int runs, run;
+    int64_t items;
+    bool split;            // equal runs of work instead of whole items
+    int64_t at, end, per;  // split: this CTA's run of work, the length of every run
+
+    __device__ __forceinline__ static int64_t tiles(const OpenArgs& a, const OpenSeq& s) {
+        return (s.n + 2ll * a.tpt - 1) / (2 * a.tpt);
+    }
+    __device__ __forceinline__ static int64_t blocks(const OpenSeq& s) { return (s.len + int64_t(kPB) - 1) / kPB; }
+
+    // The sequence of the k-th item (UNITS: unit); k becomes its number within the sequence.
+    template <bool UNITS>
+    __device__ __forceinline__ int locate(const OpenArgs& a, int64_t& k, OpenSeq& s) const {
+        const int64_t* const table = UNITS ? units_at : items_at;
+        int lo = 0, hi = runs;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (table[mid] <= k) lo = mid;
+            else hi = mid;
+        }
+        k -= table[lo];
+        int b = lo * run;
+        s = open_seq(a, b);
+        while (b + 1 < a.kv.B) {
+            const int64_t n = tiles(a, s) * a.kv.Hkv * (UNITS ? 1 + blocks(s) : 1);
+            if (k < n) break;
+            k -= n;
+            s = open_seq(a, ++b);
+        }
+        return b;
+    }
+    __device__ __forceinline__ static void item(const OpenArgs& a, int b, const OpenSeq& s, int64_t k, OpenPiece& p) {
+        const uint32_t nt = max(1u, static_cast<uint32_t>(tiles(a, s)));
+        uint32_t h, j;
+        if (k <= 0xFFFFFFFFll) {
+            h = static_cast<uint32_t>(k) / nt;
+            j = static_cast<uint32_t>(k) - h * nt;
+        } else {
+            h = static_cast<uint32_t>(k / nt);
+            j = static_cast<uint32_t>(k % nt);
+        }
+        p.valid = 1;
+        p.b = b;
+        p.h = min(static_cast<int>(h), a.kv.Hkv - 1);
+        p.len = s.len;
+        const int tok0 = static_cast<int>(j) * 2 * a.tpt;
+        p.row0 = s.first + tok0;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) p.tokens[t] = max(0, min(s.n - tok0 - t * a.tpt, a.tpt));
+        p.b0 = 0;
+        p.b1 = static_cast<int>(blocks(s));
+        p.first = p.last = 0;
+        p.starts = 1;
+    }
+    __device__ __forceinline__ OpenPiece next(const OpenArgs& a) {
+        OpenPiece p;
+        p.valid = 0;
+        OpenSeq s;
+        if (!split) {
+            // items are dealt to whichever CTA asks next (who computes an item does not change its
+            // result); one lane asks
+            uint32_t k = 0;
+            if ((threadIdx.x & 31) == 0) k = atomicAdd(a.count + 2 * gridDim.x, 1u);
+            int64_t r = __shfl_sync(~0u, k, 0);
+            if (r >= items) return p;
+            const int b = locate<false>(a, r, s);
+            item(a, b, s, r, p);
+            return p;
+        }
+        while (at < end) {
+            int64_t r = at;
+            const int b = locate<true>(a, r, s);
+            const int64_t each = 1 + blocks(s);
+            const int64_t k = r / each, u0 = at - (r - k * each), u1 = u0 + each;
+            item(a, b, s, k, p);
+            const int from = max(static_cast<int>(at - u0) - 1, 0);
+            at = min(end, u1);
+            const int upto = static_cast<int>(at - u0) - 1;
+            if (upto == 0 && each > 1) {  // the start alone: its blocks are the next CTA's
+                p.valid = 0;
+                continue;
+            }
+            p.first = static_cast<int>((u0 + (each > 1)) / per);
+            p.last = static_cast<int>((u1 - 1) / per);
+            p.starts = from == 0;
+            p.b0 = from;
+            p.b1 = upto;
+            return p;
+        }
+        return p;
+    }
+};
+
+// Rows of V past the item's last key or in a page that is not there, in a group of 16 that the product
+// reads: their weights are 0, but 0 times what they hold may be NaN; they are cleared first (by both
+// tiles' warps alike).
+template <int D>
+__device__ __noinline__ void clear_rows(uint8_t* block, int in, uint32_t have, int lane) {
+    constexpr int kLanes = D / 8;  // to a row, 16 bytes each per 64 columns
+    const int upto = min(kPB, (in + 15) & ~15), piece = lane % kLanes;
+    for (int r = (have == 0xFFu ? in : 0) + lane / kLanes; r < upto; r += 32 / kLanes)
+        if (r >= in || !((have >> (r >> 4)) & 1u))
+            *reinterpret_cast<uint4*>(block + (piece >> 3) * 16384 + r * 128 + (piece & 7) * 16) = make_uint4(0, 0, 0, 0);
+}
+
+// Where a row's result goes. Its sums are scaled by `scale`, which this sets anew where the row is joined
+// with its result over other keys; add() then adds that result, and put() rounds and writes.
+template <int D, bool FP8>
+struct OpenRow {
+    float* part = nullptr;
+    const float* other = nullptr;
+    __nv_bfloat16* out = nullptr;
+    float* lse_at = nullptr;
+    float by = 0.0f, lse = 0.0f;
+    // row, head: of Q; m, l: maximum and sum; on: there is such a row
+    __device__ __forceinline__ OpenRow(const OpenArgs& a, bool on, int64_t row, int64_t head, float m, float l,
+                                       float v_scale, float& scale) {
+        if (!on) return;
+        constexpr float kRaise = FP8 ? kRaiseLog2 : 0.0f;
+        const int64_t at = row * a.Hq + head;
+        out = a.out + row * a.ldo + head * D;
+        if (a.part) {
+            part = a.part + at * D;
+            lse = l == 0.0f ? -CUDART_INF_F : m + log2f(l) - kRaise;
+            lse_at = a.part_lse + at;
+            return;
+        }
+        if (a.lse) lse_at = a.lse + at;
+        if (a.other) {
+            const float lo = __ldcg(a.other_lse + at);
+            const Joined j = join_keys(m, l, kRaise, lo);
+            scale = j.own * v_scale;
+            by = j.other;
+            lse = j.lse;
+            if (lo != -CUDART_INF_F) other = a.other + at * D;
+        } else if (a.lse) {
+            lse = l == 0.0f ? -CUDART_INF_F : (m + log2f(l) - kRaise) * 0.69314718055994531f;
+        }
+    }
+    // N columns from `col` on, scaled already
+    template <int N>
+    __device__ __forceinline__ void put(float (&v)[N], int col) const {
+        if (part) {
+#pragma unroll
+            for (int k = 0; k < N; k += 4)
+                *reinterpret_cast<float4*>(part + col + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+            return;
+        }
+        if (other) {
+#pragma unroll
+            for (int k = 0; k < N; k += 4) {
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(other + col + k));
+                v[k] += x.x * by;
+                v[k + 1] += x.y * by;
+                v[k + 2] += x.z * by;
+                v[k + 3] += x.w * by;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < N; k += 8) {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = v[k + e];
+            *reinterpret_cast<uint4*>(out + col + k) = pack8_bf16(x);
+        }
+    }
+    __device__ __forceinline__ void put_lse() const {
+        if (lse_at) *lse_at = lse;
+    }
+};
+
+// The result of the first `count` rows of tile t of a split item, from its contributors' slots, first
+// to last. The tile's N threads call it (who: the thread's number), P to a row, each with an equal part
+// of the columns: 16 loads of 16 bytes in flight, however few the rows.
+template <int D, bool FP8, int N, int P>
+__device__ __forceinline__ void join_open(const OpenArgs& a, const OpenPiece& p, int t, int who, int count,
+                                          const float* slots, float v_scale) {
+    constexpr int kRows = N / P, kCols = D / P;      // a thread's columns
+    constexpr int kChunk = kCols < 64 ? kCols : 64;  // of which it sums so many at a time,
+    constexpr int kAtOnce = 64 / kChunk;             // of so many contributors
+    const int r = who % kRows, part = who / kRows;
+    const int from = p.first, upto = p.last;
+    if (r >= count) return;
+    auto slot_of = [&](int cta) {
+        return slots + (static_cast<int64_t>(cta) * 2 + (cta == from)) * 2 * kPromptSlotFloats;
+    };
+    float mm = -CUDART_INF_F, ll = 0.0f;
+    for (int x0 = from; x0 <= upto; x0 += kJoinLoads) {
+        float mx[kJoinLoads], lx[kJoinLoads], top = mm;
+#pragma unroll
+        for (int u = 0; u < kJoinLoads; ++u) {
+            const float* src = slot_of(min(x0 + u, upto)) + 128 * 128 + r;
+            mx[u] = __ldcg(src);
+            lx[u] = x0 + u <= upto ? __ldcg(src + 128) : 0.0f;
+        }
+#pragma unroll
+        for (int u = 0; u < kJoinLoads; ++u) top = fmaxf(top, mx[u]);
+        const float safe = top == -CUDART_INF_F ? 0.0f : top;
+        ll *= exp2_approx(mm - safe);
+        mm = top;
+#pragma unroll
+        for (int u = 0; u < kJoinLoads; ++u) ll += exp2_approx(mx[u] - safe) * lx[u];
+    }
+    const float safe = mm == -CUDART_INF_F ? 0.0f : mm;
+    float scale = ll == 0.0f ? 0.0f : v_scale / ll;
+    const OpenRow<D, FP8> to(a, true, p.row0 + t * a.tpt + r / a.G, static_cast<int64_t>(p.h) * a.G + r % a.G, mm, ll,
+                             v_scale, scale);
+#pragma unroll 1
+    for (int col = part * kCols; col < (part + 1) * kCols; col += kChunk) {
+        float v[kChunk];
+#pragma unroll
+        for (int k = 0; k < kChunk; ++k) v[k] = 0.0f;
+#pragma unroll 1
+        for (int x0 = from; x0 <= upto; x0 += kAtOnce) {
+            float4 y[kAtOnce][kChunk / 4];
+            float w[kAtOnce];
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                const float* src = slot_of(min(x0 + u, upto));
+#pragma unroll
+                for (int k = 0; k < kChunk / 4; ++k)
+                    y[u][k] = __ldcg(reinterpret_cast<const float4*>(src + (col + 4 * k) * 128 + r * 4));
+                w[u] = __ldcg(src + 128 * 128 + r);
+            }
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                // past the last one, sums of 0 as well (see the row kernel)
+                const bool on = x0 + u <= upto;
+                const float f = on ? exp2_approx(w[u] - safe) : 0.0f;
+#pragma unroll
+                for (int k = 0; k < kChunk / 4; ++k) {
+                    v[4 * k] += f * (on ? y[u][k].x : 0.0f);
+                    v[4 * k + 1] += f * (on ? y[u][k].y : 0.0f);
+                    v[4 * k + 2] += f * (on ? y[u][k].z : 0.0f);
+                    v[4 * k + 3] += f * (on ? y[u][k].w : 0.0f);
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kChunk; ++k) v[k] = ll == 0.0f ? 0.0f : v[k] * scale;
+        to.put(v, col);
+    }
+    if (part == 0) to.put_lse();
+}
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__(OpenShape<D, FP8>::kThreads, 1)
+attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ OpenArgs a) {
+    using L = OpenShape<D, FP8>;
+    constexpr int NST = L::kStages, NRAW = L::kRaws, U = L::U, W0 = L::kWarp0;
+    constexpr uint32_t kIdescS = prompt_idesc(kSB, FP8, false);
+    constexpr uint32_t kIdescO = prompt_idesc(D, FP8, true);
+    constexpr uint32_t kHalf = 16384;  // bytes of 64 columns x 128 rows
+
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* const base_ptr = smem_raw + (base - raw);
+    const uint32_t bars = base + L::kBars;
+    auto full = [&](int s) { return bars + 8u * s; };
+    auto empty = [&](int s) { return bars + 8u * (NST + s); };
+    auto raw_full = [&](int s) { return bars + 8u * (2 * NST + s); };
+    auto raw_empty = [&](int s) { return bars + 8u * (2 * NST + NRAW + s); };
+    const uint32_t more = bars + 8u * (2 * NST + 2 * NRAW);
+    auto q_full = [&](int t) { return more + 8u * t; };
+    const uint32_t q_empty = more + 16u;
+    const uint32_t drain = more + 24u;
+    auto join_in = [&](int t) { return more + 32u + 8u * t; };
+    auto join_out = [&](int t) { return more + 48u + 8u * t; };
+    auto meet = [&](int t) { return more + 64u + 8u * t; };
+    auto s_full = [&](int t, int buf) { return more + 80u + 16u * t + 8u * buf; };
+    auto p_full = [&](int t, int buf) { return more + 112u + 16u * t + 8u * buf; };
+    // of the streams (tile, parity)
+    auto o_full = [&](int t, int u) { return more + 144u + 16u * t + 8u * u; };
+    auto o_empty = [&](int t, int u) { return more + 176u + 16u * t + 8u * u; };
+    auto pv_done = [&](int t, int u) { return more + 208u + 16u * t + 8u * u; };
+    auto piece_full = [&](int s) { return more + 240u + 8u * s; };
+    auto piece_empty = [&](int s) { return more + 272u + 8u * s; };
+    static_assert(304 <= 48 * 8, "barriers");
+    uint32_t* const ctl = reinterpret_cast<uint32_t*>(base_ptr + L::kCtl);
+    volatile uint32_t* const abort_flag = ctl + 1;
+    uint32_t* const s_last = ctl + 2;           // [2]
+    volatile uint32_t* const groups = ctl + 4;  // [8] loaded groups of 16 keys of the last 8 blocks
+    auto piece_of = [&](uint32_t k) {
+        return reinterpret_cast<const OpenPiece*>(base_ptr + L::kPieces0 + (k % kOpenPieces) * 64);
+    };
+    int64_t* const items_at = reinterpret_cast<int64_t*>(base_ptr + L::kTables);
+    int64_t* const units_at = items_at + kOpenRuns + 1;
+    int64_t* const found = units_at + kOpenRuns + 1;  // items, units, longest item
+
+    const int warp = __shfl_sync(~0u, static_cast<int>(threadIdx.x) >> 5, 0);
+    const int lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NST; ++s) {
+            ptx::mbar_init(full(s), FP8 ? L::kConvert : 1);
+            ptx::mbar_init(empty(s), 2);
+        }
+        for (int s = 0; s < NRAW; ++s) {
+            ptx::mbar_init(raw_full(s), 1);
+            ptx::mbar_init(raw_empty(s), L::kConvert);
+        }
+        for (int t = 0; t < 2; ++t) {
+            ptx::mbar_init(q_full(t), FP8 ? 4 * U : 1);
+            for (int buf = 0; buf < 2; ++buf) {
+                ptx::mbar_init(s_full(t, buf), 1);
+                ptx::mbar_init(p_full(t, buf), 4);
+                ptx::mbar_init(o_full(t, buf), 1);
+                ptx::mbar_init(o_empty(t, buf), 4 * U);
+                ptx::mbar_init(pv_done(t, buf), 1);
+            }
+            ptx::mbar_init(join_in(t), 4 * U);
+            ptx::mbar_init(join_out(t), 1);
+            ptx::mbar_init(meet(t), 4 * U);
+        }
+        for (int s = 0; s < kOpenPieces; ++s) {
+            ptx::mbar_init(piece_full(s), 1);
+            ptx::mbar_init(piece_empty(s), W0 + 3 + L::kConvert);
+        }
+        ptx::mbar_init(q_empty, 2);
+        ptx::mbar_init(drain, 2);
+        *abort_flag = 0u;
+        ptx::fence_barrier_init();
+    }
+    if (!FP8 && warp == W0 + 1 && lane == 0) {
+        ptx::prefetch_tensormap(&tmQ);
+        ptx::prefetch_tensormap(&tmK);
+        ptx::prefetch_tensormap(&tmV);
+    }
+    if (warp == W0) {
+        ptx::tmem_alloc(ptx::smem_addr(ctl), 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+
+    if (a.part) {
+        // rows of no sequence have no keys; whoever joins their results has to know
+        const int first = max(0, min(a.cu_q[0], a.T)), last = max(0, min(a.cu_q[a.kv.B], a.T));
+        const int64_t n = (first + static_cast<int64_t>(a.T) - last) * a.Hq;
+        for (int64_t i = static_cast<int64_t>(blockIdx.x) * L::kThreads + threadIdx.x; i < n;
+             i += static_cast<int64_t>(gridDim.x) * L::kThreads)
+            a.part_lse[i < static_cast<int64_t>(first) * a.Hq ? i : i + static_cast<int64_t>(last - first) * a.Hq] =
+                -CUDART_INF_F;
+    }
+
+    // ---------------------------------------------------------------- the work list
+    OpenWork work;
+    work.items_at = items_at;
+    work.units_at = units_at;
+    work.run = (a.kv.B + kOpenRuns - 1) / kOpenRuns;
+    work.runs = (a.kv.B + work.run - 1) / work.run;
+    if (threadIdx.x == 0) found[2] = 0;
+    __syncthreads();
+    for (int e = threadIdx.x; e < work.runs; e += L::kThreads) {
+        int64_t items = 0, units = 0;
+        int most = 0;
+        for (int b = e * work.run; b < min(a.kv.B, (e + 1) * work.run); ++b) {
+            const OpenSeq s = open_seq(a, b);
+            const int64_t n = OpenWork::tiles(a, s) * a.kv.Hkv, each = 1 + OpenWork::blocks(s);
+            items += n;
+            units += n * each;
+            if (n) most = max(most, static_cast<int>(each));
+        }
+        items_at[e] = items;
+        units_at[e] = units;
+        atomicMax(reinterpret_cast<int*>(found + 2), most);
+    }
+    __syncthreads();
+    if (warp < 2) {
+        // running sums, a table to a warp
+        int64_t* const table = warp ? units_at : items_at;
+        const int each = (work.runs + 31) / 32;
+        int64_t sum = 0;
+        for (int i = 0; i < each; ++i)
+            if (lane * each + i < work.runs) sum += table[lane * each + i];
+        int64_t before = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(~0u, before, o);
+            if (lane >= o) before += v;
+        }
+        if (lane == 31) found[warp] = before;
+        before -= sum;
+        for (int i = 0; i < each; ++i)
+            if (lane * each + i < work.runs) {
+                const int64_t n = table[lane * each + i];
+                table[lane * each + i] = before;
+                before += n;
+            }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    work.items = found[0];
+    work.split = false;
+    work.at = work.end = 0;
+    work.per = 1;
+    {
+        // Work is split evenly where the longest item, or about half of it in the last round, would keep
+        // the GPU waiting for more than a tenth over what the split's partial sums and joins cost:
+        // kJoinFew blocks of time where there is no more than an item for a CTA, kJoinMany where there
+        // are more (every CTA then has two pieces to hand over, and what was dealt would have filled
+        // the gaps).
+        constexpr int kJoinFew = 8, kJoinMany = 16;
+        const int64_t total = found[1], g = gridDim.x;
+        const int64_t most = *reinterpret_cast<const int*>(found + 2);
+        const int64_t share = max((total + g - 1) / g, int64_t(1));
+        const int64_t whole = work.items <= g ? most : share + most / 2;
+        const int join = work.items <= g ? kJoinFew : kJoinMany;
+        if (10 * whole > 11 * (share + join)) {
+            work.split = true;
+            work.per = share;
+            work.at = share * blockIdx.x;
+            work.end = min(work.at + share, total);
+        }
+    }
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(ctl);
+    auto tmem_s = [&](int t, int buf) { return tmem + 256u + 128u * t + kSB * buf; };
+    auto tmem_o = [&](int t, int u) { return tmem + static_cast<uint32_t>(D * (U * t + u)); };
+    // (polls for a while before the bounded wait, which reads the global timer)
+    auto wait = [&](uint32_t bar, uint32_t parity, int role, uint64_t limit_ns = ptx::kWaitLimitNs) {
+        bool done = false;
+        for (int n = 0; n < 64 && !done; ++n) done = ptx::mbar_try_wait(bar, parity);
+        return __all_sync(~0u, done || ptx::mbar_wait(bar, parity, abort_flag, a.kv.status, kOpenCode | role, limit_ns));
+    };
+
+    if (warp < W0) regs_up<L::kSoftmaxRegs>();
+    else regs_down<L::kOtherRegs>();
+
+    // The pieces, in the order that every role goes through them. next_piece() waits for one (null:
+    // no more, or a wait gave up); release_piece() hands its slot back.
+    uint32_t piece_at = 0;
+    auto next_piece = [&]() -> const OpenPiece* {
+        if (!wait(piece_full(piece_at % kOpenPieces), (piece_at / kOpenPieces) & 1u, 15, kPieceWaitNs)) return nullptr;
+        const OpenPiece* p = piece_of(piece_at);
+        return p->valid ? p : nullptr;
+    };
+    auto release_piece = [&] {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(piece_empty(piece_at % kOpenPieces));
+        ++piece_at;
+    };
+
+    if (warp < W0) {
+        // ------------------------------------------------------------ softmax of one stream
+        const int t = (warp >> 2) / U, u = (warp >> 2) % U;
+        const int row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        uint32_t s_phase = 0, o_phase = 0, q_empty_phase = 0, q_full_phase = 0, j_phase = 0, meet_phase = 0, blocks = 0;
+        uint32_t pv_count = 0;  // products P V of this stream so far
+        const int token = row / a.G, head = row - token * a.G;
+        while (const OpenPiece* p = next_piece()) {
+            const int tokens = p->tokens[t];
+            const bool mine = token < tokens;
+            // the row and head of Q that this thread has
+            auto qrow = [&] { return static_cast<int64_t>(p->row0) + t * a.tpt + token; };
+            auto qhead = [&] { return static_cast<int64_t>(p->h) * a.G + head; };
+            const int len = p->len, b0 = p->b0, b1 = p->b1;
+            const int begin = p->begin(), end = p->end(t);
+            float c = a.scale_log2;
+            if constexpr (FP8) {
+                if (b1 > b0) {
+                    if (tokens > 0) {
+                        // Q in fp16, scaled (query_exponent). A row's D / 8 lanes load 16 bytes each,
+                        // neighbours side by side, up to 8 loads in flight (a thread to a row, 16 bytes of
+                        // 32 rows to a load: 7 us for 256 rows of 128). The factor that the row was
+                        // divided by goes to the thread that has the row.
+                        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kSteps = 32 / U / kAtOnce;
+                        constexpr int kLoads = kSteps < 8 ? kSteps : 8;
+                        float* const up = reinterpret_cast<float*>(base_ptr + L::kUp) + t * 128;
+                        const __nv_bfloat16* mine_at = mine ? a.q + qrow() * a.ldq + qhead() * D : nullptr;
+                        if (!wait(q_empty, q_empty_phase ^ 1u, 1, kPieceWaitNs)) break;
+#pragma unroll 1
+                        for (int x0 = 0; x0 < kSteps; x0 += kLoads) {
+                            uint4 v[kLoads];
+#pragma unroll
+                            for (int x = 0; x < kLoads; ++x) {
+                                const int r = u * (32 / U) + (x0 + x) * kAtOnce + lane / kLanes;
+                                const auto at = __shfl_sync(~0u, reinterpret_cast<unsigned long long>(mine_at), r);
+                                v[x] = make_uint4(0, 0, 0, 0);
+                                if (at) v[x] = load16(reinterpret_cast<const uint8_t*>(at) + 16 * (lane % kLanes));
+                            }
+#pragma unroll
+                            for (int x = 0; x < kLoads; ++x) {
+                                const int r = u * (32 / U) + (x0 + x) * kAtOnce + lane / kLanes, piece = lane % kLanes;
+                                float f[8], big = 0.0f;
+                                unpack8(v[x], f);
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(f[k]));
+#pragma unroll
+                                for (int o = 1; o < kLanes; o <<= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, o));
+                                const int e = query_exponent(big), in_tile = (warp & 3) * 32 + r;
+                                const float down = power_of_two(-e);
+                                uint8_t* const dst = base_ptr + t * L::kTile + in_tile * 128;
+                                *reinterpret_cast<uint4*>(dst + (piece >> 3) * kHalf + (((piece & 7) ^ (in_tile & 7)) << 4)) =
+                                    make_uint4(pack_half2(f[0] * down, f[1] * down), pack_half2(f[2] * down, f[3] * down),
+                                               pack_half2(f[4] * down, f[5] * down), pack_half2(f[6] * down, f[7] * down));
+                                if (piece == 0) up[in_tile] = power_of_two(e);
+                            }
+                        }
+                        fence_async_shared();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(q_full(t));
+                        if (!wait(q_full(t), q_full_phase, 4)) break;
+                        q_full_phase ^= 1u;
+                        c = c * a.kv.scales[p->h] * up[row];
+                        if (c == 0.0f) c = FLT_MIN;  // 0 times a masked score of -infinity would be NaN
+                    }
+                    q_empty_phase ^= 1u;
+                }
+            }
+            float m = -CUDART_INF_F, l = 0.0f;  // reference maximum (log2 units), sum
+            const uint32_t block0 = blocks - b0;
+            blocks += b1 - b0;
+            bool ok = true;
+            for (int j = begin + u; j < end; j += U) {
+                const int buf = j & 1;
+                if (!(ok = wait(s_full(t, buf), (s_phase >> buf) & 1u, 2))) break;
+                s_phase ^= 1u << buf;
+                const uint32_t have = (groups[(block0 + (j >> 1)) & 7] >> (4 * buf)) & 0xFu;
+                ptx::tc_fence_after();
+                const uint32_t ts = tmem_s(t, buf) + lanes;
+                // 32 of the step's keys, those that are not there masked
+                const int below = len - j * kSB;
+                const bool cut = below < kSB || have != 0xFu;
+                auto load = [&](int half, uint32_t (&s)[32]) {
+                    ptx::tmem_ld_32x32b_x32(ts + 32 * half, s);
+                };
+                auto loaded = [&](int half, uint32_t (&s)[32]) {
+                    ptx::tmem_wait_ld(s);
+                    if (cut) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            s[k] = 32 * half + k < below && ((have >> (2 * half + (k >> 4))) & 1u) ? s[k] : 0xFF800000u;
+                    }
+                };
+                uint32_t lo[32], hi[32];
+                load(1, hi);
+                load(0, lo);
+                loaded(1, hi);
+                float top[4];
+                auto highest = [&](const uint32_t (&s)[32]) {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            top[x] = max3(top[x], __uint_as_float(s[k + x]), __uint_as_float(s[k + 4 + x]));
+                };
+#pragma unroll
+                for (int x = 0; x < 4; ++x) top[x] = -CUDART_INF_F;
+                highest(hi);
+                loaded(0, lo);
+                highest(lo);
+                const float now = fmaxf(max3(top[0], top[1], top[2]), top[3]) * c;
+                const bool move = now > m + kLazyLog2;
+                if (__any_sync(~0u, move)) {
+                    const float f = move ? exp2_approx(m - now) : 1.0f;
+                    if (move) m = now;
+                    l *= f;
+                    // O of the steps before is scaled, once the last of their products is done
+                    if (j >= begin + U) {
+                        if (!(ok = wait(pv_done(t, u), (pv_count - 1) & 1u, 17))) break;
+                        ptx::tc_fence_after();
+#pragma unroll 1
+                        for (int x = 0; x < D; x += 16) {
+                            uint32_t o[16];
+                            ptx::tmem_ld_32x32b_x16_wait(tmem_o(t, u) + lanes + x, o);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                            ptx::tmem_st_32x32b_x16_wait(tmem_o(t, u) + lanes + x, o);
+                        }
+                    }
+                }
+                ++pv_count;
+                // P = 2^(S c - m), two values to an instruction where there is one; rounded to 16 bits for
+                // the product with V, of V's type (both operands of these instructions have one type):
+                // half a step of a weight is 2^-8 of it in bf16, 2^-11 in fp16; its sum is taken before
+                const float shift = (FP8 ? kRaiseLog2 : 0.0f) - (m == -CUDART_INF_F ? 0.0f : m);
+                const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
+                float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                auto weights = [&](int half, const uint32_t (&s)[32]) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        float2 e = fma2(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), c2, shift2);
+                        e.x = exp2_approx(e.x);
+                        e.y = exp2_approx(e.y);
+                        sum[k & 1] = add2(sum[k & 1], e);
+                        w[k] = FP8 ? pack_half2(e.x, e.y) : pack_bf162(e.x, e.y);
+                    }
+                    tmem_st_x16(ts + 16 * half, w);
+                };
+                // (P takes the columns of the first 32 keys' scores. Where registers are few, the last 32's
+                // are loaded a second time.)
+                weights(0, lo);
+                if constexpr (L::kReload) {
+                    load(1, hi);
+                    loaded(1, hi);
+                }
+                weights(1, hi);
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                tmem_wait_st();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full(t, buf));
+            }
+            if (!ok) break;
+            // -------------------------------------------------------- the tile's result
+            if (tokens == 0) {
+                release_piece();
+                continue;
+            }
+            // steps of the tile's streams; their factors (of one reference maximum for both)
+            const int steps = end - begin;
+            float factor[U];
+            factor[0] = 1.0f;
+            if constexpr (U == 2) {
+                float2* const at = reinterpret_cast<float2*>(base_ptr + L::kMeet) + (meet_phase * 2 + t) * 2 * 128;
+                at[u * 128 + row] = make_float2(m, l);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(meet(t));
+                if (!wait(meet(t), meet_phase, 18)) break;
+                meet_phase ^= 1u;
+                const float2 other = at[(u ^ 1) * 128 + row];
+                const float both = fmaxf(m, other.x), safe = both == -CUDART_INF_F ? 0.0f : both;
+                const float fm = exp2_approx(m - safe), fo = exp2_approx(other.x - safe);
+                l = l * fm + other.y * fo;
+                m = both;
+                factor[u] = fm;
+                factor[u ^ 1] = fo;
+            }
+            const bool whole = p->first == p->last;
+            float* const slots = a.partial + static_cast<int64_t>(t) * kPromptSlotFloats;
+            float* const slot = slots + (static_cast<int64_t>(blockIdx.x) * 2 + p->starts) * 2 * kPromptSlotFloats;
+            const float v_scale = FP8 ? a.kv.scales[a.kv.Hkv + p->h] : 1.0f;
+            float inv = l == 0.0f ? 0.0f : v_scale / l;  // no keys: zeros
+            const OpenRow<D, FP8> to(a, mine && whole, qrow(), qhead(), m, l, v_scale, inv);
+#pragma unroll
+            for (int x = 0; x < U; ++x)
+                if (steps > x) {
+                    if (!(ok = wait(o_full(t, x), (o_phase >> x) & 1u, 3))) break;
+                    o_phase ^= 1u << x;
+                }
+            if (!ok) break;
+            ptx::tc_fence_after();
+            constexpr int kCols = D / U;  // this stream's part of the columns
+#pragma unroll 1
+            for (int col = u * kCols; col < (u + 1) * kCols; col += 16) {
+                __syncwarp();
+                float v[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[k] = 0.0f;
+#pragma unroll
+                for (int x = 0; x < U; ++x)
+                    if (steps > x) {
+                        uint32_t o[16];
+                        ptx::tmem_ld_32x32b_x16_wait(tmem_o(t, x) + lanes + col, o);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            v[k] = U == 1 ? __uint_as_float(o[k]) : fmaf(factor[x], __uint_as_float(o[k]), v[k]);
+                    }
+                if (mine && whole) {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) v[k] = l == 0.0f ? 0.0f : v[k] * inv;
+                    to.put(v, col);
+                } else if (mine) {
+#pragma unroll
+                    for (int k = 0; k < 16; k += 4)
+                        __stcg(reinterpret_cast<float4*>(slot + (col + k) * 128 + row * 4),
+                               make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]));
+                }
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+#pragma unroll
+                for (int x = 0; x < U; ++x)
+                    if (steps > x) mbar_arrive(o_empty(t, x));
+            }
+            if (whole) {
+                if (u == 0) to.put_lse();
+            } else {
+                // The last contributor to arrive sums all of them, first to last (see the row kernel);
+                // each tile's threads count and join on their own.
+                if (mine && u == 0) {
+                    __stcg(slot + 128 * 128 + row, m);
+                    __stcg(slot + 128 * 128 + 128 + row, l);
+                }
+                __threadfence();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(join_in(t));
+                if (warp == 4 * U * t) {
+                    if (!wait(join_in(t), j_phase, 13)) break;
+                    if (lane == 0) {
+                        __threadfence();
+                        const uint32_t n = atomicAdd(a.count + 2 * p->first + t, 1u);
+                        s_last[t] = n == static_cast<uint32_t>(p->last - p->first);
+                        if (s_last[t]) a.count[2 * p->first + t] = 0;
+                        __threadfence();
+                        mbar_arrive(join_out(t));
+                    }
+                    __syncwarp();
+                }
+                if (!wait(join_out(t), j_phase, 14)) break;
+                j_phase ^= 1u;
+                if (*reinterpret_cast<volatile uint32_t*>(s_last + t)) {
+                    __threadfence();
+                    const int count = tokens * a.G, who = u * 128 + row;
+                    constexpr int N = 128 * U;
+                    if (count > 64) join_open<D, FP8, N, U>(a, *p, t, who, count, slots, v_scale);
+                    else if (count > 32) join_open<D, FP8, N, 2 * U>(a, *p, t, who, count, slots, v_scale);
+                    else if (D == 64 || count > 16) join_open<D, FP8, N, 4 * U>(a, *p, t, who, count, slots, v_scale);
+                    else if constexpr (D == 128) join_open<D, FP8, N, 8>(a, *p, t, who, count, slots, v_scale);
+                }
+            }
+            release_piece();
+        }
+    } else if (warp == W0 || warp == W0 + 2) {
+        // ------------------------------------------------------------ MMAs of one tile
+        const int t = (warp - W0) >> 1;
+        const uint64_t dq = sdesc_k128(base + t * L::kTile);
+        uint32_t stage = 0, phase = 0, q_phase = 0, p_phase = 0, o_phase = 0, blocks = 0;
+        bool ok = true;
+        while (ok) {
+            const OpenPiece* p = next_piece();
+            if (!p) break;
+            const int b0 = p->b0, b1 = p->b1, begin = p->begin(), end = p->end(t), len = p->len;
+            if (b1 > b0) {
+                // (a tile without rows waits for the other's: its word that Q is free must not come
+                // before that of the piece before is complete)
+                const int x = p->tokens[t] > 0 ? t : 0;
+                if (!(ok = wait(q_full(x), (q_phase >> x) & 1u, 4))) break;
+                q_phase ^= p->tokens[1] > 0 ? 3u : 1u;
+                ptx::tc_fence_after();
+            }
+            // Round i: O += P V for the two steps of block i - 1, each followed by S of the step
+            // two later (block i), which may overwrite that P once its product has been issued.
+            for (int i = b0; i <= b1; ++i) {
+                const uint32_t vs = stage, vph = phase;
+                uint32_t ks = vs, kph = vph;
+                if (i > b0 && ++ks == NST) {
+                    ks = 0;
+                    kph ^= 1u;
+                }
+                const uint32_t sv = L::kStage0 + vs * L::kTile;
+                const uint64_t dv = sdesc_v(base + sv), dk = sdesc_k128(base + L::kStage0 + ks * L::kTile);
+                if (i > b0) {
+                    if (!(ok = wait(full(vs), vph, 5))) break;
+                    const uint32_t have = groups[(blocks + i - 1 - b0) & 7];
+                    if (len < i * kPB || have != 0xFFu) {
+                        clear_rows<D>(base_ptr + sv, len - (i - 1) * kPB, have, lane);
+                        fence_async_shared();
+                        __syncwarp();
+                    }
+                }
+                if (i < b1) {
+                    if (!(ok = wait(full(ks), kph, 8))) break;
+                    ptx::tc_fence_after();
+                }
+#pragma unroll
+                for (int par = 0; par < 2; ++par) {
+                    const int jv = 2 * (i - 1) + par, jk = 2 * i + par;
+                    const int u = U == 2 ? par : 0;
+                    const uint32_t ts = tmem_s(t, par), to = tmem_o(t, u);
+                    if (i > b0 && jv < end) {
+                        const bool fresh = jv < begin + U;
+                        if (fresh) {  // the stream's result before this one has been read
+                            if (!(ok = wait(o_empty(t, u), ((o_phase >> u) & 1u) ^ 1u, 6))) break;
+                            o_phase ^= 1u << u;
+                        }
+                        if (!(ok = wait(p_full(t, par), (p_phase >> par) & 1u, 7))) break;
+                        p_phase ^= 1u << par;
+                        ptx::tc_fence_after();
+                        const int groups16 = min(kSB, len - jv * kSB + 15) / 16;
+                        if (elect_one()) {
+                            if (groups16 == kSB / 16) {
+#pragma unroll
+                                for (int k = 0; k < kSB / 16; ++k)
+                                    mma_ts(to, ts + 8 * k, dv + 512 * par + 128 * k, kIdescO, k == 0 ? !fresh : 1u);
+                            } else {
+                                for (int k = 0; k < groups16; ++k)
+                                    mma_ts(to, ts + 8 * k, dv + 512 * par + 128 * k, kIdescO, k == 0 ? !fresh : 1u);
+                            }
+                            ptx::mma_commit(pv_done(t, u));
+                            if (jv + U >= end) ptx::mma_commit(o_full(t, u));
+                        }
+                        __syncwarp();
+                    }
+                    if (i < b1 && jk < end) {
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < D / 16; ++k) {
+                                const uint32_t off = (k >> 2) * (kHalf >> 4) + 2 * (k & 3);
+                                ptx::mma_bf16_ss(ts, dq + off, dk + 512 * par + off, kIdescS, k ? 1u : 0u);
+                            }
+                            ptx::mma_commit(s_full(t, par));
+                        }
+                        __syncwarp();
+                    }
+                }
+                if (!ok) break;
+                if (elect_one()) {
+                    if (i > b0) ptx::mma_commit(empty(vs));
+                    if (i < b1) ptx::mma_commit(empty(ks));
+                    if (i + 1 == b1) ptx::mma_commit(q_empty);  // the last use of Q
+                }
+                __syncwarp();
+                stage = ks;
+                phase = kph;
+                if (i < b1 && ++stage == NST) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (!ok) break;
+            blocks += b1 - b0;
+            release_piece();
+        }
+        __syncwarp();
+        if (elect_one()) {
+            // every product has completed before tensor memory is released
+            ptx::mma_commit(drain);
+            ptx::mbar_wait_drain(drain, 0);
+        }
+        __syncwarp();
+    } else if (warp == W0 + 1) {
+        // ------------------------------------------------------------ TMA producer
+        const int rows = min(1 << a.kv.page_shift, kPB);  // of a copy
+        const int copies = kPB / rows;
+        uint32_t stage = 0, phase = 0, issued = 0, q_phase = 0, q_loads[2] = {0, 0}, blocks = 0;
+        constexpr int NR = FP8 ? NRAW : NST;
+        bool ok = true;
+        while (ok) {
+            const OpenPiece* p = next_piece();
+            if (!p) break;
+            const int b0 = p->b0, b1 = p->b1, h = p->h, b = p->b, len = p->len;
+            // whether this lane copies a part of block i (not past the last key)
+            auto wanted = [&](int i) { return lane < copies && i < b1 && i * kPB + lane * rows < len; };
+            // the table's entry for this lane's copy of a block, looked up a block ahead
+            auto entry = [&](int i) { return wanted(i) ? kv_entry(a.kv, b, i * kPB + lane * rows) : 0; };
+            int next = entry(b0);
+            for (int i = b0; ok && i < b1; ++i) {
+                const int key = i * kPB + lane * rows;
+                const bool in = wanted(i);
+                const int found_page = next;
+                next = entry(i + 1);
+                const int64_t page = in ? kv_checked(a.kv, found_page) : -1;
+                const uint32_t there = __ballot_sync(~0u, page >= 0);
+                // groups of 16 keys that are there; those outside the item's keys count as such
+                uint32_t have = 0xFFu;
+                const uint32_t missing = __ballot_sync(~0u, in && page < 0);
+                if (missing) {
+                    for (int x = 0; x < copies; ++x)
+                        if ((missing >> x) & 1u) have &= ~(((1u << (rows / 16)) - 1u) << (x * (rows / 16)));
+                }
+                const int slot = key & ((1 << a.kv.page_shift) - 1);
+                for (int kv = 0; kv < 2; ++kv) {
+                    const uint32_t bar_full = FP8 ? raw_full(stage) : full(stage);
+                    if (!(ok = wait(FP8 ? raw_empty(stage) : empty(stage), phase ^ 1u, 10))) break;
+#ifdef TPMLP_TEST_SKIP_STAGE
+                    // a stage that is never filled: the waits for it run out
+                    const bool fill = issued != TPMLP_TEST_SKIP_STAGE;
+#else
+                    constexpr bool fill = true;
+#endif
+                    if (lane == 0 && fill) {
+                        if (kv == 0) groups[(blocks + i - b0) & 7] = have;
+                        ptx::mbar_arrive_expect_tx(bar_full, static_cast<uint32_t>(__popc(there) * rows) * D * (FP8 ? 1 : 2));
+                    }
+                    __syncwarp();
+                    if (page >= 0 && fill) {
+                        if constexpr (FP8) {
+                            bulk_load(base + L::kRaw0 + stage * L::kRaw + lane * rows * D,
+                                      (kv ? a.kv.V : a.kv.K) + page * a.kv.page_bytes + h * a.kv.head_bytes +
+                                          static_cast<int64_t>(slot) * D,
+                                      static_cast<uint32_t>(rows) * D, bar_full);
+                        } else {
+                            const uint32_t dst = base + L::kStage0 + stage * L::kTile + lane * rows * 128;
+#pragma unroll
+                            for (int x = 0; x < D / 64; ++x)
+                                ptx::tma_load_3d(dst + x * kHalf, kv ? &tmV : &tmK, bar_full, 64 * x,
+                                                 (h << a.kv.page_shift) + slot, static_cast<int>(page));
+                        }
+                    }
+                    __syncwarp();
+                    ++issued;
+                    if (++stage == NR) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                    if (!FP8 && i == b0 && kv == 0) {
+                        // Q after the first keys, which need not wait for the piece before
+                        if (!(ok = wait(q_empty, q_phase ^ 1u, 9, kPieceWaitNs))) break;
+                        q_phase ^= 1u;
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            if (p->tokens[t] == 0) continue;
+                            if (lane == 0) {
+                                ptx::mbar_arrive_expect_tx(q_full(t), static_cast<uint32_t>(a.tpt * a.G) * D * 2);
+                                for (int x = 0; x < D / 64; ++x)
+                                    ptx::tma_load_3d(base + t * L::kTile + x * kHalf, &tmQ, q_full(t), 64 * x, h * a.G,
+                                                     p->row0 + t * a.tpt);
+                            }
+                            ++q_loads[t];
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
+            if (!ok) break;
+            blocks += b1 - b0;
+            release_piece();
+        }
+        if ((!ok || *abort_flag) && lane == 0) {
+            // wait for the copies still in flight before the CTA may exit (also when another role
+            // gave up, and no piece came after the last one)
+            for (uint32_t s = 0; s < NR && s < issued; ++s) {
+                const uint32_t last = s + ((issued - 1 - s) / NR) * NR;
+                ptx::mbar_wait_drain(FP8 ? raw_full(s) : full(s), (last / NR) & 1u);
+            }
+            for (int t = 0; t < 2; ++t)
+                if (q_loads[t]) ptx::mbar_wait_drain(q_full(t), (q_loads[t] - 1) & 1u);
+        }
+        __syncwarp();
+    } else if (warp == W0 + 3) {
+        // ------------------------------------------------------------ work list
+        for (;; ++piece_at) {
+            if (!wait(piece_empty(piece_at % kOpenPieces), ((piece_at / kOpenPieces) & 1u) ^ 1u, 16, kPieceWaitNs)) break;
+            const OpenPiece p = work.next(a);
+            if (lane == 0) {
+                if (p.valid) *const_cast<OpenPiece*>(piece_of(piece_at)) = p;
+                else const_cast<OpenPiece*>(piece_of(piece_at))->valid = 0;
+                mbar_arrive(piece_full(piece_at % kOpenPieces));
+            }
+            __syncwarp();
+            if (!p.valid) break;
+        }
+        if (!work.split && lane == 0) {
+            // the last CTA to have asked in vain leaves the counters at 0 for the next launch
+            uint32_t* const done = a.count + 2 * gridDim.x + 1;
+            if (atomicAdd(done, 1u) == gridDim.x - 1) {
+                done[-1] = 0;
+                done[0] = 0;
+            }
+        }
+    } else if (FP8) {
+        // ------------------------------------------------------------ e4m3 -> fp16
+        uint32_t rs = 0, rph = 0, stage = 0, phase = 0;
+        bool ok = true;
+        const int tid = (warp - W0 - 4) * 32 + lane;
+        while (ok) {
+            const OpenPiece* p = next_piece();
+            if (!p) break;
+            const int n = 2 * (p->b1 - p->b0);
+            release_piece();
+            for (int x0 = 0; x0 < n; ++x0) {
+                if (!(ok = wait(raw_full(rs), rph, 11))) break;
+                if (!(ok = wait(empty(stage), phase ^ 1u, 12))) break;
+                const uint8_t* src = base_ptr + L::kRaw0 + rs * L::kRaw;
+                uint8_t* dst = base_ptr + L::kStage0 + stage * L::kTile;
+                constexpr int kAll = 32 * (FP8 ? L::kConvert : 1);
+                constexpr int kParts = kPB * D / 16 / kAll;  // 16-byte parts per thread
+                uint4 v[kParts];
+#pragma unroll
+                for (int x = 0; x < kParts; ++x) v[x] = *reinterpret_cast<const uint4*>(src + (x * kAll + tid) * 16);
+#pragma unroll
+                for (int x = 0; x < kParts; ++x) {
+                    const int part = x * kAll + tid;
+                    const int r = part / (D / 16), j = part % (D / 16);
+                    uint4 lo, hi;
+                    e4m3x4_to_half2(v[x].x, lo.x, lo.y);
+                    e4m3x4_to_half2(v[x].y, lo.z, lo.w);
+                    e4m3x4_to_half2(v[x].z, hi.x, hi.y);
+                    e4m3x4_to_half2(v[x].w, hi.z, hi.w);
+                    // the two 16-byte chunks in an order that spreads a row's writes over all banks
+                    uint8_t* const d = dst + (j >> 2) * kHalf + r * 128;
+                    const int c0 = 2 * (j & 3), swap = (j >> 2) & 1;
+                    *reinterpret_cast<uint4*>(d + (((c0 + swap) ^ (r & 7)) << 4)) = swap ? hi : lo;
+                    *reinterpret_cast<uint4*>(d + (((c0 + 1 - swap) ^ (r & 7)) << 4)) = swap ? lo : hi;
+                }
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(full(stage));
+                    mbar_arrive(raw_empty(rs));
+                }
+                if (++rs == NRAW) {
+                    rs = 0;
+                    rph ^= 1u;
+                }
+                if (++stage == NST) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+    }
+
+    __syncwarp();
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == W0) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace tpmlp

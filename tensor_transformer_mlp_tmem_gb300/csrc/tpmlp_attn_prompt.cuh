@@ -66,10 +66,6 @@ struct PromptArgs {
     int32_t window;
     float* partial;   // [CTAs][2 pieces][2 tiles] slots
     uint32_t* count;  // [CTAs][2 tiles] arrivals, then items dealt and CTAs done; 0 between launches
-    // OPEN: where results go instead of out, in fp32 (null: they go to out), or what they are joined
-    // with on the way to out (null: nothing); both as RowArgs' other and other_lse
-    float *part, *part_lse;
-    const float *other, *other_lse;
 };
 
 template <int D, bool FP8>
@@ -190,9 +186,8 @@ __host__ __device__ constexpr uint32_t prompt_idesc(int N, bool half, bool b_mn)
 // A sequence's new tokens: rows [first, first + n) of Q, at positions len - n ...
 struct PromptSeq {
     int first, n, len;
-    template <bool OPEN>
     __device__ __forceinline__ int hi(int token) const {  // keys that the token may see end here
-        return OPEN ? len : max(0, min(len, len - n + token + 1));
+        return max(0, min(len, len - n + token + 1));
     }
 };
 __device__ __forceinline__ PromptSeq prompt_seq(const PromptArgs& a, int b) {
@@ -229,20 +224,19 @@ __device__ __forceinline__ int prompt_lo_key(const PromptArgs& a, int hi) {
 }
 
 // The steps and blocks of tokens [tok0, tok0 + 2 tpt) of a sequence.
-template <bool OPEN>
 __device__ __forceinline__ void item_blocks(const PromptArgs& a, Piece& p) {
     p.b0 = 0x7FFFFFFF;
     p.b1 = 0;
-    p.lo_key = prompt_lo_key(a, p.seq.hi<OPEN>(p.tok0));
+    p.lo_key = prompt_lo_key(a, p.seq.hi(p.tok0));
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         const int k0 = p.tok0 + t * a.tpt;
         p.tokens[t] = max(0, min(p.seq.n - k0, a.tpt));
         p.lo[t] = p.hi[t] = p.last_hi[t] = 0;
         if (p.tokens[t] > 0) {
-            p.last_hi[t] = p.seq.hi<OPEN>(k0 + p.tokens[t] - 1);
+            p.last_hi[t] = p.seq.hi(k0 + p.tokens[t] - 1);
             p.hi[t] = (p.last_hi[t] + kSB - 1) / kSB;
-            p.lo[t] = min(p.hi[t], prompt_lo_key(a, p.seq.hi<OPEN>(k0)) / kSB);
+            p.lo[t] = min(p.hi[t], prompt_lo_key(a, p.seq.hi(k0)) / kSB);
         }
         if (p.hi[t] > p.lo[t]) {
             p.b0 = min(p.b0, p.lo[t] / 2);
@@ -258,7 +252,6 @@ __device__ __forceinline__ void item_blocks(const PromptArgs& a, Piece& p) {
 // tokens (most keys) to the first. A group has two items or more for each CTA: with one, a last
 // group's largest items were started when little else was left (GPT-3-shaped prompt: 326 us, so 302,
 // both in one session; 305-324 over all).
-template <bool OPEN>
 struct PromptWork {
     const int64_t* coarse;  // items before each run of `run` sequences
     const int* units;       // work before each item (split lists)
@@ -298,7 +291,7 @@ struct PromptWork {
         p.seq = s;
         p.h = min(h0 + j % heads, a.kv.Hkv - 1);
         p.tok0 = (nt - 1 - j / heads) * 2 * a.tpt;
-        item_blocks<OPEN>(a, p);
+        item_blocks(a, p);
     }
     __device__ __forceinline__ Piece next(const PromptArgs& a) {
         Piece p;
@@ -354,7 +347,7 @@ struct PromptWork {
 struct SeenByAll {
     int lo, hi;
     __device__ __forceinline__ SeenByAll(const PromptArgs& a, const Piece& p)
-        : lo(prompt_lo_key(a, max(p.last_hi[0], p.last_hi[1]))), hi(p.seq.hi<false>(p.tok0)) {}
+        : lo(prompt_lo_key(a, max(p.last_hi[0], p.last_hi[1]))), hi(p.seq.hi(p.tok0)) {}
     __device__ __forceinline__ bool operator()(int key) const { return key >= lo && key < hi; }
 };
 template <bool FP8>
@@ -441,69 +434,11 @@ __device__ __noinline__ void add_cleared(const PromptArgs& a, const Piece& p, in
     tmem_wait_st();
 }
 
-// OPEN: where a row's result goes. Its sums are scaled by `scale`, which this sets anew where the row
-// is joined with its result over other keys; add() then adds that result, and store() writes to
-// a.part where there is one.
-template <int D, bool FP8, bool OPEN>
-struct OpenRow {
-    float* part = nullptr;
-    const float* other = nullptr;
-    int64_t at = 0;
-    float by = 0.0f, lse = 0.0f;
-    // row: token * Hq + head; m, l: maximum and sum; on: there is such a row
-    __device__ __forceinline__ OpenRow(const PromptArgs& a, bool on, int64_t row, float m, float l, float v_scale,
-                                       float& scale) {
-        if constexpr (OPEN) {
-            if (!on) return;
-            at = row;
-            constexpr float kRaise = FP8 ? kRaiseLog2 : 0.0f;
-            if (a.part) {
-                part = a.part + row * D;
-                lse = l == 0.0f ? -CUDART_INF_F : m + log2f(l) - kRaise;
-            } else if (a.other) {
-                const float lo = __ldcg(a.other_lse + row);
-                const Joined j = join_keys(m, l, kRaise, lo);
-                scale = j.own * v_scale;
-                by = j.other;
-                lse = j.lse;
-                if (lo != -CUDART_INF_F) other = a.other + row * D;
-            } else {
-                lse = l == 0.0f ? -CUDART_INF_F : (m + log2f(l) - kRaise) * 0.69314718055994531f;
-            }
-        }
-    }
-    template <int N>
-    __device__ __forceinline__ void add(float (&v)[N], int col) const {
-        if constexpr (OPEN) {
-            if (!other) return;
-#pragma unroll
-            for (int k = 0; k < N; k += 4) {
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(other + col + k));
-                v[k] += x.x * by;
-                v[k + 1] += x.y * by;
-                v[k + 2] += x.z * by;
-                v[k + 3] += x.w * by;
-            }
-        }
-    }
-    template <int N>
-    __device__ __forceinline__ void store(const float (&v)[N], int col) const {
-        if (!part) return;
-#pragma unroll
-        for (int k = 0; k < N; k += 4)
-            *reinterpret_cast<float4*>(part + col + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-    }
-    __device__ __forceinline__ void store_lse(const PromptArgs& a) const {
-        if (part) a.part_lse[at] = lse;
-        else if (a.lse) a.lse[at] = lse;
-    }
-};
-
 // The result of the first `count` rows of tile t of a split item, from its contributors' slots, first
 // to last. The tile's 128 threads call it (row: the thread's number), P to a row of the result, each
 // with an equal part of the columns: 16 loads of 16 bytes in flight, however few the rows. One token of
 // 16 heads over 131072 keys, 51 contributors: 56 us (with one thread to a row: 113).
-template <int D, bool FP8, bool OPEN, int P>
+template <int D, bool FP8, int P>
 __device__ __forceinline__ void join_rows(const PromptArgs& a, const Piece& p, int t, int row, int count,
                                           const float* slots, float v_scale) {
     constexpr int kRows = 128 / P, kCols = D / P;       // a thread's columns
@@ -533,10 +468,9 @@ __device__ __forceinline__ void join_rows(const PromptArgs& a, const Piece& p, i
         for (int u = 0; u < kJoinLoads; ++u) ll += exp2_approx(mx[u] - safe) * lx[u];
     }
     const float safe = mm == -CUDART_INF_F ? 0.0f : mm;
-    float scale = ll == 0.0f ? 0.0f : v_scale / ll;
+    const float scale = ll == 0.0f ? 0.0f : v_scale / ll;
     const int64_t to = p.seq.first + p.tok0 + t * a.tpt + r / a.G;
     const int64_t to_head = static_cast<int64_t>(p.h) * a.G + r % a.G;
-    const OpenRow<D, FP8, OPEN> open(a, true, to * a.Hq + to_head, mm, ll, v_scale, scale);
     __nv_bfloat16* const dst = a.out + to * a.ldo + to_head * D;
 #pragma unroll 1
     for (int col = part * kCols; col < (part + 1) * kCols; col += kChunk) {
@@ -574,23 +508,15 @@ __device__ __forceinline__ void join_rows(const PromptArgs& a, const Piece& p, i
             float z[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) z[e] = ll == 0.0f ? 0.0f : v[k + e] * scale;
-            open.add(z, col + k);
-            if (OPEN && a.part) open.store(z, col + k);
-            else *reinterpret_cast<uint4*>(dst + col + k) = pack8_bf16(z);
+            *reinterpret_cast<uint4*>(dst + col + k) = pack8_bf16(z);
         }
     }
-    if (part == 0) {
-        if constexpr (OPEN) open.store_lse(a);
-        else if (a.lse)
-            a.lse[to * a.Hq + to_head] =
-                ll == 0.0f ? -CUDART_INF_F : (mm + log2f(ll) - (FP8 ? kRaiseLog2 : 0.0f)) * 0.69314718055994531f;
-    }
+    if (a.lse && part == 0)
+        a.lse[to * a.Hq + to_head] =
+            ll == 0.0f ? -CUDART_INF_F : (mm + log2f(ll) - (FP8 ? kRaiseLog2 : 0.0f)) * 0.69314718055994531f;
 }
 
-// OPEN: every token sees all keys of its sequence (attention to another sequence's states, or to a
-// prefix that the rows share). All rows of a tile then see the same keys, so values that are not finite
-// need no second computation.
-template <int D, bool FP8, bool OPEN>
+template <int D, bool FP8>
 __global__ void __launch_bounds__(PromptSmem<D, FP8>::kThreads, 1)
 attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PromptArgs a) {
@@ -679,20 +605,8 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
 
-    if constexpr (OPEN) {
-        // rows of no sequence have no keys; whoever joins their results has to know
-        if (a.part) {
-            const int first = max(0, min(a.cu_q[0], a.T)), last = max(0, min(a.cu_q[a.kv.B], a.T));
-            const int64_t n = (first + static_cast<int64_t>(a.T) - last) * a.Hq;
-            for (int64_t i = static_cast<int64_t>(blockIdx.x) * L::kThreads + threadIdx.x; i < n;
-                 i += static_cast<int64_t>(gridDim.x) * L::kThreads)
-                a.part_lse[i < static_cast<int64_t>(first) * a.Hq ? i : i + static_cast<int64_t>(last - first) * a.Hq] =
-                    -CUDART_INF_F;
-        }
-    }
-
     // ---------------------------------------------------------------- the work list
-    PromptWork<OPEN> work;
+    PromptWork work;
     work.coarse = coarse;
     work.units = units;
     work.run = (a.kv.B + kCoarse - 1) / kCoarse;
@@ -700,7 +614,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     for (int e = threadIdx.x; e < work.runs; e += L::kThreads) {
         int64_t n = 0;
         for (int b = e * work.run; b < min(a.kv.B, (e + 1) * work.run); ++b)
-            n += static_cast<int64_t>(PromptWork<OPEN>::tiles(a, prompt_seq(a, b))) * a.kv.Hkv;
+            n += static_cast<int64_t>(PromptWork::tiles(a, prompt_seq(a, b))) * a.kv.Hkv;
         coarse[e] = n;
     }
     __syncthreads();
@@ -874,9 +788,9 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             float m = -CUDART_INF_F, l = 0.0f;  // reference maximum (log2 units), sum
             const int begin = p->begin(t), end = p->end(t);
             // keys that this row sees: [lo, hi); that every row of the tile sees: [last_lo, first_hi)
-            const int hi = p->seq.hi<OPEN>(mine ? tok : p->seq.n - 1);
+            const int hi = p->seq.hi(mine ? tok : p->seq.n - 1);
             const int lo = prompt_lo_key(a, hi);
-            const int first_hi = p->seq.hi<OPEN>(p->tok0 + t * a.tpt);
+            const int first_hi = p->seq.hi(p->tok0 + t * a.tpt);
             const int last_lo = prompt_lo_key(a, p->last_hi[t]);
             const uint32_t block0 = blocks - p->b0;
             blocks += p->b1 - p->b0;
@@ -997,26 +911,24 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 }
             };
             auto put_lse = [&](float mm, float ll) {
-                if constexpr (!OPEN) if (a.lse && mine)
+                if (a.lse && mine)
                     a.lse[qrow * a.Hq + qhead] =
                         ll == 0.0f ? -CUDART_INF_F
                                    : (mm + log2f(ll) - (FP8 ? kRaiseLog2 : 0.0f)) * 0.69314718055994531f;
             };
-            float inv = l == 0.0f ? 0.0f : v_scale / l;  // no keys: zeros
-            const OpenRow<D, FP8, OPEN> open(a, mine && whole, qrow * a.Hq + qhead, m, l, v_scale, inv);
+            const float inv = l == 0.0f ? 0.0f : v_scale / l;  // no keys: zeros
             const bool any = end > begin;
             // The tile has to be done again if a row's sums are not finite though its weights' is
             // (one token to an item: all rows see the same keys).
-            const int careful = OPEN ? 0 : p->careful;
-            const bool suspect = !OPEN && any && mine && a.cu_q && !careful && l - l == 0.0f;
+            const int careful = p->careful;
+            const bool suspect = any && mine && a.cu_q && !careful && l - l == 0.0f;
             // (the other tile's result may stand already)
             const bool give = p->tokens[t] > 0 && (!careful || ((careful >> t) & 1));
             if (any) {
                 if (!wait(o_full(t), o_phase, 3)) break;
                 o_phase ^= 1u;
                 ptx::tc_fence_after();
-                if constexpr (!OPEN)
-                    if (careful) add_cleared<D, FP8>(a, *p, lo, mine ? hi : 0, tmem_o(t) + lanes);
+                if (careful) add_cleared<D, FP8>(a, *p, lo, mine ? hi : 0, tmem_o(t) + lanes);
             }
             float2 not_finite[4] = {};  // NaN once a sum is not finite
             auto check = [&] {
@@ -1059,15 +971,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                             float v[32];
 #pragma unroll
                             for (int k = 0; k < 32; ++k) v[k] = l == 0.0f ? 0.0f : __uint_as_float(o[x][k]);
-                            if constexpr (OPEN) {
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) v[k] *= inv;
-                                open.add(v, col + 32 * x);
-                                if (a.part) open.store(v, col + 32 * x);
-                                else put(col + 32 * x, v, 1.0f);
-                            } else {
-                                put(col + 32 * x, v, inv);
-                            }
+                            put(col + 32 * x, v, inv);
                         } else if (mine) {
 #pragma unroll
                             for (int k = 0; k < 32; k += 4)
@@ -1079,9 +983,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 }
             }
             if (whole) {
-                if constexpr (OPEN) {
-                    if (mine) open.store_lse(a);
-                } else if (give) put_lse(m, l);
+                if (give) put_lse(m, l);
             } else if (give) {
                 // The last contributor to arrive sums all of them, first to last (see the row
                 // kernel); each tile's 128 threads count and join on their own.
@@ -1112,10 +1014,10 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 if (*reinterpret_cast<volatile uint32_t*>(s_last + t)) {
                     __threadfence();
                     const int count = p->tokens[t] * a.G;
-                    if (count > 64) join_rows<D, FP8, OPEN, 1>(a, *p, t, row, count, slots, v_scale);
-                    else if (count > 32) join_rows<D, FP8, OPEN, 2>(a, *p, t, row, count, slots, v_scale);
-                    else if (count > 16) join_rows<D, FP8, OPEN, 4>(a, *p, t, row, count, slots, v_scale);
-                    else join_rows<D, FP8, OPEN, 8>(a, *p, t, row, count, slots, v_scale);
+                    if (count > 64) join_rows<D, FP8, 1>(a, *p, t, row, count, slots, v_scale);
+                    else if (count > 32) join_rows<D, FP8, 2>(a, *p, t, row, count, slots, v_scale);
+                    else if (count > 16) join_rows<D, FP8, 4>(a, *p, t, row, count, slots, v_scale);
+                    else join_rows<D, FP8, 8>(a, *p, t, row, count, slots, v_scale);
                 }
             }
             release_piece();
