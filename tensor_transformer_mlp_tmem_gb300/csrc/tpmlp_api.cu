@@ -1639,6 +1639,7 @@ void tpmlp_destroy(tpmlp_ctx* c) {
     cudaFree(c->attn_partial);
     cudaFree(c->attn_count);
     cudaFree(c->norm_w);
+    cudaFree(c->tail_partial);
     for (float* p : c->shared) cudaFree(p);
     cudaFree(c->status);
     if (cur >= 0 && cur != c->device) cudaSetDevice(cur);

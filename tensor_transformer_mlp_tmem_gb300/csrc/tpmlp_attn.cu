@@ -106,6 +106,7 @@ int tpmlp_attn_create(tpmlp_ctx** out, int32_t Hq, int32_t Hkv, int32_t D, int32
                                     static_cast<size_t>(c->num_sms) * 4 * kPromptSlotFloats);
     const size_t counters = ctas + 2;  // a counter per CTA (prompt: per tile), the deal's two
     c->attn_counters = counters;
+    c->attn_partial_floats = partial;
     const size_t scales = static_cast<size_t>(Hkv) * 2;
     cudaError_t e;
     float* ones = new (std::nothrow) float[scales];

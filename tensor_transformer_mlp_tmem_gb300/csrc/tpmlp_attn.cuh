@@ -321,6 +321,102 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) append_kernel(c
     }
 }
 
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// ------------------------------------------------------------------ results over other keys
+// fp32 values of a tile's partial sums in a slot: O in groups of 4 columns [D/4][128][4], m [128], l [128].
+constexpr int kPromptSlotFloats = 128 * 128 + 256;
+constexpr float kRaiseLog2 = 6.0f;  // e4m3 caches: a tile's fp16 weights are raised by 2^6 (see the rows)
+constexpr int kJoinLoads = 8;  // contributors of a split range whose sums a thread loads at once
+
+// Where a row's result over the keys of another cache lies (tpmlp_attn_open.cuh writes it).
+struct __align__(16) RowOf {
+    float log;        // whole: log2 of the sum of its weights; -infinity: no keys, and no result is looked at
+    int first, last;  // split: the contributing CTAs
+    int place;        // split: tile * 128 + row in their slots; whole: -1
+};
+__device__ __forceinline__ RowOf row_of(const RowOf* p) {
+    const uint4 v = load16(reinterpret_cast<const uint8_t*>(p));
+    return {__uint_as_float(v.x), static_cast<int>(v.y), static_cast<int>(v.z), static_cast<int>(v.w)};
+}
+
+// That result: of a whole row in fp32 at `whole`, of a split one from its contributors, first to last.
+template <bool FP8>
+struct OtherRow {
+    const float* whole;
+    const float* slot;  // first contributor's column 0; the others' are 4 slots apart (and 2 back)
+    RowOf of;
+    float top, scale, log;  // log: log2 of the sum of weights
+    __device__ __forceinline__ const float* at(int cta) const {
+        return slot + (static_cast<int64_t>(cta - of.first) * 4 - (cta != of.first ? 2 : 0)) * kPromptSlotFloats;
+    }
+    __device__ __forceinline__ OtherRow(const RowOf& from, const float* slots, const float* row, float v_scale)
+        : whole(row), of(from) {
+        log = of.log;
+        if (of.place < 0) return;
+        const int r = of.place & 127;
+        slot = slots + (static_cast<int64_t>(of.first) * 4 + 2 + (of.place >> 7)) * kPromptSlotFloats + r * 4;
+        float m = -CUDART_INF_F, l = 0.0f;
+        for (int c0 = of.first; c0 <= of.last; c0 += kJoinLoads) {
+            float mx[kJoinLoads], lx[kJoinLoads], t = m;
+#pragma unroll
+            for (int u = 0; u < kJoinLoads; ++u) {
+                const float* p = at(min(c0 + u, of.last)) + 128 * 128 - r * 3;
+                mx[u] = __ldcg(p);
+                lx[u] = c0 + u <= of.last ? __ldcg(p + 128) : 0.0f;
+            }
+#pragma unroll
+            for (int u = 0; u < kJoinLoads; ++u) t = fmaxf(t, mx[u]);
+            const float safe = t == -CUDART_INF_F ? 0.0f : t;
+            l *= exp2_approx(m - safe);
+            m = t;
+#pragma unroll
+            for (int u = 0; u < kJoinLoads; ++u) l += exp2_approx(mx[u] - safe) * lx[u];
+        }
+        top = m == -CUDART_INF_F ? 0.0f : m;
+        scale = l == 0.0f ? 0.0f : v_scale / l;
+        log = l == 0.0f ? -CUDART_INF_F : m + log2f(l) - (FP8 ? kRaiseLog2 : 0.0f);
+    }
+    // y times columns d .. d + 3 of it, added to v
+    __device__ __forceinline__ void add(float4& v, int d, float y) const {
+        if (log == -CUDART_INF_F) return;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (of.place < 0) {
+            o = __ldcg(reinterpret_cast<const float4*>(whole + d));
+        } else {
+            for (int c0 = of.first; c0 <= of.last; c0 += kJoinLoads) {
+                float mx[kJoinLoads];
+                float4 x[kJoinLoads];
+#pragma unroll
+                for (int u = 0; u < kJoinLoads; ++u) {
+                    const float* p = at(min(c0 + u, of.last));
+                    mx[u] = __ldcg(p + 128 * 128 - (of.place & 127) * 3);
+                    x[u] = __ldcg(reinterpret_cast<const float4*>(p + d * 128));
+                }
+#pragma unroll
+                for (int u = 0; u < kJoinLoads; ++u) {
+                    // past the last one, sums of 0 as well (see the row kernel)
+                    const bool on = c0 + u <= of.last;
+                    const float f = on ? exp2_approx(mx[u] - top) : 0.0f;
+                    o.x += f * (on ? x[u].x : 0.0f);
+                    o.y += f * (on ? x[u].y : 0.0f);
+                    o.z += f * (on ? x[u].z : 0.0f);
+                    o.w += f * (on ? x[u].w : 0.0f);
+                }
+            }
+            y *= scale;
+        }
+        v.x += y * o.x;
+        v.y += y * o.y;
+        v.z += y * o.z;
+        v.w += y * o.w;
+    }
+};
+
 // ------------------------------------------------------------------ rows
 // Attention of one token of each sequence: row b has G query heads to each kv head, and attends to
 // keys [lo, hi) of sequence b.
@@ -337,9 +433,11 @@ struct RowArgs {
     int32_t window;
     float* partial;         // [CTAs][2] slots of RowSlot floats
     uint32_t* count;        // [CTAs] arrivals, 0 between launches
-    // JOIN: each row's result over keys of another cache, fp32 [rows][Hq][D], and the log2 of its sum
-    // of weights [rows][Hq] (-infinity: no keys, and the result is not looked at)
-    const float *other, *other_lse;
+    // JOIN: each row's result over keys of another cache: fp32 [rows][Hq][D], where it lies [rows][Hq],
+    // and the slots of partial sums of those that were split
+    const float* other;
+    const RowOf* other_of;
+    const float* other_slots;
 };
 
 // How a row's sums over its own keys (maximum m in log2 units, sum l of weights that were raised by
@@ -373,7 +471,6 @@ constexpr int kRowWarps = 8;
 // heads to a kv head 118, 104, 100, 101; one sequence of 131072 keys 88, 87, 85, 88.
 constexpr int kSegmentStart = 2;
 constexpr int kRowThreads = 32 * kRowWarps;
-constexpr int kJoinLoads = 8;  // contributors of a split range whose sums a thread loads at once
 // e4m3 caches: fp16 weights are raised by 2^10, so that the small ones of a long cache stay clear of
 // fp16's smallest steps; it cancels against the sum.
 constexpr float kRowRaise = 10.0f;
@@ -421,12 +518,6 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 __device__ __forceinline__ uint32_t pack_bf162(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-__device__ __forceinline__ float exp2_approx(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 // e4m3 caches: the power of two by which a query row is divided before it is rounded to fp16, from
@@ -870,16 +961,16 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
             const int64_t head = static_cast<int64_t>(h) * a.G + q0 + r;
             if constexpr (JOIN) {
                 const int64_t at_row = static_cast<int64_t>(row) * a.Hq + head;
-                const float lo = __ldcg(a.other_lse + at_row);
-                const Joined j = join_keys(mm, ll, FP8 ? kRowRaise : 0.0f, lo);
-                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (lo != -CUDART_INF_F) x = __ldcg(reinterpret_cast<const float4*>(a.other + at_row * D + d));
-                const float own = j.own * v_scale;
+                const OtherRow<FP8> other(row_of(a.other_of + at_row), a.other_slots, a.other + at_row * D, v_scale);
+                const Joined x = join_keys(mm, ll, FP8 ? kRowRaise : 0.0f, other.log);
+                const float own = x.own * v_scale;
+                v = make_float4(v.x * own, v.y * own, v.z * own, v.w * own);
+                other.add(v, d, x.other);
                 uint2 w;
-                w.x = pack_bf162(v.x * own + x.x * j.other, v.y * own + x.y * j.other);
-                w.y = pack_bf162(v.z * own + x.z * j.other, v.w * own + x.w * j.other);
+                w.x = pack_bf162(v.x, v.y);
+                w.y = pack_bf162(v.z, v.w);
                 *reinterpret_cast<uint2*>(a.out + row * a.ldo + head * D + d) = w;
-                if (a.lse && d == 0) a.lse[at_row] = j.lse;
+                if (a.lse && d == 0) a.lse[at_row] = x.lse;
                 return;
             }
             const float inv = ll == 0.0f ? 0.0f : v_scale / ll;  // no keys: zeros

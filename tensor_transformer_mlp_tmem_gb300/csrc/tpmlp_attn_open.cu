@@ -20,9 +20,9 @@ int launch_open(tpmlp_ctx* c, const CUtensorMap& q, const CUtensorMap& k, const 
     return launch(c, kern, c->num_sms, S::kThreads, S::kTotal, s, q, k, v, a);
 }
 
-// part, part_lse: see OpenArgs.
+// part, part_of: see OpenArgs.
 int run_open(tpmlp_ctx* c, const RowArgs& r, const int32_t* cu_q, int64_t T, cudaStream_t s,
-                    float* part = nullptr, float* part_lse = nullptr) {
+                    float* part = nullptr, RowOf* part_of = nullptr) {
     OpenArgs a{};
     a.kv = r.kv;
     a.q = r.q;
@@ -36,12 +36,13 @@ int run_open(tpmlp_ctx* c, const RowArgs& r, const int32_t* cu_q, int64_t T, cud
     a.G = r.G;
     a.tpt = kPB / r.G;
     a.scale_log2 = r.scale_log2;
-    a.partial = c->attn_partial;
+    a.partial = r.partial;
     a.count = c->attn_count;
     a.part = part;
-    a.part_lse = part_lse;
+    a.part_of = part_of;
     a.other = r.other;
-    a.other_lse = r.other_lse;
+    a.other_of = r.other_of;
+    a.other_slots = r.other_slots;
     CUtensorMap q{}, k{}, v{};
     if (int rc = prompt_maps(c, r, T, a.tpt, &q, &k, &v)) return rc;
     if (c->head_dim == 128)
@@ -49,15 +50,23 @@ int run_open(tpmlp_ctx* c, const RowArgs& r, const int32_t* cu_q, int64_t T, cud
     return is_e4m3(c) ? launch_open<64, true>(c, q, k, v, a, s) : launch_open<64, false>(c, q, k, v, a, s);
 }
 
-// The workspace of decode_shared holds `rows` sequences.
-int reserve_shared(tpmlp_ctx* c, int64_t rows, cudaStream_t s, bool own_call) {
+// The workspace of decode_shared: results over prefixes, fp32 [rows][Hq][D], and where each lies [rows][Hq].
+// The own keys' split ranges have partial sums of their own, since the prefixes' are read with them.
+size_t shared_bytes(const tpmlp_ctx* c, int64_t rows) {
+    return static_cast<size_t>(rows) * c->heads_q * (c->head_dim * sizeof(float) + sizeof(RowOf));
+}
+
+// It holds `rows` sequences (s: the stream that a call is on; null: tpmlp_attn_reserve).
+int reserve_shared(tpmlp_ctx* c, int64_t rows, const cudaStream_t* s) {
     if (rows <= c->shared_rows) return TPMLP_OK;
-    if (!own_call)
-        if (int rc = refuse_allocation(c, s, "tpmlp_attn_reserve before the capture")) return rc;
+    if (s)
+        if (int rc = refuse_allocation(c, *s, "tpmlp_attn_reserve before the capture")) return rc;
+    if (!c->tail_partial)
+        if (int rc = allocate(c, reinterpret_cast<void**>(&c->tail_partial), c->attn_partial_floats * sizeof(float)))
+            return rc;
     const int64_t now = std::max(rows, 2 * c->shared_rows);
     void* p = nullptr;
-    const size_t bytes = static_cast<size_t>(now) * c->heads_q * (c->head_dim + 1) * sizeof(float);
-    if (int rc = allocate(c, &p, bytes)) return rc;
+    if (int rc = allocate(c, &p, shared_bytes(c, now))) return rc;
     c->shared[c->shared_n++] = static_cast<float*>(p);
     c->shared_rows = now;
     return TPMLP_OK;
@@ -84,7 +93,7 @@ int tpmlp_attn_reserve(tpmlp_ctx* c, int64_t max_sequences) {
     if (int rc = check_attention(c)) return rc;
     if (max_sequences < 0) return TPMLP_ERR_INVALID_ARG;
     if (max_sequences > INT_MAX / 2) return TPMLP_ERR_UNSUPPORTED_SHAPE;
-    return reserve_shared(c, max_sequences, nullptr, true);
+    return reserve_shared(c, max_sequences, nullptr);
 }
 
 int tpmlp_attn_decode_shared(tpmlp_ctx* c, const void* Q, int64_t ldq, const tpmlp_kv* prefix,
@@ -100,15 +109,17 @@ int tpmlp_attn_decode_shared(tpmlp_ctx* c, const void* Q, int64_t ldq, const tpm
     if (!cu) return TPMLP_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(cu) & 3) return TPMLP_ERR_MISALIGNED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (int rc = reserve_shared(c, kv->B, s, false)) return rc;
+    if (int rc = reserve_shared(c, kv->B, &s)) return rc;
     float* const part = c->shared[c->shared_n - 1];
-    float* const part_lse = part + c->shared_rows * c->heads_q * c->head_dim;
+    RowOf* const part_of = reinterpret_cast<RowOf*>(part + c->shared_rows * c->heads_q * c->head_dim);
     const RowArgs p = row_args(c, Q, ldq, prefix, scale, 0, Out, ldo, nullptr);
-    if (int rc = run_open(c, p, cu, kv->B, s, part, part_lse)) return rc;
+    if (int rc = run_open(c, p, cu, kv->B, s, part, part_of)) return rc;
     RowArgs a = row_args(c, Q, ldq, kv, scale, 0, Out, ldo, Lse);
     a.rows = kv->B;
+    a.partial = c->tail_partial;
     a.other = part;
-    a.other_lse = part_lse;
+    a.other_of = part_of;
+    a.other_slots = c->attn_partial;
     if (a.G > row_heads(c->head_dim, is_e4m3(c))) return run_open(c, a, nullptr, kv->B, s);
     return run_rows<true>(c, a, s);
 }

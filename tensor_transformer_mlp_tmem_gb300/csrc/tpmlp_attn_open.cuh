@@ -27,7 +27,11 @@
 namespace tpmlp {
 
 constexpr int kOpenCode = 0x4000;  // wait sites: kOpenCode | role
+// A step's weights, with e4m3 caches raised by 2^kRaiseLog2, may sum to this much before a row's reference
+// follows its maximum: bf16 weights lose nothing up there, fp16 ones must stay below 65504.
+constexpr float kOpenMost = 0x1p14f;
 constexpr int kOpenRuns = 512;     // entries of the table of sequences
+constexpr int kOpenPieces = 4;     // pieces between the work list's warp and the others
 
 struct OpenArgs {
     KvView kv;
@@ -42,27 +46,25 @@ struct OpenArgs {
     float* partial;   // [CTAs][2 pieces][2 tiles] slots of kPromptSlotFloats
     uint32_t* count;  // [CTAs][2 tiles] arrivals, then items dealt and CTAs done; 0 between launches
     // where results go instead of out, in fp32 (null: they go to out), or what they are joined with on
-    // the way to out (null: nothing); both as RowArgs' other and other_lse
-    float *part, *part_lse;
-    const float *other, *other_lse;
+    // the way to out (null: nothing)
+    float* part;     // fp32 [T][Hq][D] (split rows: their contributors' slots in `partial`)
+    RowOf* part_of;  // [T][Hq]
+    const float* other;  // these as in RowArgs
+    const RowOf* other_of;
+    const float* other_slots;
 };
 
 template <int D, bool FP8>
 struct OpenShape {
-    static constexpr int U = D == 64 ? 2 : 1;  // streams to a tile
-    static constexpr int kGroups = 2 * U;      // of four softmax warps
     static constexpr int kConvert = FP8 ? (D == 64 ? 4 : 8) : 0;  // warps that convert
-    static constexpr int kWarp0 = 4 * kGroups;                    // first of the other roles
-    static constexpr int kThreads = 32 * (kWarp0 + 4 + kConvert);
+    static constexpr int kThreads = 32 * (12 + kConvert);
     // Registers of a softmax thread and of the others: together at most what the block is launched with
-    // (65536 over its threads, a multiple of 8 each: 168, 96, 96, 80).
+    // (65536 over its threads, a multiple of 8 each: 168, 128, 96).
     static constexpr int kLaunch = 65536 / kThreads / 8 * 8;
-    static constexpr int kSoftmaxRegs = D == 128 ? (FP8 ? 144 : 184) : (FP8 ? 88 : 104);
-    static constexpr int kOtherRegs = D == 128 ? (FP8 ? 64 : 136) : 64;
-    static_assert(32 * kWarp0 * kSoftmaxRegs + (kThreads - 32 * kWarp0) * kOtherRegs <= kThreads * kLaunch,
+    static constexpr int kSoftmaxRegs = FP8 ? (D == 64 ? 168 : 144) : 184;
+    static constexpr int kOtherRegs = FP8 ? (D == 64 ? 88 : 64) : 136;
+    static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunch,
                   "the register split draws on what the block was launched with");
-
-    static constexpr bool kReload = U == 2 && FP8;  // scores are loaded twice instead of being held
 
     static constexpr uint32_t kTile = kPB * D * 2;  // a Q, K or V tile of 16-bit values
     static constexpr uint32_t kRaw = FP8 ? kPB * D : 0;
@@ -74,22 +76,13 @@ struct OpenShape {
     static constexpr int kNumBars = 2 * kStages + 2 * kRaws + 48;
     static constexpr uint32_t kCtl = kBars + 8 * kNumBars;  // TMEM address, abort, s_last [2], groups [8]
     static constexpr uint32_t kPieces0 = kCtl + 64;
-    static constexpr uint32_t kMeet = kPieces0 + 4 * 64;    // [2][2 tiles][U][128] (m, l), U = 2
-    static constexpr uint32_t kUp = kMeet + (U == 2 ? 2 * 2 * U * 128 * 8 : 0);  // [2 tiles][128] fp32, e4m3
-    static constexpr uint32_t kTables = kUp + (FP8 ? 2 * 128 * 4 : 0);
+    static constexpr uint32_t kUp = kPieces0 + kOpenPieces * 64;  // [2 tiles][128] fp32, e4m3
+    static constexpr uint32_t kStore0 = (kUp + (FP8 ? 2 * 128 * 4 : 0) + 127) / 128 * 128;
+    static constexpr uint32_t kTables = kStore0 + 8 * 2048;  // 2 KB of output staging per softmax warp
     static constexpr uint32_t kTotal = 1024 + kTables + 2 * (kOpenRuns + 1) * 8 + 64;
     static_assert(kTotal <= 232448, "dynamic shared memory per CTA");
     static_assert(kStages / 2 + 1 < 8, "blocks in flight, against the ring of loaded groups");
 };
-
-__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
 
 // A sequence's rows: [first, first + n) of Q, all of which see its first `len` keys.
 struct OpenSeq {
@@ -119,7 +112,6 @@ struct OpenPiece {
     }
 };
 static_assert(sizeof(OpenPiece) <= 64, "piece slots");
-constexpr int kOpenPieces = 4;  // between the work list's warp and the others
 
 // The CTA's work list. A sequence's items are numbered by kv head and then by tile, so that those that
 // share keys are at work together. An item's work is a unit for its start and its blocks.
@@ -128,6 +120,7 @@ struct OpenWork {
     int runs, run;
     int64_t items;
     bool split;            // equal runs of work instead of whole items
+    bool dealt;            // whole items: this CTA has had its first
     int64_t at, end, per;  // split: this CTA's run of work, the length of every run
 
     __device__ __forceinline__ static int64_t tiles(const OpenArgs& a, const OpenSeq& s) {
@@ -184,11 +177,15 @@ struct OpenWork {
         p.valid = 0;
         OpenSeq s;
         if (!split) {
-            // items are dealt to whichever CTA asks next (who computes an item does not change its
-            // result); one lane asks
-            uint32_t k = 0;
-            if ((threadIdx.x & 31) == 0) k = atomicAdd(a.count + 2 * gridDim.x, 1u);
-            int64_t r = __shfl_sync(~0u, k, 0);
+            // the first item goes by the CTA's number, the others are dealt to whichever CTA asks next
+            // (who computes an item does not change its result); one lane asks
+            uint32_t k = blockIdx.x;
+            if (dealt) {
+                if ((threadIdx.x & 31) == 0) k = gridDim.x + atomicAdd(a.count + 2 * gridDim.x, 1u);
+                k = __shfl_sync(~0u, k, 0);
+            }
+            dealt = true;
+            int64_t r = k;
             if (r >= items) return p;
             const int b = locate<false>(a, r, s);
             item(a, b, s, r, p);
@@ -231,81 +228,66 @@ __device__ __noinline__ void clear_rows(uint8_t* block, int in, uint32_t have, i
 }
 
 // Where a row's result goes. Its sums are scaled by `scale`, which this sets anew where the row is joined
-// with its result over other keys; add() then adds that result, and put() rounds and writes.
+// with its result over other keys; add() then adds that result.
 template <int D, bool FP8>
 struct OpenRow {
-    float* part = nullptr;
-    const float* other = nullptr;
     __nv_bfloat16* out = nullptr;
     float* lse_at = nullptr;
-    float by = 0.0f, lse = 0.0f;
+    float lse = 0.0f, by = 0.0f;
+    int64_t at = 0;
     // row, head: of Q; m, l: maximum and sum; on: there is such a row
     __device__ __forceinline__ OpenRow(const OpenArgs& a, bool on, int64_t row, int64_t head, float m, float l,
                                        float v_scale, float& scale) {
         if (!on) return;
         constexpr float kRaise = FP8 ? kRaiseLog2 : 0.0f;
-        const int64_t at = row * a.Hq + head;
+        at = row * a.Hq + head;
         out = a.out + row * a.ldo + head * D;
-        if (a.part) {
-            part = a.part + at * D;
-            lse = l == 0.0f ? -CUDART_INF_F : m + log2f(l) - kRaise;
-            lse_at = a.part_lse + at;
-            return;
-        }
         if (a.lse) lse_at = a.lse + at;
         if (a.other) {
-            const float lo = __ldcg(a.other_lse + at);
-            const Joined j = join_keys(m, l, kRaise, lo);
+            const Joined j = join_keys(m, l, kRaise, other(a, v_scale).log);
             scale = j.own * v_scale;
             by = j.other;
             lse = j.lse;
-            if (lo != -CUDART_INF_F) other = a.other + at * D;
-        } else if (a.lse) {
-            lse = l == 0.0f ? -CUDART_INF_F : (m + log2f(l) - kRaise) * 0.69314718055994531f;
+        } else if (a.part || a.lse) {
+            lse = l == 0.0f ? -CUDART_INF_F : m + log2f(l) - kRaise;
+            if (!a.part) lse *= 0.69314718055994531f;
         }
     }
-    // N columns from `col` on, scaled already
+    __device__ __forceinline__ OtherRow<FP8> other(const OpenArgs& a, float v_scale) const {
+        return OtherRow<FP8>(row_of(a.other_of + at), a.other_slots, a.other + at * D, v_scale);
+    }
+    // the result over the other keys, added to N columns from `col` on that are scaled already
     template <int N>
-    __device__ __forceinline__ void put(float (&v)[N], int col) const {
-        if (part) {
+    __device__ __forceinline__ void add(const OpenArgs& a, float (&v)[N], int col, float v_scale) const {
+        if (!a.other || !out) return;
+        const OtherRow<FP8> x = other(a, v_scale);
 #pragma unroll
-            for (int k = 0; k < N; k += 4)
-                *reinterpret_cast<float4*>(part + col + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-            return;
-        }
-        if (other) {
-#pragma unroll
-            for (int k = 0; k < N; k += 4) {
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(other + col + k));
-                v[k] += x.x * by;
-                v[k + 1] += x.y * by;
-                v[k + 2] += x.z * by;
-                v[k + 3] += x.w * by;
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < N; k += 8) {
-            float x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = v[k + e];
-            *reinterpret_cast<uint4*>(out + col + k) = pack8_bf16(x);
+        for (int k = 0; k < N; k += 4) {
+            float4 y = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+            x.add(y, col + k, by);
+            v[k] = y.x;
+            v[k + 1] = y.y;
+            v[k + 2] = y.z;
+            v[k + 3] = y.w;
         }
     }
-    __device__ __forceinline__ void put_lse() const {
-        if (lse_at) *lse_at = lse;
+    __device__ __forceinline__ void put_lse(const OpenArgs& a) const {
+        if (!out) return;
+        if (a.part) a.part_of[at] = RowOf{lse, 0, 0, -1};
+        else if (lse_at) *lse_at = lse;
     }
 };
 
 // The result of the first `count` rows of tile t of a split item, from its contributors' slots, first
-// to last. The tile's N threads call it (who: the thread's number), P to a row, each with an equal part
-// of the columns: 16 loads of 16 bytes in flight, however few the rows.
-template <int D, bool FP8, int N, int P>
-__device__ __forceinline__ void join_open(const OpenArgs& a, const OpenPiece& p, int t, int who, int count,
+// to last. The tile's 128 threads call it (row: the thread's number), P to a row of the result, each
+// with an equal part of the columns: 16 loads of 16 bytes in flight, however few the rows.
+template <int D, bool FP8, int P>
+__device__ __forceinline__ void join_open(const OpenArgs& a, const OpenPiece& p, int t, int row, int count,
                                           const float* slots, float v_scale) {
-    constexpr int kRows = N / P, kCols = D / P;      // a thread's columns
+    constexpr int kRows = 128 / P, kCols = D / P;    // a thread's columns
     constexpr int kChunk = kCols < 64 ? kCols : 64;  // of which it sums so many at a time,
     constexpr int kAtOnce = 64 / kChunk;             // of so many contributors
-    const int r = who % kRows, part = who / kRows;
+    const int r = row % kRows, part = row / kRows;
     const int from = p.first, upto = p.last;
     if (r >= count) return;
     auto slot_of = [&](int cta) {
@@ -365,9 +347,16 @@ __device__ __forceinline__ void join_open(const OpenArgs& a, const OpenPiece& p,
         }
 #pragma unroll
         for (int k = 0; k < kChunk; ++k) v[k] = ll == 0.0f ? 0.0f : v[k] * scale;
-        to.put(v, col);
+        to.add(a, v, col, v_scale);
+#pragma unroll
+        for (int k = 0; k < kChunk; k += 8) {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = v[k + e];
+            *reinterpret_cast<uint4*>(to.out + col + k) = pack8_bf16(x);
+        }
     }
-    if (part == 0) to.put_lse();
+    if (part == 0) to.put_lse(a);
 }
 
 template <int D, bool FP8>
@@ -375,7 +364,7 @@ __global__ void __launch_bounds__(OpenShape<D, FP8>::kThreads, 1)
 attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ OpenArgs a) {
     using L = OpenShape<D, FP8>;
-    constexpr int NST = L::kStages, NRAW = L::kRaws, U = L::U, W0 = L::kWarp0;
+    constexpr int NST = L::kStages, NRAW = L::kRaws, W0 = 8;
     constexpr uint32_t kIdescS = prompt_idesc(kSB, FP8, false);
     constexpr uint32_t kIdescO = prompt_idesc(D, FP8, true);
     constexpr uint32_t kHalf = 16384;  // bytes of 64 columns x 128 rows
@@ -395,13 +384,11 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     const uint32_t drain = more + 24u;
     auto join_in = [&](int t) { return more + 32u + 8u * t; };
     auto join_out = [&](int t) { return more + 48u + 8u * t; };
-    auto meet = [&](int t) { return more + 64u + 8u * t; };
     auto s_full = [&](int t, int buf) { return more + 80u + 16u * t + 8u * buf; };
     auto p_full = [&](int t, int buf) { return more + 112u + 16u * t + 8u * buf; };
-    // of the streams (tile, parity)
-    auto o_full = [&](int t, int u) { return more + 144u + 16u * t + 8u * u; };
-    auto o_empty = [&](int t, int u) { return more + 176u + 16u * t + 8u * u; };
-    auto pv_done = [&](int t, int u) { return more + 208u + 16u * t + 8u * u; };
+    auto o_full = [&](int t) { return more + 144u + 8u * t; };
+    auto o_empty = [&](int t) { return more + 160u + 8u * t; };
+    auto pv_done = [&](int t) { return more + 176u + 8u * t; };
     auto piece_full = [&](int s) { return more + 240u + 8u * s; };
     auto piece_empty = [&](int s) { return more + 272u + 8u * s; };
     static_assert(304 <= 48 * 8, "barriers");
@@ -429,17 +416,16 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             ptx::mbar_init(raw_empty(s), L::kConvert);
         }
         for (int t = 0; t < 2; ++t) {
-            ptx::mbar_init(q_full(t), FP8 ? 4 * U : 1);
+            ptx::mbar_init(q_full(t), FP8 ? 4 : 1);
             for (int buf = 0; buf < 2; ++buf) {
                 ptx::mbar_init(s_full(t, buf), 1);
                 ptx::mbar_init(p_full(t, buf), 4);
-                ptx::mbar_init(o_full(t, buf), 1);
-                ptx::mbar_init(o_empty(t, buf), 4 * U);
-                ptx::mbar_init(pv_done(t, buf), 1);
             }
-            ptx::mbar_init(join_in(t), 4 * U);
+            ptx::mbar_init(o_full(t), 1);
+            ptx::mbar_init(o_empty(t), 4);
+            ptx::mbar_init(pv_done(t), 1);
+            ptx::mbar_init(join_in(t), 4);
             ptx::mbar_init(join_out(t), 1);
-            ptx::mbar_init(meet(t), 4 * U);
         }
         for (int s = 0; s < kOpenPieces; ++s) {
             ptx::mbar_init(piece_full(s), 1);
@@ -468,8 +454,8 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         const int64_t n = (first + static_cast<int64_t>(a.T) - last) * a.Hq;
         for (int64_t i = static_cast<int64_t>(blockIdx.x) * L::kThreads + threadIdx.x; i < n;
              i += static_cast<int64_t>(gridDim.x) * L::kThreads)
-            a.part_lse[i < static_cast<int64_t>(first) * a.Hq ? i : i + static_cast<int64_t>(last - first) * a.Hq] =
-                -CUDART_INF_F;
+            a.part_of[i < static_cast<int64_t>(first) * a.Hq ? i : i + static_cast<int64_t>(last - first) * a.Hq] =
+                RowOf{-CUDART_INF_F, 0, 0, -1};
     }
 
     // ---------------------------------------------------------------- the work list
@@ -521,7 +507,7 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     __syncthreads();
     ptx::tc_fence_after();
     work.items = found[0];
-    work.split = false;
+    work.split = work.dealt = false;
     work.at = work.end = 0;
     work.per = 1;
     {
@@ -545,7 +531,7 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     }
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(ctl);
     auto tmem_s = [&](int t, int buf) { return tmem + 256u + 128u * t + kSB * buf; };
-    auto tmem_o = [&](int t, int u) { return tmem + static_cast<uint32_t>(D * (U * t + u)); };
+    auto tmem_o = [&](int t) { return tmem + static_cast<uint32_t>(D * t); };
     // (polls for a while before the bounded wait, which reads the global timer)
     auto wait = [&](uint32_t bar, uint32_t parity, int role, uint64_t limit_ns = ptx::kWaitLimitNs) {
         bool done = false;
@@ -571,12 +557,12 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     };
 
     if (warp < W0) {
-        // ------------------------------------------------------------ softmax of one stream
-        const int t = (warp >> 2) / U, u = (warp >> 2) % U;
+        // ------------------------------------------------------------ softmax of one tile
+        const int t = warp >> 2;
         const int row = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        uint32_t s_phase = 0, o_phase = 0, q_empty_phase = 0, q_full_phase = 0, j_phase = 0, meet_phase = 0, blocks = 0;
-        uint32_t pv_count = 0;  // products P V of this stream so far
+        uint32_t s_phase = 0, o_phase = 0, q_empty_phase = 0, j_phase = 0, blocks = 0;
+        uint32_t pv_count = 0;  // products P V of this tile so far
         const int token = row / a.G, head = row - token * a.G;
         while (const OpenPiece* p = next_piece()) {
             const int tokens = p->tokens[t];
@@ -594,8 +580,7 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                         // neighbours side by side, up to 8 loads in flight (a thread to a row, 16 bytes of
                         // 32 rows to a load: 7 us for 256 rows of 128). The factor that the row was
                         // divided by goes to the thread that has the row.
-                        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kSteps = 32 / U / kAtOnce;
-                        constexpr int kLoads = kSteps < 8 ? kSteps : 8;
+                        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kSteps = 32 / kAtOnce, kLoads = 8;
                         float* const up = reinterpret_cast<float*>(base_ptr + L::kUp) + t * 128;
                         const __nv_bfloat16* mine_at = mine ? a.q + qrow() * a.ldq + qhead() * D : nullptr;
                         if (!wait(q_empty, q_empty_phase ^ 1u, 1, kPieceWaitNs)) break;
@@ -604,14 +589,14 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                             uint4 v[kLoads];
 #pragma unroll
                             for (int x = 0; x < kLoads; ++x) {
-                                const int r = u * (32 / U) + (x0 + x) * kAtOnce + lane / kLanes;
+                                const int r = (x0 + x) * kAtOnce + lane / kLanes;
                                 const auto at = __shfl_sync(~0u, reinterpret_cast<unsigned long long>(mine_at), r);
                                 v[x] = make_uint4(0, 0, 0, 0);
                                 if (at) v[x] = load16(reinterpret_cast<const uint8_t*>(at) + 16 * (lane % kLanes));
                             }
 #pragma unroll
                             for (int x = 0; x < kLoads; ++x) {
-                                const int r = u * (32 / U) + (x0 + x) * kAtOnce + lane / kLanes, piece = lane % kLanes;
+                                const int r = (x0 + x) * kAtOnce + lane / kLanes, piece = lane % kLanes;
                                 float f[8], big = 0.0f;
                                 unpack8(v[x], f);
 #pragma unroll
@@ -630,19 +615,17 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                         fence_async_shared();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(q_full(t));
-                        if (!wait(q_full(t), q_full_phase, 4)) break;
-                        q_full_phase ^= 1u;
                         c = c * a.kv.scales[p->h] * up[row];
                         if (c == 0.0f) c = FLT_MIN;  // 0 times a masked score of -infinity would be NaN
                     }
                     q_empty_phase ^= 1u;
                 }
             }
-            float m = -CUDART_INF_F, l = 0.0f;  // reference maximum (log2 units), sum
+            float m = -CUDART_INF_F, l = 0.0f;  // reference (log2 units), sum
             const uint32_t block0 = blocks - b0;
             blocks += b1 - b0;
             bool ok = true;
-            for (int j = begin + u; j < end; j += U) {
+            for (int j = begin; j < end; ++j) {
                 const int buf = j & 1;
                 if (!(ok = wait(s_full(t, buf), (s_phase >> buf) & 1u, 2))) break;
                 s_phase ^= 1u << buf;
@@ -652,9 +635,6 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 // 32 of the step's keys, those that are not there masked
                 const int below = len - j * kSB;
                 const bool cut = below < kSB || have != 0xFu;
-                auto load = [&](int half, uint32_t (&s)[32]) {
-                    ptx::tmem_ld_32x32b_x32(ts + 32 * half, s);
-                };
                 auto loaded = [&](int half, uint32_t (&s)[32]) {
                     ptx::tmem_wait_ld(s);
                     if (cut) {
@@ -663,70 +643,78 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                             s[k] = 32 * half + k < below && ((have >> (2 * half + (k >> 4))) & 1u) ? s[k] : 0xFF800000u;
                     }
                 };
-                uint32_t lo[32], hi[32];
-                load(1, hi);
-                load(0, lo);
-                loaded(1, hi);
-                float top[4];
-                auto highest = [&](const uint32_t (&s)[32]) {
-#pragma unroll
-                    for (int k = 0; k < 32; k += 8)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            top[x] = max3(top[x], __uint_as_float(s[k + x]), __uint_as_float(s[k + 4 + x]));
-                };
-#pragma unroll
-                for (int x = 0; x < 4; ++x) top[x] = -CUDART_INF_F;
-                highest(hi);
-                loaded(0, lo);
-                highest(lo);
-                const float now = fmaxf(max3(top[0], top[1], top[2]), top[3]) * c;
-                const bool move = now > m + kLazyLog2;
-                if (__any_sync(~0u, move)) {
-                    const float f = move ? exp2_approx(m - now) : 1.0f;
-                    if (move) m = now;
-                    l *= f;
-                    // O of the steps before is scaled, once the last of their products is done
-                    if (j >= begin + U) {
-                        if (!(ok = wait(pv_done(t, u), (pv_count - 1) & 1u, 17))) break;
-                        ptx::tc_fence_after();
-#pragma unroll 1
-                        for (int x = 0; x < D; x += 16) {
-                            uint32_t o[16];
-                            ptx::tmem_ld_32x32b_x16_wait(tmem_o(t, u) + lanes + x, o);
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                            ptx::tmem_st_32x32b_x16_wait(tmem_o(t, u) + lanes + x, o);
-                        }
-                    }
-                }
-                ++pv_count;
                 // P = 2^(S c - m), two values to an instruction where there is one; rounded to 16 bits for
                 // the product with V, of V's type (both operands of these instructions have one type):
-                // half a step of a weight is 2^-8 of it in bf16, 2^-11 in fp16; its sum is taken before
-                const float shift = (FP8 ? kRaiseLog2 : 0.0f) - (m == -CUDART_INF_F ? 0.0f : m);
-                const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
-                float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-                auto weights = [&](int half, const uint32_t (&s)[32]) {
-                    uint32_t w[16];
+                // half a step of a weight is 2^-8 of it in bf16, 2^-11 in fp16; its sum is taken before.
+                // The reference m is the maximum of the first step, and stays while a step's weights sum
+                // to no more than kOpenMost: there is no need to look for a step's maximum then. Where they
+                // do, or the row has met no key yet, the reference becomes the maximum so far, and P is made
+                // again. (A weight's relative error does not depend on the reference.)
+                bool look = j == begin;
+                uint32_t w[32];
+                float2 sum[2];
+#pragma unroll 1
+                for (;;) {
+                    uint32_t s[32];
+                    if (look) {
+                        float top[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll 1
+                        for (int half = 0; half < 2; ++half) {
+                            ptx::tmem_ld_32x32b_x32(ts + 32 * half, s);
+                            loaded(half, s);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        float2 e = fma2(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), c2, shift2);
-                        e.x = exp2_approx(e.x);
-                        e.y = exp2_approx(e.y);
-                        sum[k & 1] = add2(sum[k & 1], e);
-                        w[k] = FP8 ? pack_half2(e.x, e.y) : pack_bf162(e.x, e.y);
+                            for (int k = 0; k < 32; k += 8)
+#pragma unroll
+                                for (int x = 0; x < 4; ++x)
+                                    top[x] = max3(top[x], __uint_as_float(s[k + x]), __uint_as_float(s[k + 4 + x]));
+                        }
+                        const float now = fmaxf(max3(top[0], top[1], top[2]), top[3]) * c;
+                        const float f = now > m ? exp2_approx(m - now) : 1.0f;
+                        if (now > m) m = now;
+                        l *= f;
+                        // O of the steps before is scaled, once the last of their products is done
+                        if (j > begin) {
+                            if (!(ok = wait(pv_done(t), (pv_count - 1) & 1u, 17))) break;
+                            ptx::tc_fence_after();
+#pragma unroll 1
+                            for (int x = 0; x < D; x += 16) {
+                                uint32_t o[16];
+                                ptx::tmem_ld_32x32b_x16_wait(tmem_o(t) + lanes + x, o);
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                                ptx::tmem_st_32x32b_x16_wait(tmem_o(t) + lanes + x, o);
+                            }
+                        }
                     }
-                    tmem_st_x16(ts + 16 * half, w);
-                };
-                // (P takes the columns of the first 32 keys' scores. Where registers are few, the last 32's
-                // are loaded a second time.)
-                weights(0, lo);
-                if constexpr (L::kReload) {
-                    load(1, hi);
-                    loaded(1, hi);
+                    const float shift = (FP8 ? kRaiseLog2 : 0.0f) - (m == -CUDART_INF_F ? 0.0f : m);
+                    const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
+                    sum[0] = sum[1] = make_float2(0.0f, 0.0f);
+                    auto weights = [&](int half) {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            float2 e = fma2(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), c2, shift2);
+                            e.x = exp2_approx(e.x);
+                            e.y = exp2_approx(e.y);
+                            sum[k & 1] = add2(sum[k & 1], e);
+                            w[16 * half + k] = FP8 ? pack_half2(e.x, e.y) : pack_bf162(e.x, e.y);
+                        }
+                    };
+                    uint32_t s1[32];
+                    ptx::tmem_ld_32x32b_x32(ts, s);
+                    loaded(0, s);
+                    ptx::tmem_ld_32x32b_x32(ts + 32, s1);
+                    weights(0);
+                    loaded(1, s1);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) s[k] = s1[k];
+                    weights(1);
+                    const float step = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                    if (look || !__any_sync(~0u, mine && (!(step <= kOpenMost) || m == -CUDART_INF_F))) break;
+                    look = true;
                 }
-                weights(1, hi);
+                if (!ok) break;
+                ++pv_count;
+                tmem_st_x32(ts, w);
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 tmem_wait_st();
                 ptx::tc_fence_before();
@@ -739,86 +727,101 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 release_piece();
                 continue;
             }
-            // steps of the tile's streams; their factors (of one reference maximum for both)
-            const int steps = end - begin;
-            float factor[U];
-            factor[0] = 1.0f;
-            if constexpr (U == 2) {
-                float2* const at = reinterpret_cast<float2*>(base_ptr + L::kMeet) + (meet_phase * 2 + t) * 2 * 128;
-                at[u * 128 + row] = make_float2(m, l);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(meet(t));
-                if (!wait(meet(t), meet_phase, 18)) break;
-                meet_phase ^= 1u;
-                const float2 other = at[(u ^ 1) * 128 + row];
-                const float both = fmaxf(m, other.x), safe = both == -CUDART_INF_F ? 0.0f : both;
-                const float fm = exp2_approx(m - safe), fo = exp2_approx(other.x - safe);
-                l = l * fm + other.y * fo;
-                m = both;
-                factor[u] = fm;
-                factor[u ^ 1] = fo;
-            }
-            const bool whole = p->first == p->last;
+            const bool whole = p->first == p->last, any = end > begin;
             float* const slots = a.partial + static_cast<int64_t>(t) * kPromptSlotFloats;
             float* const slot = slots + (static_cast<int64_t>(blockIdx.x) * 2 + p->starts) * 2 * kPromptSlotFloats;
             const float v_scale = FP8 ? a.kv.scales[a.kv.Hkv + p->h] : 1.0f;
             float inv = l == 0.0f ? 0.0f : v_scale / l;  // no keys: zeros
             const OpenRow<D, FP8> to(a, mine && whole, qrow(), qhead(), m, l, v_scale, inv);
-#pragma unroll
-            for (int x = 0; x < U; ++x)
-                if (steps > x) {
-                    if (!(ok = wait(o_full(t, x), (o_phase >> x) & 1u, 3))) break;
-                    o_phase ^= 1u << x;
-                }
-            if (!ok) break;
-            ptx::tc_fence_after();
-            constexpr int kCols = D / U;  // this stream's part of the columns
-#pragma unroll 1
-            for (int col = u * kCols; col < (u + 1) * kCols; col += 16) {
-                __syncwarp();
-                float v[16];
-#pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] = 0.0f;
-#pragma unroll
-                for (int x = 0; x < U; ++x)
-                    if (steps > x) {
-                        uint32_t o[16];
-                        ptx::tmem_ld_32x32b_x16_wait(tmem_o(t, x) + lanes + col, o);
-#pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            v[k] = U == 1 ? __uint_as_float(o[k]) : fmaf(factor[x], __uint_as_float(o[k]), v[k]);
-                    }
-                if (mine && whole) {
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) v[k] = l == 0.0f ? 0.0f : v[k] * inv;
-                    to.put(v, col);
-                } else if (mine) {
-#pragma unroll
-                    for (int k = 0; k < 16; k += 4)
-                        __stcg(reinterpret_cast<float4*>(slot + (col + k) * 128 + row * 4),
-                               make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]));
-                }
+            if (any) {
+                if (!wait(o_full(t), o_phase, 3)) break;
+                o_phase ^= 1u;
+                ptx::tc_fence_after();
             }
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
+            uint8_t* const stage = base_ptr + L::kStore0 + warp * 2048;
+            __nv_bfloat16* rows_to[4];  // rows 8k + lane / 4, from their lanes
 #pragma unroll
-                for (int x = 0; x < U; ++x)
-                    if (steps > x) mbar_arrive(o_empty(t, x));
+            for (int k = 0; k < 4; ++k)
+                rows_to[k] = reinterpret_cast<__nv_bfloat16*>(
+                    __shfl_sync(~0u, reinterpret_cast<unsigned long long>(to.out), 8 * k + (lane >> 2)));
+#pragma unroll 1
+            for (int col = 0; col < D; col += 32) {
+                __syncwarp();
+                uint32_t o[32];
+                if (any) {
+                    ptx::tmem_ld_32x32b_x32(tmem_o(t) + lanes + col, o);
+                    ptx::tmem_wait_ld(o);
+                    if (col + 32 == D) {
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(o_empty(t));
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = 0u;
+                }
+                if (!whole) {
+                    if (mine) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            __stcg(reinterpret_cast<float4*>(slot + (col + k) * 128 + row * 4),
+                                   make_float4(__uint_as_float(o[k]), __uint_as_float(o[k + 1]),
+                                               __uint_as_float(o[k + 2]), __uint_as_float(o[k + 3])));
+                    }
+                    continue;
+                }
+                float v[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) v[k] = l == 0.0f ? 0.0f : __uint_as_float(o[k]) * inv;
+                if (a.part) {
+                    if (mine) {
+                        float* const dst = a.part + to.at * D + col;
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            *reinterpret_cast<float4*>(dst + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                    }
+                    continue;
+                }
+                to.add(a, v, col, v_scale);
+                // through shared memory, so that four lanes write 64 contiguous bytes of a row (a line of
+                // a store takes the SM a cycle, however few of its bytes are written)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = v[8 * k + e];
+                    *reinterpret_cast<uint4*>(stage + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) = pack8_bf16(x);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int r = 8 * k + (lane >> 2), x = lane & 3;
+                    const uint4 y = *reinterpret_cast<const uint4*>(stage + r * 64 + ((x ^ ((r >> 1) & 3)) << 4));
+                    if (rows_to[k]) *reinterpret_cast<uint4*>(rows_to[k] + col + 8 * x) = y;
+                }
             }
             if (whole) {
-                if (u == 0) to.put_lse();
+                to.put_lse(a);
+            } else if (a.part) {
+                // whoever reads the rows' results sums the contributors (they are read by many CTAs; a
+                // join by the last contributor alone took 20 us of 10 contributors' sums of 256 rows)
+                if (mine) {
+                    __stcg(slot + 128 * 128 + row, m);
+                    __stcg(slot + 128 * 128 + 128 + row, l);
+                    if (p->starts)
+                        a.part_of[qrow() * a.Hq + qhead()] = RowOf{0.0f, p->first, p->last, t * 128 + row};
+                }
             } else {
                 // The last contributor to arrive sums all of them, first to last (see the row kernel);
-                // each tile's threads count and join on their own.
-                if (mine && u == 0) {
+                // each tile's 128 threads count and join on their own.
+                if (mine) {
                     __stcg(slot + 128 * 128 + row, m);
                     __stcg(slot + 128 * 128 + 128 + row, l);
                 }
                 __threadfence();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(join_in(t));
-                if (warp == 4 * U * t) {
+                if (warp == 4 * t) {
                     if (!wait(join_in(t), j_phase, 13)) break;
                     if (lane == 0) {
                         __threadfence();
@@ -834,12 +837,11 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 j_phase ^= 1u;
                 if (*reinterpret_cast<volatile uint32_t*>(s_last + t)) {
                     __threadfence();
-                    const int count = tokens * a.G, who = u * 128 + row;
-                    constexpr int N = 128 * U;
-                    if (count > 64) join_open<D, FP8, N, U>(a, *p, t, who, count, slots, v_scale);
-                    else if (count > 32) join_open<D, FP8, N, 2 * U>(a, *p, t, who, count, slots, v_scale);
-                    else if (D == 64 || count > 16) join_open<D, FP8, N, 4 * U>(a, *p, t, who, count, slots, v_scale);
-                    else if constexpr (D == 128) join_open<D, FP8, N, 8>(a, *p, t, who, count, slots, v_scale);
+                    const int count = tokens * a.G;
+                    if (count > 64) join_open<D, FP8, 1>(a, *p, t, row, count, slots, v_scale);
+                    else if (count > 32) join_open<D, FP8, 2>(a, *p, t, row, count, slots, v_scale);
+                    else if (count > 16) join_open<D, FP8, 4>(a, *p, t, row, count, slots, v_scale);
+                    else join_open<D, FP8, 8>(a, *p, t, row, count, slots, v_scale);
                 }
             }
             release_piece();
@@ -889,13 +891,12 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 #pragma unroll
                 for (int par = 0; par < 2; ++par) {
                     const int jv = 2 * (i - 1) + par, jk = 2 * i + par;
-                    const int u = U == 2 ? par : 0;
-                    const uint32_t ts = tmem_s(t, par), to = tmem_o(t, u);
+                    const uint32_t ts = tmem_s(t, par), to = tmem_o(t);
                     if (i > b0 && jv < end) {
-                        const bool fresh = jv < begin + U;
-                        if (fresh) {  // the stream's result before this one has been read
-                            if (!(ok = wait(o_empty(t, u), ((o_phase >> u) & 1u) ^ 1u, 6))) break;
-                            o_phase ^= 1u << u;
+                        const bool fresh = jv == begin;
+                        if (fresh) {  // the tile's result before this one has been read
+                            if (!(ok = wait(o_empty(t), o_phase ^ 1u, 6))) break;
+                            o_phase ^= 1u;
                         }
                         if (!(ok = wait(p_full(t, par), (p_phase >> par) & 1u, 7))) break;
                         p_phase ^= 1u << par;
@@ -910,8 +911,8 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                                 for (int k = 0; k < groups16; ++k)
                                     mma_ts(to, ts + 8 * k, dv + 512 * par + 128 * k, kIdescO, k == 0 ? !fresh : 1u);
                             }
-                            ptx::mma_commit(pv_done(t, u));
-                            if (jv + U >= end) ptx::mma_commit(o_full(t, u));
+                            ptx::mma_commit(pv_done(t));
+                            if (jv + 1 == end) ptx::mma_commit(o_full(t));
                         }
                         __syncwarp();
                     }

@@ -46,12 +46,9 @@ constexpr int kPromptCode = 0x2000;  // wait sites: kPromptCode | role
 // most). The roles that such a wait is for have the usual limit for every step of theirs, and end
 // this one at once when they give up.
 constexpr uint64_t kPieceWaitNs = 60ull * 1000 * 1000 * 1000;
-// fp32 values of a tile's partial sums: O in groups of 4 columns [D/4][128][4], m [128], l [128].
-constexpr int kPromptSlotFloats = 128 * 128 + 256;
 // A row's reference maximum follows its running maximum only when that has grown by more than
 // 2^8: weights then stay below 2^8 (no loss in fp32, bf16 or fp16) and O is rarely rescaled.
 constexpr float kLazyLog2 = 8.0f;
-constexpr float kRaiseLog2 = 6.0f;  // e4m3 caches: fp16 weights are raised by 2^6 (see the rows)
 
 struct PromptArgs {
     KvView kv;

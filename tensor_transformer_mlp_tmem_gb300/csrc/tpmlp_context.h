@@ -104,9 +104,11 @@ struct tpmlp_ctx {
     uint16_t* norm_w = nullptr;      // [heads_q + heads_kv][head_dim] bf16 (tpmlp_attn_set_norms)
     bool norm_on = false, norm_per_head = false;
     float norm_eps = 0.0f;
-    // tpmlp_attn_decode_shared: results over prefixes, fp32 [shared_rows][heads_q][head_dim] and the
-    // logs [shared_rows][heads_q]. Captured graphs hold a buffer's address, so the smaller ones before
-    // the last stay until the context goes; each is at least twice the one before.
+    size_t attn_partial_floats = 0;  // values of attn_partial
+    // tpmlp_attn_decode_shared: results over prefixes (tpmlp_attn_open.cu) of shared_rows sequences.
+    // Captured graphs hold a buffer's address, so the smaller ones before the last stay until the context
+    // goes; each is at least twice the one before. tail_partial: a second attn_partial.
+    float* tail_partial = nullptr;
     float* shared[40] = {};
     int shared_n = 0;
     int64_t shared_rows = 0;
