@@ -333,88 +333,11 @@ constexpr int kPromptSlotFloats = 128 * 128 + 256;
 constexpr float kRaiseLog2 = 6.0f;  // e4m3 caches: a tile's fp16 weights are raised by 2^6 (see the rows)
 constexpr int kJoinLoads = 8;  // contributors of a split range whose sums a thread loads at once
 
-// Where a row's result over the keys of another cache lies (tpmlp_attn_open.cuh writes it).
+// Where a row's result over some of its keys lies, for the kernel that joins it with another.
 struct __align__(16) RowOf {
     float log;        // whole: log2 of the sum of its weights; -infinity: no keys, and no result is looked at
-    int first, last;  // split: the contributing CTAs
+    int first, last;  // split: the contributing CTAs of the kernel that made it
     int place;        // split: tile * 128 + row in their slots; whole: -1
-};
-__device__ __forceinline__ RowOf row_of(const RowOf* p) {
-    const uint4 v = load16(reinterpret_cast<const uint8_t*>(p));
-    return {__uint_as_float(v.x), static_cast<int>(v.y), static_cast<int>(v.z), static_cast<int>(v.w)};
-}
-
-// That result: of a whole row in fp32 at `whole`, of a split one from its contributors, first to last.
-template <bool FP8>
-struct OtherRow {
-    const float* whole;
-    const float* slot;  // first contributor's column 0; the others' are 4 slots apart (and 2 back)
-    RowOf of;
-    float top, scale, log;  // log: log2 of the sum of weights
-    __device__ __forceinline__ const float* at(int cta) const {
-        return slot + (static_cast<int64_t>(cta - of.first) * 4 - (cta != of.first ? 2 : 0)) * kPromptSlotFloats;
-    }
-    __device__ __forceinline__ OtherRow(const RowOf& from, const float* slots, const float* row, float v_scale)
-        : whole(row), of(from) {
-        log = of.log;
-        if (of.place < 0) return;
-        const int r = of.place & 127;
-        slot = slots + (static_cast<int64_t>(of.first) * 4 + 2 + (of.place >> 7)) * kPromptSlotFloats + r * 4;
-        float m = -CUDART_INF_F, l = 0.0f;
-        for (int c0 = of.first; c0 <= of.last; c0 += kJoinLoads) {
-            float mx[kJoinLoads], lx[kJoinLoads], t = m;
-#pragma unroll
-            for (int u = 0; u < kJoinLoads; ++u) {
-                const float* p = at(min(c0 + u, of.last)) + 128 * 128 - r * 3;
-                mx[u] = __ldcg(p);
-                lx[u] = c0 + u <= of.last ? __ldcg(p + 128) : 0.0f;
-            }
-#pragma unroll
-            for (int u = 0; u < kJoinLoads; ++u) t = fmaxf(t, mx[u]);
-            const float safe = t == -CUDART_INF_F ? 0.0f : t;
-            l *= exp2_approx(m - safe);
-            m = t;
-#pragma unroll
-            for (int u = 0; u < kJoinLoads; ++u) l += exp2_approx(mx[u] - safe) * lx[u];
-        }
-        top = m == -CUDART_INF_F ? 0.0f : m;
-        scale = l == 0.0f ? 0.0f : v_scale / l;
-        log = l == 0.0f ? -CUDART_INF_F : m + log2f(l) - (FP8 ? kRaiseLog2 : 0.0f);
-    }
-    // y times columns d .. d + 3 of it, added to v
-    __device__ __forceinline__ void add(float4& v, int d, float y) const {
-        if (log == -CUDART_INF_F) return;
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (of.place < 0) {
-            o = __ldcg(reinterpret_cast<const float4*>(whole + d));
-        } else {
-            for (int c0 = of.first; c0 <= of.last; c0 += kJoinLoads) {
-                float mx[kJoinLoads];
-                float4 x[kJoinLoads];
-#pragma unroll
-                for (int u = 0; u < kJoinLoads; ++u) {
-                    const float* p = at(min(c0 + u, of.last));
-                    mx[u] = __ldcg(p + 128 * 128 - (of.place & 127) * 3);
-                    x[u] = __ldcg(reinterpret_cast<const float4*>(p + d * 128));
-                }
-#pragma unroll
-                for (int u = 0; u < kJoinLoads; ++u) {
-                    // past the last one, sums of 0 as well (see the row kernel)
-                    const bool on = c0 + u <= of.last;
-                    const float f = on ? exp2_approx(mx[u] - top) : 0.0f;
-                    o.x += f * (on ? x[u].x : 0.0f);
-                    o.y += f * (on ? x[u].y : 0.0f);
-                    o.z += f * (on ? x[u].z : 0.0f);
-                    o.w += f * (on ? x[u].w : 0.0f);
-                }
-            }
-            y *= scale;
-        }
-        v.x += y * o.x;
-        v.y += y * o.y;
-        v.z += y * o.z;
-        v.w += y * o.w;
-    }
 };
 
 // ------------------------------------------------------------------ rows
@@ -433,27 +356,10 @@ struct RowArgs {
     int32_t window;
     float* partial;         // [CTAs][2] slots of RowSlot floats
     uint32_t* count;        // [CTAs] arrivals, 0 between launches
-    // JOIN: each row's result over keys of another cache: fp32 [rows][Hq][D], where it lies [rows][Hq],
-    // and the slots of partial sums of those that were split
-    const float* other;
-    const RowOf* other_of;
-    const float* other_slots;
+    // PART: where results go instead of out, fp32 [rows][Hq][D], and what they are [rows][Hq]
+    float* part;
+    RowOf* part_of;
 };
-
-// How a row's sums over its own keys (maximum m in log2 units, sum l of weights that were raised by
-// 2^raise) and its result over other keys, whose weights sum to 2^lo, make one softmax: the factors of
-// the unscaled sum and of that result, and the log of the sum of all weights.
-struct Joined {
-    float own, other, lse;
-};
-__device__ __forceinline__ Joined join_keys(float m, float l, float raise, float lo) {
-    const float mine = l == 0.0f ? -CUDART_INF_F : m + log2f(l) - raise;
-    const float top = fmaxf(mine, lo), safe = top == -CUDART_INF_F ? 0.0f : top;
-    const float x = exp2f(mine - safe), y = exp2f(lo - safe), sum = x + y;
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // no keys at all: zeros
-    return {l == 0.0f ? 0.0f : x * inv / l, y * inv,
-            sum == 0.0f ? -CUDART_INF_F : (top + log2f(sum)) * 0.69314718055994531f};
-}
 
 // Query heads to a kv head that this kernel takes, at most; decode of wider groups goes to the prompt
 // kernel, whose products' tiles they fill and which takes the same time for any G, while this
@@ -577,10 +483,11 @@ __device__ __forceinline__ int v_dim(int g, int e) {
     else return (D / 8) * g + e;
 }
 
-// JOIN: the launch before is the one that writes a.other, and nothing else that this kernel reads. That
-// launch let this one start only when everything before itself was done, so only what follows the first
-// segment's keys waits for it.
-template <int D, bool FP8, int NT, int PASSES, bool JOIN>
+// PART: results go to a.part in fp32, for a launch after this one. The launch before reads and writes
+// nothing that this one does (counters that it uses lie behind this kernel's), and let this one start only
+// when everything before itself was done; so this kernel waits for it at its own end alone, for the launch
+// after it to find both complete.
+template <int D, bool FP8, int NT, int PASSES, bool PART>
 __global__ void __launch_bounds__(kRowThreads, RowShape<D, FP8, NT>::kCtasPerSm)
 attn_row_kernel(const __grid_constant__ RowArgs a) {
     using S = RowShape<D, FP8, NT>;
@@ -594,12 +501,10 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
 
-    if constexpr (!JOIN) ptx::griddep_wait();
+    if constexpr (!PART) ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    bool waited = !JOIN;
-    auto wait_for_other = [&] {
-        if (!waited) ptx::griddep_wait();
-        waited = true;
+    auto leave = [&] {
+        if constexpr (PART) ptx::griddep_wait();
     };
 
     auto steps_of = [&](const RowRange& x) {
@@ -626,7 +531,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
             if (lane >= o) sum += v;
         }
         share(__shfl_sync(~0u, sum, 31) * per_row);
-        if (at >= end) return wait_for_other();
+        if (at >= end) return leave();
         row = __ffs(__ballot_sync(~0u, at < sum * per_row)) - 1;
         row_start = __shfl_sync(~0u, sum - c, row) * per_row;
     } else {
@@ -640,7 +545,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
 #pragma unroll
         for (int w = 0; w < kRowWarps; ++w) total += s_scan[w];
         share(total * per_row);
-        if (at >= end) return wait_for_other();
+        if (at >= end) return leave();
         int64_t before = 0;
         for (int r0 = 0; r0 < a.rows; r0 += kRowThreads) {
             const int r = r0 + tid;
@@ -668,7 +573,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         }
         row = static_cast<int>(s_found[0]);
         row_start = s_found[1];
-        if (row < 0) return wait_for_other();  // only if the lengths changed during the launch
+        if (row < 0) return leave();  // only if the lengths changed during the launch
     }
     RowRange range = row_range(a, row);
     int steps = steps_of(range);
@@ -684,7 +589,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         const int step0 = max(static_cast<int>(at - segment_start) - kSegmentStart, 0);
         at = min(end, segment_start + steps + kSegmentStart);
         const int n = static_cast<int>(at - segment_start) - kSegmentStart - step0;
-        if (n <= 0) return wait_for_other();  // the start alone: the segment's steps are the next CTA's
+        if (n <= 0) return leave();  // the start alone: the segment's steps are the next CTA's
         const int h = part / PASSES;
         const int q0 = part % PASSES * S::kRows;  // the pass's query heads of the group
         auto heads = [&] { return PASSES > 1 ? min(a.G - q0, S::kRows) : a.G; };  // of them
@@ -918,7 +823,6 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
                 }
         }
 
-        wait_for_other();  // (the partial sums' memory is the launch's before, too)
         // The warps' sums of this segment, joined in shared memory.
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -959,18 +863,13 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
 
         auto finish = [&](int r, int d, float4 v, float mm, float ll) {
             const int64_t head = static_cast<int64_t>(h) * a.G + q0 + r;
-            if constexpr (JOIN) {
+            if constexpr (PART) {
+                const float by = ll == 0.0f ? 0.0f : v_scale / ll;
                 const int64_t at_row = static_cast<int64_t>(row) * a.Hq + head;
-                const OtherRow<FP8> other(row_of(a.other_of + at_row), a.other_slots, a.other + at_row * D, v_scale);
-                const Joined x = join_keys(mm, ll, FP8 ? kRowRaise : 0.0f, other.log);
-                const float own = x.own * v_scale;
-                v = make_float4(v.x * own, v.y * own, v.z * own, v.w * own);
-                other.add(v, d, x.other);
-                uint2 w;
-                w.x = pack_bf162(v.x, v.y);
-                w.y = pack_bf162(v.z, v.w);
-                *reinterpret_cast<uint2*>(a.out + row * a.ldo + head * D + d) = w;
-                if (a.lse && d == 0) a.lse[at_row] = x.lse;
+                *reinterpret_cast<float4*>(a.part + at_row * D + d) = make_float4(v.x * by, v.y * by, v.z * by, v.w * by);
+                if (d == 0)
+                    a.part_of[at_row] = RowOf{
+                        ll == 0.0f ? -CUDART_INF_F : mm + log2f(ll) - (FP8 ? kRowRaise : 0.0f), 0, 0, -1};
                 return;
             }
             const float inv = ll == 0.0f ? 0.0f : v_scale / ll;  // no keys: zeros
@@ -1072,6 +971,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
             }
         }
     }
+    leave();
 }
 
 }  // namespace tpmlp

@@ -40,9 +40,6 @@ int run_open(tpmlp_ctx* c, const RowArgs& r, const int32_t* cu_q, int64_t T, cud
     a.count = c->attn_count;
     a.part = part;
     a.part_of = part_of;
-    a.other = r.other;
-    a.other_of = r.other_of;
-    a.other_slots = r.other_slots;
     CUtensorMap q{}, k{}, v{};
     if (int rc = prompt_maps(c, r, T, a.tpt, &q, &k, &v)) return rc;
     if (c->head_dim == 128)
@@ -50,10 +47,31 @@ int run_open(tpmlp_ctx* c, const RowArgs& r, const int32_t* cu_q, int64_t T, cud
     return is_e4m3(c) ? launch_open<64, true>(c, q, k, v, a, s) : launch_open<64, false>(c, q, k, v, a, s);
 }
 
-// The workspace of decode_shared: results over prefixes, fp32 [rows][Hq][D], and where each lies [rows][Hq].
-// The own keys' split ranges have partial sums of their own, since the prefixes' are read with them.
-size_t shared_bytes(const tpmlp_ctx* c, int64_t rows) {
+template <int D, bool FP8>
+int launch_join(tpmlp_ctx* c, const JoinPartsArgs& a, cudaStream_t s) {
+    constexpr int64_t kHeads = kJoinThreads / (D / 4);  // of a block
+    return launch(c, join_parts_kernel<D, FP8>, (a.heads + kHeads - 1) / kHeads, kJoinThreads, 0, s, a);
+}
+
+int run_join(tpmlp_ctx* c, const JoinPartsArgs& a, cudaStream_t s) {
+    if (c->head_dim == 128) return is_e4m3(c) ? launch_join<128, true>(c, a, s) : launch_join<128, false>(c, a, s);
+    return is_e4m3(c) ? launch_join<64, true>(c, a, s) : launch_join<64, false>(c, a, s);
+}
+
+// The workspace of decode_shared: results over prefixes and over own keys, each fp32 [rows][Hq][D] and what
+// they are [rows][Hq]. Own keys' split ranges have partial sums of their own, since the prefixes' are read
+// with them.
+struct SharedPart {
+    float* part;
+    RowOf* of;
+};
+size_t part_bytes(const tpmlp_ctx* c, int64_t rows) {
     return static_cast<size_t>(rows) * c->heads_q * (c->head_dim * sizeof(float) + sizeof(RowOf));
+}
+SharedPart shared_part(const tpmlp_ctx* c, int which) {
+    char* const p = reinterpret_cast<char*>(c->shared[c->shared_n - 1]) + which * part_bytes(c, c->shared_rows);
+    const int64_t values = c->shared_rows * c->heads_q * c->head_dim;
+    return {reinterpret_cast<float*>(p), reinterpret_cast<RowOf*>(reinterpret_cast<float*>(p) + values)};
 }
 
 // It holds `rows` sequences (s: the stream that a call is on; null: tpmlp_attn_reserve).
@@ -66,7 +84,7 @@ int reserve_shared(tpmlp_ctx* c, int64_t rows, const cudaStream_t* s) {
             return rc;
     const int64_t now = std::max(rows, 2 * c->shared_rows);
     void* p = nullptr;
-    if (int rc = allocate(c, &p, shared_bytes(c, now))) return rc;
+    if (int rc = allocate(c, &p, 2 * part_bytes(c, now))) return rc;
     c->shared[c->shared_n++] = static_cast<float*>(p);
     c->shared_rows = now;
     return TPMLP_OK;
@@ -110,18 +128,27 @@ int tpmlp_attn_decode_shared(tpmlp_ctx* c, const void* Q, int64_t ldq, const tpm
     if (reinterpret_cast<uintptr_t>(cu) & 3) return TPMLP_ERR_MISALIGNED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (int rc = reserve_shared(c, kv->B, &s)) return rc;
-    float* const part = c->shared[c->shared_n - 1];
-    RowOf* const part_of = reinterpret_cast<RowOf*>(part + c->shared_rows * c->heads_q * c->head_dim);
+    const SharedPart common = shared_part(c, 0), own = shared_part(c, 1);
     const RowArgs p = row_args(c, Q, ldq, prefix, scale, 0, Out, ldo, nullptr);
-    if (int rc = run_open(c, p, cu, kv->B, s, part, part_of)) return rc;
-    RowArgs a = row_args(c, Q, ldq, kv, scale, 0, Out, ldo, Lse);
+    if (int rc = run_open(c, p, cu, kv->B, s, common.part, common.of)) return rc;
+    RowArgs a = row_args(c, Q, ldq, kv, scale, 0, Out, ldo, nullptr);
     a.rows = kv->B;
     a.partial = c->tail_partial;
-    a.other = part;
-    a.other_of = part_of;
-    a.other_slots = c->attn_partial;
-    if (a.G > row_heads(c->head_dim, is_e4m3(c))) return run_open(c, a, nullptr, kv->B, s);
-    return run_rows<true>(c, a, s);
+    a.part = own.part;
+    a.part_of = own.of;
+    const bool wide = a.G > row_heads(c->head_dim, is_e4m3(c));
+    if (int rc = wide ? run_open(c, a, nullptr, kv->B, s, own.part, own.of) : run_rows<true>(c, a, s)) return rc;
+    JoinPartsArgs j{};
+    j.side[0] = {common.part, common.of, c->attn_partial};
+    j.side[1] = {own.part, own.of, c->tail_partial};
+    j.out = a.out;
+    j.ldo = ldo;
+    j.lse = Lse;
+    j.heads = static_cast<int64_t>(kv->B) * c->heads_q;
+    j.Hq = c->heads_q;
+    j.G = a.G;
+    j.v_scale = c->kv_scale + c->heads_kv;
+    return run_join(c, j, s);
 }
 
 int tpmlp_attn_cross_packed(const tpmlp_attend_args* a) {

@@ -45,13 +45,10 @@ struct OpenArgs {
     float scale_log2;
     float* partial;   // [CTAs][2 pieces][2 tiles] slots of kPromptSlotFloats
     uint32_t* count;  // [CTAs][2 tiles] arrivals, then items dealt and CTAs done; 0 between launches
-    // where results go instead of out, in fp32 (null: they go to out), or what they are joined with on
-    // the way to out (null: nothing)
-    float* part;     // fp32 [T][Hq][D] (split rows: their contributors' slots in `partial`)
-    RowOf* part_of;  // [T][Hq]
-    const float* other;  // these as in RowArgs
-    const RowOf* other_of;
-    const float* other_slots;
+    // where results go instead of out (null: they go to out), for join_parts_kernel: fp32 [T][Hq][D]
+    // and what they are [T][Hq]; those of split items stay in their contributors' slots of `partial`
+    float* part;
+    RowOf* part_of;
 };
 
 template <int D, bool FP8>
@@ -215,6 +212,12 @@ struct OpenWork {
     }
 };
 
+// The logs of a row's sum of weights: of its sum l by the maximum m.
+__device__ __forceinline__ float log2_of(float m, float l, bool fp8) {
+    return l == 0.0f ? -CUDART_INF_F : m + log2f(l) - (fp8 ? kRaiseLog2 : 0.0f);
+}
+__device__ __forceinline__ float natural_log(float m, float l, bool fp8) { return log2_of(m, l, fp8) * 0.69314718055994531f; }
+
 // Rows of V past the item's last key or in a page that is not there, in a group of 16 that the product
 // reads: their weights are 0, but 0 times what they hold may be NaN; they are cleared first (by both
 // tiles' warps alike).
@@ -226,57 +229,6 @@ __device__ __noinline__ void clear_rows(uint8_t* block, int in, uint32_t have, i
         if (r >= in || !((have >> (r >> 4)) & 1u))
             *reinterpret_cast<uint4*>(block + (piece >> 3) * 16384 + r * 128 + (piece & 7) * 16) = make_uint4(0, 0, 0, 0);
 }
-
-// Where a row's result goes. Its sums are scaled by `scale`, which this sets anew where the row is joined
-// with its result over other keys; add() then adds that result.
-template <int D, bool FP8>
-struct OpenRow {
-    __nv_bfloat16* out = nullptr;
-    float* lse_at = nullptr;
-    float lse = 0.0f, by = 0.0f;
-    int64_t at = 0;
-    // row, head: of Q; m, l: maximum and sum; on: there is such a row
-    __device__ __forceinline__ OpenRow(const OpenArgs& a, bool on, int64_t row, int64_t head, float m, float l,
-                                       float v_scale, float& scale) {
-        if (!on) return;
-        constexpr float kRaise = FP8 ? kRaiseLog2 : 0.0f;
-        at = row * a.Hq + head;
-        out = a.out + row * a.ldo + head * D;
-        if (a.lse) lse_at = a.lse + at;
-        if (a.other) {
-            const Joined j = join_keys(m, l, kRaise, other(a, v_scale).log);
-            scale = j.own * v_scale;
-            by = j.other;
-            lse = j.lse;
-        } else if (a.part || a.lse) {
-            lse = l == 0.0f ? -CUDART_INF_F : m + log2f(l) - kRaise;
-            if (!a.part) lse *= 0.69314718055994531f;
-        }
-    }
-    __device__ __forceinline__ OtherRow<FP8> other(const OpenArgs& a, float v_scale) const {
-        return OtherRow<FP8>(row_of(a.other_of + at), a.other_slots, a.other + at * D, v_scale);
-    }
-    // the result over the other keys, added to N columns from `col` on that are scaled already
-    template <int N>
-    __device__ __forceinline__ void add(const OpenArgs& a, float (&v)[N], int col, float v_scale) const {
-        if (!a.other || !out) return;
-        const OtherRow<FP8> x = other(a, v_scale);
-#pragma unroll
-        for (int k = 0; k < N; k += 4) {
-            float4 y = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-            x.add(y, col + k, by);
-            v[k] = y.x;
-            v[k + 1] = y.y;
-            v[k + 2] = y.z;
-            v[k + 3] = y.w;
-        }
-    }
-    __device__ __forceinline__ void put_lse(const OpenArgs& a) const {
-        if (!out) return;
-        if (a.part) a.part_of[at] = RowOf{lse, 0, 0, -1};
-        else if (lse_at) *lse_at = lse;
-    }
-};
 
 // The result of the first `count` rows of tile t of a split item, from its contributors' slots, first
 // to last. The tile's 128 threads call it (row: the thread's number), P to a row of the result, each
@@ -311,9 +263,10 @@ __device__ __forceinline__ void join_open(const OpenArgs& a, const OpenPiece& p,
         for (int u = 0; u < kJoinLoads; ++u) ll += exp2_approx(mx[u] - safe) * lx[u];
     }
     const float safe = mm == -CUDART_INF_F ? 0.0f : mm;
-    float scale = ll == 0.0f ? 0.0f : v_scale / ll;
-    const OpenRow<D, FP8> to(a, true, p.row0 + t * a.tpt + r / a.G, static_cast<int64_t>(p.h) * a.G + r % a.G, mm, ll,
-                             v_scale, scale);
+    const float scale = ll == 0.0f ? 0.0f : v_scale / ll;
+    const int64_t to = p.row0 + t * a.tpt + r / a.G;
+    const int64_t to_head = static_cast<int64_t>(p.h) * a.G + r % a.G;
+    __nv_bfloat16* const dst = a.out + to * a.ldo + to_head * D;
 #pragma unroll 1
     for (int col = part * kCols; col < (part + 1) * kCols; col += kChunk) {
         float v[kChunk];
@@ -346,17 +299,14 @@ __device__ __forceinline__ void join_open(const OpenArgs& a, const OpenPiece& p,
             }
         }
 #pragma unroll
-        for (int k = 0; k < kChunk; ++k) v[k] = ll == 0.0f ? 0.0f : v[k] * scale;
-        to.add(a, v, col, v_scale);
-#pragma unroll
         for (int k = 0; k < kChunk; k += 8) {
-            float x[8];
+            float z[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = v[k + e];
-            *reinterpret_cast<uint4*>(to.out + col + k) = pack8_bf16(x);
+            for (int e = 0; e < 8; ++e) z[e] = ll == 0.0f ? 0.0f : v[k + e] * scale;
+            *reinterpret_cast<uint4*>(dst + col + k) = pack8_bf16(z);
         }
     }
-    if (part == 0) to.put_lse(a);
+    if (a.lse && part == 0) a.lse[to * a.Hq + to_head] = natural_log(mm, ll, FP8);
 }
 
 template <int D, bool FP8>
@@ -448,8 +398,8 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
 
-    if (a.part) {
-        // rows of no sequence have no keys; whoever joins their results has to know
+    if (a.part && a.cu_q) {
+        // rows of no sequence have no keys; the kernel that joins their results has to know
         const int first = max(0, min(a.cu_q[0], a.T)), last = max(0, min(a.cu_q[a.kv.B], a.T));
         const int64_t n = (first + static_cast<int64_t>(a.T) - last) * a.Hq;
         for (int64_t i = static_cast<int64_t>(blockIdx.x) * L::kThreads + threadIdx.x; i < n;
@@ -731,8 +681,9 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             float* const slots = a.partial + static_cast<int64_t>(t) * kPromptSlotFloats;
             float* const slot = slots + (static_cast<int64_t>(blockIdx.x) * 2 + p->starts) * 2 * kPromptSlotFloats;
             const float v_scale = FP8 ? a.kv.scales[a.kv.Hkv + p->h] : 1.0f;
-            float inv = l == 0.0f ? 0.0f : v_scale / l;  // no keys: zeros
-            const OpenRow<D, FP8> to(a, mine && whole, qrow(), qhead(), m, l, v_scale, inv);
+            const float inv = l == 0.0f ? 0.0f : v_scale / l;  // no keys: zeros
+            const int64_t at = qrow() * a.Hq + qhead();
+            __nv_bfloat16* const dst = mine ? a.out + qrow() * a.ldo + qhead() * D : nullptr;
             if (any) {
                 if (!wait(o_full(t), o_phase, 3)) break;
                 o_phase ^= 1u;
@@ -743,7 +694,7 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 rows_to[k] = reinterpret_cast<__nv_bfloat16*>(
-                    __shfl_sync(~0u, reinterpret_cast<unsigned long long>(to.out), 8 * k + (lane >> 2)));
+                    __shfl_sync(~0u, reinterpret_cast<unsigned long long>(dst), 8 * k + (lane >> 2)));
 #pragma unroll 1
             for (int col = 0; col < D; col += 32) {
                 __syncwarp();
@@ -775,14 +726,13 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 for (int k = 0; k < 32; ++k) v[k] = l == 0.0f ? 0.0f : __uint_as_float(o[k]) * inv;
                 if (a.part) {
                     if (mine) {
-                        float* const dst = a.part + to.at * D + col;
+                        float* const part = a.part + at * D + col;
 #pragma unroll
                         for (int k = 0; k < 32; k += 4)
-                            *reinterpret_cast<float4*>(dst + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                            *reinterpret_cast<float4*>(part + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
                     }
                     continue;
                 }
-                to.add(a, v, col, v_scale);
                 // through shared memory, so that four lanes write 64 contiguous bytes of a row (a line of
                 // a store takes the SM a cycle, however few of its bytes are written)
 #pragma unroll
@@ -801,15 +751,14 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 }
             }
             if (whole) {
-                to.put_lse(a);
+                if (a.part && mine) a.part_of[at] = RowOf{log2_of(m, l, FP8), 0, 0, -1};
+                else if (a.lse && mine) a.lse[at] = natural_log(m, l, FP8);
             } else if (a.part) {
-                // whoever reads the rows' results sums the contributors (they are read by many CTAs; a
-                // join by the last contributor alone took 20 us of 10 contributors' sums of 256 rows)
+                // (a join by the last contributor alone took 20 us of 10 contributors' sums of 256 rows)
                 if (mine) {
                     __stcg(slot + 128 * 128 + row, m);
                     __stcg(slot + 128 * 128 + 128 + row, l);
-                    if (p->starts)
-                        a.part_of[qrow() * a.Hq + qhead()] = RowOf{0.0f, p->first, p->last, t * 128 + row};
+                    if (p->starts) a.part_of[at] = RowOf{0.0f, p->first, p->last, t * 128 + row};
                 }
             } else {
                 // The last contributor to arrive sums all of them, first to last (see the row kernel);
@@ -1133,6 +1082,105 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, 512);
     }
+}
+
+// ------------------------------------------------------------------ two parts of a row's keys
+// A row's results over two parts of its keys, with one softmax over both.
+struct JoinPartsArgs {
+    struct Side {
+        const float* part;  // as OpenArgs' part, part_of and partial
+        const RowOf* of;
+        const float* slots;
+    } side[2];
+    __nv_bfloat16* out;
+    int64_t ldo;
+    float* lse;
+    int64_t heads;  // rows * Hq
+    int32_t Hq, G;
+    const float* v_scale;  // e4m3: [Hkv]
+};
+constexpr int kJoinThreads = 128;
+
+// D / 4 lanes to a head, four columns each. Bound by latency: where the results lie, the contributors'
+// maxima and sums, their columns. MEASURED
+template <int D, bool FP8>
+__global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const __grid_constant__ JoinPartsArgs a) {
+    constexpr int kLanes = D / 4;
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / kLanes) + threadIdx.x / kLanes;
+    if (at >= a.heads) return;
+    const int d = static_cast<int>(threadIdx.x % kLanes) * 4;
+    const int64_t row = at / a.Hq;
+    const int head = static_cast<int>(at - row * a.Hq);
+    float log[2];
+    float4 o[2];
+    uint4 where[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) where[x] = load16(reinterpret_cast<const uint8_t*>(a.side[x].of + at));
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int first = static_cast<int>(where[x].y), last = static_cast<int>(where[x].z), place = static_cast<int>(where[x].w);
+        o[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        log[x] = __uint_as_float(where[x].x);
+        if (place < 0) {
+            if (log[x] != -CUDART_INF_F) o[x] = __ldcg(reinterpret_cast<const float4*>(a.side[x].part + at * D + d));
+            continue;
+        }
+        // a split row: its contributors, first to last (one pass with a running maximum)
+        const int r = place & 127;
+        const float* const slots = a.side[x].slots + static_cast<int64_t>(place >> 7) * kPromptSlotFloats;
+        float m = -CUDART_INF_F, l = 0.0f;
+        for (int c0 = first; c0 <= last; c0 += kJoinLoads) {
+            float mx[kJoinLoads], lx[kJoinLoads], top = m;
+            float4 v[kJoinLoads];
+#pragma unroll
+            for (int u = 0; u < kJoinLoads; ++u) {
+                const int c = min(c0 + u, last);
+                const float* p = slots + (static_cast<int64_t>(c) * 2 + (c == first)) * 2 * kPromptSlotFloats;
+                mx[u] = __ldcg(p + 128 * 128 + r);
+                lx[u] = __ldcg(p + 128 * 128 + 128 + r);
+                v[u] = __ldcg(reinterpret_cast<const float4*>(p + d * 128 + r * 4));
+            }
+#pragma unroll
+            for (int u = 0; u < kJoinLoads; ++u) top = fmaxf(top, mx[u]);
+            const float safe = top == -CUDART_INF_F ? 0.0f : top;
+            const float f = exp2_approx(m - safe);
+            m = top;
+            l *= f;
+            o[x] = make_float4(o[x].x * f, o[x].y * f, o[x].z * f, o[x].w * f);
+#pragma unroll
+            for (int u = 0; u < kJoinLoads; ++u) {
+                // past the last one, sums of 0 as well (see the row kernel)
+                const bool on = c0 + u <= last;
+                const float w = on ? exp2_approx(mx[u] - safe) : 0.0f;
+                l += w * lx[u];
+                o[x].x += w * (on ? v[u].x : 0.0f);
+                o[x].y += w * (on ? v[u].y : 0.0f);
+                o[x].z += w * (on ? v[u].z : 0.0f);
+                o[x].w += w * (on ? v[u].w : 0.0f);
+            }
+        }
+        const float by = l == 0.0f ? 0.0f : (FP8 ? a.v_scale[head / a.G] : 1.0f) / l;
+        o[x] = make_float4(o[x].x * by, o[x].y * by, o[x].z * by, o[x].w * by);
+        log[x] = log2_of(m, l, FP8);
+    }
+    const float top = fmaxf(log[0], log[1]), safe = top == -CUDART_INF_F ? 0.0f : top;
+    float w[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) w[x] = exp2f(log[x] - safe);
+    const float sum = w[0] + w[1], inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // no keys at all: zeros
+    // (a part without keys has no say: 0 times its result would do but for what is not finite)
+    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        if (log[x] == -CUDART_INF_F) continue;
+        const float f = w[x] * inv;
+        y = make_float4(y.x + o[x].x * f, y.y + o[x].y * f, y.z + o[x].z * f, y.w + o[x].w * f);
+    }
+    *reinterpret_cast<uint2*>(a.out + row * a.ldo + static_cast<int64_t>(head) * D + d) =
+        make_uint2(pack_bf162(y.x, y.y), pack_bf162(y.z, y.w));
+    if (a.lse && d == 0) a.lse[at] = sum == 0.0f ? -CUDART_INF_F : (top + log2f(sum)) * 0.69314718055994531f;
 }
 
 }  // namespace tpmlp
