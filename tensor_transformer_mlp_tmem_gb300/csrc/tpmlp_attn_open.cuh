@@ -27,11 +27,8 @@
 namespace tpmlp {
 
 constexpr int kOpenCode = 0x4000;  // wait sites: kOpenCode | role
-// A step's weights, with e4m3 caches raised by 2^kRaiseLog2, may sum to this much before a row's reference
-// follows its maximum: bf16 weights lose nothing up there, fp16 ones must stay below 65504.
-constexpr float kOpenMost = 0x1p14f;
 constexpr int kOpenRuns = 512;     // entries of the table of sequences
-constexpr int kOpenPieces = 4;     // pieces between the work list's warp and the others
+constexpr int kOpenPieces = 2;     // pieces between the work list's warp and the others
 
 struct OpenArgs {
     KvView kv;
@@ -582,88 +579,62 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 const uint32_t have = (groups[(block0 + (j >> 1)) & 7] >> (4 * buf)) & 0xFu;
                 ptx::tc_fence_after();
                 const uint32_t ts = tmem_s(t, buf) + lanes;
-                // 32 of the step's keys, those that are not there masked
+                uint32_t s[kSB];
+                ptx::tmem_ld_32x32b_x32(ts, *reinterpret_cast<uint32_t(*)[32]>(s));
+                ptx::tmem_ld_32x32b_x32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+                ptx::tmem_wait_ld(*reinterpret_cast<uint32_t(*)[32]>(s));
+                ptx::tmem_wait_ld(*reinterpret_cast<uint32_t(*)[32]>(s + 32));
                 const int below = len - j * kSB;
-                const bool cut = below < kSB || have != 0xFu;
-                auto loaded = [&](int half, uint32_t (&s)[32]) {
-                    ptx::tmem_wait_ld(s);
-                    if (cut) {
+                if (below < kSB || have != 0xFu) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            s[k] = 32 * half + k < below && ((have >> (2 * half + (k >> 4))) & 1u) ? s[k] : 0xFF800000u;
+                    for (int k = 0; k < kSB; ++k) s[k] = k < below && ((have >> (k >> 4)) & 1u) ? s[k] : 0xFF800000u;
+                }
+                float top[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    top[x] = __uint_as_float(s[x]);
+#pragma unroll
+                    for (int k = 4; k < kSB - 4; k += 8)
+                        top[x] = max3(top[x], __uint_as_float(s[k + x]), __uint_as_float(s[k + 4 + x]));
+                    top[x] = fmaxf(top[x], __uint_as_float(s[kSB - 4 + x]));
+                }
+                const float now = fmaxf(max3(top[0], top[1], top[2]), top[3]) * c;
+                const bool move = now > m + kLazyLog2;
+                if (__any_sync(~0u, move)) {
+                    const float f = move ? exp2_approx(m - now) : 1.0f;
+                    if (move) m = now;
+                    l *= f;
+                    // O of the steps before is scaled, once the last of their products is done
+                    if (j > begin) {
+                        if (!(ok = wait(pv_done(t), (pv_count - 1) & 1u, 17))) break;
+                        ptx::tc_fence_after();
+#pragma unroll 1
+                        for (int x = 0; x < D; x += 32) {
+                            uint32_t o[32];
+                            ptx::tmem_ld_32x32b_x32(tmem_o(t) + lanes + x, o);
+                            ptx::tmem_wait_ld(o);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                            tmem_st_x32(tmem_o(t) + lanes + x, o);
+                        }
                     }
-                };
+                }
+                ++pv_count;
                 // P = 2^(S c - m), two values to an instruction where there is one; rounded to 16 bits for
                 // the product with V, of V's type (both operands of these instructions have one type):
-                // half a step of a weight is 2^-8 of it in bf16, 2^-11 in fp16; its sum is taken before.
-                // The reference m is the maximum of the first step, and stays while a step's weights sum
-                // to no more than kOpenMost: there is no need to look for a step's maximum then. Where they
-                // do, or the row has met no key yet, the reference becomes the maximum so far, and P is made
-                // again. (A weight's relative error does not depend on the reference.)
-                bool look = j == begin;
+                // half a step of a weight is 2^-8 of it in bf16, 2^-11 in fp16; its sum is taken before
+                const float shift = (FP8 ? kRaiseLog2 : 0.0f) - (m == -CUDART_INF_F ? 0.0f : m);
+                const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
+                float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                 uint32_t w[32];
-                float2 sum[2];
-#pragma unroll 1
-                for (;;) {
-                    uint32_t s[32];
-                    if (look) {
-                        float top[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-#pragma unroll 1
-                        for (int half = 0; half < 2; ++half) {
-                            ptx::tmem_ld_32x32b_x32(ts + 32 * half, s);
-                            loaded(half, s);
 #pragma unroll
-                            for (int k = 0; k < 32; k += 8)
-#pragma unroll
-                                for (int x = 0; x < 4; ++x)
-                                    top[x] = max3(top[x], __uint_as_float(s[k + x]), __uint_as_float(s[k + 4 + x]));
-                        }
-                        const float now = fmaxf(max3(top[0], top[1], top[2]), top[3]) * c;
-                        const float f = now > m ? exp2_approx(m - now) : 1.0f;
-                        if (now > m) m = now;
-                        l *= f;
-                        // O of the steps before is scaled, once the last of their products is done
-                        if (j > begin) {
-                            if (!(ok = wait(pv_done(t), (pv_count - 1) & 1u, 17))) break;
-                            ptx::tc_fence_after();
-#pragma unroll 1
-                            for (int x = 0; x < D; x += 16) {
-                                uint32_t o[16];
-                                ptx::tmem_ld_32x32b_x16_wait(tmem_o(t) + lanes + x, o);
-#pragma unroll
-                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                                ptx::tmem_st_32x32b_x16_wait(tmem_o(t) + lanes + x, o);
-                            }
-                        }
-                    }
-                    const float shift = (FP8 ? kRaiseLog2 : 0.0f) - (m == -CUDART_INF_F ? 0.0f : m);
-                    const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
-                    sum[0] = sum[1] = make_float2(0.0f, 0.0f);
-                    auto weights = [&](int half) {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            float2 e = fma2(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), c2, shift2);
-                            e.x = exp2_approx(e.x);
-                            e.y = exp2_approx(e.y);
-                            sum[k & 1] = add2(sum[k & 1], e);
-                            w[16 * half + k] = FP8 ? pack_half2(e.x, e.y) : pack_bf162(e.x, e.y);
-                        }
-                    };
-                    uint32_t s1[32];
-                    ptx::tmem_ld_32x32b_x32(ts, s);
-                    loaded(0, s);
-                    ptx::tmem_ld_32x32b_x32(ts + 32, s1);
-                    weights(0);
-                    loaded(1, s1);
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) s[k] = s1[k];
-                    weights(1);
-                    const float step = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                    if (look || !__any_sync(~0u, mine && (!(step <= kOpenMost) || m == -CUDART_INF_F))) break;
-                    look = true;
+                for (int k = 0; k < 32; ++k) {
+                    float2 e = fma2(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), c2, shift2);
+                    e.x = exp2_approx(e.x);
+                    e.y = exp2_approx(e.y);
+                    sum[k & 1] = add2(sum[k & 1], e);
+                    w[k] = FP8 ? pack_half2(e.x, e.y) : pack_bf162(e.x, e.y);
                 }
-                if (!ok) break;
-                ++pv_count;
                 tmem_st_x32(ts, w);
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 tmem_wait_st();
