@@ -73,7 +73,7 @@ struct OpenShape {
     static constexpr uint32_t kUp = kPieces0 + kOpenPieces * 64;  // [2 tiles][128] fp32, e4m3
     static constexpr uint32_t kStore0 = (kUp + (FP8 ? 2 * 128 * 4 : 0) + 127) / 128 * 128;
     static constexpr uint32_t kTables = kStore0 + 8 * 2048;  // 2 KB of output staging per softmax warp
-    static constexpr uint32_t kTotal = 1024 + kTables + 2 * (kOpenRuns + 1) * 8 + 64;
+    static constexpr uint32_t kTotal = 1024 + kTables + 2 * kOpenRuns * 4 + 64;
     static_assert(kTotal <= 232448, "dynamic shared memory per CTA");
     static_assert(kStages / 2 + 1 < 8, "blocks in flight, against the ring of loaded groups");
 };
@@ -108,24 +108,25 @@ struct OpenPiece {
 static_assert(sizeof(OpenPiece) <= 64, "piece slots");
 
 // The CTA's work list. A sequence's items are numbered by kv head and then by tile, so that those that
-// share keys are at work together. An item's work is a unit for its start and its blocks.
+// share keys are at work together. An item's work is a unit for its start and its blocks. The numbers of
+// items and of split lists' units stay below 2^31 (32-bit divisions: a first piece 5000 cycles earlier).
 struct OpenWork {
-    const int64_t *items_at, *units_at;  // items and work before each run of `run` sequences
+    const uint32_t *items_at, *units_at;  // items and work before each run of `run` sequences
     int runs, run;
-    int64_t items;
+    uint32_t items;
     bool split;            // equal runs of work instead of whole items
     bool dealt;            // whole items: this CTA has had its first
-    int64_t at, end, per;  // split: this CTA's run of work, the length of every run
+    uint32_t at, end, per;  // split: this CTA's run of work, the length of every run
 
-    __device__ __forceinline__ static int64_t tiles(const OpenArgs& a, const OpenSeq& s) {
-        return (s.n + 2ll * a.tpt - 1) / (2 * a.tpt);
+    __device__ __forceinline__ static uint32_t tiles(const OpenArgs& a, const OpenSeq& s) {
+        return (static_cast<uint32_t>(s.n) + 2u * a.tpt - 1u) / (2u * a.tpt);
     }
-    __device__ __forceinline__ static int64_t blocks(const OpenSeq& s) { return (s.len + int64_t(kPB) - 1) / kPB; }
+    __device__ __forceinline__ static uint32_t blocks(const OpenSeq& s) { return (static_cast<uint32_t>(s.len) + kPB - 1u) / kPB; }
 
     // The sequence of the k-th item (UNITS: unit); k becomes its number within the sequence.
     template <bool UNITS>
-    __device__ __forceinline__ int locate(const OpenArgs& a, int64_t& k, OpenSeq& s) const {
-        const int64_t* const table = UNITS ? units_at : items_at;
+    __device__ __forceinline__ int locate(const OpenArgs& a, uint32_t& k, OpenSeq& s) const {
+        const uint32_t* const table = UNITS ? units_at : items_at;
         int lo = 0, hi = runs;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -136,26 +137,18 @@ struct OpenWork {
         int b = lo * run;
         s = open_seq(a, b);
         while (b + 1 < a.kv.B) {
-            const int64_t n = tiles(a, s) * a.kv.Hkv * (UNITS ? 1 + blocks(s) : 1);
+            const uint32_t n = tiles(a, s) * a.kv.Hkv * (UNITS ? 1 + blocks(s) : 1);
             if (k < n) break;
             k -= n;
             s = open_seq(a, ++b);
         }
         return b;
     }
-    __device__ __forceinline__ static void item(const OpenArgs& a, int b, const OpenSeq& s, int64_t k, OpenPiece& p) {
-        const uint32_t nt = max(1u, static_cast<uint32_t>(tiles(a, s)));
-        uint32_t h, j;
-        if (k <= 0xFFFFFFFFll) {
-            h = static_cast<uint32_t>(k) / nt;
-            j = static_cast<uint32_t>(k) - h * nt;
-        } else {
-            h = static_cast<uint32_t>(k / nt);
-            j = static_cast<uint32_t>(k % nt);
-        }
+    __device__ __forceinline__ static void item(const OpenArgs& a, int b, const OpenSeq& s, uint32_t k, OpenPiece& p) {
+        const uint32_t nt = max(1u, tiles(a, s)), h = k / nt, j = k - h * nt;
         p.valid = 1;
         p.b = b;
-        p.h = min(static_cast<int>(h), a.kv.Hkv - 1);
+        p.h = static_cast<int>(min(h, static_cast<uint32_t>(a.kv.Hkv - 1)));
         p.len = s.len;
         const int tok0 = static_cast<int>(j) * 2 * a.tpt;
         p.row0 = s.first + tok0;
@@ -179,17 +172,15 @@ struct OpenWork {
                 k = __shfl_sync(~0u, k, 0);
             }
             dealt = true;
-            int64_t r = k;
-            if (r >= items) return p;
-            const int b = locate<false>(a, r, s);
-            item(a, b, s, r, p);
+            if (k >= items) return p;
+            const int b = locate<false>(a, k, s);
+            item(a, b, s, k, p);
             return p;
         }
         while (at < end) {
-            int64_t r = at;
+            uint32_t r = at;
             const int b = locate<true>(a, r, s);
-            const int64_t each = 1 + blocks(s);
-            const int64_t k = r / each, u0 = at - (r - k * each), u1 = u0 + each;
+            const uint32_t each = 1 + blocks(s), k = r / each, u0 = at - (r - k * each), u1 = u0 + each;
             item(a, b, s, k, p);
             const int from = max(static_cast<int>(at - u0) - 1, 0);
             at = min(end, u1);
@@ -346,9 +337,9 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     auto piece_of = [&](uint32_t k) {
         return reinterpret_cast<const OpenPiece*>(base_ptr + L::kPieces0 + (k % kOpenPieces) * 64);
     };
-    int64_t* const items_at = reinterpret_cast<int64_t*>(base_ptr + L::kTables);
-    int64_t* const units_at = items_at + kOpenRuns + 1;
-    int64_t* const found = units_at + kOpenRuns + 1;  // items, units, longest item
+    uint32_t* const items_at = reinterpret_cast<uint32_t*>(base_ptr + L::kTables);
+    uint32_t* const units_at = items_at + kOpenRuns;
+    uint32_t* const found = units_at + kOpenRuns;  // items, units (at most 2^31), longest item
 
     const int warp = __shfl_sync(~0u, static_cast<int>(threadIdx.x) >> 5, 0);
     const int lane = threadIdx.x & 31;
@@ -413,40 +404,42 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     work.runs = (a.kv.B + work.run - 1) / work.run;
     if (threadIdx.x == 0) found[2] = 0;
     __syncthreads();
+    constexpr uint32_t kMost = 1u << 31;
     for (int e = threadIdx.x; e < work.runs; e += L::kThreads) {
-        int64_t items = 0, units = 0;
-        int most = 0;
+        uint64_t items = 0, units = 0;
+        uint32_t most = 0;
         for (int b = e * work.run; b < min(a.kv.B, (e + 1) * work.run); ++b) {
             const OpenSeq s = open_seq(a, b);
-            const int64_t n = OpenWork::tiles(a, s) * a.kv.Hkv, each = 1 + OpenWork::blocks(s);
+            const uint64_t n = static_cast<uint64_t>(OpenWork::tiles(a, s)) * a.kv.Hkv;
+            const uint32_t each = 1 + OpenWork::blocks(s);
             items += n;
             units += n * each;
-            if (n) most = max(most, static_cast<int>(each));
+            if (n) most = max(most, each);
         }
-        items_at[e] = items;
-        units_at[e] = units;
-        atomicMax(reinterpret_cast<int*>(found + 2), most);
+        items_at[e] = static_cast<uint32_t>(min(items, static_cast<uint64_t>(kMost)));
+        units_at[e] = static_cast<uint32_t>(min(units, static_cast<uint64_t>(kMost)));
+        if (most) atomicMax(found + 2, most);
     }
     __syncthreads();
     if (warp < 2) {
         // running sums, a table to a warp
-        int64_t* const table = warp ? units_at : items_at;
+        uint32_t* const table = warp ? units_at : items_at;
         const int each = (work.runs + 31) / 32;
-        int64_t sum = 0;
+        uint64_t sum = 0;
         for (int i = 0; i < each; ++i)
             if (lane * each + i < work.runs) sum += table[lane * each + i];
-        int64_t before = sum;
+        uint64_t before = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(~0u, before, o);
+            const uint64_t v = __shfl_up_sync(~0u, before, o);
             if (lane >= o) before += v;
         }
-        if (lane == 31) found[warp] = before;
+        if (lane == 31) found[warp] = static_cast<uint32_t>(min(before, static_cast<uint64_t>(kMost)));
         before -= sum;
         for (int i = 0; i < each; ++i)
             if (lane * each + i < work.runs) {
-                const int64_t n = table[lane * each + i];
-                table[lane * each + i] = before;
+                const uint32_t n = table[lane * each + i];
+                table[lane * each + i] = static_cast<uint32_t>(min(before, static_cast<uint64_t>(kMost)));
                 before += n;
             }
     }
@@ -463,16 +456,15 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         // kJoinFew blocks of time where there is no more than an item for a CTA, kJoinMany where there
         // are more (every CTA then has two pieces to hand over, and what was dealt would have filled
         // the gaps).
-        constexpr int kJoinFew = 8, kJoinMany = 16;
-        const int64_t total = found[1], g = gridDim.x;
-        const int64_t most = *reinterpret_cast<const int*>(found + 2);
-        const int64_t share = max((total + g - 1) / g, int64_t(1));
-        const int64_t whole = work.items <= g ? most : share + most / 2;
-        const int join = work.items <= g ? kJoinFew : kJoinMany;
-        if (10 * whole > 11 * (share + join)) {
+        constexpr uint32_t kJoinFew = 8, kJoinMany = 16;
+        const uint32_t total = found[1], g = gridDim.x, most = found[2];
+        const uint32_t share = max((total + g - 1) / g, 1u);
+        const uint32_t whole = work.items <= g ? most : share + most / 2;
+        const uint32_t join = work.items <= g ? kJoinFew : kJoinMany;
+        if (total < kMost && 10ull * whole > 11ull * (share + join)) {
             work.split = true;
             work.per = share;
-            work.at = share * blockIdx.x;
+            work.at = min(share * blockIdx.x, total);
             work.end = min(work.at + share, total);
         }
     }
@@ -524,10 +516,10 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 if (b1 > b0) {
                     if (tokens > 0) {
                         // Q in fp16, scaled (query_exponent). A row's D / 8 lanes load 16 bytes each,
-                        // neighbours side by side, up to 8 loads in flight (a thread to a row, 16 bytes of
+                        // neighbours side by side, all in flight together (a thread to a row, 16 bytes of
                         // 32 rows to a load: 7 us for 256 rows of 128). The factor that the row was
                         // divided by goes to the thread that has the row.
-                        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kSteps = 32 / kAtOnce, kLoads = 8;
+                        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kSteps = 32 / kAtOnce, kLoads = kSteps;
                         float* const up = reinterpret_cast<float*>(base_ptr + L::kUp) + t * 128;
                         const __nv_bfloat16* mine_at = mine ? a.q + qrow() * a.ldq + qhead() * D : nullptr;
                         if (!wait(q_empty, q_empty_phase ^ 1u, 1, kPieceWaitNs)) break;
