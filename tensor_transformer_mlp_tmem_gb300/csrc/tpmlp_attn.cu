@@ -58,7 +58,7 @@ int64_t append_tokens(const tpmlp_ctx* c, int64_t units, int64_t T) {
     return std::max<int64_t>(1, std::min({hold, fill, static_cast<int64_t>(kAppendTokens)}));
 }
 
-template <int D, bool FP8, bool NORM>
+template <int D, bool FP8, int NORM>
 int launch_append(tpmlp_ctx* c, const AppendArgs& a, cudaStream_t s) {
     if (a.tokens > 1)
         return launch(c, append_kernel<D, FP8, true, NORM>, (a.T + int64_t(a.tokens) - 1) / a.tokens,
@@ -68,7 +68,8 @@ int launch_append(tpmlp_ctx* c, const AppendArgs& a, cudaStream_t s) {
 
 template <int D, bool FP8>
 int run_append(tpmlp_ctx* c, const AppendArgs& a, cudaStream_t s) {
-    return c->norm_on ? launch_append<D, FP8, true>(c, a, s) : launch_append<D, FP8, false>(c, a, s);
+    if (!c->norm_on) return launch_append<D, FP8, kNormNone>(c, a, s);
+    return c->norm_per_head ? launch_append<D, FP8, kNormHeads>(c, a, s) : launch_append<D, FP8, kNormShared>(c, a, s);
 }
 
 }  // namespace
@@ -230,7 +231,6 @@ int tpmlp_attn_append(tpmlp_ctx* c, const void* Q, int64_t ldq, const void* K, i
         a.parts = static_cast<int32_t>((units + a.part_units - 1) / a.part_units);
         a.wq = reinterpret_cast<const __nv_bfloat16*>(c->norm_w);
         a.wk = a.wq + static_cast<int64_t>(c->heads_q) * c->head_dim;
-        a.w_stride = c->norm_per_head ? c->head_dim : 0;
         a.eps = c->norm_eps;
     }
     a.T = static_cast<int32_t>(T);

@@ -81,12 +81,12 @@ struct AppendArgs {
     int32_t tokens;     // tokens per block (more than one: parts is 1)
     uint32_t per_unit;  // 2^32 / units of a token, rounded up
     double turns[64];   // whole turns per position of each pair
-    // norms of query and key heads (NORM): weights, elements from head to head (0: all heads share
-    // them), what is added to the mean square
-    const __nv_bfloat16 *wq, *wk;
-    int64_t w_stride;
-    float eps;
+    const __nv_bfloat16 *wq, *wk;  // norms: weights of query and key heads
+    float eps;                     // what is added to the mean square
 };
+// Norms of an append: none, with weights that all heads share (a block keeps them in shared memory),
+// with a weight for every head.
+constexpr int kNormNone = 0, kNormShared = 1, kNormHeads = 2;
 
 // Loads of what another kernel of the stream may have just written: through L2 (the read-only
 // path must not be used while this kernel may overlap the writer's end).
@@ -182,11 +182,12 @@ __device__ __forceinline__ void norm_head(float (&x0)[8], float (&x1)[8], const 
 // write neighbouring 16 bytes; where halves are rotated they are the partners. Bound by DRAM: 16384
 // tokens of 32 query and 8 kv heads of 128 in 67 us, 6.0 TB/s, 89 % of a copy's rate (256 threads a
 // block, each loading a unit when it had the sines: 87 us).
-template <int D, bool FP8, bool MANY, bool NORM>
+template <int D, bool FP8, bool MANY, int NORM>
 __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) append_kernel(const __grid_constant__ AppendArgs a) {
     constexpr int kTokens = MANY ? kAppendTokens : 1;
     __shared__ float2 trig[kTokens * (D / 2)];
     __shared__ int2 places[kTokens];  // MANY: position and page of each token
+    __shared__ uint4 weights[NORM == kNormShared ? 2 * D / 8 : 1];  // of queries, then of keys
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     constexpr int kUnits = D / 16;  // units per head
@@ -236,6 +237,8 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) append_kernel(c
         }
         if (first == begin) {
             if (!MANY && pos < 0) return;
+            if (NORM == kNormShared && threadIdx.x < 2 * D / 8)
+                weights[threadIdx.x] = reinterpret_cast<const uint4*>(threadIdx.x < D / 8 ? a.wq : a.wk)[threadIdx.x % (D / 8)];
             // the table's entry, asked for before the sines of many tokens and after those of one
             // (16384 tokens of 12 + 12 heads of 64: 30 against 35 us; of 32 + 8 heads of 128: 70 against 67)
             auto look_up = [&] {
@@ -272,9 +275,15 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) append_kernel(c
             float x0[8], x1[8];
             unpack8(raw[y][0], x0);
             unpack8(raw[y][1], x1);
-            if constexpr (NORM) {
+            if constexpr (NORM == kNormShared) {
                 if (w.kind != 2) {
-                    const __nv_bfloat16* const weight = (w.kind == 0 ? a.wq : a.wk) + w.h * a.w_stride;
+                    const uint4* const weight = weights + w.kind * (D / 8);
+                    norm_head<D>(x0, x1, weight[w.d0 / 8], weight[w.d1 / 8], a.eps);
+                }
+            }
+            if constexpr (NORM == kNormHeads) {
+                if (w.kind != 2) {
+                    const __nv_bfloat16* const weight = (w.kind == 0 ? a.wq : a.wk) + w.h * D;
                     norm_head<D>(x0, x1, *reinterpret_cast<const uint4*>(weight + w.d0),
                                  *reinterpret_cast<const uint4*>(weight + w.d1), a.eps);
                 }
