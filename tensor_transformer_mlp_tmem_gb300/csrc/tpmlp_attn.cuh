@@ -380,12 +380,12 @@ struct RowArgs {
 //   D = 64, e4m3:  G = 16: 77, 194; 17: 125, 191; 32: 129, 191; from G = 33 on three times and more
 constexpr int row_heads(int D, bool fp8) { return D == 128 ? (fp8 ? 16 : 8) : (fp8 ? 32 : 16); }
 
-constexpr int kRowWarps = 8;
+// Warps of a block.
+constexpr int row_warps(bool part) { return part ? 4 : 8; }
 // A segment's fixed time (its start, merge and result) in steps, as it counts in the CTAs' shares. 0, 1,
 // 2, 3: 64 sequences of 8192 keys at most x 32 heads 617, 590, 591, 595 us; 48 sequences in e4m3, 12
 // heads to a kv head 118, 104, 100, 101; one sequence of 131072 keys 88, 87, 85, 88.
-constexpr int kSegmentStart = 2;
-constexpr int kRowThreads = 32 * kRowWarps;
+constexpr int segment_start_steps(bool) { return 2; }
 // e4m3 caches: fp16 weights are raised by 2^10, so that the small ones of a long cache stay clear of
 // fp16's smallest steps; it cancels against the sum.
 constexpr float kRowRaise = 10.0f;
@@ -469,20 +469,21 @@ __device__ __forceinline__ RowRange row_range(const RowArgs& a, int b) {
 // free (591 against 690 us; 12 heads to a kv head in e4m3 100 against 101). A warp holds NT = 1 or 2 blocks of
 // 8 query heads (2: one CTA an SM). e4m3 values are converted to fp16 in registers (the 8-bit forms
 // of these matrix instructions take three times as long as the fp16 ones on this GPU).
-template <int D, bool FP8, int NT>
+template <int D, bool FP8, int NT, int W>
 struct RowShape {
+    static constexpr int kWarps = W, kThreads = 32 * W;
     static constexpr int kElem = FP8 ? 1 : 2;
     static constexpr int kSub = 256 / (D * kElem);   // subtiles of 16 keys
     static constexpr int KT = 16 * kSub;
-    static constexpr int kStep = KT * kRowWarps;     // keys of a CTA's step
+    static constexpr int kStep = KT * W;     // keys of a CTA's step
     static constexpr int kRows = 8 * NT;             // query heads
-    static constexpr int kCtasPerSm = NT == 1 ? 2 : 1;
+    static constexpr int kCtasPerSm = (NT == 1 ? 16 : 8) / W;
     static constexpr int NK = D * kElem / 64;        // 16-byte pieces of a K row per thread
     static constexpr int NV = D / 8;                 // V dimensions per thread
     static constexpr int kVPieces = NV * kElem >= 16 ? NV * kElem / 16 : 1;  // 16-byte pieces of a V row
     static constexpr int kQRegs = D / 8;             // Q registers of 8 query heads
     static constexpr int kPitch = D + 4;             // fp32 row of the merge buffer
-    static constexpr int kSmem = kRowWarps * 8 * NT * (kPitch + 2) * 4;
+    static constexpr int kSmem = W * 8 * NT * (kPitch + 2) * 4;
 };
 
 // The dimension that element e of lane group g's V registers stands for.
@@ -493,18 +494,19 @@ __device__ __forceinline__ int v_dim(int g, int e) {
 }
 
 // PART: results go to a.part in fp32, for a launch after this one. The launch before reads and writes
-// nothing that this one does (counters that it uses lie behind this kernel's), and let this one start only
+// nothing that this one does, and let this one start only
 // when everything before itself was done; so this kernel waits for it at its own end alone, for the launch
 // after it to find both complete.
 template <int D, bool FP8, int NT, int PASSES, bool PART>
-__global__ void __launch_bounds__(kRowThreads, RowShape<D, FP8, NT>::kCtasPerSm)
+__global__ void __launch_bounds__(32 * row_warps(PART), RowShape<D, FP8, NT, row_warps(PART)>::kCtasPerSm)
 attn_row_kernel(const __grid_constant__ RowArgs a) {
-    using S = RowShape<D, FP8, NT>;
+    using S = RowShape<D, FP8, NT, row_warps(PART)>;
+    constexpr int kSegmentStart = segment_start_steps(PART);
     extern __shared__ __align__(16) float smem[];  // (read and written in float4)
     float* const sO = smem;                                       // [parts][rows][pitch]
-    float* const sM = sO + kRowWarps * S::kRows * S::kPitch;      // [parts][rows]
-    float* const sL = sM + kRowWarps * S::kRows;                  // [parts][rows]
-    __shared__ int64_t s_scan[kRowWarps + 1];
+    float* const sM = sO + S::kWarps * S::kRows * S::kPitch;      // [parts][rows]
+    float* const sL = sM + S::kWarps * S::kRows;                  // [parts][rows]
+    __shared__ int64_t s_scan[S::kWarps + 1];
     __shared__ int64_t s_found[2];
     __shared__ uint32_t s_last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -545,18 +547,18 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         row_start = __shfl_sync(~0u, sum - c, row) * per_row;
     } else {
         int64_t mine = 0;
-        for (int r = tid; r < a.rows; r += kRowThreads) mine += kSegmentStart + steps_of(row_range(a, r));
+        for (int r = tid; r < a.rows; r += S::kThreads) mine += kSegmentStart + steps_of(row_range(a, r));
 #pragma unroll
         for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(~0u, mine, o);
         if (lane == 0) s_scan[warp] = mine;
         __syncthreads();
         int64_t total = 0;
 #pragma unroll
-        for (int w = 0; w < kRowWarps; ++w) total += s_scan[w];
+        for (int w = 0; w < S::kWarps; ++w) total += s_scan[w];
         share(total * per_row);
         if (at >= end) return leave();
         int64_t before = 0;
-        for (int r0 = 0; r0 < a.rows; r0 += kRowThreads) {
+        for (int r0 = 0; r0 < a.rows; r0 += S::kThreads) {
             const int r = r0 + tid;
             const int64_t c = r < a.rows ? kSegmentStart + steps_of(row_range(a, r)) : 0;
             int64_t sum = c;
@@ -576,7 +578,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
                 s_found[0] = r;
                 s_found[1] = first;
             }
-            for (int w = 0; w < kRowWarps; ++w) before += s_scan[w];
+            for (int w = 0; w < S::kWarps; ++w) before += s_scan[w];
             __syncthreads();
             if (s_found[0] >= 0) break;
         }
@@ -664,7 +666,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         const int64_t head_off = h * a.kv.head_bytes;
         const int lo16 = range.lo & ~15;
         for (int it = 0; it < n; ++it) {
-            const int key0 = lo16 + ((step0 + it) * kRowWarps + warp) * S::KT;
+            const int key0 = lo16 + ((step0 + it) * S::kWarps + warp) * S::KT;
             if (key0 >= range.hi) break;  // the warp's keys only grow
             int page[S::kSub];
             bool ok[S::kSub];
@@ -891,16 +893,16 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
                     ll == 0.0f ? -CUDART_INF_F
                                : (mm + log2f(ll) - (FP8 ? kRowRaise : 0.0f)) * 0.69314718055994531f;
         };
-        for (int i = tid; i < heads() * (D / 4); i += kRowThreads) {
+        for (int i = tid; i < heads() * (D / 4); i += S::kThreads) {
             const int r = i / (D / 4), d = (i % (D / 4)) * 4;
             float mm = -CUDART_INF_F;
 #pragma unroll
-            for (int w = 0; w < kRowWarps; ++w) mm = fmaxf(mm, sM[w * S::kRows + r]);
+            for (int w = 0; w < S::kWarps; ++w) mm = fmaxf(mm, sM[w * S::kRows + r]);
             const float safe = mm == -CUDART_INF_F ? 0.0f : mm;
             float ll = 0.0f;
             float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-            for (int w = 0; w < kRowWarps; ++w) {
+            for (int w = 0; w < S::kWarps; ++w) {
                 const float f = exp2_approx(sM[w * S::kRows + r] - safe);
                 const float4 x = *reinterpret_cast<const float4*>(sO + (w * S::kRows + r) * S::kPitch + d);
                 ll += f * sL[w * S::kRows + r];
@@ -929,7 +931,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
             if (s_last) {
                 __threadfence();
                 if (tid == 0) a.count[first] = 0;
-                for (int i = tid; i < heads() * (D / 4); i += kRowThreads) {
+                for (int i = tid; i < heads() * (D / 4); i += S::kThreads) {
                     const int r = i / (D / 4), d = (i % (D / 4)) * 4;
                     // (one pass with a running maximum, the loads of eight contributors in flight)
                     float mm = -CUDART_INF_F, ll = 0.0f;

@@ -119,7 +119,7 @@ int allow_smem(tpmlp_ctx* c, Kernel kern, uint32_t smem, std::atomic<uint64_t>& 
 
 template <int D, bool FP8, int NT, int PASSES, bool PART>
 int launch_rows(tpmlp_ctx* c, const RowArgs& a, cudaStream_t s) {
-    using S = RowShape<D, FP8, NT>;
+    using S = RowShape<D, FP8, NT, row_warps(PART)>;
     auto kern = attn_row_kernel<D, FP8, NT, PASSES, PART>;
     static std::atomic<uint64_t> done{0};
     // Loads in flight lie in what shared memory leaves of an SM's 256 KB. Without this an SM keeps the split
@@ -128,7 +128,7 @@ int launch_rows(tpmlp_ctx* c, const RowArgs& a, cudaStream_t s) {
     constexpr int kCarveout = static_cast<int>((S::kCtasPerSm * (S::kSmem + 2048) * 100 + 233471) / 233472);
     if (int rc = allow_smem(c, kern, S::kSmem, done, kCarveout)) return rc;
     const int grid = c->num_sms * S::kCtasPerSm;
-    return launch(c, kern, grid, kRowThreads, S::kSmem, s, a);
+    return launch(c, kern, grid, S::kThreads, S::kSmem, s, a);
 }
 
 template <int D, bool FP8, bool PART>

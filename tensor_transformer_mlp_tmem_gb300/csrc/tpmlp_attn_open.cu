@@ -74,17 +74,36 @@ SharedPart shared_part(const tpmlp_ctx* c, int which) {
     return {reinterpret_cast<float*>(p), reinterpret_cast<RowOf*>(reinterpret_cast<float*>(p) + values)};
 }
 
+// Clears new memory, before any stream's work may meet it (streams made without blocking do not wait for
+// the default stream, where this runs); frees it if that fails.
+int clear_new(tpmlp_ctx* c, void* p, size_t bytes) {
+    cudaError_t e = cudaMemset(p, 0, bytes);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
+    if (e == cudaSuccess) return TPMLP_OK;
+    cudaFree(p);
+    return fail_cuda(c, e, "clearing the workspace of decode_shared");
+}
+
 // It holds `rows` sequences (s: the stream that a call is on; null: tpmlp_attn_reserve).
 int reserve_shared(tpmlp_ctx* c, int64_t rows, const cudaStream_t* s) {
     if (rows <= c->shared_rows) return TPMLP_OK;
     if (s)
         if (int rc = refuse_allocation(c, *s, "tpmlp_attn_reserve before the capture")) return rc;
-    if (!c->tail_partial)
-        if (int rc = allocate(c, reinterpret_cast<void**>(&c->tail_partial), c->attn_partial_floats * sizeof(float)))
-            return rc;
+    if (!c->tail_partial) {
+        // two slots and a counter to a CTA of either kernel (the open kernel's counters are the context's)
+        const size_t ctas = static_cast<size_t>(c->num_sms) * 16 / row_warps(true);
+        const size_t floats = std::max(c->attn_partial_floats, ctas * 2 * kRowSlotFloats);
+        void* p = nullptr;
+        if (int rc = allocate(c, &p, floats * sizeof(float) + ctas * sizeof(uint32_t))) return rc;
+        uint32_t* const count = reinterpret_cast<uint32_t*>(static_cast<float*>(p) + floats);
+        if (int rc = clear_new(c, p, floats * sizeof(float) + ctas * sizeof(uint32_t))) return rc;
+        c->tail_partial = static_cast<float*>(p);
+        c->tail_count = count;
+    }
     const int64_t now = std::max(rows, 2 * c->shared_rows);
     void* p = nullptr;
     if (int rc = allocate(c, &p, 2 * part_bytes(c, now))) return rc;
+    if (int rc = clear_new(c, p, 2 * part_bytes(c, now))) return rc;
     c->shared[c->shared_n++] = static_cast<float*>(p);
     c->shared_rows = now;
     return TPMLP_OK;
@@ -137,6 +156,7 @@ int tpmlp_attn_decode_shared(tpmlp_ctx* c, const void* Q, int64_t ldq, const tpm
     a.part = own.part;
     a.part_of = own.of;
     const bool wide = a.G > row_heads(c->head_dim, is_e4m3(c));
+    if (!wide) a.count = c->tail_count;
     if (int rc = wide ? run_open(c, a, nullptr, kv->B, s, own.part, own.of) : run_rows<true>(c, a, s)) return rc;
     JoinPartsArgs j{};
     j.side[0] = {common.part, common.of, c->attn_partial};
@@ -147,6 +167,7 @@ int tpmlp_attn_decode_shared(tpmlp_ctx* c, const void* Q, int64_t ldq, const tpm
     j.heads = static_cast<int64_t>(kv->B) * c->heads_q;
     j.Hq = c->heads_q;
     j.G = a.G;
+    j.ctas = c->num_sms;
     j.v_scale = c->kv_scale + c->heads_kv;
     return run_join(c, j, s);
 }

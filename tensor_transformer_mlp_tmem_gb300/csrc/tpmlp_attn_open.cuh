@@ -123,7 +123,8 @@ struct OpenWork {
     }
     __device__ __forceinline__ static uint32_t blocks(const OpenSeq& s) { return (static_cast<uint32_t>(s.len) + kPB - 1u) / kPB; }
 
-    // The sequence of the k-th item (UNITS: unit); k becomes its number within the sequence.
+    // The sequence of the k-th item (UNITS: unit); k becomes its number within the sequence. For a whole
+    // warp.
     template <bool UNITS>
     __device__ __forceinline__ int locate(const OpenArgs& a, uint32_t& k, OpenSeq& s) const {
         const uint32_t* const table = UNITS ? units_at : items_at;
@@ -134,15 +135,31 @@ struct OpenWork {
             else hi = mid;
         }
         k -= table[lo];
-        int b = lo * run;
-        s = open_seq(a, b);
-        while (b + 1 < a.kv.B) {
-            const uint32_t n = tiles(a, s) * a.kv.Hkv * (UNITS ? 1 + blocks(s) : 1);
-            if (k < n) break;
-            k -= n;
-            s = open_seq(a, ++b);
+        // within the run, 32 sequences at a time
+        const int lane = threadIdx.x & 31, upto = min(a.kv.B, (lo + 1) * run);
+        for (int b0 = lo * run;; b0 += 32) {
+            OpenSeq mine{0, 0, 0};
+            if (b0 + lane < upto) mine = open_seq(a, b0 + lane);
+            const uint32_t n = tiles(a, mine) * a.kv.Hkv * (UNITS ? 1 + blocks(mine) : 1);
+            uint32_t sum = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t v = __shfl_up_sync(~0u, sum, o);
+                if (lane >= o) sum += v;
+            }
+            const uint32_t past = __ballot_sync(~0u, k < sum);
+            // (none only if the lengths changed during the launch)
+            if (!past && b0 + 32 < upto) {
+                k -= __shfl_sync(~0u, sum, 31);
+                continue;
+            }
+            const int at = past ? __ffs(past) - 1 : min(31, upto - 1 - b0);
+            k -= __shfl_sync(~0u, sum - n, at);
+            s.first = __shfl_sync(~0u, mine.first, at);
+            s.n = __shfl_sync(~0u, mine.n, at);
+            s.len = __shfl_sync(~0u, mine.len, at);
+            return b0 + at;
         }
-        return b;
     }
     __device__ __forceinline__ static void item(const OpenArgs& a, int b, const OpenSeq& s, uint32_t k, OpenPiece& p) {
         const uint32_t nt = max(1u, tiles(a, s)), h = k / nt, j = k - h * nt;
@@ -1060,6 +1077,7 @@ struct JoinPartsArgs {
     float* lse;
     int64_t heads;  // rows * Hq
     int32_t Hq, G;
+    int32_t ctas;          // of the kernel that made split rows' sums
     const float* v_scale;  // e4m3: [Hkv]
 };
 constexpr int kJoinThreads = 128;
@@ -1083,7 +1101,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const __grid_c
     for (int x = 0; x < 2; ++x) where[x] = load16(reinterpret_cast<const uint8_t*>(a.side[x].of + at));
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-        const int first = static_cast<int>(where[x].y), last = static_cast<int>(where[x].z), place = static_cast<int>(where[x].w);
+        // (held to the slots there are: a launch that gave up may have left another call's)
+        const int first = min(static_cast<int>(where[x].y), a.ctas - 1), last = min(static_cast<int>(where[x].z), a.ctas - 1);
+        const int place = min(static_cast<int>(where[x].w), 255);
         o[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         log[x] = __uint_as_float(where[x].x);
         if (place < 0) {

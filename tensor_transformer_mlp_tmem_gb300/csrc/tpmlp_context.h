@@ -109,6 +109,7 @@ struct tpmlp_ctx {
     // Captured graphs hold a buffer's address, so the smaller ones before the last stay until the context
     // goes; each is at least twice the one before. tail_partial: a second attn_partial.
     float* tail_partial = nullptr;
+    uint32_t* tail_count = nullptr;  // behind tail_partial
     float* shared[40] = {};
     int shared_n = 0;
     int64_t shared_rows = 0;
