@@ -639,13 +639,16 @@ TPMLP_API int tpmlp_attn_cross(tpmlp_ctx *ctx, const void *Q, int64_t ldq, int64
  *           be kv's)
  *   cu      device int32 [prefix->B + 1], not decreasing, at most kv->B: sequences cu[g] .. cu[g + 1] - 1
  *           have prefix g; those before cu[0] and from cu[prefix->B] on have none
- *   kv      each sequence's own keys, with the new token's, as in tpmlp_attn_decode. A key's rotation is
- *           the caller's: own keys are appended at their positions behind the prefix, so kv's page table
- *           for tpmlp_attn_append may differ from the one here
+ *   kv      each sequence's own keys, with the new token's, as in tpmlp_attn_decode. tpmlp_attn_append rotates
+ *           by the position at which it writes, so it takes a table of a sequence's whole pages (the
+ *           prefix's, then its own), of which kv's table here is the part behind the prefix: what a
+ *           prefix holds past its last full page is then each sequence's own
  * The rest as in tpmlp_attn_decode, without a window. A sequence without keys of its own attends to its
- * prefix alone. Two launches; kv->B == 0 is a no-op. Results over prefixes pass through a workspace in
- * fp32 that grows with kv->B: tpmlp_attn_reserve first, to keep the allocation out of a timed region;
- * under stream capture a call that would have to grow it returns INVALID_ARG.
+ * prefix alone. Three launches (the prefixes, the own keys, the join; with prefix->B == 0 one: it is then
+ * tpmlp_attn_decode); kv->B == 0 is a no-op. The results over prefixes and own keys pass through a
+ * workspace in fp32 that grows with kv->B (about 40 MB with the first call): tpmlp_attn_reserve first, to
+ * keep the allocation out of a timed region; under stream capture a call that would have to grow it
+ * returns INVALID_ARG.
  * Errors: as tpmlp_attn_decode, and OOM.
  */
 TPMLP_API int tpmlp_attn_decode_shared(tpmlp_ctx *ctx, const void *Q, int64_t ldq,
@@ -654,9 +657,10 @@ TPMLP_API int tpmlp_attn_decode_shared(tpmlp_ctx *ctx, const void *Q, int64_t ld
                                        float *Lse, void *stream);
 
 /*
- * Make the workspace of tpmlp_attn_decode_shared hold max_sequences sequences (Hq * (D + 1) fp32 each). A
- * workspace that grows keeps its smaller forms until tpmlp_destroy, for the graphs that were captured
- * with them. Errors: INVALID_ARG, UNSUPPORTED_SHAPE, OOM, CUDA.
+ * Make the workspace of tpmlp_attn_decode_shared hold max_sequences sequences (2 Hq (D + 4) fp32 each). A
+ * workspace that grows doubles at least, and keeps its smaller forms until tpmlp_destroy, for the graphs
+ * that were captured with them. It waits for the default stream; not for stream capture.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, OOM, CUDA.
  */
 TPMLP_API int tpmlp_attn_reserve(tpmlp_ctx *ctx, int64_t max_sequences);
 
