@@ -251,7 +251,7 @@ int tpmlp_attn_decode(tpmlp_ctx* c, const void* Q, int64_t ldq, const tpmlp_kv* 
     a.rows = kv->B;
     if (a.G > row_heads(c->head_dim, is_e4m3(c)))
         return run_prompt(c, a, nullptr, kv->B, static_cast<cudaStream_t>(stream));
-    return run_rows<false>(c, a, static_cast<cudaStream_t>(stream));
+    return run_rows<kRowsDecode>(c, a, static_cast<cudaStream_t>(stream), a.G);
 }
 
 int tpmlp_attn_prompt(tpmlp_ctx* c, const void* Q, int64_t ldq, int64_t T, const int32_t* cu_q,

@@ -365,10 +365,32 @@ struct RowArgs {
     int32_t window;
     float* partial;         // [CTAs][2] slots of RowSlot floats
     uint32_t* count;        // [CTAs] arrivals, 0 between launches
-    // PART: where results go instead of out, fp32 [rows][Hq][D], and what they are [rows][Hq]
+    // kRowsPart: where results go instead of out, fp32 [rows][Hq][D], and what they are [rows][Hq]
     float* part;
     RowOf* part_of;
+    // kRowsCross: sequence b has rows cu_q[b] .. cu_q[b + 1] - 1 of Q's T; nothing is done if any has more
+    // than `few` rows of a kv head (its tokens * G)
+    const int32_t* cu_q;
+    int32_t T;
+    int32_t few;
 };
+// What the row kernel computes: a row of each sequence (decode), the same with results for a later launch,
+// or the few rows that each sequence has.
+constexpr int kRowsDecode = 0, kRowsPart = 1, kRowsCross = 2;
+
+// A sequence's rows of Q: [first, first + n).
+struct RowSpan {
+    int first, n;
+};
+__device__ __forceinline__ RowSpan row_span(const int32_t* cu_q, int T, int b) {
+    RowSpan x;
+    x.first = max(0, min(cu_q[b], T));
+    x.n = max(0, min(cu_q[b + 1], T) - x.first);
+    return x;
+}
+__device__ __forceinline__ bool is_many(const RowSpan& x, int G, int few) {
+    return static_cast<int64_t>(x.n) * G > few;
+}
 
 // Query heads to a kv head that this kernel takes, at most; decode of wider groups goes to the prompt
 // kernel, whose products' tiles they fill and which takes the same time for any G, while this
@@ -381,11 +403,11 @@ struct RowArgs {
 constexpr int row_heads(int D, bool fp8) { return D == 128 ? (fp8 ? 16 : 8) : (fp8 ? 32 : 16); }
 
 // Warps of a block.
-constexpr int row_warps(bool part) { return part ? 4 : 8; }
+constexpr int row_warps(int mode) { return mode == kRowsPart ? 4 : 8; }
 // A segment's fixed time (its start, merge and result) in steps, as it counts in the CTAs' shares. 0, 1,
 // 2, 3: 64 sequences of 8192 keys at most x 32 heads 617, 590, 591, 595 us; 48 sequences in e4m3, 12
 // heads to a kv head 118, 104, 100, 101; one sequence of 131072 keys 88, 87, 85, 88.
-constexpr int segment_start_steps(bool) { return 2; }
+constexpr int kSegmentStart = 2;
 // e4m3 caches: fp16 weights are raised by 2^10, so that the small ones of a long cache stay clear of
 // fp16's smallest steps; it cancels against the sum.
 constexpr float kRowRaise = 10.0f;
@@ -493,15 +515,15 @@ __device__ __forceinline__ int v_dim(int g, int e) {
     else return (D / 8) * g + e;
 }
 
-// PART: results go to a.part in fp32, for a launch after this one. The launch before reads and writes
+// kRowsPart: results go to a.part in fp32, for a launch after this one. The launch before reads and writes
 // nothing that this one does, and let this one start only
 // when everything before itself was done; so this kernel waits for it at its own end alone, for the launch
 // after it to find both complete.
-template <int D, bool FP8, int NT, int PASSES, bool PART>
-__global__ void __launch_bounds__(32 * row_warps(PART), RowShape<D, FP8, NT, row_warps(PART)>::kCtasPerSm)
+template <int D, bool FP8, int NT, int PASSES, int MODE>
+__global__ void __launch_bounds__(32 * row_warps(MODE), RowShape<D, FP8, NT, row_warps(MODE)>::kCtasPerSm)
 attn_row_kernel(const __grid_constant__ RowArgs a) {
-    using S = RowShape<D, FP8, NT, row_warps(PART)>;
-    constexpr int kSegmentStart = segment_start_steps(PART);
+    using S = RowShape<D, FP8, NT, row_warps(MODE)>;
+    constexpr bool PART = MODE == kRowsPart, CROSS = MODE == kRowsCross;
     extern __shared__ __align__(16) float smem[];  // (read and written in float4)
     float* const sO = smem;                                       // [parts][rows][pitch]
     float* const sM = sO + S::kWarps * S::kRows * S::kPitch;      // [parts][rows]
@@ -521,6 +543,16 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
     auto steps_of = [&](const RowRange& x) {
         return max(1, (x.hi - (x.lo & ~15) + S::kStep - 1) / S::kStep);
     };
+    // (CROSS: a sequence's rows are taken S::kRows at a time)
+    RowSpan span{0, 0};
+    auto chunks_of = [&](const RowSpan& x) {
+        return static_cast<int>((static_cast<int64_t>(x.n) * a.G + S::kRows - 1) / S::kRows);
+    };
+    auto work_of = [&](int r) -> int64_t {
+        const int64_t c = kSegmentStart + steps_of(row_range(a, r));
+        if constexpr (CROSS) return c * chunks_of(row_span(a.cu_q, a.T, r));
+        return c;
+    };
     // Sum of the rows' work: a (row, kv head, pass) segment's is its row's steps and kSegmentStart, and
     // each CTA takes an equal run of all segments' work. Then the row that holds this CTA's first unit.
     const int64_t per_row = static_cast<int64_t>(a.kv.Hkv) * PASSES;
@@ -534,7 +566,9 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
     };
     if (a.rows <= 32) {
         // every warp for itself, a row to a lane: no barrier in a small call's way
-        const uint32_t c = lane < a.rows ? kSegmentStart + steps_of(row_range(a, lane)) : 0;
+        if constexpr (CROSS)
+            if (__any_sync(~0u, lane < a.rows && is_many(row_span(a.cu_q, a.T, lane), a.G, a.few))) return;
+        const uint32_t c = lane < a.rows ? static_cast<uint32_t>(work_of(lane)) : 0;
         uint32_t sum = c;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -546,8 +580,13 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         row = __ffs(__ballot_sync(~0u, at < sum * per_row)) - 1;
         row_start = __shfl_sync(~0u, sum - c, row) * per_row;
     } else {
+        if constexpr (CROSS) {
+            bool many = false;
+            for (int r = tid; r < a.rows; r += S::kThreads) many |= is_many(row_span(a.cu_q, a.T, r), a.G, a.few);
+            if (__syncthreads_or(many)) return;
+        }
         int64_t mine = 0;
-        for (int r = tid; r < a.rows; r += S::kThreads) mine += kSegmentStart + steps_of(row_range(a, r));
+        for (int r = tid; r < a.rows; r += S::kThreads) mine += work_of(r);
 #pragma unroll
         for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(~0u, mine, o);
         if (lane == 0) s_scan[warp] = mine;
@@ -560,7 +599,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         int64_t before = 0;
         for (int r0 = 0; r0 < a.rows; r0 += S::kThreads) {
             const int r = r0 + tid;
-            const int64_t c = r < a.rows ? kSegmentStart + steps_of(row_range(a, r)) : 0;
+            const int64_t c = r < a.rows ? work_of(r) : 0;
             int64_t sum = c;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -588,8 +627,13 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
     }
     RowRange range = row_range(a, row);
     int steps = steps_of(range);
+    int parts = a.kv.Hkv * PASSES;  // segments of the row
+    if constexpr (CROSS) {
+        span = row_span(a.cu_q, a.T, row);
+        parts = a.kv.Hkv * chunks_of(span);
+    }
     int64_t segment_start;  // first unit of the current segment
-    int part;               // kv head * PASSES + pass
+    int part;               // kv head * PASSES + pass (CROSS: chunk of rows)
     {
         const int64_t into = at - row_start;
         part = static_cast<int>(into / (steps + kSegmentStart));
@@ -601,9 +645,18 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         at = min(end, segment_start + steps + kSegmentStart);
         const int n = static_cast<int>(at - segment_start) - kSegmentStart - step0;
         if (n <= 0) return leave();  // the start alone: the segment's steps are the next CTA's
-        const int h = part / PASSES;
-        const int q0 = part % PASSES * S::kRows;  // the pass's query heads of the group
-        auto heads = [&] { return PASSES > 1 ? min(a.G - q0, S::kRows) : a.G; };  // of them
+        const int chunks = CROSS ? chunks_of(span) : PASSES;
+        const int h = part / chunks;
+        const int q0 = part % chunks * S::kRows;  // the pass's query heads of the group (CROSS: rows x heads)
+        auto heads = [&] {  // of them
+            if constexpr (CROSS) return min(span.n * a.G - q0, S::kRows);
+            return PASSES > 1 ? min(a.G - q0, S::kRows) : a.G;
+        };
+        // the row of Q and Out, and the head of it, of the pass's r-th
+        auto row_at = [&](int r) -> int64_t { return CROSS ? span.first + (q0 + r) / a.G : row; };
+        auto head_at = [&](int r) -> int64_t {
+            return static_cast<int64_t>(h) * a.G + (CROSS ? (q0 + r) % a.G : q0 + r);
+        };
 
         // Q in the reduction order of the K pieces; for an 8-bit cache's products in fp16, scaled
         // (query_exponent), and the scores scaled back.
@@ -612,8 +665,8 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int qi = nt * 8 + g;
-            const __nv_bfloat16* src = a.q + row * a.ldq + (static_cast<int64_t>(h) * a.G + q0 + qi) * D;
             const bool on = qi < heads();
+            const __nv_bfloat16* src = a.q + row_at(on ? qi : 0) * a.ldq + head_at(on ? qi : 0) * D;
             if constexpr (!FP8) {
 #pragma unroll
                 for (int j = 0; j < S::NK; ++j) {
@@ -873,7 +926,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         const float v_scale = FP8 ? a.kv.scales[a.kv.Hkv + h] : 1.0f;
 
         auto finish = [&](int r, int d, float4 v, float mm, float ll) {
-            const int64_t head = static_cast<int64_t>(h) * a.G + q0 + r;
+            const int64_t head = head_at(r);
             if constexpr (PART) {
                 const float by = ll == 0.0f ? 0.0f : v_scale / ll;
                 const int64_t at_row = static_cast<int64_t>(row) * a.Hq + head;
@@ -887,9 +940,9 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
             uint2 w;
             w.x = pack_bf162(v.x * inv, v.y * inv);
             w.y = pack_bf162(v.z * inv, v.w * inv);
-            *reinterpret_cast<uint2*>(a.out + row * a.ldo + head * D + d) = w;
+            *reinterpret_cast<uint2*>(a.out + row_at(r) * a.ldo + head * D + d) = w;
             if (a.lse && d == 0)
-                a.lse[static_cast<int64_t>(row) * a.Hq + head] =
+                a.lse[row_at(r) * a.Hq + head] =
                     ll == 0.0f ? -CUDART_INF_F
                                : (mm + log2f(ll) - (FP8 ? kRowRaise : 0.0f)) * 0.69314718055994531f;
         };
@@ -974,9 +1027,17 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
 
         // the next segment
         segment_start += steps + kSegmentStart;
-        if (++part == a.kv.Hkv * PASSES) {
+        if (++part == parts) {
             part = 0;
-            if (++row < a.rows) {
+            if constexpr (CROSS) {  // (sequences without rows are passed over)
+                do {
+                    if (++row == a.rows) return;
+                    span = row_span(a.cu_q, a.T, row);
+                } while (span.n == 0);
+                parts = a.kv.Hkv * chunks_of(span);
+                range = row_range(a, row);
+                steps = steps_of(range);
+            } else if (++row < a.rows) {
                 range = row_range(a, row);
                 steps = steps_of(range);
             }

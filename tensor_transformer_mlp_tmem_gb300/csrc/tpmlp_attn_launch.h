@@ -117,10 +117,10 @@ int allow_smem(tpmlp_ctx* c, Kernel kern, uint32_t smem, std::atomic<uint64_t>& 
     return TPMLP_OK;
 }
 
-template <int D, bool FP8, int NT, int PASSES, bool PART>
+template <int D, bool FP8, int NT, int PASSES, int MODE>
 int launch_rows(tpmlp_ctx* c, const RowArgs& a, cudaStream_t s) {
-    using S = RowShape<D, FP8, NT, row_warps(PART)>;
-    auto kern = attn_row_kernel<D, FP8, NT, PASSES, PART>;
+    using S = RowShape<D, FP8, NT, row_warps(MODE)>;
+    auto kern = attn_row_kernel<D, FP8, NT, PASSES, MODE>;
     static std::atomic<uint64_t> done{0};
     // Loads in flight lie in what shared memory leaves of an SM's 256 KB. Without this an SM keeps the split
     // of the launch before it while that has room enough: behind a prompt kernel 28 KB of loads, and 64
@@ -131,19 +131,20 @@ int launch_rows(tpmlp_ctx* c, const RowArgs& a, cudaStream_t s) {
     return launch(c, kern, grid, S::kThreads, S::kSmem, s, a);
 }
 
-template <int D, bool FP8, bool PART>
-int run_rows_of(tpmlp_ctx* c, const RowArgs& a, cudaStream_t s) {
-    if constexpr (row_heads(D, FP8) > 16)
-        if (a.G > 16) return launch_rows<D, FP8, 2, 2, PART>(c, a, s);
+template <int D, bool FP8, int MODE>
+int run_rows_of(tpmlp_ctx* c, const RowArgs& a, cudaStream_t s, int64_t heads) {
+    if constexpr (row_heads(D, FP8) > 16 && MODE != kRowsCross)
+        if (heads > 16) return launch_rows<D, FP8, 2, 2, MODE>(c, a, s);
     if constexpr (row_heads(D, FP8) > 8)
-        if (a.G > 8) return launch_rows<D, FP8, 2, 1, PART>(c, a, s);
-    return launch_rows<D, FP8, 1, 1, PART>(c, a, s);
+        if (heads > 8) return launch_rows<D, FP8, 2, 1, MODE>(c, a, s);
+    return launch_rows<D, FP8, 1, 1, MODE>(c, a, s);
 }
 
-template <bool PART>
-int run_rows(tpmlp_ctx* c, const RowArgs& a, cudaStream_t s) {
-    if (c->head_dim == 128) return is_e4m3(c) ? run_rows_of<128, true, PART>(c, a, s) : run_rows_of<128, false, PART>(c, a, s);
-    return is_e4m3(c) ? run_rows_of<64, true, PART>(c, a, s) : run_rows_of<64, false, PART>(c, a, s);
+// heads: query heads to a kv head (kRowsCross: of a sequence's rows, about).
+template <int MODE>
+int run_rows(tpmlp_ctx* c, const RowArgs& a, cudaStream_t s, int64_t heads) {
+    if (c->head_dim == 128) return is_e4m3(c) ? run_rows_of<128, true, MODE>(c, a, s, heads) : run_rows_of<128, false, MODE>(c, a, s, heads);
+    return is_e4m3(c) ? run_rows_of<64, true, MODE>(c, a, s, heads) : run_rows_of<64, false, MODE>(c, a, s, heads);
 }
 
 // The pool as [page][Hkv * page size][D], in boxes of 64 columns and one page's (at most a

@@ -40,6 +40,7 @@ int run_open(tpmlp_ctx* c, const RowArgs& r, const int32_t* cu_q, int64_t T, cud
     a.count = c->attn_count;
     a.part = part;
     a.part_of = part_of;
+    a.few = r.few;
     CUtensorMap q{}, k{}, v{};
     if (int rc = prompt_maps(c, r, T, a.tpt, &q, &k, &v)) return rc;
     if (c->head_dim == 128)
@@ -91,7 +92,7 @@ int reserve_shared(tpmlp_ctx* c, int64_t rows, const cudaStream_t* s) {
         if (int rc = refuse_allocation(c, *s, "tpmlp_attn_reserve before the capture")) return rc;
     if (!c->tail_partial) {
         // two slots and a counter to a CTA of either kernel (the open kernel's counters are the context's)
-        const size_t ctas = static_cast<size_t>(c->num_sms) * 16 / row_warps(true);
+        const size_t ctas = static_cast<size_t>(c->num_sms) * 16 / row_warps(kRowsPart);
         const size_t floats = std::max(c->attn_partial_floats, ctas * 2 * kRowSlotFloats);
         void* p = nullptr;
         if (int rc = allocate(c, &p, floats * sizeof(float) + ctas * sizeof(uint32_t))) return rc;
@@ -122,8 +123,19 @@ int tpmlp_attn_cross(tpmlp_ctx* c, const void* Q, int64_t ldq, int64_t T, const 
     if (int rc = check_attend(c, Q, ldq, kv, scale, Out, ldo, Lse)) return rc;
     if (!cu_q) return TPMLP_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(cu_q) & 3) return TPMLP_ERR_MISALIGNED;
-    const RowArgs a = row_args(c, Q, ldq, kv, scale, 0, Out, ldo, Lse);
-    return run_open(c, a, cu_q, T, static_cast<cudaStream_t>(stream));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    RowArgs a = row_args(c, Q, ldq, kv, scale, 0, Out, ldo, Lse);
+    // Few rows to a sequence on average: the row kernel, if it finds that no sequence has many, and then
+    // the open one, if there is one that has (the one that finds otherwise takes 2 us). MEASURED
+    const int64_t heads = (T * a.G + kv->B - 1) / kv->B;
+    if (heads <= row_heads(c->head_dim, is_e4m3(c))) {
+        a.rows = kv->B;
+        a.cu_q = cu_q;
+        a.T = static_cast<int32_t>(T);
+        a.few = heads <= 8 ? 16 : 32;
+        if (int rc = run_rows<kRowsCross>(c, a, s, heads)) return rc;
+    }
+    return run_open(c, a, cu_q, T, s);
 }
 
 int tpmlp_attn_reserve(tpmlp_ctx* c, int64_t max_sequences) {
@@ -157,7 +169,7 @@ int tpmlp_attn_decode_shared(tpmlp_ctx* c, const void* Q, int64_t ldq, const tpm
     a.part_of = own.of;
     const bool wide = a.G > row_heads(c->head_dim, is_e4m3(c));
     if (!wide) a.count = c->tail_count;
-    if (int rc = wide ? run_open(c, a, nullptr, kv->B, s, own.part, own.of) : run_rows<true>(c, a, s)) return rc;
+    if (int rc = wide ? run_open(c, a, nullptr, kv->B, s, own.part, own.of) : run_rows<kRowsPart>(c, a, s, a.G)) return rc;
     JoinPartsArgs j{};
     j.side[0] = {common.part, common.of, c->attn_partial};
     j.side[1] = {own.part, own.of, c->tail_partial};

@@ -46,6 +46,7 @@ struct OpenArgs {
     // and what they are [T][Hq]; those of split items stay in their contributors' slots of `partial`
     float* part;
     RowOf* part_of;
+    int32_t few;  // above 0: as RowArgs', whose kernel has computed all rows if no sequence has more
 };
 
 template <int D, bool FP8>
@@ -361,6 +362,13 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     const int warp = __shfl_sync(~0u, static_cast<int>(threadIdx.x) >> 5, 0);
     const int lane = threadIdx.x & 31;
 
+    if (a.few > 0) {
+        // The row kernel, the launch before, let this one start when everything before itself was done:
+        // cu_q can be read. Where there is nothing left to do, only the order of launches is kept.
+        bool many = false;
+        for (int b = threadIdx.x; b < a.kv.B; b += L::kThreads) many |= is_many(row_span(a.cu_q, a.T, b), a.G, a.few);
+        if (!__syncthreads_or(many)) return ptx::griddep_wait();
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < NST; ++s) {
             ptx::mbar_init(full(s), FP8 ? L::kConvert : 1);

@@ -75,6 +75,49 @@ def test_long_sequences_are_split(lib, kv, Hq, Hkv, D, page, lens, new):
     check_rows(c, q, got, lse, rows[:6] + rows[6::23] + rows[-3:], Hq, D, 1.0 / math.sqrt(D))
 
 
+FEW = [  # Hq, Hkv, D, page, keys, rows: few rows to a sequence, up to two blocks of 8 or 16 with their heads
+    (12, 12, 64, 16, [577, 1, 0, 300], [4, 4, 3, 4]),
+    (8, 8, 128, 32, [40, 129, 1000], [1, 16, 0]),               # two blocks of 8
+    (6, 2, 128, 64, [40, 129, 1000, 7], [2, 5, 0, 1]),          # three heads to a kv head
+    (5, 5, 64, 16, [5 + b for b in range(40)], [(3 * b) % 7 for b in range(40)]),
+    (4, 1, 64, 128, [100, 0, 31], [0, 0, 2]),
+    (4, 4, 128, 64, [9001, 20], [3, 1]),                        # split and joined
+    (16, 2, 64, 32, [3000, 70], [4, 1]),
+    (3, 3, 128, 16, [200, 100, 50], [1, 17, 1]),                # one sequence with too many: the other kernel
+    (3, 3, 64, 16, [31] * 50, [1] * 49 + [40]),
+    (2, 1, 64, 16, [100] * 3, [0, 0, 0]),
+]
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Hq,Hkv,D,page,lens,new", FEW)
+def test_few_rows(lib, kv, Hq, Hkv, D, page, lens, new):
+    test_matches_definition(lib, kv, Hq, Hkv, D, page, lens, new)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_replays_change_from_few_rows_to_many(lib, kv):
+    """A captured call follows the rows that the offsets name at each replay, whichever kernel has them."""
+    Hq, Hkv, D, page, lens = 4, 4, 128, 32, [300, 70, 129]
+    c = ref.make(Hkv, D, page, kv, lens, seed=29)
+    q = queries(20, Hq, D, 29)
+    with tp.Attention(Hq, Hkv, D, page, kv_dtype=kv) as attn:
+        cache, qd, cu = on_device(c, attn), q.cuda(), starts([7, 6, 7])
+        out = torch.empty_like(qd)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            attn.cross(qd, cu, cache, out=out)
+        for new in ([7, 6, 7], [20, 0, 0], [0, 16, 4], [1, 2, 17]):
+            cu.copy_(starts(new))
+            out.fill_(7.0)
+            graph.replay()
+            ok(attn)
+            want, lse = attn.cross(qd, cu, cache, return_lse=True)
+            ok(attn)
+            assert torch.equal(out, want)
+            check_rows(c, q, out, lse, all_keys(lens, new), Hq, D, D ** -0.5)
+
+
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 def test_many_items(lib, kv):
     """More items than a block tabulates."""
@@ -89,9 +132,12 @@ def test_many_items(lib, kv):
     check_rows(c, q, got, lse, rows[:2] + rows[1::401] + rows[-2:], Hq, D, 0.125)
 
 
-def test_many_sequences(lib):
-    """More sequences than the work list's table has entries, of 0 to 40 keys and 0 to 2 rows."""
+@pytest.mark.parametrize("one", [0, 30])
+def test_many_sequences(lib, one):
+    """More sequences than the work list's table has entries, of 0 to 40 keys and 0 to 2 rows, or one of
+    more (the other kernel)."""
     lens, new = [(7 * b) % 41 for b in range(700)], [b % 3 for b in range(700)]
+    new[601] += one
     c = ref.make(1, 64, 16, "bf16", lens, seed=4)
     q = queries(sum(new), 3, 64, 4)
     with tp.Attention(3, 1, 64, 16) as attn:
