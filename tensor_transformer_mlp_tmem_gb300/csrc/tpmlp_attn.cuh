@@ -365,18 +365,18 @@ struct RowArgs {
     int32_t window;
     float* partial;         // [CTAs][2] slots of RowSlot floats
     uint32_t* count;        // [CTAs] arrivals, 0 between launches
-    // kRowsPart: where results go instead of out, fp32 [rows][Hq][D], and what they are [rows][Hq]
+    // kRowsPart, kRowsCrossPart: where results go instead of out, fp32 [rows][Hq][D], and what they are [rows][Hq]
     float* part;
     RowOf* part_of;
-    // kRowsCross: sequence b has rows cu_q[b] .. cu_q[b + 1] - 1 of Q's T; nothing is done if any has more
+    // kRowsCross, kRowsCrossPart: sequence b has rows cu_q[b] .. cu_q[b + 1] - 1 of Q's T; nothing is done if any has more
     // than `few` rows of a kv head (its tokens * G)
     const int32_t* cu_q;
     int32_t T;
     int32_t few;
 };
 // What the row kernel computes: a row of each sequence (decode), the same with results for a later launch,
-// or the few rows that each sequence has.
-constexpr int kRowsDecode = 0, kRowsPart = 1, kRowsCross = 2;
+// the few rows that each sequence has, or these with results for a later launch.
+constexpr int kRowsDecode = 0, kRowsPart = 1, kRowsCross = 2, kRowsCrossPart = 3;
 
 // A sequence's rows of Q: [first, first + n).
 struct RowSpan {
@@ -387,6 +387,14 @@ __device__ __forceinline__ RowSpan row_span(const int32_t* cu_q, int T, int b) {
     x.first = max(0, min(cu_q[b], T));
     x.n = max(0, min(cu_q[b + 1], T) - x.first);
     return x;
+}
+// The rows of Q before the first sequence's and behind the last's.
+__device__ __forceinline__ void clear_rows_of_none(RowOf* part_of, const int32_t* cu_q, int B, int T, int Hq) {
+    const int first = max(0, min(cu_q[0], T)), last = max(0, min(cu_q[B], T));
+    const int64_t n = (first + static_cast<int64_t>(T) - last) * Hq, before = static_cast<int64_t>(first) * Hq;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
+         i += static_cast<int64_t>(gridDim.x) * blockDim.x)
+        part_of[i < before ? i : i + static_cast<int64_t>(last - first) * Hq] = RowOf{-CUDART_INF_F, 0, 0, -1};
 }
 __device__ __forceinline__ bool is_many(const RowSpan& x, int G, int few) {
     return static_cast<int64_t>(x.n) * G > few;
@@ -523,7 +531,7 @@ template <int D, bool FP8, int NT, int PASSES, int MODE>
 __global__ void __launch_bounds__(32 * row_warps(MODE), RowShape<D, FP8, NT, row_warps(MODE)>::kCtasPerSm)
 attn_row_kernel(const __grid_constant__ RowArgs a) {
     using S = RowShape<D, FP8, NT, row_warps(MODE)>;
-    constexpr bool PART = MODE == kRowsPart, CROSS = MODE == kRowsCross;
+    constexpr bool PART = MODE == kRowsPart, CROSS = MODE == kRowsCross || MODE == kRowsCrossPart;
     extern __shared__ __align__(16) float smem[];  // (read and written in float4)
     float* const sO = smem;                                       // [parts][rows][pitch]
     float* const sM = sO + S::kWarps * S::kRows * S::kPitch;      // [parts][rows]
@@ -542,6 +550,11 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
 
     auto steps_of = [&](const RowRange& x) {
         return max(1, (x.hi - (x.lo & ~15) + S::kStep - 1) / S::kStep);
+    };
+    // (rows of no sequence have no keys; the kernel that joins their results has to know)
+    auto no_rows = [&] {
+        if constexpr (MODE == kRowsCrossPart)
+            clear_rows_of_none(a.part_of, a.cu_q, a.rows, a.T, a.Hq);
     };
     // (CROSS: a sequence's rows are taken S::kRows at a time)
     RowSpan span{0, 0};
@@ -568,6 +581,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
         // every warp for itself, a row to a lane: no barrier in a small call's way
         if constexpr (CROSS)
             if (__any_sync(~0u, lane < a.rows && is_many(row_span(a.cu_q, a.T, lane), a.G, a.few))) return;
+        no_rows();
         const uint32_t c = lane < a.rows ? static_cast<uint32_t>(work_of(lane)) : 0;
         uint32_t sum = c;
 #pragma unroll
@@ -585,6 +599,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
             for (int r = tid; r < a.rows; r += S::kThreads) many |= is_many(row_span(a.cu_q, a.T, r), a.G, a.few);
             if (__syncthreads_or(many)) return;
         }
+        no_rows();
         int64_t mine = 0;
         for (int r = tid; r < a.rows; r += S::kThreads) mine += work_of(r);
 #pragma unroll
@@ -927,9 +942,9 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
 
         auto finish = [&](int r, int d, float4 v, float mm, float ll) {
             const int64_t head = head_at(r);
-            if constexpr (PART) {
+            if constexpr (MODE == kRowsPart || MODE == kRowsCrossPart) {
                 const float by = ll == 0.0f ? 0.0f : v_scale / ll;
-                const int64_t at_row = static_cast<int64_t>(row) * a.Hq + head;
+                const int64_t at_row = row_at(r) * a.Hq + head;
                 *reinterpret_cast<float4*>(a.part + at_row * D + d) = make_float4(v.x * by, v.y * by, v.z * by, v.w * by);
                 if (d == 0)
                     a.part_of[at_row] = RowOf{

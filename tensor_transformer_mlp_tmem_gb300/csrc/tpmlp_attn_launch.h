@@ -133,14 +133,14 @@ int launch_rows(tpmlp_ctx* c, const RowArgs& a, cudaStream_t s) {
 
 template <int D, bool FP8, int MODE>
 int run_rows_of(tpmlp_ctx* c, const RowArgs& a, cudaStream_t s, int64_t heads) {
-    if constexpr (row_heads(D, FP8) > 16 && MODE != kRowsCross)
+    if constexpr (row_heads(D, FP8) > 16 && MODE < kRowsCross)
         if (heads > 16) return launch_rows<D, FP8, 2, 2, MODE>(c, a, s);
     if constexpr (row_heads(D, FP8) > 8)
         if (heads > 8) return launch_rows<D, FP8, 2, 1, MODE>(c, a, s);
     return launch_rows<D, FP8, 1, 1, MODE>(c, a, s);
 }
 
-// heads: query heads to a kv head (kRowsCross: of a sequence's rows, about).
+// heads: query heads to a kv head (kRowsCross, kRowsCrossPart: of a sequence's rows, about).
 template <int MODE>
 int run_rows(tpmlp_ctx* c, const RowArgs& a, cudaStream_t s, int64_t heads) {
     if (c->head_dim == 128) return is_e4m3(c) ? run_rows_of<128, true, MODE>(c, a, s, heads) : run_rows_of<128, false, MODE>(c, a, s, heads);

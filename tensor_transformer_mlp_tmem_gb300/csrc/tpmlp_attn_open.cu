@@ -20,9 +20,7 @@ int launch_open(tpmlp_ctx* c, const CUtensorMap& q, const CUtensorMap& k, const 
     return launch(c, kern, c->num_sms, S::kThreads, S::kTotal, s, q, k, v, a);
 }
 
-// part, part_of: see OpenArgs.
-int run_open(tpmlp_ctx* c, const RowArgs& r, const int32_t* cu_q, int64_t T, cudaStream_t s,
-                    float* part = nullptr, RowOf* part_of = nullptr) {
+int run_open(tpmlp_ctx* c, const RowArgs& r, const int32_t* cu_q, int64_t T, cudaStream_t s) {
     OpenArgs a{};
     a.kv = r.kv;
     a.q = r.q;
@@ -38,14 +36,32 @@ int run_open(tpmlp_ctx* c, const RowArgs& r, const int32_t* cu_q, int64_t T, cud
     a.scale_log2 = r.scale_log2;
     a.partial = r.partial;
     a.count = c->attn_count;
-    a.part = part;
-    a.part_of = part_of;
+    a.part = r.part;
+    a.part_of = r.part_of;
     a.few = r.few;
     CUtensorMap q{}, k{}, v{};
     if (int rc = prompt_maps(c, r, T, a.tpt, &q, &k, &v)) return rc;
     if (c->head_dim == 128)
         return is_e4m3(c) ? launch_open<128, true>(c, q, k, v, a, s) : launch_open<128, false>(c, q, k, v, a, s);
     return is_e4m3(c) ? launch_open<64, true>(c, q, k, v, a, s) : launch_open<64, false>(c, q, k, v, a, s);
+}
+
+// Each sequence's rows over all of its keys (MODE: kRowsCross, kRowsCrossPart). Few rows to a sequence on
+// average: the row kernel, if it finds that no sequence has many, and then the open one, if there is one
+// that has (the other ends at once). Both against the open kernel alone, us: 16 x 4 rows on 577 keys x 12
+// heads of 64 13, 19 (e4m3 10, 22); 64 x 4 on 1500 x 20 of 64 84, 126 (63, 157); 8 x 8 on 1500 x 32 of 128
+// 41, 42 (30, 48); 16 x 3 on 577 x 24 of 64, 6 to a kv head 12.1, 11.5 (8, 13).
+template <int MODE>
+int run_all_keys(tpmlp_ctx* c, RowArgs a, const int32_t* cu_q, int64_t T, cudaStream_t s) {
+    const int64_t heads = (T * a.G + a.kv.B - 1) / a.kv.B;
+    if (heads <= row_heads(c->head_dim, is_e4m3(c))) {
+        a.rows = a.kv.B;
+        a.cu_q = cu_q;
+        a.T = static_cast<int32_t>(T);
+        a.few = heads <= 8 ? 16 : 32;
+        if (int rc = run_rows<MODE>(c, a, s, heads)) return rc;
+    }
+    return run_open(c, a, cu_q, T, s);
 }
 
 template <int D, bool FP8>
@@ -125,17 +141,7 @@ int tpmlp_attn_cross(tpmlp_ctx* c, const void* Q, int64_t ldq, int64_t T, const 
     if (reinterpret_cast<uintptr_t>(cu_q) & 3) return TPMLP_ERR_MISALIGNED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     RowArgs a = row_args(c, Q, ldq, kv, scale, 0, Out, ldo, Lse);
-    // Few rows to a sequence on average: the row kernel, if it finds that no sequence has many, and then
-    // the open one, if there is one that has (the one that finds otherwise takes 2 us). MEASURED
-    const int64_t heads = (T * a.G + kv->B - 1) / kv->B;
-    if (heads <= row_heads(c->head_dim, is_e4m3(c))) {
-        a.rows = kv->B;
-        a.cu_q = cu_q;
-        a.T = static_cast<int32_t>(T);
-        a.few = heads <= 8 ? 16 : 32;
-        if (int rc = run_rows<kRowsCross>(c, a, s, heads)) return rc;
-    }
-    return run_open(c, a, cu_q, T, s);
+    return run_all_keys<kRowsCross>(c, a, cu_q, T, s);
 }
 
 int tpmlp_attn_reserve(tpmlp_ctx* c, int64_t max_sequences) {
@@ -160,8 +166,10 @@ int tpmlp_attn_decode_shared(tpmlp_ctx* c, const void* Q, int64_t ldq, const tpm
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (int rc = reserve_shared(c, kv->B, &s)) return rc;
     const SharedPart common = shared_part(c, 0), own = shared_part(c, 1);
-    const RowArgs p = row_args(c, Q, ldq, prefix, scale, 0, Out, ldo, nullptr);
-    if (int rc = run_open(c, p, cu, kv->B, s, common.part, common.of)) return rc;
+    RowArgs p = row_args(c, Q, ldq, prefix, scale, 0, Out, ldo, nullptr);
+    p.part = common.part;
+    p.part_of = common.of;
+    if (int rc = run_all_keys<kRowsCrossPart>(c, p, cu, kv->B, s)) return rc;
     RowArgs a = row_args(c, Q, ldq, kv, scale, 0, Out, ldo, nullptr);
     a.rows = kv->B;
     a.partial = c->tail_partial;
@@ -169,7 +177,7 @@ int tpmlp_attn_decode_shared(tpmlp_ctx* c, const void* Q, int64_t ldq, const tpm
     a.part_of = own.of;
     const bool wide = a.G > row_heads(c->head_dim, is_e4m3(c));
     if (!wide) a.count = c->tail_count;
-    if (int rc = wide ? run_open(c, a, nullptr, kv->B, s, own.part, own.of) : run_rows<kRowsPart>(c, a, s, a.G)) return rc;
+    if (int rc = wide ? run_open(c, a, nullptr, kv->B, s) : run_rows<kRowsPart>(c, a, s, a.G)) return rc;
     JoinPartsArgs j{};
     j.side[0] = {common.part, common.of, c->attn_partial};
     j.side[1] = {own.part, own.of, c->tail_partial};

@@ -367,7 +367,10 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         // cu_q can be read. Where there is nothing left to do, only the order of launches is kept.
         bool many = false;
         for (int b = threadIdx.x; b < a.kv.B; b += L::kThreads) many |= is_many(row_span(a.cu_q, a.T, b), a.G, a.few);
-        if (!__syncthreads_or(many)) return ptx::griddep_wait();
+        if (!__syncthreads_or(many)) {
+            ptx::griddep_launch_dependents();
+            return ptx::griddep_wait();
+        }
     }
     if (threadIdx.x == 0) {
         for (int s = 0; s < NST; ++s) {
@@ -411,15 +414,8 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
 
-    if (a.part && a.cu_q) {
-        // rows of no sequence have no keys; the kernel that joins their results has to know
-        const int first = max(0, min(a.cu_q[0], a.T)), last = max(0, min(a.cu_q[a.kv.B], a.T));
-        const int64_t n = (first + static_cast<int64_t>(a.T) - last) * a.Hq;
-        for (int64_t i = static_cast<int64_t>(blockIdx.x) * L::kThreads + threadIdx.x; i < n;
-             i += static_cast<int64_t>(gridDim.x) * L::kThreads)
-            a.part_of[i < static_cast<int64_t>(first) * a.Hq ? i : i + static_cast<int64_t>(last - first) * a.Hq] =
-                RowOf{-CUDART_INF_F, 0, 0, -1};
-    }
+    // (rows of no sequence have no keys; the kernel that joins their results has to know)
+    if (a.part && a.cu_q) clear_rows_of_none(a.part_of, a.cu_q, a.kv.B, a.T, a.Hq);
 
     // ---------------------------------------------------------------- the work list
     OpenWork work;

@@ -67,6 +67,12 @@ SHAPES = [  # Hq, Hkv, D, page, prefixes, first sequence with one, sequences of 
     (17, 1, 128, 32, [2000], 0, [2], [20, 2000]),
     (16, 16, 128, 64, [65], 0, [300], [(7 * b) % 41 for b in range(300)]),
     (33, 1, 64, 16, [64, 64], 0, [2, 2], [1, 1, 1, 0]),
+    # few rows to a prefix (the row kernel), some of two blocks, and one prefix with too many among few
+    (12, 12, 64, 16, [77, 0, 129, 5], 1, [4, 2, 0, 1], [3, 0, 17, 1, 40, 9, 0, 300, 2]),
+    (4, 4, 128, 32, [300, 40], 0, [12, 3], [b for b in range(15)]),
+    (6, 2, 128, 16, [9001], 2, [2], [5, 0, 3, 70, 1]),
+    (2, 2, 128, 64, [100] * 40, 0, [b % 3 for b in range(40)], [b % 5 for b in range(45)]),
+    (2, 2, 64, 64, [100] * 40, 3, [1] * 39 + [30], [b % 5 for b in range(80)]),
 ]
 
 
