@@ -410,7 +410,9 @@ __device__ __forceinline__ bool is_many(const RowSpan& x, int G, int few) {
 //   D = 64, e4m3:  G = 16: 77, 194; 17: 125, 191; 32: 129, 191; from G = 33 on three times and more
 constexpr int row_heads(int D, bool fp8) { return D == 128 ? (fp8 ? 16 : 8) : (fp8 ? 32 : 16); }
 
-// Warps of a block.
+// Warps of a block. With fewer a block's joins hold up fewer loads, but a long sequence meets more blocks.
+// kRowsPart, whose own keys are often few, with 8, 4, 2: 64 x up to 1024 keys x 32 heads (with a prefix of
+// 16) 111, 104, 102 us; 96 x up to 511 in e4m3, 12 heads to a kv head 56, 51, 48; one of 131072 97, 102, 120.
 constexpr int row_warps(int mode) { return mode == kRowsPart ? 4 : 8; }
 // A segment's fixed time (its start, merge and result) in steps, as it counts in the CTAs' shares. 0, 1,
 // 2, 3: 64 sequences of 8192 keys at most x 32 heads 617, 590, 591, 595 us; 48 sequences in e4m3, 12

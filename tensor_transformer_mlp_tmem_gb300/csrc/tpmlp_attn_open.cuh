@@ -8,18 +8,26 @@
 // rows of an item see the same keys, which is what this kernel is made of:
 //  - every item of a sequence has the same number of blocks, so that a CTA finds its share of the work
 //    by arithmetic, for any number of items;
-//  - values that are not finite need no second way (no row has a weight of 0 for a key it should not
-//    see, but for the last block's, whose rows are cleared);
-//  - heads of 64 leave tensor memory for an accumulator O for even and one for odd steps. Each has its
-//    own four softmax warps (a stream), whose maxima and sums meet at the end of the item.
+//  - values that are not finite need no second way: no row has a weight of 0 for a key that another
+//    sees, and the last block's rows behind the keys are cleared.
 //
-// Warps: 4 per stream do softmax (D = 64: streams (tile, parity) 00, 01, 10, 11; D = 128: one to a
-// tile), then one warp each for the MMAs of tile 0, the loads, the MMAs of tile 1 and the work list;
-// e4m3 caches: further ones convert the loaded bytes to fp16.
+// Warps: 0-3 softmax of tile 0, 4-7 of tile 1, 8 and 10 issue the MMAs of tile 0 and 1, 9 loads K, V and
+// Q, 11 makes the work list; e4m3 caches: further ones convert the loaded bytes to fp16.
 //
-// What bounds it: a softmax step is a chain of latencies of one warp (load of S 110 cycles, maximum 270,
-// weights 355, store 50, hand-over 200, alone on its scheduler), so the streams on a scheduler share it
-// well: MEASURED
+// What bounds it, per block of 128 keys and 256 rows: with heads of 128 in bf16 1.7 us (1.5 PFLOP/s,
+// 3200 cycles), of which the products take 2560: S's 64 columns make the tensor core read Q again for
+// every 64 keys, 48 cycles a product where 32 would do. With an e4m3 cache 1.9 us: shared memory moves
+// 384 KB a block at 128 bytes a cycle. With heads of 64 1.35 us (0.9 PFLOP/s): a softmax step is a chain of
+// one warp (scores 110 cycles, maximum 270, weights 355, store 50, hand-over 200; 1000 alone on its
+// scheduler, 1300 with the other tile's), and the products' issue and latency another of 800. Items of
+// one tile's rows: 1.43 (DRAM, 5.9 TB/s), 1.0 us with heads of 64. An item costs about 2 us beside its
+// blocks, e4m3 ones 5: Q, the first scores and the result.
+// Tried: no search for a step's maximum while its weights' sum stays small (1.41 us with heads of 64, the
+// sum's check costs what the search did); softmax warps and accumulators of their own for even and odd
+// steps (1.25 us, but 1 us more an item; 66 us for 24 ragged sequences of 20 heads of 64, against 56);
+// every second block for an idle second tile (0.83 us with heads of 64, 1 us more an item, and 0.03 us more
+// where it is not idle); the next step's scores loaded beside the hand-over (registers spill); four
+// pieces ahead in the work list (items are dealt too early: 66 us, against 56 with two).
 #pragma once
 
 #include "tpmlp_attn_prompt.cuh"
@@ -1085,6 +1093,7 @@ struct JoinPartsArgs {
     const float* v_scale;  // e4m3: [Hkv]
 };
 constexpr int kJoinThreads = 128;
+constexpr int kPartLoads = 4;  // contributors whose sums a thread loads at once
 
 // D / 4 lanes to a head, four columns each. Bound by latency: where the results lie, the contributors'
 // maxima and sums, their columns. MEASURED
@@ -1118,34 +1127,33 @@ __global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const __grid_c
         const int r = place & 127;
         const float* const slots = a.side[x].slots + static_cast<int64_t>(place >> 7) * kPromptSlotFloats;
         float m = -CUDART_INF_F, l = 0.0f;
-        for (int c0 = first; c0 <= last; c0 += kJoinLoads) {
-            float mx[kJoinLoads], lx[kJoinLoads], top = m;
-            float4 v[kJoinLoads];
+        for (int c0 = first; c0 <= last; c0 += kPartLoads) {
+            float mx[kPartLoads], lx[kPartLoads], top = m;
+            float4 v[kPartLoads];
 #pragma unroll
-            for (int u = 0; u < kJoinLoads; ++u) {
-                const int c = min(c0 + u, last);
+            for (int u = 0; u < kPartLoads; ++u) {
+                const int c = c0 + u;
+                const bool on = c <= last;
                 const float* p = slots + (static_cast<int64_t>(c) * 2 + (c == first)) * 2 * kPromptSlotFloats;
-                mx[u] = __ldcg(p + 128 * 128 + r);
-                lx[u] = __ldcg(p + 128 * 128 + 128 + r);
-                v[u] = __ldcg(reinterpret_cast<const float4*>(p + d * 128 + r * 4));
+                mx[u] = on ? __ldcg(p + 128 * 128 + r) : -CUDART_INF_F;
+                lx[u] = on ? __ldcg(p + 128 * 128 + 128 + r) : 0.0f;
+                v[u] = on ? __ldcg(reinterpret_cast<const float4*>(p + d * 128 + r * 4)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             }
 #pragma unroll
-            for (int u = 0; u < kJoinLoads; ++u) top = fmaxf(top, mx[u]);
+            for (int u = 0; u < kPartLoads; ++u) top = fmaxf(top, mx[u]);
             const float safe = top == -CUDART_INF_F ? 0.0f : top;
             const float f = exp2_approx(m - safe);
             m = top;
             l *= f;
             o[x] = make_float4(o[x].x * f, o[x].y * f, o[x].z * f, o[x].w * f);
 #pragma unroll
-            for (int u = 0; u < kJoinLoads; ++u) {
-                // past the last one, sums of 0 as well (see the row kernel)
-                const bool on = c0 + u <= last;
-                const float w = on ? exp2_approx(mx[u] - safe) : 0.0f;
+            for (int u = 0; u < kPartLoads; ++u) {
+                const float w = exp2_approx(mx[u] - safe);
                 l += w * lx[u];
-                o[x].x += w * (on ? v[u].x : 0.0f);
-                o[x].y += w * (on ? v[u].y : 0.0f);
-                o[x].z += w * (on ? v[u].z : 0.0f);
-                o[x].w += w * (on ? v[u].w : 0.0f);
+                o[x].x += w * v[u].x;
+                o[x].y += w * v[u].y;
+                o[x].z += w * v[u].z;
+                o[x].w += w * v[u].w;
             }
         }
         const float by = l == 0.0f ? 0.0f : (FP8 ? a.v_scale[head / a.G] : 1.0f) / l;
