@@ -64,15 +64,22 @@ int run_all_keys(tpmlp_ctx* c, RowArgs a, const int32_t* cu_q, int64_t T, cudaSt
     return run_open(c, a, cu_q, T, s);
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, int SLICES>
 int launch_join(tpmlp_ctx* c, const JoinPartsArgs& a, cudaStream_t s) {
-    constexpr int64_t kHeads = kJoinThreads / (D / 4);  // of a block
-    return launch(c, join_parts_kernel<D, FP8>, (a.heads + kHeads - 1) / kHeads, kJoinThreads, 0, s, a);
+    constexpr int64_t kHeads = kJoinThreads / (D / 4 * SLICES);  // of a block
+    return launch(c, join_parts_kernel<D, FP8, SLICES>, (a.heads + kHeads - 1) / kHeads, kJoinThreads, 0, s, a);
 }
 
-int run_join(tpmlp_ctx* c, const JoinPartsArgs& a, cudaStream_t s) {
-    if (c->head_dim == 128) return is_e4m3(c) ? launch_join<128, true>(c, a, s) : launch_join<128, false>(c, a, s);
-    return is_e4m3(c) ? launch_join<64, true>(c, a, s) : launch_join<64, false>(c, a, s);
+// prefixes: whose items are split over about so many CTAs as there are for each (see the kernel).
+int run_join(tpmlp_ctx* c, const JoinPartsArgs& a, int64_t prefixes, cudaStream_t s) {
+    const int64_t tiles = std::max(prefixes, a.heads / c->heads_kv / (2 * kPB));
+    const bool many = c->num_sms >= 8 * tiles * c->heads_kv;
+    if (c->head_dim == 128) {
+        if (is_e4m3(c)) return many ? launch_join<128, true, 4>(c, a, s) : launch_join<128, true, 1>(c, a, s);
+        return many ? launch_join<128, false, 4>(c, a, s) : launch_join<128, false, 1>(c, a, s);
+    }
+    if (is_e4m3(c)) return many ? launch_join<64, true, 4>(c, a, s) : launch_join<64, true, 1>(c, a, s);
+    return many ? launch_join<64, false, 4>(c, a, s) : launch_join<64, false, 1>(c, a, s);
 }
 
 // The workspace of decode_shared: results over prefixes and over own keys, each fp32 [rows][Hq][D] and what
@@ -189,7 +196,7 @@ int tpmlp_attn_decode_shared(tpmlp_ctx* c, const void* Q, int64_t ldq, const tpm
     j.G = a.G;
     j.ctas = c->num_sms;
     j.v_scale = c->kv_scale + c->heads_kv;
-    return run_join(c, j, s);
+    return run_join(c, j, prefix->B, s);
 }
 
 int tpmlp_attn_cross_packed(const tpmlp_attend_args* a) {

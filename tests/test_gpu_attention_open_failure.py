@@ -46,9 +46,9 @@ def stall_lib(tmp_path_factory):
 def test_wait_runs_out_and_is_reported(lib, stall_lib, kv, call):
     """One item over all CTAs: 500 blocks of keys give most of them three or four (the stage is met), 150
     one (it is not). The second call, with fewer keys, is right."""
-    Hq, Hkv, D, page, rows = 4, 1, 128, 64, 3
+    Hq, Hkv, D, page, rows = 4, 1, 128, 64, 20  # (more rows than the row kernel takes)
     longest, shorter = 64000, 19200
-    c = ref.make(Hkv, D, page, kv, [longest, 40, 7, 300], seed=41)
+    c = ref.make(Hkv, D, page, kv, [longest] + [(40, 7, 300)[b % 3] for b in range(rows)], seed=41)
     q = torch.randn((rows, Hq * D), generator=torch.Generator().manual_seed(41)).bfloat16().cuda()
     K, V, table, lens = c["K"].cuda(), c["V"].cuda(), c["table"].cuda(), c["lens"].cuda()
     cu = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
