@@ -105,6 +105,8 @@ int tpmlp_attn_create(tpmlp_ctx** out, int32_t Hq, int32_t Hkv, int32_t D, int32
     // two slots per CTA of either kernel (the prompt kernel's hold two tiles each)
     const size_t partial = std::max(ctas * 2 * kRowSlotFloats,
                                     static_cast<size_t>(c->num_sms) * 4 * kPromptSlotFloats);
+    // (cross attention's results that are joined apart)
+    const size_t behind = static_cast<size_t>(cross_part_heads(c)) * (D * sizeof(float) + sizeof(RowOf));
     const size_t counters = ctas + 2;  // a counter per CTA (prompt: per tile), the deal's two
     c->attn_counters = counters;
     c->attn_partial_floats = partial;
@@ -117,7 +119,7 @@ int tpmlp_attn_create(tpmlp_ctx** out, int32_t Hq, int32_t Hkv, int32_t D, int32
     }
     std::fill(ones, ones + scales, 1.0f);
     if ((e = cudaMalloc(&c->kv_scale, scales * sizeof(float))) != cudaSuccess ||
-        (e = cudaMalloc(&c->attn_partial, partial * sizeof(float))) != cudaSuccess ||
+        (e = cudaMalloc(&c->attn_partial, partial * sizeof(float) + behind)) != cudaSuccess ||
         (e = cudaMalloc(&c->attn_count, counters * sizeof(uint32_t))) != cudaSuccess ||
         (e = cudaMalloc(&c->status, kStatusWords * sizeof(int))) != cudaSuccess ||
         (e = cudaMemset(c->attn_count, 0, counters * sizeof(uint32_t))) != cudaSuccess ||

@@ -346,7 +346,7 @@ constexpr int kJoinLoads = 8;  // contributors of a split range whose sums a thr
 struct __align__(16) RowOf {
     float log;        // whole: log2 of the sum of its weights; -infinity: no keys, and no result is looked at
     int first, last;  // split: the contributing CTAs of the kernel that made it
-    int place;        // split: tile * 128 + row in their slots; whole: -1
+    int place;        // split: tile * 128 + row in their slots; whole: -1; a row that is not to be written: -2
 };
 
 // ------------------------------------------------------------------ rows
@@ -388,13 +388,13 @@ __device__ __forceinline__ RowSpan row_span(const int32_t* cu_q, int T, int b) {
     x.n = max(0, min(cu_q[b + 1], T) - x.first);
     return x;
 }
-// The rows of Q before the first sequence's and behind the last's.
-__device__ __forceinline__ void clear_rows_of_none(RowOf* part_of, const int32_t* cu_q, int B, int T, int Hq) {
+// The rows of Q before the first sequence's and behind the last's: no keys.
+__device__ __forceinline__ void clear_rows_of_none(RowOf* part_of, const int32_t* cu_q, int B, int T, int Hq, int place) {
     const int first = max(0, min(cu_q[0], T)), last = max(0, min(cu_q[B], T));
     const int64_t n = (first + static_cast<int64_t>(T) - last) * Hq, before = static_cast<int64_t>(first) * Hq;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
          i += static_cast<int64_t>(gridDim.x) * blockDim.x)
-        part_of[i < before ? i : i + static_cast<int64_t>(last - first) * Hq] = RowOf{-CUDART_INF_F, 0, 0, -1};
+        part_of[i < before ? i : i + static_cast<int64_t>(last - first) * Hq] = RowOf{-CUDART_INF_F, 0, 0, place};
 }
 __device__ __forceinline__ bool is_many(const RowSpan& x, int G, int few) {
     return static_cast<int64_t>(x.n) * G > few;
@@ -556,7 +556,7 @@ attn_row_kernel(const __grid_constant__ RowArgs a) {
     // (rows of no sequence have no keys; the kernel that joins their results has to know)
     auto no_rows = [&] {
         if constexpr (MODE == kRowsCrossPart)
-            clear_rows_of_none(a.part_of, a.cu_q, a.rows, a.T, a.Hq);
+            clear_rows_of_none(a.part_of, a.cu_q, a.rows, a.T, a.Hq, -1);
     };
     // (CROSS: a sequence's rows are taken S::kRows at a time)
     RowSpan span{0, 0};

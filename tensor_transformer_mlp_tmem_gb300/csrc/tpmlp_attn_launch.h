@@ -14,6 +14,16 @@
 
 namespace tpmlp {
 
+// Items of cross attention that about so many CTAs or more share leave their parts to a join of its own, by
+// all SMs, where sequences may have enough keys for that. With and without, us: 128 rows on 65536 keys x 32
+// heads (8 kv heads) 116, 125; 20 on 30000 38, 55; 64 x 8 heads on 30000 of one kv head 41, 100; 4 x 64 rows
+// on 3000 x 16 heads (8) 27.6, 28.7; 2 x 100 on 577 x 16 of 64, whose items are not split, 14.2, 11.3.
+constexpr int kJoinApart = 4, kJoinApartKeys = 2048;
+// Rows x heads of such a call at most: two tiles to an item, and an item to kJoinApart SMs.
+inline int64_t cross_part_heads(const tpmlp_ctx* c) {
+    return static_cast<int64_t>(c->num_sms) / kJoinApart * 2 * kPB;
+}
+
 inline bool is_e4m3(const tpmlp_ctx* c) { return (c->flags & TPMLP_FLAG_KV_E4M3) != 0; }
 
 // Rows of `width` bf16 elements at pitch ld that 16-byte loads may read.

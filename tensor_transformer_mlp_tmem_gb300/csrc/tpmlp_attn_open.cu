@@ -20,7 +20,8 @@ int launch_open(tpmlp_ctx* c, const CUtensorMap& q, const CUtensorMap& k, const 
     return launch(c, kern, c->num_sms, S::kThreads, S::kTotal, s, q, k, v, a);
 }
 
-int run_open(tpmlp_ctx* c, const RowArgs& r, const int32_t* cu_q, int64_t T, cudaStream_t s) {
+int run_open(tpmlp_ctx* c, const RowArgs& r, const int32_t* cu_q, int64_t T, cudaStream_t s,
+             int32_t rows_of_none = -1) {
     OpenArgs a{};
     a.kv = r.kv;
     a.q = r.q;
@@ -38,12 +39,64 @@ int run_open(tpmlp_ctx* c, const RowArgs& r, const int32_t* cu_q, int64_t T, cud
     a.count = c->attn_count;
     a.part = r.part;
     a.part_of = r.part_of;
+    a.rows_of_none = rows_of_none;
     a.few = r.few;
     CUtensorMap q{}, k{}, v{};
     if (int rc = prompt_maps(c, r, T, a.tpt, &q, &k, &v)) return rc;
     if (c->head_dim == 128)
         return is_e4m3(c) ? launch_open<128, true>(c, q, k, v, a, s) : launch_open<128, false>(c, q, k, v, a, s);
     return is_e4m3(c) ? launch_open<64, true>(c, q, k, v, a, s) : launch_open<64, false>(c, q, k, v, a, s);
+}
+
+// The workspace of decode_shared: results over prefixes and over own keys, each fp32 [rows][Hq][D] and what
+// they are [rows][Hq]. Own keys' split ranges have partial sums of their own, since the prefixes' are read
+// with them.
+struct SharedPart {
+    float* part;
+    RowOf* of;
+};
+size_t part_bytes(const tpmlp_ctx* c, int64_t rows) {
+    return static_cast<size_t>(rows) * c->heads_q * (c->head_dim * sizeof(float) + sizeof(RowOf));
+}
+SharedPart shared_part(const tpmlp_ctx* c, int which) {
+    char* const p = reinterpret_cast<char*>(c->shared[c->shared_n - 1]) + which * part_bytes(c, c->shared_rows);
+    const int64_t values = c->shared_rows * c->heads_q * c->head_dim;
+    return {reinterpret_cast<float*>(p), reinterpret_cast<RowOf*>(reinterpret_cast<float*>(p) + values)};
+}
+
+template <int D, bool FP8, int SLICES>
+int launch_join(tpmlp_ctx* c, const JoinPartsArgs& a, cudaStream_t s) {
+    constexpr int64_t kHeads = kJoinThreads / (D / 4 * SLICES);  // of a block
+    return launch(c, join_parts_kernel<D, FP8, SLICES>, (a.heads + kHeads - 1) / kHeads, kJoinThreads, 0, s, a);
+}
+
+// CTAs that an item of `heads` rows x heads of B sequences is split over, about, if their keys are many.
+int64_t split_over(const tpmlp_ctx* c, int64_t B, int64_t heads) {
+    const int64_t tiles = std::max(B, (heads / c->heads_kv + 2 * kPB - 1) / (2 * kPB));
+    return c->num_sms / (tiles * c->heads_kv);
+}
+
+// Joins the parts of `rows` rows of Q over keys of B sequences.
+int run_join(tpmlp_ctx* c, JoinPartsArgs a, int64_t B, int64_t rows, cudaStream_t s) {
+    a.heads = rows * c->heads_q;
+    a.Hq = c->heads_q;
+    a.G = c->heads_q / c->heads_kv;
+    a.ctas = c->num_sms;
+    a.v_scale = c->kv_scale + c->heads_kv;
+    const bool many = split_over(c, B, a.heads) >= 8;
+    if (c->head_dim == 128) {
+        if (is_e4m3(c)) return many ? launch_join<128, true, 4>(c, a, s) : launch_join<128, true, 1>(c, a, s);
+        return many ? launch_join<128, false, 4>(c, a, s) : launch_join<128, false, 1>(c, a, s);
+    }
+    if (is_e4m3(c)) return many ? launch_join<64, true, 4>(c, a, s) : launch_join<64, true, 1>(c, a, s);
+    return many ? launch_join<64, false, 4>(c, a, s) : launch_join<64, false, 1>(c, a, s);
+}
+
+// The memory behind attn_partial for a call of tpmlp_attn_cross whose items are split over kJoinApart
+// CTAs or more, and so are few.
+SharedPart cross_part(const tpmlp_ctx* c) {
+    float* const p = c->attn_partial + c->attn_partial_floats;
+    return {p, reinterpret_cast<RowOf*>(p + static_cast<size_t>(cross_part_heads(c)) * c->head_dim)};
 }
 
 // Each sequence's rows over all of its keys (MODE: kRowsCross, kRowsCrossPart). Few rows to a sequence on
@@ -61,41 +114,21 @@ int run_all_keys(tpmlp_ctx* c, RowArgs a, const int32_t* cu_q, int64_t T, cudaSt
         a.few = heads <= 8 ? 16 : 32;
         if (int rc = run_rows<MODE>(c, a, s, heads)) return rc;
     }
-    return run_open(c, a, cu_q, T, s);
-}
-
-template <int D, bool FP8, int SLICES>
-int launch_join(tpmlp_ctx* c, const JoinPartsArgs& a, cudaStream_t s) {
-    constexpr int64_t kHeads = kJoinThreads / (D / 4 * SLICES);  // of a block
-    return launch(c, join_parts_kernel<D, FP8, SLICES>, (a.heads + kHeads - 1) / kHeads, kJoinThreads, 0, s, a);
-}
-
-// prefixes: whose items are split over about so many CTAs as there are for each (see the kernel).
-int run_join(tpmlp_ctx* c, const JoinPartsArgs& a, int64_t prefixes, cudaStream_t s) {
-    const int64_t tiles = std::max(prefixes, a.heads / c->heads_kv / (2 * kPB));
-    const bool many = c->num_sms >= 8 * tiles * c->heads_kv;
-    if (c->head_dim == 128) {
-        if (is_e4m3(c)) return many ? launch_join<128, true, 4>(c, a, s) : launch_join<128, true, 1>(c, a, s);
-        return many ? launch_join<128, false, 4>(c, a, s) : launch_join<128, false, 1>(c, a, s);
+    const int64_t keys = static_cast<int64_t>(a.kv.table_pages) << a.kv.page_shift;
+    if (MODE == kRowsCross && heads > row_heads(c->head_dim, is_e4m3(c)) && keys >= kJoinApartKeys &&
+        split_over(c, a.kv.B, T * c->heads_q) >= kJoinApart) {
+        JoinPartsArgs j{};
+        const SharedPart part = cross_part(c);
+        j.side[0] = {part.part, part.of, c->attn_partial};
+        j.out = a.out;
+        j.ldo = a.ldo;
+        j.lse = a.lse;
+        a.part = part.part;
+        a.part_of = part.of;
+        if (int rc = run_open(c, a, cu_q, T, s, -2)) return rc;  // (rows of no sequence stay as they are)
+        return run_join(c, j, a.kv.B, T, s);
     }
-    if (is_e4m3(c)) return many ? launch_join<64, true, 4>(c, a, s) : launch_join<64, true, 1>(c, a, s);
-    return many ? launch_join<64, false, 4>(c, a, s) : launch_join<64, false, 1>(c, a, s);
-}
-
-// The workspace of decode_shared: results over prefixes and over own keys, each fp32 [rows][Hq][D] and what
-// they are [rows][Hq]. Own keys' split ranges have partial sums of their own, since the prefixes' are read
-// with them.
-struct SharedPart {
-    float* part;
-    RowOf* of;
-};
-size_t part_bytes(const tpmlp_ctx* c, int64_t rows) {
-    return static_cast<size_t>(rows) * c->heads_q * (c->head_dim * sizeof(float) + sizeof(RowOf));
-}
-SharedPart shared_part(const tpmlp_ctx* c, int which) {
-    char* const p = reinterpret_cast<char*>(c->shared[c->shared_n - 1]) + which * part_bytes(c, c->shared_rows);
-    const int64_t values = c->shared_rows * c->heads_q * c->head_dim;
-    return {reinterpret_cast<float*>(p), reinterpret_cast<RowOf*>(reinterpret_cast<float*>(p) + values)};
+    return run_open(c, a, cu_q, T, s);
 }
 
 // Clears new memory, before any stream's work may meet it (streams made without blocking do not wait for
@@ -191,12 +224,7 @@ int tpmlp_attn_decode_shared(tpmlp_ctx* c, const void* Q, int64_t ldq, const tpm
     j.out = a.out;
     j.ldo = ldo;
     j.lse = Lse;
-    j.heads = static_cast<int64_t>(kv->B) * c->heads_q;
-    j.Hq = c->heads_q;
-    j.G = a.G;
-    j.ctas = c->num_sms;
-    j.v_scale = c->kv_scale + c->heads_kv;
-    return run_join(c, j, prefix->B, s);
+    return run_join(c, j, prefix->B, kv->B, s);
 }
 
 int tpmlp_attn_cross_packed(const tpmlp_attend_args* a) {

@@ -54,6 +54,7 @@ struct OpenArgs {
     // and what they are [T][Hq]; those of split items stay in their contributors' slots of `partial`
     float* part;
     RowOf* part_of;
+    int32_t rows_of_none;  // place of the rows of no sequence in part_of
     int32_t few;  // above 0: as RowArgs', whose kernel has computed all rows if no sequence has more
 };
 
@@ -423,7 +424,7 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     ptx::griddep_launch_dependents();
 
     // (rows of no sequence have no keys; the kernel that joins their results has to know)
-    if (a.part && a.cu_q) clear_rows_of_none(a.part_of, a.cu_q, a.kv.B, a.T, a.Hq);
+    if (a.part && a.cu_q) clear_rows_of_none(a.part_of, a.cu_q, a.kv.B, a.T, a.Hq, a.rows_of_none);
 
     // ---------------------------------------------------------------- the work list
     OpenWork work;
@@ -1077,10 +1078,10 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 }
 
 // ------------------------------------------------------------------ two parts of a row's keys
-// A row's results over two parts of its keys, with one softmax over both.
+// A row's results over two parts of its keys (or one), with one softmax over both.
 struct JoinPartsArgs {
     struct Side {
-        const float* part;  // as OpenArgs' part, part_of and partial
+        const float* part;  // as OpenArgs' part, part_of (null: there is no such part) and partial
         const RowOf* of;
         const float* slots;
     } side[2];
@@ -1119,11 +1120,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const __grid_c
     bool split[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x)
-        where[x] = on ? load16(reinterpret_cast<const uint8_t*>(a.side[x].of + at)) : make_uint4(0xFF800000u, 0, 0, ~0u);
+        where[x] = on && a.side[x].of ? load16(reinterpret_cast<const uint8_t*>(a.side[x].of + at)) : make_uint4(0xFF800000u, 0, 0, ~0u);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         // (held to the slots there are: a launch that gave up may have left another call's)
-        const int first = min(static_cast<int>(where[x].y), a.ctas - 1), last = min(static_cast<int>(where[x].z), a.ctas - 1);
+        const uint32_t most = a.ctas - 1;
+        const int first = static_cast<int>(min(where[x].y, most)), last = static_cast<int>(min(where[x].z, most));
         const int place = min(static_cast<int>(where[x].w), 255);
         o[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         log[x] = __uint_as_float(where[x].x);
@@ -1169,7 +1171,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const __grid_c
         if (lane == 0) s_ml[x][mine][slice] = make_float2(m, l);
     }
     __syncthreads();
-    if (!on || slice > 0) return;
+    if (!on || slice > 0 || static_cast<int>(where[0].w) == -2) return;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         if (!split[x]) continue;

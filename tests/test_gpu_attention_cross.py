@@ -59,6 +59,9 @@ def test_matches_definition(lib, kv, Hq, Hkv, D, page, lens, new):
     (4, 1, 64, 16, [20011, 5, 0, 129], [40, 2, 3, 129]),
     (5, 5, 128, 128, [7000, 6999], [300, 17]),
     (20, 1, 128, 32, [5003], [1]),
+    (8, 1, 64, 64, [30000], [64]),                 # many contributors: joined by a launch of its own
+    (32, 8, 128, 64, [9000, 0, 40], [20, 30, 3]),
+    (6, 2, 64, 16, [4001, 2047, 130], [200, 1, 77]),
 ])
 def test_long_sequences_are_split(lib, kv, Hq, Hkv, D, page, lens, new):
     c = ref.make(Hkv, D, page, kv, lens, seed=17)
@@ -70,9 +73,16 @@ def test_long_sequences_are_split(lib, kv, Hq, Hkv, D, page, lens, new):
         ok(attn)
         for _ in range(3):  # deterministic, and the counters are back at 0
             assert torch.equal(attn.cross(q.cuda(), cu, cache), got)
+        # rows of no sequence, before and behind the others, stay as they are
+        wide = torch.cat([q[:1].expand(2, -1), q, q[:1].expand(3, -1)]).cuda()
+        out = torch.full_like(wide, 7.0)
+        again, lse2 = attn.cross(wide, cu + 2, cache, out=out, return_lse=True)
+        assert bool((out[:2] == 7.0).all()) and bool((out[-3:] == 7.0).all())
         ok(attn)
     rows = all_keys(lens, new)
     check_rows(c, q, got, lse, rows[:6] + rows[6::23] + rows[-3:], Hq, D, 1.0 / math.sqrt(D))
+    # (more rows may be another kernel's)
+    check_rows(c, wide.cpu(), again, lse2, all_keys(lens, new, 2)[::23], Hq, D, 1.0 / math.sqrt(D))
 
 
 FEW = [  # Hq, Hkv, D, page, keys, rows: few rows to a sequence, up to two blocks of 8 or 16 with their heads
