@@ -486,7 +486,7 @@ TPMLP_API int tpmlp_linear_forward(tpmlp_ctx *ctx, const void *X, int64_t M, voi
  *   D          head size: 64 or 128
  *   page_size  keys per page: 16, 32, 64, 128 or 256
  *   flags      0 or TPMLP_FLAG_KV_E4M3
- * Allocates the scales, the workspace of split key ranges (about 40 MB) and the status word. The
+ * Allocates the scales, the workspace of split key ranges (about 45 MB) and the status word. The
  * context is used with the tpmlp_attn_* calls, tpmlp_destroy and the diagnostic calls; the other
  * entry points reject it with TPMLP_ERR_INVALID_ARG. Like the GEMM calls, its calls on different
  * streams must not overlap on the GPU (they share the workspace). All of its calls can be
@@ -624,8 +624,9 @@ TPMLP_API int tpmlp_attn_prompt(tpmlp_ctx *ctx, const void *Q, int64_t ldq, int6
  * for rows t = cu_q[b] .. cu_q[b + 1] - 1, each sequence's keys being read once for up to 256 / G of
  * them. Rows, Lse and rows of no sequence as in tpmlp_attn_prompt; a sequence without keys gives zeros
  * and -infinity. With one row to a sequence, tpmlp_attn_decode without a window computes the same.
- * One launch, or two where sequences have few rows on average (which of two kernels takes them is found
- * from cu_q on the device); T == 0 or B == 0 is a no-op.
+ * One launch; two where sequences have few rows on average (which of two kernels takes them is found from
+ * cu_q on the device) or where few rows attend to what may be many keys (the second joins what SMs did).
+ * T == 0 or B == 0 is a no-op.
  * Errors: as tpmlp_attn_decode.
  */
 TPMLP_API int tpmlp_attn_cross(tpmlp_ctx *ctx, const void *Q, int64_t ldq, int64_t T,
@@ -645,8 +646,8 @@ TPMLP_API int tpmlp_attn_cross(tpmlp_ctx *ctx, const void *Q, int64_t ldq, int64
  *           prefix's, then its own), of which kv's table here is the part behind the prefix: what a
  *           prefix holds past its last full page is then each sequence's own
  * The rest as in tpmlp_attn_decode, without a window. A sequence without keys of its own attends to its
- * prefix alone. Three launches (the prefixes, the own keys, the join; with prefix->B == 0 one: it is then
- * tpmlp_attn_decode); kv->B == 0 is a no-op. The results over prefixes and own keys pass through a
+ * prefix alone. Three or four launches (the prefixes as in tpmlp_attn_cross, the own keys, the join; with
+ * prefix->B == 0 it is tpmlp_attn_decode); kv->B == 0 is a no-op. The results over prefixes and own keys pass through a
  * workspace in fp32 that grows with kv->B (about 40 MB with the first call): tpmlp_attn_reserve first, to
  * keep the allocation out of a timed region; under stream capture a call that would have to grow it
  * returns INVALID_ARG.

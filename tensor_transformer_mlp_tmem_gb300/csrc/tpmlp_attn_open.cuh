@@ -85,7 +85,7 @@ struct OpenShape {
     static constexpr uint32_t kTables = kStore0 + 8 * 2048;  // 2 KB of output staging per softmax warp
     static constexpr uint32_t kTotal = 1024 + kTables + 2 * kOpenRuns * 4 + 64;
     static_assert(kTotal <= 232448, "dynamic shared memory per CTA");
-    static_assert(kStages / 2 + 1 < 8, "blocks in flight, against the ring of loaded groups");
+    static_assert((kStages + kRaws) / 2 + 1 < 8, "blocks in flight, against the ring of loaded groups");
 };
 
 // A sequence's rows: [first, first + n) of Q, all of which see its first `len` keys.
@@ -131,7 +131,9 @@ struct OpenWork {
     __device__ __forceinline__ static uint32_t tiles(const OpenArgs& a, const OpenSeq& s) {
         return (static_cast<uint32_t>(s.n) + 2u * a.tpt - 1u) / (2u * a.tpt);
     }
-    __device__ __forceinline__ static uint32_t blocks(const OpenSeq& s) { return (static_cast<uint32_t>(s.len) + kPB - 1u) / kPB; }
+    __device__ __forceinline__ static uint32_t blocks(const OpenSeq& s) {
+        return (static_cast<uint32_t>(s.len) + kPB - 1u) / kPB;
+    }
 
     // The sequence of the k-th item (UNITS: unit); k becomes its number within the sequence. For a whole
     // warp.
