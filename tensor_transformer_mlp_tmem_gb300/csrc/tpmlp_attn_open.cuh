@@ -3,9 +3,9 @@
 //
 // Tiles, items, key blocks and the two products are those of the causal kernel
 // (tpmlp_attn_prompt.cuh): a tile is up to 128 rows (row = token * G + head of the group), an item two
-// tiles of one kv head, K and V come in blocks of 128 keys, and the tiles step through them 64 keys
-// at a time: S = Q K^T in tensor memory, P = 2^(S c - m) over S in 16 bits, O += P V. Without a mask all
-// rows of an item see the same keys, which is what this kernel is made of:
+// tiles of one kv head, K and V come in blocks of 128 keys, and the tiles step through them (e4m3: half a
+// block at a time): S = Q K^T in tensor memory, P = 2^(S c - m) over S in 16 bits, O += P V. Without a mask
+// all rows of an item see the same keys, which is what this kernel is made of:
 //  - every item of a sequence has the same number of blocks, so that a CTA finds its share of the work
 //    by arithmetic, for any number of items;
 //  - values that are not finite need no second way: no row has a weight of 0 for a key that another
@@ -14,19 +14,25 @@
 // Warps: 0-3 softmax of tile 0, 4-7 of tile 1, 8 and 10 issue the MMAs of tile 0 and 1, 9 loads K, V and
 // Q, 11 makes the work list; e4m3 caches: further ones convert the loaded bytes to fp16.
 //
-// What bounds it, per block of 128 keys and 256 rows: with heads of 128 in bf16 1.7 us (1.5 PFLOP/s,
-// 3200 cycles), of which the products take 2560: S's 64 columns make the tensor core read Q again for
-// every 64 keys, 48 cycles a product where 32 would do. With an e4m3 cache 1.9 us: shared memory moves
-// 384 KB a block at 128 bytes a cycle. With heads of 64 1.35 us (0.9 PFLOP/s): a softmax step is a chain of
-// one warp (scores 110 cycles, maximum 270, weights 355, store 50, hand-over 200; 1000 alone on its
-// scheduler, 1300 with the other tile's), and the products' issue and latency another of 800. Items of
-// one tile's rows: 1.43 (DRAM, 5.9 TB/s), 1.0 us with heads of 64. An item costs about 2 us beside its
-// blocks, e4m3 ones 5: Q, the first scores and the result.
-// Tried: no search for a step's maximum while its weights' sum stays small (1.41 us with heads of 64, the
-// sum's check costs what the search did); softmax warps and accumulators of their own for even and odd
-// steps (1.25 us, but 1 us more an item; 66 us for 24 ragged sequences of 20 heads of 64, against 56);
-// every second block for an idle second tile (0.83 us with heads of 64, 1 us more an item, and 0.03 us more
-// where it is not idle); the next step's scores loaded beside the hand-over (registers spill); four
+// A step of a whole block (bf16) reads Q once for its scores, and a product of 128 columns takes the tensor
+// core 64 cycles where two of 64 take 96. All 128 scores stay in a thread's registers; the weights of the
+// first 96 keys are handed over before those of the last 32, whose product with V is the shorter wait. With
+// half a block a step: 550 us for 8 x 1024 rows on 4096 keys x 32 heads and more of 128 (now 510), 126 for 95 x
+// 256 rows x 8 heads of 64 on 2048 keys (now 115); items of one tile of 64 rows there 93 (now 97), and on 64 keys
+// 19.7 (now 23). In e4m3, whose threads have registers for 64 scores, reading those of the first half once
+// more instead takes 701 us for what takes 650.
+// What bounds it, per block of 128 keys and 256 rows: with heads of 128 in bf16 2900 cycles, of which the
+// products take 2050; the rest is the chain of a tile's scores, maximum, weights and products, which the
+// other tile's fill in part; items whose keys come from DRAM 1.67 us (5.8 TB/s). With an e4m3 cache 1.9 us:
+// shared memory moves 384 KB a block at 128 bytes a cycle. With heads of 64 1.2 us (e4m3 1.45): the chain
+// of a tile. Items of one tile's rows: 1.4 (DRAM, 5.9 TB/s), 1.0 us with heads of 64. An item costs about
+// 2 us beside its blocks, e4m3 ones 5: Q, the first scores and the result.
+// Tried, with steps of 64 keys (1.35 us a block with heads of 64): no search for a step's maximum while its
+// weights' sum stays small (1.41 us, the sum's check costs what the search did); softmax warps and
+// accumulators of their own for even and odd steps (1.25 us, but 1 us more an item; 66 us for 24 ragged
+// sequences of 20 heads of 64, against 56); every second block for an idle second tile (0.83 us, 1 us more
+// an item, and 0.03 us more where it is not idle); the next step's scores loaded beside the hand-over
+// (registers spill); four
 // pieces ahead in the work list (items are dealt too early: 66 us, against 56 with two).
 #pragma once
 
@@ -87,6 +93,15 @@ struct OpenShape {
     static_assert(kTotal <= 232448, "dynamic shared memory per CTA");
     static_assert((kStages + kRaws) / 2 + 1 < 8, "blocks in flight, against the ring of loaded groups");
 };
+
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+        :
+        : "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+          "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
 
 // A sequence's rows: [first, first + n) of Q, all of which see its first `len` keys.
 struct OpenSeq {
@@ -332,7 +347,10 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ OpenArgs a) {
     using L = OpenShape<D, FP8>;
     constexpr int NST = L::kStages, NRAW = L::kRaws, W0 = 8;
-    constexpr uint32_t kIdescS = prompt_idesc(kSB, FP8, false);
+    constexpr bool kBlockStep = !FP8;              // a softmax step is a whole block
+    constexpr int kKeys = kBlockStep ? kPB : kSB;  // of a softmax step
+    constexpr int kFirst = kBlockStep ? 96 : kSB;  // of a block's first product with V
+    constexpr uint32_t kIdescS = prompt_idesc(kKeys, FP8, false);
     constexpr uint32_t kIdescO = prompt_idesc(D, FP8, true);
     constexpr uint32_t kHalf = 16384;  // bytes of 64 columns x 128 rows
 
@@ -596,31 +614,41 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             const uint32_t block0 = blocks - b0;
             blocks += b1 - b0;
             bool ok = true;
-            for (int j = begin; j < end; ++j) {
-                const int buf = j & 1;
+            for (int j = begin; j < end; j += kKeys / kSB) {
+                const int buf = kBlockStep ? 0 : j & 1;
                 if (!(ok = wait(s_full(t, buf), (s_phase >> buf) & 1u, 2))) break;
                 s_phase ^= 1u << buf;
-                const uint32_t have = (groups[(block0 + (j >> 1)) & 7] >> (4 * buf)) & 0xFu;
+                constexpr uint32_t kHave = (1u << (kKeys / 16)) - 1u;
+                const uint32_t have = (groups[(block0 + (j >> 1)) & 7] >> (4 * buf)) & kHave;
                 ptx::tc_fence_after();
                 const uint32_t ts = tmem_s(t, buf) + lanes;
-                uint32_t s[kSB];
-                ptx::tmem_ld_32x32b_x32(ts, *reinterpret_cast<uint32_t(*)[32]>(s));
-                ptx::tmem_ld_32x32b_x32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
-                ptx::tmem_wait_ld(*reinterpret_cast<uint32_t(*)[32]>(s));
-                ptx::tmem_wait_ld(*reinterpret_cast<uint32_t(*)[32]>(s + 32));
-                const int below = len - j * kSB;
-                if (below < kSB || have != 0xFu) {
+                uint32_t s[kKeys];
 #pragma unroll
-                    for (int k = 0; k < kSB; ++k) s[k] = k < below && ((have >> (k >> 4)) & 1u) ? s[k] : 0xFF800000u;
+                for (int x0 = 0; x0 < kKeys; x0 += 64) {
+#pragma unroll
+                    for (int x = x0; x < x0 + 64; x += 32) ptx::tmem_ld_32x32b_x32(ts + x, *reinterpret_cast<uint32_t(*)[32]>(s + x));
+#pragma unroll
+                    for (int x = x0; x < x0 + 64; x += 32) ptx::tmem_wait_ld(*reinterpret_cast<uint32_t(*)[32]>(s + x));
+                }
+                const int below = len - j * kSB;
+                if (below < kKeys || have != kHave) {
+#pragma unroll
+                    for (int x = 0; x < kKeys; x += 16) {
+                        const int n = (have >> (x >> 4)) & 1u ? below - x : 0;
+                        if (n < 16) {
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) s[x + k] = k < n ? s[x + k] : 0xFF800000u;
+                        }
+                    }
                 }
                 float top[4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     top[x] = __uint_as_float(s[x]);
 #pragma unroll
-                    for (int k = 4; k < kSB - 4; k += 8)
+                    for (int k = 4; k < kKeys - 4; k += 8)
                         top[x] = max3(top[x], __uint_as_float(s[k + x]), __uint_as_float(s[k + 4 + x]));
-                    top[x] = fmaxf(top[x], __uint_as_float(s[kSB - 4 + x]));
+                    top[x] = fmaxf(top[x], __uint_as_float(s[kKeys - 4 + x]));
                 }
                 const float now = fmaxf(max3(top[0], top[1], top[2]), top[3]) * c;
                 const bool move = now > m + kLazyLog2;
@@ -628,18 +656,25 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                     const float f = move ? exp2_approx(m - now) : 1.0f;
                     if (move) m = now;
                     l *= f;
-                    // O of the steps before is scaled, once the last of their products is done
+                    // O of the steps before is scaled, once the last of their products is done (with whole
+                    // blocks it was before these scores)
                     if (j > begin) {
-                        if (!(ok = wait(pv_done(t), (pv_count - 1) & 1u, 17))) break;
+                        if (!kBlockStep && !(ok = wait(pv_done(t), (pv_count - 1) & 1u, 17))) break;
                         ptx::tc_fence_after();
+                        constexpr int kAtOnce = kBlockStep ? 16 : 32;
 #pragma unroll 1
-                        for (int x = 0; x < D; x += 32) {
-                            uint32_t o[32];
-                            ptx::tmem_ld_32x32b_x32(tmem_o(t) + lanes + x, o);
-                            ptx::tmem_wait_ld(o);
+                        for (int x = 0; x < D; x += kAtOnce) {
+                            uint32_t o[kAtOnce];
+                            if constexpr (kBlockStep) {
+                                ptx::tmem_ld_32x32b_x16_wait(tmem_o(t) + lanes + x, o);
+                            } else {
+                                ptx::tmem_ld_32x32b_x32(tmem_o(t) + lanes + x, o);
+                                ptx::tmem_wait_ld(o);
+                            }
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                            tmem_st_x32(tmem_o(t) + lanes + x, o);
+                            for (int k = 0; k < kAtOnce; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                            if constexpr (kBlockStep) tmem_st_x16(tmem_o(t) + lanes + x, o);
+                            else tmem_st_x32(tmem_o(t) + lanes + x, o);
                         }
                     }
                 }
@@ -650,21 +685,29 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 const float shift = (FP8 ? kRaiseLog2 : 0.0f) - (m == -CUDART_INF_F ? 0.0f : m);
                 const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
                 float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-                uint32_t w[32];
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    float2 e = fma2(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), c2, shift2);
-                    e.x = exp2_approx(e.x);
-                    e.y = exp2_approx(e.y);
-                    sum[k & 1] = add2(sum[k & 1], e);
-                    w[k] = FP8 ? pack_half2(e.x, e.y) : pack_bf162(e.x, e.y);
+                for (int part = 0; part < (kBlockStep ? 2 : 1); ++part) {
+                    if (part > 0 && below <= kFirst) break;
+                    const int from = part * kFirst, upto = part ? kKeys : kFirst;
+                    uint32_t w[kFirst / 2];
+#pragma unroll
+                    for (int k = 0; k < kFirst / 2; ++k) {
+                        if (k >= (upto - from) / 2) break;
+                        const uint32_t* const x = s + from + 2 * k;
+                        float2 e = fma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), c2, shift2);
+                        e.x = exp2_approx(e.x);
+                        e.y = exp2_approx(e.y);
+                        sum[k & 1] = add2(sum[k & 1], e);
+                        w[k] = FP8 ? pack_half2(e.x, e.y) : pack_bf162(e.x, e.y);
+                    }
+                    if (part == 0) tmem_st_x32(ts, w);
+                    if (kBlockStep) tmem_st_x16(ts + (part ? 48 : 32), w + (part ? 0 : 32));
+                    tmem_wait_st();
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_full(t, buf + part));
                 }
-                tmem_st_x32(ts, w);
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                tmem_wait_st();
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_full(t, buf));
             }
             if (!ok) break;
             // -------------------------------------------------------- the tile's result
@@ -808,8 +851,8 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 q_phase ^= p->tokens[1] > 0 ? 3u : 1u;
                 ptx::tc_fence_after();
             }
-            // Round i: O += P V for the two steps of block i - 1, each followed by S of the step
-            // two later (block i), which may overwrite that P once its product has been issued.
+            // Round i: O += P V for both parts of block i - 1, and S of block i, which may overwrite those P
+            // once their products have been issued: after the second (whole blocks), or half by half.
             for (int i = b0; i <= b1; ++i) {
                 const uint32_t vs = stage, vph = phase;
                 uint32_t ks = vs, kph = vph;
@@ -834,10 +877,13 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 }
 #pragma unroll
                 for (int par = 0; par < 2; ++par) {
-                    const int jv = 2 * (i - 1) + par, jk = 2 * i + par;
+                    const int jk = 2 * i + par;
                     const uint32_t ts = tmem_s(t, par), to = tmem_o(t);
-                    if (i > b0 && jv < end) {
-                        const bool fresh = jv == begin;
+                    // groups of 16 keys [k0, k1) of the block
+                    const int in16 = (len - (i - 1) * kPB + 15) / 16;
+                    const int k0 = par ? kFirst / 16 : 0, k1 = min(par ? kPB / 16 : kFirst / 16, in16);
+                    if (i > b0 && begin < end && k1 > k0) {
+                        const bool fresh = par == 0 && i == b0 + 1;
                         if (fresh) {  // the tile's result before this one has been read
                             if (!(ok = wait(o_empty(t), o_phase ^ 1u, 6))) break;
                             o_phase ^= 1u;
@@ -845,29 +891,29 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                         if (!(ok = wait(p_full(t, par), (p_phase >> par) & 1u, 7))) break;
                         p_phase ^= 1u << par;
                         ptx::tc_fence_after();
-                        const int groups16 = min(kSB, len - jv * kSB + 15) / 16;
                         if (elect_one()) {
-                            if (groups16 == kSB / 16) {
+                            const uint32_t p0 = kBlockStep ? tmem_s(t, 0) : ts - 8 * k0;
+                            if (k1 == (par ? kPB / 16 : kFirst / 16)) {
 #pragma unroll
-                                for (int k = 0; k < kSB / 16; ++k)
-                                    mma_ts(to, ts + 8 * k, dv + 512 * par + 128 * k, kIdescO, k == 0 ? !fresh : 1u);
+                                for (int k = 0; k < (par ? kPB - kFirst : kFirst) / 16; ++k)
+                                    mma_ts(to, p0 + 8 * (k0 + k), dv + 128 * (k0 + k), kIdescO, k == 0 ? !fresh : 1u);
                             } else {
-                                for (int k = 0; k < groups16; ++k)
-                                    mma_ts(to, ts + 8 * k, dv + 512 * par + 128 * k, kIdescO, k == 0 ? !fresh : 1u);
+                                for (int k = k0; k < k1; ++k) mma_ts(to, p0 + 8 * k, dv + 128 * k, kIdescO, k == k0 ? !fresh : 1u);
                             }
-                            ptx::mma_commit(pv_done(t));
-                            if (jv + 1 == end) ptx::mma_commit(o_full(t));
+                            if (!kBlockStep) ptx::mma_commit(pv_done(t));
+                            if (i == b1 && (par == 1 || in16 <= kFirst / 16)) ptx::mma_commit(o_full(t));
                         }
                         __syncwarp();
                     }
-                    if (i < b1 && jk < end) {
+                    if (i < b1 && (kBlockStep ? par == 1 && jk - 1 < end : jk < end)) {
                         if (elect_one()) {
 #pragma unroll
                             for (int k = 0; k < D / 16; ++k) {
                                 const uint32_t off = (k >> 2) * (kHalf >> 4) + 2 * (k & 3);
-                                ptx::mma_bf16_ss(ts, dq + off, dk + 512 * par + off, kIdescS, k ? 1u : 0u);
+                                ptx::mma_bf16_ss(kBlockStep ? tmem_s(t, 0) : ts, dq + off, dk + (kBlockStep ? 0 : 512 * par) + off,
+                                                 kIdescS, k ? 1u : 0u);
                             }
-                            ptx::mma_commit(s_full(t, par));
+                            ptx::mma_commit(s_full(t, kBlockStep ? 0 : par));
                         }
                         __syncwarp();
                     }
