@@ -624,8 +624,9 @@ TPMLP_API int tpmlp_attn_prompt(tpmlp_ctx *ctx, const void *Q, int64_t ldq, int6
  * for rows t = cu_q[b] .. cu_q[b + 1] - 1, each sequence's keys being read once for up to 256 / G of
  * them. Rows, Lse and rows of no sequence as in tpmlp_attn_prompt; a sequence without keys gives zeros
  * and -infinity. With one row to a sequence, tpmlp_attn_decode without a window computes the same.
- * One launch; two where sequences have few rows on average (which of two kernels takes them is found from
- * cu_q on the device) or where few rows attend to what may be many keys (the second joins what SMs did).
+ * One launch; two where sequences have few rows on average and all of them more (which of two kernels
+ * takes them is found from cu_q on the device), or where few sequences attend to what may be many keys
+ * (the second joins what the SMs did).
  * T == 0 or B == 0 is a no-op.
  * Errors: as tpmlp_attn_decode.
  */

@@ -103,7 +103,8 @@ SharedPart cross_part(const tpmlp_ctx* c) {
 // average: the row kernel, if it finds that no sequence has many, and then the open one, if there is one
 // that has (the other ends at once). Both against the open kernel alone, us: 16 x 4 rows on 577 keys x 12
 // heads of 64 13, 19 (e4m3 10, 22); 64 x 4 on 1500 x 20 of 64 84, 126 (63, 157); 8 x 8 on 1500 x 32 of 128
-// 41, 42 (30, 48); 16 x 3 on 577 x 24 of 64, 6 to a kv head 12.1, 11.5 (8, 13).
+// 41, 42 (30, 48); 16 x 3 on 577 x 24 of 64, 6 to a kv head 12.1, 11.5 (8, 13). Where all rows together are
+// few the open kernel is left out (decode of 5 sequences x 12 heads of 64 behind 511 keys 9.3, with it 12.9).
 template <int MODE>
 int run_all_keys(tpmlp_ctx* c, RowArgs a, const int32_t* cu_q, int64_t T, cudaStream_t s) {
     const int64_t heads = (T * a.G + a.kv.B - 1) / a.kv.B;
@@ -113,6 +114,7 @@ int run_all_keys(tpmlp_ctx* c, RowArgs a, const int32_t* cu_q, int64_t T, cudaSt
         a.T = static_cast<int32_t>(T);
         a.few = heads <= 8 ? 16 : 32;
         if (int rc = run_rows<MODE>(c, a, s, heads)) return rc;
+        if (T * a.G <= a.few) return TPMLP_OK;  // (no sequence can have more)
     }
     const int64_t keys = static_cast<int64_t>(a.kv.table_pages) << a.kv.page_shift;
     if (MODE == kRowsCross && heads > row_heads(c->head_dim, is_e4m3(c)) && keys >= kJoinApartKeys &&

@@ -17,10 +17,10 @@
 // A step of a whole block (bf16) reads Q once for its scores, and a product of 128 columns takes the tensor
 // core 64 cycles where two of 64 take 96. All 128 scores stay in a thread's registers; the weights of the
 // first 96 keys are handed over before those of the last 32, whose product with V is the shorter wait. With
-// half a block a step: 550 us for 8 x 1024 rows on 4096 keys x 32 heads and more of 128 (now 510), 126 for 95 x
-// 256 rows x 8 heads of 64 on 2048 keys (now 115); items of one tile of 64 rows there 93 (now 97), and on 64 keys
-// 19.7 (now 23). In e4m3, whose threads have registers for 64 scores, reading those of the first half once
-// more instead takes 701 us for what takes 650.
+// half a block a step: 4 x 1024 rows on 4096 keys x 96 heads of 128 550 us (now 510), 95 x 256 rows on 2048
+// keys x 8 heads of 64 126 (now 115); 64 rows there 93 (now 97), and 256 rows on 64 keys 19.7 (now 23). In
+// e4m3, whose threads have registers for 64 scores, whole blocks with the first half's scores read once
+// more: 2 x 1000 rows on 24000 keys x 32 heads of 128 701 us (half a block a step: 650).
 // What bounds it, per block of 128 keys and 256 rows: with heads of 128 in bf16 2900 cycles, of which the
 // products take 2050; the rest is the chain of a tile's scores, maximum, weights and products, which the
 // other tile's fill in part; items whose keys come from DRAM 1.67 us (5.8 TB/s). With an e4m3 cache 1.9 us:
@@ -32,8 +32,8 @@
 // accumulators of their own for even and odd steps (1.25 us, but 1 us more an item; 66 us for 24 ragged
 // sequences of 20 heads of 64, against 56); every second block for an idle second tile (0.83 us, 1 us more
 // an item, and 0.03 us more where it is not idle); the next step's scores loaded beside the hand-over
-// (registers spill); four
-// pieces ahead in the work list (items are dealt too early: 66 us, against 56 with two).
+// (registers spill); four pieces ahead in the work list (items are dealt too early: 66 us, against 56 with
+// two).
 #pragma once
 
 #include "tpmlp_attn_prompt.cuh"
