@@ -106,6 +106,27 @@ def test_few_rows(lib, kv, Hq, Hkv, D, page, lens, new):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 64), (128, 256)])
+def test_lengths_about_the_parts_of_a_block(lib, kv, D, page):
+    lens = [x + d for x in (0, 16, 64, 96, 112, 128, 192, 224, 256) for d in (-1, 0, 1) if x + d >= 0]
+    new = [(70, 1, 130)[b % 3] for b in range(len(lens))]
+    test_matches_definition(lib, kv, 3, 3, D, page, lens, new)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_scores_that_rise_from_block_to_block(lib, kv, D):
+    """Scores of some hundreds: rows' references move in block after block, in some rows of a tile only."""
+    Hq, Hkv, lens, new = 4, 2, [1500, 333, 7000], [150, 40, 130]
+    c = ref.make(Hkv, D, 64, kv, lens, seed=31)
+    q = queries(sum(new), Hq, D, 31)
+    with tp.Attention(Hq, Hkv, D, 64, kv_dtype=kv) as attn:
+        got, lse = attn.cross(q.cuda(), starts(new), on_device(c, attn), scale=4.0, return_lse=True)
+        ok(attn)
+    check_rows(c, q, got, lse, all_keys(lens, new)[::7], Hq, D, 4.0)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 def test_replays_change_from_few_rows_to_many(lib, kv):
     """A captured call follows the rows that the offsets name at each replay, whichever kernel has them."""
     Hq, Hkv, D, page, lens = 4, 4, 128, 32, [300, 70, 129]
