@@ -143,7 +143,9 @@ __device__ __forceinline__ float head_sum(float v) {
 
 // The lane's 16 elements x0, x1 of a head over the head's root mean square, times their weights (bf16,
 // 8 to a register group): x / sqrt(mean x^2 + eps) * w, in fp32 and not rounded. Squares that leave
-// fp32 are taken once more of x 2^-80, where eps vanishes beside them.
+// fp32 are taken once more of x 2^-80, where eps vanishes beside them. The weights come last: x over the
+// root is of ordinary size whatever x is, while the root's reciprocal (2^-128 to 2^20) times a weight may be
+// neither a number of fp32 nor a whole one.
 template <int D>
 __device__ __forceinline__ void norm_head(float (&x0)[8], float (&x1)[8], const uint4& w0, const uint4& w1, float eps) {
     auto squares = [&](float down) {
@@ -165,10 +167,10 @@ __device__ __forceinline__ void norm_head(float (&x0)[8], float (&x1)[8], const 
     float w[8];
     unpack8(w0, w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x0[j] *= by * w[j];
+    for (int j = 0; j < 8; ++j) x0[j] = x0[j] * by * w[j];
     unpack8(w1, w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x1[j] *= by * w[j];
+    for (int j = 0; j < 8; ++j) x1[j] = x1[j] * by * w[j];
 }
 
 // A block takes a token, one of `parts` equal parts of it where there are few tokens, or (MANY)
