@@ -616,7 +616,8 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             bool ok = true;
             for (int j = begin; j < end; j += kKeys / kSB) {
                 const int buf = kBlockStep ? 0 : j & 1;
-                if (!(ok = wait(s_full(t, buf), (s_phase >> buf) & 1u, 2))) break;
+                // (a tile that had no rows in the piece before is here while the other goes through that one)
+                if (!(ok = wait(s_full(t, buf), (s_phase >> buf) & 1u, 2, j == begin ? kPieceWaitNs : ptx::kWaitLimitNs))) break;
                 s_phase ^= 1u << buf;
                 constexpr uint32_t kHave = (1u << (kKeys / 16)) - 1u;
                 const uint32_t have = (groups[(block0 + (j >> 1)) & 7] >> (4 * buf)) & kHave;
