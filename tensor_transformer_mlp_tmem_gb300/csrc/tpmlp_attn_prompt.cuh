@@ -794,7 +794,8 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             bool ok = true;
             for (int j = begin; j < end; ++j) {
                 const int buf = j & 1;
-                if (!(ok = wait(s_full(t, buf), (s_phase >> buf) & 1u, 2))) break;
+                // (bf16: a tile that had no rows in the piece before is here while the other goes through that one)
+                if (!(ok = wait(s_full(t, buf), (s_phase >> buf) & 1u, 2, j == begin ? kPieceWaitNs : ptx::kWaitLimitNs))) break;
                 s_phase ^= 1u << buf;
                 const uint32_t have = (groups[(block0 + (j >> 1)) & 7] >> (4 * buf)) & 0xFu;
                 ptx::tc_fence_after();

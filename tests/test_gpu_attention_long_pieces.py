@@ -30,7 +30,7 @@ def short_lib(tmp_path_factory):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
-@pytest.mark.parametrize("call", ["cross"])
+@pytest.mark.parametrize("call", ["cross", "prompt"])
 def test_a_tile_without_rows_waits_for_the_others_piece(lib, short_lib, kv, call):
     """Two items to a CTA, in turn of 1 and of 200 rows, each on 409600 keys (all on one page): 304 items of
     3201 units on 152 SMs, split in runs of 6402, so that every CTA has one item of one tile and then
