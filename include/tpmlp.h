@@ -527,8 +527,9 @@ TPMLP_API int tpmlp_attn_set_scales(tpmlp_ctx *ctx, const void *k_scale, const v
  *                       (per_head 1); copied, and may be freed once the stream has passed this call.
  *                       Both NULL: no norms
  *   eps                 2^-40 <= eps <= 1
- * It applies to appends made afterwards. A captured append keeps per_head and eps and reads the weights
- * of the last call anew on replay. The first call allocates their memory (not under stream capture).
+ * It applies to appends made afterwards. A captured append keeps per_head and eps, and on replay reads the
+ * weights of the last call with its per_head; calls with the other one, or without norms, leave it as it
+ * is. The first call allocates the weights' memory (not under stream capture).
  * Errors: INVALID_ARG, MISALIGNED, OOM, CUDA.
  */
 TPMLP_API int tpmlp_attn_set_norms(tpmlp_ctx *ctx, const void *q_weight, const void *k_weight,

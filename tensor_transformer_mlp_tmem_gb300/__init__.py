@@ -817,7 +817,8 @@ class Attention:
     def set_norms(self, q_weight, k_weight, eps: float = 1e-6, stream=None):
         """append() norms every query and key head x before it rotates it: x over the root of the mean
         of its squares plus eps, times a weight. bf16 CUDA weights [D], shared by the heads, or [Hq, D]
-        and [Hkv, D]; None and None: no norms."""
+        and [Hkv, D]; None and None: no norms. A captured append() reads on replay the weights that were
+        last set of its kind (shared, or per head)."""
         import torch
         heads = False
         if q_weight is not None or k_weight is not None:

@@ -58,6 +58,17 @@ int64_t append_tokens(const tpmlp_ctx* c, int64_t units, int64_t T) {
     return std::max<int64_t>(1, std::min({hold, fill, static_cast<int64_t>(kAppendTokens)}));
 }
 
+// Where the norms' weights of either kind lie.
+struct NormWeights {
+    uint16_t *q, *k;
+};
+NormWeights norm_weights(const tpmlp_ctx* c, bool per_head) {
+    const int64_t D = c->head_dim;
+    if (per_head) return {c->norm_w, c->norm_w + c->heads_q * D};
+    uint16_t* const shared = c->norm_w + (static_cast<int64_t>(c->heads_q) + c->heads_kv) * D;
+    return {shared, shared + D};
+}
+
 template <int D, bool FP8, int NORM>
 int launch_append(tpmlp_ctx* c, const AppendArgs& a, cudaStream_t s) {
     if (a.tokens > 1)
@@ -172,15 +183,16 @@ int tpmlp_attn_set_norms(tpmlp_ctx* c, const void* q_weight, const void* k_weigh
     if (int rc = check_device(c)) return rc;
     if (!aligned16(q_weight) || !aligned16(k_weight)) return TPMLP_ERR_MISALIGNED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // Weights per head and shared ones have places of their own, so that a captured append finds its kind's.
     const size_t head = static_cast<size_t>(c->head_dim) * sizeof(uint16_t);
     if (!c->norm_w) {
         if (int rc = refuse_allocation(c, s, "tpmlp_attn_set_norms before the capture")) return rc;
-        if (int rc = allocate(c, reinterpret_cast<void**>(&c->norm_w), (c->heads_q + c->heads_kv) * head)) return rc;
+        if (int rc = allocate(c, reinterpret_cast<void**>(&c->norm_w), (c->heads_q + c->heads_kv + 2) * head)) return rc;
     }
     const size_t nq = per_head ? c->heads_q : 1, nk = per_head ? c->heads_kv : 1;
-    TPMLP_CUDA(c, cudaMemcpyAsync(c->norm_w, q_weight, nq * head, cudaMemcpyDeviceToDevice, s));
-    TPMLP_CUDA(c, cudaMemcpyAsync(c->norm_w + c->heads_q * c->head_dim, k_weight, nk * head,
-                                  cudaMemcpyDeviceToDevice, s));
+    const NormWeights to = norm_weights(c, per_head != 0);
+    TPMLP_CUDA(c, cudaMemcpyAsync(to.q, q_weight, nq * head, cudaMemcpyDeviceToDevice, s));
+    TPMLP_CUDA(c, cudaMemcpyAsync(to.k, k_weight, nk * head, cudaMemcpyDeviceToDevice, s));
     c->norm_on = true;
     c->norm_per_head = per_head != 0;
     c->norm_eps = eps;
@@ -231,8 +243,9 @@ int tpmlp_attn_append(tpmlp_ctx* c, const void* Q, int64_t ldq, const void* K, i
         const int32_t per_head = c->head_dim / 16;
         a.part_units = (a.part_units + per_head - 1) / per_head * per_head;
         a.parts = static_cast<int32_t>((units + a.part_units - 1) / a.part_units);
-        a.wq = reinterpret_cast<const __nv_bfloat16*>(c->norm_w);
-        a.wk = a.wq + static_cast<int64_t>(c->heads_q) * c->head_dim;
+        const NormWeights w = norm_weights(c, c->norm_per_head);
+        a.wq = reinterpret_cast<const __nv_bfloat16*>(w.q);
+        a.wk = reinterpret_cast<const __nv_bfloat16*>(w.k);
         a.eps = c->norm_eps;
     }
     a.T = static_cast<int32_t>(T);

@@ -101,7 +101,8 @@ struct tpmlp_ctx {
     float* attn_partial = nullptr;   // partial sums of split key ranges (tpmlp_attn.cuh)
     uint32_t* attn_count = nullptr;  // arrivals at a split key range, one counter per CTA
     size_t attn_counters = 0;        // entries of attn_count
-    uint16_t* norm_w = nullptr;      // [heads_q + heads_kv][head_dim] bf16 (tpmlp_attn_set_norms)
+    // tpmlp_attn_set_norms, bf16: weights per head [heads_q + heads_kv][head_dim], then shared ones [2][head_dim]
+    uint16_t* norm_w = nullptr;
     bool norm_on = false, norm_per_head = false;
     float norm_eps = 0.0f;
     size_t attn_partial_floats = 0;  // values of attn_partial
