@@ -164,13 +164,18 @@ __device__ __forceinline__ void norm_head(float (&x0)[8], float (&x1)[8], const 
         eps = 0.0f;
     }
     const float by = rsqrtf(s * (1.0f / D) + eps) * down;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        x0[j] *= by;
+        x1[j] *= by;
+    }
     float w[8];
     unpack8(w0, w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x0[j] = x0[j] * by * w[j];
+    for (int j = 0; j < 8; ++j) x0[j] *= w[j];
     unpack8(w1, w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x1[j] = x1[j] * by * w[j];
+    for (int j = 0; j < 8; ++j) x1[j] *= w[j];
 }
 
 // A block takes a token, one of `parts` equal parts of it where there are few tokens, or (MANY)
