@@ -274,7 +274,12 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
 // ------------------------------------------------------------------ programmatic dependent launch
 // A kernel launched with programmatic stream serialisation may start while the kernel before it
 // in the stream is still running. griddep_wait blocks until that kernel has completed and its
-// memory operations are visible; nothing may touch global memory before it.
+// memory operations are visible; nothing may touch global memory before it. The exception: where
+// one call launches both kernels, and the first one's CTAs call griddep_launch_dependents behind
+// their own griddep_wait, all launches before the first are complete when the second starts. It may
+// then read what they have written (from L2, or behind a fence: L1 may hold older lines) and write
+// what the first neither reads nor writes. It still has to call griddep_wait before it ends, since
+// the kernel after it waits for it alone.
 // griddep_launch_dependents lets the next such kernel in the stream be scheduled onto SMs as
 // this grid's CTAs leave them (it still waits in its own griddep_wait).
 __device__ __forceinline__ void griddep_wait() {

@@ -96,8 +96,10 @@ inline int allocate(tpmlp_ctx* c, void** p, size_t bytes) {
     return TPMLP_ERR_OOM;
 }
 
-// Launch with programmatic stream serialisation (the kernels wait in griddep_wait before they
-// touch global memory).
+// Launch with programmatic stream serialisation. The kernels wait in griddep_wait before they touch global
+// memory, but for two that come behind another launch of their own call, whose CTAs let them start only
+// after a griddep_wait of theirs: the row kernel of kRowsPart (behind run_all_keys), and the tile kernel's
+// look at cu_q (behind the row kernel).
 template <typename Kernel, typename... Args>
 int launch(tpmlp_ctx* c, Kernel kern, int64_t grid, int threads, uint32_t smem, cudaStream_t s,
            const Args&... args) {

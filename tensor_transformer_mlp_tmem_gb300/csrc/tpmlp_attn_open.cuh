@@ -393,9 +393,10 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 
     if (a.few > 0) {
         // The row kernel, the launch before, let this one start when everything before itself was done:
-        // cu_q can be read. Where there is nothing left to do, only the order of launches is kept.
+        // cu_q can be read (from L2). Where there is nothing left to do, only the order of launches is kept:
+        // what comes next may start beside the row kernel, and is done after it.
         bool many = false;
-        for (int b = threadIdx.x; b < a.kv.B; b += L::kThreads) many |= is_many(row_span(a.cu_q, a.T, b), a.G, a.few);
+        for (int b = threadIdx.x; b < a.kv.B; b += L::kThreads) many |= is_many(row_span<true>(a.cu_q, a.T, b), a.G, a.few);
         if (!__syncthreads_or(many)) {
             ptx::griddep_launch_dependents();
             return ptx::griddep_wait();
