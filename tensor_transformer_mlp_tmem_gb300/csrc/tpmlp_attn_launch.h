@@ -14,17 +14,25 @@
 
 namespace tpmlp {
 
-// Items of cross attention that about so many CTAs or more share leave their parts to a join of its own, by
-// all SMs, where sequences may have enough keys for that. With and without, us: 128 rows on 65536 keys x 32
-// heads (8 kv heads) 116, 125; 20 on 30000 38, 55; 64 x 8 heads on 30000 of one kv head 41, 100; 4 x 64 rows
-// on 3000 x 16 heads (8) 27.6, 28.7; 2 x 100 on 577 x 16 of 64, whose items are not split, 14.2, 11.3.
-constexpr int kJoinApart = 4, kJoinApartKeys = 2048;
-// Rows x heads of such a call at most: two tiles to an item, and an item to kJoinApart SMs.
-inline int64_t cross_part_heads(const tpmlp_ctx* c) {
-    return static_cast<int64_t>(c->num_sms) / kJoinApart * 2 * kPB;
-}
-
 inline bool is_e4m3(const tpmlp_ctx* c) { return (c->flags & TPMLP_FLAG_KV_E4M3) != 0; }
+
+// Items of cross attention that about so many CTAs or more share leave their parts to a join of its own, by
+// all SMs, where a sequence's table has room for so many keys (its length is on the device: short ones
+// behind wide tables pay the launch, 2 x 100 rows on 577 keys x 16 heads of 64 14.2 us, 11.3 without). With
+// and without, us, at so many CTAs to an item:
+//   D = 128, bf16: 4: 2 x 300 rows on 9000 keys x 12 heads 59.2, 59.5, 1 x 256 on 4096 x 32 39.0, 38.2;
+//     6: 1 x 256 on 2304 x 24 28.8, 31.9; 19: 1 x 256 on 4096 x 8 24.7, 41.1
+//   D = 128, e4m3: 4: the first 74.4, 75.6, the second 45.2, 46.9; 6: 34.0, 39.2; 19: 27.0, 48.0
+//   D = 64, bf16: 4: 2 x 300 on 9000 x 12 43.4, 43.8, 1 x 40 on 16384 x 32 45.1, 45.1; 6: 3 x 200 on 5000 x 8
+//     25.3, 26.0; 9: 1 x 256 on 4096 x 16 19.6, 22.7; 76: 64 x 8 heads on 30000 keys of one kv head 27.7, 45.4
+//   D = 64, e4m3: 4: the first 54.6, 52.5, the second 58.0, 52.9; 6: 34.4, 30.1; 9: 25.6, 28.2; 12: 1 x 40 on
+//     4096 x 12 18.4, 17.9, 2 x 200 on 4096 x 6 20.6, 23.5; 76: 40.3, 58.3
+inline int join_apart(const tpmlp_ctx* c) { return c->head_dim == 64 && is_e4m3(c) ? 9 : 4; }
+constexpr int kJoinApartKeys = 2048;
+// Rows x heads of such a call at most: two tiles to an item, and an item to join_apart SMs.
+inline int64_t cross_part_heads(const tpmlp_ctx* c) {
+    return static_cast<int64_t>(c->num_sms) / join_apart(c) * 2 * kPB;
+}
 
 // Rows of `width` bf16 elements at pitch ld that 16-byte loads may read.
 inline int check_rows(tpmlp_ctx* c, const void* p, int64_t ld, int64_t width) {

@@ -92,33 +92,48 @@ int run_join(tpmlp_ctx* c, JoinPartsArgs a, int64_t B, int64_t rows, cudaStream_
     return many ? launch_join<64, false, 4>(c, a, s) : launch_join<64, false, 1>(c, a, s);
 }
 
-// The memory behind attn_partial for a call of tpmlp_attn_cross whose items are split over kJoinApart
+// The memory behind attn_partial for a call of tpmlp_attn_cross whose items are split over join_apart
 // CTAs or more, and so are few.
 SharedPart cross_part(const tpmlp_ctx* c) {
     float* const p = c->attn_partial + c->attn_partial_floats;
     return {p, reinterpret_cast<RowOf*>(p + static_cast<size_t>(cross_part_heads(c)) * c->head_dim)};
 }
 
-// Each sequence's rows over all of its keys (MODE: kRowsCross, kRowsCrossPart). Few rows to a sequence on
-// average: the row kernel, if it finds that no sequence has many, and then the open one, if there is one
-// that has (the other ends at once). Both against the open kernel alone, us: 16 x 4 rows on 577 keys x 12
-// heads of 64 13, 19 (e4m3 10, 22); 64 x 4 on 1500 x 20 of 64 84, 126 (63, 157); 8 x 8 on 1500 x 32 of 128
+// Which launches take T rows of Q over the keys of B sequences, whose tables hold `keys` each. Few rows to a
+// sequence on average: the row kernel, if it finds that no sequence has many, and then the open one, if there
+// is one that has (the other ends at once). Both against the open kernel alone, us: 16 x 4 rows on 577 keys x
+// 12 heads of 64 13, 19 (e4m3 10, 22); 64 x 4 on 1500 x 20 of 64 84, 126 (63, 157); 8 x 8 on 1500 x 32 of 128
 // 41, 42 (30, 48); 16 x 3 on 577 x 24 of 64, 6 to a kv head 12.1, 11.5 (8, 13). Where all rows together are
 // few the open kernel is left out (decode of 5 sequences x 12 heads of 64 behind 511 keys 9.3, with it 12.9).
+struct AllKeysPath {
+    int64_t heads;  // rows x heads of a kv head to a sequence, on average
+    bool rows, open, apart;  // the row kernel, the open one, a join of the open one's parts
+    int few;        // rows x heads of a sequence that the row kernel takes
+};
+AllKeysPath all_keys_path(const tpmlp_ctx* c, int64_t B, int64_t T, int64_t keys) {
+    AllKeysPath x{};
+    const int64_t G = c->heads_q / c->heads_kv;
+    x.heads = (T * G + B - 1) / B;
+    x.rows = x.heads <= row_heads(c->head_dim, is_e4m3(c));
+    x.few = x.heads <= 8 ? 16 : 32;
+    x.open = !x.rows || T * G > x.few;  // (else no sequence can have more)
+    x.apart = !x.rows && keys >= kJoinApartKeys && split_over(c, B, T * c->heads_q) >= join_apart(c);
+    return x;
+}
+
+// Each sequence's rows over all of its keys (MODE: kRowsCross, kRowsCrossPart).
 template <int MODE>
 int run_all_keys(tpmlp_ctx* c, RowArgs a, const int32_t* cu_q, int64_t T, cudaStream_t s) {
-    const int64_t heads = (T * a.G + a.kv.B - 1) / a.kv.B;
-    if (heads <= row_heads(c->head_dim, is_e4m3(c))) {
+    const AllKeysPath x = all_keys_path(c, a.kv.B, T, static_cast<int64_t>(a.kv.table_pages) << a.kv.page_shift);
+    if (x.rows) {
         a.rows = a.kv.B;
         a.cu_q = cu_q;
         a.T = static_cast<int32_t>(T);
-        a.few = heads <= 8 ? 16 : 32;
-        if (int rc = run_rows<MODE>(c, a, s, heads)) return rc;
-        if (T * a.G <= a.few) return TPMLP_OK;  // (no sequence can have more)
+        a.few = x.few;
+        if (int rc = run_rows<MODE>(c, a, s, x.heads)) return rc;
+        if (!x.open) return TPMLP_OK;
     }
-    const int64_t keys = static_cast<int64_t>(a.kv.table_pages) << a.kv.page_shift;
-    if (MODE == kRowsCross && heads > row_heads(c->head_dim, is_e4m3(c)) && keys >= kJoinApartKeys &&
-        split_over(c, a.kv.B, T * c->heads_q) >= kJoinApart) {
+    if (MODE == kRowsCross && x.apart) {
         JoinPartsArgs j{};
         const SharedPart part = cross_part(c);
         j.side[0] = {part.part, part.of, c->attn_partial};
@@ -242,3 +257,13 @@ int tpmlp_attn_decode_shared_packed(const tpmlp_shared_args* a) {
 }
 
 }  // extern "C"
+
+#ifdef TPMLP_TEST_HOOKS
+// Test builds only: the launches of cross attention of T rows over the keys of B sequences (bit 0: the row
+// kernel, 1: the open one, 2: the join of its parts), and the rows x heads that such a join has room for.
+extern "C" TPMLP_API int tpmlp_test_cross_path(const tpmlp_ctx* c, int64_t B, int64_t T, int64_t keys) {
+    const AllKeysPath x = all_keys_path(c, B, T, keys);
+    return x.rows | x.open << 1 | x.apart << 2;
+}
+extern "C" TPMLP_API int64_t tpmlp_test_cross_room(const tpmlp_ctx* c) { return cross_part_heads(c); }
+#endif
