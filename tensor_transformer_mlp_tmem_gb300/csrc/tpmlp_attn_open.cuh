@@ -570,37 +570,34 @@ attn_open_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                         // neighbours side by side, all in flight together (a thread to a row, 16 bytes of
                         // 32 rows to a load: 7 us for 256 rows of 128). The factor that the row was
                         // divided by goes to the thread that has the row.
-                        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kSteps = 32 / kAtOnce, kLoads = kSteps;
+                        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kLoads = 32 / kAtOnce;
                         float* const up = reinterpret_cast<float*>(base_ptr + L::kUp) + t * 128;
                         const __nv_bfloat16* mine_at = mine ? a.q + qrow() * a.ldq + qhead() * D : nullptr;
                         if (!wait(q_empty, q_empty_phase ^ 1u, 1, kPieceWaitNs)) break;
-#pragma unroll 1
-                        for (int x0 = 0; x0 < kSteps; x0 += kLoads) {
-                            uint4 v[kLoads];
+                        uint4 v[kLoads];
 #pragma unroll
-                            for (int x = 0; x < kLoads; ++x) {
-                                const int r = (x0 + x) * kAtOnce + lane / kLanes;
-                                const auto at = __shfl_sync(~0u, reinterpret_cast<unsigned long long>(mine_at), r);
-                                v[x] = make_uint4(0, 0, 0, 0);
-                                if (at) v[x] = load16(reinterpret_cast<const uint8_t*>(at) + 16 * (lane % kLanes));
-                            }
+                        for (int x = 0; x < kLoads; ++x) {
+                            const int r = x * kAtOnce + lane / kLanes;
+                            const auto at = __shfl_sync(~0u, reinterpret_cast<unsigned long long>(mine_at), r);
+                            v[x] = make_uint4(0, 0, 0, 0);
+                            if (at) v[x] = load16(reinterpret_cast<const uint8_t*>(at) + 16 * (lane % kLanes));
+                        }
 #pragma unroll
-                            for (int x = 0; x < kLoads; ++x) {
-                                const int r = (x0 + x) * kAtOnce + lane / kLanes, piece = lane % kLanes;
-                                float f[8], big = 0.0f;
-                                unpack8(v[x], f);
+                        for (int x = 0; x < kLoads; ++x) {
+                            const int r = x * kAtOnce + lane / kLanes, piece = lane % kLanes;
+                            float f[8], big = 0.0f;
+                            unpack8(v[x], f);
 #pragma unroll
-                                for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(f[k]));
+                            for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(f[k]));
 #pragma unroll
-                                for (int o = 1; o < kLanes; o <<= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, o));
-                                const int e = query_exponent(big), in_tile = (warp & 3) * 32 + r;
-                                const float down = power_of_two(-e);
-                                uint8_t* const dst = base_ptr + t * L::kTile + in_tile * 128;
-                                *reinterpret_cast<uint4*>(dst + (piece >> 3) * kHalf + (((piece & 7) ^ (in_tile & 7)) << 4)) =
-                                    make_uint4(pack_half2(f[0] * down, f[1] * down), pack_half2(f[2] * down, f[3] * down),
-                                               pack_half2(f[4] * down, f[5] * down), pack_half2(f[6] * down, f[7] * down));
-                                if (piece == 0) up[in_tile] = power_of_two(e);
-                            }
+                            for (int o = 1; o < kLanes; o <<= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, o));
+                            const int e = query_exponent(big), in_tile = (warp & 3) * 32 + r;
+                            const float down = power_of_two(-e);
+                            uint8_t* const dst = base_ptr + t * L::kTile + in_tile * 128;
+                            *reinterpret_cast<uint4*>(dst + (piece >> 3) * kHalf + (((piece & 7) ^ (in_tile & 7)) << 4)) =
+                                make_uint4(pack_half2(f[0] * down, f[1] * down), pack_half2(f[2] * down, f[3] * down),
+                                           pack_half2(f[4] * down, f[5] * down), pack_half2(f[6] * down, f[7] * down));
+                            if (piece == 0) up[in_tile] = power_of_two(e);
                         }
                         fence_async_shared();
                         __syncwarp();

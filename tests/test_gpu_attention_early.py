@@ -1,4 +1,5 @@
-"""Calls whose lengths, tables, offsets and scales the kernels just before have written."""
+"""Calls whose lengths, tables, offsets and scales the kernels just before have written, and prefixes in pools
+of their own."""
 import pytest
 import torch
 
@@ -51,3 +52,29 @@ def test_lengths_tables_and_offsets_written_just_before(lib, kv, wide):
         ok(attn)
     for r, x, y in zip(rounds, slow, fast):
         assert all(torch.equal(a, b) for a, b in zip(pick(x, r[2]), pick(y, r[2])))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("members", [[3, 2], [40, 1]])
+def test_prefixes_in_pools_of_their_own(lib, kv, members):
+    """The prefixes' pools may be others than the sequences', with pages as far apart as they like."""
+    Hq, Hkv, D, page, prefix = 6, 2, 128, 32, [300, 65]
+    lens = [(17 * b) % 90 for b in range(sum(members))]
+    c = ref.make(Hkv, D, page, kv, prefix + lens, seed=29)
+    q = queries(len(lens), Hq, D, 29).cuda()
+    with tp.Attention(Hq, Hkv, D, page, kv_dtype=kv) as attn:
+        cache, shared = split(c, attn, 2)
+        want, lse = attn.decode_shared(q, cache, shared, starts(members), return_lse=True)
+        ids = shared.page_table[shared.page_table >= 0].long()
+        table = torch.full_like(shared.page_table, -1)
+        table[shared.page_table >= 0] = torch.arange(len(ids), dtype=torch.int32, device="cuda")
+        pools = []
+        for pool in (shared.K, shared.V):
+            apart = torch.empty((len(ids), 3, Hkv, page, D), dtype=pool.dtype, device="cuda")
+            apart.view(torch.uint8).fill_(0x7F)
+            apart[:, 0] = pool[ids]
+            pools.append(apart[:, 0])
+        other = tp.PagedCache(attn, *pools, table, shared.lens)
+        got, lse2 = attn.decode_shared(q, cache, other, starts(members), return_lse=True)
+        ok(attn)
+        assert torch.equal(got, want) and torch.equal(lse, lse2)
