@@ -972,7 +972,8 @@ class Attention:
         """decode() of sequences that share prefixes: sequences cu[g] .. cu[g + 1] - 1 (cu int32
         [prefix.B + 1]) attend to the keys of prefix g, a sequence of the PagedCache `prefix`, and then
         to their own in `cache` (their new token's included). A prefix's keys are read once for all of
-        its sequences; sequences before cu[0] and from cu[prefix.B] on have no prefix."""
+        its sequences; sequences before cu[0] and from cu[prefix.B] on have no prefix. For short prefixes or
+        few sequences, decode() over tables that name the prefix's pages first is faster (tpmlp.h)."""
         kv, shared, B = cache._of(self), prefix._of(self), cache.B
         at = self._ints(cu, prefix.B + 1, "cu")
         ldq = self._rows(q, B, self._wq, "q")

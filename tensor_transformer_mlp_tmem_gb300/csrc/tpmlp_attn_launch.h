@@ -16,10 +16,10 @@ namespace tpmlp {
 
 inline bool is_e4m3(const tpmlp_ctx* c) { return (c->flags & TPMLP_FLAG_KV_E4M3) != 0; }
 
-// Items of cross attention that about so many CTAs or more share leave their parts to a join of its own, by
+// Items of cross attention that about so many SMs or more share leave their parts to a join of its own, by
 // all SMs, where a sequence's table has room for so many keys (its length is on the device: short ones
 // behind wide tables pay the launch, 2 x 100 rows on 577 keys x 16 heads of 64 14.2 us, 11.3 without). With
-// and without, us, at so many CTAs to an item:
+// and without, us, at so many SMs to an item:
 //   D = 128, bf16: 4: 2 x 300 rows on 9000 keys x 12 heads 59.2, 59.5, 1 x 256 on 4096 x 32 39.0, 38.2;
 //     6: 1 x 256 on 2304 x 24 28.8, 31.9; 19: 1 x 256 on 4096 x 8 24.7, 41.1
 //   D = 128, e4m3: 4: the first 74.4, 75.6, the second 45.2, 46.9; 6: 34.0, 39.2; 19: 27.0, 48.0

@@ -1146,7 +1146,7 @@ constexpr int kPartLoads = 4;  // contributors whose sums a thread loads at once
 // D / 4 lanes to each of kSlices slices of a head's contributors, four columns each; the slices' sums meet
 // in shared memory. Bound by latency: where the results lie, then the contributors' maxima, sums and
 // columns, kPartLoads contributors of a slice at a time. 4 slices against 1, the whole decode_shared: 64
-// sequences x 8 heads of one kv head, 76 contributors 35, 48 us; 192 x 12 heads of 64, 13 contributors 65, 72;
+// sequences x 8 heads of one kv head, 59 contributors 35, 48 us; 192 x 12 heads of 64, 13 contributors 65, 72;
 // 128 x 32 on 8 kv heads, 10 contributors 204, 206; 96 x 96 on 8 kv heads, 3 contributors 94, 88.
 template <int D, bool FP8, int kSlices>
 __global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const __grid_constant__ JoinPartsArgs a) {
